@@ -252,7 +252,7 @@ def _probs(s):
     above, same = x > least, x == least
     keep = above | (same & (same.cumsum(-1) <= k - above.sum(-1, keepdim=True)))
     ids = torch.where(keep, torch.arange(V, device="cuda"), V).topk(k, -1, largest=False, sorted=True).values
-    order = x.gather(-1, ids).sort(-1, descending=True, stable=True).indices
+    order = x.gather(-1, ids).sort(dim=-1, descending=True, stable=True).indices
     ids = ids.gather(-1, order)
     w = e.gather(-1, ids).double()
     w = w / w.sum(-1, keepdim=True)
@@ -342,7 +342,7 @@ def exact(case, seed):
             if c["k"] == 0:
                 out[r] = w / w.sum()
                 continue
-            w, ids = w.sort(descending=True, stable=True)
+            w, ids = w.sort(dim=-1, descending=True, stable=True)
             w, ids = w[:c["k"]] / w[:c["k"]].sum(), ids[:c["k"]]
             cum, keep = 0.0, 0
             for x in w.tolist():
