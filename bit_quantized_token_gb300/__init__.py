@@ -30,7 +30,7 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))) + [HEADER]
 
 ABI_VERSION = 1
-LLM_F32, LLM_BF16, LLM_F16, LLM_Q4G64 = 0, 1, 2, 3
+LLM_F32, LLM_BF16, LLM_F16, LLM_Q4G64, LLM_Q8G32 = 0, 1, 2, 3, 4
 LLM_NO_GRAPH, LLM_NO_PDL, LLM_MULTI_KERNEL, LLM_DATAFLOW_STEP = 1, 2, 4, 8
 LLM_DEBUG_BATCH_HIDDEN = 16
 LLM_W4A8 = 64
@@ -45,11 +45,12 @@ EXPORTS = ["llm_model_create", "llm_model_destroy", "llm_prefill", "llm_prefill_
            "llm_decode_step_batch", "llm_kv_reset", "llm_kv_write", "llm_kv_read", "llm_kv_read_q8", "llm_kv_len",
            "llm_debug_hidden", "llm_debug_unpack", "llm_model_stats", "llm_profile_step", "llm_time_kernel", "llm_sync",
            "llm_last_error", "llm_op_matvec", "llm_op_matvec_w4a8", "llm_matvec_noalloc", "llm_phase_times", "llm_debug_fail_alloc",
-           "llm_debug_hidden_batch"]
+           "llm_debug_hidden_batch", "llm_tree_attention", "llm_token_probs", "llm_verify_tree", "llm_commit_tree"]
 
 
 # translation units of the library, compiled in parallel and linked into one shared object
-UNITS = ["llmq.cu", "step_kernels.cu", "step_kernels_kv8.cu", "stepll_kernels.cu"]
+UNITS = ["llmq.cu", "step_kernels.cu", "step_kernels_kv8.cu", "stepll_kernels.cu", "tree.cu", "tree_attn_64.cu",
+         "tree_attn_128.cu"]
 BUILD_DIR = os.path.join(_HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -168,6 +169,10 @@ def lib() -> C.CDLL:
             "llm_phase_times": (i32, [P, i32, i32, i32, P, C.c_int64]),
             "llm_debug_fail_alloc": (i32, [i32]),
             "llm_debug_hidden_batch": (i32, [P, P]),
+            "llm_tree_attention": (i32, [P, P]),
+            "llm_token_probs": (i32, [P, C.c_int64, P, C.c_int64, i32, i32, C.c_float, i32, C.c_float, P]),
+            "llm_verify_tree": (i32, [P, P]),
+            "llm_commit_tree": (i32, [P, P, i32, i32, P, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -404,3 +409,6 @@ def matvec_noalloc(model: Model, name: str, x, y, stream: int | None = None) -> 
     library); see llm_matvec_noalloc in include/llmq.h.
     """
     _check(lib().llm_matvec_noalloc(model.h, name.encode(), _ptr(x), _ptr(y), stream), model.h)
+
+
+from .tree import KVView, commit_tree, token_probs, tree_attention, tree_masks, verify_tree  # noqa: E402

@@ -26,6 +26,7 @@
 #include "stepll.cuh"
 #include "batch.cuh"
 #include "sample.cuh"
+#include "tree.cuh"
 #include "llmq.h"
 
 using namespace llmq;
@@ -1125,6 +1126,14 @@ int finish_call(llm_model* m, float* logits_out, const float* d_logits, size_t n
 }
 
 }  // namespace
+
+int llmq::op_error(int code, const char* msg) noexcept {
+  try {
+    g_create_error = msg;
+  } catch (...) {  // no memory for the text: the code alone
+  }
+  return code;
+}
 
 extern "C" {
 

@@ -17,10 +17,10 @@
 // sequential fp32 softmax, nucleus and draw.
 #pragma once
 #include "common.cuh"
+#include "sample_key.cuh"
 
 namespace llmq {
 
-constexpr int kSampleMaxK = 64;
 constexpr int kSampleThreads = 1024;
 constexpr int kSampleKPT = 32;  // logits a thread keeps per batch (a batch: 32768 logits)
 
@@ -58,13 +58,6 @@ __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint2 k) {
     c = make_uint4(hi1 ^ c.y ^ k.x, lo1, hi0 ^ c.w ^ k.y, lo0);
   }
   return c;
-}
-
-// Order-preserving key of a float: a larger value has a larger key (-0 as +0).
-__device__ __forceinline__ uint32_t sample_key(float x) {
-  uint32_t b = __float_as_uint(x);
-  if (b == 0x80000000u) b = 0u;
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
 // Exclusive prefix sum of one int per thread over the CTA (fixed order).

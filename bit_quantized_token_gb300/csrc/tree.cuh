@@ -1,0 +1,103 @@
+// Tree decoding: parameters and launchers of the operators that score a tree
+// of drafted tokens (tree_attn.cuh), turn logits into token probabilities,
+// verify the drafts and commit the kept ones to the K/V cache (tree.cu).
+// Every kernel here is stateless: work split over several CTAs is joined
+// inside a thread block cluster through distributed shared memory, so no call
+// needs a workspace, and calls on any streams or in any graphs share nothing.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+namespace llmq {
+
+constexpr int kTreeMaxNodes = 64;  // a node's visible set is one 64-bit word
+
+// A kernel's dynamic shared memory limit, set once per device (one of these,
+// static, beside each kernel's launch: its size never changes).
+class SmemLimit {
+ public:
+  template <typename Kern>
+  cudaError_t raise(Kern kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done_.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
+struct KvRows {              // K and V rows of one layer: a cache, or the drafted tree's own
+  const uint8_t* k = nullptr;      // bf16 values, or int8 codes (then the scales are set)
+  const uint8_t* v = nullptr;
+  const uint16_t* ks = nullptr;    // fp16 scales of each 32 values
+  const uint16_t* vs = nullptr;
+  int64_t seq = 0, head = 0, row = 0;     // strides in elements of k and v
+  int64_t sseq = 0, shead = 0, srow = 0;  // strides of the scales
+  int rows = 0;                    // rows a head holds
+};
+
+struct TreeAttnParams {
+  const void* q;             // bf16 or fp32
+  void* out;                 // the type of q
+  int64_t q_seq, q_node, q_head, o_seq, o_node, o_head;  // strides in elements
+  KvRows cache, tree;        // tree.k null: the cache alone
+  const int* lens;           // [B] cache rows that every node sees
+  const uint64_t* mask;      // [B][n] tree rows that a node sees
+  const int* counts;         // [B] nodes of a sequence, or null: n
+  int64_t mask_seq;
+  float c;                   // scale * log2(e)
+  int B, n, Hkv, gq;
+  int S;                     // CTAs of a cluster: splits of the keys
+};
+
+// f32: q and out are fp32 (else bf16); q8: int8 rows. n_sm: SMs of the device.
+cudaError_t launch_tree_attn(const TreeAttnParams& p, int hd, bool f32, bool q8, int n_sm, cudaStream_t st);
+cudaError_t launch_tree_attn_64(TreeAttnParams p, bool f32, bool q8, int n_sm, cudaStream_t st);
+cudaError_t launch_tree_attn_128(TreeAttnParams p, bool f32, bool q8, int n_sm, cudaStream_t st);
+
+struct TokenProbsParams {
+  const float* logits;
+  float* probs;
+  int64_t l_row, p_row;      // strides in elements
+  int R, V;
+  float c;                   // log2(e) / temperature
+  int top_k;                 // 0: every token
+  float top_p;
+  int cap = 0;               // set by the launch: floats of a slice
+};
+cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t st);
+
+struct VerifyParams {
+  const int *tokens, *parents;  // [B][n]
+  const int* counts;            // [B] or null
+  const float* u;               // [B][n]
+  const float *p, *q;           // [B][n][V]; q null: the drafts are certain choices
+  int64_t p_seq, p_node, q_seq, q_node;
+  const int* targets;           // [B][n] greedy mode: the target's choice after each node (p null)
+  int *path, *n_path, *next;
+  int B, n, V;
+};
+cudaError_t launch_verify_tree(const VerifyParams& p, int n_sm, cudaStream_t st);
+
+struct CommitParams {
+  KvRows cache, tree;        // strides of one layer; layer strides below
+  int64_t c_layer, c_slayer, t_layer, t_slayer;
+  const int *lens, *path, *n_path;
+  int* new_lens;             // may be lens itself
+  int64_t path_seq;
+  int B, L, Hkv, n, row_bytes, srow_bytes;  // bytes of a row of k or v, and of its scales (0: none)
+};
+cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st);
+
+// Records the calling thread's error text of a call without a model (llm_last_error(NULL)); returns code.
+int op_error(int code, const char* msg) noexcept;
+
+}  // namespace llmq

@@ -1,0 +1,8 @@
+// Tree attention, head dimension 128 (see tree_attn.cuh).
+#include "tree_attn.cuh"
+
+namespace llmq {
+cudaError_t launch_tree_attn_128(TreeAttnParams p, bool f32, bool q8, int n_sm, cudaStream_t st) {
+  return launch_tree_attn_hd<128>(p, f32, q8, n_sm, st);
+}
+}  // namespace llmq

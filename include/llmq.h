@@ -45,7 +45,8 @@ typedef enum {
   LLM_ERR_NOT_FOUND = -8      /* tensor name unknown */
 } llm_status;
 
-typedef enum { LLM_F32 = 0, LLM_BF16 = 1, LLM_F16 = 2, LLM_Q4G64 = 3 } llm_dtype;
+typedef enum { LLM_F32 = 0, LLM_BF16 = 1, LLM_F16 = 2, LLM_Q4G64 = 3,
+               LLM_Q8G32 = 4 /* int8 codes with one fp16 scale per 32 values (llm_kv_view) */ } llm_dtype;
 
 /* llm_config.flags */
 #define LLM_NO_GRAPH 1u       /* launch the step's kernels one by one (debugging) */
@@ -323,8 +324,8 @@ int llm_phase_times(llm_model* m, int32_t seq, int32_t first_token, int32_t n_st
  * swallowed). */
 int llm_sync(llm_model* m);
 
-/* Last error text of the model (m may be NULL: the last create error of this
- * thread). Never NULL; owned by the library.
+/* Last error text of the model (m may be NULL: the last error of this thread
+ * in a create or in a call without a model). Never NULL; owned by the library.
  * Source: as llm_sync. */
 const char* llm_last_error(const llm_model* m);
 
@@ -369,6 +370,112 @@ int llm_op_matvec_w4a8(const llm_tensor* w, const float* x, float* y);
  * touching the stream or the model. Device ordinals of 64 and above:
  * LLM_ERR_UNSUPPORTED. */
 int llm_matvec_noalloc(const llm_model* m, const char* name, const float* x, float* y, void* cuda_stream);
+
+/* ---- tree decoding ---------------------------------------------------------
+ * Operators of a decoding step that verifies a tree of drafted tokens: node 0
+ * is the root (the last chosen token), every other node a draft whose parent
+ * has a lower index. llm_tree_attention scores all nodes over the cache in one
+ * pass, llm_token_probs turns logits into the sampler's probabilities,
+ * llm_verify_tree decides which drafts are kept, llm_commit_tree moves the
+ * kept nodes' K/V rows into the cache; llm_decode_tree runs all of them for a
+ * model's own sequence.
+ *
+ * Each of the four works on the caller's device buffers on the current device
+ * and on `cuda_stream` (NULL: the legacy default stream). They are
+ * asynchronous, allocate nothing, keep nothing between calls and can be
+ * captured into a graph; calls on different streams share no state. Errors
+ * (INVALID_ARG, UNSUPPORTED, CUDA) are returned before any launch, with their
+ * reason in llm_last_error(NULL) of the calling thread. Buffers must stay
+ * valid, and outputs must not overlap inputs where not said otherwise. Lengths,
+ * counts, paths and tokens are read on the device: values outside their range
+ * never lead out of a buffer (they are clamped or their node is skipped).
+ * Source: no page drafts tokens; the cache formats are llm_kv_write's. */
+
+/* K and V rows in device memory, [seq][layer][head][row][head_dim] at any
+ * strides (in elements, multiples of 16 bytes; a row is contiguous; k and v
+ * 16-byte aligned and laid out alike). LLM_BF16, or LLM_Q8G32: int8 codes and
+ * fp16 scales [..][head_dim / 32] at the scale strides (multiples of
+ * head_dim / 32, aligned to a row of scales). head_dim 64 or 128. */
+typedef struct {
+  int32_t dtype;
+  int32_t n_seq, n_layers, n_heads, rows, head_dim;
+  void *k, *v, *k_scales, *v_scales;
+  int64_t seq_stride, layer_stride, head_stride, row_stride;
+  int64_t scale_seq_stride, scale_layer_stride, scale_head_stride, scale_row_stride;
+} llm_kv_view;
+
+typedef struct {
+  int32_t dtype;                /* of q and out: LLM_BF16 or LLM_F32 */
+  int32_t n_seq, n_nodes, n_heads;  /* n_nodes 1..64; n_heads a multiple of the cache's heads */
+  const void* q;                /* [n_seq][n_nodes][n_heads][head_dim], already rotated */
+  void* out;                    /* the same shape; rows of nodes at or past counts[b] are left as they were */
+  int64_t q_strides[3], out_strides[3];  /* elements (seq, node, head), multiples of 16 bytes */
+  const llm_kv_view* cache;     /* one layer; the first n_seq sequences */
+  const llm_kv_view* tree;      /* the nodes' own rows (node j at row j), or NULL: the cache alone */
+  const int32_t* lens;          /* [n_seq] cache rows that every node sees (clamped to 0..rows) */
+  const uint64_t* mask;         /* [n_seq][n_nodes] bit j: the node sees tree row j (not read when tree is NULL) */
+  const int32_t* counts;        /* [n_seq] nodes of each sequence (clamped to 0..n_nodes), or NULL: n_nodes */
+  float scale;                  /* of the scores, usually 1/sqrt(head_dim) */
+} llm_tree_attention_args;
+
+/* out = softmax(scale q K^T over the visible rows) V; query head h reads kv
+ * head h / (n_heads / cache heads). Products on the tensor cores, sums in
+ * fp32; fp32 queries and their probabilities carry 24 bits, for bf16 queries
+ * the probabilities at least 8 (rounding below that of the output). A node that sees no row gets
+ * zeros. A row that a node does not see has no influence on it, whatever it
+ * holds. With n_nodes = 1 and tree = NULL this is one decode token's
+ * attention over a cache that already holds its row. */
+int llm_tree_attention(const llm_tree_attention_args* args, void* cuda_stream);
+
+/* probs[r] = the distribution the sampler of llm_set_sampling draws from:
+ * the top_k largest logits (1..64, ties to the lower id; 0: all of them), of
+ * softmax(logit / temperature) over them the shortest prefix whose mass reaches
+ * top_p, renormalised; every other token 0. fp32 rows at the given strides
+ * (elements); probs may be logits itself. A NaN logit counts as -inf, +inf as the
+ * largest finite value, a row without a finite logit gives zeros.
+ * UNSUPPORTED: top_p < 1 without a top_k, vocab over 524288 (819200 without
+ * top_k). */
+int llm_token_probs(const float* logits, int64_t logits_stride, float* probs, int64_t probs_stride, int32_t n_rows,
+                    int32_t vocab, float temperature, int32_t top_k, float top_p, void* cuda_stream);
+
+typedef struct {
+  int32_t n_seq, n_nodes, vocab;  /* n_nodes 1..64 */
+  const int32_t* tokens;          /* [n_seq][n_nodes]; the root's is not tested */
+  const int32_t* parents;         /* [n_seq][n_nodes] a lower node's index; other values: the node is never reached */
+  const int32_t* counts;          /* [n_seq] or NULL, as in llm_tree_attention */
+  const float* uniforms;          /* [n_seq][n_nodes] in [0, 1): entry i >= 1 tests node i, entry 0 draws the last token */
+  const float* probs;             /* [n_seq][n_nodes][vocab] target probabilities after each node */
+  int64_t probs_strides[2];       /* elements (seq, node) */
+  const float* draft_probs;       /* the same shape: what each node's children were drawn from (independently), or
+                                     NULL: the children are fixed choices (a top-k tree, a lookup) */
+  int64_t draft_strides[2];
+  const int32_t* targets;         /* [n_seq][n_nodes] greedy mode instead of probs: the target's choice after each node */
+  int32_t* path;                  /* [n_seq][n_nodes] out: kept nodes from the root on, then -1 */
+  int32_t* n_path;                /* [n_seq] out: how many (at least 1, the root) */
+  int32_t* next;                  /* [n_seq] out: the token that follows the last kept node */
+} llm_verify_tree_args;
+
+/* Speculative sampling over a tree; the tokens that come out are distributed
+ * as the target's own. From the root, the current node's children are tested
+ * in index order. r = probs[node], m = 1; child i with token x is kept when
+ * u_i q(x) < r(x) / m and becomes the current node; otherwise r becomes
+ * max(r/m - q, 0) and m its sum (a rejection that leaves nothing does not
+ * count). Without draft_probs q(x) = 1 and a rejected token loses its
+ * probability. When no child is left, next is the first token where the running
+ * sum of r exceeds u_0 times r's sum (vocab - 1 if r has no mass). Decisions
+ * are made with sums of at least 45 bits. Negative and NaN probabilities count
+ * as 0; a token outside 0..vocab-1 is never kept. counts[b] = 0: path all -1,
+ * n_path 0, next -1. Greedy mode: a child is kept when its token equals
+ * targets[current]; next = targets[last]. */
+int llm_verify_tree(const llm_verify_tree_args* args, void* cuda_stream);
+
+/* cache row lens[b] + k = tree row path[b][k] for k < n_path[b], in every layer
+ * and head, K, V and scales; new_lens[b] = lens[b] + n_path[b] (new_lens may be
+ * lens). Rows past the cache's end are dropped and new_lens stops there;
+ * entries of path outside 0..rows-1 leave their cache row as it was. path [n_seq][n_nodes]. */
+int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n_seq, int32_t n_nodes,
+                    const int32_t* lens, const int32_t* path, const int32_t* n_path, int32_t* new_lens,
+                    void* cuda_stream);
 
 #ifdef __cplusplus
 }
