@@ -45,7 +45,7 @@ EXPORTS = ["llm_model_create", "llm_model_destroy", "llm_prefill", "llm_prefill_
            "llm_decode_step_batch", "llm_kv_reset", "llm_kv_write", "llm_kv_read", "llm_kv_read_q8", "llm_kv_len",
            "llm_debug_hidden", "llm_debug_unpack", "llm_model_stats", "llm_profile_step", "llm_time_kernel", "llm_sync",
            "llm_last_error", "llm_op_matvec", "llm_op_matvec_w4a8", "llm_matvec_noalloc", "llm_phase_times", "llm_debug_fail_alloc",
-           "llm_debug_hidden_batch", "llm_tree_attention", "llm_token_probs", "llm_verify_tree", "llm_commit_tree"]
+           "llm_debug_hidden_batch", "llm_tree_attention", "llm_tree_status", "llm_token_probs", "llm_verify_tree", "llm_commit_tree"]
 
 
 # translation units of the library, compiled in parallel and linked into one shared object
@@ -170,6 +170,7 @@ def lib() -> C.CDLL:
             "llm_debug_fail_alloc": (i32, [i32]),
             "llm_debug_hidden_batch": (i32, [P, P]),
             "llm_tree_attention": (i32, [P, P]),
+            "llm_tree_status": (i32, [P]),
             "llm_token_probs": (i32, [P, C.c_int64, P, C.c_int64, i32, i32, C.c_float, i32, C.c_float, P]),
             "llm_verify_tree": (i32, [P, P]),
             "llm_commit_tree": (i32, [P, P, i32, i32, P, P, P, P, P]),
@@ -411,4 +412,4 @@ def matvec_noalloc(model: Model, name: str, x, y, stream: int | None = None) -> 
     _check(lib().llm_matvec_noalloc(model.h, name.encode(), _ptr(x), _ptr(y), stream), model.h)
 
 
-from .tree import KVView, commit_tree, token_probs, tree_attention, tree_masks, verify_tree  # noqa: E402
+from .tree import KVView, commit_tree, token_probs, tree_attention, tree_masks, tree_status, verify_tree  # noqa: E402

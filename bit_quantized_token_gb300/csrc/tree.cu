@@ -676,6 +676,21 @@ int cuda_bad(cudaError_t e, const char* what) {
   return op_error(e == cudaErrorMemoryAllocation ? LLM_ERR_OOM : LLM_ERR_CUDA, msg);
 }
 
+// Status word of the tree attention's bounded waits, one per device.
+__device__ int g_tree_status;
+
+cudaError_t status_word(int dev, int** p) {
+  static std::atomic<int*> known[64];
+  *p = dev < 64 ? known[dev].load(std::memory_order_acquire) : nullptr;
+  if (*p) return cudaSuccess;
+  void* a = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&a, g_tree_status);
+  if (e != cudaSuccess) return e;
+  *p = static_cast<int*>(a);
+  if (dev < 64) known[dev].store(*p, std::memory_order_release);
+  return cudaSuccess;
+}
+
 // Checks of one call: the current device, and that every buffer is its memory.
 struct Call {
   int dev = -1, n_sm = 0, rc = LLM_OK;
@@ -836,6 +851,9 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
   p.mask_seq = a->n_nodes;
   p.counts = a->counts;
   p.c = (float)((double)a->scale * 1.4426950408889634);
+  if (std::fabs(p.c) < 1e-30f) p.c = 1e-30f;  // a scale of 0: every score below 2^-60, and c times -inf still -inf
+  const cudaError_t es = status_word(c.dev, &p.status);
+  if (es != cudaSuccess) return cuda_bad(es, "status word");
   p.B = a->n_seq;
   p.n = a->n_nodes;
   p.Hkv = v.n_heads;
@@ -843,6 +861,18 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
   return finish(launch_tree_attn(p, (int)hd, a->dtype == LLM_F32, v.dtype == LLM_Q8G32, c.n_sm,
                                  static_cast<cudaStream_t>(cuda_stream)),
                 "tree attention launch");
+}
+
+int llm_tree_status(void* cuda_stream) {
+  Call c;
+  int *p = nullptr, st = 0;
+  cudaError_t e = c.e != cudaSuccess ? c.e : status_word(c.dev, &p);
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, p, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && st) e = cudaMemsetAsync(p, 0, sizeof(int), s);
+  if (e != cudaSuccess) return cuda_bad(e, "tree status");
+  return st & ST_TIMEOUT ? bad(LLM_ERR_TIMEOUT, "a device-side wait of a tree attention exceeded its limit") : LLM_OK;
 }
 
 int llm_token_probs(const float* logits, int64_t logits_stride, float* probs, int64_t probs_stride, int32_t n_rows,

@@ -56,6 +56,7 @@ struct TreeAttnParams {
   float c;                   // scale * log2(e)
   int B, n, Hkv, gq;
   int S;                     // CTAs of a cluster: splits of the keys
+  int* status;               // the device's status word (bounded waits)
 };
 
 // f32: q and out are fp32 (else bf16); q8: int8 rows. n_sm: SMs of the device.

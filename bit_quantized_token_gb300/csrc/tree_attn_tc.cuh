@@ -1,0 +1,707 @@
+// Tree attention over bf16 rows on the fifth-generation tensor cores.
+//
+// The products run transposed, so that the few query rows are the narrow side:
+//   S^T [128 keys x N rows] = K_tile Q^T     (A = the K tile as TMA lays it down, K-major)
+//   O^T [dims x N rows]    += V_tile^T P^T   (A = the V tile, read MN-major; B = P, [key][row])
+// A thread of a softmax warp is one key: it reads its scores from tensor
+// memory, turns them into probabilities and writes them as a row of P, so no
+// exchange between threads is needed. Instead of the running maximum, a
+// reference within 2^60 of it does: it starts as the first key's scores and is
+// renewed (and O rescaled) only when a score passes it by more than 2^60; bf16
+// and fp32 keep their relative precision over that range.
+// A tile is read as units of 128 keys x 64 dims (16 KB, one TMA box, 128-byte
+// swizzle): K and V units stream through one ring. Of each P V product's 128
+// rows the upper 64 read ones instead of V, so lanes 64.. hold the sums of P.
+// Warp roles: 4 softmax warps per block of NB rows (G blocks share the units),
+// one TMA warp, one warp that issues every MMA. A block's next scores are
+// computed right after its P V, while the other block (or the other CTA on the
+// SM, where shared memory lets two fit) is in its softmax.
+#pragma once
+#include <cuda.h>
+
+#include "tree_attn.cuh"
+
+namespace llmq {
+
+struct TreeAttnTcParams {
+  CUtensorMap ck, cv, tk, tv;  // cache and tree rows: [seq][head][row][dim], boxes of 128 rows x 64 dims
+  TreeAttnParams p;
+};
+
+constexpr int kMaxSplits = 8;  // CTAs of a cluster (the portable limit)
+
+template <int HD, bool F32, int NB, int G>
+struct TreeTc {
+  static constexpr int N = NB * G, BK = 128, H = HD / 64;
+  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : (N > 64 ? 1 : 2);  // parts of the queries, of P
+  static constexpr int NT = 32 * (4 * G + 2);
+  static constexpr int kUnit = BK * 128;                                 // bytes: 64 dims of a K or V tile
+  static constexpr int kRowP = NB >= 64 ? 128 : 2 * NB;                  // bytes of a key's row of a P atom
+  static constexpr int kPart = BK * 2 * NB;                              // bytes of a part of P of one block
+  static constexpr int kP = G * NP * kPart, kQ = NQ * N * HD * 2, kOnes = 2048;
+  static constexpr int kOffRow = 1024;                                   // of the small arrays: [N] row masks
+  static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4 * kMaxSplits) + 3 * kTreeMaxNodes * (HD / 32) * 4;
+  static constexpr int kFixed = kP + kQ + kOnes + kSmall + 1024;
+  static constexpr int kOut = N * HD * 4;                                // fp32 results, over the ring at the end
+  static constexpr int kLimit = 232448, kHalf = 115712;                  // shared memory of a CTA alone, of two on an SM
+  static constexpr int kMin = 2 * H > kOut / kUnit ? 2 * H : kOut / kUnit;
+  static constexpr bool two = kFixed + (kMin > 4 ? kMin : 4) * kUnit <= kHalf;
+  static constexpr int fit = ((two ? kHalf : kLimit) - kFixed) / kUnit;
+  static constexpr int NST = fit < 12 ? fit : 12;
+  static constexpr int kSmem = NST * kUnit + kFixed;
+  static_assert(NST >= kMin && NST >= 3, "shared memory");
+  static constexpr int kUsed = (1 + H) * N;                              // S, and O of every 64 dims
+  static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+};
+
+// A warp's bounded wait with one answer for all lanes.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status);
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, status));
+}
+// A bounded wait: past the limit the CTA's abort flag and the device's status
+// word are set and every wait of the CTA returns at once, so that all loops
+// run to their end (on data that does not matter) and no barrier is missed.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  unsigned long long start = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 63) {
+      if (*abort_flag) return false;
+      const unsigned long long t = globaltimer();
+      if (start == 0) {
+        start = t;
+      } else if (t - start > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(status, ST_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int row, int head, int seq,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(row), "r"(head), "r"(seq), "r"(smem_u32(bar))
+      : "memory");
+}
+// The MMA warp runs converged, so that addresses stay in uniform registers, and
+// one elected lane (always the same of a full warp) issues.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      :
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  if (elect_lane())
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// Shared memory matrix descriptor: start, leading and stride byte offsets in
+// 16-byte units; swizzle 2: 128 B, 4: 64 B, 6: 32 B.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t start, uint32_t lbo, uint32_t sbo, uint64_t swizzle) {
+  return (uint64_t)((start & 0x3FFFF) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
+         (1ull << 46) | (swizzle << 61);
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// W columns of this warp's 32 lanes, one lane per thread
+template <int W>
+__device__ __forceinline__ void tc_ld(float (&v)[W], uint32_t addr) {
+  static_assert(W == 16 || W == 32, "columns");
+  if constexpr (W == 16)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(addr));
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+                 : "r"(addr));
+}
+// Waits for the loads; the values pass through, so that no use of them moves ahead of the wait.
+template <int W>
+__device__ __forceinline__ void tc_wait_ld(float (&v)[W]) {
+  if constexpr (W == 16)
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]) : : "memory");
+  else
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]) : : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// the 128 threads of softmax group g (named barriers 1..G)
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory"); }
+__device__ __forceinline__ bool group_any(int g, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(g + 1)
+      : "memory");
+  return r != 0;
+}
+
+template <int HD, bool F32, int NB, int G>
+__global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB, G>::two ? 2 : 1) tree_attn_tc_kernel(
+    const __grid_constant__ TreeAttnTcParams tp) {
+  using C = TreeTc<HD, F32, NB, G>;
+  constexpr int N = C::N, NT = C::NT, NST = C::NST, NQ = C::NQ, NP = C::NP, NG = HD / 32, BK = C::BK, H = C::H;
+  constexpr float kLazy = 60.f, kNone = -3e38f;  // kNone: the reference before any visible score
+  extern __shared__ uint8_t sm_raw[];
+  const TreeAttnParams& p = tp.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.z, hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
+  const int len_b = p.lens[b], cnt_b = p.counts ? p.counts[b] : p.n;
+  const int cnt = min(max(cnt_b, 0), p.n);
+  if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
+  const int len = min(max(len_b, 0), p.cache.rows);
+  const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
+  const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S);
+
+  uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  uint8_t* sring = sm;
+  uint8_t* sp = sring + NST * C::kUnit;   // [G][NP] parts of P
+  uint8_t* sq = sp + C::kP;               // [NQ][H][N][128 B]
+  uint8_t* sones = sq + C::kQ;
+  uint8_t* small = sones + C::kOnes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(small);
+  uint64_t *full = bars, *empty = bars + 12, *s_full = bars + 24, *p_full = bars + 26, *drain = bars + 28;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);
+  int* s_any = reinterpret_cast<int*>(small + 260);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 264);
+  uint64_t* smask = reinterpret_cast<uint64_t*>(small + 512);          // [64]
+  uint64_t* srow = reinterpret_cast<uint64_t*>(small + C::kOffRow);    // [N] what each row sees of the tree
+  float* sm_m = reinterpret_cast<float*>(srow + N);             // [N] references
+  float* sm_w = sm_m + N;                                       // [4][N]
+  float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);        // [N]
+  float* sw = reinterpret_cast<float*>(sml + N);                // [kMaxSplits][N]
+  uint32_t* snf = reinterpret_cast<uint32_t*>(sw + kMaxSplits * N);     // [3][64][NG]
+
+  // TMA: the units in the order in which the MMAs release them
+  auto request = [&](int i) {  // unit i: of tile t0 + i / 2H, K then V
+    const int t = t0 + i / (2 * H), u = i % (2 * H), slot = i % NST;
+    const bool tree = t >= n_pre;
+    const CUtensorMap* map = u >= H ? (tree ? &tp.tv : &tp.cv) : (tree ? &tp.tk : &tp.ck);
+    mbar_expect_tx(full + slot, C::kUnit);
+    tma_box(sring + slot * C::kUnit, map, 64 * (u % H), tree ? 0 : t * BK, hkv, b, full + slot);
+  };
+  const int n_units = 2 * H * (t1 - t0);
+  if (warp == 4 * G) {  // the ring's barriers are this warp's own: the first units are on their way at once
+    if (lane == 0) {
+      *s_abort = 0;
+      *s_any = 0;
+      for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+      mbar_fence_init();
+      for (int i = 0; i < NST && i < n_units; ++i) request(i);
+    }
+  } else if (warp == 4 * G + 1) {
+    if (lane == 0) {
+      for (int g = 0; g < G; ++g) mbar_init(s_full + g, 1), mbar_init(p_full + g, 128);
+      mbar_init(drain, 1);
+      mbar_fence_init();
+    }
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                 "r"((uint32_t)C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else {
+    // the query rows' bf16 parts, 128-byte rows of 64 dims, chunks permuted as by TMA's 128-byte swizzle
+    if (p.tree.k)
+      for (int i = tid; i < kTreeMaxNodes; i += 128 * G)
+        smask[i] = i < cnt ? p.mask[(int64_t)b * p.mask_seq + i] : 0;
+#pragma unroll 2
+    for (int i = tid; i < N * (HD / 8); i += 128 * G) {
+      const int r = i / (HD / 8), ch = i % (HD / 8), node = (m0 + r) / p.gq, h = hkv * p.gq + (m0 + r) % p.gq;
+      const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
+      uint8_t* dst = sq + (ch / 8) * N * 128 + r * 128 + 16 * ((ch & 7) ^ (r & 7));
+      if constexpr (F32) {
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (node < cnt) {
+          const float4 lo = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off);
+          const float4 hi = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off + 4);
+          x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+        }
+        float part[8][3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split_bf16<3>(x[e], part[e]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(dst + k * N * HD * 2) =
+              make_uint4(pack_bf16x2(part[0][k], part[1][k]), pack_bf16x2(part[2][k], part[3][k]),
+                         pack_bf16x2(part[4][k], part[5][k]), pack_bf16x2(part[6][k], part[7][k]));
+      } else {
+        *reinterpret_cast<uint4*>(dst) = node < cnt
+                                             ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    for (int i = tid; i < C::kOnes / 16; i += 128 * G)
+      reinterpret_cast<uint4*>(sones)[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (p.tree.k && t1 == n_tiles)
+      for (int i = tid; i < 3 * kTreeMaxNodes * NG; i += 128 * G) snf[i] = 0;
+    for (int i = tid; i < N; i += 128 * G) sm_m[i] = kNone;
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;  // S of block g at columns g NB, O of 64 dims u at N (1 + u) + g NB
+  uint64_t seen = 0;              // tree rows that some node sees
+  if (p.tree.k) {
+    const uint64_t a = smask[lane] | smask[lane + 32];
+    seen = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(a >> 32)) << 32) |
+           __reduce_or_sync(0xffffffffu, (uint32_t)a);
+    if (cnt < 64) seen &= (1ull << cnt) - 1;
+  }
+
+  if (warp == 4 * G) {
+    if (lane == 0) {
+      int i = min(NST, n_units);
+      for (; i < n_units; ++i) {
+        if (!tc_wait(empty + i % NST, (i / NST - 1) & 1, s_abort, p.status)) break;
+        request(i);
+      }
+      if (*s_abort)  // leave no copy in flight
+        for (int j = max(0, i - NST); j < i; ++j) {
+          const unsigned long long s0 = globaltimer();
+          while (!mbar_try_wait(full + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
+          }
+        }
+    }
+  } else if (warp == 4 * G + 1) {
+    // ---- MMA: commits release units and publish scores
+    constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NB >> 3) << 17) | (8u << 24);
+    constexpr uint32_t idesc_s = base_i, idesc_o = base_i | (1u << 15) | (1u << 16);  // O: A and B MN-major
+    constexpr uint64_t swp = NB >= 64 ? 2 : (NB == 32 ? 4 : 6);
+    constexpr uint32_t step_p = 16 * C::kRowP, sbo_p = 8 * C::kRowP;
+    const uint32_t uq = smem_u32(sq), up = smem_u32(sp), ur = smem_u32(sring), uo = smem_u32(sones);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto scores = [&](int g, int t) {
+#pragma unroll
+      for (int u = 0; u < H; ++u) {
+        const int i = 2 * H * (t - t0) + u, slot = i % NST;
+        if (!tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status)) return false;
+        tc_fence_after();
+        const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
+        const uint64_t dq = tc_desc(uq + u * N * 128 + g * NB * 128, 16, 1024, 2);
+        if (elect_lane()) {
+#pragma unroll
+          for (int k = NQ - 1; k >= 0; --k)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
+              tc_mma(tm + g * NB, da + 2 * ks, dq + (k * H * N * 128 >> 4) + 2 * ks, idesc_s,
+                     u > 0 || k < NQ - 1 || ks > 0);
+        }
+        __syncwarp();
+        if (g == G - 1) tc_commit(empty + slot);
+      }
+      tc_commit(s_full + g);
+      return true;
+    };
+    bool ok = true;
+    for (int g = 0; g < G && ok && t0 < t1; ++g) ok = scores(g, t0);
+    for (int t = t0; t < t1 && ok; ++t)
+#pragma unroll 1
+      for (int g = 0; g < G && ok; ++g) {
+        ok = tc_wait_warp(p_full + g, (t - t0) & 1, s_abort, p.status);
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+          const int i = 2 * H * (t - t0) + H + u, slot = i % NST;
+          ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v = ur + slot * C::kUnit;
+          // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
+          const uint64_t da = tc_desc(v, uo - v, 1024, 2);
+          const uint64_t dp = tc_desc(up + g * NP * C::kPart, BK * 128, sbo_p, swp);
+          if (elect_lane()) {
+#pragma unroll
+            for (int k = NP - 1; k >= 0; --k)
+#pragma unroll
+              for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
+                tc_mma(tm + N * (1 + u) + g * NB, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                       dp + ((k * C::kPart + ks * step_p) >> 4), idesc_o, t > t0 || k < NP - 1 || ks > 0);
+          }
+          __syncwarp();
+          if (g == G - 1) tc_commit(empty + slot);
+        }
+        if (!ok) break;
+        if (t + 1 < t1) ok = scores(g, t + 1);
+        else tc_commit(s_full + g);  // the block's O is complete
+      }
+    if (!ok) {  // no MMA may outlive its operands
+      tc_commit(drain);
+      const unsigned long long s0 = globaltimer();
+      while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
+      }
+    }
+  } else {
+    // ---- softmax: thread = key
+    const int g = warp >> 2, key = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * NB, tO = tS + N;
+    float* m = sm_m + g * NB;
+    const float masked = p.c < 0.f ? INFINITY : -INFINITY;  // times c: -inf (c is not 0)
+    if (p.tree.k)
+      for (int r = key; r < NB; r += 128) {
+        const int node = (m0 + g * NB + r) / p.gq;
+        srow[g * NB + r] = node < cnt ? smask[node] & seen : 0;
+      }
+    group_sync(g);
+    // whether row r of the block sees this thread's tree row
+    const uint32_t* vis = reinterpret_cast<const uint32_t*>(srow + g * NB) + (warp & 1);
+    auto sees = [&](int r) { return key < kTreeMaxNodes && ((vis[2 * r] >> lane) & 1); };
+    for (int t = t0; t < t1; ++t) {
+      const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
+      const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
+      if (!whole) {  // V rows that are not there become zeros, non-finite tree values too (noted for the rows that see them)
+        for (int u = 0; u < H; ++u) {
+          const int i = 2 * H * (t - t0) + H + u;
+          tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
+        }
+#pragma unroll 4
+        for (int c = 0; c < HD / 8 && (tree || !valid); ++c) {
+          const int slot = (2 * H * (t - t0) + H + c / 8) % NST;
+          uint4* x = reinterpret_cast<uint4*>(sring + slot * C::kUnit + key * 128 + 16 * ((c & 7) ^ (key & 7)));
+          if (!valid) {
+            *x = make_uint4(0u, 0u, 0u, 0u);
+          } else if (tree) {
+            const uint4 w = *x;
+            uint32_t inf = 0;  // whether an exponent is all ones
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t v = (&w.x)[j] & 0x7F807F80u;
+              inf |= (v & 0xFFFFu) == 0x7F80u || (v >> 16) == 0x7F80u;
+            }
+            if (inf) {
+              uint16_t* e = reinterpret_cast<uint16_t*>(x);
+#pragma unroll 1
+              for (int j = 0; j < 8; ++j)
+                if ((e[j] & 0x7F80u) == 0x7F80u) {
+                  const int kind = (e[j] & 0x7Fu) ? 2 : e[j] >> 15, d = 8 * c + j;
+                  atomicOr(snf + (kind * kTreeMaxNodes + key) * NG + (d >> 5), 1u << (d & 31));
+                  e[j] = 0;
+                }
+              *s_any = 1;
+            }
+          }
+        }
+      }
+      tc_wait(s_full + g, (t - t0) & 1, s_abort, p.status);
+      tc_fence_after();
+      if (t == t0) {  // the references: the score of the first key that a row sees (renewed below if not finite)
+        float* first = reinterpret_cast<float*>(sp + g * NP * C::kPart);  // [64][NB], where P comes to lie
+        if (warp < 4 * g + (tree ? 2 : 1))
+#pragma unroll 1
+          for (int c0 = 0; c0 < NB; c0 += 16) {
+            float s[16];
+            tc_ld(s, tS + c0);
+            tc_wait_ld(s);
+            if (tree || lane == 0)
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<float4*>(first + key * NB + c0 + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+          }
+        group_sync(g);
+        for (int r = key; r < NB; r += 128) {
+          const int j = tree ? __ffsll(srow[g * NB + r]) - 1 : 0;
+          const float y = j >= 0 ? first[j * NB + r] * p.c : INFINITY;
+          m[r] = fabsf(y) < 1e38f ? y : kNone;
+        }
+        group_sync(g);
+      }
+      uint8_t* prow = sp + g * NP * C::kPart + key * C::kRowP;
+      for (;;) {
+        // probabilities with the references as they are; the largest excess over them
+        float top = -INFINITY;
+        constexpr int W = NB >= 32 ? 32 : 16;
+        auto take = [&](float (&s)[W], int c0) {
+          if (tree) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+              if (!sees(c0 + j)) s[j] = masked;
+          } else if (!whole && !valid) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) s[j] = masked;
+          }
+#pragma unroll
+          for (int h = 0; h < W / 8; ++h) {
+            float part[8][NP];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float y = fmaf(s[8 * h + j], p.c, -m[c0 + 8 * h + j]);
+              top = fmaxf(top, y);
+              split_bf16<NP>(ex2(y), part[j]);
+            }
+            const int chunk = (c0 + 8 * h) / 8, sel = NB >= 64 ? key & 7 : (NB == 32 ? (key >> 1) & 3 : (key >> 2) & 1);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+              *reinterpret_cast<uint4*>(prow + k * C::kPart + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ sel)) =
+                  make_uint4(pack_bf16x2(part[0][k], part[1][k]), pack_bf16x2(part[2][k], part[3][k]),
+                             pack_bf16x2(part[4][k], part[5][k]), pack_bf16x2(part[6][k], part[7][k]));
+          }
+        };
+        float sa[W], sb[W];  // the next columns load while these are worked on
+        tc_ld(sa, tS);
+#pragma unroll 1
+        for (int c0 = 0; c0 < NB; c0 += 2 * W) {
+          tc_wait_ld(sa);
+          if (c0 + W < NB) tc_ld(sb, tS + c0 + W);
+          take(sa, c0);
+          if (c0 + W < NB) {
+            tc_wait_ld(sb);
+            if (c0 + 2 * W < NB) tc_ld(sa, tS + c0 + 2 * W);
+            take(sb, c0 + W);
+          }
+        }
+        if (!group_any(g, top > kLazy)) break;
+        // renew the references: the maxima per warp, then over the four; rescale O and the sums
+#pragma unroll 1
+        for (int c0 = 0; c0 < NB; c0 += 16) {
+          float s[16];
+          tc_ld(s, tS + c0);
+          tc_wait_ld(s);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const bool in = tree ? sees(c0 + j) : valid;
+            float y = in ? s[j] * p.c : -INFINITY;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+            if (lane == 0) sm_w[(warp & 3) * N + g * NB + c0 + j] = y;
+          }
+        }
+        group_sync(g);
+        for (int r = key; r < NB; r += 128) {
+          const float* w = sm_w + g * NB + r;
+          const float old = m[r], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
+          m[r] = now;
+          sw[g * NB + r] = old == now ? 1.f : exp2f(old - now);
+        }
+        group_sync(g);
+        if (t > t0) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < NB * H; c0 += 16) {
+            const uint32_t at = tO + (c0 / NB) * N + c0 % NB;
+            float s[16];
+            tc_ld(s, at);
+            tc_wait_ld(s);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[j] *= sw[g * NB + c0 % NB + j];
+            tc_st16(at, s);
+          }
+          tc_wait_st();
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(p_full + g);
+    }
+    // ---- O^T and the sums to shared memory, [row][dim]
+    if (t0 < t1) tc_wait(s_full + g, (t1 - t0) & 1, s_abort, p.status);
+    tc_fence_after();
+    // every block's last MMAs have read the ring and P before any block writes over them
+    asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
+    float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
+    const bool have = t0 < t1;
+#pragma unroll 1
+    for (int c0 = 0; c0 < NB * H; c0 += 16) {
+      const int u = c0 / NB, r0 = c0 % NB;
+      float s[16];
+      if (have) {
+        tc_ld(s, tO + u * N + r0);
+        tc_wait_ld(s);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float x = have ? s[j] : 0.f;
+        if (key < 64) so[(r0 + j) * HD + 64 * u + key] = x;
+        if (u == 0 && key == 64) sml[g * NB + r0 + j] = make_float2(m[r0 + j], x);
+      }
+    }
+    if (p.tree.k && have && t1 == n_tiles && *s_any && key < 64) {  // non-finite tree values, where they are seen
+      for (int d = key; d < HD; d += 64)
+        for (int r = 0; r < NB; ++r)
+          for (uint64_t v = srow[g * NB + r]; v; v &= v - 1) {
+            const int j = __ffsll(v) - 1;
+            const float bad[3] = {INFINITY, -INFINITY, NAN};
+#pragma unroll
+            for (int kind = 0; kind < 3; ++kind)
+              if ((snf[(kind * kTreeMaxNodes + j) * NG + (d >> 5)] >> (d & 31)) & 1) so[r * HD + d] += bad[kind];
+          }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cg::cluster_group cl = cg::this_cluster();
+  __syncthreads();
+  // ---- the cluster's S key ranges: rank k writes its share of the rows
+  if (p.S > 1) cl.sync();
+  float* so = reinterpret_cast<float*>(sm);
+  for (int r = tid; r < N; r += NT) {
+    float2 ml[kMaxSplits];  // all loads in flight: a rank's answer takes long
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) ml[k] = k < p.S ? cl.map_shared_rank(sml, k)[r] : make_float2(kNone, 0.f);
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) {
+      ml[k].x = ml[k].x <= kNone ? 0.f : exp2f(ml[k].x - M);
+      L += ml[k].y * ml[k].x;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+      if (k < p.S) sw[k * N + r] = ml[k].x * inv;
+  }
+  __syncthreads();
+  const int rows = min(N, cnt * p.gq - m0), n4 = rows * HD / 4;
+  const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
+  for (int i = i0 + tid; i < i1; i += NT) {
+    const int r = i / (HD / 4), node = (m0 + r) / p.gq, h = hkv * p.gq + (m0 + r) % p.gq;
+    float4 x[kMaxSplits], a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+      if (k < p.S) x[k] = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k))[i];
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+      if (k < p.S) {
+        const float f = sw[k * N + r];
+        a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y), a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
+      }
+    const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % (HD / 4));
+    if constexpr (F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = a;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off) =
+          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+  if (p.S > 1) cl.sync();  // a CTA's shared memory lives until every rank has read it
+  // Freed last: no two CTAs that hold and that wait for tensor memory share an
+  // SM (kernels whose columns exceed half take all of its shared memory), so a
+  // CTA that holds it while its cluster gathers cannot keep a peer waiting.
+  if (warp == 4 * G + 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kCols));
+  }
+}
+
+// cuTensorMapEncodeTiled, looked up once; null where the driver has none.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiled tensor_map_encoder() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// The map of one K or V tensor [seq][head][row][dim]; false where TMA cannot address it.
+inline bool encode_rows(CUtensorMap* map, const uint8_t* base, const KvRows& r, int B, int heads, int hd) {
+  const EncodeTiled enc = tensor_map_encoder();
+  if (!enc || r.rows < 1) return false;
+  const int64_t row = r.rows > 1 ? r.row : hd;
+  const int64_t head = heads > 1 ? r.head : row * r.rows, seq = B > 1 ? r.seq : head * heads;
+  const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)r.rows, (cuuint64_t)heads, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)row * 2, (cuuint64_t)head * 2, (cuuint64_t)seq * 2};
+  for (const cuuint64_t s : strides)
+    if (s == 0 || s % 16 || s >= (1ull << 40)) return false;
+  const cuuint32_t box[4] = {64, 128, 1, 1}, step[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD, bool F32, int NB, int G>
+cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
+  using C = TreeTc<HD, F32, NB, G>;
+  const auto kern = tree_attn_tc_kernel<HD, F32, NB, G>;
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(kern, C::kSmem);
+  if (e != cudaSuccess) return e;
+  TreeAttnParams& p = tp.p;
+  const int m_tiles = (p.n * p.gq + C::N - 1) / C::N;
+  const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
+  const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
+  int S = 1;
+  // split the keys until every SM has a CTA: more splits cost their merges (32 sequences of 512..2048 rows,
+  // 256 clusters: 51.8 / 56.8 / 66.6 us for 1 / 2 / 4; 128 clusters of 1024..8192 rows: 232 / 213 / 226)
+  while (S < kMaxSplits && S < tiles && clusters * S < n_sm) S *= 2;
+  p.S = S;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(S, p.Hkv * m_tiles, p.B);
+  cfg.blockDim = dim3(C::NT);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tp);
+}
+
+// bf16 rows; false: TMA cannot address these tensors (strides of 0, or of 2^40 bytes).
+template <int HD>
+bool launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStream_t st, cudaError_t* e) {
+  TreeAttnTcParams tp;
+  tp.p = p;
+  const bool cache = p.cache.rows > 0, tree = p.tree.k != nullptr;
+  if (cache && !(encode_rows(&tp.ck, p.cache.k, p.cache, p.B, p.Hkv, HD) &&
+                 encode_rows(&tp.cv, p.cache.v, p.cache, p.B, p.Hkv, HD)))
+    return false;
+  if (tree && !(encode_rows(&tp.tk, p.tree.k, p.tree, p.B, p.Hkv, HD) &&
+                encode_rows(&tp.tv, p.tree.v, p.tree, p.B, p.Hkv, HD)))
+    return false;
+  const int M = p.n * p.gq;
+  // two blocks of rows once there are 32: their softmax and MMAs overlap, and
+  // eight softmax warps fill an SM's schedulers twice
+  if (f32)
+    *e = M <= 16   ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st)
+         : M <= 32 ? launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st)
+                   : launch_tree_tc_t<HD, true, 32, 2>(tp, n_sm, st);
+  else
+    *e = M <= 16   ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)
+         : M <= 32 ? launch_tree_tc_t<HD, false, 16, 2>(tp, n_sm, st)
+         : M <= 64 ? launch_tree_tc_t<HD, false, 32, 2>(tp, n_sm, st)
+         : HD == 128 || M <= 128 ? launch_tree_tc_t<HD, false, 64, 2>(tp, n_sm, st)
+                                 : launch_tree_tc_t<HD, false, HD == 64 ? 128 : 64, 2>(tp, n_sm, st);
+  return true;
+}
+
+}  // namespace llmq

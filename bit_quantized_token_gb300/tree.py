@@ -157,6 +157,12 @@ def tree_attention(q, cache: KVView, tree: KVView | None, lens, mask, out, count
         _check(rc)
 
 
+def tree_status(stream: int | None = None) -> None:
+    """Wait for the stream and raise if a tree attention's device-side wait passed its limit; see llm_tree_status."""
+    L = _lib or _load()
+    _check(L.llm_tree_status(stream))
+
+
 def token_probs(logits, out, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0,
                 stream: int | None = None) -> None:
     """out [rows, vocab] = the distribution that set_sampling's options draw from; see llm_token_probs."""

@@ -427,6 +427,11 @@ typedef struct {
  * attention over a cache that already holds its row. */
 int llm_tree_attention(const llm_tree_attention_args* args, void* cuda_stream);
 
+/* Wait for `cuda_stream` and report whether a device-side wait of a
+ * llm_tree_attention on the current device passed its limit (2 s) since the last call
+ * (TIMEOUT: the outputs of that call are not valid). */
+int llm_tree_status(void* cuda_stream);
+
 /* probs[r] = the distribution the sampler of llm_set_sampling draws from:
  * the top_k largest logits (1..64, ties to the lower id; 0: all of them), of
  * softmax(logit / temperature) over them the shortest prefix whose mass reaches
