@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 #include <utility>
 
 #include "common.cuh"
@@ -38,54 +39,110 @@ cudaError_t launch_cluster(Kern kern, dim3 grid, int threads, int cluster, size_
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// ---- sums that decide integers --------------------------------------------------
+// A sum over a vocabulary picks a token, so it is carried far beyond fp32: as an
+// unevaluated pair of floats (two-sums and fused products, ~2^-46 relative).
+// This GPU has 64 times fewer fp64 than fp32 lanes: the same reductions in fp64
+// took 10 us of a 20 us verification.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const Two t = two_sum(a.h, b.h);
+  const float l = __fadd_rn(t.l, __fadd_rn(a.l, b.l)), h = __fadd_rn(t.h, l);
+  return {h, __fsub_rn(l, __fsub_rn(h, t.h))};
+}
+__device__ __forceinline__ Two two_prod(float a, float b) {
+  const float h = __fmul_rn(a, b);
+  return {h, __fmaf_rn(a, b, -h)};
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  const Two p = two_prod(a.h, b.h);
+  const float l = __fadd_rn(p.l, __fadd_rn(__fmul_rn(a.h, b.l), __fmul_rn(a.l, b.h))), h = __fadd_rn(p.h, l);
+  return {h, __fsub_rn(l, __fsub_rn(h, p.h))};
+}
+__device__ __forceinline__ bool operator<(Two a, Two b) {
+  return a.h < b.h || (a.h == b.h && a.l < b.l);  // both normalised: |l| at most half a step of h
+}
+__device__ __forceinline__ Two two_recip(Two m) {  // one Newton step from the fp32 reciprocal
+  const float r = __fdiv_rn(1.f, m.h);
+  const float e = __fsub_rn(__fmaf_rn(-m.h, r, 1.f), __fmul_rn(m.l, r));
+  const float l = __fmul_rn(r, e), h = __fadd_rn(r, l);
+  return {h, __fsub_rn(l, __fsub_rn(h, r))};
+}
+__device__ __forceinline__ Two two_xor(Two v, int o) {
+  return {__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)};
+}
+template <int LANES>
+__device__ __forceinline__ Two two_reduce(Two v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v = v + two_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ Two two_scan(Two v, int lane) {  // inclusive, over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two y = {__shfl_up_sync(0xffffffffu, v.h, o), __shfl_up_sync(0xffffffffu, v.l, o)};
+    if (lane >= o) v = v + y;
+  }
+  return v;
+}
+
 // ---- token probabilities -----------------------------------------------------
 // p_j = 2^(c (l_j - m)) / sum over the kept tokens, c = log2(e) / T. A cluster
 // owns a row: every CTA keeps its slice in shared memory, so the row is read
-// once and written once; a CTA's (max, sum) and, with top_k, its sorted top_k
+// once and written once; a CTA's (max, sum) or, with top_k, its sorted top_k
 // candidates are all that crosses the cluster. A NaN counts as -inf, +inf as
 // the largest finite value; a row without a finite logit is all zeros.
 constexpr int kProbThreads = 512;
 constexpr int kProbSlice = 51200;  // floats of a row that one CTA keeps
+constexpr int kProbTopSlice = 32768;
 
 __device__ __forceinline__ float clean_logit(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
 
-// Sum / max over the CTA in a fixed order, to every thread.
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float* s_warp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float y = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? fmaxf(v, y) : v + y;
+// A slice of a row in global memory: [off, end) from a 16-byte boundary on,
+// whole float4s [v0, v1), up to three floats before and after them.
+struct Slice {
+  int off, end, v0, v1, head, tail;
+  __device__ Slice(const float* p, int n) {
+    off = (int)((reinterpret_cast<uintptr_t>(p) >> 2) & 3);
+    end = off + n;
+    v0 = (off + 3) / 4;
+    v1 = end / 4;
+    head = min(4 * v0, end);
+    tail = max(4 * v1, head);
   }
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s_warp[threadIdx.x & 31 & (kProbThreads / 32 - 1)];
-#pragma unroll
-  for (int o = kProbThreads / 64; o > 0; o >>= 1) {
-    const float y = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? fmaxf(v, y) : v + y;
-  }
-  __syncthreads();
-  return v;
-}
+};
 
-// The slice [a, a + n) of a row to shared memory, aligned as in global memory
-// (the returned offset, 0..3 floats), 16 bytes at a time where it is; f(x, i)
-// maps the value of element i.
+// The slice [p, p + n) to shared memory at the same alignment; f(x) maps a
+// group of one or four values. Four 16-byte loads of a thread in flight.
 template <typename F>
-__device__ __forceinline__ int load_slice(float* sx, const float* src, int n, F f) {
-  const int off = (int)((reinterpret_cast<uintptr_t>(src) >> 2) & 3);
-  const float* base = src - off;
-  const int end = off + n, v0 = (off + 3) / 4, v1 = end / 4;
-  for (int i = v0 + threadIdx.x; i < v1; i += kProbThreads) {
-    float4 x = __ldcs(reinterpret_cast<const float4*>(base) + i);
-    x.x = f(x.x), x.y = f(x.y), x.z = f(x.z), x.w = f(x.w);
-    reinterpret_cast<float4*>(sx)[i] = x;
+__device__ __forceinline__ void load_slice(float* sx, const float* p, const Slice& c, F f) {
+  const float4* base = reinterpret_cast<const float4*>(p - c.off);
+  constexpr int U = 4;
+  for (int i0 = c.v0 + threadIdx.x; i0 < c.v1; i0 += U * kProbThreads) {
+    float4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kProbThreads < c.v1) x[u] = __ldcs(base + i0 + u * kProbThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * kProbThreads < c.v1) {
+        float v[4] = {clean_logit(x[u].x), clean_logit(x[u].y), clean_logit(x[u].z), clean_logit(x[u].w)};
+        f(v);
+        reinterpret_cast<float4*>(sx)[i0 + u * kProbThreads] = make_float4(v[0], v[1], v[2], v[3]);
+      }
   }
-  const int head = min(4 * v0, end), tail = max(4 * v1, head);
-  if (threadIdx.x < head - off) sx[off + threadIdx.x] = f(base[off + threadIdx.x]);
-  if (threadIdx.x < end - tail) sx[tail + threadIdx.x] = f(base[tail + threadIdx.x]);
-  return off;
+  const int e = threadIdx.x < 4 ? c.off + (int)threadIdx.x : c.tail + (int)threadIdx.x - 4;
+  if (threadIdx.x < 8 && (threadIdx.x < 4 ? e < c.head : e < c.end)) {
+    float v[1] = {clean_logit(p[e - c.off])};
+    f(v);
+    sx[e] = v[0];
+  }
 }
 
 struct ProbRange {  // slice of CTA `rank` of C: starts on a multiple of 4
@@ -97,72 +154,98 @@ struct ProbRange {  // slice of CTA `rank` of C: starts on a multiple of 4
   }
 };
 
+// Every token: a thread's running (max, sum) while the slice streams in, one
+// reduction, one exchange, and the probabilities computed on the way out.
+// 256 x 151936: read and written once, 311 MB.
 __global__ void __launch_bounds__(kProbThreads) softmax_rows_kernel(const TokenProbsParams p) {
   extern __shared__ __align__(16) float sx[];
-  __shared__ float s_warp[32];
-  __shared__ float2 s_ms;
+  __shared__ float2 s_warp[kProbThreads / 32];
+  __shared__ float2 s_ms[16];
   cg::cluster_group cl = cg::this_cluster();
-  const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x;
+  const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
+  auto started = cl.barrier_arrive();  // shared memory of another CTA: only once that CTA runs
   const ProbRange r(p.V, rank, C);
-  float mx = -INFINITY;
-  const int off = load_slice(sx, p.logits + (int64_t)row * p.l_row + r.a, r.n, [&](float x) {
-    x = clean_logit(x);
-    mx = fmaxf(mx, x);
-    return x;
-  });
-  mx = block_reduce<true>(mx, s_warp);  // its barriers publish sx
-  const float m = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f;
-  for (int i = off + tid; i < off + r.n; i += kProbThreads) {
-    const float e = exp2f((sx[i] - m) * p.c);
-    sx[i] = e;
-    sum += e;
-  }
-  sum = block_reduce<false>(sum, s_warp);
-  if (tid == 0) s_ms = make_float2(mx, sum);
-  cl.sync();
-  float M = -INFINITY, S = 0.f;
-  for (int k = 0; k < C; ++k) M = fmaxf(M, cl.map_shared_rank(&s_ms, k)->x);
-  for (int k = 0; k < C; ++k) {
-    const float2 o = *cl.map_shared_rank(&s_ms, k);
-    if (o.x != -INFINITY) S += o.y * exp2f((o.x - M) * p.c);
-  }
-  const float f = S > 0.f && mx != -INFINITY ? exp2f((mx - M) * p.c) / S : 0.f;
-  float* dst = p.probs + (int64_t)row * p.p_row + r.a;
-  const int doff = (int)((reinterpret_cast<uintptr_t>(dst) >> 2) & 3);
-  if (doff == off) {
-    float* base = dst - off;
-    const int end = off + r.n, v0 = (off + 3) / 4, v1 = end / 4, head = min(4 * v0, end), tail = max(4 * v1, head);
-    for (int i = v0 + tid; i < v1; i += kProbThreads) {
-      float4 x = reinterpret_cast<const float4*>(sx)[i];
-      x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-      __stcs(reinterpret_cast<float4*>(base) + i, x);
+  const float* src = p.logits + (int64_t)row * p.l_row + r.a;
+  const Slice sl(src, r.n);
+  float m = -INFINITY, sum = 0.f;
+  load_slice(sx, src, sl, [&](auto& v) {
+    constexpr int W = sizeof(v) / sizeof(float);
+    float top = v[0];
+#pragma unroll
+    for (int j = 1; j < W; ++j) top = fmaxf(top, v[j]);
+    if (top > m) {
+      sum = m == -INFINITY ? 0.f : sum * exp2f((m - top) * p.c);
+      m = top;
     }
-    if (tid < head - off) base[off + tid] = sx[off + tid] * f;
-    if (tid < end - tail) base[tail + tid] = sx[tail + tid] * f;
-  } else {
-    for (int i = tid; i < r.n; i += kProbThreads) dst[i] = sx[off + i] * f;
+    if (m != -INFINITY)
+#pragma unroll
+      for (int j = 0; j < W; ++j) sum += exp2f((v[j] - m) * p.c);
+  });
+  auto join = [&](float m2, float s2) {  // (m, sum) and (m2, s2) at their common maximum
+    const float M = fmaxf(m, m2);
+    sum = (m == -INFINITY ? 0.f : sum * exp2f((m - M) * p.c)) + (m2 == -INFINITY ? 0.f : s2 * exp2f((m2 - M) * p.c));
+    m = M;
+  };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+    join(m2, s2);
   }
-  cl.sync();  // s_ms lives until every rank has read it
+  if (lane == 0) s_warp[tid >> 5] = make_float2(m, sum);
+  cl.barrier_wait(std::move(started));
+  __syncthreads();
+  if (tid < 32) {
+    const float2 w = tid < kProbThreads / 32 ? s_warp[tid] : make_float2(-INFINITY, 0.f);
+    m = w.x, sum = w.y;
+#pragma unroll
+    for (int o = kProbThreads / 64; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+      join(m2, s2);
+    }
+    m = __shfl_sync(0xffffffffu, m, 0);
+    sum = __shfl_sync(0xffffffffu, sum, 0);
+    if (tid < C) cl.map_shared_rank(s_ms, tid)[rank] = make_float2(m, sum);  // to every rank
+  }
+  cl.sync();  // after it no rank touches another's memory
+  m = -INFINITY, sum = 0.f;
+  for (int k = 0; k < C; ++k) join(s_ms[k].x, s_ms[k].y);
+  const float f = sum > 0.f ? 1.f / sum : 0.f, M = m == -INFINITY ? 0.f : m;
+  float* dst = p.probs + (int64_t)row * p.p_row + r.a;
+  auto prob = [&](float x) { return exp2f((x - M) * p.c) * f; };
+  if ((int)((reinterpret_cast<uintptr_t>(dst) >> 2) & 3) == sl.off) {
+    float4* base = reinterpret_cast<float4*>(dst - sl.off);
+#pragma unroll 4
+    for (int i = sl.v0 + tid; i < sl.v1; i += kProbThreads) {
+      const float4 x = reinterpret_cast<const float4*>(sx)[i];
+      __stcs(base + i, make_float4(prob(x.x), prob(x.y), prob(x.z), prob(x.w)));
+    }
+    if (tid < sl.head - sl.off) dst[tid] = prob(sx[sl.off + tid]);
+    if (tid < sl.end - sl.tail) dst[sl.tail - sl.off + tid] = prob(sx[sl.tail + tid]);
+  } else {
+    for (int i = tid; i < r.n; i += kProbThreads) dst[i] = prob(sx[sl.off + i]);
+  }
 }
 
 // With top_k: 64-bit keys (order-preserving value, complement of the token id)
 // make every logit's place unique, ties to the lower id. Of G = 128 groups of a
 // CTA's threads the k-th largest group maximum is at most the CTA's k-th
 // largest key, so the keys from it on, a few more than k, hold the CTA's top k;
-// their ranks among themselves sort them, and rank 0 of the cluster merges the
-// C sorted lists by binary search, cuts the nucleus and writes the kept tokens
-// over the zeros that every CTA has written to its slice.
+// their ranks among themselves sort them. The sorted lists go to rank 0, which
+// merges them by binary search, cuts the nucleus and writes every listed token;
+// the other tokens are zeros that each CTA writes to its slice meanwhile
+// (listed ones are marked there and left out). Bound by latency at few rows.
 constexpr int kProbGroups = 128;
+constexpr int kFewCand = 768;
 
 struct TopKShared {
   unsigned long long gmax[kProbGroups];
-  unsigned long long top[kSampleMaxK];  // this CTA's largest keys, sorted
-  int n_top, n_cand;
-  unsigned long long thr;
-  unsigned long long all[16 * kSampleMaxK];
-  unsigned long long sorted[kSampleMaxK];
+  unsigned long long few[kFewCand];               // the candidates' keys while they are few
+  unsigned long long top[kSampleMaxK];            // this CTA's largest keys, sorted
+  unsigned long long all[16][kSampleMaxK];        // rank 0: every rank's
+  unsigned long long sorted[16 * kSampleMaxK];
   int n_all[16];
+  int n_cand;
+  unsigned long long thr;
 };
 
 __device__ __forceinline__ float key_value(unsigned long long k) {
@@ -173,185 +256,206 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
 __global__ void __launch_bounds__(kProbThreads) topk_rows_kernel(const TokenProbsParams p) {
   extern __shared__ __align__(16) float sx[];
   __shared__ TopKShared s;
+  using u64 = unsigned long long;
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x;
+  auto started = cl.barrier_arrive();
   const ProbRange r(p.V, rank, C);
   const int K = min(p.top_k, p.V);
   int* cand = reinterpret_cast<int*>(sx + p.cap + 4);
-  const int off = load_slice(sx, p.logits + (int64_t)row * p.l_row + r.a, r.n,
-                             [&](float x) { return clean_logit(x); });
+  const float* src = p.logits + (int64_t)row * p.l_row + r.a;
+  const Slice sl(src, r.n);
+  load_slice(sx, src, sl, [](auto&) {});
   if (tid == 0) s.n_cand = 0;
   __syncthreads();
-  auto key = [&](int i) {  // of slice element i; 0: a logit that can never be kept
-    const float x = sx[off + i];
-    return x == -INFINITY ? 0ull
-                          : ((unsigned long long)sample_key(x) << 32) | (uint32_t)(0x7FFFFFFF - (r.a + i));
+  auto key = [&](int i) {  // of slice element i; 0: a logit that is never kept
+    const float x = sx[sl.off + i];
+    return x == -INFINITY ? 0ull : ((u64)sample_key(x) << 32) | (uint32_t)(0x7FFFFFFF - (r.a + i));
   };
-  unsigned long long best = 0;
+  u64 best = 0;
+#pragma unroll 4
   for (int i = tid; i < r.n; i += kProbThreads) best = max(best, key(i));
   best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
   best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
   if ((tid & 3) == 0) s.gmax[tid >> 2] = best;
   __syncthreads();
-  if (tid < kProbGroups) {  // the group maximum with K - 1 larger ones (group maxima differ, or are 0)
-    const unsigned long long v = s.gmax[tid];
+  {  // the group maximum with K - 1 larger ones (group maxima differ, or are 0): four threads count for each
+    const int gi = tid >> 2, part = tid & 3;
     int above = 0;
-#pragma unroll 8
-    for (int j = 0; j < kProbGroups; ++j) above += s.gmax[j] > v || (s.gmax[j] == v && j < tid);
-    if (above == K - 1) s.thr = v;
-  }
-  // zeros while the candidates are found
-  float* dst = p.probs + (int64_t)row * p.p_row + r.a;
-  const unsigned long long* sthr = &s.thr;
-  __syncthreads();
-  const unsigned long long thr = max(*sthr, 1ull);
-  for (int i = tid; i < r.n; i += kProbThreads)
-    if (key(i) >= thr) cand[atomicAdd(&s.n_cand, 1)] = i;
-  {
-    const int doff = (int)((reinterpret_cast<uintptr_t>(dst) >> 2) & 3);
-    float* base = dst - doff;
-    const int end = doff + r.n, v0 = (doff + 3) / 4, v1 = end / 4, head = min(4 * v0, end), tail = max(4 * v1, head);
-    for (int i = v0 + tid; i < v1; i += kProbThreads)
-      __stcs(reinterpret_cast<float4*>(base) + i, make_float4(0.f, 0.f, 0.f, 0.f));
-    if (tid < head - doff) base[doff + tid] = 0.f;
-    if (tid < end - tail) base[tail + tid] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kProbGroups / 4; ++j) {
+      const int o = part + 4 * j;
+      above += s.gmax[o] > best || (s.gmax[o] == best && o < gi);
+    }
+    above += __shfl_xor_sync(0xffffffffu, above, 1);
+    above += __shfl_xor_sync(0xffffffffu, above, 2);
+    if (part == 0 && above == K - 1) s.thr = best;
   }
   __syncthreads();
+  const u64 thr = max(s.thr, 1ull);
+#pragma unroll 4
+  for (int i = tid; i < r.n; i += kProbThreads) {
+    const u64 v = key(i);
+    if (v >= thr) {
+      const int at = atomicAdd(&s.n_cand, 1);
+      cand[at] = i;
+      if (at < kFewCand) s.few[at] = v;
+    }
+  }
+  __syncthreads();
+  // ranks among the candidates (keys are unique: the list's order does not matter)
   const int nc = s.n_cand;
-  if (tid == 0) s.n_top = min(nc, K);
-  for (int i = tid; i < nc; i += kProbThreads) {  // the order of the list does not matter: keys are unique
-    const unsigned long long v = key(cand[i]);
-    int above = 0;
-    for (int j = 0; j < nc; ++j) above += key(cand[j]) > v;
-    if (above < K) s.top[above] = v;
+  if (nc <= kFewCand) {
+    for (int i = tid >> 2; i < ((nc + 7) & ~7); i += kProbThreads / 4) {  // whole warps take part
+      const u64 v = i < nc ? s.few[i] : 0;
+      int above = 0;
+#pragma unroll 4
+      for (int j = tid & 3; j < nc; j += 4) above += s.few[j] > v;
+      above += __shfl_xor_sync(0xffffffffu, above, 1);
+      above += __shfl_xor_sync(0xffffffffu, above, 2);
+      if ((tid & 3) == 0 && i < nc && above < K) s.top[above] = v;
+    }
+  } else {
+    for (int i = tid; i < nc; i += kProbThreads) {
+      const u64 v = key(cand[i]);
+      int above = 0;
+      for (int j = 0; j < nc; ++j) above += key(cand[j]) > v;
+      if (above < K) s.top[above] = v;
+    }
   }
-  cl.sync();
-  if (rank == 0) {
-    if (tid < C) s.n_all[tid] = cl.map_shared_rank(&s.n_top, tid)[0];
-    __syncthreads();
-    for (int i = tid; i < C * kSampleMaxK; i += kProbThreads) {
-      const int k = i / kSampleMaxK, j = i % kSampleMaxK;
-      if (j < s.n_all[k]) s.all[i] = cl.map_shared_rank(s.top, k)[j];
-    }
-    __syncthreads();
-    int total = 0;
-    for (int k = 0; k < C; ++k) total += s.n_all[k];
-    const int n = min(total, K);
-    for (int i = tid; i < C * kSampleMaxK; i += kProbThreads) {
-      const int own = i / kSampleMaxK;
-      if (i % kSampleMaxK >= s.n_all[own]) continue;
-      const unsigned long long v = s.all[i];
-      int above = i % kSampleMaxK;
-      for (int k = 0; k < C; ++k) {
-        if (k == own) continue;
-        int lo = 0, hi = s.n_all[k];  // keys of list k larger than v
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (s.all[k * kSampleMaxK + mid] > v) lo = mid + 1;
-          else hi = mid;
-        }
-        above += lo;
-      }
-      if (above < n) s.sorted[above] = v;
-    }
-    __syncthreads();
-    if (tid < 32) {  // lane l: tokens l and l + 32 in order; sums in fp64 (a cut-off compares them with top_p)
-      const float m = n > 0 ? key_value(s.sorted[0]) : 0.f;
-      float e[2];
-      double w[2], cum[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = tid + 32 * h;
-        e[h] = j < n ? exp2f((key_value(s.sorted[j]) - m) * p.c) : 0.f;
-        w[h] = e[h];
-        cum[h] = w[h];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, cum[h], o);
-          if (tid >= o) cum[h] += y;
+  cl.barrier_wait(std::move(started));
+  __syncthreads();
+  const int nt = min(nc, K);
+  if (tid < nt) {
+    const u64 v = s.top[tid];
+    cl.map_shared_rank(&s.all[0][0], 0)[rank * kSampleMaxK + tid] = v;
+    const int i = 0x7FFFFFFF - (int)(uint32_t)v - r.a;
+    sx[sl.off + i] = NAN;  // listed: written by rank 0 (no other entry is NaN)
+  }
+  if (tid == 0) cl.map_shared_rank(s.n_all, 0)[rank] = nt;
+  auto arrived = cl.barrier_arrive();
+  __syncthreads();
+  {
+    float* dst = p.probs + (int64_t)row * p.p_row + r.a;
+    const Slice d(dst, r.n);
+    if (d.off == sl.off) {
+      float4* base = reinterpret_cast<float4*>(dst - d.off);
+      for (int i = d.v0 + tid; i < d.v1; i += kProbThreads) {
+        const float4 x = reinterpret_cast<const float4*>(sx)[i];
+        if (x.x == x.x && x.y == x.y && x.z == x.z && x.w == x.w) {
+          __stcs(base + i, make_float4(0.f, 0.f, 0.f, 0.f));
+        } else {
+          float* e = reinterpret_cast<float*>(base + i);
+          if (x.x == x.x) e[0] = 0.f;
+          if (x.y == x.y) e[1] = 0.f;
+          if (x.z == x.z) e[2] = 0.f;
+          if (x.w == x.w) e[3] = 0.f;
         }
       }
-      cum[1] += __shfl_sync(0xffffffffu, cum[0], 31);
-      const double tot = __shfl_sync(0xffffffffu, cum[1], 31);
-      bool in[2];
-      double kept = 0.0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        in[h] = tid + 32 * h < n && (tid + 32 * h == 0 || cum[h] - w[h] < (double)p.top_p * tot);
-        kept += in[h] ? w[h] : 0.0;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) kept += __shfl_xor_sync(0xffffffffu, kept, o);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = tid + 32 * h;
-        if (j < n) s.sorted[j] = (s.sorted[j] & 0xFFFFFFFFull) |
-                                 ((unsigned long long)__float_as_uint(in[h] ? (float)(w[h] / kept) : 0.f) << 32);
-      }
+      const int e = tid < 4 ? d.off + tid : d.tail + tid - 4;
+      if (tid < 8 && (tid < 4 ? e < d.head : e < d.end) && sx[e] == sx[e]) dst[e - d.off] = 0.f;
+    } else {
+      for (int i = tid; i < r.n; i += kProbThreads)
+        if (sx[sl.off + i] == sx[sl.off + i]) dst[i] = 0.f;
     }
-    if (tid == 0) s.n_top = n;
   }
-  cl.sync();  // every slice's zeros are written, the kept tokens are known
-  if (rank == 0 && tid < s.n_top) {
-    const unsigned long long v = s.sorted[tid];
-    const int id = 0x7FFFFFFF - (int)(uint32_t)v;
-    p.probs[(int64_t)row * p.p_row + id] = __uint_as_float((uint32_t)(v >> 32));
+  cl.barrier_wait(std::move(arrived));
+  if (rank != 0) return;  // nothing of another rank is read from here on
+  int total = 0;
+  for (int k = 0; k < C; ++k) total += s.n_all[k];
+  const int n = min(total, K);
+  for (int i = tid; i < C * kSampleMaxK; i += kProbThreads) {
+    const int own = i / kSampleMaxK, j = i % kSampleMaxK;
+    if (j >= s.n_all[own]) continue;
+    const u64 v = s.all[own][j];
+    int place = 0;
+    for (int k0 = 0; k0 < C; k0 += 4) {  // four lists at a time: how many of each are larger
+      int lo[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int step = kSampleMaxK; step > 0; step >>= 1)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int k = k0 + q, at = lo[q] + step;
+          if (k < C && at <= s.n_all[k] && s.all[k][at - 1] > v) lo[q] = at;
+        }
+      place += (lo[0] + lo[1]) + (lo[2] + lo[3]);
+    }
+    s.sorted[place] = v;
+  }
+  __syncthreads();
+  float* out = p.probs + (int64_t)row * p.p_row;
+  if (tid < 32) {  // lane l: tokens l and l + 32 in order
+    const float m = n > 0 ? key_value(s.sorted[0]) : 0.f;
+    float e[2];
+    Two cum[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = tid + 32 * h;
+      e[h] = j < n ? exp2f((key_value(s.sorted[j]) - m) * p.c) : 0.f;
+      cum[h] = two_scan({e[h], 0.f}, tid);
+    }
+    cum[1] = cum[1] + Two{__shfl_sync(0xffffffffu, cum[0].h, 31), __shfl_sync(0xffffffffu, cum[0].l, 31)};
+    const Two tot = {__shfl_sync(0xffffffffu, cum[1].h, 31), __shfl_sync(0xffffffffu, cum[1].l, 31)};
+    const Two limit = tot * Two{p.top_p, 0.f};
+    bool in[2];
+    float kept = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // kept while the mass ahead of it is below top_p
+      in[h] = tid + 32 * h < n && (tid + 32 * h == 0 || cum[h] + Two{-e[h], 0.f} < limit);
+      kept += in[h] ? e[h] : 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) kept += __shfl_xor_sync(0xffffffffu, kept, o);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = tid + 32 * h;
+      if (j < n) out[0x7FFFFFFF - (int)(uint32_t)s.sorted[j]] = in[h] ? e[h] / kept : 0.f;
+    }
+  } else {
+    for (int j = n + tid - 32; j < total; j += kProbThreads - 32) out[0x7FFFFFFF - (int)(uint32_t)s.sorted[j]] = 0.f;
   }
 }
 
 // ---- draft verification ---------------------------------------------------------
-// Sums over a vocabulary decide an integer, so they are exact far beyond fp32:
-// each thread adds unevaluated pairs of floats (two-sums, ~2^-46 relative), the
-// pairs meet in fp64. fp64 arithmetic per element would cost 50 times more here
-// (2 results per clock and SM against 128).
-struct Two {
-  float h, l;
-};
-__device__ __forceinline__ Two two_sum(float a, float b) {
-  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
-  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
-}
-__device__ __forceinline__ void two_add(Two& acc, Two x) {
-  const Two t = two_sum(acc.h, x.h);
-  acc.h = t.h;
-  acc.l = __fadd_rn(acc.l, __fadd_rn(t.l, x.l));
-}
-__device__ __forceinline__ double two_double(Two x) { return (double)x.h + (double)x.l; }
-
 constexpr int kVerThreads = 512;
 
 struct VerShared {
-  int tok[kTreeMaxNodes], par[kTreeMaxNodes], path[kTreeMaxNodes];
+  int tok[kTreeMaxNodes], path[kTreeMaxNodes];
   float u[kTreeMaxNodes], px[kTreeMaxNodes], qx[kTreeMaxNodes];
-  double mass[kTreeMaxNodes + 1];  // what rejection k - 1 left, in all
-  Two inv[kTreeMaxNodes + 1];      // its reciprocal
-  double warp_sum[kVerThreads / 32];
-  double sums[2][16];              // every rank's slice sum, in two buffers used in turn
+  unsigned long long child[kTreeMaxNodes];  // the nodes below each node
+  Two mass[kTreeMaxNodes + 1];  // what k rejections left, in all
+  Two inv[kTreeMaxNodes + 1];   // its reciprocal
+  Two warp_sum[kVerThreads / 32];
+  Two sums[2][16];              // every rank's slice sum, in two buffers used in turn
+  Two scan[kVerThreads / 32];
+  int first, last;
 };
 
-// What k rejections leave of p(j), unnormalised after the last one.
+// What k rejections leave of p(j), unnormalised after the last one. K: k where
+// it is 0 or 1 (exact, no reciprocals), 2: any k.
+template <int K>
 __device__ __forceinline__ Two residual(float p, float q, const Two* inv, int k) {
   Two r = {fmaxf(p, 0.f), 0.f};  // a NaN probability counts as 0
   q = fmaxf(q, 0.f);
-  for (int i = 0; i < k; ++i) {
-    if (i > 0) {
-      const Two f = inv[i];
-      const float h = __fmul_rn(r.h, f.h);
-      r = {h, __fmaf_rn(r.h, f.h, -h) + (r.h * f.l + r.l * f.h)};
-    }
-    const Two t = two_sum(r.h, -q);
-    const Two d = two_sum(t.h, __fadd_rn(t.l, r.l));
+  for (int i = 0; i < (K < 2 ? K : k); ++i) {
+    if (K == 2 && i > 0) r = r * inv[i];
+    const Two d = K == 2 ? r + Two{-q, 0.f} : two_sum(r.h, -q);
     r = d.h > 0.f ? d : Two{0.f, 0.f};
   }
   return r;
+}
+__device__ __forceinline__ Two residual_any(float p, float q, const Two* inv, int k) {
+  return k == 0 ? residual<0>(p, q, inv, k) : k == 1 ? residual<1>(p, q, inv, k) : residual<2>(p, q, inv, k);
 }
 
 // One cluster per sequence. Every CTA walks the tree on the same prefetched
 // values, so the walk needs no communication; the vocabulary is read only for
 // the masses of rejections that a later sibling needs, and once for the final
-// draw: each rank sums its slice, the ranks exchange their sums, and the rank,
-// the warp, the lane and the token where the running sum passes u tot are
-// found level by level.
+// draw: each rank sums its slice (a lane's loads of eight elements in flight),
+// the ranks exchange their sums, and the rank, the warp's part and the token
+// where the running sum passes u tot are found level by level. Bound by
+// latency: launch, three dependent loads, one cluster exchange; 32 rows of
+// 151936 p and q (39 MB) stream meanwhile.
 template <bool SOFT>  // SOFT: draft probabilities are given
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams p) {
   __shared__ VerShared s;
@@ -359,8 +463,21 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   const int C = cl.num_blocks(), rank = cl.block_rank(), b = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = kVerThreads / 32;
-  const int cnt = p.counts ? min(max(p.counts[b], 0), p.n) : p.n, V = p.V;
+  using u64 = unsigned long long;
+  const int V = p.V;
   int* path_out = p.path + (int64_t)b * p.n;
+  const float* pb = p.p + (int64_t)b * p.p_seq;
+  const float* qb = SOFT ? p.q + (int64_t)b * p.q_seq : nullptr;
+  // every node's test values at once
+  int par = -1, tok = 0;
+  float u = 0.f;
+  if (tid < p.n) {
+    const int64_t at = (int64_t)b * p.n + tid;
+    if (tid) par = p.parents[at];
+    tok = p.tokens[at];
+    u = p.u[at];
+  }
+  const int cnt = p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
   if (cnt == 0) {  // nothing is chosen (the same in every CTA of the cluster)
     if (rank == 0) {
       if (tid < p.n) path_out[tid] = -1;
@@ -368,76 +485,106 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     }
     return;
   }
-  const float* pb = p.p + (int64_t)b * p.p_seq;
-  const float* qb = SOFT ? p.q + (int64_t)b * p.q_seq : nullptr;
-  if (tid < cnt) {  // every node's test values at once
-    const int64_t at = (int64_t)b * p.n + tid;
-    const int par = tid ? p.parents[at] : -1, tok = p.tokens[at];
-    const bool ok = par >= 0 && par < tid && tok >= 0 && tok < V;
+  auto started = cl.barrier_arrive();  // shared memory of another CTA: only once that CTA runs
+  if (tid < kTreeMaxNodes) s.child[tid] = 0;
+  if (tid == 0) s.path[0] = 0, s.mass[0] = {1.f, 0.f}, s.first = kVerThreads, s.last = -1;
+  __syncthreads();
+  if (tid < cnt) {
+    const bool below = par >= 0 && par < tid, ok = below && tok >= 0 && tok < V;
     s.tok[tid] = tok;
-    s.par[tid] = par < tid ? par : -1;
-    s.u[tid] = p.u[at];
+    s.u[tid] = u;
     s.px[tid] = ok ? fmaxf(pb[(int64_t)par * p.p_node + tok], 0.f) : 0.f;
     s.qx[tid] = ok && SOFT ? fmaxf(qb[(int64_t)par * p.q_node + tok], 0.f) : 1.f;
+    if (below) atomicOr(&s.child[par], 1ull << tid);
   }
-  if (tid == 0) s.path[0] = 0, s.mass[0] = 1.0;
   __syncthreads();
-  // warp `warp` owns elements w0 .. w1 of the row, a multiple of 32 but for the end
-  const int chunk = (V + 32 * C * NW - 1) / (32 * C * NW);  // elements of a lane when lanes own runs
+  if constexpr (!SOFT) {  // an earlier sibling with the same token takes its probability
+    if (tid > 0 && tid < cnt && par >= 0 && par < tid)
+      for (u64 w = s.child[par] & ((1ull << tid) - 1); w; w &= w - 1)
+        if (s.tok[__ffsll(w) - 1] == tok) s.px[tid] = 0.f;
+    __syncthreads();
+  }
+  cl.barrier_wait(std::move(started));
+  // warp `warp` owns elements w0 .. w1 of the row, 32 chunk of them but for the end
+  const int chunk = (V + 32 * C * NW - 1) / (32 * C * NW);
   const int w0 = (int)min((int64_t)V, (int64_t)32 * chunk * (rank * NW + warp)), w1 = min(V, w0 + 32 * chunk);
   int turn = 0, cur = 0, n_path = 1, k = 0;  // k: rejections that count at `cur`
-  auto removed = [&](int j) {  // !SOFT: a rejected child's token
-    for (int i = cur + 1; i < cnt; ++i)
-      if (s.par[i] == cur && s.tok[i] == j) return true;
+  const float *pr = nullptr, *qr = nullptr;
+  u64 gone_bits = 0;     // !SOFT: which of this lane's elements (the first 64) are rejected tokens
+  bool gone_far = false;  // and whether one beyond is
+  auto rejected = [&](int j) {
+    for (u64 w = s.child[cur]; w; w &= w - 1)
+      if (s.tok[__ffsll(w) - 1] == j) return true;
     return false;
   };
-  bool holes = false;  // !SOFT: whether a rejected token falls into this warp's elements
-  const float *pr = nullptr, *qr = nullptr;
-  auto element = [&](int j) {
-    if constexpr (SOFT) {
-      return residual(pr[j], k ? qr[j] : 0.f, s.inv, k);
-    } else {
-      const float x = fmaxf(pr[j], 0.f);
-      return Two{holes && removed(j) ? 0.f : x, 0.f};
+  auto sum = [&](auto kk) {
+    constexpr int K = decltype(kk)::value;
+    Two a[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    for (int e = 0; e < chunk; e += 8) {
+      float x[8], y[8];
+      const int i0 = w0 + 32 * e + lane;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        const bool in = e + v < chunk && i0 + 32 * v < w1;
+        x[v] = in ? __ldg(pr + i0 + 32 * v) : 0.f;
+        if constexpr (K > 0) y[v] = in ? __ldg(qr + i0 + 32 * v) : 0.f;
+      }
+      if constexpr (!SOFT) {
+        const uint32_t bits = e < 64 ? (uint32_t)(gone_bits >> e) : 0u;
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          if ((bits >> v) & 1) x[v] = 0.f;
+        if (gone_far && e >= 64)
+          for (int v = 0; v < 8; ++v)
+            if (rejected(i0 + 32 * v)) x[v] = 0.f;
+      }
+#pragma unroll
+      for (int v = 0; v < 8; ++v) a[v & 1] = a[v & 1] + residual<K>(x[v], K > 0 ? y[v] : 0.f, s.inv, k);
     }
+    return a[0] + a[1];
   };
   auto total = [&]() {  // the sum over the row of `cur` after k rejections; leaves warp_sum and sums
     pr = pb + (int64_t)cur * p.p_node;
-    if constexpr (SOFT) qr = qb + (int64_t)cur * p.q_node;
-    else
-      for (int i = cur + 1; i < cnt; ++i) holes |= s.par[i] == cur && s.tok[i] >= w0 && s.tok[i] < w1;
-    Two acc = {0.f, 0.f};
-#pragma unroll 8
-    for (int i = w0 + lane; i < w1; i += 32) two_add(acc, element(i));
-    double d = two_double(acc);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    Two d;
+    if constexpr (SOFT) {
+      qr = qb + (int64_t)cur * p.q_node;
+      d = k == 0   ? sum(std::integral_constant<int, 0>{})
+          : k == 1 ? sum(std::integral_constant<int, 1>{})
+                   : sum(std::integral_constant<int, 2>{});
+    } else {
+      for (u64 w = s.child[cur]; w; w &= w - 1) {
+        const int off = s.tok[__ffsll(w) - 1] - w0, e = off >> 5;
+        if (off >= 0 && e < chunk && (off & 31) == lane) {
+          if (e < 64) gone_bits |= 1ull << e;
+          else gone_far = true;
+        }
+      }
+      d = sum(std::integral_constant<int, 0>{});
+    }
+    d = two_reduce<32>(d);
     if (lane == 0) s.warp_sum[warp] = d;
     __syncthreads();
     if (warp == 0) {
-      d = lane < NW ? s.warp_sum[lane] : 0.0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      d = two_reduce<32>(lane < NW ? s.warp_sum[lane] : Two{0.f, 0.f});
       if (lane < C) cl.map_shared_rank(&s.sums[turn][0], lane)[rank] = d;
     }
     cl.sync();
-    double t = 0.0;
-    for (int r = 0; r < C; ++r) t += s.sums[turn][r];
+    const Two t = two_reduce<16>((lane & 15) < C ? s.sums[turn][lane & 15] : Two{0.f, 0.f});
     turn ^= 1;  // the other ranks have left the other buffer before this call's barrier
     return t;
   };
   bool known = true;  // s.mass[k], s.inv[k] are set
-  double gone = 0.0;  // !SOFT: probability of the rejected children
-  for (int i = 1; i < cnt; ++i) {
-    if (s.par[i] != cur) continue;
+  Two left = {1.f, 0.f};  // !SOFT: 1 less the probability of the rejected children
+  for (u64 w = s.child[0]; w;) {
+    const int i = __ffsll(w) - 1;
+    w &= w - 1;
     bool take;
     if constexpr (SOFT) {
       if (!known) {
-        const double m = total();
-        if (m > 0.0) {
+        const Two m = total();
+        if (m.h > 0.f) {
           if (tid == 0) {
-            const float h = (float)(1.0 / m);
-            s.inv[k] = {h, (float)(1.0 / m - (double)h)};
+            s.inv[k] = two_recip(m);
             s.mass[k] = m;
           }
           __syncthreads();
@@ -446,91 +593,90 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
         }
         known = true;
       }
-      take = (double)s.u[i] * (double)s.qx[i] * s.mass[k] < two_double(residual(s.px[i], s.qx[i], s.inv, k));
-    } else {  // an earlier sibling with the same token has taken its probability
-      double x = s.px[i];
-      for (int j = cur + 1; j < i; ++j)
-        if (s.par[j] == cur && s.tok[j] == s.tok[i]) x = 0.0;
-      take = (double)s.u[i] * (1.0 - gone) < x;
-      gone += x;
+      const Two r = residual_any(s.px[i], s.qx[i], s.inv, k);
+      take = two_prod(s.u[i], s.qx[i]) * s.mass[k] < r;
+    } else {
+      const float x = s.px[i];
+      take = left * Two{s.u[i], 0.f} < Two{x, 0.f};
+      left = left + Two{-x, 0.f};
     }
+    if (i >= cnt) take = false;
     if (take) {
       if (tid == 0) s.path[n_path] = i;
       cur = i;
       ++n_path;
       k = 0;
-      gone = 0.0;
+      left = {1.f, 0.f};
       known = true;
+      w = s.child[i];
     } else if (SOFT) {
       ++k;
       known = false;
     }
   }
   // ---- the next token, from what is left at `cur`
-  double tot = total();
-  while (SOFT && k > 0 && !(tot > 0.0)) {
+  Two tot = total();
+  while (SOFT && k > 0 && !(tot.h > 0.f)) {
     --k;
     tot = total();
   }
-  const double* sums = s.sums[turn ^ 1];
-  const double target = (double)s.u[0] * tot;
-  int owner = -1, last = -1;
-  double base = 0.0, cum = 0.0;
-  for (int r = 0; r < C && owner < 0; ++r) {
-    if (sums[r] > 0.0) last = r, base = cum;
-    cum += sums[r];
-    if (cum > target) owner = r;
-  }
-  if (owner < 0) owner = last;  // u beyond the sum's last bit
+  const Two target = tot * Two{s.u[0], 0.f};
+  // the rank where the running sum passes the target (every warp finds it from the same sums)
+  const Two* sums = s.sums[turn ^ 1];
+  Two mine = lane < C ? sums[lane] : Two{0.f, 0.f};
+  Two incl = two_scan(mine, lane);
+  unsigned over = __ballot_sync(0xffffffffu, mine.h > 0.f && target < incl), some = __ballot_sync(0xffffffffu, mine.h > 0.f);
+  int owner = over ? __ffs(over) - 1 : 31 - __clz(some);  // none passes: the last with any mass (u beyond the sum's last bit)
+  Two base = incl + Two{-mine.h, -mine.l};
+  base = {__shfl_sync(0xffffffffu, base.h, max(owner, 0)), __shfl_sync(0xffffffffu, base.l, max(owner, 0))};
   if (rank == 0 && tid < p.n) path_out[tid] = tid < n_path ? s.path[tid] : -1;
   if (rank == 0 && tid == 0) {
     p.n_path[b] = n_path;
     if (owner < 0) p.next[b] = V - 1;  // a row without mass
   }
-  if (owner == rank) {
-    int ow = -1, lw = 0;
-    double wbase = base, wcum = base;
-    for (int w = 0; w < NW && ow < 0; ++w) {
-      if (s.warp_sum[w] > 0.0) lw = w, wbase = wcum;
-      wcum += s.warp_sum[w];
-      if (wcum > target) ow = w;
+  if (owner != rank) return;  // no rank reads or writes another's memory from here on
+  mine = lane < NW ? s.warp_sum[lane] : Two{0.f, 0.f};
+  incl = base + two_scan(mine, lane);
+  over = __ballot_sync(0xffffffffu, mine.h > 0.f && target < incl);
+  some = __ballot_sync(0xffffffffu, mine.h > 0.f);
+  const int ow = over ? __ffs(over) - 1 : max(31 - __clz(some), 0);
+  base = incl + Two{-mine.h, -mine.l};
+  base = {__shfl_sync(0xffffffffu, base.h, ow), __shfl_sync(0xffffffffu, base.l, ow)};
+  // that warp's 32 chunk elements, a run for each thread of the CTA
+  const int o0 = (int)min((int64_t)V, (int64_t)32 * chunk * (rank * NW + ow)), o1 = min(V, o0 + 32 * chunk);
+  const int run = (o1 - o0 + kVerThreads - 1) / kVerThreads;
+  const int l0 = min(o1, o0 + tid * run), l1 = min(o1, l0 + run);
+  auto element = [&](int j) {
+    if constexpr (SOFT) return residual_any(pr[j], k ? qr[j] : 0.f, s.inv, k);
+    else return Two{rejected(j) ? 0.f : fmaxf(pr[j], 0.f), 0.f};
+  };
+  Two acc = {0.f, 0.f};
+#pragma unroll 4
+  for (int i = l0; i < l1; ++i) acc = acc + element(i);
+  const Two upto = two_scan(acc, lane);
+  if (lane == 31) s.scan[warp] = upto;
+  __syncthreads();
+  mine = lane < warp ? s.scan[lane] : Two{0.f, 0.f};
+  base = base + two_reduce<32>(mine);
+  incl = base + upto;
+  // the first thread whose running sum passes the target; none: the last with any mass
+  if (acc.h > 0.f) {
+    if (target < incl) atomicMin(&s.first, tid);
+    atomicMax(&s.last, tid);
+  }
+  __syncthreads();
+  if (tid == (s.first < kVerThreads ? s.first : s.last)) {
+    Two at = incl + Two{-acc.h, -acc.l};
+    int pick = V - 1;
+    for (int i = l0; i < l1; ++i) {
+      const Two x = element(i);
+      at = at + x;
+      if (x.h > 0.f) pick = i;
+      if (x.h > 0.f && target < at) break;
     }
-    if (ow < 0) ow = lw;
-    if (warp == ow) {
-      // lane l: the run of `chunk` elements from w0 + l chunk
-      const int l0 = min(w1, w0 + lane * chunk), l1 = min(w1, l0 + chunk);
-      Two acc = {0.f, 0.f};
-#pragma unroll 8
-      for (int i = l0; i < l1; ++i) two_add(acc, element(i));
-      const double mine = two_double(acc);
-      double incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned over = __ballot_sync(0xffffffffu, wbase + incl > target && mine > 0.0);
-      const unsigned some = __ballot_sync(0xffffffffu, mine > 0.0);
-      const int ol = over ? __ffs(over) - 1 : 31 - __clz(some);
-      double run = wbase + __shfl_sync(0xffffffffu, incl - mine, ol);
-      const int r0 = __shfl_sync(0xffffffffu, l0, ol), r1 = __shfl_sync(0xffffffffu, l1, ol);
-      int pick = -1, fallback = V - 1;
-      for (int i0 = r0; i0 < r1 && pick < 0; i0 += 32) {
-        const double x = i0 + lane < r1 ? two_double(element(i0 + lane)) : 0.0;
-        double in = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, in, o);
-          if (lane >= o) in += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, x > 0.0 && run + in > target);
-        const unsigned pos = __ballot_sync(0xffffffffu, x > 0.0);
-        if (hit) pick = i0 + __ffs(hit) - 1;
-        if (pos) fallback = i0 + 31 - __clz(pos);
-        run += __shfl_sync(0xffffffffu, in, 31);
-      }
-      if (lane == 0) p.next[b] = pick >= 0 ? pick : fallback;
-    }
+    p.next[b] = pick;
+  } else if (s.last < 0 && tid == 0) {
+    p.next[b] = V - 1;
   }
 }
 
@@ -561,36 +707,47 @@ __global__ void __launch_bounds__(kTreeMaxNodes) verify_greedy_kernel(const Veri
 }
 
 // ---- commit -----------------------------------------------------------------------
-// cache row len + k = tree row path[k] for every layer, head, K and V: 16-byte
-// copies, a thread per chunk, four rows' loads of a thread in flight.
+// cache row len + k = tree row path[k] for every layer, head, K and V. A thread
+// owns 16 bytes of four rows (all loads before the stores): few threads carry
+// enough bytes in flight, and the index arithmetic is small beside them.
+constexpr int kCommitRows = 4;
 __global__ void __launch_bounds__(256) commit_kernel(const CommitParams p) {
-  __shared__ int s_path[kTreeMaxNodes];
   const int b = blockIdx.y, tid = threadIdx.x;
   const int len = max(p.lens[b], 0);
   const int n = min(min(max(p.n_path[b], 0), p.n), max(p.cache.rows - len, 0));
-  if (tid < p.n) s_path[tid] = p.path[(int64_t)b * p.path_seq + tid];
-  __syncthreads();
-  const int ch = p.row_bytes / 16, per_head = n * ch;
-  const int64_t total = (int64_t)2 * p.L * p.Hkv * per_head;
+  if (p.new_lens != p.lens && blockIdx.x == 0 && tid == 0) p.new_lens[b] = len + n;
+  const int ch = p.row_bytes / 16, c = tid % ch, slots = 256 / ch;  // 4, 8 or 16 chunks a row
+  const int rows = 2 * p.L * p.Hkv * n, first = blockIdx.x * kCommitRows * slots + tid / ch;
+  if (first >= rows) return;
   const int esize = p.srow_bytes ? 1 : 2;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + tid; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int lh = (int)(i / per_head), r = (int)(i - (int64_t)lh * per_head), k = r / ch, c = r - k * ch;
-    const int kv = lh & 1, h = (lh >> 1) % p.Hkv, l = (lh >> 1) / p.Hkv, node = s_path[k];
-    if (node < 0 || node >= p.tree.rows) continue;
-    const uint8_t* src = (kv ? p.tree.v : p.tree.k) +
-                         esize * (b * p.tree.seq + l * p.t_layer + h * p.tree.head + node * p.tree.row) + 16 * c;
-    uint8_t* dst = const_cast<uint8_t*>(kv ? p.cache.v : p.cache.k) +
-                   esize * (b * p.cache.seq + l * p.c_layer + h * p.cache.head + (len + k) * p.cache.row) + 16 * c;
-    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-    if (c == 0 && p.srow_bytes) {
-      const uint16_t* ss = (kv ? p.tree.vs : p.tree.ks) + b * p.tree.sseq + l * p.t_slayer + h * p.tree.shead +
-                           node * p.tree.srow;
-      uint16_t* sd = const_cast<uint16_t*>(kv ? p.cache.vs : p.cache.ks) + b * p.cache.sseq + l * p.c_slayer +
-                     h * p.cache.shead + (len + k) * p.cache.srow;
-      for (int e = 0; e < p.srow_bytes / 2; ++e) sd[e] = ss[e];
+  uint4 x[kCommitRows];
+  uint8_t* dst[kCommitRows];
+#pragma unroll
+  for (int u = 0; u < kCommitRows; ++u) {
+    const int i = first + u * slots;
+    dst[u] = nullptr;
+    if (i < rows) {
+      const int lh = i / n, k = i - lh * n, kv = lh & 1, h = (lh >> 1) % p.Hkv, l = (lh >> 1) / p.Hkv;
+      const int node = p.path[(int64_t)b * p.path_seq + k];
+      if (node >= 0 && node < p.tree.rows) {
+        x[u] = *reinterpret_cast<const uint4*>(
+            (kv ? p.tree.v : p.tree.k) +
+            esize * (b * p.tree.seq + l * p.t_layer + h * p.tree.head + node * p.tree.row) + 16 * c);
+        dst[u] = const_cast<uint8_t*>(kv ? p.cache.v : p.cache.k) +
+                 esize * (b * p.cache.seq + l * p.c_layer + h * p.cache.head + (len + k) * p.cache.row) + 16 * c;
+        if (c == 0 && p.srow_bytes) {
+          const uint16_t* ss = (kv ? p.tree.vs : p.tree.ks) + b * p.tree.sseq + l * p.t_slayer + h * p.tree.shead +
+                               node * p.tree.srow;
+          uint16_t* sd = const_cast<uint16_t*>(kv ? p.cache.vs : p.cache.ks) + b * p.cache.sseq + l * p.c_slayer +
+                         h * p.cache.shead + (len + k) * p.cache.srow;
+          for (int e = 0; e < p.srow_bytes / 2; ++e) sd[e] = ss[e];
+        }
+      }
     }
   }
-  if (p.new_lens != p.lens && blockIdx.x == 0 && tid == 0) p.new_lens[b] = len + n;
+#pragma unroll
+  for (int u = 0; u < kCommitRows; ++u)
+    if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
 }
 __global__ void __launch_bounds__(256) advance_kernel(const CommitParams p) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
@@ -608,7 +765,7 @@ int pow2_at_least(int x) {
 }  // namespace
 
 cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t st) {
-  const int max_slice = p.top_k ? 32768 : kProbSlice;
+  const int max_slice = p.top_k ? kProbTopSlice : kProbSlice;
   int C = pow2_at_least((p.V + max_slice - 1) / max_slice);
   if (C > 16) return cudaErrorInvalidValue;
   while (C < 8 && (int64_t)p.R * C < 2 * n_sm && p.V / (2 * C) >= 2048) C *= 2;
@@ -626,7 +783,7 @@ cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t
   const int cand = kSampleMaxK * 4 * ((slice + kProbThreads - 1) / kProbThreads);
   TokenProbsParams q = p;
   q.cap = slice;
-  cudaError_t e = lim_k.raise(topk_rows_kernel, 210 * 1024);
+  cudaError_t e = lim_k.raise(topk_rows_kernel, (kProbTopSlice + 4 + kSampleMaxK * 4 * kProbTopSlice / kProbThreads) * 4);
   if (e == cudaSuccess && C > 8)
     e = cudaFuncSetAttribute(topk_rows_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e == cudaSuccess
@@ -646,9 +803,8 @@ cudaError_t launch_verify_tree(const VerifyParams& p, int n_sm, cudaStream_t st)
 }
 
 cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st) {
-  const int64_t chunks = (int64_t)2 * p.L * p.Hkv * p.n * (p.row_bytes / 16);
-  const int blocks = (int)((chunks + 255) / 256 < 4096 ? (chunks + 255) / 256 : 4096);
-  commit_kernel<<<dim3(blocks, p.B), 256, 0, st>>>(p);
+  const int64_t rows = (int64_t)2 * p.L * p.Hkv * p.n, per = kCommitRows * 256 / (p.row_bytes / 16);
+  commit_kernel<<<dim3((unsigned)((rows + per - 1) / per), p.B), 256, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.new_lens == p.lens) {  // every copy has read the lengths before they advance
     advance_kernel<<<(p.B + 255) / 256, 256, 0, st>>>(p);
@@ -885,7 +1041,7 @@ int llm_token_probs(const float* logits, int64_t logits_stride, float* probs, in
       !c.need(top_k >= 0 && top_k <= kSampleMaxK, LLM_ERR_INVALID_ARG, "top_k must be in 0..64") ||
       !c.need(top_p > 0.f && top_p <= 1.f, LLM_ERR_INVALID_ARG, "top_p must be in (0, 1]") ||
       !c.need(top_k > 0 || top_p == 1.f, LLM_ERR_UNSUPPORTED, "top_p below 1 needs a top_k") ||
-      !c.need(vocab <= (top_k ? 16 * 32768 : 16 * kProbSlice), LLM_ERR_UNSUPPORTED, "%svocab %lld is too large", "",
+      !c.need(vocab <= (top_k ? 16 * kProbTopSlice : 16 * kProbSlice), LLM_ERR_UNSUPPORTED, "%svocab %lld is too large", "",
               vocab) ||
       !c.need((int64_t)n_rows * 16 <= 0x7FFFFFFF, LLM_ERR_UNSUPPORTED, "too many rows") ||
       !c.need(n_rows == 1 || probs_stride >= vocab, LLM_ERR_INVALID_ARG, "rows of probs overlap") ||
@@ -956,6 +1112,8 @@ int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n
   Call c;
   if (!c.need(n_nodes >= 1 && n_nodes <= kTreeMaxNodes, LLM_ERR_UNSUPPORTED, "%sn_nodes %lld (1..64)", "", n_nodes) ||
       !c.need(n_seq >= 1, LLM_ERR_INVALID_ARG, "n_seq is not positive") || !check_view(c, cache, "cache") ||
+      !c.need((int64_t)2 * cache->n_layers * cache->n_heads * n_nodes < (1ll << 31), LLM_ERR_UNSUPPORTED,
+              "too many layers and heads") ||
       !check_view(c, tree, "tree") ||
       !c.need(cache->dtype == tree->dtype && cache->head_dim == tree->head_dim && cache->n_heads == tree->n_heads &&
                   cache->n_layers == tree->n_layers && cache->n_seq >= n_seq && tree->n_seq >= n_seq &&
