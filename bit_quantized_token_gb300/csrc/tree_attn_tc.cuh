@@ -12,6 +12,10 @@
 // A tile is read as units of 128 keys x 64 dims (16 KB, one TMA box, 128-byte
 // swizzle): K and V units stream through one ring. Of each P V product's 128
 // rows the upper 64 read ones instead of V, so lanes 64.. hold the sums of P.
+// fp32 operands are parts in bf16 (24 bits in three, 16 in two): the parts of Q
+// and of P are columns of their own in one product each, so that A, whose fetch
+// from shared memory (4 KB, 32 cycles) bounds these narrow products, is fetched
+// once; the sums over the parts are formed on the way out.
 // Warp roles: 4 softmax warps per block of NB rows (G blocks share the units),
 // one TMA warp, one warp that issues every MMA. A block's next scores are
 // computed right after its P V, while the other block (or the other CTA on the
@@ -34,11 +38,12 @@ template <int HD, bool F32, int NB, int G>
 struct TreeTc {
   static constexpr int N = NB * G, BK = 128, H = HD / 64;
   static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : (N > 64 ? 1 : 2);  // parts of the queries, of P
+  static constexpr int NS = NQ * NB, NO = NP * NB;                        // columns of a block's S, of its O (64 dims)
   static constexpr int NT = 32 * (4 * G + 2);
-  static constexpr int kUnit = BK * 128;                                 // bytes: 64 dims of a K or V tile
-  static constexpr int kRowP = NB >= 64 ? 128 : 2 * NB;                  // bytes of a key's row of a P atom
-  static constexpr int kPart = BK * 2 * NB;                              // bytes of a part of P of one block
-  static constexpr int kP = G * NP * kPart, kQ = NQ * N * HD * 2, kOnes = 2048;
+  static constexpr int kUnit = BK * 128;                                  // bytes: 64 dims of a K or V tile
+  static constexpr int kRowP = NO >= 48 ? 128 : 2 * NO;                   // bytes of a key's row of a P atom (64 columns)
+  static constexpr int kPBlock = BK * kRowP * ((NO + 63) / 64);           // bytes of a block's P
+  static constexpr int kP = G * kPBlock, kQ = NQ * N * HD * 2, kOnes = 2048;
   static constexpr int kOffRow = 1024;                                   // of the small arrays: [N] row masks
   static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4 * kMaxSplits) + 3 * kTreeMaxNodes * (HD / 32) * 4;
   static constexpr int kFixed = kP + kQ + kOnes + kSmall + 1024;
@@ -50,7 +55,8 @@ struct TreeTc {
   static constexpr int NST = fit < 12 ? fit : 12;
   static constexpr int kSmem = NST * kUnit + kFixed;
   static_assert(NST >= kMin && NST >= 3, "shared memory");
-  static constexpr int kUsed = (1 + H) * N;                              // S, and O of every 64 dims
+  static constexpr int kUsed = G * (NS + H * NO);                        // S, and O of every 64 dims
+  static_assert(kUsed <= 512, "tensor memory");
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
 
@@ -153,6 +159,23 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// a, b as NP bf16 pairs whose sums carry 8 NP bits
+template <int NP>
+__device__ __forceinline__ void split_pack(float a, float b, uint32_t (&part)[NP]) {
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    part[k] = pack_bf16x2(a, b);
+    if (k + 1 < NP) {
+      a -= __uint_as_float(part[k] << 16);
+      b -= __uint_as_float(part[k] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // the 128 threads of softmax group g (named barriers 1..G)
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory"); }
 __device__ __forceinline__ bool group_any(int g, bool x) {
@@ -171,7 +194,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     const __grid_constant__ TreeAttnTcParams tp) {
   using C = TreeTc<HD, F32, NB, G>;
   constexpr int N = C::N, NT = C::NT, NST = C::NST, NQ = C::NQ, NP = C::NP, NG = HD / 32, BK = C::BK, H = C::H;
-  constexpr float kLazy = 60.f, kNone = -3e38f;  // kNone: the reference before any visible score
+  constexpr float kNone = -3e38f;  // the reference before any visible score
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -185,8 +208,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   uint8_t* sring = sm;
-  uint8_t* sp = sring + NST * C::kUnit;   // [G][NP] parts of P
-  uint8_t* sq = sp + C::kP;               // [NQ][H][N][128 B]
+  uint8_t* sp = sring + NST * C::kUnit;   // [G] blocks of P: [atom of 64 columns][key][kRowP], columns part by part
+  uint8_t* sq = sp + C::kP;               // [H][G][NQ][NB][128 B]
   uint8_t* sones = sq + C::kQ;
   uint8_t* small = sones + C::kOnes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
@@ -196,7 +219,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 264);
   uint64_t* smask = reinterpret_cast<uint64_t*>(small + 512);          // [64]
   uint64_t* srow = reinterpret_cast<uint64_t*>(small + C::kOffRow);    // [N] what each row sees of the tree
-  float* sm_m = reinterpret_cast<float*>(srow + N);             // [N] references
+  float* sm_m = reinterpret_cast<float*>(srow + N);             // [N] references, negated
   float* sm_w = sm_m + N;                                       // [4][N]
   float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);        // [N]
   float* sw = reinterpret_cast<float*>(sml + N);                // [kMaxSplits][N]
@@ -239,7 +262,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     for (int i = tid; i < N * (HD / 8); i += 128 * G) {
       const int r = i / (HD / 8), ch = i % (HD / 8), node = (m0 + r) / p.gq, h = hkv * p.gq + (m0 + r) % p.gq;
       const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
-      uint8_t* dst = sq + (ch / 8) * N * 128 + r * 128 + 16 * ((ch & 7) ^ (r & 7));
+      uint8_t* dst = sq + (((ch / 8) * G + r / NB) * NQ * NB + r % NB) * 128 + 16 * ((ch & 7) ^ (r & 7));
       if constexpr (F32) {
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (node < cnt) {
@@ -252,7 +275,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         for (int e = 0; e < 8; ++e) split_bf16<3>(x[e], part[e]);
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-          *reinterpret_cast<uint4*>(dst + k * N * HD * 2) =
+          *reinterpret_cast<uint4*>(dst + k * NB * 128) =
               make_uint4(pack_bf16x2(part[0][k], part[1][k]), pack_bf16x2(part[2][k], part[3][k]),
                          pack_bf16x2(part[4][k], part[5][k]), pack_bf16x2(part[6][k], part[7][k]));
       } else {
@@ -265,13 +288,13 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       reinterpret_cast<uint4*>(sones)[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
     if (p.tree.k && t1 == n_tiles)
       for (int i = tid; i < 3 * kTreeMaxNodes * NG; i += 128 * G) snf[i] = 0;
-    for (int i = tid; i < N; i += 128 * G) sm_m[i] = kNone;
+    for (int i = tid; i < N; i += 128 * G) sm_m[i] = -kNone;
     fence_async_smem();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;  // S of block g at columns g NB, O of 64 dims u at N (1 + u) + g NB
+  const uint32_t tmem = *s_tmem;  // S of block g at columns g NS, O of 64 dims u at G NS + (u G + g) NO
   uint64_t seen = 0;              // tree rows that some node sees
   if (p.tree.k) {
     const uint64_t a = smask[lane] | smask[lane + 32];
@@ -296,9 +319,10 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     }
   } else if (warp == 4 * G + 1) {
     // ---- MMA: commits release units and publish scores
-    constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NB >> 3) << 17) | (8u << 24);
-    constexpr uint32_t idesc_s = base_i, idesc_o = base_i | (1u << 15) | (1u << 16);  // O: A and B MN-major
-    constexpr uint64_t swp = NB >= 64 ? 2 : (NB == 32 ? 4 : 6);
+    constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 x bf16, 128 rows
+    constexpr uint32_t idesc_s = base_i | ((uint32_t)(C::NS >> 3) << 17);
+    constexpr uint32_t idesc_o = base_i | ((uint32_t)(C::NO >> 3) << 17) | (1u << 15) | (1u << 16);  // A and B MN-major
+    constexpr uint64_t swp = C::kRowP == 128 ? 2 : (C::kRowP == 64 ? 4 : 6);
     constexpr uint32_t step_p = 16 * C::kRowP, sbo_p = 8 * C::kRowP;
     const uint32_t uq = smem_u32(sq), up = smem_u32(sp), ur = smem_u32(sring), uo = smem_u32(sones);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -309,14 +333,11 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         if (!tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status)) return false;
         tc_fence_after();
         const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
-        const uint64_t dq = tc_desc(uq + u * N * 128 + g * NB * 128, 16, 1024, 2);
+        const uint64_t dq = tc_desc(uq + (u * G + g) * C::NS * 128, 16, 1024, 2);
         if (elect_lane()) {
 #pragma unroll
-          for (int k = NQ - 1; k >= 0; --k)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
-              tc_mma(tm + g * NB, da + 2 * ks, dq + (k * H * N * 128 >> 4) + 2 * ks, idesc_s,
-                     u > 0 || k < NQ - 1 || ks > 0);
+          for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
+            tc_mma(tm + g * C::NS, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
         }
         __syncwarp();
         if (g == G - 1) tc_commit(empty + slot);
@@ -339,14 +360,12 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           const uint32_t v = ur + slot * C::kUnit;
           // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
           const uint64_t da = tc_desc(v, uo - v, 1024, 2);
-          const uint64_t dp = tc_desc(up + g * NP * C::kPart, BK * 128, sbo_p, swp);
+          const uint64_t dp = tc_desc(up + g * C::kPBlock, BK * 128, sbo_p, swp);
           if (elect_lane()) {
 #pragma unroll
-            for (int k = NP - 1; k >= 0; --k)
-#pragma unroll
-              for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
-                tc_mma(tm + N * (1 + u) + g * NB, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
-                       dp + ((k * C::kPart + ks * step_p) >> 4), idesc_o, t > t0 || k < NP - 1 || ks > 0);
+            for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
+              tc_mma(tm + G * C::NS + (u * G + g) * C::NO, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                     dp + (ks * step_p >> 4), idesc_o, t > t0 || ks > 0);
           }
           __syncwarp();
           if (g == G - 1) tc_commit(empty + slot);
@@ -364,8 +383,9 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   } else {
     // ---- softmax: thread = key
     const int g = warp >> 2, key = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * NB, tO = tS + N;
-    float* m = sm_m + g * NB;
+    const uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * C::NS;
+    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + G * C::NS + g * C::NO;  // of 64 dims u: + u G NO
+    float* m = sm_m + g * NB;  // the references, negated
     const float masked = p.c < 0.f ? INFINITY : -INFINITY;  // times c: -inf (c is not 0)
     if (p.tree.k)
       for (int r = key; r < NB; r += 128) {
@@ -376,6 +396,18 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     // whether row r of the block sees this thread's tree row
     const uint32_t* vis = reinterpret_cast<const uint32_t*>(srow + g * NB) + (warp & 1);
     auto sees = [&](int r) { return key < kTreeMaxNodes && ((vis[2 * r] >> lane) & 1); };
+    constexpr int W = NB >= 32 && NQ == 1 ? 32 : 16;
+    auto load = [&](float (&v)[NQ][W], int c0) {
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) tc_ld(v[k], tS + k * NB + c0);
+    };
+    auto ready = [&](float (&v)[NQ][W]) {  // waits, and adds the parts, the small ones first
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) tc_wait_ld(v[k]);
+      if constexpr (NQ == 3)
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[0][j] += v[1][j] + v[2][j];
+    };
     for (int t = t0; t < t1; ++t) {
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
       const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
@@ -415,32 +447,36 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       tc_wait(s_full + g, (t - t0) & 1, s_abort, p.status);
       tc_fence_after();
       if (t == t0) {  // the references: the score of the first key that a row sees (renewed below if not finite)
-        float* first = reinterpret_cast<float*>(sp + g * NP * C::kPart);  // [64][NB], where P comes to lie
+        float* first = reinterpret_cast<float*>(sp + g * C::kPBlock);  // [64][NB], where P comes to lie
+        static_assert(64 * NB * 4 <= C::kPBlock, "room for the first scores");
         if (warp < 4 * g + (tree ? 2 : 1))
 #pragma unroll 1
-          for (int c0 = 0; c0 < NB; c0 += 16) {
-            float s[16];
-            tc_ld(s, tS + c0);
-            tc_wait_ld(s);
+          for (int c0 = 0; c0 < NB; c0 += W) {
+            float v[NQ][W];
+            load(v, c0);
+            ready(v);
             if (tree || lane == 0)
 #pragma unroll
-              for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<float4*>(first + key * NB + c0 + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+              for (int j = 0; j < W; j += 4)
+                *reinterpret_cast<float4*>(first + key * NB + c0 + j) =
+                    make_float4(v[0][j], v[0][j + 1], v[0][j + 2], v[0][j + 3]);
           }
         group_sync(g);
-        for (int r = key; r < NB; r += 128) {
-          const int j = tree ? __ffsll(srow[g * NB + r]) - 1 : 0;
-          const float y = j >= 0 ? first[j * NB + r] * p.c : INFINITY;
-          m[r] = fabsf(y) < 1e38f ? y : kNone;
+        float y = INFINITY;
+        if (key < NB) {  // a thread per row (NB <= 128)
+          const int j = tree ? __ffsll(srow[g * NB + key]) - 1 : 0;
+          if (j >= 0) y = first[j * NB + key] * p.c;
+          m[key] = fabsf(y) < 1e38f ? -y : -kNone;
         }
         group_sync(g);
       }
-      uint8_t* prow = sp + g * NP * C::kPart + key * C::kRowP;
+      uint8_t* prow = sp + g * C::kPBlock + key * C::kRowP;
+      const int sel = C::kRowP == 128 ? key & 7 : (C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
       for (;;) {
         // probabilities with the references as they are; the largest excess over them
-        float top = -INFINITY;
-        constexpr int W = NB >= 32 ? 32 : 16;
-        auto take = [&](float (&s)[W], int c0) {
+        uint32_t top = 0;  // of P's first parts, two at a time
+        auto take = [&](float (&v)[NQ][W], int c0) {
+          float(&s)[W] = v[0];
           if (tree) {
 #pragma unroll
             for (int j = 0; j < W; ++j)
@@ -451,67 +487,73 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           }
 #pragma unroll
           for (int h = 0; h < W / 8; ++h) {
-            float part[8][NP];
+            uint32_t part[4][NP];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float y = fmaf(s[8 * h + j], p.c, -m[c0 + 8 * h + j]);
-              top = fmaxf(top, y);
-              split_bf16<NP>(ex2(y), part[j]);
+            for (int j = 0; j < 8; j += 4) {
+              const float4 ref = *reinterpret_cast<const float4*>(m + c0 + 8 * h + j);
+              float y[4] = {ref.x, ref.y, ref.z, ref.w};
+              fma2(y[0], y[1], s[8 * h + j], s[8 * h + j + 1], p.c, p.c);
+              fma2(y[2], y[3], s[8 * h + j + 2], s[8 * h + j + 3], p.c, p.c);
+              split_pack<NP>(ex2(y[0]), ex2(y[1]), part[j / 2]);
+              split_pack<NP>(ex2(y[2]), ex2(y[3]), part[j / 2 + 1]);
+              top = max_bf16x2(top, max_bf16x2(part[j / 2][0], part[j / 2 + 1][0]));
             }
-            const int chunk = (c0 + 8 * h) / 8, sel = NB >= 64 ? key & 7 : (NB == 32 ? (key >> 1) & 3 : (key >> 2) & 1);
 #pragma unroll
-            for (int k = 0; k < NP; ++k)
-              *reinterpret_cast<uint4*>(prow + k * C::kPart + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ sel)) =
-                  make_uint4(pack_bf16x2(part[0][k], part[1][k]), pack_bf16x2(part[2][k], part[3][k]),
-                             pack_bf16x2(part[4][k], part[5][k]), pack_bf16x2(part[6][k], part[7][k]));
+            for (int k = 0; k < NP; ++k) {
+              const int chunk = (k * NB + c0 + 8 * h) / 8;
+              *reinterpret_cast<uint4*>(prow + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ sel)) =
+                  make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
+            }
           }
         };
-        float sa[W], sb[W];  // the next columns load while these are worked on
-        tc_ld(sa, tS);
+        float va[NQ][W], vb[NQ][W];  // the next columns load while these are worked on
+        load(va, 0);
 #pragma unroll 1
         for (int c0 = 0; c0 < NB; c0 += 2 * W) {
-          tc_wait_ld(sa);
-          if (c0 + W < NB) tc_ld(sb, tS + c0 + W);
-          take(sa, c0);
+          ready(va);
+          if (c0 + W < NB) load(vb, c0 + W);
+          take(va, c0);
           if (c0 + W < NB) {
-            tc_wait_ld(sb);
-            if (c0 + 2 * W < NB) tc_ld(sa, tS + c0 + 2 * W);
-            take(sb, c0 + W);
+            ready(vb);
+            if (c0 + 2 * W < NB) load(va, c0 + 2 * W);
+            take(vb, c0 + W);
           }
         }
-        if (!group_any(g, top > kLazy)) break;
+        constexpr float kLimit = 1152921504606846976.f;  // 2^60
+        const bool over = __uint_as_float(top << 16) > kLimit || __uint_as_float(top & 0xFFFF0000u) > kLimit;
+        if (!group_any(g, over)) break;
         // renew the references: the maxima per warp, then over the four; rescale O and the sums
 #pragma unroll 1
-        for (int c0 = 0; c0 < NB; c0 += 16) {
-          float s[16];
-          tc_ld(s, tS + c0);
-          tc_wait_ld(s);
+        for (int c0 = 0; c0 < NB; c0 += W) {
+          float v[NQ][W];
+          load(v, c0);
+          ready(v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < W; ++j) {
             const bool in = tree ? sees(c0 + j) : valid;
-            float y = in ? s[j] * p.c : -INFINITY;
+            float y = in ? v[0][j] * p.c : -INFINITY;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
             if (lane == 0) sm_w[(warp & 3) * N + g * NB + c0 + j] = y;
           }
         }
         group_sync(g);
-        for (int r = key; r < NB; r += 128) {
-          const float* w = sm_w + g * NB + r;
-          const float old = m[r], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
-          m[r] = now;
-          sw[g * NB + r] = old == now ? 1.f : exp2f(old - now);
+        if (key < NB) {
+          const float* w = sm_w + g * NB + key;
+          const float old = -m[key], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
+          m[key] = -now;
+          sw[g * NB + key] = old == now ? 1.f : exp2f(old - now);
         }
         group_sync(g);
         if (t > t0) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < NB * H; c0 += 16) {
-            const uint32_t at = tO + (c0 / NB) * N + c0 % NB;
+          for (int c0 = 0; c0 < C::NO * H; c0 += 16) {
+            const uint32_t at = tO + (c0 / C::NO) * G * C::NO + c0 % C::NO;
             float s[16];
             tc_ld(s, at);
             tc_wait_ld(s);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] *= sw[g * NB + c0 % NB + j];
+            for (int j = 0; j < 16; ++j) s[j] *= sw[g * NB + (c0 + j) % NB];
             tc_st16(at, s);
           }
           tc_wait_st();
@@ -531,16 +573,21 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 #pragma unroll 1
     for (int c0 = 0; c0 < NB * H; c0 += 16) {
       const int u = c0 / NB, r0 = c0 % NB;
-      float s[16];
+      float s[NP][16];
       if (have) {
-        tc_ld(s, tO + u * N + r0);
-        tc_wait_ld(s);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) tc_ld(s[k], tO + u * G * C::NO + k * NB + r0);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) tc_wait_ld(s[k]);
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float x = have ? s[j] : 0.f;
+        float x = 0.f;
+        if (have)
+#pragma unroll
+          for (int k = NP - 1; k >= 0; --k) x += s[k][j];
         if (key < 64) so[(r0 + j) * HD + 64 * u + key] = x;
-        if (u == 0 && key == 64) sml[g * NB + r0 + j] = make_float2(m[r0 + j], x);
+        if (u == 0 && key == 64) sml[g * NB + r0 + j] = make_float2(-m[r0 + j], x);
       }
     }
     if (p.tree.k && have && t1 == n_tiles && *s_any && key < 64) {  // non-finite tree values, where they are seen
@@ -688,19 +735,24 @@ bool launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStream_t st
   if (tree && !(encode_rows(&tp.tk, p.tree.k, p.tree, p.B, p.Hkv, HD) &&
                 encode_rows(&tp.tv, p.tree.v, p.tree, p.B, p.Hkv, HD)))
     return false;
-  const int M = p.n * p.gq;
-  // two blocks of rows once there are 32: their softmax and MMAs overlap, and
-  // eight softmax warps fill an SM's schedulers twice
+  // Rows of a CTA: as many as there are (K and V are read once for them), in two
+  // blocks once there are 32 (one block's softmax overlaps the other's MMAs); but
+  // fewer while the clusters, split eight ways, would leave SMs without a CTA
+  // (16 nodes x 8 heads over 4097 rows, fp32: 64 rows a CTA 24.6 us, 16 rows %s).
+  const int M = p.n * p.gq, most = f32 ? (HD == 64 ? 64 : 32) : (HD == 64 ? 256 : 128);
+  int N = 16;
+  while (N < M && N < most) N *= 2;
+  while (N > 16 && (int64_t)p.B * p.Hkv * ((M + N - 1) / N) * kMaxSplits < n_sm) N /= 2;
   if (f32)
-    *e = M <= 16   ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st)
-         : M <= 32 ? launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st)
-                   : launch_tree_tc_t<HD, true, 32, 2>(tp, n_sm, st);
+    *e = N == 16   ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st)
+         : N == 32 ? launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st)
+                   : launch_tree_tc_t<HD, true, HD == 64 ? 32 : 16, 2>(tp, n_sm, st);
   else
-    *e = M <= 16   ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)
-         : M <= 32 ? launch_tree_tc_t<HD, false, 16, 2>(tp, n_sm, st)
-         : M <= 64 ? launch_tree_tc_t<HD, false, 32, 2>(tp, n_sm, st)
-         : HD == 128 || M <= 128 ? launch_tree_tc_t<HD, false, 64, 2>(tp, n_sm, st)
-                                 : launch_tree_tc_t<HD, false, HD == 64 ? 128 : 64, 2>(tp, n_sm, st);
+    *e = N == 16    ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)
+         : N == 32  ? launch_tree_tc_t<HD, false, 16, 2>(tp, n_sm, st)
+         : N == 64  ? launch_tree_tc_t<HD, false, 32, 2>(tp, n_sm, st)
+         : N == 128 ? launch_tree_tc_t<HD, false, 64, 2>(tp, n_sm, st)
+                    : launch_tree_tc_t<HD, false, HD == 64 ? 128 : 64, 2>(tp, n_sm, st);
   return true;
 }
 

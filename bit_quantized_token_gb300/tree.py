@@ -11,6 +11,8 @@ Tensors are torch CUDA tensors of the current device (anything with ``shape``,
 from __future__ import annotations
 
 import ctypes as C
+import struct
+import sys
 
 import bit_quantized_token_gb300 as _base
 from bit_quantized_token_gb300 import LLM_BF16, LLM_F32, LLM_Q8G32, LlmError
@@ -39,14 +41,23 @@ class _VerifyArgs(C.Structure):
                 ("targets", C.c_void_p), ("path", C.c_void_p), ("n_path", C.c_void_p), ("next", C.c_void_p)]
 
 
+# The argument structs as native-layout packers: one call fills a struct, and
+# the bytes belong to the calling thread alone.
+_ATTENTION = struct.Struct("@4i2P6q5Pf0P").pack
+_VERIFY = struct.Struct("@3i5P2qP2q4P").pack
+
 _lib = None
-_names: dict = {}  # dtype object -> its name ("bfloat16", ...)
+_i32 = _i64 = _f32 = _f16 = _bf16 = _i8 = None  # torch's dtype objects, once a tensor has come in
 
 
 def _load():
-    global _lib
+    global _lib, _i32, _i64, _f32, _f16, _bf16, _i8
     if _lib is None:
-        _lib = _base.lib()
+        lib = _base.lib()
+        torch = sys.modules["torch"]  # the tensors are torch's
+        _i32, _i64, _f32, _f16, _bf16, _i8 = (torch.int32, torch.int64, torch.float32, torch.float16, torch.bfloat16,
+                                              torch.int8)
+        _lib = lib
     return _lib
 
 
@@ -60,19 +71,16 @@ def _check(rc: int) -> None:
 
 
 def _name(t) -> str:
-    d = t.dtype
-    n = _names.get(d)
-    if n is None:
-        n = _names[d] = str(d).rpartition(".")[2]
-    return n
+    return str(t.dtype).rpartition(".")[2]
 
 
-def _flat(t, name: str, dtype: str, shape: tuple):
+def _flat(t, name: str, dtype, shape: tuple) -> int:
     """Address of a contiguous tensor of this type and shape."""
     if t is None:
         _fail(f"{name} is needed")
-    if _name(t) != dtype or t.shape != shape or not t.is_contiguous():
-        _fail(f"{name}: a contiguous {dtype} tensor of shape {shape} is needed, not {_name(t)} {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _fail(f"{name}: a contiguous {str(dtype).rpartition('.')[2]} tensor of shape {shape} is needed, not {_name(t)} "
+              f"{tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -85,14 +93,15 @@ class KVView:
     """
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
+        _lib or _load()
         q8 = k_scales is not None
-        dtype = "int8" if q8 else "bfloat16"
+        dtype = _i8 if q8 else _bf16
         if len(k.shape) not in (4, 5):
             _fail(f"k has {len(k.shape)} dimensions, not 4 (or 5 with layers)")
         if (k_scales is None) != (v_scales is None):
             _fail("scales are given for both k and v or for neither")
-        if _name(k) != dtype or _name(v) != dtype:
-            _fail(f"k and v are {_name(k)} and {_name(v)}, not {dtype}", _UNSUPPORTED)
+        if k.dtype is not dtype or v.dtype is not dtype:
+            _fail(f"k and v are {_name(k)} and {_name(v)}, not {'int8' if q8 else 'bfloat16'}", _UNSUPPORTED)
         if v.shape != k.shape or v.stride() != k.stride():
             _fail("k and v differ in shape or strides")
         s = self._struct = _KvView()
@@ -106,7 +115,7 @@ class KVView:
         if q8:
             want = tuple(k.shape[:-1]) + (shape[-1] // 32,)
             for t in (k_scales, v_scales):
-                if _name(t) != "float16" or tuple(t.shape) != want:
+                if t.dtype is not _f16 or tuple(t.shape) != want:
                     _fail(f"scales: float16 of shape {want} are needed, not {_name(t)} {tuple(t.shape)}")
             if k_scales.stride() != v_scales.stride():
                 _fail("the scales of k and v differ in strides")
@@ -132,27 +141,24 @@ def tree_attention(q, cache: KVView, tree: KVView | None, lens, mask, out, count
     """out = attention of q [seq, node, head, head_dim] over the cache's first lens[seq] rows and the tree rows
     whose bits mask [seq, node] (int64) sets; see llm_tree_attention. tree None: the cache alone (mask unused)."""
     L = _lib or _load()
-    B, n, H, hd = q.shape
-    name = _name(q)
-    if out.shape != q.shape or _name(out) != name:
+    shape, dt = q.shape, q.dtype
+    B, n, H, hd = shape
+    if out.shape != shape or out.dtype is not dt:
         _fail("out must have q's shape and type")
-    if name not in ("bfloat16", "float32"):
-        _fail(f"queries of type {name} (bfloat16 or float32)", _UNSUPPORTED)
+    if dt is not _bf16 and dt is not _f32:
+        _fail(f"queries of type {_name(q)} (bfloat16 or float32)", _UNSUPPORTED)
     if cache.shape[4] != hd:
         _fail(f"q has head_dim {hd}, the cache {cache.shape[4]}")
-    qs, os_ = q.stride(), out.stride()
-    if qs[3] != 1 or os_[3] != 1:
+    q0, q1, q2, q3 = q.stride()
+    o0, o1, o2, o3 = out.stride()
+    if q3 != 1 or o3 != 1:
         _fail("a head's values must be contiguous in q and out")
-    a = _AttentionArgs(LLM_F32 if name == "float32" else LLM_BF16, B, n, H, q.data_ptr(), out.data_ptr(), qs[:3],
-                       os_[:3], cache._at)
-    a.lens = _flat(lens, "lens", "int32", (B,))
-    if tree is not None:
-        a.tree = tree._at
-        a.mask = _flat(mask, "mask", "int64", (B, n))
-    if counts is not None:
-        a.counts = _flat(counts, "counts", "int32", (B,))
-    a.scale = hd ** -0.5 if scale is None else scale
-    rc = L.llm_tree_attention(C.byref(a), stream)
+    rc = L.llm_tree_attention(
+        _ATTENTION(LLM_F32 if dt is _f32 else LLM_BF16, B, n, H, q.data_ptr(), out.data_ptr(), q0, q1, q2, o0, o1, o2,
+                   cache._at, 0 if tree is None else tree._at, _flat(lens, "lens", _i32, (B,)),
+                   0 if tree is None else _flat(mask, "mask", _i64, (B, n)),
+                   0 if counts is None else _flat(counts, "counts", _i32, (B,)),
+                   hd ** -0.5 if scale is None else scale), stream)
     if rc:
         _check(rc)
 
@@ -168,7 +174,7 @@ def token_probs(logits, out, temperature: float = 1.0, top_k: int = 0, top_p: fl
     """out [rows, vocab] = the distribution that set_sampling's options draw from; see llm_token_probs."""
     L = _lib or _load()
     R, V = logits.shape
-    if out.shape != logits.shape or _name(logits) != "float32" or _name(out) != "float32":
+    if out.shape != logits.shape or logits.dtype is not _f32 or out.dtype is not _f32:
         _fail("logits and out must be float32 of one shape")
     ls, os_ = logits.stride(), out.stride()
     if V > 1 and (ls[1] != 1 or os_[1] != 1):
@@ -183,42 +189,40 @@ def verify_tree(tokens, parents, uniforms, probs, path, n_path, next_token, draf
     """Which drafts are kept (path, n_path) and the token after them (next_token); see llm_verify_tree.
     probs, draft_probs [seq, node, vocab] float32; greedy mode: probs None and targets [seq, node] int32."""
     L = _lib or _load()
-    B, n = tokens.shape
-    a = _VerifyArgs(B, n)
-    a.tokens = _flat(tokens, "tokens", "int32", (B, n))
-    a.parents = _flat(parents, "parents", "int32", (B, n))
-    a.path = _flat(path, "path", "int32", (B, n))
-    a.n_path = _flat(n_path, "n_path", "int32", (B,))
-    a.next = _flat(next_token, "next_token", "int32", (B,))
-    if counts is not None:
-        a.counts = _flat(counts, "counts", "int32", (B,))
-    if targets is not None:
-        a.targets = _flat(targets, "targets", "int32", (B, n))
+    B, n = shape = tokens.shape
+    V = p = p0 = p1 = q = q0 = q1 = u = 0
     if probs is not None:
-        a.vocab = probs.shape[-1]
-        a.uniforms = _flat(uniforms, "uniforms", "float32", (B, n))
-        for t, ptr, strides in ((probs, "probs", "probs_strides"), (draft_probs, "draft_probs", "draft_strides")):
-            if t is None:
-                continue
-            st = t.stride()
-            if _name(t) != "float32" or tuple(t.shape) != (B, n, a.vocab) or (a.vocab > 1 and st[2] != 1):
-                _fail(f"{ptr}: float32 of shape {(B, n, a.vocab)} with contiguous rows is needed")
-            setattr(a, ptr, t.data_ptr())
-            setattr(a, strides, st[:2])
+        V = probs.shape[2]
+        u = _flat(uniforms, "uniforms", _f32, shape)
+        p, p0, p1 = _rows(probs, "probs", (B, n, V))
+        if draft_probs is not None:
+            q, q0, q1 = _rows(draft_probs, "draft_probs", (B, n, V))
     elif draft_probs is not None:
         _fail("draft_probs need probs")
-    rc = L.llm_verify_tree(C.byref(a), stream)
+    rc = L.llm_verify_tree(
+        _VERIFY(B, n, V, _flat(tokens, "tokens", _i32, shape), _flat(parents, "parents", _i32, shape),
+                0 if counts is None else _flat(counts, "counts", _i32, (B,)), u, p, p0, p1, q, q0, q1,
+                0 if targets is None else _flat(targets, "targets", _i32, shape), _flat(path, "path", _i32, shape),
+                _flat(n_path, "n_path", _i32, (B,)), _flat(next_token, "next_token", _i32, (B,))), stream)
     if rc:
         _check(rc)
+
+
+def _rows(t, name: str, shape: tuple):
+    """Address and outer strides of a [seq, node, vocab] float32 tensor with contiguous rows."""
+    s0, s1, s2 = t.stride()
+    if t.dtype is not _f32 or t.shape != shape or (s2 != 1 and shape[2] > 1):
+        _fail(f"{name}: float32 of shape {shape} with contiguous rows is needed")
+    return t.data_ptr(), s0, s1
 
 
 def commit_tree(cache: KVView, tree: KVView, lens, path, n_path, new_lens, stream: int | None = None) -> None:
     """Cache rows lens[seq] + k = tree rows path[seq, k], k < n_path[seq], in every layer; see llm_commit_tree."""
     L = _lib or _load()
-    B, n = path.shape
-    rc = L.llm_commit_tree(cache._at, tree._at, B, n, _flat(lens, "lens", "int32", (B,)),
-                           _flat(path, "path", "int32", (B, n)), _flat(n_path, "n_path", "int32", (B,)),
-                           _flat(new_lens, "new_lens", "int32", (B,)), stream)
+    B, n = shape = path.shape
+    rc = L.llm_commit_tree(cache._at, tree._at, B, n, _flat(lens, "lens", _i32, (B,)),
+                           _flat(path, "path", _i32, shape), _flat(n_path, "n_path", _i32, (B,)),
+                           _flat(new_lens, "new_lens", _i32, (B,)), stream)
     if rc:
         _check(rc)
 

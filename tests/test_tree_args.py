@@ -158,3 +158,10 @@ def test_struct_layouts_match_c(tmp_path):
         want.append(C.sizeof(s))
         want += [getattr(s, f).offset for f, _ in s._fields_]
     assert got == want
+    # the packers lay their bytes out as the structs
+    a = bt._AttentionArgs.from_buffer_copy(bt._ATTENTION(*range(1, 18), 18.5))
+    assert (a.dtype, a.n_heads, a.q, a.out, list(a.q_strides), list(a.out_strides), a.cache, a.counts, a.scale) == (
+        1, 4, 5, 6, [7, 8, 9], [10, 11, 12], 13, 17, 18.5)
+    v = bt._VerifyArgs.from_buffer_copy(bt._VERIFY(*range(1, 18)))
+    assert (v.vocab, v.tokens, v.probs, list(v.probs_strides), v.draft_probs, list(v.draft_strides), v.next) == (
+        3, 4, 8, [9, 10], 11, [12, 13], 17)
