@@ -14,18 +14,19 @@ namespace llmq {
 
 constexpr int kTreeMaxNodes = 64;  // a node's visible set is one 64-bit word
 
-// A kernel's dynamic shared memory limit, set once per device (one of these,
+// A kernel's dynamic shared memory limit (and the leave for clusters of 16), set once per device (one of these,
 // static, beside each kernel's launch: its size never changes).
 class SmemLimit {
  public:
   template <typename Kern>
-  cudaError_t raise(Kern kern, int bytes) {
+  cudaError_t raise(Kern kern, int bytes, bool cluster16 = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (dev < 64 && (done_.load(std::memory_order_acquire) & bit)) return cudaSuccess;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && cluster16) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_release);
     return e;
   }
@@ -56,6 +57,7 @@ struct TreeAttnParams {
   float c;                   // scale * log2(e)
   int B, n, Hkv, gq;
   int S;                     // CTAs of a cluster: splits of the keys
+  bool sorted;               // blocks take the sequences longest first
   int* status;               // the device's status word (bounded waits)
 };
 

@@ -19,7 +19,8 @@
 // Warp roles: 4 softmax warps per block of NB rows (G blocks share the units),
 // one TMA warp, one warp that issues every MMA. A block's next scores are
 // computed right after its P V, while the other block (or the other CTA on the
-// SM, where shared memory lets two fit) is in its softmax.
+// SM, where shared memory lets two fit) is in its softmax; a lone block has two
+// buffers of S and P and is a tile ahead with its scores.
 #pragma once
 #include <cuda.h>
 
@@ -32,7 +33,7 @@ struct TreeAttnTcParams {
   TreeAttnParams p;
 };
 
-constexpr int kMaxSplits = 8;  // CTAs of a cluster (the portable limit)
+constexpr int kMaxSplits = 16;  // CTAs of a cluster
 
 template <int HD, bool F32, int NB, int G>
 struct TreeTc {
@@ -43,19 +44,24 @@ struct TreeTc {
   static constexpr int kUnit = BK * 128;                                  // bytes: 64 dims of a K or V tile
   static constexpr int kRowP = NO >= 48 ? 128 : 2 * NO;                   // bytes of a key's row of a P atom (64 columns)
   static constexpr int kPBlock = BK * kRowP * ((NO + 63) / 64);           // bytes of a block's P
-  static constexpr int kP = G * kPBlock, kQ = NQ * N * HD * 2, kOnes = 2048;
+  static constexpr int kQ = NQ * N * HD * 2, kOnes = 2048;
   static constexpr int kOffRow = 1024;                                   // of the small arrays: [N] row masks
-  static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4 * kMaxSplits) + 3 * kTreeMaxNodes * (HD / 32) * 4;
-  static constexpr int kFixed = kP + kQ + kOnes + kSmall + 1024;
+  static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4) + 3 * kTreeMaxNodes * (HD / 32) * 4;
+  static constexpr int kRest = kQ + kOnes + kSmall + 1024;
   static constexpr int kOut = N * HD * 4;                                // fp32 results, over the ring at the end
   static constexpr int kLimit = 232448, kHalf = 115712;                  // shared memory of a CTA alone, of two on an SM
-  static constexpr int kMin = 2 * H > kOut / kUnit ? 2 * H : kOut / kUnit;
-  static constexpr bool two = kFixed + (kMin > 4 ? kMin : 4) * kUnit <= kHalf;
+  // a tile's K and V units and, of 64 dims, the next K unit must fit
+  static constexpr int kLeast = H == 1 ? 3 : 4, kMin = kLeast > kOut / kUnit ? kLeast : kOut / kUnit;
+  // One block of rows: S and P twice, so that the next scores are ready when a
+  // softmax ends (where two CTAs then still fit on an SM).
+  static constexpr int DB = G == 1 && kRest + 2 * kPBlock + kMin * kUnit <= kHalf ? 2 : 1;
+  static constexpr int kFixed = kRest + G * DB * kPBlock;
+  static constexpr bool two = kFixed + kMin * kUnit <= kHalf;
   static constexpr int fit = ((two ? kHalf : kLimit) - kFixed) / kUnit;
   static constexpr int NST = fit < 12 ? fit : 12;
   static constexpr int kSmem = NST * kUnit + kFixed;
-  static_assert(NST >= kMin && NST >= 3, "shared memory");
-  static constexpr int kUsed = G * (NS + H * NO);                        // S, and O of every 64 dims
+  static_assert(NST >= kMin, "shared memory");
+  static constexpr int kUsed = G * (DB * NS + H * NO);                   // S, and O of every 64 dims
   static_assert(kUsed <= 512, "tensor memory");
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
@@ -189,16 +195,38 @@ __device__ __forceinline__ bool group_any(int g, bool x) {
   return r != 0;
 }
 
+// The sequence with the z-th longest cache of at most 64 (every warp finds it by
+// itself): blocks start in grid order, and starting the long sequences first
+// leaves the short ones to fill the end.
+__device__ __forceinline__ int nth_longest(const int* lens, int B, int z, int lane) {
+  const int a = lane < B ? lens[lane] : -1, c = lane + 32 < B ? lens[lane + 32] : -1;
+  int ra = 0, rc = 0;  // sequences ahead of this lane's two
+  for (int j = 0; j < min(B, 32); ++j) {
+    const int o = __shfl_sync(0xffffffffu, a, j);
+    ra += o > a || (o == a && j < lane);
+    rc += o >= c;
+  }
+  for (int j = 32; j < B; ++j) {
+    const int o = __shfl_sync(0xffffffffu, c, j - 32);
+    ra += o > a;
+    rc += o > c || (o == c && j < lane + 32);
+  }
+  const unsigned ha = __ballot_sync(0xffffffffu, lane < B && ra == z);
+  const unsigned hc = __ballot_sync(0xffffffffu, lane + 32 < B && rc == z);
+  return ha ? __ffs(ha) - 1 : 31 + __ffs(hc);
+}
+
 template <int HD, bool F32, int NB, int G>
 __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB, G>::two ? 2 : 1) tree_attn_tc_kernel(
     const __grid_constant__ TreeAttnTcParams tp) {
   using C = TreeTc<HD, F32, NB, G>;
-  constexpr int N = C::N, NT = C::NT, NST = C::NST, NQ = C::NQ, NP = C::NP, NG = HD / 32, BK = C::BK, H = C::H;
+  constexpr int N = C::N, NT = C::NT, NST = C::NST, NQ = C::NQ, NP = C::NP, NG = HD / 32, BK = C::BK, H = C::H, DB = C::DB;
   constexpr float kNone = -3e38f;  // the reference before any visible score
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.z, hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
+  const int hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
+  const int b = p.sorted ? nth_longest(p.lens, p.B, blockIdx.z, lane) : blockIdx.z;
   const int len_b = p.lens[b], cnt_b = p.counts ? p.counts[b] : p.n;
   const int cnt = min(max(cnt_b, 0), p.n);
   if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
@@ -208,12 +236,12 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   uint8_t* sring = sm;
-  uint8_t* sp = sring + NST * C::kUnit;   // [G] blocks of P: [atom of 64 columns][key][kRowP], columns part by part
-  uint8_t* sq = sp + C::kP;               // [H][G][NQ][NB][128 B]
+  uint8_t* sp = sring + NST * C::kUnit;   // [DB][G] blocks of P: [atom of 64 columns][key][kRowP], columns part by part
+  uint8_t* sq = sp + DB * G * C::kPBlock;               // [H][G][NQ][NB][128 B]
   uint8_t* sones = sq + C::kQ;
   uint8_t* small = sones + C::kOnes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
-  uint64_t *full = bars, *empty = bars + 12, *s_full = bars + 24, *p_full = bars + 26, *drain = bars + 28;
+  uint64_t *full = bars, *empty = bars + 12, *s_full = bars + 24, *p_full = bars + 26, *o_done = bars + 28, *drain = bars + 30;
   volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);
   int* s_any = reinterpret_cast<int*>(small + 260);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 264);
@@ -222,18 +250,26 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   float* sm_m = reinterpret_cast<float*>(srow + N);             // [N] references, negated
   float* sm_w = sm_m + N;                                       // [4][N]
   float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);        // [N]
-  float* sw = reinterpret_cast<float*>(sml + N);                // [kMaxSplits][N]
-  uint32_t* snf = reinterpret_cast<uint32_t*>(sw + kMaxSplits * N);     // [3][64][NG]
+  float* sfac = reinterpret_cast<float*>(sml + N);              // [N] rescaling of O and the sums
+  uint32_t* snf = reinterpret_cast<uint32_t*>(sfac + N);        // [3][64][NG]
+  float* sw = reinterpret_cast<float*>(sp);                     // [kMaxSplits][N] merge weights, when P is done with
+  static_assert(kMaxSplits * N * 4 <= DB * G * C::kPBlock, "merge weights");
 
   // TMA: the units in the order in which the MMAs release them
-  auto request = [&](int i) {  // unit i: of tile t0 + i / 2H, K then V
-    const int t = t0 + i / (2 * H), u = i % (2 * H), slot = i % NST;
+  const int n_own = t1 - t0, n_units = 2 * H * n_own;
+  // The ring's order, in halves (K or V) of the CTA's tiles: K0 V0 K1 V1 .., or,
+  // with scores a tile ahead, K0 K1 V0 K2 V1 ..
+  auto k_unit = [&](int t) { return H * (DB == 1 ? 2 * t : t == 0 ? 0 : 2 * t - 1); };
+  auto v_unit = [&](int t) { return H * (DB == 1 ? 2 * t + 1 : t == n_own - 1 ? 2 * t + 1 : 2 * t + 2); };
+  auto request = [&](int i) {
+    const int j = i / H, u = i % H, slot = i % NST;
+    const bool val = DB == 1 ? j & 1 : j > 0 && (!(j & 1) || j == 2 * n_own - 1);
+    const int t = t0 + (DB == 1 ? j / 2 : j == 2 * n_own - 1 ? n_own - 1 : val ? j / 2 - 1 : (j + 1) / 2);
     const bool tree = t >= n_pre;
-    const CUtensorMap* map = u >= H ? (tree ? &tp.tv : &tp.cv) : (tree ? &tp.tk : &tp.ck);
+    const CUtensorMap* map = val ? (tree ? &tp.tv : &tp.cv) : (tree ? &tp.tk : &tp.ck);
     mbar_expect_tx(full + slot, C::kUnit);
-    tma_box(sring + slot * C::kUnit, map, 64 * (u % H), tree ? 0 : t * BK, hkv, b, full + slot);
+    tma_box(sring + slot * C::kUnit, map, 64 * u, tree ? 0 : t * BK, hkv, b, full + slot);
   };
-  const int n_units = 2 * H * (t1 - t0);
   if (warp == 4 * G) {  // the ring's barriers are this warp's own: the first units are on their way at once
     if (lane == 0) {
       *s_abort = 0;
@@ -244,7 +280,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     }
   } else if (warp == 4 * G + 1) {
     if (lane == 0) {
-      for (int g = 0; g < G; ++g) mbar_init(s_full + g, 1), mbar_init(p_full + g, 128);
+      for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
       mbar_init(drain, 1);
       mbar_fence_init();
     }
@@ -258,7 +294,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     if (p.tree.k)
       for (int i = tid; i < kTreeMaxNodes; i += 128 * G)
         smask[i] = i < cnt ? p.mask[(int64_t)b * p.mask_seq + i] : 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = tid; i < N * (HD / 8); i += 128 * G) {
       const int r = i / (HD / 8), ch = i % (HD / 8), node = (m0 + r) / p.gq, h = hkv * p.gq + (m0 + r) % p.gq;
       const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
@@ -294,7 +330,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;  // S of block g at columns g NS, O of 64 dims u at G NS + (u G + g) NO
+  const uint32_t tmem = *s_tmem;  // S of block g at columns g NS (buffer d: d NS), O of 64 dims u at DB G NS + (u G + g) NO
   uint64_t seen = 0;              // tree rows that some node sees
   if (p.tree.k) {
     const uint64_t a = smask[lane] | smask[lane + 32];
@@ -326,10 +362,12 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     constexpr uint32_t step_p = 16 * C::kRowP, sbo_p = 8 * C::kRowP;
     const uint32_t uq = smem_u32(sq), up = smem_u32(sp), ur = smem_u32(sring), uo = smem_u32(sones);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    // block g's tile t0 + t: buffers and barriers x = g (DB 1) or t & 1 (DB 2)
     auto scores = [&](int g, int t) {
+      const int x = DB == 2 ? t & 1 : g;
 #pragma unroll
       for (int u = 0; u < H; ++u) {
-        const int i = 2 * H * (t - t0) + u, slot = i % NST;
+        const int i = k_unit(t) + u, slot = i % NST;
         if (!tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status)) return false;
         tc_fence_after();
         const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
@@ -337,42 +375,44 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         if (elect_lane()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
-            tc_mma(tm + g * C::NS, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
+            tc_mma(tm + x * C::NS, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
         }
         __syncwarp();
         if (g == G - 1) tc_commit(empty + slot);
       }
-      tc_commit(s_full + g);
+      tc_commit(s_full + x);
       return true;
     };
     bool ok = true;
-    for (int g = 0; g < G && ok && t0 < t1; ++g) ok = scores(g, t0);
-    for (int t = t0; t < t1 && ok; ++t)
+    for (int t = 0; t < DB && t < n_own && ok; ++t)
+      for (int g = 0; g < G && ok; ++g) ok = scores(g, t);
+    for (int t = 0; t < n_own && ok; ++t)
 #pragma unroll 1
       for (int g = 0; g < G && ok; ++g) {
-        ok = tc_wait_warp(p_full + g, (t - t0) & 1, s_abort, p.status);
+        const int x = DB == 2 ? t & 1 : g;
+        ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
 #pragma unroll
         for (int u = 0; u < H; ++u) {
-          const int i = 2 * H * (t - t0) + H + u, slot = i % NST;
+          const int i = v_unit(t) + u, slot = i % NST;
           ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t v = ur + slot * C::kUnit;
           // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
           const uint64_t da = tc_desc(v, uo - v, 1024, 2);
-          const uint64_t dp = tc_desc(up + g * C::kPBlock, BK * 128, sbo_p, swp);
+          const uint64_t dp = tc_desc(up + x * C::kPBlock, BK * 128, sbo_p, swp);
           if (elect_lane()) {
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
-              tc_mma(tm + G * C::NS + (u * G + g) * C::NO, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
-                     dp + (ks * step_p >> 4), idesc_o, t > t0 || ks > 0);
+              tc_mma(tm + DB * G * C::NS + (u * G + g) * C::NO, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                     dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
           }
           __syncwarp();
           if (g == G - 1) tc_commit(empty + slot);
         }
         if (!ok) break;
-        if (t + 1 < t1) ok = scores(g, t + 1);
-        else tc_commit(s_full + g);  // the block's O is complete
+        tc_commit(o_done + g);
+        if (t + DB < n_own) ok = scores(g, t + DB);
       }
     if (!ok) {  // no MMA may outlive its operands
       tc_commit(drain);
@@ -383,8 +423,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   } else {
     // ---- softmax: thread = key
     const int g = warp >> 2, key = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * C::NS;
-    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + G * C::NS + g * C::NO;  // of 64 dims u: + u G NO
+    uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * C::NS;
+    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + DB * G * C::NS + g * C::NO;  // of 64 dims u: + u G NO
     float* m = sm_m + g * NB;  // the references, negated
     const float masked = p.c < 0.f ? INFINITY : -INFINITY;  // times c: -inf (c is not 0)
     if (p.tree.k)
@@ -413,12 +453,12 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
       if (!whole) {  // V rows that are not there become zeros, non-finite tree values too (noted for the rows that see them)
         for (int u = 0; u < H; ++u) {
-          const int i = 2 * H * (t - t0) + H + u;
+          const int i = v_unit(t - t0) + u;
           tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
         }
 #pragma unroll 4
         for (int c = 0; c < HD / 8 && (tree || !valid); ++c) {
-          const int slot = (2 * H * (t - t0) + H + c / 8) % NST;
+          const int slot = (v_unit(t - t0) + c / 8) % NST;
           uint4* x = reinterpret_cast<uint4*>(sring + slot * C::kUnit + key * 128 + 16 * ((c & 7) ^ (key & 7)));
           if (!valid) {
             *x = make_uint4(0u, 0u, 0u, 0u);
@@ -444,10 +484,13 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           }
         }
       }
-      tc_wait(s_full + g, (t - t0) & 1, s_abort, p.status);
+      // these scores: this buffer's last P V is done too
+      const int x = DB == 2 ? (t - t0) & 1 : g;
+      tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
       tc_fence_after();
+      if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NS;
       if (t == t0) {  // the references: the score of the first key that a row sees (renewed below if not finite)
-        float* first = reinterpret_cast<float*>(sp + g * C::kPBlock);  // [64][NB], where P comes to lie
+        float* first = reinterpret_cast<float*>(sp + x * C::kPBlock);  // [64][NB], where P comes to lie
         static_assert(64 * NB * 4 <= C::kPBlock, "room for the first scores");
         if (warp < 4 * g + (tree ? 2 : 1))
 #pragma unroll 1
@@ -470,7 +513,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         }
         group_sync(g);
       }
-      uint8_t* prow = sp + g * C::kPBlock + key * C::kRowP;
+      uint8_t* prow = sp + x * C::kPBlock + key * C::kRowP;
       const int sel = C::kRowP == 128 ? key & 7 : (C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
       for (;;) {
         // probabilities with the references as they are; the largest excess over them
@@ -542,10 +585,12 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           const float* w = sm_w + g * NB + key;
           const float old = -m[key], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
           m[key] = -now;
-          sw[g * NB + key] = old == now ? 1.f : exp2f(old - now);
+          sfac[g * NB + key] = old == now ? 1.f : exp2f(old - now);
         }
         group_sync(g);
         if (t > t0) {
+          tc_wait(o_done + g, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V is in O
+          tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < C::NO * H; c0 += 16) {
             const uint32_t at = tO + (c0 / C::NO) * G * C::NO + c0 % C::NO;
@@ -553,7 +598,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
             tc_ld(s, at);
             tc_wait_ld(s);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] *= sw[g * NB + (c0 + j) % NB];
+            for (int j = 0; j < 16; ++j) s[j] *= sfac[g * NB + (c0 + j) % NB];
             tc_st16(at, s);
           }
           tc_wait_st();
@@ -561,10 +606,12 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       }
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(p_full + g);
+      mbar_arrive(p_full + x);
     }
     // ---- O^T and the sums to shared memory, [row][dim]
-    if (t0 < t1) tc_wait(s_full + g, (t1 - t0) & 1, s_abort, p.status);
+    // (one phase at a time: with two buffers the last but one P V may still run)
+    if (DB == 2 && n_own > 1) tc_wait(o_done + g, (n_own - 2) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait(o_done + g, (n_own - 1) & 1, s_abort, p.status);
     tc_fence_after();
     // every block's last MMAs have read the ring and P before any block writes over them
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
@@ -631,16 +678,20 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
   for (int i = i0 + tid; i < i1; i += NT) {
     const int r = i / (HD / 4), node = (m0 + r) / p.gq, h = hkv * p.gq + (m0 + r) % p.gq;
-    float4 x[kMaxSplits], a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < p.S; k0 += 8) {
+      float4 x[8];
 #pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k)
-      if (k < p.S) x[k] = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k))[i];
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < p.S) x[k] = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k0 + k))[i];
 #pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k)
-      if (k < p.S) {
-        const float f = sw[k * N + r];
-        a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y), a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
-      }
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < p.S) {
+          const float f = sw[(k0 + k) * N + r];
+          a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y), a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
+        }
+    }
     const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % (HD / 4));
     if constexpr (F32)
       *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = a;
@@ -697,17 +748,22 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   using C = TreeTc<HD, F32, NB, G>;
   const auto kern = tree_attn_tc_kernel<HD, F32, NB, G>;
   static SmemLimit limit;
-  cudaError_t e = limit.raise(kern, C::kSmem);
+  cudaError_t e = limit.raise(kern, C::kSmem, true);
   if (e != cudaSuccess) return e;
   TreeAttnParams& p = tp.p;
   const int m_tiles = (p.n * p.gq + C::N - 1) / C::N;
   const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
   int S = 1;
-  // split the keys until every SM has a CTA: more splits cost their merges (32 sequences of 512..2048 rows,
-  // 256 clusters: 51.8 / 56.8 / 66.6 us for 1 / 2 / 4; 128 clusters of 1024..8192 rows: 232 / 213 / 226)
-  while (S < kMaxSplits && S < tiles && clusters * S < n_sm) S *= 2;
+  // Split the keys until every SM has a CTA; where two fit, also to fill both
+  // places while 16 tiles are left for each: more splits cost their merges
+  // (32 sequences x 8 kv heads, 17 tiles: 43 / 48 / 67 us for 1 / 2 / 4; 16 x 4 x 4 row
+  // tiles, 65 tiles: 129 / 109 / 132; 8 clusters of 513 tiles: 667 / 340 / 179 / 96 for 1 to 8).
+  while (S < kMaxSplits && S < tiles &&
+         (clusters * S < n_sm || (C::two && clusters * S < 2 * n_sm && tiles / (2 * S) >= 16)))
+    S *= 2;
   p.S = S;
+  p.sorted = p.B > 1 && p.B <= 64;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(S, p.Hkv * m_tiles, p.B);
   cfg.blockDim = dim3(C::NT);
@@ -738,21 +794,22 @@ bool launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStream_t st
   // Rows of a CTA: as many as there are (K and V are read once for them), in two
   // blocks once there are 32 (one block's softmax overlaps the other's MMAs); but
   // fewer while the clusters, split eight ways, would leave SMs without a CTA
-  // (16 nodes x 8 heads over 4097 rows, fp32: 64 rows a CTA 24.6 us, 16 rows %s).
-  const int M = p.n * p.gq, most = f32 ? (HD == 64 ? 64 : 32) : (HD == 64 ? 256 : 128);
+  // (16 nodes x 8 heads over 4097 rows, fp32: 16 / 32 / 64 rows 16.5 / 18.6 / 20.6 us).
+  // 128 rows at most: 256 fill tensor memory and leave one CTA on an SM (16 x 64
+  // nodes over 1024..8192 rows: 119 against 109 us).
+  const int M = p.n * p.gq, most = f32 ? (HD == 64 ? 64 : 32) : 128;
   int N = 16;
   while (N < M && N < most) N *= 2;
-  while (N > 16 && (int64_t)p.B * p.Hkv * ((M + N - 1) / N) * kMaxSplits < n_sm) N /= 2;
+  while (N > 16 && (int64_t)p.B * p.Hkv * ((M + N - 1) / N) * 8 < n_sm) N /= 2;
   if (f32)
     *e = N == 16   ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st)
          : N == 32 ? launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st)
                    : launch_tree_tc_t<HD, true, HD == 64 ? 32 : 16, 2>(tp, n_sm, st);
   else
-    *e = N == 16    ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)
-         : N == 32  ? launch_tree_tc_t<HD, false, 16, 2>(tp, n_sm, st)
-         : N == 64  ? launch_tree_tc_t<HD, false, 32, 2>(tp, n_sm, st)
-         : N == 128 ? launch_tree_tc_t<HD, false, 64, 2>(tp, n_sm, st)
-                    : launch_tree_tc_t<HD, false, HD == 64 ? 128 : 64, 2>(tp, n_sm, st);
+    *e = N == 16   ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)
+         : N == 32 ? launch_tree_tc_t<HD, false, 16, 2>(tp, n_sm, st)
+         : N == 64 ? launch_tree_tc_t<HD, false, 32, 2>(tp, n_sm, st)
+                   : launch_tree_tc_t<HD, false, 64, 2>(tp, n_sm, st);
   return true;
 }
 
