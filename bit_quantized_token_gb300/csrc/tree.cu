@@ -21,24 +21,6 @@ cudaError_t launch_tree_attn(const TreeAttnParams& p, int hd, bool f32, bool q8,
 
 namespace {
 
-template <typename Kern, typename Params>
-cudaError_t launch_cluster(Kern kern, dim3 grid, int threads, int cluster, size_t smem, cudaStream_t st,
-                           const Params& p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 // ---- sums that decide integers --------------------------------------------------
 // A sum over a vocabulary picks a token, so it is carried far beyond fp32: as an
 // unevaluated pair of floats (two-sums and fused products, ~2^-46 relative).
@@ -164,6 +146,8 @@ __global__ void __launch_bounds__(kProbThreads) softmax_rows_kernel(const TokenP
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
   auto started = cl.barrier_arrive();  // shared memory of another CTA: only once that CTA runs
+  pdl_wait();
+  pdl_trigger();
   const ProbRange r(p.V, rank, C);
   const float* src = p.logits + (int64_t)row * p.l_row + r.a;
   const Slice sl(src, r.n);
@@ -260,6 +244,8 @@ __global__ void __launch_bounds__(kProbThreads) topk_rows_kernel(const TokenProb
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x;
   auto started = cl.barrier_arrive();
+  pdl_wait();
+  pdl_trigger();
   const ProbRange r(p.V, rank, C);
   const int K = min(p.top_k, p.V);
   int* cand = reinterpret_cast<int*>(sx + p.cap + 4);
@@ -468,6 +454,8 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   int* path_out = p.path + (int64_t)b * p.n;
   const float* pb = p.p + (int64_t)b * p.p_seq;
   const float* qb = SOFT ? p.q + (int64_t)b * p.q_seq : nullptr;
+  pdl_wait();
+  pdl_trigger();
   // every node's test values at once
   int par = -1, tok = 0;
   float u = 0.f;
@@ -685,6 +673,8 @@ __global__ void __launch_bounds__(kTreeMaxNodes) verify_greedy_kernel(const Veri
   __shared__ int tok[kTreeMaxNodes], par[kTreeMaxNodes], tgt[kTreeMaxNodes], path[kTreeMaxNodes];
   __shared__ int s_n;
   const int b = blockIdx.x, tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
   const int cnt = p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
   if (tid < cnt) {
     const int64_t at = (int64_t)b * p.n + tid;
@@ -713,6 +703,8 @@ __global__ void __launch_bounds__(kTreeMaxNodes) verify_greedy_kernel(const Veri
 constexpr int kCommitRows = 4;
 __global__ void __launch_bounds__(256) commit_kernel(const CommitParams p) {
   const int b = blockIdx.y, tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
   const int len = max(p.lens[b], 0);
   const int n = min(min(max(p.n_path[b], 0), p.n), max(p.cache.rows - len, 0));
   if (p.new_lens != p.lens && blockIdx.x == 0 && tid == 0) p.new_lens[b] = len + n;
@@ -751,6 +743,8 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitParams p) {
 }
 __global__ void __launch_bounds__(256) advance_kernel(const CommitParams p) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
   if (b >= p.B) return;
   const int len = max(p.lens[b], 0);
   p.new_lens[b] = len + min(min(max(p.n_path[b], 0), p.n), max(p.cache.rows - len, 0));
@@ -793,8 +787,7 @@ cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t
 
 cudaError_t launch_verify_tree(const VerifyParams& p, int n_sm, cudaStream_t st) {
   if (p.targets) {
-    verify_greedy_kernel<<<p.B, kTreeMaxNodes, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_cluster(verify_greedy_kernel, dim3(p.B), kTreeMaxNodes, 1, 0, st, p);
   }
   int C = 1;
   while (C < 8 && p.V / (2 * C) >= 2 * kVerThreads) C *= 2;
@@ -804,12 +797,9 @@ cudaError_t launch_verify_tree(const VerifyParams& p, int n_sm, cudaStream_t st)
 
 cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st) {
   const int64_t rows = (int64_t)2 * p.L * p.Hkv * p.n, per = kCommitRows * 256 / (p.row_bytes / 16);
-  commit_kernel<<<dim3((unsigned)((rows + per - 1) / per), p.B), 256, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && p.new_lens == p.lens) {  // every copy has read the lengths before they advance
-    advance_kernel<<<(p.B + 255) / 256, 256, 0, st>>>(p);
-    e = cudaGetLastError();
-  }
+  cudaError_t e = launch_cluster(commit_kernel, dim3((unsigned)((rows + per - 1) / per), p.B), 256, 1, 0, st, p);
+  if (e == cudaSuccess && p.new_lens == p.lens)  // every copy has read the lengths before they advance
+    e = launch_cluster(advance_kernel, dim3((p.B + 255) / 256), 256, 1, 0, st, p);
   return e;
 }
 

@@ -35,6 +35,30 @@ class SmemLimit {
   std::atomic<uint64_t> done_{0};
 };
 
+// Launch in clusters along x (of one CTA: none), as a programmatic dependent:
+// the launch and a kernel's set-up overlap the end of the kernel before it. Every
+// kernel launched so waits (griddepcontrol) before its first access to global
+// memory, in every thread, so stream order holds as without it.
+template <typename Kern, typename Params>
+cudaError_t launch_cluster(Kern kern, dim3 grid, int threads, int cluster, size_t smem, cudaStream_t st,
+                           const Params& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 struct KvRows {              // K and V rows of one layer: a cache, or the drafted tree's own
   const uint8_t* k = nullptr;      // bf16 values, or int8 codes (then the scales are set)
   const uint8_t* v = nullptr;

@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(32 * WM * WK) tree_attn_kernel(const __grid_co
   extern __shared__ __align__(128) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wm = warp / WK, wk = warp % WK;
   const int b = blockIdx.z, g = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * MT, rank = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
   const int cnt = p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
   if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
   const int len = min(max(p.lens[b], 0), p.cache.rows);
@@ -517,19 +519,7 @@ cudaError_t launch_tree_attn_t(TreeAttnParams p, int n_sm, cudaStream_t st) {
   int S = 1;
   while (S < 8 && S < tiles && clusters * S < 4 * n_sm) S *= 2;
   p.S = S;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(S, p.Hkv * m_tiles, p.B);
-  cfg.blockDim = dim3(C::NT);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, p);
 }
 
 template <int HD, bool F32, bool KV8>

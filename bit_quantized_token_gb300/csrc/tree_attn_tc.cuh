@@ -225,15 +225,6 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
-  const int b = p.sorted ? nth_longest(p.lens, p.B, blockIdx.z, lane) : blockIdx.z;
-  const int len_b = p.lens[b], cnt_b = p.counts ? p.counts[b] : p.n;
-  const int cnt = min(max(cnt_b, 0), p.n);
-  if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
-  const int len = min(max(len_b, 0), p.cache.rows);
-  const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
-  const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S);
-
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   uint8_t* sring = sm;
   uint8_t* sp = sring + NST * C::kUnit;   // [DB][G] blocks of P: [atom of 64 columns][key][kRowP], columns part by part
@@ -256,6 +247,22 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   static_assert(kMaxSplits * N * 4 <= DB * G * C::kPBlock, "merge weights");
 
   // TMA: the units in the order in which the MMAs release them
+  if (tid == 4 * G * 32) {
+    *s_abort = 0;
+    *s_any = 0;
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+    mbar_fence_init();
+  }
+  pdl_wait();  // nothing before this touches global memory
+  pdl_trigger();
+  const int hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
+  const int b = p.sorted ? nth_longest(p.lens, p.B, blockIdx.z, lane) : blockIdx.z;
+  const int len_b = p.lens[b], cnt_b = p.counts ? p.counts[b] : p.n;
+  const int cnt = min(max(cnt_b, 0), p.n);
+  if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
+  const int len = min(max(len_b, 0), p.cache.rows);
+  const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
+  const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S);
   const int n_own = t1 - t0, n_units = 2 * H * n_own;
   // The ring's order, in halves (K or V) of the CTA's tiles: K0 V0 K1 V1 .., or,
   // with scores a tile ahead, K0 K1 V0 K2 V1 ..
@@ -271,13 +278,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     tma_box(sring + slot * C::kUnit, map, 64 * u, tree ? 0 : t * BK, hkv, b, full + slot);
   };
   if (warp == 4 * G) {  // the ring's barriers are this warp's own: the first units are on their way at once
-    if (lane == 0) {
-      *s_abort = 0;
-      *s_any = 0;
-      for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
-      mbar_fence_init();
+    if (lane == 0)
       for (int i = 0; i < NST && i < n_units; ++i) request(i);
-    }
   } else if (warp == 4 * G + 1) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       mbar_fence_init();
     }
     __syncwarp();
+    // (after pdl_wait: held earlier, it could be what the kernel before this one is waiting for)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
                  "r"((uint32_t)C::kCols)
                  : "memory");
@@ -764,19 +767,7 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
     S *= 2;
   p.S = S;
   p.sorted = p.B > 1 && p.B <= 64;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(S, p.Hkv * m_tiles, p.B);
-  cfg.blockDim = dim3(C::NT);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tp);
+  return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, tp);
 }
 
 // bf16 rows; false: TMA cannot address these tensors (strides of 0, or of 2^40 bytes).
