@@ -99,6 +99,7 @@ struct TokenProbsParams {
   int top_k;                 // 0: every token
   float top_p;
   int cap = 0;               // set by the launch: floats of a slice
+  int* status;               // the device's status word (bounded waits)
 };
 cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t st);
 

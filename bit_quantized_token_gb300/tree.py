@@ -164,7 +164,7 @@ def tree_attention(q, cache: KVView, tree: KVView | None, lens, mask, out, count
 
 
 def tree_status(stream: int | None = None) -> None:
-    """Wait for the stream and raise if a tree attention's device-side wait passed its limit; see llm_tree_status."""
+    """Wait for the stream and raise if a tree operator's device-side wait passed its limit; see llm_tree_status."""
     L = _lib or _load()
     _check(L.llm_tree_status(stream))
 

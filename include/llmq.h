@@ -428,8 +428,8 @@ typedef struct {
 int llm_tree_attention(const llm_tree_attention_args* args, void* cuda_stream);
 
 /* Wait for `cuda_stream` and report whether a device-side wait of a
- * llm_tree_attention on the current device passed its limit (2 s) since the last call
- * (TIMEOUT: the outputs of that call are not valid). */
+ * llm_tree_attention or llm_token_probs on the current device passed its limit
+ * (2 s) since the last call (TIMEOUT: the outputs of that call are not valid). */
 int llm_tree_status(void* cuda_stream);
 
 /* probs[r] = the distribution the sampler of llm_set_sampling draws from:
