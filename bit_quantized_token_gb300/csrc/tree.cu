@@ -4,7 +4,6 @@
 
 #include <cmath>
 #include <cstdio>
-#include <type_traits>
 #include <utility>
 
 #include "common.cuh"
@@ -475,6 +474,10 @@ __global__ void __launch_bounds__(kProbThreads) topk_rows_kernel(const TokenProb
 
 // ---- draft verification ---------------------------------------------------------
 constexpr int kVerThreads = 512;
+template <int K>
+struct Const {
+  static constexpr int value = K;
+};
 
 struct VerShared {
   int tok[kTreeMaxNodes], path[kTreeMaxNodes];
@@ -489,21 +492,26 @@ struct VerShared {
   int first, last;
 };
 
-// What k rejections leave of p(j), unnormalised after the last one. K: k where
-// it is 0 or 1 (exact, no reciprocals), 2: any k.
-template <int K>
-__device__ __forceinline__ Two residual(float p, float q, const Two* inv, int k) {
-  Two r = {fmaxf(p, 0.f), 0.f};  // a NaN probability counts as 0
+// What k rejections leave of p(j), unnormalised after the last one; a NaN
+// probability counts as 0. One rejection (or none: q = 0) is exact. The general
+// case is a call: inlined with the rest, the kernel's 200 KB of code, fetched
+// once by every CTA, were what a small tree waited for.
+__device__ __forceinline__ Two residual1(float p, float q) {
   q = fmaxf(q, 0.f);
-  for (int i = 0; i < (K < 2 ? K : k); ++i) {
-    if (K == 2 && i > 0) r = r * inv[i];
-    const Two d = K == 2 ? r + Two{-q, 0.f} : two_sum(r.h, -q);
+  const float h = __fsub_rn(p, q);
+  // (p >= q >= 0 where the difference counts: three operations are exact)
+  return h > 0.f ? Two{h, __fsub_rn(__fsub_rn(p, h), q)} : Two{0.f, 0.f};
+}
+static __device__ __noinline__ Two residual_of(float p, float q, const Two* inv, int k) {
+  Two r = {fmaxf(p, 0.f), 0.f};
+  q = fmaxf(q, 0.f);
+#pragma unroll 1
+  for (int i = 0; i < k; ++i) {
+    if (i > 0) r = r * inv[i];
+    const Two d = r + Two{-q, 0.f};
     r = d.h > 0.f ? d : Two{0.f, 0.f};
   }
   return r;
-}
-__device__ __forceinline__ Two residual_any(float p, float q, const Two* inv, int k) {
-  return k == 0 ? residual<0>(p, q, inv, k) : k == 1 ? residual<1>(p, q, inv, k) : residual<2>(p, q, inv, k);
 }
 
 // One cluster per sequence. Every CTA walks the tree on the same prefetched
@@ -576,13 +584,16 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   u64 gone_bits = 0;     // !SOFT: which of this lane's elements (the first 64) are rejected tokens
   bool gone_far = false;  // and whether one beyond is
   auto rejected = [&](int j) {
+#pragma unroll 1
     for (u64 w = s.child[cur]; w; w &= w - 1)
       if (s.tok[__ffsll(w) - 1] == j) return true;
     return false;
   };
+  // this lane's part of it, after K (2: any number of) rejections
   auto sum = [&](auto kk) {
     constexpr int K = decltype(kk)::value;
     Two a[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 2
     for (int e = 0; e < chunk; e += 8) {
       float x[8], y[8];
       const int i0 = w0 + 32 * e + lane;
@@ -598,23 +609,29 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
         for (int v = 0; v < 8; ++v)
           if ((bits >> v) & 1) x[v] = 0.f;
         if (gone_far && e >= 64)
+#pragma unroll 1
           for (int v = 0; v < 8; ++v)
             if (rejected(i0 + 32 * v)) x[v] = 0.f;
       }
 #pragma unroll
-      for (int v = 0; v < 8; ++v) a[v & 1] = two_add(a[v & 1], residual<K>(x[v], K > 0 ? y[v] : 0.f, s.inv, k));
+      for (int v = 0; v < 8; ++v) {
+        if constexpr (K == 0) {
+          const Two t = two_sum(a[v & 1].h, fmaxf(x[v], 0.f));
+          a[v & 1] = {t.h, __fadd_rn(a[v & 1].l, t.l)};
+        } else {
+          a[v & 1] = two_add(a[v & 1], K == 1 ? residual1(x[v], y[v]) : residual_of(x[v], y[v], s.inv, k));
+        }
+      }
     }
     return two_add(a[0], a[1]);
   };
-  auto total = [&]() {  // the sum over the row of `cur` after k rejections; leaves warp_sum and sums
+  // the sum over the row of `cur` after k rejections; leaves warp_sum and sums
+  auto total = [&]() {
     pr = pb + (int64_t)cur * p.p_node;
-    Two d;
     if constexpr (SOFT) {
       qr = qb + (int64_t)cur * p.q_node;
-      d = k == 0   ? sum(std::integral_constant<int, 0>{})
-          : k == 1 ? sum(std::integral_constant<int, 1>{})
-                   : sum(std::integral_constant<int, 2>{});
     } else {
+#pragma unroll 1
       for (u64 w = s.child[cur]; w; w &= w - 1) {
         const int off = s.tok[__ffsll(w) - 1] - w0, e = off >> 5;
         if (off >= 0 && e < chunk && (off & 31) == lane) {
@@ -622,8 +639,10 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
           else gone_far = true;
         }
       }
-      d = sum(std::integral_constant<int, 0>{});
     }
+    Two d;
+    if constexpr (SOFT) d = k == 0 ? sum(Const<0>{}) : k == 1 ? sum(Const<1>{}) : sum(Const<2>{});
+    else d = sum(Const<0>{});
     d = two_reduce<32>(d);
     if (lane == 0) s.warp_sum[warp] = d;
     __syncthreads();
@@ -636,56 +655,50 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     turn ^= 1;  // the other ranks have left the other buffer before this call's barrier
     return t;
   };
-  bool known = true;  // s.mass[k], s.inv[k] are set
-  Two left = {1.f, 0.f};  // !SOFT: 1 less the probability of the rejected children
+  bool known = true;     // s.mass[k], s.inv[k] are set
+  Two left = {1.f, 0.f}; // !SOFT: 1 less the probability of the rejected children
+  Two tot;
   const u64 first_take = s.take;
-  for (u64 w = s.child[0]; w;) {
-    const int i = __ffsll(w) - 1;
-    w &= w - 1;
-    bool take;
-    if (k == 0) {
-      take = (first_take >> i) & 1;
-      if (!SOFT) left = two_sum(1.f, -s.px[i]);
-    } else if constexpr (SOFT) {
-      if (!known) {
-        const Two m = total();
-        if (m.h > 0.f) {
-          if (tid == 0) {
-            s.inv[k] = two_recip(m);
-            s.mass[k] = m;
-          }
-          __syncthreads();
-        } else {  // nothing is left: that rejection does not count
-          --k;
-        }
-        known = true;
+  for (u64 w = s.child[0];;) {
+#pragma unroll 1
+    while (w && (!SOFT || known)) {  // as far as it goes without a sum
+      const int i = __ffsll(w) - 1;
+      w &= w - 1;
+      bool take;
+      if (k == 0) {
+        take = (first_take >> i) & 1;
+        if (!SOFT) left = two_sum(1.f, -s.px[i]);
+      } else if constexpr (SOFT) {
+        take = two_prod(s.u[i], s.qx[i]) * s.mass[k] < residual_of(s.px[i], s.qx[i], s.inv, k);
+      } else {
+        const float x = s.px[i];
+        take = left * Two{s.u[i], 0.f} < Two{x, 0.f};
+        left = left + Two{-x, 0.f};
       }
-      // (--k may have left no rejection: inv and mass of 0 are those of p itself)
-      const Two r = residual_any(s.px[i], s.qx[i], s.inv, k);
-      take = two_prod(s.u[i], s.qx[i]) * s.mass[k] < r;
-    } else {
-      const float x = s.px[i];
-      take = left * Two{s.u[i], 0.f} < Two{x, 0.f};
-      left = left + Two{-x, 0.f};
+      if (take && i < cnt) {
+        if (tid == 0) s.path[n_path] = i;
+        cur = i;
+        ++n_path;
+        k = 0;
+        w = s.child[i];
+      } else {
+        ++k;
+        known = false;
+      }
     }
-    if (i >= cnt) take = false;
-    if (take) {
-      if (tid == 0) s.path[n_path] = i;
-      cur = i;
-      ++n_path;
-      k = 0;
-      known = true;
-      w = s.child[i];
-    } else {
-      ++k;
-      known = false;
-    }
-  }
-  // ---- the next token, from what is left at `cur`
-  Two tot = total();
-  while (SOFT && k > 0 && !(tot.h > 0.f)) {
-    --k;
     tot = total();
+    if (!SOFT) break;
+    if (tot.h > 0.f || k == 0) {
+      if (w == 0) break;  // no child is left: tot is what the next token is drawn from
+      if (tid == 0) {
+        s.inv[k] = two_recip(tot);
+        s.mass[k] = tot;
+      }
+      __syncthreads();
+    } else {
+      --k;  // nothing was left: that rejection does not count (the mass of the one before it is known)
+    }
+    known = true;
   }
   const Two target = tot * Two{s.u[0], 0.f};
   // the rank where the running sum passes the target (every warp finds it from the same sums)
@@ -727,7 +740,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     ys[e] = SOFT && k && l0 + e < l1 ? qr[l0 + e] : 0.f;
   }
   auto element = [&](int e, float x, float y) {
-    if constexpr (SOFT) return residual_any(x, y, s.inv, k);
+    if constexpr (SOFT) return k < 2 ? residual1(x, y) : residual_of(x, y, s.inv, k);
     else return Two{(e < 64 ? (holes >> e) & 1 : rejected(l0 + e)) ? 0.f : fmaxf(x, 0.f), 0.f};
   };
   auto far = [&](int e) { return element(e, pr[l0 + e], SOFT && k ? qr[l0 + e] : 0.f); };
@@ -807,20 +820,22 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitParams p) {
   const int len = max(p.lens[b], 0);
   const int n = min(min(max(p.n_path[b], 0), p.n), max(p.cache.rows - len, 0));
   if (p.new_lens != p.lens && blockIdx.x == 0 && tid == 0) p.new_lens[b] = len + n;
-  const int ch = p.row_bytes / 16, c = tid % ch, slots = 256 / ch;  // 4, 8 or 16 chunks a row
-  const int rows = 2 * p.L * p.Hkv * n, first = blockIdx.x * kCommitRows * slots + tid / ch;
+  const int lch = p.row_bytes == 256 ? 4 : p.row_bytes == 128 ? 3 : 2;  // log2 of a row's 16-byte chunks
+  const int c = tid & ((1 << lch) - 1), slots = 256 >> lch;
+  const int rows = 2 * p.L * p.Hkv * n, first = blockIdx.x * kCommitRows * slots + (tid >> lch);
   if (first >= rows) return;
   const int esize = p.srow_bytes ? 1 : 2;
+  int lh = first / n, k = first - lh * n;  // row first + u slots: (layer, head, K or V) lh, node k of the path
+  const int step_lh = slots / n, step_k = slots - step_lh * n;
   uint4 x[kCommitRows];
   uint8_t* dst[kCommitRows];
 #pragma unroll
   for (int u = 0; u < kCommitRows; ++u) {
-    const int i = first + u * slots;
     dst[u] = nullptr;
-    if (i < rows) {
-      const int lh = i / n, k = i - lh * n, kv = lh & 1, h = (lh >> 1) % p.Hkv, l = (lh >> 1) / p.Hkv;
+    if (first + u * slots < rows) {
       const int node = p.path[(int64_t)b * p.path_seq + k];
       if (node >= 0 && node < p.tree.rows) {
+        const int kv = lh & 1, l = p.by_heads.div(lh >> 1), h = (lh >> 1) - l * p.Hkv;
         x[u] = *reinterpret_cast<const uint4*>(
             (kv ? p.tree.v : p.tree.k) +
             esize * (b * p.tree.seq + l * p.t_layer + h * p.tree.head + node * p.tree.row) + 16 * c);
@@ -831,10 +846,14 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitParams p) {
                                node * p.tree.srow;
           uint16_t* sd = const_cast<uint16_t*>(kv ? p.cache.vs : p.cache.ks) + b * p.cache.sseq + l * p.c_slayer +
                          h * p.cache.shead + (len + k) * p.cache.srow;
+#pragma unroll 1
           for (int e = 0; e < p.srow_bytes / 2; ++e) sd[e] = ss[e];
         }
       }
     }
+    lh += step_lh;
+    k += step_k;
+    if (k >= n) k -= n, ++lh;
   }
 #pragma unroll
   for (int u = 0; u < kCommitRows; ++u)
@@ -1065,7 +1084,8 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
       !c.need(v.n_seq >= a->n_seq && v.n_layers == 1, LLM_ERR_INVALID_ARG,
               "the cache view holds fewer sequences, or several layers") ||
       !c.need((int64_t)v.n_heads * ((int64_t)a->n_nodes * (a->n_heads / v.n_heads) / 16 + 1) <= 65535,
-              LLM_ERR_UNSUPPORTED, "too many heads"))
+              LLM_ERR_UNSUPPORTED, "too many heads") ||
+      !c.need((int64_t)a->n_nodes * (a->n_heads / v.n_heads) < 65536, LLM_ERR_UNSUPPORTED, "too many heads"))
     return c.rc;
   if (t && (!check_view(c, t, "tree") ||
             !c.need(t->dtype == v.dtype && t->head_dim == v.head_dim && t->n_heads == v.n_heads && t->n_layers == 1 &&
@@ -1103,6 +1123,7 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
   p.n = a->n_nodes;
   p.Hkv = v.n_heads;
   p.gq = a->n_heads / v.n_heads;
+  p.by_gq = FastDiv(p.gq);
   return finish(launch_tree_attn(p, (int)hd, a->dtype == LLM_F32, v.dtype == LLM_Q8G32, c.n_sm,
                                  static_cast<cudaStream_t>(cuda_stream)),
                 "tree attention launch");
@@ -1203,7 +1224,9 @@ int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n
   Call c;
   if (!c.need(n_nodes >= 1 && n_nodes <= kTreeMaxNodes, LLM_ERR_UNSUPPORTED, "%sn_nodes %lld (1..64)", "", n_nodes) ||
       !c.need(n_seq >= 1, LLM_ERR_INVALID_ARG, "n_seq is not positive") || !check_view(c, cache, "cache") ||
-      !c.need((int64_t)2 * cache->n_layers * cache->n_heads * n_nodes < (1ll << 31), LLM_ERR_UNSUPPORTED,
+      !c.need((int64_t)2 * cache->n_layers * cache->n_heads * n_nodes < (1ll << 31) &&
+                  (int64_t)cache->n_layers * cache->n_heads * cache->n_heads < (1ll << 32),
+              LLM_ERR_UNSUPPORTED,
               "too many layers and heads") ||
       !check_view(c, tree, "tree") ||
       !c.need(cache->dtype == tree->dtype && cache->head_dim == tree->head_dim && cache->n_heads == tree->n_heads &&
@@ -1239,6 +1262,7 @@ int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n
   p.n = n_nodes;
   p.row_bytes = cache->head_dim * (q8 ? 1 : 2);
   p.srow_bytes = q8 ? cache->head_dim / 16 : 0;
+  p.by_heads = FastDiv(p.Hkv);
   return finish(launch_commit_tree(p, static_cast<cudaStream_t>(cuda_stream)), "commit launch");
 }
 

@@ -59,6 +59,16 @@ cudaError_t launch_cluster(Kern kern, dim3 grid, int threads, int cluster, size_
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// x / d as one multiplication, exact while x d < 2^32 (the callers check).
+struct FastDiv {
+  uint32_t mul = 0;
+  FastDiv() = default;
+  explicit FastDiv(int d) : mul(d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0) {}
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int x) const { return mul ? (int)__umulhi((uint32_t)x, mul) : x; }
+#endif
+};
+
 struct KvRows {              // K and V rows of one layer: a cache, or the drafted tree's own
   const uint8_t* k = nullptr;      // bf16 values, or int8 codes (then the scales are set)
   const uint8_t* v = nullptr;
@@ -80,6 +90,7 @@ struct TreeAttnParams {
   int64_t mask_seq;
   float c;                   // scale * log2(e)
   int B, n, Hkv, gq;
+  FastDiv by_gq;
   int S;                     // CTAs of a cluster: splits of the keys
   bool sorted;               // blocks take the sequences longest first
   int* status;               // the device's status word (bounded waits)
@@ -121,6 +132,7 @@ struct CommitParams {
   const int *lens, *path, *n_path;
   int* new_lens;             // may be lens itself
   int64_t path_seq;
+  FastDiv by_heads;
   int B, L, Hkv, n, row_bytes, srow_bytes;  // bytes of a row of k or v, and of its scales (0: none)
 };
 cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st);

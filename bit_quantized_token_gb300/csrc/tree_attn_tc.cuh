@@ -74,7 +74,8 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, vol
 // A bounded wait: past the limit the CTA's abort flag and the device's status
 // word are set and every wait of the CTA returns at once, so that all loops
 // run to their end (on data that does not matter) and no barrier is missed.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+// (A call: the kernel's code is fetched anew by every CTA, and short ones wait for it.)
+static __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   unsigned long long start = 0;
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -90,6 +91,9 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
       }
     }
   }
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return mbar_try_wait(bar, parity) || tc_wait_long(bar, parity, abort_flag, status);
 }
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int row, int head, int seq,
                                         uint64_t* bar) {
@@ -279,6 +283,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   };
   if (warp == 4 * G) {  // the ring's barriers are this warp's own: the first units are on their way at once
     if (lane == 0)
+#pragma unroll 1
       for (int i = 0; i < NST && i < n_units; ++i) request(i);
   } else if (warp == 4 * G + 1) {
     if (lane == 0) {
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         smask[i] = i < cnt ? p.mask[(int64_t)b * p.mask_seq + i] : 0;
 #pragma unroll 4
     for (int i = tid; i < N * (HD / 8); i += 128 * G) {
-      const int r = i / (HD / 8), ch = i % (HD / 8), node = (m0 + r) / p.gq, h = hkv * p.gq + (m0 + r) % p.gq;
+      const int r = i / (HD / 8), ch = i % (HD / 8), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
       const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
       uint8_t* dst = sq + (((ch / 8) * G + r / NB) * NQ * NB + r % NB) * 128 + 16 * ((ch & 7) ^ (r & 7));
       if constexpr (F32) {
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     // block g's tile t0 + t: buffers and barriers x = g (DB 1) or t & 1 (DB 2)
     auto scores = [&](int g, int t) {
       const int x = DB == 2 ? t & 1 : g;
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < H; ++u) {
         const int i = k_unit(t) + u, slot = i % NST;
         if (!tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status)) return false;
@@ -387,34 +392,35 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       return true;
     };
     bool ok = true;
-    for (int t = 0; t < DB && t < n_own && ok; ++t)
-      for (int g = 0; g < G && ok; ++g) ok = scores(g, t);
-    for (int t = 0; t < n_own && ok; ++t)
+#pragma unroll 1
+    for (int t = -DB; t < n_own && ok; ++t)
 #pragma unroll 1
       for (int g = 0; g < G && ok; ++g) {
-        const int x = DB == 2 ? t & 1 : g;
-        ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
+        if (t >= 0) {
+          const int x = DB == 2 ? t & 1 : g;
+          ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
+#pragma unroll 1
+          for (int u = 0; u < H; ++u) {
+            const int i = v_unit(t) + u, slot = i % NST;
+            ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v = ur + slot * C::kUnit;
+            // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
+            const uint64_t da = tc_desc(v, uo - v, 1024, 2);
+            const uint64_t dp = tc_desc(up + x * C::kPBlock, BK * 128, sbo_p, swp);
+            if (elect_lane()) {
 #pragma unroll
-        for (int u = 0; u < H; ++u) {
-          const int i = v_unit(t) + u, slot = i % NST;
-          ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t v = ur + slot * C::kUnit;
-          // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
-          const uint64_t da = tc_desc(v, uo - v, 1024, 2);
-          const uint64_t dp = tc_desc(up + x * C::kPBlock, BK * 128, sbo_p, swp);
-          if (elect_lane()) {
-#pragma unroll
-            for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
-              tc_mma(tm + DB * G * C::NS + (u * G + g) * C::NO, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
-                     dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
+              for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
+                tc_mma(tm + DB * G * C::NS + (u * G + g) * C::NO, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                       dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
+            }
+            __syncwarp();
+            if (g == G - 1) tc_commit(empty + slot);
           }
-          __syncwarp();
-          if (g == G - 1) tc_commit(empty + slot);
+          if (!ok) break;
+          tc_commit(o_done + g);
         }
-        if (!ok) break;
-        tc_commit(o_done + g);
         if (t + DB < n_own) ok = scores(g, t + DB);
       }
     if (!ok) {  // no MMA may outlive its operands
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     const float masked = p.c < 0.f ? INFINITY : -INFINITY;  // times c: -inf (c is not 0)
     if (p.tree.k)
       for (int r = key; r < NB; r += 128) {
-        const int node = (m0 + g * NB + r) / p.gq;
+        const int node = p.by_gq.div(m0 + g * NB + r);
         srow[g * NB + r] = node < cnt ? smask[node] & seen : 0;
       }
     group_sync(g);
@@ -659,17 +665,18 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   // ---- the cluster's S key ranges: rank k writes its share of the rows
   if (p.S > 1) cl.sync();
   float* so = reinterpret_cast<float*>(sm);
-  for (int r = tid; r < N; r += NT) {
+  const int rows = min(N, cnt * p.gq - m0);
+  for (int r = tid; r < rows; r += NT) {
     float2 ml[kMaxSplits];  // all loads in flight: a rank's answer takes long
 #pragma unroll
     for (int k = 0; k < kMaxSplits; ++k) ml[k] = k < p.S ? cl.map_shared_rank(sml, k)[r] : make_float2(kNone, 0.f);
-    float M = -INFINITY, L = 0.f;
+    float M = ml[0].x, L = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k) M = fmaxf(M, ml[k].x);
+    for (int k = 1; k < kMaxSplits; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
     for (int k = 0; k < kMaxSplits; ++k) {
-      ml[k].x = ml[k].x <= kNone ? 0.f : exp2f(ml[k].x - M);
-      L += ml[k].y * ml[k].x;
+      ml[k].x = ml[k].x <= kNone ? 0.f : ex2(ml[k].x - M);
+      L = fmaf(ml[k].y, ml[k].x, L);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
 #pragma unroll
@@ -677,10 +684,10 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       if (k < p.S) sw[k * N + r] = ml[k].x * inv;
   }
   __syncthreads();
-  const int rows = min(N, cnt * p.gq - m0), n4 = rows * HD / 4;
+  const int n4 = rows * HD / 4;
   const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
   for (int i = i0 + tid; i < i1; i += NT) {
-    const int r = i / (HD / 4), node = (m0 + r) / p.gq, h = hkv * p.gq + (m0 + r) % p.gq;
+    const int r = i / (HD / 4), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int k0 = 0; k0 < p.S; k0 += 8) {
