@@ -220,6 +220,63 @@ __device__ __forceinline__ int nth_longest(const int* lens, int B, int z, int la
   return ha ? __ffs(ha) - 1 : 31 + __ffs(hc);
 }
 
+// The cluster's S key ranges joined: rank k writes its share of the rows. so: a
+// rank's unnormalised O [N][HD], sml its (reference, sum) per row.
+template <int HD, bool F32, int N, int NT>
+__device__ __forceinline__ void join_splits(const TreeAttnParams& p, float* so, float2* sml, float* sw, int rank, int b,
+                                            int hkv, int m0, int rows) {
+  constexpr float kNone = -3e38f;
+  const int tid = threadIdx.x;
+  cg::cluster_group cl = cg::this_cluster();
+  __syncthreads();
+  // ---- the cluster's S key ranges: rank k writes its share of the rows
+  if (p.S > 1) cl.sync();
+  for (int r = tid; r < rows; r += NT) {
+    float2 ml[kMaxSplits];  // all loads in flight: a rank's answer takes long
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) ml[k] = k < p.S ? cl.map_shared_rank(sml, k)[r] : make_float2(kNone, 0.f);
+    float M = ml[0].x, L = 0.f;
+#pragma unroll
+    for (int k = 1; k < kMaxSplits; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) {
+      ml[k].x = ml[k].x <= kNone ? 0.f : ex2(ml[k].x - M);
+      L = fmaf(ml[k].y, ml[k].x, L);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+      if (k < p.S) sw[k * N + r] = ml[k].x * inv;
+  }
+  __syncthreads();
+  const int n4 = rows * HD / 4;
+  const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
+  for (int i = i0 + tid; i < i1; i += NT) {
+    const int r = i / (HD / 4), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < p.S; k0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < p.S) x[k] = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k0 + k))[i];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < p.S) {
+          const float f = sw[(k0 + k) * N + r];
+          a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y), a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
+        }
+    }
+    const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % (HD / 4));
+    if constexpr (F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = a;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off) =
+          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+  if (p.S > 1) cl.sync();  // a CTA's shared memory lives until every rank has read it
+}
+
 template <int HD, bool F32, int NB, int G>
 __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB, G>::two ? 2 : 1) tree_attn_tc_kernel(
     const __grid_constant__ TreeAttnTcParams tp) {
@@ -660,56 +717,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     tc_fence_before();
   }
   __syncwarp();
-  cg::cluster_group cl = cg::this_cluster();
-  __syncthreads();
-  // ---- the cluster's S key ranges: rank k writes its share of the rows
-  if (p.S > 1) cl.sync();
-  float* so = reinterpret_cast<float*>(sm);
-  const int rows = min(N, cnt * p.gq - m0);
-  for (int r = tid; r < rows; r += NT) {
-    float2 ml[kMaxSplits];  // all loads in flight: a rank's answer takes long
-#pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k) ml[k] = k < p.S ? cl.map_shared_rank(sml, k)[r] : make_float2(kNone, 0.f);
-    float M = ml[0].x, L = 0.f;
-#pragma unroll
-    for (int k = 1; k < kMaxSplits; ++k) M = fmaxf(M, ml[k].x);
-#pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k) {
-      ml[k].x = ml[k].x <= kNone ? 0.f : ex2(ml[k].x - M);
-      L = fmaf(ml[k].y, ml[k].x, L);
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
-#pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k)
-      if (k < p.S) sw[k * N + r] = ml[k].x * inv;
-  }
-  __syncthreads();
-  const int n4 = rows * HD / 4;
-  const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
-  for (int i = i0 + tid; i < i1; i += NT) {
-    const int r = i / (HD / 4), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int k0 = 0; k0 < p.S; k0 += 8) {
-      float4 x[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < p.S) x[k] = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k0 + k))[i];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < p.S) {
-          const float f = sw[(k0 + k) * N + r];
-          a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y), a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
-        }
-    }
-    const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % (HD / 4));
-    if constexpr (F32)
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = a;
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off) =
-          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-  }
-  if (p.S > 1) cl.sync();  // a CTA's shared memory lives until every rank has read it
+  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sw, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
   // Freed last: no two CTAs that hold and that wait for tensor memory share an
   // SM (kernels whose columns exceed half take all of its shared memory), so a
   // CTA that holds it while its cluster gathers cannot keep a peer waiting.
@@ -737,20 +745,31 @@ inline EncodeTiled tensor_map_encoder() {
   return fn;
 }
 
-// The map of one K or V tensor [seq][head][row][dim]; false where TMA cannot address it.
-inline bool encode_rows(CUtensorMap* map, const uint8_t* base, const KvRows& r, int B, int heads, int hd) {
+// The map of one K or V tensor [seq][head][row][dim] of bf16 or int8; false where TMA cannot address it.
+template <int HD, bool Q8>
+bool encode_rows(CUtensorMap* map, const uint8_t* base, const KvRows& r, int B, int heads) {
   const EncodeTiled enc = tensor_map_encoder();
   if (!enc || r.rows < 1) return false;
-  const int64_t row = r.rows > 1 ? r.row : hd;
+  const int64_t row = r.rows > 1 ? r.row : HD;
   const int64_t head = heads > 1 ? r.head : row * r.rows, seq = B > 1 ? r.seq : head * heads;
-  const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)r.rows, (cuuint64_t)heads, (cuuint64_t)B};
-  const cuuint64_t strides[3] = {(cuuint64_t)row * 2, (cuuint64_t)head * 2, (cuuint64_t)seq * 2};
+  const cuuint64_t dims[4] = {(cuuint64_t)HD, (cuuint64_t)r.rows, (cuuint64_t)heads, (cuuint64_t)B};
+  const cuuint64_t size = Q8 ? 1 : 2, strides[3] = {row * size, head * size, seq * size};
   for (const cuuint64_t s : strides)
     if (s == 0 || s % 16 || s >= (1ull << 40)) return false;
-  const cuuint32_t box[4] = {64, 128, 1, 1}, step[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint32_t box[4] = {Q8 ? HD : 64, 128, 1, 1}, step[4] = {1, 1, 1, 1};
+  return enc(map, Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             Q8 && HD == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <int HD, bool Q8>
+bool encode_all(TreeAttnTcParams& tp) {
+  const TreeAttnParams& p = tp.p;
+  if (p.cache.rows > 0 && !(encode_rows<HD, Q8>(&tp.ck, p.cache.k, p.cache, p.B, p.Hkv) &&
+                            encode_rows<HD, Q8>(&tp.cv, p.cache.v, p.cache, p.B, p.Hkv)))
+    return false;
+  return p.tree.k == nullptr || (encode_rows<HD, Q8>(&tp.tk, p.tree.k, p.tree, p.B, p.Hkv) &&
+                                 encode_rows<HD, Q8>(&tp.tv, p.tree.v, p.tree, p.B, p.Hkv));
 }
 
 template <int HD, bool F32, int NB, int G>
@@ -782,13 +801,7 @@ template <int HD>
 bool launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStream_t st, cudaError_t* e) {
   TreeAttnTcParams tp;
   tp.p = p;
-  const bool cache = p.cache.rows > 0, tree = p.tree.k != nullptr;
-  if (cache && !(encode_rows(&tp.ck, p.cache.k, p.cache, p.B, p.Hkv, HD) &&
-                 encode_rows(&tp.cv, p.cache.v, p.cache, p.B, p.Hkv, HD)))
-    return false;
-  if (tree && !(encode_rows(&tp.tk, p.tree.k, p.tree, p.B, p.Hkv, HD) &&
-                encode_rows(&tp.tv, p.tree.v, p.tree, p.B, p.Hkv, HD)))
-    return false;
+  if (!encode_all<HD, false>(tp)) return false;
   // Rows of a CTA: as many as there are (K and V are read once for them), in two
   // blocks once there are 32 (one block's softmax overlaps the other's MMAs); but
   // fewer while the clusters, split eight ways, would leave SMs without a CTA
