@@ -1029,7 +1029,11 @@ bool check_view(Call& c, const llm_kv_view* v, const char* name) {
   if (!c.need(v->seq_stride >= 0 && v->layer_stride >= 0 && v->head_stride >= 0 && v->row_stride >= 0 &&
                   v->seq_stride % m == 0 && v->layer_stride % m == 0 && v->head_stride % m == 0 &&
                   v->row_stride % m == 0,
-              LLM_ERR_INVALID_ARG, "%s: a stride is negative or no multiple of 16 bytes", name))
+              LLM_ERR_INVALID_ARG, "%s: a stride is negative or no multiple of 16 bytes", name) ||
+      !c.need(v->rows <= 1 || v->row_stride > 0, LLM_ERR_INVALID_ARG, "%s: the row stride is 0", name) ||
+      !c.need(v->seq_stride < (1ll << 38) && v->layer_stride < (1ll << 38) && v->head_stride < (1ll << 38) &&
+                  v->row_stride < (1ll << 38),
+              LLM_ERR_UNSUPPORTED, "%s: a stride of 2^38 elements or more", name))
     return false;
   if (q8 && !c.need(v->scale_seq_stride >= 0 && v->scale_layer_stride >= 0 && v->scale_head_stride >= 0 &&
                     v->scale_row_stride >= 0 && v->scale_seq_stride % sm == 0 && v->scale_layer_stride % sm == 0 &&

@@ -1,5 +1,5 @@
 // Tree decoding: parameters and launchers of the operators that score a tree
-// of drafted tokens (tree_attn.cuh), turn logits into token probabilities,
+// of drafted tokens (tree_attn.cuh, tree_attn_q8.cuh), turn logits into token probabilities,
 // verify the drafts and commit the kept ones to the K/V cache (tree.cu).
 // Every kernel here is stateless: work split over several CTAs is joined
 // inside a thread block cluster through distributed shared memory, so no call
@@ -98,8 +98,8 @@ struct TreeAttnParams {
 
 // f32: q and out are fp32 (else bf16); q8: int8 rows. n_sm: SMs of the device.
 cudaError_t launch_tree_attn(const TreeAttnParams& p, int hd, bool f32, bool q8, int n_sm, cudaStream_t st);
-cudaError_t launch_tree_attn_64(TreeAttnParams p, bool f32, bool q8, int n_sm, cudaStream_t st);
-cudaError_t launch_tree_attn_128(TreeAttnParams p, bool f32, bool q8, int n_sm, cudaStream_t st);
+cudaError_t launch_tree_attn_64(const TreeAttnParams& p, bool f32, bool q8, int n_sm, cudaStream_t st);
+cudaError_t launch_tree_attn_128(const TreeAttnParams& p, bool f32, bool q8, int n_sm, cudaStream_t st);
 
 struct TokenProbsParams {
   const float* logits;

@@ -1,12 +1,36 @@
-// Attention of a tree of drafted tokens over the K/V cache.
+// Attention of a tree of drafted tokens over bf16 K/V rows.
 //
 // A sequence's n nodes (n <= 64) share its cached prefix; node i also sees the
 // tree rows whose bits its mask sets. The gq query heads of a kv head and the
 // n nodes form M = n gq query rows against the same keys (row r: node r / gq,
 // head r % gq), so one pass over K and V serves all of them:
 //   o_r = sum_j 2^(c s_rj - m_r) v_j / sum_j 2^(c s_rj - m_r),  s_rj = q_r . k_j,
-// with c = scale log2(e) and the running maximum m_r and sum in fp32.
+// with c = scale log2(e), the references m_r and the sums in fp32.
+//
+// The products run transposed, so that the few query rows are the narrow side:
+//   S^T [128 keys x N rows] = K_tile Q^T     (A = the K tile as TMA lays it down, K-major)
+//   O^T [dims x N rows]    += V_tile^T P^T   (A = the V tile, read MN-major; B = P, [key][row])
+// A thread of a softmax warp is one key: it reads its scores from tensor
+// memory, turns them into probabilities and writes them as a row of P, so no
+// exchange between threads is needed. Instead of the running maximum, a
+// reference within 2^60 of it does: it starts as the first key's scores and is
+// renewed (and O rescaled) only when a score passes it by more than 2^60; bf16
+// and fp32 keep their relative precision over that range.
+// A tile is read as units of 128 keys x 64 dims (16 KB, one TMA box, 128-byte
+// swizzle): K and V units stream through one ring. Of each P V product's 128
+// rows the upper 64 read ones instead of V, so lanes 64.. hold the sums of P.
+// fp32 operands are parts in bf16 (24 bits in three, 16 in two): the parts of Q
+// and of P are columns of their own in one product each, so that A, whose fetch
+// from shared memory (4 KB, 32 cycles) bounds these narrow products, is fetched
+// once; the sums over the parts are formed on the way out.
+// Warp roles: 4 softmax warps per block of NB rows (G blocks share the units),
+// one TMA warp, one warp that issues every MMA. A block's next scores are
+// computed right after its P V, while the other block (or the other CTA on the
+// SM, where shared memory lets two fit) is in its softmax; a lone block has two
+// buffers of S and P and is a tile ahead with its scores.
 #pragma once
+#include <cuda.h>
+
 #include <cooperative_groups.h>
 
 #include "attn_mma.cuh"
@@ -15,486 +39,246 @@
 namespace llmq {
 namespace cg = cooperative_groups;
 
-// 16-byte asynchronous copy; zeros where !ok (nothing is read then)
-__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
-}
-
-// Four int8 codes (a word) as two bf16 pairs, exactly: 128 + (c & 127) and
-// 128 + (c & 128) are bf16 integers below 512 of the same step, and their
-// difference is c.
-__device__ __forceinline__ uint2 i8x4_to_bf16(uint32_t w) {
-  uint32_t r[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t b = __byte_perm(w, 0u, h ? 0x4342 : 0x4140);  // bytes 2h, 2h+1 in the low halves' bytes
-    const uint32_t a = (b & 0x007F007Fu) | 0x43004300u, s = (b & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&s));
-    r[h] = *reinterpret_cast<const uint32_t*>(&d);
-  }
-  return make_uint2(r[0], r[1]);
-}
-
-// x as a sum of bf16 parts: part i is the rounding of what the earlier ones
-// left, so two parts carry 16 bits of the mantissa and three all 24.
-template <int N>
-__device__ __forceinline__ void split_bf16(float x, float (&part)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    part[i] = __bfloat162float(__float2bfloat16_rn(x));
-    x -= part[i];
-  }
-}
-
-// The mma.sync form: a CTA owns MT = 16 WM rows of a (sequence, kv head) and a
-// range of key tiles; warp (wm, wk) scores rows 16 wm .. +15 against keys
-// KW wk .. of every tile of BK keys. Tiles stream through a ring of cp.async
-// stages (three tiles of 32 KB in flight keep HBM busy with two CTAs on an
-// SM); every warp keeps its own running softmax state, so a tile costs one CTA
-// barrier, and the WK states, then the cluster's S ranges of keys, merge at
-// the end. fp32 queries enter as three bf16 parts (24 bits), their
-// probabilities too; for bf16 queries, which are exact, the probabilities
-// enter as two parts (relative error 2^-17, below the output's own rounding).
-// int8 rows are widened to bf16 (exact) once per tile for all warps; a key
-// group's scale multiplies its partial scores, a value group's scale the
-// probabilities of that group's products.
-template <int HD, bool F32, bool KV8, int WM, int WK>
-struct TreeAttn {
-  static constexpr int BK = HD == 64 ? 128 : 64, KW = BK / WK, NT = 32 * WM * WK, MT = 16 * WM;
-  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2, NG = HD / 32, NST = 3;
-  static constexpr int kTile = BK * HD;                               // elements of a K or V tile
-  static constexpr int kStage = KV8 ? 2 * kTile + 4 * BK * NG : 4 * kTile;  // bytes
-  static constexpr int kWork = KV8 ? 4 * kTile : 0;                   // widened K and V
-  static constexpr int kRing = NST * kStage + kWork;
-  static constexpr int kMerge = WK * MT * HD * 4;                     // over the ring, after the last tile
-  static constexpr int kQ = NQ * MT * HD * 2;
-  static constexpr int kOffQ = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kOffMl = kOffQ + kQ;                           // [WK][MT] (max, sum)
-  static constexpr int kOffW = kOffMl + WK * MT * 8;                  // [16][MT] merge weights
-  static constexpr int kOffMask = kOffW + 16 * MT * 4;                // [64] masks
-  static constexpr int kOffNf = kOffMask + 8 * kTreeMaxNodes;         // [3][64][HD / 32] non-finite values
-  static constexpr int kSmem = kOffNf + 3 * kTreeMaxNodes * NG * 4 + 16;
+struct TreeAttnTcParams {
+  CUtensorMap ck, cv, tk, tv;  // cache and tree rows: [seq][head][row][dim], boxes of 128 rows x 64 dims
+  TreeAttnParams p;
+  // 0 where a stride is 0 (all sequences, or heads, share the rows), else 1: TMA takes no stride of 0
+  int c_seq, c_head, t_seq, t_head;
 };
 
-template <int HD, bool F32, bool KV8, int WM, int WK>
-__global__ void __launch_bounds__(32 * WM * WK) tree_attn_kernel(const __grid_constant__ TreeAttnParams p) {
-  using C = TreeAttn<HD, F32, KV8, WM, WK>;
-  constexpr int BK = C::BK, KW = C::KW, NT = C::NT, MT = C::MT, NQ = C::NQ, NP = C::NP, NG = C::NG, NST = C::NST;
-  constexpr int CH = HD / 8;  // 16-byte chunks of a bf16 row
-  extern __shared__ __align__(128) uint8_t sm[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wm = warp / WK, wk = warp % WK;
-  const int b = blockIdx.z, g = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * MT, rank = blockIdx.x;
-  pdl_wait();
-  pdl_trigger();
-  const int cnt = p.counts ? min(max(p.counts[b], 0), p.n) : p.n;
-  if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
-  const int len = min(max(p.lens[b], 0), p.cache.rows);
-  const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
-  const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S);
-  uint16_t* sq = reinterpret_cast<uint16_t*>(sm + C::kOffQ);
-  float2* sml = reinterpret_cast<float2*>(sm + C::kOffMl);
-  float* sw = reinterpret_cast<float*>(sm + C::kOffW);
-  uint64_t* smask = reinterpret_cast<uint64_t*>(sm + C::kOffMask);
-  uint32_t* snf = reinterpret_cast<uint32_t*>(sm + C::kOffNf);
-  int* s_any = reinterpret_cast<int*>(snf + 3 * kTreeMaxNodes * NG);
+constexpr int kMaxSplits = 16;  // CTAs of a cluster
 
-  const int64_t cb = (int64_t)b * p.cache.seq + (int64_t)g * p.cache.head;
-  const int64_t tb = (int64_t)b * p.tree.seq + (int64_t)g * p.tree.head;
-  const int64_t csb = (int64_t)b * p.cache.sseq + (int64_t)g * p.cache.shead;
-  const int64_t tsb = (int64_t)b * p.tree.sseq + (int64_t)g * p.tree.shead;
+template <int HD, bool F32, int NB, int G>
+struct TreeTc {
+  static constexpr int N = NB * G, BK = 128, H = HD / 64;
+  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : (N > 64 ? 1 : 2);  // parts of the queries, of P
+  static constexpr int NS = NQ * NB, NO = NP * NB;                        // columns of a block's S, of its O (64 dims)
+  static constexpr int NT = 32 * (4 * G + 2);
+  static constexpr int kUnit = BK * 128;                                  // bytes: 64 dims of a K or V tile
+  static constexpr int kRowP = NO >= 48 ? 128 : 2 * NO;                   // bytes of a key's row of a P atom (64 columns)
+  static constexpr int kPBlock = BK * kRowP * ((NO + 63) / 64);           // bytes of a block's P
+  static constexpr int kQ = NQ * N * HD * 2, kOnes = 2048;
+  static constexpr int kOffRow = 1024;                                   // of the small arrays: [N] row masks
+  static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4) + 3 * kTreeMaxNodes * (HD / 32) * 4;
+  static constexpr int kRest = kQ + kOnes + kSmall + 1024;
+  static constexpr int kOut = N * HD * 4;                                // fp32 results, over the ring at the end
+  static constexpr int kLimit = 232448, kHalf = 115712;                  // shared memory of a CTA alone, of two on an SM
+  // a tile's K and V units and, of 64 dims, the next K unit must fit
+  static constexpr int kLeast = H == 1 ? 3 : 4, kMin = kLeast > kOut / kUnit ? kLeast : kOut / kUnit;
+  // One block of rows: S and P twice, so that the next scores are ready when a
+  // softmax ends (where two CTAs then still fit on an SM).
+  static constexpr int DB = G == 1 && kRest + 2 * kPBlock + kMin * kUnit <= kHalf ? 2 : 1;
+  static constexpr int kFixed = kRest + G * DB * kPBlock;
+  static constexpr bool two = kFixed + kMin * kUnit <= kHalf;
+  static constexpr int fit = ((two ? kHalf : kLimit) - kFixed) / kUnit;
+  static constexpr int NST = fit < 12 ? fit : 12;
+  static constexpr int kSmem = NST * kUnit + kFixed;
+  static_assert(NST >= kMin, "shared memory");
+  static constexpr int kUsed = G * (DB * NS + H * NO);                   // S, and O of every 64 dims
+  static_assert(kUsed <= 512, "tensor memory");
+  static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+};
 
-  uint64_t seen = 0;  // tree rows that some node of the sequence sees: no other is read
-  if (p.tree.k) {
-    for (int i = tid; i < kTreeMaxNodes; i += NT) smask[i] = i < cnt ? p.mask[(int64_t)b * p.mask_seq + i] : 0;
-    if (tid == 0) *s_any = 0;
-    __syncthreads();
-    const uint64_t a = smask[lane] | smask[lane + 32];
-    seen = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(a >> 32)) << 32) |
-           __reduce_or_sync(0xffffffffu, (uint32_t)a);
-    if (cnt < 64) seen &= (1ull << cnt) - 1;
+// A warp's bounded wait with one answer for all lanes.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status);
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, status));
+}
+// A bounded wait: past the limit the CTA's abort flag and the device's status
+// word are set and every wait of the CTA returns at once, so that all loops
+// run to their end (on data that does not matter) and no barrier is missed.
+// (A call: the kernel's code is fetched anew by every CTA, and short ones wait for it.)
+static __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  unsigned long long start = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 63) {
+      if (*abort_flag) return false;
+      const unsigned long long t = globaltimer();
+      if (start == 0) {
+        start = t;
+      } else if (t - start > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(status, ST_TIMEOUT);
+        return false;
+      }
+    }
   }
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return mbar_try_wait(bar, parity) || tc_wait_long(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int row, int head, int seq,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(row), "r"(head), "r"(seq), "r"(smem_u32(bar))
+      : "memory");
+}
+// The MMA warp runs converged, so that addresses stay in uniform registers, and
+// one elected lane (always the same of a full warp) issues.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      :
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  if (elect_lane())
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// Shared memory matrix descriptor: start, leading and stride byte offsets in
+// 16-byte units; swizzle 2: 128 B, 4: 64 B, 6: 32 B.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t start, uint32_t lbo, uint32_t sbo, uint64_t swizzle) {
+  return (uint64_t)((start & 0x3FFFF) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
+         (1ull << 46) | (swizzle << 61);
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// W columns of this warp's 32 lanes, one lane per thread
+template <int W>
+__device__ __forceinline__ void tc_ld(float (&v)[W], uint32_t addr) {
+  static_assert(W == 16 || W == 32, "columns");
+  if constexpr (W == 16)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(addr));
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+                 : "r"(addr));
+}
+// Waits for the loads; the values pass through, so that no use of them moves ahead of the wait.
+template <int W>
+__device__ __forceinline__ void tc_wait_ld(float (&v)[W]) {
+  if constexpr (W == 16)
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]) : : "memory");
+  else
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]) : : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// a, b as NP bf16 pairs whose sums carry 8 NP bits
+template <int NP>
+__device__ __forceinline__ void split_pack(float a, float b, uint32_t (&part)[NP]) {
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    part[k] = pack_bf16x2(a, b);
+    if (k + 1 < NP) {
+      a -= __uint_as_float(part[k] << 16);
+      b -= __uint_as_float(part[k] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// the 128 threads of softmax group g (named barriers 1..G)
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory"); }
+__device__ __forceinline__ bool group_any(int g, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(g + 1)
+      : "memory");
+  return r != 0;
+}
 
-  auto stage = [&](int t) {
-    uint8_t* base = sm + (t % NST) * C::kStage;
-    const bool tree = t >= n_pre;
-    const KvRows& r = tree ? p.tree : p.cache;
-    const int row0 = tree ? 0 : t * BK;
-    const int64_t off = tree ? tb : cb, soff = tree ? tsb : csb;
-    auto ok = [&](int row) { return tree ? row < kTreeMaxNodes && ((seen >> (row & 63)) & 1) : row0 + row < len; };
-    if constexpr (KV8) {
-      constexpr int C8 = HD / 16;
-      for (int i = tid; i < 2 * BK * C8; i += NT) {
-        const int kv = i >= BK * C8, j = i - kv * BK * C8, row = j / C8, ch = j % C8;
-        const bool in = ok(row);
-        const uint8_t* src = (kv ? r.v : r.k) + (in ? off + (int64_t)(row0 + row) * r.row + 16 * ch : 0);
-        cp_async16_or_zero(base + kv * C::kTile + row * HD + 16 * (ch ^ (row & (C8 - 1))), src, in);
-      }
-      uint16_t* sc = reinterpret_cast<uint16_t*>(base + 2 * C::kTile);  // [2][BK][NG]
-      for (int i = tid; i < 2 * BK; i += NT) {
-        const int kv = i >= BK, row = i - kv * BK;
-        uint16_t* dst = sc + i * NG;
-        if (ok(row)) cp_async_small<2 * NG>(dst, (kv ? r.vs : r.ks) + soff + (int64_t)(row0 + row) * r.srow);
-        else
-#pragma unroll
-          for (int e = 0; e < NG; ++e) dst[e] = 0;
-      }
-    } else {
-      for (int i = tid; i < 2 * BK * CH; i += NT) {
-        const int kv = i >= BK * CH, j = i - kv * BK * CH, row = j / CH, ch = j % CH;
-        const bool in = ok(row);
-        const uint8_t* src = (kv ? r.v : r.k) + (in ? 2 * (off + (int64_t)(row0 + row) * r.row + 8 * ch) : 0);
-        cp_async16_or_zero(base + 2 * (kv * C::kTile + tile_off<HD, HD, true>(row, ch)), src, in);
-      }
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < NST - 1; ++i) {
-    if (t0 + i < t1) stage(t0 + i);
-    cp_async_commit();
+// The sequence with the z-th longest cache of at most 64 (every warp finds it by
+// itself): blocks start in grid order, and starting the long sequences first
+// leaves the short ones to fill the end.
+__device__ __forceinline__ int nth_longest(const int* lens, int B, int z, int lane) {
+  const int a = lane < B ? lens[lane] : -1, c = lane + 32 < B ? lens[lane + 32] : -1;
+  int ra = 0, rc = 0;  // sequences ahead of this lane's two
+  for (int j = 0; j < min(B, 32); ++j) {
+    const int o = __shfl_sync(0xffffffffu, a, j);
+    ra += o > a || (o == a && j < lane);
+    rc += o >= c;
   }
-  // the query rows as bf16 parts, in the tiles' permuted chunks
-  for (int i = tid; i < MT * CH; i += NT) {
-    const int r = i / CH, ch = i % CH, node = (m0 + r) / p.gq, h = g * p.gq + (m0 + r) % p.gq;
-    const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
-    const int dst = tile_off<HD, HD, true>(r, ch);
-    if constexpr (F32) {
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (node < cnt) {
-        const float4 lo = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off);
-        const float4 hi = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off + 4);
-        x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
-      }
-      float part[8][3];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) split_bf16<3>(x[e], part[e]);
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint4*>(sq + k * MT * HD + dst) =
-            make_uint4(pack_bf16x2(part[0][k], part[1][k]), pack_bf16x2(part[2][k], part[3][k]),
-                       pack_bf16x2(part[4][k], part[5][k]), pack_bf16x2(part[6][k], part[7][k]));
-    } else {
-      *reinterpret_cast<uint4*>(sq + dst) =
-          node < cnt ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off)
-                     : make_uint4(0u, 0u, 0u, 0u);
-    }
+  for (int j = 32; j < B; ++j) {
+    const int o = __shfl_sync(0xffffffffu, c, j - 32);
+    ra += o > a;
+    rc += o > c || (o == c && j < lane + 32);
   }
-  const int r8 = lane & 7, mi = lane >> 3, gr = lane >> 2, tq = lane & 3;
-  const int node0 = (m0 + 16 * wm + gr) / p.gq, node1 = (m0 + 16 * wm + gr + 8) / p.gq;
-  float o[HD / 8][4], mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < HD / 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  const unsigned ha = __ballot_sync(0xffffffffu, lane < B && ra == z);
+  const unsigned hc = __ballot_sync(0xffffffffu, lane + 32 < B && rc == z);
+  return ha ? __ffs(ha) - 1 : 31 + __ffs(hc);
+}
 
-  for (int t = t0; t < t1; ++t) {
-    cp_async_wait_group<NST - 2>();
-    __syncthreads();  // the tile has landed for every thread, and its predecessor's slot is free
-    if (t + NST - 1 < t1) stage(t + NST - 1);
-    cp_async_commit();
-    const bool tree = t >= n_pre;
-    uint8_t* base = sm + (t % NST) * C::kStage;
-    uint16_t* kt = reinterpret_cast<uint16_t*>(base);
-    uint16_t* vt = kt + C::kTile;
-    const uint16_t* sc = reinterpret_cast<const uint16_t*>(base + 2 * C::kTile);
-    if constexpr (KV8) {
-      constexpr int C8 = HD / 16;
-      kt = reinterpret_cast<uint16_t*>(sm + NST * C::kStage);
-      vt = kt + C::kTile;
-      for (int i = tid; i < 2 * BK * C8; i += NT) {
-        const int kv = i >= BK * C8, j = i - kv * BK * C8, row = j / C8, ch = j % C8;
-        const uint4 w = *reinterpret_cast<const uint4*>(base + kv * C::kTile + row * HD + 16 * (ch ^ (row & (C8 - 1))));
-        const uint2 a = i8x4_to_bf16(w.x), c = i8x4_to_bf16(w.y), d = i8x4_to_bf16(w.z), e = i8x4_to_bf16(w.w);
-        *reinterpret_cast<uint4*>(kt + kv * C::kTile + tile_off<HD, HD, true>(row, 2 * ch)) = make_uint4(a.x, a.y, c.x, c.y);
-        *reinterpret_cast<uint4*>(kt + kv * C::kTile + tile_off<HD, HD, true>(row, 2 * ch + 1)) =
-            make_uint4(d.x, d.y, e.x, e.y);
-      }
-      __syncthreads();
-    } else if (tree) {
-      // a value that is not finite must not reach the nodes that do not see
-      // it (0 * inf is NaN): it becomes 0 here and is added to the rows that
-      // do see it at the end
-      for (int i = tid; i < 3 * kTreeMaxNodes * NG; i += NT) snf[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < kTreeMaxNodes * HD; i += NT) {
-        const int row = i / HD, d = i % HD;
-        uint16_t* x = vt + tile_off<HD, HD, true>(row, d >> 3) + (d & 7);
-        if ((*x & 0x7F80u) == 0x7F80u) {
-          const int kind = (*x & 0x7Fu) ? 2 : *x >> 15;
-          atomicOr(snf + (kind * kTreeMaxNodes + row) * NG + (d >> 5), 1u << (d & 31));
-          *x = 0;
-          *s_any = 1;
-        }
-      }
-      __syncthreads();
-    }
-    const int k0 = KW * wk;
-    float s[KW / 8][4];
-#pragma unroll
-    for (int j = 0; j < KW / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-    const int lim = tree ? kTreeMaxNodes : len - t * BK;  // rows of the tile that exist
-    if (k0 < lim) {
-      if constexpr (KV8) {
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) {
-          float sg[KW / 8][4];
-#pragma unroll
-          for (int j = 0; j < KW / 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sg[j][e] = 0.f;
-#pragma unroll
-          for (int ks = 2 * gg; ks < 2 * gg + 2; ++ks) {
-            uint32_t qf[NQ][4];
-#pragma unroll
-            for (int k = 0; k < NQ; ++k)
-              ldsm_x4(qf[k], sq + k * MT * HD + tile_off<HD, HD, true>(16 * wm + 8 * (mi & 1) + r8, 2 * ks + (mi >> 1)));
-#pragma unroll
-            for (int j = 0; j < KW / 8; j += 2) {
-              uint32_t kb[4];
-              ldsm_x4(kb, kt + tile_off<HD, HD, true>(k0 + 8 * j + 8 * (mi >> 1) + r8, 2 * ks + (mi & 1)));
-#pragma unroll
-              for (int k = NQ - 1; k >= 0; --k) {
-                mma_bf16_16816(sg[j], qf[k], kb[0], kb[1]);
-                mma_bf16_16816(sg[j + 1], qf[k], kb[2], kb[3]);
-              }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < KW / 8; ++j) {
-            const float s0 = __half2float(__ushort_as_half(sc[(k0 + 8 * j + 2 * tq) * NG + gg]));
-            const float s1 = __half2float(__ushort_as_half(sc[(k0 + 8 * j + 2 * tq + 1) * NG + gg]));
-            s[j][0] = fmaf(sg[j][0], s0, s[j][0]);
-            s[j][1] = fmaf(sg[j][1], s1, s[j][1]);
-            s[j][2] = fmaf(sg[j][2], s0, s[j][2]);
-            s[j][3] = fmaf(sg[j][3], s1, s[j][3]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks) {
-          uint32_t qf[NQ][4];
-#pragma unroll
-          for (int k = 0; k < NQ; ++k)
-            ldsm_x4(qf[k], sq + k * MT * HD + tile_off<HD, HD, true>(16 * wm + 8 * (mi & 1) + r8, 2 * ks + (mi >> 1)));
-#pragma unroll
-          for (int j = 0; j < KW / 8; j += 2) {
-            uint32_t kb[4];
-            ldsm_x4(kb, kt + tile_off<HD, HD, true>(k0 + 8 * j + 8 * (mi >> 1) + r8, 2 * ks + (mi & 1)));
-#pragma unroll
-            for (int k = NQ - 1; k >= 0; --k) {
-              mma_bf16_16816(s[j], qf[k], kb[0], kb[1]);
-              mma_bf16_16816(s[j + 1], qf[k], kb[2], kb[3]);
-            }
-          }
-        }
-      }
-      const bool whole = !tree && k0 + KW <= lim;
-      const uint64_t v0 = tree ? (node0 < cnt ? smask[node0] : 0) & seen : 0;
-      const uint64_t v1 = tree ? (node1 < cnt ? smask[node1] : 0) & seen : 0;
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < KW / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[j][e] * p.c;
-          if (!whole) {
-            const int key = k0 + 8 * j + 2 * tq + (e & 1);
-            const bool in = tree ? key < kTreeMaxNodes && (((e < 2 ? v0 : v1) >> (key & 63)) & 1) : key < lim;
-            x = in ? x : -INFINITY;
-          }
-          s[j][e] = x;
-          mx[e >> 1] = fmaxf(mx[e >> 1], x);
-        }
-      float mnew[2], f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        mnew[h] = fmaxf(mrun[h], mx[h]);
-        f[h] = mrun[h] == mnew[h] ? 1.f : exp2f(mrun[h] - mnew[h]);
-      }
-      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          o[i][0] *= f[0];
-          o[i][1] *= f[0];
-          o[i][2] *= f[1];
-          o[i][3] *= f[1];
-        }
-        lrun[0] *= f[0];
-        lrun[1] *= f[1];
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mrun[h] = mnew[h];
-        if (mnew[h] == -INFINITY) mnew[h] = 0.f;  // nothing seen yet: every 2^-inf below is 0
-      }
-#pragma unroll
-      for (int j = 0; j < KW / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[j][e] = exp2f(s[j][e] - mnew[e >> 1]);
-          lrun[e >> 1] += s[j][e];
-        }
-#pragma unroll
-      for (int c = 0; c < KW / 16; ++c) {
-        const int kr = k0 + 16 * c;
-        if constexpr (KV8) {
-          const uint16_t* vsc = sc + BK * NG;
-#pragma unroll
-          for (int gg = 0; gg < NG; ++gg) {
-            float pp[8][NP];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {  // i: n-tile half (i / 4) and element
-              const int key = kr + 8 * (i >> 2) + 2 * tq + (i & 1);
-              const float w = __half2float(__ushort_as_half(vsc[key * NG + gg]));
-              const float x = s[2 * c + (i >> 2)][i & 3];
-              split_bf16<NP>(x == 0.f ? 0.f : x * w, pp[i]);  // a masked row's scale may be anything
-            }
-            uint32_t pa[NP][4];
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-              pa[k][0] = pack_bf16x2(pp[0][k], pp[1][k]);
-              pa[k][1] = pack_bf16x2(pp[2][k], pp[3][k]);
-              pa[k][2] = pack_bf16x2(pp[4][k], pp[5][k]);
-              pa[k][3] = pack_bf16x2(pp[6][k], pp[7][k]);
-            }
-#pragma unroll
-            for (int nt = 4 * gg; nt < 4 * gg + 4; nt += 2) {
-              uint32_t vb[4];
-              ldsm_x4_t(vb, vt + tile_off<HD, HD, true>(kr + 8 * (mi & 1) + r8, nt + (mi >> 1)));
-#pragma unroll
-              for (int k = NP - 1; k >= 0; --k) {
-                mma_bf16_16816(o[nt], pa[k], vb[0], vb[1]);
-                mma_bf16_16816(o[nt + 1], pa[k], vb[2], vb[3]);
-              }
-            }
-          }
-        } else {
-          float pp[8][NP];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) split_bf16<NP>(s[2 * c + (i >> 2)][i & 3], pp[i]);
-          uint32_t pa[NP][4];
-#pragma unroll
-          for (int k = 0; k < NP; ++k) {
-            pa[k][0] = pack_bf16x2(pp[0][k], pp[1][k]);
-            pa[k][1] = pack_bf16x2(pp[2][k], pp[3][k]);
-            pa[k][2] = pack_bf16x2(pp[4][k], pp[5][k]);
-            pa[k][3] = pack_bf16x2(pp[6][k], pp[7][k]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < HD / 8; nt += 2) {
-            uint32_t vb[4];
-            ldsm_x4_t(vb, vt + tile_off<HD, HD, true>(kr + 8 * (mi & 1) + r8, nt + (mi >> 1)));
-#pragma unroll
-            for (int k = NP - 1; k >= 0; --k) {
-              mma_bf16_16816(o[nt], pa[k], vb[0], vb[1]);
-              mma_bf16_16816(o[nt + 1], pa[k], vb[2], vb[3]);
-            }
-          }
-        }
-      }
-    }
-    if constexpr (KV8) __syncthreads();  // the widened tile has been read
-  }
-  cp_async_wait_all();
-  // non-finite tree values, to the rows that see them (the rank with the tree
-  // tile, one warp of the WK that share the rows)
-  if (!KV8 && p.tree.k && t0 < t1 && t1 == n_tiles && wk == 0 && *s_any) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int node = h ? node1 : node0;
-      uint64_t v = node < cnt ? smask[node] & seen : 0;
-      while (v) {
-        const int j = __ffsll(v) - 1;
-        v &= v - 1;
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int d = 8 * i + 2 * tq + e;
-            const float bad[3] = {INFINITY, -INFINITY, NAN};
-#pragma unroll
-            for (int kind = 0; kind < 3; ++kind)
-              if ((snf[(kind * kTreeMaxNodes + j) * NG + (d >> 5)] >> (d & 31)) & 1) {
-                if (h) o[i][2 + e] += bad[kind];
-                else o[i][e] += bad[kind];
-              }
-          }
-      }
-    }
-  }
-  // ---- the WK warps of each row -> the CTA's state -> the cluster's
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 1);
-    lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 2);
-  }
-  __syncthreads();  // the ring is free
-  float* so = reinterpret_cast<float*>(sm);  // [WK][MT][HD]
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 16 * wm + gr + 8 * h;
-    float* dst = so + (wk * MT + r) * HD + 2 * tq;
-#pragma unroll
-    for (int i = 0; i < HD / 8; ++i) *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
-    if (tq == 0) sml[wk * MT + r] = make_float2(mrun[h], lrun[h]);
-  }
-  __syncthreads();
-  for (int r = tid; r < MT; r += NT) {  // weights of the WK states, the CTA's (max, sum) in their place
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int w = 0; w < WK; ++w) M = fmaxf(M, sml[w * MT + r].x);
-#pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      const float2 ml = sml[w * MT + r];
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      sw[w * MT + r] = f;
-      L += ml.y * f;
-    }
-    sml[r] = make_float2(M, L);
-  }
-  __syncthreads();
-  for (int i = tid; i < MT * HD / 4; i += NT) {
-    const int r = i / (HD / 4);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      const float4 x = reinterpret_cast<const float4*>(so + w * MT * HD)[i];
-      const float f = sw[w * MT + r];
-      // a state without keys has weight 0 and o = 0
-      a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
-    }
-    reinterpret_cast<float4*>(so)[i] = a;
-  }
+// The cluster's S key ranges joined: rank k writes its share of the rows. so: a
+// rank's unnormalised O [N][HD], sml its (reference, sum) per row.
+template <int HD, bool F32, int N, int NT>
+__device__ __forceinline__ void join_splits(const TreeAttnParams& p, float* so, float2* sml, float* sw, int rank, int b,
+                                            int hkv, int m0, int rows) {
+  constexpr float kNone = -3e38f;
+  const int tid = threadIdx.x;
   cg::cluster_group cl = cg::this_cluster();
+  __syncthreads();
+  // ---- the cluster's S key ranges: rank k writes its share of the rows
   if (p.S > 1) cl.sync();
-  else __syncthreads();
-  for (int r = tid; r < MT; r += NT) {
-    float M = -INFINITY, L = 0.f;
-    for (int k = 0; k < p.S; ++k) M = fmaxf(M, cl.map_shared_rank(sml, k)[r].x);
-    for (int k = 0; k < p.S; ++k) {
-      const float2 ml = cl.map_shared_rank(sml, k)[r];
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      sw[k * MT + r] = f;
-      L += ml.y * f;
+  for (int r = tid; r < rows; r += NT) {
+    float2 ml[kMaxSplits];  // all loads in flight: a rank's answer takes long
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) ml[k] = k < p.S ? cl.map_shared_rank(sml, k)[r] : make_float2(kNone, 0.f);
+    float M = ml[0].x, L = 0.f;
+#pragma unroll
+    for (int k = 1; k < kMaxSplits; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) {
+      ml[k].x = ml[k].x <= kNone ? 0.f : ex2(ml[k].x - M);
+      L = fmaf(ml[k].y, ml[k].x, L);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
-    for (int k = 0; k < p.S; ++k) sw[k * MT + r] *= inv;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+      if (k < p.S) sw[k * N + r] = ml[k].x * inv;
   }
   __syncthreads();
-  const int n4 = MT * HD / 4, i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
+  const int n4 = rows * HD / 4;
+  const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
   for (int i = i0 + tid; i < i1; i += NT) {
-    const int r = i / (HD / 4), node = (m0 + r) / p.gq, h = g * p.gq + (m0 + r) % p.gq;
-    if (node >= cnt) continue;
+    const int r = i / (HD / 4), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < p.S; ++k) {
-      const float4 x = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k))[i];
-      const float f = sw[k * MT + r];
-      a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+#pragma unroll 1
+    for (int k0 = 0; k0 < p.S; k0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < p.S) x[k] = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k0 + k))[i];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < p.S) {
+          const float f = sw[(k0 + k) * N + r];
+          a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y), a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
+        }
     }
     const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % (HD / 4));
     if constexpr (F32)
@@ -506,34 +290,552 @@ __global__ void __launch_bounds__(32 * WM * WK) tree_attn_kernel(const __grid_co
   if (p.S > 1) cl.sync();  // a CTA's shared memory lives until every rank has read it
 }
 
-template <int HD, bool F32, bool KV8, int WM, int WK>
-cudaError_t launch_tree_attn_t(TreeAttnParams p, int n_sm, cudaStream_t st) {
-  using C = TreeAttn<HD, F32, KV8, WM, WK>;
-  const auto kern = tree_attn_kernel<HD, F32, KV8, WM, WK>;
+template <int HD, bool F32, int NB, int G>
+__global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB, G>::two ? 2 : 1) tree_attn_tc_kernel(
+    const __grid_constant__ TreeAttnTcParams tp) {
+  using C = TreeTc<HD, F32, NB, G>;
+  constexpr int N = C::N, NT = C::NT, NST = C::NST, NQ = C::NQ, NP = C::NP, NG = HD / 32, BK = C::BK, H = C::H, DB = C::DB;
+  constexpr float kNone = -3e38f;  // the reference before any visible score
+  extern __shared__ uint8_t sm_raw[];
+  const TreeAttnParams& p = tp.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  uint8_t* sring = sm;
+  uint8_t* sp = sring + NST * C::kUnit;   // [DB][G] blocks of P: [atom of 64 columns][key][kRowP], columns part by part
+  uint8_t* sq = sp + DB * G * C::kPBlock;               // [H][G][NQ][NB][128 B]
+  uint8_t* sones = sq + C::kQ;
+  uint8_t* small = sones + C::kOnes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(small);
+  uint64_t *full = bars, *empty = bars + 12, *s_full = bars + 24, *p_full = bars + 26, *o_done = bars + 28, *drain = bars + 30;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);
+  int* s_any = reinterpret_cast<int*>(small + 260);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 264);
+  uint64_t* smask = reinterpret_cast<uint64_t*>(small + 512);          // [64]
+  uint64_t* srow = reinterpret_cast<uint64_t*>(small + C::kOffRow);    // [N] what each row sees of the tree
+  float* sm_m = reinterpret_cast<float*>(srow + N);             // [N] references, negated
+  float* sm_w = sm_m + N;                                       // [4][N]
+  float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);        // [N]
+  float* sfac = reinterpret_cast<float*>(sml + N);              // [N] rescaling of O and the sums
+  uint32_t* snf = reinterpret_cast<uint32_t*>(sfac + N);        // [3][64][NG]
+  float* sw = reinterpret_cast<float*>(sp);                     // [kMaxSplits][N] merge weights, when P is done with
+  static_assert(kMaxSplits * N * 4 <= DB * G * C::kPBlock, "merge weights");
+
+  // TMA: the units in the order in which the MMAs release them
+  if (tid == 4 * G * 32) {
+    *s_abort = 0;
+    *s_any = 0;
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+    mbar_fence_init();
+  }
+  pdl_wait();  // nothing before this touches global memory
+  pdl_trigger();
+  const int hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
+  const int b = p.sorted ? nth_longest(p.lens, p.B, blockIdx.z, lane) : blockIdx.z;
+  const int len_b = p.lens[b], cnt_b = p.counts ? p.counts[b] : p.n;
+  const int cnt = min(max(cnt_b, 0), p.n);
+  if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
+  const int len = min(max(len_b, 0), p.cache.rows);
+  const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
+  const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S);
+  const int n_own = t1 - t0, n_units = 2 * H * n_own;
+  // The ring's order, in halves (K or V) of the CTA's tiles: K0 V0 K1 V1 .., or,
+  // with scores a tile ahead, K0 K1 V0 K2 V1 ..
+  auto k_unit = [&](int t) { return H * (DB == 1 ? 2 * t : t == 0 ? 0 : 2 * t - 1); };
+  auto v_unit = [&](int t) { return H * (DB == 1 ? 2 * t + 1 : t == n_own - 1 ? 2 * t + 1 : 2 * t + 2); };
+  auto request = [&](int i) {
+    const int j = i / H, u = i % H, slot = i % NST;
+    const bool val = DB == 1 ? j & 1 : j > 0 && (!(j & 1) || j == 2 * n_own - 1);
+    const int t = t0 + (DB == 1 ? j / 2 : j == 2 * n_own - 1 ? n_own - 1 : val ? j / 2 - 1 : (j + 1) / 2);
+    const bool tree = t >= n_pre;
+    const CUtensorMap* map = val ? (tree ? &tp.tv : &tp.cv) : (tree ? &tp.tk : &tp.ck);
+    mbar_expect_tx(full + slot, C::kUnit);
+    tma_box(sring + slot * C::kUnit, map, 64 * u, tree ? 0 : t * BK, hkv * (tree ? tp.t_head : tp.c_head),
+            b * (tree ? tp.t_seq : tp.c_seq), full + slot);
+  };
+  if (warp == 4 * G) {  // the ring's barriers are this warp's own: the first units are on their way at once
+    if (lane == 0)
+#pragma unroll 1
+      for (int i = 0; i < NST && i < n_units; ++i) request(i);
+  } else if (warp == 4 * G + 1) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
+      mbar_init(drain, 1);
+      mbar_fence_init();
+    }
+    __syncwarp();
+    // (after pdl_wait: held earlier, it could be what the kernel before this one is waiting for)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                 "r"((uint32_t)C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else {
+    // the query rows' bf16 parts, 128-byte rows of 64 dims, chunks permuted as by TMA's 128-byte swizzle
+    if (p.tree.k)
+      for (int i = tid; i < kTreeMaxNodes; i += 128 * G)
+        smask[i] = i < cnt ? p.mask[(int64_t)b * p.mask_seq + i] : 0;
+#pragma unroll 4
+    for (int i = tid; i < N * (HD / 8); i += 128 * G) {
+      const int r = i / (HD / 8), ch = i % (HD / 8), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
+      const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
+      uint8_t* dst = sq + (((ch / 8) * G + r / NB) * NQ * NB + r % NB) * 128 + 16 * ((ch & 7) ^ (r & 7));
+      if constexpr (F32) {
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (node < cnt) {
+          const float4 lo = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off);
+          const float4 hi = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off + 4);
+          x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+        }
+        uint32_t part[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_pack<3>(x[2 * e], x[2 * e + 1], part[e]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(dst + k * NB * 128) = make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
+      } else {
+        *reinterpret_cast<uint4*>(dst) = node < cnt
+                                             ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    for (int i = tid; i < C::kOnes / 16; i += 128 * G)
+      reinterpret_cast<uint4*>(sones)[i] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (p.tree.k && t1 == n_tiles)
+      for (int i = tid; i < 3 * kTreeMaxNodes * NG; i += 128 * G) snf[i] = 0;
+    for (int i = tid; i < N; i += 128 * G) sm_m[i] = -kNone;
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;  // S of block g at columns g NS (buffer d: d NS), O of 64 dims u at DB G NS + (u G + g) NO
+  uint64_t seen = 0;              // tree rows that some node sees
+  if (p.tree.k) {
+    const uint64_t a = smask[lane] | smask[lane + 32];
+    seen = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(a >> 32)) << 32) |
+           __reduce_or_sync(0xffffffffu, (uint32_t)a);
+    if (cnt < 64) seen &= (1ull << cnt) - 1;
+  }
+
+  if (warp == 4 * G) {
+    if (lane == 0) {
+      int i = min(NST, n_units);
+      for (; i < n_units; ++i) {
+        if (!tc_wait(empty + i % NST, (i / NST - 1) & 1, s_abort, p.status)) break;
+        request(i);
+      }
+      if (*s_abort)  // leave no copy in flight
+        for (int j = max(0, i - NST); j < i; ++j) {
+          const unsigned long long s0 = globaltimer();
+          while (!mbar_try_wait(full + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
+          }
+        }
+    }
+  } else if (warp == 4 * G + 1) {
+    // ---- MMA: commits release units and publish scores
+    constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 x bf16, 128 rows
+    constexpr uint32_t idesc_s = base_i | ((uint32_t)(C::NS >> 3) << 17);
+    constexpr uint32_t idesc_o = base_i | ((uint32_t)(C::NO >> 3) << 17) | (1u << 15) | (1u << 16);  // A and B MN-major
+    constexpr uint64_t swp = C::kRowP == 128 ? 2 : (C::kRowP == 64 ? 4 : 6);
+    constexpr uint32_t step_p = 16 * C::kRowP, sbo_p = 8 * C::kRowP;
+    const uint32_t uq = smem_u32(sq), up = smem_u32(sp), ur = smem_u32(sring), uo = smem_u32(sones);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    // block g's tile t0 + t: buffers and barriers x = g (DB 1) or t & 1 (DB 2)
+    auto scores = [&](int g, int t) {
+      const int x = DB == 2 ? t & 1 : g;
+#pragma unroll 1
+      for (int u = 0; u < H; ++u) {
+        const int i = k_unit(t) + u, slot = i % NST;
+        if (!tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status)) return false;
+        tc_fence_after();
+        const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
+        const uint64_t dq = tc_desc(uq + (u * G + g) * C::NS * 128, 16, 1024, 2);
+        if (elect_lane()) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
+            tc_mma(tm + x * C::NS, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
+        }
+        __syncwarp();
+        if (g == G - 1) tc_commit(empty + slot);
+      }
+      tc_commit(s_full + x);
+      return true;
+    };
+    bool ok = true;
+#pragma unroll 1
+    for (int t = -DB; t < n_own && ok; ++t)
+#pragma unroll 1
+      for (int g = 0; g < G && ok; ++g) {
+        if (t >= 0) {
+          const int x = DB == 2 ? t & 1 : g;
+          ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
+#pragma unroll 1
+          for (int u = 0; u < H; ++u) {
+            const int i = v_unit(t) + u, slot = i % NST;
+            ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v = ur + slot * C::kUnit;
+            // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
+            const uint64_t da = tc_desc(v, uo - v, 1024, 2);
+            const uint64_t dp = tc_desc(up + x * C::kPBlock, BK * 128, sbo_p, swp);
+            if (elect_lane()) {
+#pragma unroll
+              for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
+                tc_mma(tm + DB * G * C::NS + (u * G + g) * C::NO, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                       dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
+            }
+            __syncwarp();
+            if (g == G - 1) tc_commit(empty + slot);
+          }
+          if (!ok) break;
+          tc_commit(o_done + g);
+        }
+        if (t + DB < n_own) ok = scores(g, t + DB);
+      }
+    if (!ok) {  // no MMA may outlive its operands
+      tc_commit(drain);
+      const unsigned long long s0 = globaltimer();
+      while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
+      }
+    }
+  } else {
+    // ---- softmax: thread = key
+    const int g = warp >> 2, key = (warp & 3) * 32 + lane;
+    uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * C::NS;
+    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + DB * G * C::NS + g * C::NO;  // of 64 dims u: + u G NO
+    float* m = sm_m + g * NB;  // the references, negated
+    const float masked = p.c < 0.f ? INFINITY : -INFINITY;  // times c: -inf (c is not 0)
+    if (p.tree.k)
+      for (int r = key; r < NB; r += 128) {
+        const int node = p.by_gq.div(m0 + g * NB + r);
+        srow[g * NB + r] = node < cnt ? smask[node] & seen : 0;
+      }
+    group_sync(g);
+    // whether row r of the block sees this thread's tree row
+    const uint32_t* vis = reinterpret_cast<const uint32_t*>(srow + g * NB) + (warp & 1);
+    auto sees = [&](int r) { return key < kTreeMaxNodes && ((vis[2 * r] >> lane) & 1); };
+    constexpr int W = NB >= 32 && NQ == 1 ? 32 : 16;
+    auto load = [&](float (&v)[NQ][W], int c0) {
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) tc_ld(v[k], tS + k * NB + c0);
+    };
+    auto ready = [&](float (&v)[NQ][W]) {  // waits, and adds the parts, the small ones first
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) tc_wait_ld(v[k]);
+      if constexpr (NQ == 3)
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[0][j] += v[1][j] + v[2][j];
+    };
+    for (int t = t0; t < t1; ++t) {
+      const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
+      const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
+      // these scores: this buffer's last P V is done too
+      const int x = DB == 2 ? (t - t0) & 1 : g;
+      tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
+      tc_fence_after();
+      if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NS;
+      if (!whole) {  // V rows that are not there become zeros, non-finite tree values too (noted for the rows that see them)
+        // (after the last P V, so that the slot's last unit has been read and its barrier is in this unit's phase)
+        if (DB == 2 && t > t0) tc_wait(o_done + g, (t - t0 - 1) & 1, s_abort, p.status);
+        for (int u = 0; u < H; ++u) {
+          const int i = v_unit(t - t0) + u;
+          tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
+        }
+#pragma unroll 4
+        for (int c = 0; c < HD / 8 && (tree || !valid); ++c) {
+          const int slot = (v_unit(t - t0) + c / 8) % NST;
+          uint4* x = reinterpret_cast<uint4*>(sring + slot * C::kUnit + key * 128 + 16 * ((c & 7) ^ (key & 7)));
+          if (!valid) {
+            *x = make_uint4(0u, 0u, 0u, 0u);
+          } else if (tree) {
+            const uint4 w = *x;
+            uint32_t inf = 0;  // whether an exponent is all ones
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t v = (&w.x)[j] & 0x7F807F80u;
+              inf |= (v & 0xFFFFu) == 0x7F80u || (v >> 16) == 0x7F80u;
+            }
+            if (inf) {
+              uint16_t* e = reinterpret_cast<uint16_t*>(x);
+#pragma unroll 1
+              for (int j = 0; j < 8; ++j)
+                if ((e[j] & 0x7F80u) == 0x7F80u) {
+                  const int kind = (e[j] & 0x7Fu) ? 2 : e[j] >> 15, d = 8 * c + j;
+                  atomicOr(snf + (kind * kTreeMaxNodes + key) * NG + (d >> 5), 1u << (d & 31));
+                  e[j] = 0;
+                }
+              *s_any = 1;
+            }
+          }
+        }
+      }
+      if (t == t0) {  // the references: the score of the first key that a row sees (renewed below if not finite)
+        float* first = reinterpret_cast<float*>(sp + x * C::kPBlock);  // [64][NB], where P comes to lie
+        static_assert(64 * NB * 4 <= C::kPBlock, "room for the first scores");
+        if (warp < 4 * g + (tree ? 2 : 1))
+#pragma unroll 1
+          for (int c0 = 0; c0 < NB; c0 += W) {
+            float v[NQ][W];
+            load(v, c0);
+            ready(v);
+            if (tree || lane == 0)
+#pragma unroll
+              for (int j = 0; j < W; j += 4)
+                *reinterpret_cast<float4*>(first + key * NB + c0 + j) =
+                    make_float4(v[0][j], v[0][j + 1], v[0][j + 2], v[0][j + 3]);
+          }
+        group_sync(g);
+        float y = INFINITY;
+        if (key < NB) {  // a thread per row (NB <= 128)
+          const int j = tree ? __ffsll(srow[g * NB + key]) - 1 : 0;
+          if (j >= 0) y = first[j * NB + key] * p.c;
+          m[key] = fabsf(y) < 1e38f ? -y : -kNone;
+        }
+        group_sync(g);
+      }
+      uint8_t* prow = sp + x * C::kPBlock + key * C::kRowP;
+      const int sel = C::kRowP == 128 ? key & 7 : (C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
+      for (;;) {
+        // probabilities with the references as they are; the largest excess over them
+        uint32_t top = 0;  // of P's first parts, two at a time
+        auto take = [&](float (&v)[NQ][W], int c0) {
+          float(&s)[W] = v[0];
+          if (tree) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+              if (!sees(c0 + j)) s[j] = masked;
+          } else if (!whole && !valid) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) s[j] = masked;
+          }
+#pragma unroll
+          for (int h = 0; h < W / 8; ++h) {
+            uint32_t part[4][NP];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const float4 ref = *reinterpret_cast<const float4*>(m + c0 + 8 * h + j);
+              float y[4] = {ref.x, ref.y, ref.z, ref.w};
+              fma2(y[0], y[1], s[8 * h + j], s[8 * h + j + 1], p.c, p.c);
+              fma2(y[2], y[3], s[8 * h + j + 2], s[8 * h + j + 3], p.c, p.c);
+              split_pack<NP>(ex2(y[0]), ex2(y[1]), part[j / 2]);
+              split_pack<NP>(ex2(y[2]), ex2(y[3]), part[j / 2 + 1]);
+              top = max_bf16x2(top, max_bf16x2(part[j / 2][0], part[j / 2 + 1][0]));
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+              const int chunk = (k * NB + c0 + 8 * h) / 8;
+              *reinterpret_cast<uint4*>(prow + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ sel)) =
+                  make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
+            }
+          }
+        };
+        float va[NQ][W], vb[NQ][W];  // the next columns load while these are worked on
+        load(va, 0);
+#pragma unroll 1
+        for (int c0 = 0; c0 < NB; c0 += 2 * W) {
+          ready(va);
+          if (c0 + W < NB) load(vb, c0 + W);
+          take(va, c0);
+          if (c0 + W < NB) {
+            ready(vb);
+            if (c0 + 2 * W < NB) load(va, c0 + 2 * W);
+            take(vb, c0 + W);
+          }
+        }
+        constexpr float kLimit = 1152921504606846976.f;  // 2^60
+        const bool over = __uint_as_float(top << 16) > kLimit || __uint_as_float(top & 0xFFFF0000u) > kLimit;
+        if (!group_any(g, over)) break;
+        // renew the references: the maxima per warp, then over the four; rescale O and the sums
+#pragma unroll 1
+        for (int c0 = 0; c0 < NB; c0 += W) {
+          float v[NQ][W];
+          load(v, c0);
+          ready(v);
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            const bool in = tree ? sees(c0 + j) : valid;
+            float y = in ? v[0][j] * p.c : -INFINITY;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+            if (lane == 0) sm_w[(warp & 3) * N + g * NB + c0 + j] = y;
+          }
+        }
+        group_sync(g);
+        if (key < NB) {
+          const float* w = sm_w + g * NB + key;
+          const float old = -m[key], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
+          m[key] = -now;
+          sfac[g * NB + key] = old == now ? 1.f : exp2f(old - now);
+        }
+        group_sync(g);
+        if (t > t0) {
+          tc_wait(o_done + g, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V is in O
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < C::NO * H; c0 += 16) {
+            const uint32_t at = tO + (c0 / C::NO) * G * C::NO + c0 % C::NO;
+            float s[16];
+            tc_ld(s, at);
+            tc_wait_ld(s);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[j] *= sfac[g * NB + (c0 + j) % NB];
+            tc_st16(at, s);
+          }
+          tc_wait_st();
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(p_full + x);
+    }
+    // ---- O^T and the sums to shared memory, [row][dim]
+    // (one phase at a time: with two buffers the last but one P V may still run)
+    if (DB == 2 && n_own > 1) tc_wait(o_done + g, (n_own - 2) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait(o_done + g, (n_own - 1) & 1, s_abort, p.status);
+    tc_fence_after();
+    // every block's last MMAs have read the ring and P before any block writes over them
+    asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
+    float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
+    const bool have = t0 < t1;
+#pragma unroll 1
+    for (int c0 = 0; c0 < NB * H; c0 += 16) {
+      const int u = c0 / NB, r0 = c0 % NB;
+      float s[NP][16];
+      if (have) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) tc_ld(s[k], tO + u * G * C::NO + k * NB + r0);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) tc_wait_ld(s[k]);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float x = 0.f;
+        if (have)
+#pragma unroll
+          for (int k = NP - 1; k >= 0; --k) x += s[k][j];
+        if (key < 64) so[(r0 + j) * HD + 64 * u + key] = x;
+        if (u == 0 && key == 64) sml[g * NB + r0 + j] = make_float2(-m[r0 + j], x);
+      }
+    }
+    if (p.tree.k && have && t1 == n_tiles && *s_any && key < 64) {  // non-finite tree values, where they are seen
+      for (int d = key; d < HD; d += 64)
+        for (int r = 0; r < NB; ++r)
+          for (uint64_t v = srow[g * NB + r]; v; v &= v - 1) {
+            const int j = __ffsll(v) - 1;
+            const float bad[3] = {INFINITY, -INFINITY, NAN};
+#pragma unroll
+            for (int kind = 0; kind < 3; ++kind)
+              if ((snf[(kind * kTreeMaxNodes + j) * NG + (d >> 5)] >> (d & 31)) & 1) so[r * HD + d] += bad[kind];
+          }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sw, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
+  // Freed last: no two CTAs that hold and that wait for tensor memory share an
+  // SM (kernels whose columns exceed half take all of its shared memory), so a
+  // CTA that holds it while its cluster gathers cannot keep a peer waiting.
+  if (warp == 4 * G + 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kCols));
+  }
+}
+
+// cuTensorMapEncodeTiled, looked up once; null where the driver has none.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiled tensor_map_encoder() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// The map of one K or V tensor [seq][head][row][dim] of bf16 or int8.
+template <int HD, bool Q8>
+bool encode_rows(CUtensorMap* map, const uint8_t* base, const KvRows& r, int B, int heads) {
+  const EncodeTiled enc = tensor_map_encoder();
+  if (!enc) return false;
+  if (r.seq == 0) B = 1;
+  if (r.head == 0) heads = 1;
+  const int64_t row = r.rows > 1 ? r.row : HD;
+  const int64_t head = heads > 1 ? r.head : row * r.rows, seq = B > 1 ? r.seq : head * heads;
+  const cuuint64_t dims[4] = {(cuuint64_t)HD, (cuuint64_t)r.rows, (cuuint64_t)heads, (cuuint64_t)B};
+  const int64_t size = Q8 ? 1 : 2;
+  const cuuint64_t strides[3] = {(cuuint64_t)(row * size), (cuuint64_t)(head * size), (cuuint64_t)(seq * size)};
+  const cuuint32_t box[4] = {Q8 ? HD : 64, 128, 1, 1}, step[4] = {1, 1, 1, 1};
+  return enc(map, Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             Q8 && HD == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <int HD, bool Q8>
+bool encode_all(TreeAttnTcParams& tp) {
+  const TreeAttnParams& p = tp.p;
+  tp.c_seq = p.cache.seq != 0, tp.c_head = p.cache.head != 0, tp.t_seq = p.tree.seq != 0, tp.t_head = p.tree.head != 0;
+  if (p.cache.rows > 0 && !(encode_rows<HD, Q8>(&tp.ck, p.cache.k, p.cache, p.B, p.Hkv) &&
+                            encode_rows<HD, Q8>(&tp.cv, p.cache.v, p.cache, p.B, p.Hkv)))
+    return false;
+  return p.tree.k == nullptr || (encode_rows<HD, Q8>(&tp.tk, p.tree.k, p.tree, p.B, p.Hkv) &&
+                                 encode_rows<HD, Q8>(&tp.tv, p.tree.v, p.tree, p.B, p.Hkv));
+}
+
+template <int HD, bool F32, int NB, int G>
+cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
+  using C = TreeTc<HD, F32, NB, G>;
+  const auto kern = tree_attn_tc_kernel<HD, F32, NB, G>;
   static SmemLimit limit;
-  cudaError_t e = limit.raise(kern, C::kSmem);
+  cudaError_t e = limit.raise(kern, C::kSmem, true);
   if (e != cudaSuccess) return e;
-  const int m_tiles = (p.n * p.gq + C::MT - 1) / C::MT;
+  TreeAttnParams& p = tp.p;
+  const int m_tiles = (p.n * p.gq + C::N - 1) / C::N;
   const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
   int S = 1;
-  while (S < 8 && S < tiles && clusters * S < 4 * n_sm) S *= 2;
+  // Split the keys until every SM has a CTA; where two fit, also to fill both
+  // places while 16 tiles are left for each: more splits cost their merges
+  // (32 sequences x 8 kv heads, 17 tiles: 43 / 48 / 67 us for 1 / 2 / 4; 16 x 4 x 4 row
+  // tiles, 65 tiles: 129 / 109 / 132; 8 clusters of 513 tiles: 667 / 340 / 179 / 96 for 1 to 8).
+  while (S < kMaxSplits && S < tiles &&
+         (clusters * S < n_sm || (C::two && clusters * S < 2 * n_sm && tiles / (2 * S) >= 16)))
+    S *= 2;
   p.S = S;
-  return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, p);
+  p.sorted = p.B > 1 && p.B <= 64;
+  return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, tp);
 }
 
-template <int HD, bool F32, bool KV8>
-cudaError_t launch_tree_attn_m(const TreeAttnParams& p, int n_sm, cudaStream_t st) {
-  const int M = p.n * p.gq;
-  if (M <= 16) return launch_tree_attn_t<HD, F32, KV8, 1, 4>(p, n_sm, st);
-  if (M <= 32) return launch_tree_attn_t<HD, F32, KV8, 2, 4>(p, n_sm, st);
-  return launch_tree_attn_t<HD, F32, KV8, 4, 2>(p, n_sm, st);
-}
-
+// bf16 rows
 template <int HD>
-cudaError_t launch_tree_attn_hd(const TreeAttnParams& p, bool f32, bool q8, int n_sm, cudaStream_t st) {
-  if (f32) return q8 ? launch_tree_attn_m<HD, true, true>(p, n_sm, st) : launch_tree_attn_m<HD, true, false>(p, n_sm, st);
-  return q8 ? launch_tree_attn_m<HD, false, true>(p, n_sm, st) : launch_tree_attn_m<HD, false, false>(p, n_sm, st);
+cudaError_t launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStream_t st) {
+  TreeAttnTcParams tp;
+  tp.p = p;
+  if (!encode_all<HD, false>(tp)) return cudaErrorNotSupported;
+  // Rows of a CTA: as many as there are (K and V are read once for them), in two
+  // blocks once there are 32 (one block's softmax overlaps the other's MMAs); but
+  // fewer while the clusters, split eight ways, would leave SMs without a CTA
+  // (16 nodes x 8 heads over 4097 rows, fp32: 16 / 32 / 64 rows 16.5 / 18.6 / 20.6 us).
+  // 128 rows at most: 256 fill tensor memory and leave one CTA on an SM (16 x 64
+  // nodes over 1024..8192 rows: 119 against 109 us).
+  const int M = p.n * p.gq, most = f32 ? (HD == 64 ? 64 : 32) : 128;
+  int N = 16;
+  while (N < M && N < most) N *= 2;
+  while (N > 16 && (int64_t)p.B * p.Hkv * ((M + N - 1) / N) * 8 < n_sm) N /= 2;
+  if (f32)
+    return N == 16   ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st)
+           : N == 32 ? launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st)
+                     : launch_tree_tc_t<HD, true, HD == 64 ? 32 : 16, 2>(tp, n_sm, st);
+  return N == 16   ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)
+         : N == 32 ? launch_tree_tc_t<HD, false, 16, 2>(tp, n_sm, st)
+         : N == 64 ? launch_tree_tc_t<HD, false, 32, 2>(tp, n_sm, st)
+                   : launch_tree_tc_t<HD, false, 64, 2>(tp, n_sm, st);
 }
 
 }  // namespace llmq

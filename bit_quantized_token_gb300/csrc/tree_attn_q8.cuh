@@ -1,5 +1,5 @@
 // Tree attention over int8 rows with a scale per 32 values, on the tensor cores
-// (the products, roles and references of tree_attn_tc.cuh; what differs:)
+// (the products, roles and references of tree_attn.cuh; what differs:)
 // - Eight converter warps widen the codes, which TMA brings as they are, to bf16
 //   (exact): four for the K tiles, four for the V tiles.
 // - S^T of each group of 32 dims has columns of its own; the softmax thread, which
@@ -12,9 +12,25 @@
 // Bound: conversion (a byte of HBM is two of shared memory written and read by the
 // MMAs) and the MMAs' fetch of it, 24 x 32 cycles a tile and block at 128 dims.
 #pragma once
-#include "tree_attn_tc.cuh"
+#include "tree_attn.cuh"
 
 namespace llmq {
+
+// Four int8 codes (a word) as two bf16 pairs, exactly: 128 + (c & 127) and
+// 128 + (c & 128) are bf16 integers below 512 of the same step, and their
+// difference is c.
+__device__ __forceinline__ uint2 i8x4_to_bf16(uint32_t w) {
+  uint32_t r[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t b = __byte_perm(w, 0u, h ? 0x4342 : 0x4140);  // bytes 2h, 2h+1 in the low halves' bytes
+    const uint32_t a = (b & 0x007F007Fu) | 0x43004300u, s = (b & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&s));
+    r[h] = *reinterpret_cast<const uint32_t*>(&d);
+  }
+  return make_uint2(r[0], r[1]);
+}
 
 template <int HD, bool F32, int G>
 struct TreeQ8 {
@@ -87,7 +103,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     uint64_t* bar = raw_full + 4 * kv + slot;
     mbar_expect_tx(bar, C::kRaw);
     tma_box(sraw + (kv * R + slot) * C::kRaw, kv ? (tree ? &tp.tv : &tp.cv) : (tree ? &tp.tk : &tp.ck), 0,
-            tree ? 0 : (t0 + t) * BK, hkv, b, bar);
+            tree ? 0 : (t0 + t) * BK, hkv * (tree ? tp.t_head : tp.c_head), b * (tree ? tp.t_seq : tp.c_seq), bar);
   };
   if (warp == kTmaWarp) {
     if (lane == 0)
@@ -484,19 +500,17 @@ cudaError_t launch_tree_q8_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, tp);
 }
 
-// false: TMA cannot address these tensors
 template <int HD>
-bool launch_tree_q8(const TreeAttnParams& p, bool f32, int n_sm, cudaStream_t st, cudaError_t* e) {
+cudaError_t launch_tree_q8(const TreeAttnParams& p, bool f32, int n_sm, cudaStream_t st) {
   TreeAttnTcParams tp;
   tp.p = p;
-  if (!encode_all<HD, true>(tp)) return false;
+  if (!encode_all<HD, true>(tp)) return cudaErrorNotSupported;
   const int M = p.n * p.gq;
+  // 16 rows a block; two blocks share the widened tiles where tensor memory holds both
   if (f32)
-    *e = HD == 128 || M <= 16 ? launch_tree_q8_t<HD, true, 1>(tp, n_sm, st)
-                              : launch_tree_q8_t<HD, true, HD == 64 ? 2 : 1>(tp, n_sm, st);
-  else
-    *e = M <= 16 ? launch_tree_q8_t<HD, false, 1>(tp, n_sm, st) : launch_tree_q8_t<HD, false, 2>(tp, n_sm, st);
-  return true;
+    return HD == 128 || M <= 16 ? launch_tree_q8_t<HD, true, 1>(tp, n_sm, st)
+                                : launch_tree_q8_t<HD, true, HD == 64 ? 2 : 1>(tp, n_sm, st);
+  return M <= 16 ? launch_tree_q8_t<HD, false, 1>(tp, n_sm, st) : launch_tree_q8_t<HD, false, 2>(tp, n_sm, st);
 }
 
 }  // namespace llmq

@@ -392,8 +392,9 @@ int llm_matvec_noalloc(const llm_model* m, const char* name, const float* x, flo
  * Source: no page drafts tokens; the cache formats are llm_kv_write's. */
 
 /* K and V rows in device memory, [seq][layer][head][row][head_dim] at any
- * strides (in elements, multiples of 16 bytes; a row is contiguous; k and v
- * 16-byte aligned and laid out alike). LLM_BF16, or LLM_Q8G32: int8 codes and
+ * strides (in elements, multiples of 16 bytes, below 2^38; a row is contiguous;
+ * k and v 16-byte aligned and laid out alike; a sequence or head stride of 0
+ * shares the rows). LLM_BF16, or LLM_Q8G32: int8 codes and
  * fp16 scales [..][head_dim / 32] at the scale strides (multiples of
  * head_dim / 32, aligned to a row of scales). head_dim 64 or 128. */
 typedef struct {

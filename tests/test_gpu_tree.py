@@ -170,6 +170,29 @@ def test_attention_without_tree(q, n):
     p.check()
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q", ["f32", "bf16"])
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+@pytest.mark.parametrize("n", [1, 20])
+def test_attention_many_tiles_to_a_cta(n, kv, q, hd):
+    """More (sequence, kv head) pairs than SMs, so that each is one CTA's, over ragged caches of up to 17 tiles."""
+    lens = (2100, 1300, 129, 1919, 640, 1, 1664, 0)
+    p = Problem(B=40, n=n, Hkv=4, gq=1, hd=hd, cap=2101, lens=lens, q=q, kv=kv)
+    for b in range(40):
+        if kv == "bf16":
+            p.v[b, :, int(p.lens[b]):] = float("nan")
+        else:
+            p.vs[b, :, int(p.lens[b]):] = float("nan")
+    p.call()
+    keep, p.B = p.out, 8
+    p.check()
+    p.out, p.lens = keep[32:], p.lens[32:]
+    for name in ("q", "k", "v", "ks", "vs", "tk", "tv", "tks", "tvs", "mask"):
+        t = getattr(p, name)
+        setattr(p, name, None if t is None else t[32:])
+    p.check()
+
+
 def test_attention_scores_far_apart_and_scale():
     for scale in (0.0, -0.3, 4.0):
         p = Problem(B=1, n=4, cap=200, lens=(200,), q="f32")
@@ -241,6 +264,22 @@ def test_attention_strided_tensors():
     p.call()
     p.check()
     assert (ob[..., hd:] == 7.0).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+def test_attention_shared_rows(kv):
+    """One prefix for every sequence, one kv head for all: strides of 0."""
+    p = Problem(B=3, n=4, Hkv=2, gq=2, cap=150, lens=(150, 3, 77), kv=kv)
+    for name in ("k", "v", "ks", "vs"):
+        t = getattr(p, name)
+        if t is not None:
+            setattr(p, name, t[:1, :1].expand(3, 2, *t.shape[2:]))
+    for name in ("tk", "tv", "tks", "tvs"):
+        t = getattr(p, name)
+        if t is not None:
+            setattr(p, name, t[:, :1].expand(3, 2, *t.shape[2:]))
+    p.call()
+    p.check()
 
 
 def test_attention_offsets_beyond_32_bits():
