@@ -45,7 +45,7 @@ EXPORTS = ["llm_model_create", "llm_model_destroy", "llm_prefill", "llm_prefill_
            "llm_decode_step_batch", "llm_kv_reset", "llm_kv_write", "llm_kv_read", "llm_kv_read_q8", "llm_kv_len",
            "llm_debug_hidden", "llm_debug_unpack", "llm_model_stats", "llm_profile_step", "llm_time_kernel", "llm_sync",
            "llm_last_error", "llm_op_matvec", "llm_op_matvec_w4a8", "llm_matvec_noalloc", "llm_phase_times", "llm_debug_fail_alloc",
-           "llm_debug_hidden_batch", "llm_tree_attention", "llm_tree_status", "llm_token_probs", "llm_verify_tree", "llm_commit_tree"]
+           "llm_debug_hidden_batch", "llm_tree_attention", "llm_tree_status", "llm_token_probs", "llm_verify_tree", "llm_commit_tree", "llm_decode_tree"]
 
 
 # translation units of the library, compiled in parallel and linked into one shared object
@@ -174,6 +174,7 @@ def lib() -> C.CDLL:
             "llm_token_probs": (i32, [P, C.c_int64, P, C.c_int64, i32, i32, C.c_float, i32, C.c_float, P]),
             "llm_verify_tree": (i32, [P, P]),
             "llm_commit_tree": (i32, [P, P, i32, i32, P, P, P, P, P]),
+            "llm_decode_tree": (i32, [P, i32, P, P, i32, P, P, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -288,6 +289,19 @@ class Model:
             tokens = np.ascontiguousarray(tokens, np.int32)
         _check(lib().llm_decode_step_batch(self.h, _ptr(tokens), self.max_batch, _ptr(logits), _ptr(argmax)),
                self.h)
+
+    def decode_tree(self, seq: int, tokens, parents, draft_probs=None, uniforms=None, logits=None):
+        """One step over a drafted tree (node 0: the last chosen token): the kept nodes and the token after them."""
+        toks, par = np.ascontiguousarray(tokens, np.int32), np.ascontiguousarray(parents, np.int32)
+        if toks.ndim != 1 or par.shape != toks.shape:
+            raise LlmError(-1, "tokens and parents must be one-dimensional and of one length")
+        u = None if uniforms is None else np.ascontiguousarray(uniforms, np.float32)
+        if u is not None and u.shape != toks.shape:
+            raise LlmError(-1, "uniforms must have one value per node")
+        path, n, nxt = np.empty(toks.size, np.int32), np.empty(1, np.int32), np.empty(1, np.int32)
+        _check(lib().llm_decode_tree(self.h, seq, toks.ctypes.data, par.ctypes.data, toks.size, _ptr(draft_probs),
+                                     _ptr(u), path.ctypes.data, n.ctypes.data, nxt.ctypes.data, _ptr(logits)), self.h)
+        return path[:int(n[0])], int(nxt[0])
 
     # ---- cache -------------------------------------------------------------
     def kv_reset(self, seq: int = -1) -> None:

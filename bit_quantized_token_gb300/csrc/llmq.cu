@@ -26,7 +26,7 @@
 #include "stepll.cuh"
 #include "batch.cuh"
 #include "sample.cuh"
-#include "tree.cuh"
+#include "tree_model.cuh"
 #include "llmq.h"
 
 using namespace llmq;
@@ -195,6 +195,19 @@ Part make_part(int n_rt, int G, int n_cta) {
 
 }  // namespace
 
+// One drafted tree on the device (llm_decode_tree); `in` is uploaded.
+struct TreeState {
+  struct In {
+    int32_t tok[kBM], pos[kBM], parent[kBM];
+    uint64_t mask[kBM];
+    float u[kBM];
+  } in;
+  struct Out {
+    int32_t path[kBM], n_path, next;
+  } out;
+  int32_t tok_io[kBM], argmax[kBM];
+};
+
 struct llm_model {
   llm_config cfg{};
   int device = 0;
@@ -277,7 +290,14 @@ struct llm_model {
   int* d_pf = nullptr;                        // batched prefill: [tok | pos | seq][pf_cap], then [2][kBM] scratch
   SampleCfg* d_samp = nullptr;                // sampling options (temperature 0: greedy)
   bool sampling = false;
+  SampleCfg samp{};                           // the same options on the host
   size_t pf_cap = 0;
+  // drafted trees (llm_decode_tree): the nodes' rows of every layer in the cache's
+  // format [L][Hkv][kBM][hd], queries and attention output, the tree and its outcome
+  uint8_t *d_tree_k = nullptr, *d_tree_v = nullptr;
+  uint16_t *d_tree_ks = nullptr, *d_tree_vs = nullptr;
+  float *d_tree_q = nullptr, *d_tree_o = nullptr;
+  TreeState* d_tree = nullptr;
   int* h_stage = nullptr;                     // pinned staging (slots: kStage*)
   float* h_logits = nullptr;                  // pinned logits of a batch-1 call with host outputs
   size_t h_logits_n = 0;
@@ -794,6 +814,8 @@ struct BatchedIO {
   bool lm;               // run the LM head with its greedy choice
   int* tok_io;           // [M] greedy choice fed back as the next token
   int* argmax_out;       // [M]
+  const uint64_t* mask;  // the rows are a drafted tree of sequence tree_seq: which of them each sees; or null
+  int tree_seq;
 };
 
 BatchedIO decode_io(llm_model* m) {
@@ -807,6 +829,89 @@ BatchedIO decode_io(llm_model* m) {
   return io;
 }
 
+// K/V rows of one layer of sequence seq, and of the drafted tree (tree: seq ignored).
+KvRows layer_rows(const llm_model* m, int seq, int l, bool tree) {
+  const llm_config& c = m->cfg;
+  KvRows r;
+  r.rows = tree ? kBM : c.max_seq;
+  r.row = c.head_dim;
+  r.head = (int64_t)r.rows * r.row;
+  r.srow = c.head_dim / 32;
+  r.shead = (int64_t)r.rows * r.srow;
+  const size_t off = (size_t)((tree ? 0 : (int64_t)seq * c.n_layers) + l) * c.n_kv_heads * r.head;
+  const size_t bytes = m->kv8 ? off : 2 * off;
+  const uint8_t* kb = tree ? m->d_tree_k : m->kv8 ? (const uint8_t*)m->d_k8 : (const uint8_t*)m->d_k;
+  const uint8_t* vb = tree ? m->d_tree_v : m->kv8 ? (const uint8_t*)m->d_v8 : (const uint8_t*)m->d_v;
+  r.k = kb + bytes;
+  r.v = vb + bytes;
+  if (m->kv8) {
+    r.ks = (tree ? m->d_tree_ks : m->d_ks) + off / 32;
+    r.vs = (tree ? m->d_tree_vs : m->d_vs) + off / 32;
+  }
+  return r;
+}
+
+// One layer's attention of a drafted tree: the nodes' queries and rows, the
+// attention over cache and tree, its output staged for the o-projection.
+cudaError_t enqueue_tree_attention(llm_model* m, const BatchedIO& io, int l) {
+  const llm_config& c = m->cfg;
+  const bool pdl = !(c.flags & LLM_NO_PDL);
+  const int hd = c.head_dim, H = c.n_kv_heads;
+  const KvRows cache = layer_rows(m, io.tree_seq, l, false), tree = layer_rows(m, 0, l, true);
+  TreeRowsParams rp{};
+  rp.qkv = m->d_bqkv;
+  rp.qkv_cols = m->q_dim + 2 * m->kv_dim;
+  rp.q_dim = m->q_dim;
+  rp.kv_dim = m->kv_dim;
+  rp.n_heads = c.n_heads;
+  rp.n_kv = H;
+  rp.pos = io.pos;
+  rp.rope = m->d_rope;
+  rp.rope_neox = c.rope_neox;
+  rp.cap = c.max_seq;
+  rp.q_norm = c.qk_norm ? m->d_norms + m->off_q_norm[l] : nullptr;
+  rp.k_norm = c.qk_norm ? m->d_norms + m->off_k_norm[l] : nullptr;
+  rp.eps = c.norm_eps;
+  rp.q = m->d_tree_q;
+  if (m->kv8) {
+    rp.k8 = (int8_t*)tree.k;
+    rp.v8 = (int8_t*)tree.v;
+    rp.ks = (uint16_t*)tree.ks;
+    rp.vs = (uint16_t*)tree.vs;
+  } else {
+    rp.k = (uint16_t*)tree.k;
+    rp.v = (uint16_t*)tree.v;
+  }
+  rp.rows = kBM;
+  rp.status = m->d_status;
+  const dim3 rg((c.n_heads + 2 * H + 3) / 4, io.M);
+  cudaError_t e = hd == 64 ? launch_cluster(tree_rows_kernel<64>, rg, 128, 1, 0, m->stream, rp, pdl)
+                           : launch_cluster(tree_rows_kernel<128>, rg, 128, 1, 0, m->stream, rp, pdl);
+  if (e != cudaSuccess) return e;
+  TreeAttnParams ap{};
+  ap.q = m->d_tree_q;
+  ap.out = m->d_tree_o;
+  ap.q_node = ap.o_node = m->q_dim;
+  ap.q_head = ap.o_head = hd;
+  ap.q_seq = ap.o_seq = (int64_t)io.M * m->q_dim;
+  ap.cache = cache;
+  ap.tree = tree;
+  ap.lens = m->d_pos + io.tree_seq;  // the next token's position: the rows that the cache holds
+  ap.mask = io.mask;
+  ap.mask_seq = io.M;
+  ap.c = (float)(1.4426950408889634 / std::sqrt((double)hd));
+  ap.B = 1;
+  ap.n = io.M;
+  ap.Hkv = H;
+  ap.gq = m->gq;
+  ap.by_gq = FastDiv(m->gq);
+  ap.status = m->d_status;
+  ap.pdl = pdl;
+  if ((e = launch_tree_attn(ap, hd, true, m->kv8, m->n_sm, m->stream)) != cudaSuccess) return e;
+  const TreeStageParams sp{m->d_tree_o, m->d_bo_hl, m->q_dim};
+  return launch_cluster(tree_stage_kernel, dim3((m->q_dim + 255) / 256, io.M), 256, 1, 0, m->stream, sp, pdl);
+}
+
 // Enqueue one pass of the batched pipeline on m->stream: a decode step of
 // every sequence, or a chunk of a prompt (all rows append their k, v first,
 // then attend causally over the cache).
@@ -814,7 +919,7 @@ cudaError_t enqueue_batched(llm_model* m, const BatchedIO& io) {
   const llm_config& c = m->cfg;
   const int L = c.n_layers, d = c.dim, B = io.M, F = c.ffn_dim;
   // the hidden-state capture copies sit between the kernels: no programmatic launches then
-  const bool capture = m->d_bhid && !io.chunk && io.M == c.max_batch;
+  const bool capture = m->d_bhid && !io.chunk && !io.mask && io.M == c.max_batch;
   const bool pdl = !(c.flags & LLM_NO_PDL) && !capture;
   auto capture_x = [&](int k) {  // the residual after the embedding (k = 0) or layer k - 1
     return capture ? cudaMemcpyAsync(m->d_bhid + (size_t)k * B * d, m->d_bx, (size_t)B * d * 4,
@@ -878,16 +983,20 @@ cudaError_t enqueue_batched(llm_model* m, const BatchedIO& io) {
     bp.seq = io.seq;
     bp.seq_kv_stride = (size_t)L * kv_layer;
     bp.part_stride = (size_t)c.n_kv_heads * m->attn_P * m->gq * (c.head_dim + 2);
-    if (io.chunk) {
-      bp.mode = BA_APPEND;
-      if ((e = launch_battn(m, bp, 1, B, pdl)) != cudaSuccess) return e;
-      bp.mode = BA_ATTEND;
+    if (io.mask) {
+      if ((e = enqueue_tree_attention(m, io, l)) != cudaSuccess) return e;
     } else {
-      bp.mode = BA_APPEND_ATTEND;
+      if (io.chunk) {
+        bp.mode = BA_APPEND;
+        if ((e = launch_battn(m, bp, 1, B, pdl)) != cudaSuccess) return e;
+        bp.mode = BA_ATTEND;
+      } else {
+        bp.mode = BA_APPEND_ATTEND;
+      }
+      // splits of LLMQ_BATTN_SPLIT_LEN positions: no cache of this model needs more than its capacity's
+      const int splits = std::min(m->attn_P, (c.max_seq + LLMQ_BATTN_SPLIT_LEN - 1) / LLMQ_BATTN_SPLIT_LEN);
+      if ((e = launch_battn(m, bp, splits, B, pdl)) != cudaSuccess) return e;
     }
-    // splits of LLMQ_BATTN_SPLIT_LEN positions: no cache of this model needs more than its capacity's
-    const int splits = std::min(m->attn_P, (c.max_seq + LLMQ_BATTN_SPLIT_LEN - 1) / LLMQ_BATTN_SPLIT_LEN);
-    if ((e = launch_battn(m, bp, splits, B, pdl)) != cudaSuccess) return e;
     p = bgemv_params(m, m->bwo[l], B);  // h = x + Wo o (staged for gate|up with ffn_norm[l])
     p.xl = m->d_bo_hl;
     p.epi = EPI_RESID;
@@ -1080,7 +1189,8 @@ int copy_out(llm_model* m, void* dst, const void* src, size_t bytes, bool* host)
 
 // Pinned staging slots (ints of h_stage): the batch-1 token in, the status
 // word, and up to 32 tokens in and 32 choices out of a batched call.
-constexpr int kStageTok = 8, kStageStatus = 10, kStageToks = 128, kStageChoice = 160, kStageInts = 256;
+constexpr int kStageTok = 8, kStageStatus = 10, kStageToks = 128, kStageChoice = 160, kStageTree = 192, kStageInts = 256;
+static_assert(kStageTree + (int)(sizeof(TreeState::Out) / 4) <= kStageInts, "staging");
 
 // Whether a call's outputs include host memory: such a call ends with one
 // synchronization, so its small transfers can go through the pinned slots.
@@ -1707,6 +1817,18 @@ int llm_model_create(const llm_config* cfg, const llm_tensor* tensors, int32_t n
   AL(m->d_prompt, (size_t)c.max_seq * 4, "prompt");
   AL(m->d_samp, sizeof(SampleCfg), "sampling options");
   {
+    const size_t rows = (size_t)L * c.n_kv_heads * kBM * hd;
+    AL(m->d_tree_k, rows * (m->kv8 ? 1 : 2), "drafted K rows");
+    AL(m->d_tree_v, rows * (m->kv8 ? 1 : 2), "drafted V rows");
+    if (m->kv8) {
+      AL(m->d_tree_ks, rows / 32 * 2, "drafted K scales");
+      AL(m->d_tree_vs, rows / 32 * 2, "drafted V scales");
+    }
+    AL(m->d_tree_q, (size_t)kBM * m->q_dim * 4, "drafted queries");
+    AL(m->d_tree_o, (size_t)kBM * m->q_dim * 4, "drafted attention");
+    AL(m->d_tree, sizeof(TreeState), "drafted tree");
+  }
+  {
     const size_t pf = ((size_t)c.max_seq + kBM - 1) / kBM * kBM;  // prompt rows, whole chunks
     AL(m->d_pf, (3 * pf + 2 * kBM) * 4, "prompt chunk rows");
     m->pf_cap = pf;
@@ -1892,6 +2014,7 @@ int llm_set_sampling(llm_model* m, float temperature, int32_t top_k, float top_p
   h.seed_hi = (uint32_t)(seed >> 32);
   CK(cudaStreamSynchronize(m->stream), "sampling sync");  // no step in flight reads the options
   CK(cudaMemcpy(m->d_samp, &h, sizeof(h), cudaMemcpyHostToDevice), "sampling upload");
+  m->samp = h;
   const bool on = temperature > 0.f;
   if (on != m->sampling) {  // the captured steps gain or lose the sampling kernel: capture again
     for (auto& g : m->graphs)
@@ -1971,6 +2094,119 @@ int llm_decode_step_batch(llm_model* m, const int32_t* tokens, int32_t n_seq, fl
                         (size_t)n_seq)) != LLM_OK)
     return rc;
   if (tokens && !host) return check_status(m);
+  return LLM_OK;
+}
+
+int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int32_t* parents, int32_t n,
+                    const float* draft_probs, const float* uniforms, int32_t* path_out, int32_t* n_path_out,
+                    int32_t* next_out, float* logits_out) {
+  NvtxRange nvtx_("llm_decode_tree");
+  int rc = check_model(m, seq);
+  if (rc) return rc;
+  const llm_config& c = m->cfg;
+  if (!tokens || !parents || !path_out || !n_path_out || !next_out)
+    return set_err(m, LLM_ERR_INVALID_ARG, "null tokens, parents or outputs");
+  if (n < 1 || n > kBM) return set_err(m, LLM_ERR_UNSUPPORTED, "a tree has 1 to 32 nodes");
+  if (m->len[seq] + n > c.max_seq) return set_err(m, LLM_ERR_CTX_FULL, "the tree would exceed max_seq");
+  if (m->sampling && !uniforms) return set_err(m, LLM_ERR_INVALID_ARG, "sampled verification needs uniforms");
+  if (draft_probs && !m->sampling)
+    return set_err(m, LLM_ERR_INVALID_ARG, "draft_probs are for sampled verification (temperature > 0)");
+  if (draft_probs && !is_device_ptr(draft_probs))
+    return set_err(m, LLM_ERR_INVALID_ARG, "draft_probs must be device memory");
+  TreeState::In in{};  // (pageable copies are staged before the call returns to this frame's end: it synchronizes)
+  CK(cudaMemcpy(in.tok, tokens, (size_t)n * 4, cudaMemcpyDefault), "token read");
+  CK(cudaMemcpy(in.parent, parents, (size_t)n * 4, cudaMemcpyDefault), "parent read");
+  if (uniforms) CK(cudaMemcpy(in.u, uniforms, (size_t)n * 4, cudaMemcpyDefault), "uniform read");
+  for (int i = 0; i < n; ++i) {
+    if (in.tok[i] < 0 || in.tok[i] >= c.vocab) return set_err(m, LLM_ERR_INVALID_ARG, "token out of range");
+    if (i && (in.parent[i] < 0 || in.parent[i] >= i))
+      return set_err(m, LLM_ERR_INVALID_ARG, "a node's parent must be a lower node");
+    if (m->sampling && !(in.u[i] >= 0.f && in.u[i] < 1.f))
+      return set_err(m, LLM_ERR_INVALID_ARG, "uniforms must be in [0, 1)");
+    in.mask[i] = (i ? in.mask[in.parent[i]] : 0) | 1ull << i;
+    in.pos[i] = i ? in.pos[in.parent[i]] + 1 : m->len[seq];
+  }
+  in.parent[0] = -1;
+  TreeState* d = m->d_tree;
+  CK(cudaMemcpyAsync(&d->in, &in, sizeof(in), cudaMemcpyHostToDevice, m->stream), "tree upload");
+  BatchedIO io{};
+  io.M = n;
+  io.tok = d->in.tok;
+  io.pos = d->in.pos;
+  io.lm = true;
+  io.tok_io = d->tok_io;
+  io.argmax_out = d->argmax;
+  io.mask = d->in.mask;
+  io.tree_seq = seq;
+  CK(enqueue_batched(m, io), "tree launch");
+  bool host = false;
+  if ((rc = copy_out(m, logits_out, m->d_blogits, (size_t)n * c.vocab * 4, &host)) != LLM_OK) return rc;
+  const bool pdl = !(c.flags & LLM_NO_PDL);
+  VerifyParams vp{};
+  vp.pdl = pdl;
+  vp.tokens = d->in.tok;
+  vp.parents = d->in.parent;
+  vp.u = d->in.u;
+  vp.path = d->out.path;
+  vp.n_path = &d->out.n_path;
+  vp.next = &d->out.next;
+  vp.B = 1;
+  vp.n = n;
+  vp.V = c.vocab;
+  if (m->sampling) {
+    TokenProbsParams pp{};
+    pp.logits = m->d_blogits;
+    pp.probs = m->d_blogits;
+    pp.l_row = pp.p_row = c.vocab;
+    pp.R = n;
+    pp.V = c.vocab;
+    pp.c = (float)(1.4426950408889634 / (double)m->samp.temperature);
+    pp.top_k = m->samp.top_k;
+    pp.top_p = m->samp.top_p;
+    pp.status = m->d_status;
+    pp.pdl = pdl;
+    CK(launch_token_probs(pp, m->n_sm, m->stream), "token probabilities launch");
+    vp.p = m->d_blogits;
+    vp.q = draft_probs;
+    vp.p_node = vp.q_node = c.vocab;
+    vp.p_seq = vp.q_seq = (int64_t)n * c.vocab;
+  } else {
+    vp.targets = d->argmax;
+  }
+  CK(launch_verify_tree(vp, m->n_sm, m->stream), "verification launch");
+  TreeState::Out* out = reinterpret_cast<TreeState::Out*>(m->h_stage + kStageTree);
+  CK(cudaMemcpyAsync(out, &d->out, sizeof(*out), cudaMemcpyDeviceToHost, m->stream), "outcome read");
+  CK(cudaMemcpyAsync(m->h_stage + kStageStatus, m->d_status, 4, cudaMemcpyDeviceToHost, m->stream), "status read");
+  CK(cudaStreamSynchronize(m->stream), "tree sync");
+  // an error leaves the sequence as it was: nothing has gone into the cache
+  if ((rc = status_of(m, m->h_stage[kStageStatus])) != LLM_OK) return rc;
+  CommitParams cp{};
+  cp.cache = layer_rows(m, seq, 0, false);
+  cp.tree = layer_rows(m, 0, 0, true);
+  cp.c_layer = c.n_kv_heads * cp.cache.head;
+  cp.c_slayer = c.n_kv_heads * cp.cache.shead;
+  cp.t_layer = c.n_kv_heads * cp.tree.head;
+  cp.t_slayer = c.n_kv_heads * cp.tree.shead;
+  cp.lens = m->d_pos + seq;
+  cp.path = d->out.path;
+  cp.n_path = &d->out.n_path;
+  cp.new_lens = m->d_pos + seq;  // the position of the next token
+  cp.path_seq = n;
+  cp.B = 1;
+  cp.L = c.n_layers;
+  cp.Hkv = c.n_kv_heads;
+  cp.by_heads = FastDiv(c.n_kv_heads);
+  cp.n = n;
+  cp.row_bytes = c.head_dim * (m->kv8 ? 1 : 2);
+  cp.srow_bytes = m->kv8 ? c.head_dim / 16 : 0;
+  cp.pdl = pdl;
+  CK(launch_commit_tree(cp, m->stream), "commit launch");
+  CK(cudaMemcpyAsync(m->d_tok + seq, &d->out.next, 4, cudaMemcpyDeviceToDevice, m->stream), "next token");
+  CK(cudaMemcpyAsync(m->d_argmax + seq, &d->out.next, 4, cudaMemcpyDeviceToDevice, m->stream), "next token");
+  m->len[seq] += out->n_path;
+  CK(cudaMemcpy(path_out, out->path, (size_t)n * 4, cudaMemcpyDefault), "path copy");
+  CK(cudaMemcpy(n_path_out, &out->n_path, 4, cudaMemcpyDefault), "path copy");
+  CK(cudaMemcpy(next_out, &out->next, 4, cudaMemcpyDefault), "next token copy");
   return LLM_OK;
 }
 

@@ -889,7 +889,7 @@ cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t
     cudaError_t e = lim_s.raise(softmax_rows_kernel, (kProbSlice + 8) * 4);
     if (e == cudaSuccess && C > 8)
       e = cudaFuncSetAttribute(softmax_rows_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return e == cudaSuccess ? launch_cluster(softmax_rows_kernel, dim3(p.R * C), kSoftThreads, C, smem, st, p) : e;
+    return e == cudaSuccess ? launch_cluster(softmax_rows_kernel, dim3(p.R * C), kSoftThreads, C, smem, st, p, p.pdl) : e;
   }
   // the keys from the threshold on belong to at most top_k of the groups of 4 threads
   const int cand = kSampleMaxK * 4 * ((slice + kProbThreads - 1) / kProbThreads);
@@ -899,25 +899,25 @@ cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t
   if (e == cudaSuccess && C > 8)
     e = cudaFuncSetAttribute(topk_rows_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e == cudaSuccess
-             ? launch_cluster(topk_rows_kernel, dim3(p.R * C), kProbThreads, C, (slice + 4 + cand) * 4, st, q)
+             ? launch_cluster(topk_rows_kernel, dim3(p.R * C), kProbThreads, C, (slice + 4 + cand) * 4, st, q, p.pdl)
              : e;
 }
 
 cudaError_t launch_verify_tree(const VerifyParams& p, int n_sm, cudaStream_t st) {
   if (p.targets) {
-    return launch_cluster(verify_greedy_kernel, dim3(p.B), kTreeMaxNodes, 1, 0, st, p);
+    return launch_cluster(verify_greedy_kernel, dim3(p.B), kTreeMaxNodes, 1, 0, st, p, p.pdl);
   }
   int C = 1;
   while (C < 8 && p.V / (2 * C) >= 2 * kVerThreads) C *= 2;
-  return p.q ? launch_cluster(verify_kernel<true>, dim3(p.B * C), kVerThreads, C, 0, st, p)
-             : launch_cluster(verify_kernel<false>, dim3(p.B * C), kVerThreads, C, 0, st, p);
+  return p.q ? launch_cluster(verify_kernel<true>, dim3(p.B * C), kVerThreads, C, 0, st, p, p.pdl)
+             : launch_cluster(verify_kernel<false>, dim3(p.B * C), kVerThreads, C, 0, st, p, p.pdl);
 }
 
 cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st) {
   const int64_t rows = (int64_t)2 * p.L * p.Hkv * p.n, per = kCommitRows * 256 / (p.row_bytes / 16);
-  cudaError_t e = launch_cluster(commit_kernel, dim3((unsigned)((rows + per - 1) / per), p.B), 256, 1, 0, st, p);
+  cudaError_t e = launch_cluster(commit_kernel, dim3((unsigned)((rows + per - 1) / per), p.B), 256, 1, 0, st, p, p.pdl);
   if (e == cudaSuccess && p.new_lens == p.lens)  // every copy has read the lengths before they advance
-    e = launch_cluster(advance_kernel, dim3((p.B + 255) / 256), 256, 1, 0, st, p);
+    e = launch_cluster(advance_kernel, dim3((p.B + 255) / 256), 256, 1, 0, st, p, p.pdl);
   return e;
 }
 

@@ -41,21 +41,21 @@ class SmemLimit {
 // memory, in every thread, so stream order holds as without it.
 template <typename Kern, typename Params>
 cudaError_t launch_cluster(Kern kern, dim3 grid, int threads, int cluster, size_t smem, cudaStream_t st,
-                           const Params& p) {
+                           const Params& p, bool pdl = true) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -92,6 +92,7 @@ struct TreeAttnParams {
   int B, n, Hkv, gq;
   FastDiv by_gq;
   int S;                     // CTAs of a cluster: splits of the keys
+  bool pdl = true;           // launch as a programmatic dependent
   bool sorted;               // blocks take the sequences longest first
   int* status;               // the device's status word (bounded waits)
 };
@@ -109,6 +110,7 @@ struct TokenProbsParams {
   float c;                   // log2(e) / temperature
   int top_k;                 // 0: every token
   float top_p;
+  bool pdl = true;
   int cap = 0;               // set by the launch: floats of a slice
   int* status;               // the device's status word (bounded waits)
 };
@@ -123,6 +125,7 @@ struct VerifyParams {
   const int* targets;           // [B][n] greedy mode: the target's choice after each node (p null)
   int *path, *n_path, *next;
   int B, n, V;
+  bool pdl = true;
 };
 cudaError_t launch_verify_tree(const VerifyParams& p, int n_sm, cudaStream_t st);
 
@@ -133,6 +136,7 @@ struct CommitParams {
   int* new_lens;             // may be lens itself
   int64_t path_seq;
   FastDiv by_heads;
+  bool pdl = true;
   int B, L, Hkv, n, row_bytes, srow_bytes;  // bytes of a row of k or v, and of its scales (0: none)
 };
 cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st);

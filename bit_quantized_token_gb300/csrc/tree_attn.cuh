@@ -809,7 +809,7 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
     S *= 2;
   p.S = S;
   p.sorted = p.B > 1 && p.B <= 64;
-  return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, tp);
+  return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, tp, p.pdl);
 }
 
 // bf16 rows

@@ -483,6 +483,26 @@ int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n
                     const int32_t* lens, const int32_t* path, const int32_t* n_path, int32_t* new_lens,
                     void* cuda_stream);
 
+/* One decoding step of sequence seq over a drafted tree of n nodes (1..32):
+ * tokens[0] is the token that follows the cache (the last chosen one),
+ * parents[i] < i for every other node; both host or device. All nodes run
+ * through the batched pipeline at once (node i at position len + its depth,
+ * seeing the cache, its ancestors and itself), then the drafts are verified
+ * (llm_verify_tree): greedily, or with sampling on (llm_set_sampling) against
+ * the sampler's distribution with `uniforms` [n] in [0, 1) (host or device) and
+ * `draft_probs` [n][vocab] (device, or NULL: fixed choices). The kept nodes'
+ * K/V rows are appended and the sequence grows by their number. path_out [n]
+ * receives the kept nodes (then -1), n_path_out their number, next_out the
+ * token after them (the next tree's root), logits_out (may be NULL) the [n][vocab] logits of
+ * every node: host or device. Synchronous. With greedy choices the tokens are
+ * those of llm_decode_greedy within floating-point tolerance. An error leaves
+ * the sequence as it was. Errors: INVALID_ARG, UNSUPPORTED (n), CTX_FULL (len + n > max_seq),
+ * NAN, CUDA, TIMEOUT.
+ * Source: no page drafts tokens; the pipeline is llm_prefill_batched's. */
+int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int32_t* parents, int32_t n,
+                    const float* draft_probs, const float* uniforms, int32_t* path_out, int32_t* n_path_out,
+                    int32_t* next_out, float* logits_out);
+
 #ifdef __cplusplus
 }
 #endif
