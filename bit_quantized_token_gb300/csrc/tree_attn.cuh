@@ -21,13 +21,13 @@
 // rows the upper 64 read ones instead of V, so lanes 64.. hold the sums of P.
 // fp32 operands are parts in bf16 (24 bits in three, 16 in two): the parts of Q
 // and of P are columns of their own in one product each, so that A, whose fetch
-// from shared memory (4 KB, 32 cycles) bounds these narrow products, is fetched
-// once; the sums over the parts are formed on the way out.
-// Warp roles: 4 softmax warps per block of NB rows (G blocks share the units),
-// one TMA warp, one warp that issues every MMA. A block's next scores are
-// computed right after its P V, while the other block (or the other CTA on the
-// SM, where shared memory lets two fit) is in its softmax; a lone block has two
-// buffers of S and P and is a tile ahead with its scores.
+// from shared memory (4 KB, ~64 cycles) bounds these narrow products, is fetched
+// once; the sums over the parts are formed on the way out. So are the rows of
+// all G blocks: a block is what four softmax warps take, not a product.
+// Warp roles: 4 softmax warps per block of NB rows, one TMA warp, one warp that
+// issues every MMA. What a softmax waits for overlaps the other CTA on the SM,
+// where shared and tensor memory let two fit; S and P have two buffers where that
+// costs no second CTA, and the scores are then a tile ahead.
 #pragma once
 #include <cuda.h>
 
@@ -53,10 +53,11 @@ struct TreeTc {
   static constexpr int N = NB * G, BK = 128, H = HD / 64;
   static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : (N > 64 ? 1 : 2);  // parts of the queries, of P
   static constexpr int NS = NQ * NB, NO = NP * NB;                        // columns of a block's S, of its O (64 dims)
+  static constexpr int NSA = G * NS, NOA = G * NO;                        // of all blocks
   static constexpr int NT = 32 * (4 * G + 2);
   static constexpr int kUnit = BK * 128;                                  // bytes: 64 dims of a K or V tile
-  static constexpr int kRowP = NO >= 48 ? 128 : 2 * NO;                   // bytes of a key's row of a P atom (64 columns)
-  static constexpr int kPBlock = BK * kRowP * ((NO + 63) / 64);           // bytes of a block's P
+  static constexpr int kRowP = NOA >= 48 ? 128 : 2 * NOA;                 // bytes of a key's row of a P atom (64 columns)
+  static constexpr int kP = BK * kRowP * ((NOA + 63) / 64);               // bytes of P
   static constexpr int kQ = NQ * N * HD * 2, kOnes = 2048;
   static constexpr int kOffRow = 1024;                                   // of the small arrays: [N] row masks
   static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4) + 3 * kTreeMaxNodes * (HD / 32) * 4;
@@ -65,16 +66,17 @@ struct TreeTc {
   static constexpr int kLimit = 232448, kHalf = 115712;                  // shared memory of a CTA alone, of two on an SM
   // a tile's K and V units and, of 64 dims, the next K unit must fit
   static constexpr int kLeast = H == 1 ? 3 : 4, kMin = kLeast > kOut / kUnit ? kLeast : kOut / kUnit;
-  // One block of rows: S and P twice, so that the next scores are ready when a
-  // softmax ends (where two CTAs then still fit on an SM).
-  static constexpr int DB = G == 1 && kRest + 2 * kPBlock + kMin * kUnit <= kHalf ? 2 : 1;
-  static constexpr int kFixed = kRest + G * DB * kPBlock;
-  static constexpr bool two = kFixed + kMin * kUnit <= kHalf;
+  static constexpr bool two1 = kRest + kP + kMin * kUnit <= kHalf && NSA + H * NOA <= 256;
+  static constexpr bool two2 = kRest + 2 * kP + kMin * kUnit <= kHalf && 2 * NSA + H * NOA <= 256;
+  static constexpr bool one2 = kRest + 2 * kP + kMin * kUnit <= kLimit && 2 * NSA + H * NOA <= 512;
+  static constexpr int DB = two2 || (!two1 && one2) ? 2 : 1;             // buffers of S and P
+  static constexpr bool two = DB == 2 ? two2 : two1;                     // CTAs on an SM
+  static constexpr int kFixed = kRest + DB * kP;
   static constexpr int fit = ((two ? kHalf : kLimit) - kFixed) / kUnit;
   static constexpr int NST = fit < 12 ? fit : 12;
   static constexpr int kSmem = NST * kUnit + kFixed;
   static_assert(NST >= kMin, "shared memory");
-  static constexpr int kUsed = G * (DB * NS + H * NO);                   // S, and O of every 64 dims
+  static constexpr int kUsed = DB * NSA + H * NOA;                       // S, and O of every 64 dims
   static_assert(kUsed <= 512, "tensor memory");
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
@@ -264,30 +266,65 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, float* so, 
   __syncthreads();
   const int n4 = rows * HD / 4;
   const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
-  for (int i = i0 + tid; i < i1; i += NT) {
+  auto store = [&](int i, float4 a) {
     const int r = i / (HD / 4), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int k0 = 0; k0 < p.S; k0 += 8) {
-      float4 x[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < p.S) x[k] = reinterpret_cast<const float4*>(cl.map_shared_rank(so, k0 + k))[i];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k0 + k < p.S) {
-          const float f = sw[(k0 + k) * N + r];
-          a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y), a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
-        }
-    }
     const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % (HD / 4));
     if constexpr (F32)
       *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = a;
     else
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off) =
           make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  };
+  auto add = [&](float4& a, float4 x, float f) {
+    a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+  };
+  auto part = [&](int k, int i) { return reinterpret_cast<const float4*>(cl.map_shared_rank(so, k))[i]; };
+  // eight loads of a thread in flight: of eight ranks where it has one element,
+  // of two ranks where it has several
+  if (i1 - i0 <= NT) {
+    const int i = i0 + tid, r = min(i, n4 - 1) / (HD / 4);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < i1)
+#pragma unroll 1
+      for (int k0 = 0; k0 < p.S; k0 += 8) {
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k < p.S) x[k] = part(k0 + k, i);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k < p.S) add(a, x[k], sw[(k0 + k) * N + r]);
+      }
+    // a CTA's shared memory lives until every rank has read it
+    if (p.S > 1) {
+      auto read = cl.barrier_arrive();
+      if (i < i1) store(i, a);
+      cl.barrier_wait(std::move(read));
+    } else if (i < i1) {
+      store(i, a);
+    }
+    return;
   }
-  if (p.S > 1) cl.sync();  // a CTA's shared memory lives until every rank has read it
+#pragma unroll 1
+  for (int i = i0 + tid; i < i1; i += 4 * NT) {
+    float4 a[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < p.S; ++k) {
+      float4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u * NT < i1) x[u] = part(k, i + u * NT);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u * NT < i1) add(a[u], x[u], sw[k * N + (i + u * NT) / (HD / 4)]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * NT < i1) store(i + u * NT, a[u]);
+  }
+  if (p.S > 1) cl.sync();
 }
 
 template <int HD, bool F32, int NB, int G>
@@ -301,8 +338,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   uint8_t* sring = sm;
-  uint8_t* sp = sring + NST * C::kUnit;   // [DB][G] blocks of P: [atom of 64 columns][key][kRowP], columns part by part
-  uint8_t* sq = sp + DB * G * C::kPBlock;               // [H][G][NQ][NB][128 B]
+  uint8_t* sp = sring + NST * C::kUnit;   // [DB] P: [atom of 64 columns][key][kRowP], columns [block][part][row]
+  uint8_t* sq = sp + DB * C::kP;          // [H][G][NQ][NB][128 B]
   uint8_t* sones = sq + C::kQ;
   uint8_t* small = sones + C::kOnes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
@@ -318,7 +355,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   float* sfac = reinterpret_cast<float*>(sml + N);              // [N] rescaling of O and the sums
   uint32_t* snf = reinterpret_cast<uint32_t*>(sfac + N);        // [3][64][NG]
   float* sw = reinterpret_cast<float*>(sp);                     // [kMaxSplits][N] merge weights, when P is done with
-  static_assert(kMaxSplits * N * 4 <= DB * G * C::kPBlock, "merge weights");
+  static_assert(kMaxSplits * N * 4 <= DB * C::kP, "merge weights");
 
   // TMA: the units in the order in which the MMAs release them
   if (tid == 4 * G * 32) {
@@ -358,7 +395,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       for (int i = 0; i < NST && i < n_units; ++i) request(i);
   } else if (warp == 4 * G + 1) {
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
+      for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 * G);
+      mbar_init(o_done, 1);
       mbar_init(drain, 1);
       mbar_fence_init();
     }
@@ -407,7 +445,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;  // S of block g at columns g NS (buffer d: d NS), O of 64 dims u at DB G NS + (u G + g) NO
+  const uint32_t tmem = *s_tmem;  // S of block g and buffer d at columns (d G + g) NS, O of 64 dims u at DB G NS + (u G + g) NO
   uint64_t seen = 0;              // tree rows that some node sees
   if (p.tree.k) {
     const uint64_t a = smask[lane] | smask[lane + 32];
@@ -433,65 +471,61 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   } else if (warp == 4 * G + 1) {
     // ---- MMA: commits release units and publish scores
     constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 x bf16, 128 rows
-    constexpr uint32_t idesc_s = base_i | ((uint32_t)(C::NS >> 3) << 17);
-    constexpr uint32_t idesc_o = base_i | ((uint32_t)(C::NO >> 3) << 17) | (1u << 15) | (1u << 16);  // A and B MN-major
+    constexpr uint32_t idesc_s = base_i | ((uint32_t)(C::NSA >> 3) << 17);
+    constexpr uint32_t idesc_o = base_i | ((uint32_t)(C::NOA >> 3) << 17) | (1u << 15) | (1u << 16);  // A and B MN-major
     constexpr uint64_t swp = C::kRowP == 128 ? 2 : (C::kRowP == 64 ? 4 : 6);
     constexpr uint32_t step_p = 16 * C::kRowP, sbo_p = 8 * C::kRowP;
     const uint32_t uq = smem_u32(sq), up = smem_u32(sp), ur = smem_u32(sring), uo = smem_u32(sones);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    // block g's tile t0 + t: buffers and barriers x = g (DB 1) or t & 1 (DB 2)
-    auto scores = [&](int g, int t) {
-      const int x = DB == 2 ? t & 1 : g;
-#pragma unroll 1
-      for (int u = 0; u < H; ++u) {
-        const int i = k_unit(t) + u, slot = i % NST;
-        if (!tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status)) return false;
-        tc_fence_after();
-        const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
-        const uint64_t dq = tc_desc(uq + (u * G + g) * C::NS * 128, 16, 1024, 2);
-        if (elect_lane()) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
-            tc_mma(tm + x * C::NS, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
-        }
-        __syncwarp();
-        if (g == G - 1) tc_commit(empty + slot);
-      }
-      tc_commit(s_full + x);
-      return true;
-    };
     bool ok = true;
 #pragma unroll 1
-    for (int t = -DB; t < n_own && ok; ++t)
+    for (int t = -DB; t < n_own && ok; ++t) {
+      if (t >= 0) {  // O += V^T P^T of tile t0 + t, from buffer x
+        const int x = DB == 2 ? t & 1 : 0;
+        ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
 #pragma unroll 1
-      for (int g = 0; g < G && ok; ++g) {
-        if (t >= 0) {
-          const int x = DB == 2 ? t & 1 : g;
-          ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
-#pragma unroll 1
-          for (int u = 0; u < H; ++u) {
-            const int i = v_unit(t) + u, slot = i % NST;
-            ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v = ur + slot * C::kUnit;
-            // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
-            const uint64_t da = tc_desc(v, uo - v, 1024, 2);
-            const uint64_t dp = tc_desc(up + x * C::kPBlock, BK * 128, sbo_p, swp);
-            if (elect_lane()) {
-#pragma unroll
-              for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
-                tc_mma(tm + DB * G * C::NS + (u * G + g) * C::NO, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
-                       dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
-            }
-            __syncwarp();
-            if (g == G - 1) tc_commit(empty + slot);
-          }
+        for (int u = 0; u < H; ++u) {
+          const int i = v_unit(t) + u, slot = i % NST;
+          ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
           if (!ok) break;
-          tc_commit(o_done + g);
+          tc_fence_after();
+          const uint32_t v = ur + slot * C::kUnit;
+          // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
+          const uint64_t da = tc_desc(v, uo - v, 1024, 2);
+          const uint64_t dp = tc_desc(up + x * C::kP, BK * 128, sbo_p, swp);
+          if (elect_lane()) {
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
+              tc_mma(tm + DB * C::NSA + u * C::NOA, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                     dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
+          }
+          __syncwarp();
+          tc_commit(empty + slot);
         }
-        if (t + DB < n_own) ok = scores(g, t + DB);
+        if (!ok) break;
+        tc_commit(o_done);
       }
+      if (t + DB < n_own) {  // S of tile t0 + t + DB, into the buffer just read
+        const int x = DB == 2 ? t & 1 : 0;
+#pragma unroll 1
+        for (int u = 0; u < H; ++u) {
+          const int i = k_unit(t + DB) + u, slot = i % NST;
+          ok = tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
+          const uint64_t dq = tc_desc(uq + u * C::NSA * 128, 16, 1024, 2);
+          if (elect_lane()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
+              tc_mma(tm + x * C::NSA, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
+          }
+          __syncwarp();
+          tc_commit(empty + slot);
+        }
+        if (ok) tc_commit(s_full + x);
+      }
+    }
     if (!ok) {  // no MMA may outlive its operands
       tc_commit(drain);
       const unsigned long long s0 = globaltimer();
@@ -502,7 +536,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     // ---- softmax: thread = key
     const int g = warp >> 2, key = (warp & 3) * 32 + lane;
     uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * C::NS;
-    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + DB * G * C::NS + g * C::NO;  // of 64 dims u: + u G NO
+    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + DB * C::NSA + g * C::NO;  // of 64 dims u: + u NOA
     float* m = sm_m + g * NB;  // the references, negated
     const float masked = p.c < 0.f ? INFINITY : -INFINITY;  // times c: -inf (c is not 0)
     if (p.tree.k)
@@ -530,13 +564,13 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
       const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
       // these scores: this buffer's last P V is done too
-      const int x = DB == 2 ? (t - t0) & 1 : g;
+      const int x = DB == 2 ? (t - t0) & 1 : 0;
       tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
       tc_fence_after();
-      if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NS;
+      if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NSA + g * C::NS;
       if (!whole) {  // V rows that are not there become zeros, non-finite tree values too (noted for the rows that see them)
         // (after the last P V, so that the slot's last unit has been read and its barrier is in this unit's phase)
-        if (DB == 2 && t > t0) tc_wait(o_done + g, (t - t0 - 1) & 1, s_abort, p.status);
+        if (DB == 2 && t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
         for (int u = 0; u < H; ++u) {
           const int i = v_unit(t - t0) + u;
           tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
@@ -570,8 +604,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         }
       }
       if (t == t0) {  // the references: the score of the first key that a row sees (renewed below if not finite)
-        float* first = reinterpret_cast<float*>(sp + x * C::kPBlock);  // [64][NB], where P comes to lie
-        static_assert(64 * NB * 4 <= C::kPBlock, "room for the first scores");
+        float* first = reinterpret_cast<float*>(sp + x * C::kP) + g * 64 * NB;  // [64][NB], where P comes to lie
+        static_assert(64 * N * 4 <= C::kP, "room for the first scores");
         if (warp < 4 * g + (tree ? 2 : 1))
 #pragma unroll 1
           for (int c0 = 0; c0 < NB; c0 += W) {
@@ -591,9 +625,10 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           if (j >= 0) y = first[j * NB + key] * p.c;
           m[key] = fabsf(y) < 1e38f ? -y : -kNone;
         }
-        group_sync(g);
+        // every block's first scores have been read: P may be written
+        asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
       }
-      uint8_t* prow = sp + x * C::kPBlock + key * C::kRowP;
+      uint8_t* prow = sp + x * C::kP + key * C::kRowP;
       const int sel = C::kRowP == 128 ? key & 7 : (C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
       for (;;) {
         // probabilities with the references as they are; the largest excess over them
@@ -623,7 +658,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
             }
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-              const int chunk = (k * NB + c0 + 8 * h) / 8;
+              const int chunk = (g * C::NO + k * NB + c0 + 8 * h) / 8;
               *reinterpret_cast<uint4*>(prow + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ sel)) =
                   make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
             }
@@ -669,11 +704,11 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         }
         group_sync(g);
         if (t > t0) {
-          tc_wait(o_done + g, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V is in O
+          tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V is in O
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < C::NO * H; c0 += 16) {
-            const uint32_t at = tO + (c0 / C::NO) * G * C::NO + c0 % C::NO;
+            const uint32_t at = tO + (c0 / C::NO) * C::NOA + c0 % C::NO;
             float s[16];
             tc_ld(s, at);
             tc_wait_ld(s);
@@ -690,8 +725,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     }
     // ---- O^T and the sums to shared memory, [row][dim]
     // (one phase at a time: with two buffers the last but one P V may still run)
-    if (DB == 2 && n_own > 1) tc_wait(o_done + g, (n_own - 2) & 1, s_abort, p.status);
-    if (n_own > 0) tc_wait(o_done + g, (n_own - 1) & 1, s_abort, p.status);
+    if (DB == 2 && n_own > 1) tc_wait(o_done, (n_own - 2) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait(o_done, (n_own - 1) & 1, s_abort, p.status);
     tc_fence_after();
     // every block's last MMAs have read the ring and P before any block writes over them
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
@@ -703,10 +738,11 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       float s[NP][16];
       if (have) {
 #pragma unroll
-        for (int k = 0; k < NP; ++k) tc_ld(s[k], tO + u * G * C::NO + k * NB + r0);
+        for (int k = 0; k < NP; ++k) tc_ld(s[k], tO + u * C::NOA + k * NB + r0);
 #pragma unroll
         for (int k = 0; k < NP; ++k) tc_wait_ld(s[k]);
       }
+      float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         float x = 0.f;
@@ -714,8 +750,10 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 #pragma unroll
           for (int k = NP - 1; k >= 0; --k) x += s[k][j];
         if (key < 64) so[(r0 + j) * HD + 64 * u + key] = x;
-        if (u == 0 && key == 64) sml[g * NB + r0 + j] = make_float2(-m[r0 + j], x);
+        sum = lane == j ? x : sum;
       }
+      // the lanes from 64 on all hold the sums: lane j of the third warp keeps row j's
+      if (u == 0 && (warp & 3) == 2 && lane < 16) sml[g * NB + r0 + lane] = make_float2(-m[r0 + lane], sum);
     }
     if (p.tree.k && have && t1 == n_tiles && *s_any && key < 64) {  // non-finite tree values, where they are seen
       for (int d = key; d < HD; d += 64)
@@ -824,14 +862,12 @@ cudaError_t launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStre
   // (16 nodes x 8 heads over 4097 rows, fp32: 16 / 32 / 64 rows 16.5 / 18.6 / 20.6 us).
   // 128 rows at most: 256 fill tensor memory and leave one CTA on an SM (16 x 64
   // nodes over 1024..8192 rows: 119 against 109 us).
-  const int M = p.n * p.gq, most = f32 ? (HD == 64 ? 64 : 32) : 128;
+  const int M = p.n * p.gq, most = f32 ? 32 : 128;
   int N = 16;
   while (N < M && N < most) N *= 2;
   while (N > 16 && (int64_t)p.B * p.Hkv * ((M + N - 1) / N) * 8 < n_sm) N /= 2;
   if (f32)
-    return N == 16   ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st)
-           : N == 32 ? launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st)
-                     : launch_tree_tc_t<HD, true, HD == 64 ? 32 : 16, 2>(tp, n_sm, st);
+    return N == 16 ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st) : launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st);
   return N == 16   ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)
          : N == 32 ? launch_tree_tc_t<HD, false, 16, 2>(tp, n_sm, st)
          : N == 64 ? launch_tree_tc_t<HD, false, 32, 2>(tp, n_sm, st)
