@@ -840,10 +840,11 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   int S = 1;
   // Split the keys until every SM has a CTA; where two fit, also to fill both
   // places while 16 tiles are left for each: more splits cost their merges
+  // A lone CTA on an SM is not split beyond one wave (64 clusters of 33 tiles: 61 / 40 / 51).
   // (32 sequences x 8 kv heads, 17 tiles: 43 / 48 / 67 us for 1 / 2 / 4; 16 x 4 x 4 row
   // tiles, 65 tiles: 129 / 109 / 132; 8 clusters of 513 tiles: 667 / 340 / 179 / 96 for 1 to 8).
   while (S < kMaxSplits && S < tiles &&
-         (clusters * S < n_sm || (C::two && clusters * S < 2 * n_sm && tiles / (2 * S) >= 16)))
+         ((C::two ? clusters * S < n_sm : 2 * clusters * S <= n_sm) || (C::two && clusters * S < 2 * n_sm && tiles / (2 * S) >= 16)))
     S *= 2;
   p.S = S;
   p.sorted = p.B > 1 && p.B <= 64;

@@ -10,7 +10,7 @@
 // Codes are always finite and a row's scale meets only its own key's
 // probabilities, so what a node does not see cannot reach it.
 // Bound: conversion (a byte of HBM is two of shared memory written and read by the
-// MMAs) and the MMAs' fetch of it, 24 x 32 cycles a tile and block at 128 dims.
+// MMAs) and the MMAs' fetch of it, 24 x ~64 cycles a tile at 128 dims.
 #pragma once
 #include "tree_attn.cuh"
 
@@ -37,28 +37,29 @@ struct TreeQ8 {
   static constexpr int NB = 16, N = NB * G, BK = 128, H = HD / 64, NG = HD / 32;
   static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
   static constexpr int NS = NQ * NB, NO = NP * NB;   // columns of a group's S and O of a block
+  static constexpr int NSA = G * NS, NOA = G * NO;   // of all blocks: one product serves them
   static constexpr int NT = 32 * (4 * G + 8 + 2);
   static constexpr int kRaw = BK * HD, kConv = BK * HD * 2;              // bytes of a K or V tile: codes, bf16
-  static constexpr int kAtoms = (2 * NO + 63) / 64;                       // of 64 columns: P of the two groups of 64 dims
-  static constexpr int kRowP = NO >= 32 ? 128 : 4 * NO;
-  static constexpr int kPUnit = BK * kRowP * kAtoms, kPBlock = H * kPUnit;
+  static constexpr int kAtoms = (2 * NOA + 63) / 64;                      // of 64 columns: P of the two groups of 64 dims
+  static constexpr int kPUnit = BK * 128 * kAtoms, kP = H * kPUnit;
   static constexpr int kQ = NQ * N * HD * 2;
   static constexpr int kOffRow = 1024;
   static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4);
-  static constexpr int kFixed = 2 * kConv + G * kPBlock + kQ + kSmall + 1024;
+  static constexpr int kFixed = 2 * kConv + kP + kQ + kSmall + 1024;
   static constexpr int fit = (232448 - kFixed) / (2 * kRaw);
   static constexpr int R = fit < 4 ? fit : 4;                             // raw tiles of each of K and V
   static constexpr int kSmem = kFixed + 2 * R * kRaw;
-  static constexpr int kUsed = G * NG * (NS + NO);
+  static constexpr int DB = NG * (2 * NSA + NOA) <= 512 ? 2 : 1;         // buffers of S: the scores are a tile ahead
+  static constexpr int kUsed = NG * (DB * NSA + NOA);
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(R >= 2 && kUsed <= 512 && N * HD * 4 <= 2 * kConv && kMaxSplits * N * 4 <= kPBlock, "fits");
+  static_assert(R >= 2 && kUsed <= 512 && N * HD * 4 <= 2 * kConv && kMaxSplits * N * 4 <= kP, "fits");
 };
 
 template <int HD, bool F32, int G>
 __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel(const __grid_constant__ TreeAttnTcParams tp) {
   using C = TreeQ8<HD, F32, G>;
   constexpr int N = C::N, NT = C::NT, NB = C::NB, NQ = C::NQ, NP = C::NP, NG = C::NG, BK = C::BK, H = C::H, R = C::R;
-  constexpr int NS = C::NS, NO = C::NO, kConvWarp = 4 * G, kTmaWarp = 4 * G + 8, kMmaWarp = 4 * G + 9;
+  constexpr int NS = C::NS, NO = C::NO, NSA = C::NSA, NOA = C::NOA, DB = C::DB, kConvWarp = 4 * G, kTmaWarp = 4 * G + 8, kMmaWarp = 4 * G + 9;
   constexpr float kNone = -3e38f;
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
@@ -66,8 +67,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   uint8_t* sconv = sm;                        // K, V: [2][H][128 keys][128 B]
   uint8_t* sraw = sconv + 2 * C::kConv;       // [2][R] tiles of codes
-  uint8_t* sp = sraw + 2 * R * C::kRaw;       // [G][H] P of two groups
-  uint8_t* sq = sp + G * C::kPBlock;          // [H][G][NQ][NB][128 B]
+  uint8_t* sp = sraw + 2 * R * C::kRaw;       // [H] P of two groups: columns [group][block][part][row]
+  uint8_t* sq = sp + C::kP;                   // [H][G][NQ][NB][128 B]
   uint8_t* small = sq + C::kQ;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
   uint64_t *raw_full = bars, *raw_empty = bars + 8, *conv_full = bars + 16, *conv_empty = bars + 18, *s_full = bars + 20,
@@ -113,9 +114,9 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(conv_full + i, 128), mbar_init(conv_empty + i, 1);
-        mbar_init(s_full + i, 1), mbar_init(p_full + i, 128), mbar_init(o_done + i, 1);
+        mbar_init(s_full + i, 1);
       }
-      mbar_init(drain, 1);
+      mbar_init(p_full, 128 * G), mbar_init(o_done, 1), mbar_init(drain, 1);
       mbar_fence_init();
     }
     __syncwarp();
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;  // S of block g, group q at columns (g NG + q) NS; O of unit u at G NG NS + (u G + g) 2 NO
+  const uint32_t tmem = *s_tmem;  // S of buffer d, group q at columns (d NG + q) NSA; O of unit u at DB NG NSA + 2 u NOA
   uint64_t seen = 0;
   if (p.tree.k) {
     const uint64_t a = smask[lane] | smask[lane + 32];
@@ -186,55 +187,53 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
-    constexpr uint32_t idesc_s = base_i | ((uint32_t)(NS >> 3) << 17);
-    constexpr uint32_t idesc_o = base_i | ((uint32_t)(2 * NO >> 3) << 17) | (1u << 15) | (1u << 16);
+    constexpr uint32_t idesc_s = base_i | ((uint32_t)(NSA >> 3) << 17);
+    constexpr uint32_t idesc_o = base_i | ((uint32_t)(2 * NOA >> 3) << 17) | (1u << 15) | (1u << 16);
     const uint32_t uq = smem_u32(sq), up = smem_u32(sp), uk = smem_u32(sconv), uv = uk + C::kConv;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
 #pragma unroll 1
-    for (int t = -1; t < n_own && ok; ++t)
+    for (int t = -DB; t < n_own && ok; ++t) {
+      if (t >= 0) {
+        ok = tc_wait_warp(p_full, t & 1, s_abort, p.status) && tc_wait_warp(conv_full + 1, t & 1, s_abort, p.status);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-      for (int g = 0; g < G && ok; ++g) {
-        if (t >= 0) {
-          ok = tc_wait_warp(p_full + g, t & 1, s_abort, p.status) &&
-               tc_wait_warp(conv_full + 1, t & 1, s_abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int u = 0; u < H; ++u) {
-            // rows 64.. are whatever lies behind the unit: their products are not read
-            const uint64_t da = tc_desc(uv + u * BK * 128, BK * 128, 1024, 2);
-            const uint64_t dp = tc_desc(up + g * C::kPBlock + u * C::kPUnit, BK * 128, 1024, 2);
-            if (elect_lane()) {
+        for (int u = 0; u < H; ++u) {
+          // rows 64.. are whatever lies behind the unit: their products are not read
+          const uint64_t da = tc_desc(uv + u * BK * 128, BK * 128, 1024, 2);
+          const uint64_t dp = tc_desc(up + u * C::kPUnit, BK * 128, 1024, 2);
+          if (elect_lane()) {
 #pragma unroll
-              for (int ks = 0; ks < BK / 16; ++ks)
-                tc_mma(tm + G * NG * NS + (u * G + g) * 2 * NO, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o,
-                       t > 0 || ks > 0);
-            }
-            __syncwarp();
+            for (int ks = 0; ks < BK / 16; ++ks)
+              tc_mma(tm + DB * NG * NSA + u * 2 * NOA, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o,
+                     t > 0 || ks > 0);
           }
-          if (g == G - 1) tc_commit(conv_empty + 1);
-          tc_commit(o_done + g);
+          __syncwarp();
         }
-        if (t + 1 < n_own) {
-          ok = tc_wait_warp(conv_full, (t + 1) & 1, s_abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int u = 0; u < H; ++u) {
-            const uint64_t da = tc_desc(uk + u * BK * 128, 16, 1024, 2);
-            const uint64_t dq = tc_desc(uq + (u * G + g) * NS * 128, 16, 1024, 2);
-            if (elect_lane()) {
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                tc_mma(tm + (g * NG + 2 * u + ks / 2) * NS, da + 2 * ks, dq + 2 * ks, idesc_s, ks & 1);
-            }
-            __syncwarp();
-          }
-          if (g == G - 1) tc_commit(conv_empty);
-          tc_commit(s_full + g);
-        }
+        tc_commit(conv_empty + 1);
+        tc_commit(o_done);
       }
+      if (t + DB < n_own) {  // S of tile t0 + t + DB, into the buffer just read
+        const int x = DB == 2 ? t & 1 : 0;
+        ok = tc_wait_warp(conv_full, (t + DB) & 1, s_abort, p.status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int u = 0; u < H; ++u) {
+          const uint64_t da = tc_desc(uk + u * BK * 128, 16, 1024, 2);
+          const uint64_t dq = tc_desc(uq + u * NSA * 128, 16, 1024, 2);
+          if (elect_lane()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma(tm + (x * NG + 2 * u + ks / 2) * NSA, da + 2 * ks, dq + 2 * ks, idesc_s, ks & 1);
+          }
+          __syncwarp();
+        }
+        tc_commit(conv_empty);
+        tc_commit(s_full + x);
+      }
+    }
     if (!ok) {  // no MMA may outlive its operands
       tc_commit(drain);
       const unsigned long long s0 = globaltimer();
@@ -269,8 +268,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   } else {
     // ---- softmax: thread = key
     const int g = warp >> 2, key = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * NG * NS;
-    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + G * NG * NS + g * 2 * NO;  // of 64 dims u: + u G 2 NO
+    uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * NS;  // of group q: + q NSA
+    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + DB * NG * NSA + g * NO;  // of group q: + q NOA
     float* m = sm_m + g * NB;
     const float masked = p.c < 0.f ? INFINITY : -INFINITY;
     if (p.tree.k && key < NB) {
@@ -314,14 +313,16 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll
       for (int i = 0; i < 2 * NW; ++i) own[i] = sc[i];
       scales(t + 1);  // the next tile's are on their way meanwhile
-      tc_wait(s_full + g, (t - t0) & 1, s_abort, p.status);
+      const int x = DB == 2 ? (t - t0) & 1 : 0;
+      tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
       tc_fence_after();
+      if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * NG * NSA + g * NS;
       auto scores = [&](float (&s)[NB]) {
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
           float v[NQ][NB];
 #pragma unroll
-          for (int k = 0; k < NQ; ++k) tc_ld(v[k], tS + q * NS + k * NB);
+          for (int k = 0; k < NQ; ++k) tc_ld(v[k], tS + q * NSA + k * NB);
 #pragma unroll
           for (int k = 0; k < NQ; ++k) tc_wait_ld(v[k]);
           const float f = scale(own, q);
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         }
       };
       if (t == t0) {  // the references: the score of the first key that a row sees
-        float* first = reinterpret_cast<float*>(sp + g * C::kPBlock);  // [64][NB], where P comes to lie
+        float* first = reinterpret_cast<float*>(sp) + g * 64 * NB;  // [64][NB], where P comes to lie
         if (warp < 4 * g + (tree ? 2 : 1)) {
           float s[NB];
           scores(s);
@@ -349,9 +350,10 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
           if (j >= 0) y = first[j * NB + key] * p.c;
           m[key] = fabsf(y) < 1e38f ? -y : -kNone;
         }
-        group_sync(g);
+        // every block's first scores have been read: P may be written
+        asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
       }
-      uint8_t* prow = sp + g * C::kPBlock + key * 128;
+      uint8_t* prow = sp + key * 128;
       for (;;) {
         float s[NB];
         scores(s);
@@ -391,11 +393,11 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll
           for (int j = 0; j < NB; ++j) l[j] *= sfac[g * NB + j];
           if (t > t0) {
-            tc_wait(o_done + g, (t - t0 - 1) & 1, s_abort, p.status);
+            tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < 2 * NO * H; c0 += 16) {
-              const uint32_t at = tO + (c0 / (2 * NO)) * G * 2 * NO + c0 % (2 * NO);
+            for (int c0 = 0; c0 < NO * NG; c0 += 16) {
+              const uint32_t at = tO + (c0 / NO) * NOA + c0 % NO;
               float o[16];
               tc_ld(o, at);
               tc_wait_ld(o);
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) l[j] += s[j];
-        if (t > t0) tc_wait(o_done + g, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V has read P
+        if (t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V has read P
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
           const float f = scale(own, NG + q);
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
             }
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-              const int chunk = ((q & 1) * NO + k * NB + 8 * h) / 8;
+              const int chunk = ((q & 1) * NOA + g * NO + k * NB + 8 * h) / 8;
               *reinterpret_cast<uint4*>(prow + (q >> 1) * C::kPUnit + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ (key & 7))) =
                   make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
             }
@@ -433,10 +435,10 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       }
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(p_full + g);
+      mbar_arrive(p_full);
     }
     // ---- O^T and the sums to shared memory, [row][dim]
-    if (n_own > 0) tc_wait(o_done + g, (n_own - 1) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait(o_done, (n_own - 1) & 1, s_abort, p.status);
     tc_fence_after();
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");  // every block's MMAs have read the tiles
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         float o[NP][NB];
         if (n_own > 0) {
 #pragma unroll
-          for (int k = 0; k < NP; ++k) tc_ld(o[k], tO + u * G * 2 * NO + (warp & 1) * NO + k * NB);
+          for (int k = 0; k < NP; ++k) tc_ld(o[k], tO + (2 * u + (warp & 1)) * NOA + k * NB);
 #pragma unroll
           for (int k = 0; k < NP; ++k) tc_wait_ld(o[k]);
         }
