@@ -190,11 +190,14 @@ __device__ __forceinline__ void split_pack(float a, float b, uint32_t (&part)[NP
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     part[k] = pack_bf16x2(a, b);
-    if (k + 1 < NP) {
-      a -= __uint_as_float(part[k] << 16);
-      b -= __uint_as_float(part[k] & 0xFFFF0000u);
-    }
+    if (k + 1 < NP) sub2(a, b, a, b, __uint_as_float(part[k] << 16), __uint_as_float(part[k] & 0xFFFF0000u));
   }
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+      "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b));
 }
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;

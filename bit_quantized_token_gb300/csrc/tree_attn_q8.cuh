@@ -327,9 +327,12 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
           for (int k = 0; k < NQ; ++k) tc_wait_ld(v[k]);
           const float f = scale(own, q);
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const float x = NQ == 3 ? v[0][j] + (v[1 % NQ][j] + v[2 % NQ][j]) : v[0][j];
-            s[j] = q == 0 ? x * f : fmaf(x, f, s[j]);
+          for (int j = 0; j < NB; j += 2) {
+            float x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[i] = NQ == 3 ? v[0][j + i] + (v[1 % NQ][j + i] + v[2 % NQ][j + i]) : v[0][j + i];
+            if (q == 0) mul2(s[j], s[j + 1], x[0], x[1], f);
+            else fma2(s[j], s[j + 1], x[0], x[1], f, f);
           }
         }
       };
@@ -367,9 +370,14 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         }
         float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          s[j] = ex2(fmaf(s[j], p.c, m[j]));
-          top = fmaxf(top, s[j]);
+        for (int j = 0; j < NB; j += 4) {
+          const float4 ref = *reinterpret_cast<const float4*>(m + j);
+          float y[4] = {ref.x, ref.y, ref.z, ref.w};
+          fma2(y[0], y[1], s[j], s[j + 1], p.c, p.c);
+          fma2(y[2], y[3], s[j + 2], s[j + 3], p.c, p.c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[j + i] = ex2(y[i]);
+          top = fmaxf(top, fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
         }
         if (group_any(g, top > 1152921504606846976.f)) {  // 2^60 past the references: renew them
           float z[NB];
@@ -412,16 +420,26 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll
         for (int j = 0; j < NB; ++j) l[j] += s[j];
         if (t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V has read P
+        // a masked key's scale may be anything: its probabilities stay 0
+        float f[NG];
+        bool odd = false;
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
-          const float f = scale(own, NG + q);
+          f[q] = scale(own, NG + q);
+          odd |= !(fabsf(f[q]) <= 65504.f);
+        }
+        const bool any_odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t part[4][NP];
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {  // (a masked key's scale may be anything)
-              const float a = s[8 * h + j], d = s[8 * h + j + 1];
-              split_pack<NP>(a == 0.f ? 0.f : a * f, d == 0.f ? 0.f : d * f, part[j / 2]);
+            for (int j = 0; j < 8; j += 2) {
+              float a, d;
+              mul2(a, d, s[8 * h + j], s[8 * h + j + 1], f[q]);
+              if (any_odd) a = s[8 * h + j] == 0.f ? 0.f : a, d = s[8 * h + j + 1] == 0.f ? 0.f : d;
+              split_pack<NP>(a, d, part[j / 2]);
             }
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
