@@ -35,6 +35,40 @@ class SmemLimit {
   std::atomic<uint64_t> done_{0};
 };
 
+// How many clusters of `size` CTAs (a power of two up to 16) the device runs at
+// once, asked once per device and size.
+class ClusterCount {
+ public:
+  template <typename Kern>
+  int get(Kern kern, int size, int threads, size_t smem) {
+    int dev = 0, lg = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    while ((1 << lg) < size) ++lg;
+    std::atomic<int>* slot = dev < kDevices ? &n_[dev][lg] : nullptr;
+    if (slot && (n = slot->load(std::memory_order_relaxed))) return n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    n = n > 0 ? n : -1;
+    if (slot) slot->store(n, std::memory_order_relaxed);
+    return n;
+  }
+
+ private:
+  static constexpr int kDevices = 16;
+  std::atomic<int> n_[kDevices][5] = {};
+};
+
 // Launch in clusters along x (of one CTA: none), as a programmatic dependent:
 // the launch and a kernel's set-up overlap the end of the kernel before it. Every
 // kernel launched so waits (griddepcontrol) before its first access to global

@@ -199,6 +199,12 @@ __device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, f
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b));
 }
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -829,6 +835,24 @@ bool encode_all(TreeAttnTcParams& tp) {
                                  encode_rows<HD, Q8>(&tp.tv, p.tree.v, p.tree, p.B, p.Hkv));
 }
 
+// Splits of a cluster's keys where a CTA has an SM to itself: least waves of
+// clusters (those of 8 and 16 leave SMs of a processing cluster over) times a CTA's
+// tiles and its start and join, about five tiles' time. Measured, us for 1, 2, 4,
+// 8, 16: 64 clusters of 33 bf16 tiles 61 / 40 / 51; int8, 8 of 33 66 / 41 / 29 / 23 / 33,
+// 16 of 129 221 / 119 / 68 / 77 / 76, 24 of 72 83 / 50 / 33 / 41 / 61.
+template <typename AtOnce>
+int lone_splits(int64_t clusters, int tiles, AtOnce at_once) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= kMaxSplits && s <= tiles; s *= 2) {
+    const int n = at_once(s);
+    if (n <= 0) continue;
+    const int64_t t = (clusters + n - 1) / n * ((tiles + s - 1) / s + 5);
+    if (t < least) least = t, best = s;
+  }
+  return best;
+}
+
 template <int HD, bool F32, int NB, int G>
 cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   using C = TreeTc<HD, F32, NB, G>;
@@ -841,14 +865,16 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
   int S = 1;
-  // Split the keys until every SM has a CTA; where two fit, also to fill both
-  // places while 16 tiles are left for each: more splits cost their merges
-  // A lone CTA on an SM is not split beyond one wave (64 clusters of 33 tiles: 61 / 40 / 51).
-  // (32 sequences x 8 kv heads, 17 tiles: 43 / 48 / 67 us for 1 / 2 / 4; 16 x 4 x 4 row
-  // tiles, 65 tiles: 129 / 109 / 132; 8 clusters of 513 tiles: 667 / 340 / 179 / 96 for 1 to 8).
-  while (S < kMaxSplits && S < tiles &&
-         ((C::two ? clusters * S < n_sm : 2 * clusters * S <= n_sm) || (C::two && clusters * S < 2 * n_sm && tiles / (2 * S) >= 16)))
-    S *= 2;
+  if constexpr (C::two) {
+    // Split the keys until every SM has a CTA, and to fill both places while 16
+    // tiles are left for each: more splits cost their merges
+    // (32 sequences x 8 kv heads, 17 tiles: 43 / 48 / 67 us for 1 / 2 / 4; 16 x 4 x 4 row
+    // tiles, 65 tiles: 129 / 109 / 132; 8 clusters of 513 tiles: 667 / 340 / 179 / 96 for 1 to 8).
+    while (S < kMaxSplits && S < tiles && (clusters * S < n_sm || (clusters * S < 2 * n_sm && tiles / (2 * S) >= 16))) S *= 2;
+  } else {
+    static ClusterCount at_once;
+    S = lone_splits(clusters, tiles, [&](int s) { return at_once.get(kern, s, C::NT, C::kSmem); });
+  }
   p.S = S;
   p.sorted = p.B > 1 && p.B <= 64;
   return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, tp, p.pdl);

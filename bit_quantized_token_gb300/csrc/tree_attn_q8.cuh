@@ -1,16 +1,17 @@
 // Tree attention over int8 rows with a scale per 32 values, on the tensor cores
 // (the products, roles and references of tree_attn.cuh; what differs:)
-// - Eight converter warps widen the codes, which TMA brings as they are, to bf16
-//   (exact): four for the K tiles, four for the V tiles.
+// - Converter warps widen the codes, which TMA brings as they are, to bf16: four
+//   for the K tiles (exact), eight for the V tiles.
 // - S^T of each group of 32 dims has columns of its own; the softmax thread, which
 //   is one key, adds them with its key's scales: s = sum_g ks_g S_g.
-// - A value's scale goes to the probabilities, p vs_g, so P has columns for every
-//   group; of a 64-dim product's 128 rows, 32 belong to each of the two groups.
-//   The sums of p itself are the threads' own (16 rows a block), added at the end.
-// Codes are always finite and a row's scale meets only its own key's
-// probabilities, so what a node does not see cannot reach it.
-// Bound: conversion (a byte of HBM is two of shared memory written and read by the
-// MMAs) and the MMAs' fetch of it, 24 x ~64 cycles a tile at 128 dims.
+// - A value is its code times its scale, 8 + 11 bits, in two bf16 parts (16 bits;
+//   fp32 queries: three, exact), each a tile of its own. A form with the scales in
+//   the probabilities, P for every group, took twice the time: the softmax wrote
+//   four times as much, and three quarters of the product were not used.
+// - The sums of p are the threads' own (16 rows a block), added at the end.
+// A non-finite scale of a tree row is left out of the products and added at the
+// end for the nodes that see the row.
+#pragma once
 #pragma once
 #include "tree_attn.cuh"
 
@@ -32,47 +33,86 @@ __device__ __forceinline__ uint2 i8x4_to_bf16(uint32_t w) {
   return make_uint2(r[0], r[1]);
 }
 
+// Loads that stay where they are written, a tile ahead of their use (the
+// compiler moves plain read-only ones down to it).
+__device__ __forceinline__ uint2 ld_early2(const uint16_t* at) {
+  uint2 w;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(at) : "memory");
+  return w;
+}
+__device__ __forceinline__ uint32_t ld_early(const uint16_t* at) {
+  uint32_t w;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w) : "l"(at) : "memory");
+  return w;
+}
+__device__ __forceinline__ uint32_t ld_early_half(const uint16_t* at) {
+  uint16_t w;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(w) : "l"(at) : "memory");
+  return w;
+}
+// Four int8 codes times f as NP bf16 parts each: out[k] has part k of the four.
+// (In bf16 arithmetic, c a rounded and the exact rest c a - hi + c b with a + b = f,
+// it took fewer instructions and 8 % more time.)
+template <int NP>
+__device__ __forceinline__ void i8x4_scaled(uint32_t w, float f, uint2 (&out)[NP]) {
+  w ^= 0x80808080u;
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + i));  // 2^23 + 128 + code
+  uint32_t a[NP], b[NP];
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    sub2(x[i], x[i + 1], x[i], x[i + 1], 8388736.f, 8388736.f);
+    mul2(x[i], x[i + 1], x[i], x[i + 1], f);
+  }
+  split_pack<NP>(x[0], x[1], a);
+  split_pack<NP>(x[2], x[3], b);
+#pragma unroll
+  for (int k = 0; k < NP; ++k) out[k] = make_uint2(a[k], b[k]);
+}
+
 template <int HD, bool F32, int G>
 struct TreeQ8 {
   static constexpr int NB = 16, N = NB * G, BK = 128, H = HD / 64, NG = HD / 32;
   static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
   static constexpr int NS = NQ * NB, NO = NP * NB;   // columns of a group's S and O of a block
   static constexpr int NSA = G * NS, NOA = G * NO;   // of all blocks: one product serves them
-  static constexpr int NT = 32 * (4 * G + 8 + 2);
+  static constexpr int NT = 32 * (4 * G + 12 + 2);
   static constexpr int kRaw = BK * HD, kConv = BK * HD * 2;              // bytes of a K or V tile: codes, bf16
-  static constexpr int kAtoms = (2 * NOA + 63) / 64;                      // of 64 columns: P of the two groups of 64 dims
-  static constexpr int kPUnit = BK * 128 * kAtoms, kP = H * kPUnit;
+  static constexpr int kP = (NOA + 63) / 64 * BK * 128;                   // atoms of 64 columns
   static constexpr int kQ = NQ * N * HD * 2;
   static constexpr int kOffRow = 1024;
   static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4);
-  static constexpr int kFixed = 2 * kConv + kP + kQ + kSmall + 1024;
+  static constexpr int PB = (1 + NP) * kConv + 2 * kP + kQ + kSmall + 1024 + 4 * kRaw <= 232448 ? 2 : 1;  // buffers of P
+  static constexpr int kFixed = (1 + NP) * kConv + PB * kP + kQ + kSmall + 1024;
   static constexpr int fit = (232448 - kFixed) / (2 * kRaw);
   static constexpr int R = fit < 4 ? fit : 4;                             // raw tiles of each of K and V
   static constexpr int kSmem = kFixed + 2 * R * kRaw;
-  static constexpr int DB = NG * (2 * NSA + NOA) <= 512 ? 2 : 1;         // buffers of S: the scores are a tile ahead
-  static constexpr int kUsed = NG * (DB * NSA + NOA);
+  static constexpr int kUsed = 2 * NG * NSA + NOA;                        // two buffers of S: the scores are a tile ahead
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(R >= 2 && kUsed <= 512 && N * HD * 4 <= 2 * kConv && kMaxSplits * N * 4 <= kP, "fits");
+  static_assert(R >= 2 && kUsed <= 512 && N * HD * 4 <= 2 * kConv && kMaxSplits * N * 4 <= kP && G * 4096 <= kP, "fits");
 };
 
 template <int HD, bool F32, int G>
 __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel(const __grid_constant__ TreeAttnTcParams tp) {
   using C = TreeQ8<HD, F32, G>;
   constexpr int N = C::N, NT = C::NT, NB = C::NB, NQ = C::NQ, NP = C::NP, NG = C::NG, BK = C::BK, H = C::H, R = C::R;
-  constexpr int NS = C::NS, NO = C::NO, NSA = C::NSA, NOA = C::NOA, DB = C::DB, kConvWarp = 4 * G, kTmaWarp = 4 * G + 8, kMmaWarp = 4 * G + 9;
+  constexpr int NS = C::NS, NO = C::NO, NSA = C::NSA, NOA = C::NOA, PB = C::PB;
+  constexpr int kConvWarp = 4 * G, kTmaWarp = 4 * G + 12, kMmaWarp = 4 * G + 13;
   constexpr float kNone = -3e38f;
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  uint8_t* sconv = sm;                        // K, V: [2][H][128 keys][128 B]
-  uint8_t* sraw = sconv + 2 * C::kConv;       // [2][R] tiles of codes
-  uint8_t* sp = sraw + 2 * R * C::kRaw;       // [H] P of two groups: columns [group][block][part][row]
-  uint8_t* sq = sp + C::kP;                   // [H][G][NQ][NB][128 B]
+  uint8_t* sconv = sm;                        // K, V's parts: [1 + NP][H][128 keys][128 B]
+  uint8_t* sraw = sconv + (1 + NP) * C::kConv;  // [2][R] tiles of codes
+  uint8_t* sp = sraw + 2 * R * C::kRaw;       // [PB] P: columns [block][part][row]
+  uint8_t* sq = sp + PB * C::kP;                   // [H][G][NQ][NB][128 B]
   uint8_t* small = sq + C::kQ;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
   uint64_t *raw_full = bars, *raw_empty = bars + 8, *conv_full = bars + 16, *conv_empty = bars + 18, *s_full = bars + 20,
            *p_full = bars + 22, *o_done = bars + 24, *drain = bars + 26;  // [2][4], then pairs
+  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(small + 272);  // tree rows with a non-finite scale of V
   volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 264);
   uint64_t* smask = reinterpret_cast<uint64_t*>(small + 512);        // [64]
@@ -85,7 +125,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 
   if (tid == 32 * kTmaWarp) {
     *s_abort = 0;
-    for (int i = 0; i < 8; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, 128);
+    *s_bad = 0;
+    for (int i = 0; i < 8; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, i < 4 ? 128 : 256);
     mbar_fence_init();
   }
   pdl_wait();
@@ -113,10 +154,10 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(conv_full + i, 128), mbar_init(conv_empty + i, 1);
-        mbar_init(s_full + i, 1);
+        mbar_init(conv_full + i, i ? 256 : 128), mbar_init(conv_empty + i, 1);
+        mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 * G), mbar_init(o_done + i, 1);
       }
-      mbar_init(p_full, 128 * G), mbar_init(o_done, 1), mbar_init(drain, 1);
+      mbar_init(drain, 1);
       mbar_fence_init();
     }
     __syncwarp();
@@ -125,7 +166,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   } else {
-    const int th = tid, nth = 32 * (4 * G + 8);
+    const int th = tid, nth = 32 * (4 * G + 12);
     if (p.tree.k)
       for (int i = th; i < kTreeMaxNodes; i += nth) smask[i] = i < cnt ? p.mask[(int64_t)b * p.mask_seq + i] : 0;
 #pragma unroll 1
@@ -158,7 +199,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;  // S of buffer d, group q at columns (d NG + q) NSA; O of unit u at DB NG NSA + 2 u NOA
+  const uint32_t tmem = *s_tmem;  // S of buffer d, group q at columns (d NG + q) NSA; O behind them
   uint64_t seen = 0;
   if (p.tree.k) {
     const uint64_t a = smask[lane] | smask[lane + 32];
@@ -188,35 +229,35 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   } else if (warp == kMmaWarp) {
     constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
     constexpr uint32_t idesc_s = base_i | ((uint32_t)(NSA >> 3) << 17);
-    constexpr uint32_t idesc_o = base_i | ((uint32_t)(2 * NOA >> 3) << 17) | (1u << 15) | (1u << 16);
+    constexpr uint32_t idesc_o = base_i | ((uint32_t)(NOA >> 3) << 17) | (1u << 15) | (1u << 16);
     const uint32_t uq = smem_u32(sq), up = smem_u32(sp), uk = smem_u32(sconv), uv = uk + C::kConv;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
 #pragma unroll 1
-    for (int t = -DB; t < n_own && ok; ++t) {
+    for (int t = -2; t < n_own && ok; ++t) {
       if (t >= 0) {
-        ok = tc_wait_warp(p_full, t & 1, s_abort, p.status) && tc_wait_warp(conv_full + 1, t & 1, s_abort, p.status);
+        const int y = t % PB;
+        ok = tc_wait_warp(p_full + y, (t / PB) & 1, s_abort, p.status) && tc_wait_warp(conv_full + 1, t & 1, s_abort, p.status);
         if (!ok) break;
         tc_fence_after();
+        const uint64_t dp = tc_desc(up + y * C::kP, BK * 128, 1024, 2);
 #pragma unroll 1
-        for (int u = 0; u < H; ++u) {
-          // rows 64.. are whatever lies behind the unit: their products are not read
-          const uint64_t da = tc_desc(uv + u * BK * 128, BK * 128, 1024, 2);
-          const uint64_t dp = tc_desc(up + u * C::kPUnit, BK * 128, 1024, 2);
+        for (int k = 0; k < NP; ++k) {
+          // at 64 dims, rows 64.. are whatever lies behind the part: their products are not read
+          const uint64_t da = tc_desc(uv + k * C::kConv, BK * 128, 1024, 2);
           if (elect_lane()) {
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-              tc_mma(tm + DB * NG * NSA + u * 2 * NOA, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o,
-                     t > 0 || ks > 0);
+              tc_mma(tm + 2 * NG * NSA, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o, t > 0 || k > 0 || ks > 0);
           }
           __syncwarp();
         }
         tc_commit(conv_empty + 1);
-        tc_commit(o_done);
+        tc_commit(o_done + y);
       }
-      if (t + DB < n_own) {  // S of tile t0 + t + DB, into the buffer just read
-        const int x = DB == 2 ? t & 1 : 0;
-        ok = tc_wait_warp(conv_full, (t + DB) & 1, s_abort, p.status);
+      if (t + 2 < n_own) {  // S of tile t0 + t + 2, into the buffer just read
+        const int x = t & 1;
+        ok = tc_wait_warp(conv_full, t & 1, s_abort, p.status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -241,35 +282,89 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       }
     }
   } else if (warp >= kConvWarp) {
-    // ---- converters: thread = row of the K (kv 0) or V tile
-    const int kv = (warp - kConvWarp) >> 2, r = (warp & 3) * 32 + lane;
-    uint8_t* conv = sconv + kv * C::kConv + r * 128;
+    // ---- converters. K: thread = row; V: thread = half a row
+    // A slot of codes is given back behind the proxy fence: the copy that fills it
+    // next is of the other proxy, and an arrival alone does not order these reads
+    // before it (without the fence, codes of four tiles on were met).
+    const bool of_v = warp >= kConvWarp + 4;
+    const int r = (warp & 3) * 32 + lane;
     const int sel = HD == 128 ? r & 7 : (r >> 1) & 3;
+    if (!of_v) {
+      uint8_t* conv = sconv + r * 128;
 #pragma unroll 1
-    for (int t = 0; t < n_own; ++t) {
-      const int slot = t % R;
-      tc_wait(raw_full + 4 * kv + slot, (t / R) & 1, s_abort, p.status);
-      const uint8_t* raw = sraw + (kv * R + slot) * C::kRaw + r * HD;
-      uint4 w[HD / 16];
+      for (int t = 0; t < n_own; ++t) {
+        const int slot = t % R;
+        tc_wait(raw_full + slot, (t / R) & 1, s_abort, p.status);
+        const uint8_t* raw = sraw + slot * C::kRaw + r * HD;
+        uint4 w[HD / 16];
 #pragma unroll
-      for (int c = 0; c < HD / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + 16 * (c ^ sel));
-      mbar_arrive(raw_empty + 4 * kv + slot);
-      if (t > 0) tc_wait(conv_empty + kv, (t - 1) & 1, s_abort, p.status);
+        for (int c = 0; c < HD / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + 16 * (c ^ sel));
+        if (t > 0) tc_wait(conv_empty, (t - 1) & 1, s_abort, p.status);
 #pragma unroll
-      for (int c = 0; c < HD / 16; ++c) {
-        const uint2 a = i8x4_to_bf16(w[c].x), d = i8x4_to_bf16(w[c].y), e = i8x4_to_bf16(w[c].z), f = i8x4_to_bf16(w[c].w);
-        uint8_t* dst = conv + (c / 4) * BK * 128;
-        *reinterpret_cast<uint4*>(dst + 16 * ((2 * (c & 3)) ^ (r & 7))) = make_uint4(a.x, a.y, d.x, d.y);
-        *reinterpret_cast<uint4*>(dst + 16 * ((2 * (c & 3) + 1) ^ (r & 7))) = make_uint4(e.x, e.y, f.x, f.y);
+        for (int c = 0; c < HD / 16; ++c) {
+          const uint2 a = i8x4_to_bf16(w[c].x), d = i8x4_to_bf16(w[c].y), e = i8x4_to_bf16(w[c].z), f = i8x4_to_bf16(w[c].w);
+          uint8_t* dst = conv + (c / 4) * BK * 128;
+          *reinterpret_cast<uint4*>(dst + 16 * ((2 * (c & 3)) ^ (r & 7))) = make_uint4(a.x, a.y, d.x, d.y);
+          *reinterpret_cast<uint4*>(dst + 16 * ((2 * (c & 3) + 1) ^ (r & 7))) = make_uint4(e.x, e.y, f.x, f.y);
+        }
+        fence_async_smem();
+        mbar_arrive(raw_empty + slot);
+        mbar_arrive(conv_full);
       }
-      fence_async_smem();
-      mbar_arrive(conv_full + kv);
+    } else {
+      constexpr int NC = HD / 32;  // chunks of 16 codes a thread
+      const int half = warp >= kConvWarp + 8;
+      uint8_t* conv = sconv + C::kConv + (HD == 128 ? half * BK * 128 : 0) + r * 128;
+      // the scales of the thread's codes (of one or two groups) in tile t: two halves a word
+      auto scales = [&](int t) -> uint32_t {
+        const bool tree = t >= n_pre;
+        if (t >= t1 || !(tree ? r < kTreeMaxNodes && ((seen >> (r & 63)) & 1) : t * BK + r < len)) return 0;  // no such row
+        const KvRows& rw = tree ? p.tree : p.cache;
+        const uint16_t* at = rw.vs + (int64_t)b * rw.sseq + (int64_t)hkv * rw.shead + (int64_t)(tree ? r : t * BK + r) * rw.srow;
+        return HD == 128 ? ld_early(at + 2 * half) : ld_early_half(at + half);
+      };
+      uint32_t next = scales(t0);
+#pragma unroll 1
+      for (int t = 0; t < n_own; ++t) {
+        const int slot = t % R;
+        uint32_t own = next;
+        next = scales(t0 + t + 1);
+        if (t0 + t >= n_pre) {  // the tree's
+          const bool b0 = (own & 0x7C00u) == 0x7C00u, b1 = (own & 0x7C000000u) == 0x7C000000u;
+          if (b0 || b1) atomicOr(s_bad, 1ull << r);
+          own &= (b0 ? 0xFFFF0000u : ~0u) & (b1 ? 0xFFFFu : ~0u);
+        }
+        const float f0 = __half2float(__ushort_as_half((uint16_t)(own & 0xFFFFu)));
+        const float f1 = HD == 128 ? __half2float(__ushort_as_half((uint16_t)(own >> 16))) : f0;
+        tc_wait(raw_full + 4 + slot, (t / R) & 1, s_abort, p.status);
+        const uint8_t* raw = sraw + (R + slot) * C::kRaw + r * HD;
+        uint4 w[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + 16 * ((half * NC + c) ^ sel));
+        if (t > 0) tc_wait(conv_empty + 1, (t - 1) & 1, s_abort, p.status);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int at = 2 * ((half * NC + c) & 3);
+          const float f = 2 * c < NC ? f0 : f1;
+          uint2 x[4][NP];
+          i8x4_scaled<NP>(w[c].x, f, x[0]), i8x4_scaled<NP>(w[c].y, f, x[1]);
+          i8x4_scaled<NP>(w[c].z, f, x[2]), i8x4_scaled<NP>(w[c].w, f, x[3]);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) {
+            *reinterpret_cast<uint4*>(conv + k * C::kConv + 16 * (at ^ (r & 7))) = make_uint4(x[0][k].x, x[0][k].y, x[1][k].x, x[1][k].y);
+            *reinterpret_cast<uint4*>(conv + k * C::kConv + 16 * ((at + 1) ^ (r & 7))) = make_uint4(x[2][k].x, x[2][k].y, x[3][k].x, x[3][k].y);
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(raw_empty + 4 + slot);
+        mbar_arrive(conv_full + 1);
+      }
     }
   } else {
     // ---- softmax: thread = key
     const int g = warp >> 2, key = (warp & 3) * 32 + lane;
-    uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * NS;  // of group q: + q NSA
-    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + DB * NG * NSA + g * NO;  // of group q: + q NOA
+    uint32_t tS = 0;  // S of block g, group 0; of group q: + q NSA
+    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + 2 * NG * NSA + g * NO;
     float* m = sm_m + g * NB;
     const float masked = p.c < 0.f ? INFINITY : -INFINITY;
     if (p.tree.k && key < NB) {
@@ -280,26 +375,25 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     const uint32_t* vis = reinterpret_cast<const uint32_t*>(srow + g * NB) + (warp & 1);
     auto sees = [&](int r) { return key < kTreeMaxNodes && ((vis[2 * r] >> lane) & 1); };
     auto valid_at = [&](int t) { return t >= n_pre ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len; };
-    // this key's scales in tile t (0 where there is no such row): K's, then V's, two halves a word
+    // this key's scales in tile t (0 where there is no such row), two halves a word
     constexpr int NW = NG / 2;
-    uint32_t sc[2 * NW];
+    uint32_t sc[NW];
     auto scales = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < 2 * NW; ++i) sc[i] = 0;
+      for (int i = 0; i < NW; ++i) sc[i] = 0;
       if (t < t1 && valid_at(t)) {
         const bool tree = t >= n_pre;
         const KvRows& rw = tree ? p.tree : p.cache;
         const int64_t off = (int64_t)b * rw.sseq + (int64_t)hkv * rw.shead + (int64_t)(tree ? key : t * BK + key) * rw.srow;
         if constexpr (NG == 4) {
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(rw.ks + off)), d = __ldg(reinterpret_cast<const uint2*>(rw.vs + off));
-          sc[0] = a.x, sc[1] = a.y, sc[2] = d.x, sc[3] = d.y;
+          const uint2 a = ld_early2(rw.ks + off);
+          sc[0] = a.x, sc[1 % NW] = a.y;
         } else {
-          sc[0] = __ldg(reinterpret_cast<const uint32_t*>(rw.ks + off));
-          sc[1] = __ldg(reinterpret_cast<const uint32_t*>(rw.vs + off));
+          sc[0] = ld_early(rw.ks + off);
         }
       }
     };
-    auto scale = [&](const uint32_t (&w)[2 * NW], int i) {
+    auto scale = [&](const uint32_t (&w)[NW], int i) {
       return __half2float(__ushort_as_half((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu)));
     };
     scales(t0);
@@ -309,30 +403,39 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll 1
     for (int t = t0; t < t1; ++t) {
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len, valid = valid_at(t);
-      uint32_t own[2 * NW];
+      uint32_t own[NW];
 #pragma unroll
-      for (int i = 0; i < 2 * NW; ++i) own[i] = sc[i];
+      for (int i = 0; i < NW; ++i) own[i] = sc[i];
       scales(t + 1);  // the next tile's are on their way meanwhile
-      const int x = DB == 2 ? (t - t0) & 1 : 0;
-      tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
+      const int i_own = t - t0, x = i_own & 1, y = i_own % PB;
+      tc_wait(s_full + x, (i_own >> 1) & 1, s_abort, p.status);
       tc_fence_after();
-      if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * NG * NSA + g * NS;
+      tS = tmem + ((uint32_t)(warp & 3) << 21) + x * NG * NSA + g * NS;
       auto scores = [&](float (&s)[NB]) {
+        constexpr int QS = F32 ? 1 : 2;
 #pragma unroll
-        for (int q = 0; q < NG; ++q) {
-          float v[NQ][NB];
+        for (int q0 = 0; q0 < NG; q0 += QS) {  // as many groups at a time as registers allow
+          float v[QS][NQ][NB];
 #pragma unroll
-          for (int k = 0; k < NQ; ++k) tc_ld(v[k], tS + q * NSA + k * NB);
+          for (int q = 0; q < QS; ++q)
 #pragma unroll
-          for (int k = 0; k < NQ; ++k) tc_wait_ld(v[k]);
-          const float f = scale(own, q);
+            for (int k = 0; k < NQ; ++k) tc_ld(v[q][k], tS + (q0 + q) * NSA + k * NB);
 #pragma unroll
-          for (int j = 0; j < NB; j += 2) {
-            float x[2];
+          for (int q = 0; q < QS; ++q)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) x[i] = NQ == 3 ? v[0][j + i] + (v[1 % NQ][j + i] + v[2 % NQ][j + i]) : v[0][j + i];
-            if (q == 0) mul2(s[j], s[j + 1], x[0], x[1], f);
-            else fma2(s[j], s[j + 1], x[0], x[1], f, f);
+            for (int k = 0; k < NQ; ++k) tc_wait_ld(v[q][k]);
+#pragma unroll
+          for (int q = 0; q < QS; ++q) {
+            const float f = scale(own, q0 + q);
+#pragma unroll
+            for (int j = 0; j < NB; j += 2) {
+              float x[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                x[i] = NQ == 3 ? v[q][0][j + i] + (v[q][1 % NQ][j + i] + v[q][2 % NQ][j + i]) : v[q][0][j + i];
+              if (q0 + q == 0) mul2(s[j], s[j + 1], x[0], x[1], f);
+              else fma2(s[j], s[j + 1], x[0], x[1], f, f);
+            }
           }
         }
       };
@@ -356,7 +459,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         // every block's first scores have been read: P may be written
         asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
       }
-      uint8_t* prow = sp + key * 128;
+      uint8_t* prow = sp + y * C::kP + key * 128;
       for (;;) {
         float s[NB];
         scores(s);
@@ -401,83 +504,74 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll
           for (int j = 0; j < NB; ++j) l[j] *= sfac[g * NB + j];
           if (t > t0) {
-            tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+            tc_wait(o_done + (i_own - 1) % PB, ((i_own - 1) / PB) & 1, s_abort, p.status);
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < NO * NG; c0 += 16) {
-              const uint32_t at = tO + (c0 / NO) * NOA + c0 % NO;
+            for (int c0 = 0; c0 < NO; c0 += 16) {
               float o[16];
-              tc_ld(o, at);
+              tc_ld(o, tO + c0);
               tc_wait_ld(o);
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] *= sfac[g * NB + j];
-              tc_st16(at, o);
+              tc_st16(tO + c0, o);
             }
             tc_wait_st();
           }
           continue;
         }
 #pragma unroll
-        for (int j = 0; j < NB; ++j) l[j] += s[j];
-        if (t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V has read P
-        // a masked key's scale may be anything: its probabilities stay 0
-        float f[NG];
-        bool odd = false;
+        for (int j = 0; j < NB; j += 2) add2(l[j], l[j + 1], l[j], l[j + 1], s[j], s[j + 1]);
+        if (i_own >= PB) tc_wait(o_done + y, (i_own / PB - 1) & 1, s_abort, p.status);  // the P V of this buffer's last tile
 #pragma unroll
-        for (int q = 0; q < NG; ++q) {
-          f[q] = scale(own, NG + q);
-          odd |= !(fabsf(f[q]) <= 65504.f);
-        }
-        const bool any_odd = __any_sync(0xffffffffu, odd);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t part[4][NP];
 #pragma unroll
-        for (int q = 0; q < NG; ++q) {
+          for (int j = 0; j < 8; j += 2) split_pack<NP>(s[8 * h + j], s[8 * h + j + 1], part[j / 2]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t part[4][NP];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              float a, d;
-              mul2(a, d, s[8 * h + j], s[8 * h + j + 1], f[q]);
-              if (any_odd) a = s[8 * h + j] == 0.f ? 0.f : a, d = s[8 * h + j + 1] == 0.f ? 0.f : d;
-              split_pack<NP>(a, d, part[j / 2]);
-            }
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-              const int chunk = ((q & 1) * NOA + g * NO + k * NB + 8 * h) / 8;
-              *reinterpret_cast<uint4*>(prow + (q >> 1) * C::kPUnit + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ (key & 7))) =
-                  make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
-            }
+          for (int k = 0; k < NP; ++k) {
+            const int chunk = (g * NO + k * NB + 8 * h) / 8;
+            *reinterpret_cast<uint4*>(prow + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ (key & 7))) =
+                make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
           }
         }
         break;
       }
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive(p_full + y);
     }
     // ---- O^T and the sums to shared memory, [row][dim]
-    if (n_own > 0) tc_wait(o_done, (n_own - 1) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait(o_done + (n_own - 1) % PB, ((n_own - 1) / PB) & 1, s_abort, p.status);
     tc_fence_after();
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");  // every block's MMAs have read the tiles
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
-    if ((warp & 3) < 2) {  // lanes 0..63: dims; the two warps' columns are their own group's
+    if (key < HD) {  // lanes are dims
+      float o[NP][NB];
+      if (n_own > 0) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) tc_ld(o[k], tO + k * NB);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) tc_wait_ld(o[k]);
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        float x = 0.f;
+        if (n_own > 0)
+#pragma unroll
+          for (int k = NP - 1; k >= 0; --k) x += o[k][j];
+        so[j * HD + key] = x;
+      }
+      const unsigned long long bad = *s_bad;
+      if (bad && t1 == n_tiles) {  // tree values with non-finite scales, where they are seen
+        const int64_t at = (int64_t)b * p.tree.seq + (int64_t)hkv * p.tree.head + key;
+        const int64_t at_s = (int64_t)b * p.tree.sseq + (int64_t)hkv * p.tree.shead + key / 32;
 #pragma unroll 1
-      for (int u = 0; u < H; ++u) {
-        float o[NP][NB];
-        if (n_own > 0) {
-#pragma unroll
-          for (int k = 0; k < NP; ++k) tc_ld(o[k], tO + (2 * u + (warp & 1)) * NOA + k * NB);
-#pragma unroll
-          for (int k = 0; k < NP; ++k) tc_wait_ld(o[k]);
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          float x = 0.f;
-          if (n_own > 0)
-#pragma unroll
-            for (int k = NP - 1; k >= 0; --k) x += o[k][j];
-          so[j * HD + 64 * u + key] = x;
-        }
+        for (int r = 0; r < NB; ++r)
+          for (uint64_t v = srow[g * NB + r] & bad; v; v &= v - 1) {
+            const int j = __ffsll(v) - 1;
+            const float f = __half2float(__ushort_as_half(p.tree.vs[at_s + j * p.tree.srow]));
+            if (!(fabsf(f) <= 65504.f)) so[r * HD + key] += f * (float)reinterpret_cast<const int8_t*>(p.tree.v)[at + j * p.tree.row];
+          }
       }
     }
 #pragma unroll
@@ -513,11 +607,10 @@ cudaError_t launch_tree_q8_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   const int m_tiles = (p.n * p.gq + C::N - 1) / C::N;
   const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
-  int S = 1;
-  while (S < kMaxSplits && S < tiles && clusters * S < n_sm) S *= 2;
-  p.S = S;
+  static ClusterCount at_once;
+  p.S = lone_splits(clusters, tiles, [&](int S) { return at_once.get(kern, S, C::NT, C::kSmem); });
   p.sorted = p.B > 1 && p.B <= 64;
-  return launch_cluster(kern, dim3(S, p.Hkv * m_tiles, p.B), C::NT, S, C::kSmem, st, tp, p.pdl);
+  return launch_cluster(kern, dim3(p.S, p.Hkv * m_tiles, p.B), C::NT, p.S, C::kSmem, st, tp, p.pdl);
 }
 
 template <int HD>
