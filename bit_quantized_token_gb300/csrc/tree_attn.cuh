@@ -384,14 +384,13 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
   const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S);
   const int n_own = t1 - t0, n_units = 2 * H * n_own;
-  // The ring's order, in halves (K or V) of the CTA's tiles: K0 V0 K1 V1 .., or,
-  // with scores a tile ahead, K0 K1 V0 K2 V1 ..
-  auto k_unit = [&](int t) { return H * (DB == 1 ? 2 * t : t == 0 ? 0 : 2 * t - 1); };
-  auto v_unit = [&](int t) { return H * (DB == 1 ? 2 * t + 1 : t == n_own - 1 ? 2 * t + 1 : 2 * t + 2); };
+  // The ring's order, in halves (K or V) of the CTA's tiles: K0 K1 V0 K2 V1 ..
+  auto k_unit = [&](int t) { return H * (t == 0 ? 0 : 2 * t - 1); };
+  auto v_unit = [&](int t) { return H * (t == n_own - 1 ? 2 * t + 1 : 2 * t + 2); };
   auto request = [&](int i) {
     const int j = i / H, u = i % H, slot = i % NST;
-    const bool val = DB == 1 ? j & 1 : j > 0 && (!(j & 1) || j == 2 * n_own - 1);
-    const int t = t0 + (DB == 1 ? j / 2 : j == 2 * n_own - 1 ? n_own - 1 : val ? j / 2 - 1 : (j + 1) / 2);
+    const bool val = j > 0 && (!(j & 1) || j == 2 * n_own - 1);
+    const int t = t0 + (j == 2 * n_own - 1 ? n_own - 1 : val ? j / 2 - 1 : (j + 1) / 2);
     const bool tree = t >= n_pre;
     const CUtensorMap* map = val ? (tree ? &tp.tv : &tp.cv) : (tree ? &tp.tk : &tp.ck);
     mbar_expect_tx(full + slot, C::kUnit);
@@ -489,50 +488,54 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     bool ok = true;
 #pragma unroll 1
     for (int t = -DB; t < n_own && ok; ++t) {
-      if (t >= 0) {  // O += V^T P^T of tile t0 + t, from buffer x
-        const int x = DB == 2 ? t & 1 : 0;
-        ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
-#pragma unroll 1
-        for (int u = 0; u < H; ++u) {
-          const int i = v_unit(t) + u, slot = i % NST;
-          ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t v = ur + slot * C::kUnit;
-          // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
-          const uint64_t da = tc_desc(v, uo - v, 1024, 2);
-          const uint64_t dp = tc_desc(up + x * C::kP, BK * 128, sbo_p, swp);
-          if (elect_lane()) {
+      const int x = DB == 2 ? t & 1 : 0;
+      if (t >= 0) ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
+      // S of tile t0 + t + DB goes into the buffer just read. With one buffer it
+      // is first: the softmax goes on with it while O is brought up to date
+      // (16 x 64 nodes over 1024..8192 rows: 99.8 us with it second).
 #pragma unroll
-            for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
-              tc_mma(tm + DB * C::NSA + u * C::NOA, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
-                     dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
-          }
-          __syncwarp();
-          tc_commit(empty + slot);
-        }
-        if (!ok) break;
-        tc_commit(o_done);
-      }
-      if (t + DB < n_own) {  // S of tile t0 + t + DB, into the buffer just read
-        const int x = DB == 2 ? t & 1 : 0;
+      for (int first = 1; first >= 0; --first) {
+        if ((first == 1) == (DB == 1)) {
+          if (t + DB >= n_own) continue;
 #pragma unroll 1
-        for (int u = 0; u < H; ++u) {
-          const int i = k_unit(t + DB) + u, slot = i % NST;
-          ok = tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
-          const uint64_t dq = tc_desc(uq + u * C::NSA * 128, 16, 1024, 2);
-          if (elect_lane()) {
+          for (int u = 0; u < H; ++u) {
+            const int i = k_unit(t + DB) + u, slot = i % NST;
+            ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = tc_desc(ur + slot * C::kUnit, 16, 1024, 2);
+            const uint64_t dq = tc_desc(uq + u * C::NSA * 128, 16, 1024, 2);
+            if (elect_lane()) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
-              tc_mma(tm + x * C::NSA, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
+              for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
+                tc_mma(tm + x * C::NSA, da + 2 * ks, dq + 2 * ks, idesc_s, u > 0 || ks > 0);
+            }
+            __syncwarp();
+            tc_commit(empty + slot);
           }
-          __syncwarp();
-          tc_commit(empty + slot);
+          if (ok) tc_commit(s_full + x);
+        } else if (t >= 0) {  // O += V^T P^T of tile t0 + t, from buffer x
+#pragma unroll 1
+          for (int u = 0; u < H; ++u) {
+            const int i = v_unit(t) + u, slot = i % NST;
+            ok = ok && tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v = ur + slot * C::kUnit;
+            // the second 64 rows of V are the ones: a fixed place, so the leading offset falls as the start rises
+            const uint64_t da = tc_desc(v, uo - v, 1024, 2);
+            const uint64_t dp = tc_desc(up + x * C::kP, BK * 128, sbo_p, swp);
+            if (elect_lane()) {
+#pragma unroll
+              for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
+                tc_mma(tm + DB * C::NSA + u * C::NOA, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                       dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
+            }
+            __syncwarp();
+            tc_commit(empty + slot);
+          }
+          if (ok) tc_commit(o_done);
         }
-        if (ok) tc_commit(s_full + x);
       }
     }
     if (!ok) {  // no MMA may outlive its operands
@@ -572,14 +575,13 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     for (int t = t0; t < t1; ++t) {
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
       const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
-      // these scores: this buffer's last P V is done too
       const int x = DB == 2 ? (t - t0) & 1 : 0;
       tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
       tc_fence_after();
       if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NSA + g * C::NS;
       if (!whole) {  // V rows that are not there become zeros, non-finite tree values too (noted for the rows that see them)
         // (after the last P V, so that the slot's last unit has been read and its barrier is in this unit's phase)
-        if (DB == 2 && t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+        if (t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
         for (int u = 0; u < H; ++u) {
           const int i = v_unit(t - t0) + u;
           tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
@@ -652,26 +654,29 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 #pragma unroll
             for (int j = 0; j < W; ++j) s[j] = masked;
           }
+          uint32_t part[W / 8][4][NP];
 #pragma unroll
-          for (int h = 0; h < W / 8; ++h) {
-            uint32_t part[4][NP];
+          for (int h = 0; h < W / 8; ++h)
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
               const float4 ref = *reinterpret_cast<const float4*>(m + c0 + 8 * h + j);
               float y[4] = {ref.x, ref.y, ref.z, ref.w};
               fma2(y[0], y[1], s[8 * h + j], s[8 * h + j + 1], p.c, p.c);
               fma2(y[2], y[3], s[8 * h + j + 2], s[8 * h + j + 3], p.c, p.c);
-              split_pack<NP>(ex2(y[0]), ex2(y[1]), part[j / 2]);
-              split_pack<NP>(ex2(y[2]), ex2(y[3]), part[j / 2 + 1]);
-              top = max_bf16x2(top, max_bf16x2(part[j / 2][0], part[j / 2 + 1][0]));
+              split_pack<NP>(ex2(y[0]), ex2(y[1]), part[h][j / 2]);
+              split_pack<NP>(ex2(y[2]), ex2(y[3]), part[h][j / 2 + 1]);
+              top = max_bf16x2(top, max_bf16x2(part[h][j / 2][0], part[h][j / 2 + 1][0]));
             }
+          // one buffer of P: the last P V has read it (with two, that of this buffer came before these scores)
+          if (DB == 1 && c0 == 0 && t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+#pragma unroll
+          for (int h = 0; h < W / 8; ++h)
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
               const int chunk = (g * C::NO + k * NB + c0 + 8 * h) / 8;
               *reinterpret_cast<uint4*>(prow + (chunk / 8) * BK * 128 + 16 * ((chunk & 7) ^ sel)) =
-                  make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
+                  make_uint4(part[h][0][k], part[h][1][k], part[h][2][k], part[h][3][k]);
             }
-          }
         };
         float va[NQ][W], vb[NQ][W];  // the next columns load while these are worked on
         load(va, 0);
