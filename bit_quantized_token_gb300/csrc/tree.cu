@@ -155,7 +155,7 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 // an SM keep both directions of HBM busy: read and written once, 311 MB for 256 x
 // 151936. Exponentials are taken once, against a reference instead of the row's
 // maximum: the largest of the first piece. A CTA whose largest logit lies 2^60
-// off its reference, either way, takes its slice again against that one. 65.5 us (71 %
+// over its reference, or below it, takes its slice again against that one. 65.5 us (71 %
 // of the copy rate); 512 threads 71.5, four pieces 66.2, one 70.6; 16 CTAs a row 75.6.
 constexpr int kSoftThreads = 256;
 constexpr int kPieces = 2;
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
     }
     const float2 w = reduce(mx, sum);
     own = make_float2(w.x == -INFINITY ? -INFINITY : ref, w.y);
-    if (turn == 1 || w.x == -INFINITY || fabsf((w.x - ref) * p.c) <= 60.f) break;
+    // (below it only where the first piece had none: small terms would be lost)
+    if (turn == 1 || w.x == -INFINITY || (w.x >= ref && (w.x - ref) * p.c <= 60.f)) break;
     ref = w.x;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the slice is overwritten by bulk copies
   }
@@ -1245,6 +1246,14 @@ int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n
   const int64_t sstride[4] = {cache->scale_seq_stride, cache->scale_layer_stride, cache->scale_head_stride,
                               cache->scale_row_stride};
   const bool q8 = cache->dtype == LLM_Q8G32;
+  // drafts kept in the cache's own rows (of the same layout) would be overwritten while others are read
+  const int64_t ahead = (static_cast<const char*>(tree->k) - static_cast<const char*>(cache->k)) / (q8 ? 1 : 2);
+  const bool alike = cache->seq_stride == tree->seq_stride && cache->layer_stride == tree->layer_stride &&
+                     cache->head_stride == tree->head_stride && cache->row_stride == tree->row_stride;
+  if (!c.need(!alike || cache->row_stride == 0 || ahead % cache->row_stride || ahead / cache->row_stride >= cache->rows ||
+                  ahead / cache->row_stride <= -(int64_t)tree->rows,
+              LLM_ERR_INVALID_ARG, "the tree's rows lie in the cache"))
+    return c.rc;
   if (!c.need(apart(cache->head_dim, 4, size, stride) && (!q8 || apart(cache->head_dim / 32, 4, size, sstride)),
               LLM_ERR_INVALID_ARG, "rows of the cache overlap") ||
       !view_memory(c, cache, "cache") || !view_memory(c, tree, "tree") || !c.device("lens", lens, 4) ||

@@ -422,7 +422,7 @@ typedef struct {
 /* out = softmax(scale q K^T over the visible rows) V; query head h reads kv
  * head h / (n_heads / cache heads). Products on the tensor cores, sums in
  * fp32; fp32 queries and their probabilities carry 24 bits, for bf16 queries
- * the probabilities at least 8 (rounding below that of the output). A node that sees no row gets
+ * the probabilities at least 8 and int8 rows' values 16 (rounding below that of the output). A node that sees no row gets
  * zeros. A row that a node does not see has no influence on it, whatever it
  * holds. With n_nodes = 1 and tree = NULL this is one decode token's
  * attention over a cache that already holds its row. */
@@ -478,7 +478,8 @@ int llm_verify_tree(const llm_verify_tree_args* args, void* cuda_stream);
 /* cache row lens[b] + k = tree row path[b][k] for k < n_path[b], in every layer
  * and head, K, V and scales; new_lens[b] = lens[b] + n_path[b] (new_lens may be
  * lens). Rows past the cache's end are dropped and new_lens stops there;
- * entries of path outside 0..rows-1 leave their cache row as it was. path [n_seq][n_nodes]. */
+ * entries of path outside 0..rows-1 leave their cache row as it was. The tree's rows
+ * are no rows of the cache (not a draft area behind lens). path [n_seq][n_nodes]. */
 int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n_seq, int32_t n_nodes,
                     const int32_t* lens, const int32_t* path, const int32_t* n_path, int32_t* new_lens,
                     void* cuda_stream);

@@ -455,6 +455,29 @@ def test_token_probs_special_values(k):
             check_probs(got[r], ref, 0.9, 10.0)
 
 
+@pytest.mark.parametrize("V", [9, 700, 33333, 151936])
+@pytest.mark.parametrize("T", [1.0, 0.05, 20.0])
+def test_token_probs_large_logits_come_late(V, T):
+    """Rows whose largest logits are far from the ones before them, in either direction."""
+    h = V // 2
+    x = 2 * T * torch.randn(7, V, device="cuda", generator=gen(7))
+    x[0, -1] += 1000 * T
+    x[1, h:] += 300 * T
+    x[2, :h] = -math.inf
+    x[2, h:] -= 40 * T
+    x[3, :h] = -math.inf
+    x[3, h:] = 6 * (x[3, h:] - 15 * T)
+    x[4, :-2] = torch.finfo(torch.float32).min
+    x[5, :h] = -1e30
+    x[5, V - 1] = 3e38
+    x[6, :h] += 500 * T
+    out = torch.empty_like(x)
+    bq.token_probs(x, out, T, 0, 1.0)
+    xs, got = x.cpu().numpy(), out.cpu().numpy()
+    for r in range(7):  # terms further than 110 down are below the tolerance's floor
+        check_probs(got[r], probs_reference(xs[r], T, 0, 1.0), T, 110.0 * T)
+
+
 # ---- verification ------------------------------------------------------------------
 def verify_reference(tokens, parents, u, p, q, cnt):
     """One sequence in 64 bits: (path, next)."""

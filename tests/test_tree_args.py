@@ -129,6 +129,15 @@ def test_overlapping_outputs_are_refused(library):
     four = [Fake((2,), torch.int32), Fake((2, 3), torch.int32), Fake((2,), torch.int32)]
     with pytest.raises(bq.LlmError, match="rows of the cache overlap"):
         bq.commit_tree(view(stride=(0, 512, 64, 1)), view(rows=3), *four, Fake((2,), torch.int32, at=1 << 21))
+    # drafts behind the lengths of the cache's own rows, or a head's rows that run into it
+    for shift in (0, 5 * 64, -2 * 64):
+        with pytest.raises(bq.LlmError, match="lie in the cache"):
+            bq.commit_tree(view(rows=8, stride=(2048, 1024, 64, 1)), view(rows=3, stride=(2048, 1024, 64, 1), at=(1 << 20) + 2 * shift),
+                           *four, Fake((2,), torch.int32, at=1 << 21))
+    for shift in (8 * 64, -3 * 64):  # beside it: refused for no such reason
+        with pytest.raises(bq.LlmError, match="current device"):
+            bq.commit_tree(view(rows=8, stride=(2048, 1024, 64, 1)), view(rows=3, stride=(2048, 1024, 64, 1), at=(1 << 20) + 2 * shift),
+                           *four, Fake((2,), torch.int32, at=1 << 21))
     with pytest.raises(bq.LlmError, match="new_lens overlaps"):
         bq.commit_tree(view(), view(rows=3), *four, Fake((2,), torch.int32, at=(1 << 20) + 4))
 
