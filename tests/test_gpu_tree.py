@@ -751,3 +751,69 @@ def test_a_decoding_step_of_all_four(kv):
     one.out = torch.full_like(q1, 7.0)
     one.call()
     one.check()
+
+
+def test_a_captured_step_replays_like_the_eager_one():
+    """Attention, probabilities (with and without top-k), verification and commit in a graph each on two streams,
+    replayed at once with new inputs, leave the bits that eager calls leave."""
+    B, n, Hkv, gq, hd, cap, V = 3, 9, 2, 2, 64, 400, 3001
+    par = torch.tensor(random_parents(n, np.random.default_rng(4)), dtype=torch.int32, device="cuda").expand(B, n).contiguous()
+
+    class Step:
+        def __init__(self, k):
+            self.k = k
+            self.p = Problem(B=B, n=n, Hkv=Hkv, gq=gq, hd=hd, cap=cap, lens=(40, 0, 350), q="bf16", seed=k)
+            self.views = self.p.cache(), self.p.tree()
+            self.logits = torch.empty(B * n, V, device="cuda")
+            self.probs = torch.empty_like(self.logits)
+            self.tokens = torch.empty(B, n, dtype=torch.int32, device="cuda")
+            self.u = torch.empty(B, n, device="cuda")
+            self.path, self.outs = self.tokens.clone(), [torch.empty(B, dtype=torch.int32, device="cuda") for _ in range(2)]
+
+        def renew(self, seed):
+            g = gen(seed)
+            self.logits.normal_(generator=g).mul_(2)
+            self.tokens.random_(0, V, generator=g)
+            best = self.logits.view(B, n, V).argmax(-1).int()
+            self.u.uniform_(generator=g).mul_(0.3)
+            self.tokens[:, 1:] = torch.where(self.u[:, 1:] < 0.2, best.gather(1, par[:, 1:].long()), self.tokens[:, 1:])
+            self.p.lens.copy_(torch.tensor([40, 0, 350], dtype=torch.int32))
+            self.p.k.normal_(generator=g)
+            self.p.v.normal_(generator=g)
+            self.p.out.fill_(7.0)
+
+        def run(self, st):
+            p = self.p
+            bq.tree_attention(p.q, *self.views, p.lens, p.mask, p.out, stream=st)
+            bq.token_probs(self.logits, self.probs, 0.8, self.k, 1.0, stream=st)
+            bq.verify_tree(self.tokens, par, self.u, self.probs.view(B, n, V), self.path, *self.outs, stream=st)
+            bq.commit_tree(*self.views, p.lens, self.path, self.outs[0], p.lens, stream=st)
+
+        def state(self):
+            p = self.p
+            return [t.clone() for t in (p.out, self.probs, self.path, *self.outs, p.lens, p.k, p.v)]
+
+    steps, streams, graphs = [Step(0), Step(20)], [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for s, st in zip(steps, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=st):
+            s.run(st.cuda_stream)
+    for rep in range(3):
+        want = []
+        for s in steps:
+            s.renew(rep)
+            s.run(None)
+            want.append(s.state())
+        for s in steps:
+            s.renew(rep)
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for s, w in zip(steps, want):
+            for a, b in zip(s.state(), w):
+                assert torch.equal(a, b)
+            assert (s.p.lens > torch.tensor([40, 0, 350], dtype=torch.int32, device="cuda")).all()
+    bq.tree_status()
