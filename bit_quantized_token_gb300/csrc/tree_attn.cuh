@@ -205,6 +205,16 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, f
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
+// Bit j of lane i's word becomes bit i of lane j's: halves of ever smaller blocks change places.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    const uint32_t low = 0xFFFFFFFFu / ((1u << m) + 1);  // the bits whose index has not m
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, m);
+    x = lane & m ? (x & ~low) | ((y & ~low) >> m) : (x & low) | ((y & low) << m);
+  }
+  return x;
+}
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -461,6 +471,11 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
            __reduce_or_sync(0xffffffffu, (uint32_t)a);
     if (cnt < 64) seen &= (1ull << cnt) - 1;
   }
+  // Steps of 16 keys of own tile t that hold a visible one: P is 0 behind them.
+  auto steps = [&](int t) {
+    const int n = t0 + t >= n_pre ? 64 - __clzll((long long)seen) : min(BK, len - (t0 + t) * BK);
+    return max(1, (n + 15) / 16);
+  };
 
   if (warp == 4 * G) {
     if (lane == 0) {
@@ -515,6 +530,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           }
           if (ok) tc_commit(s_full + x);
         } else if (t >= 0) {  // O += V^T P^T of tile t0 + t, from buffer x
+          const int n_steps = steps(t);
 #pragma unroll 1
           for (int u = 0; u < H; ++u) {
             const int i = v_unit(t) + u, slot = i % NST;
@@ -528,8 +544,9 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
             if (elect_lane()) {
 #pragma unroll
               for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
-                tc_mma(tm + DB * C::NSA + u * C::NOA, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
-                       dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
+                if (ks < n_steps)
+                  tc_mma(tm + DB * C::NSA + u * C::NOA, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
+                         dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
             }
             __syncwarp();
             tc_commit(empty + slot);
@@ -557,9 +574,6 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         srow[g * NB + r] = node < cnt ? smask[node] & seen : 0;
       }
     group_sync(g);
-    // whether row r of the block sees this thread's tree row
-    const uint32_t* vis = reinterpret_cast<const uint32_t*>(srow + g * NB) + (warp & 1);
-    auto sees = [&](int r) { return key < kTreeMaxNodes && ((vis[2 * r] >> lane) & 1); };
     constexpr int W = NB >= 32 && NQ == 1 ? 32 : 16;
     auto load = [&](float (&v)[NQ][W], int c0) {
 #pragma unroll
@@ -579,41 +593,16 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
       tc_fence_after();
       if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NSA + g * C::NS;
-      if (!whole) {  // V rows that are not there become zeros, non-finite tree values too (noted for the rows that see them)
-        // (after the last P V, so that the slot's last unit has been read and its barrier is in this unit's phase)
-        if (t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
-        for (int u = 0; u < H; ++u) {
-          const int i = v_unit(t - t0) + u;
-          tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
-        }
-#pragma unroll 4
-        for (int c = 0; c < HD / 8 && (tree || !valid); ++c) {
-          const int slot = (v_unit(t - t0) + c / 8) % NST;
-          uint4* x = reinterpret_cast<uint4*>(sring + slot * C::kUnit + key * 128 + 16 * ((c & 7) ^ (key & 7)));
-          if (!valid) {
-            *x = make_uint4(0u, 0u, 0u, 0u);
-          } else if (tree) {
-            const uint4 w = *x;
-            uint32_t inf = 0;  // whether an exponent is all ones
+      // tree: whether row r of the block sees this thread's tree row
+      uint32_t rv[(NB + 31) / 32] = {};
+      if (tree)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t v = (&w.x)[j] & 0x7F807F80u;
-              inf |= (v & 0xFFFFu) == 0x7F80u || (v >> 16) == 0x7F80u;
-            }
-            if (inf) {
-              uint16_t* e = reinterpret_cast<uint16_t*>(x);
-#pragma unroll 1
-              for (int j = 0; j < 8; ++j)
-                if ((e[j] & 0x7F80u) == 0x7F80u) {
-                  const int kind = (e[j] & 0x7Fu) ? 2 : e[j] >> 15, d = 8 * c + j;
-                  atomicOr(snf + (kind * kTreeMaxNodes + key) * NG + (d >> 5), 1u << (d & 31));
-                  e[j] = 0;
-                }
-              *s_any = 1;
-            }
-          }
-        }
-      }
+        for (int r0 = 0; r0 < NB; r0 += 32)
+          rv[r0 / 32] = transpose_bits(key < kTreeMaxNodes && r0 + lane < NB
+                                           ? reinterpret_cast<const uint32_t*>(srow + g * NB + r0 + lane)[warp & 1]
+                                           : 0u,
+                                       lane);
+      auto sees = [&](int r) { return (((NB > 32 && r >= 32 ? rv[NB / 32 - (NB >= 32)] : rv[0]) >> (r & 31)) & 1) != 0; };
       if (t == t0) {  // the references: the score of the first key that a row sees (renewed below if not finite)
         float* first = reinterpret_cast<float*>(sp + x * C::kP) + g * 64 * NB;  // [64][NB], where P comes to lie
         static_assert(64 * N * 4 <= C::kP, "room for the first scores");
@@ -731,6 +720,44 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
             tc_st16(at, s);
           }
           tc_wait_st();
+        }
+      }
+      if (!whole) {
+        // V rows that are not there become zeros, non-finite tree values too (noted for the
+        // rows that see them), in the steps that are multiplied. After the last P V, so that
+        // the slot's last unit has been read and its barrier is in this unit's phase.
+        if (t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+        for (int u = 0; u < H; ++u) {
+          const int i = v_unit(t - t0) + u;
+          tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
+        }
+        const int r0 = tree ? 0 : len - t * BK, n_chunks = (16 * steps(t - t0) - r0) * (HD / 8);
+#pragma unroll 1
+        for (int i = tid; i < n_chunks; i += 128 * G) {
+          const int row = r0 + i / (HD / 8), c = i % (HD / 8), slot = (v_unit(t - t0) + c / 8) % NST;
+          uint4* at = reinterpret_cast<uint4*>(sring + slot * C::kUnit + row * 128 + 16 * ((c & 7) ^ (row & 7)));
+          if (!tree || !((seen >> row) & 1)) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+          }
+          const uint4 w = *at;
+          uint32_t inf = 0;  // whether an exponent is all ones
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v = (&w.x)[j] & 0x7F807F80u;
+            inf |= (v & 0xFFFFu) == 0x7F80u || (v >> 16) == 0x7F80u;
+          }
+          if (inf) {
+            uint16_t* e = reinterpret_cast<uint16_t*>(at);
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j)
+              if ((e[j] & 0x7F80u) == 0x7F80u) {
+                const int kind = (e[j] & 0x7Fu) ? 2 : e[j] >> 15, d = 8 * c + j;
+                atomicOr(snf + (kind * kTreeMaxNodes + row) * NG + (d >> 5), 1u << (d & 31));
+                e[j] = 0;
+              }
+            *s_any = 1;
+          }
         }
       }
       fence_async_smem();

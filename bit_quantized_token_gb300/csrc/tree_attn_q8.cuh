@@ -207,6 +207,10 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
            __reduce_or_sync(0xffffffffu, (uint32_t)a);
     if (cnt < 64) seen &= (1ull << cnt) - 1;
   }
+  auto steps = [&](int t) {  // of 16 keys that hold a visible one (see tree_attn_tc_kernel)
+    const int n = t0 + t >= n_pre ? 64 - __clzll((long long)seen) : min(BK, len - (t0 + t) * BK);
+    return max(1, (n + 15) / 16);
+  };
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
@@ -240,6 +244,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         ok = tc_wait_warp(p_full + y, (t / PB) & 1, s_abort, p.status) && tc_wait_warp(conv_full + 1, t & 1, s_abort, p.status);
         if (!ok) break;
         tc_fence_after();
+        const int n_steps = steps(t);
         const uint64_t dp = tc_desc(up + y * C::kP, BK * 128, 1024, 2);
 #pragma unroll 1
         for (int k = 0; k < NP; ++k) {
@@ -248,7 +253,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
           if (elect_lane()) {
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-              tc_mma(tm + 2 * NG * NSA, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o, t > 0 || k > 0 || ks > 0);
+              if (ks < n_steps)
+                tc_mma(tm + 2 * NG * NSA, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o, t > 0 || k > 0 || ks > 0);
           }
           __syncwarp();
         }
@@ -372,8 +378,12 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       srow[g * NB + key] = node < cnt ? smask[node] & seen : 0;
     }
     group_sync(g);
-    const uint32_t* vis = reinterpret_cast<const uint32_t*>(srow + g * NB) + (warp & 1);
-    auto sees = [&](int r) { return key < kTreeMaxNodes && ((vis[2 * r] >> lane) & 1); };
+    auto row_bits = [&]() {  // bit r: row r of the block sees this thread's tree row
+      return transpose_bits(key < kTreeMaxNodes && lane < NB
+                                ? reinterpret_cast<const uint32_t*>(srow + g * NB + lane)[warp & 1]
+                                : 0u,
+                            lane);
+    };
     auto valid_at = [&](int t) { return t >= n_pre ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len; };
     // this key's scales in tile t (0 where there is no such row), two halves a word
     constexpr int NW = NG / 2;
@@ -464,9 +474,10 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         float s[NB];
         scores(s);
         if (tree) {
+          const uint32_t bits = row_bits();
 #pragma unroll
           for (int j = 0; j < NB; ++j)
-            if (!sees(j)) s[j] = masked;
+            if (!((bits >> j) & 1)) s[j] = masked;
         } else if (!whole && !valid) {
 #pragma unroll
           for (int j = 0; j < NB; ++j) s[j] = masked;
@@ -485,9 +496,10 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         if (group_any(g, top > 1152921504606846976.f)) {  // 2^60 past the references: renew them
           float z[NB];
           scores(z);
+          const uint32_t bits = tree ? row_bits() : valid ? ~0u : 0u;
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
-            const bool in = tree ? sees(j) : valid;
+            const bool in = (bits >> j) & 1;
             float y = in ? z[j] * p.c : -INFINITY;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
