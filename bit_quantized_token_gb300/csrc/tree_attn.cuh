@@ -254,96 +254,78 @@ __device__ __forceinline__ int nth_longest(const int* lens, int B, int z, int la
   return ha ? __ffs(ha) - 1 : 31 + __ffs(hc);
 }
 
-// The cluster's S key ranges joined: rank k writes its share of the rows. so: a
-// rank's unnormalised O [N][HD], sml its (reference, sum) per row.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// The cluster's S key ranges joined (S a power of two, so it divides N). so: a
+// rank's unnormalised O [N][HD], sml its (reference, sum) per row. Rank q owns the
+// rows from q share on: every rank stores its part of them into q's `in`
+// ([S][share] rows, their (reference, sum), room for weights: kJoin bytes), and q
+// adds the parts from its own shared memory. (Loads from the other ranks took a
+// round trip for the weights and one for the parts, and a barrier more.) With S >
+// 1 every thread has arrived once (cluster_arrive) when its CTA's part of `in` was free.
+template <int HD, int N>
+constexpr int kJoin = N * HD * 4 + N * 12;
 template <int HD, bool F32, int N, int NT>
-__device__ __forceinline__ void join_splits(const TreeAttnParams& p, float* so, float2* sml, float* sw, int rank, int b,
-                                            int hkv, int m0, int rows) {
+__device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float* so, const float2* sml, uint8_t* in,
+                                            int rank, int b, int hkv, int m0, int rows) {
   constexpr float kNone = -3e38f;
-  const int tid = threadIdx.x;
-  cg::cluster_group cl = cg::this_cluster();
+  constexpr int R4 = HD / 4;
+  const int tid = threadIdx.x, S = p.S, share = (rows + S - 1) / S;
+  const float4* part = reinterpret_cast<const float4*>(so);  // [S][share][R4]
+  const float2* ml = sml;                                    // [S][share]
+  float* sw = reinterpret_cast<float*>(in + N * HD * 4 + N * 8);
   __syncthreads();
-  // ---- the cluster's S key ranges: rank k writes its share of the rows
-  if (p.S > 1) cl.sync();
-  for (int r = tid; r < rows; r += NT) {
-    float2 ml[kMaxSplits];  // all loads in flight: a rank's answer takes long
-#pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k) ml[k] = k < p.S ? cl.map_shared_rank(sml, k)[r] : make_float2(kNone, 0.f);
-    float M = ml[0].x, L = 0.f;
-#pragma unroll
-    for (int k = 1; k < kMaxSplits; ++k) M = fmaxf(M, ml[k].x);
-#pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k) {
-      ml[k].x = ml[k].x <= kNone ? 0.f : ex2(ml[k].x - M);
-      L = fmaf(ml[k].y, ml[k].x, L);
+  if (S > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    float4* in4 = reinterpret_cast<float4*>(in);
+    float2* in_ml = reinterpret_cast<float2*>(in + N * HD * 4);
+    const uint32_t inv = (65535 + share) / share;  // r / share = r inv >> 16 (r and share at most 128)
+    cluster_wait();
+#pragma unroll 4
+    for (int i = tid; i < rows * R4; i += NT) {
+      const int r = i / R4, q = r * inv >> 16;
+      cl.map_shared_rank(in4, q)[(rank * share + r - q * share) * R4 + i % R4] = part[i];
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
-#pragma unroll
-    for (int k = 0; k < kMaxSplits; ++k)
-      if (k < p.S) sw[k * N + r] = ml[k].x * inv;
+    for (int r = tid; r < rows; r += NT) {
+      const int q = r * inv >> 16;
+      cl.map_shared_rank(in_ml, q)[rank * share + r - q * share] = sml[r];
+    }
+    cluster_arrive();
+    cluster_wait();  // every part is here, and no rank touches another's memory from here on
+    part = in4, ml = in_ml;
+  }
+  const int own = min(share, rows - rank * share);  // (none: 0 or less)
+  for (int r = tid; r < own; r += NT) {
+    float M = ml[r].x, L = 0.f;
+    for (int k = 1; k < S; ++k) M = fmaxf(M, ml[k * share + r].x);
+    for (int k = 0; k < S; ++k) {
+      const float2 x = ml[k * share + r];
+      const float w = x.x <= kNone ? 0.f : ex2(x.x - M);
+      L = fmaf(x.y, w, L);
+      sw[k * share + r] = w;
+    }
+    const float f = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
+    for (int k = 0; k < S; ++k) sw[k * share + r] *= f;
   }
   __syncthreads();
-  const int n4 = rows * HD / 4;
-  const int i0 = (int)((int64_t)n4 * rank / p.S), i1 = (int)((int64_t)n4 * (rank + 1) / p.S);
-  auto store = [&](int i, float4 a) {
-    const int r = i / (HD / 4), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
-    const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % (HD / 4));
+#pragma unroll 2
+  for (int i = tid; i < own * R4; i += NT) {
+    const int r = i / R4, row = m0 + rank * share + r, node = p.by_gq.div(row), h = hkv * p.gq + row - node * p.gq;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) {
+      const float4 x = part[k * share * R4 + i];
+      const float f = sw[k * share + r];
+      a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+    }
+    const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % R4);
     if constexpr (F32)
       *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = a;
     else
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off) =
           make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-  };
-  auto add = [&](float4& a, float4 x, float f) {
-    a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
-  };
-  auto part = [&](int k, int i) { return reinterpret_cast<const float4*>(cl.map_shared_rank(so, k))[i]; };
-  // eight loads of a thread in flight: of eight ranks where it has one element,
-  // of two ranks where it has several
-  if (i1 - i0 <= NT) {
-    const int i = i0 + tid, r = min(i, n4 - 1) / (HD / 4);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < i1)
-#pragma unroll 1
-      for (int k0 = 0; k0 < p.S; k0 += 8) {
-        float4 x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k0 + k < p.S) x[k] = part(k0 + k, i);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k0 + k < p.S) add(a, x[k], sw[(k0 + k) * N + r]);
-      }
-    // a CTA's shared memory lives until every rank has read it
-    if (p.S > 1) {
-      auto read = cl.barrier_arrive();
-      if (i < i1) store(i, a);
-      cl.barrier_wait(std::move(read));
-    } else if (i < i1) {
-      store(i, a);
-    }
-    return;
   }
-#pragma unroll 1
-  for (int i = i0 + tid; i < i1; i += 4 * NT) {
-    float4 a[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int k = 0; k < p.S; ++k) {
-      float4 x[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u * NT < i1) x[u] = part(k, i + u * NT);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u * NT < i1) add(a[u], x[u], sw[k * N + (i + u * NT) / (HD / 4)]);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i + u * NT < i1) store(i + u * NT, a[u]);
-  }
-  if (p.S > 1) cl.sync();
 }
 
 template <int HD, bool F32, int NB, int G>
@@ -373,8 +355,10 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);        // [N]
   float* sfac = reinterpret_cast<float*>(sml + N);              // [N] rescaling of O and the sums
   uint32_t* snf = reinterpret_cast<uint32_t*>(sfac + N);        // [3][64][NG]
-  float* sw = reinterpret_cast<float*>(sp);                     // [kMaxSplits][N] merge weights, when P is done with
-  static_assert(kMaxSplits * N * 4 <= DB * C::kP, "merge weights");
+  // the other ranks' parts at the end: behind this one's in the ring, or over P
+  constexpr bool in_ring = C::kOut + kJoin<HD, N> <= NST * C::kUnit;
+  uint8_t* sjoin = in_ring ? sring + C::kOut : sp;
+  static_assert(in_ring || kJoin<HD, N> <= DB * C::kP + C::kQ, "room for the other ranks' parts");
 
   // TMA: the units in the order in which the MMAs release them
   if (tid == 4 * G * 32) {
@@ -771,6 +755,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     tc_fence_after();
     // every block's last MMAs have read the ring and P before any block writes over them
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
+    if (p.S > 1) cluster_arrive();
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
     const bool have = t0 < t1;
 #pragma unroll 1
@@ -810,7 +795,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     tc_fence_before();
   }
   __syncwarp();
-  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sw, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
+  if (warp >= 4 * G && p.S > 1) cluster_arrive();
+  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
   // Freed last: no two CTAs that hold and that wait for tensor memory share an
   // SM (kernels whose columns exceed half take all of its shared memory), so a
   // CTA that holds it while its cluster gathers cannot keep a peer waiting.

@@ -90,7 +90,7 @@ struct TreeQ8 {
   static constexpr int kSmem = kFixed + 2 * R * kRaw;
   static constexpr int kUsed = 2 * NG * NSA + NOA;                        // two buffers of S: the scores are a tile ahead
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(R >= 2 && kUsed <= 512 && N * HD * 4 <= 2 * kConv && kMaxSplits * N * 4 <= kP && G * 4096 <= kP, "fits");
+  static_assert(R >= 2 && kUsed <= 512 && N * HD * 4 <= 2 * kConv && G * 4096 <= kP, "fits");
 };
 
 template <int HD, bool F32, int G>
@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   float* sm_w = sm_m + N;                                            // [4][N]
   float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);             // [N]
   float* sfac = reinterpret_cast<float*>(sml + N);                   // [N]
-  float* sw = reinterpret_cast<float*>(sp);                          // merge weights, when P is done with
+  uint8_t* sjoin = sconv + N * HD * 4;                               // the other ranks' parts at the end
+  static_assert(N * HD * 4 + kJoin<HD, N> <= (1 + NP) * C::kConv, "room for them");
 
   if (tid == 32 * kTmaWarp) {
     *s_abort = 0;
@@ -556,6 +557,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     if (n_own > 0) tc_wait(o_done + (n_own - 1) % PB, ((n_own - 1) / PB) & 1, s_abort, p.status);
     tc_fence_after();
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");  // every block's MMAs have read the tiles
+    if (p.S > 1) cluster_arrive();
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
     if (key < HD) {  // lanes are dims
       float o[NP][NB];
@@ -601,7 +603,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     tc_fence_before();
   }
   __syncwarp();
-  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sw, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
+  if (warp >= kConvWarp && p.S > 1) cluster_arrive();
+  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
   if (warp == kMmaWarp) {  // (freed last: see tree_attn_tc_kernel)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kCols));
