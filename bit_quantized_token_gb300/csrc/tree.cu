@@ -1,5 +1,6 @@
 // Token probabilities, draft verification and the commit of accepted rows, and
 // the C entries of the tree-decoding operators (see tree.cuh).
+#include <cuda.h>
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -956,10 +957,27 @@ cudaError_t status_word(int dev, int** p) {
   return cudaSuccess;
 }
 
+// cuMemGetAddressRange, looked up once; null where the driver has none.
+using AddressRange = CUresult (*)(CUdeviceptr*, size_t*, CUdeviceptr);
+AddressRange address_range() {
+  static const AddressRange fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<AddressRange>(f);
+  }();
+  return fn;
+}
+
 // Checks of one call: the current device, and that every buffer is its memory.
 struct Call {
   int dev = -1, n_sm = 0, rc = LLM_OK;
   cudaError_t e = cudaSuccess;  // reported by the first buffer's check, after those of sizes
+  uintptr_t lo = 0, size = 0;   // the allocation of the last buffer looked up
   Call() {
     static std::atomic<int> sms[64];
     e = cudaGetDevice(&dev);
@@ -985,6 +1003,8 @@ struct Call {
       rc = cuda_bad(e, "current device");
       return false;
     }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (at - lo < size) return true;  // in the allocation of the buffer before: a pool's small tensors share one
     cudaPointerAttributes a{};
     if (cudaPointerGetAttributes(&a, p) != cudaSuccess) cudaGetLastError();
     const bool dm = a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
@@ -992,6 +1012,10 @@ struct Call {
       rc = bad(LLM_ERR_INVALID_ARG, "%s is not memory of the current device", name);
       return false;
     }
+    CUdeviceptr base = 0;
+    size_t n = 0;
+    const auto range = address_range();
+    if (range && range(&base, &n, static_cast<CUdeviceptr>(at)) == CUDA_SUCCESS) lo = base, size = n;
     return true;
   }
   bool need(bool ok, int code, const char* fmt, const char* a = "", long long b = 0) {
@@ -1198,7 +1222,7 @@ int llm_verify_tree(const llm_verify_tree_args* a, void* cuda_stream) {
     return c.rc;
   if (a->probs &&
       (!c.need(a->vocab >= 1 && a->vocab <= (1 << 30), LLM_ERR_INVALID_ARG, "vocab is not in 1..2^30") ||
-       !c.device("probs", a->probs, 4) || !c.device("uniforms", a->uniforms, 4) ||
+       !c.device("uniforms", a->uniforms, 4) || !c.device("probs", a->probs, 4) ||
        (a->draft_probs && !c.device("draft_probs", a->draft_probs, 4)) ||
        !c.need(a->probs_strides[0] >= 0 && a->probs_strides[1] >= 0 && a->draft_strides[0] >= 0 &&
                    a->draft_strides[1] >= 0,
