@@ -28,6 +28,12 @@
 // issues every MMA. What a softmax waits for overlaps the other CTA on the SM,
 // where shared and tensor memory let two fit; S and P have two buffers where that
 // costs no second CTA, and the scores are then a tile ahead.
+// Measured (GB300): 32 sequences x 8 nodes, 16/8 heads x 128 over 512..2048 rows
+// 36.6 us, 70 % of the copy rate: what two CTAs' rings hold on their way to an SM.
+// 16 x 64 nodes, 32/4 heads x 64 over 1024..8192 rows 84 us: a tile's chain from
+// scores to probabilities to P V (3,200 cycles, two CTAs an SM) and the uneven last
+// CTAs. 16 fp32 nodes over 4097 rows 12.2 us and one over 256 rows 5.9: start, a few
+// tiles, join.
 #pragma once
 #include <cuda.h>
 
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       if (t >= 0) ok = tc_wait_warp(p_full + x, (DB == 2 ? t >> 1 : t) & 1, s_abort, p.status);
       // S of tile t0 + t + DB goes into the buffer just read. With one buffer it
       // is first: the softmax goes on with it while O is brought up to date
-      // (16 x 64 nodes over 1024..8192 rows: 99.8 us with it second).
+      // (16 x 64 nodes over 1024..8192 rows: 91.4 us so, 99.8 with it second).
 #pragma unroll
       for (int first = 1; first >= 0; --first) {
         if ((first == 1) == (DB == 1)) {
@@ -886,8 +892,9 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   if constexpr (C::two) {
     // Split the keys until every SM has a CTA, and to fill both places while 16
     // tiles are left for each: more splits cost their merges
-    // (32 sequences x 8 kv heads, 17 tiles: 43 / 48 / 67 us for 1 / 2 / 4; 16 x 4 x 4 row
-    // tiles, 65 tiles: 129 / 109 / 132; 8 clusters of 513 tiles: 667 / 340 / 179 / 96 for 1 to 8).
+    // (32 sequences x 8 kv heads, 17 tiles: 37 / 39 / 45 us for 1 / 2 / 3; 16 x 4 x 4 row
+    // tiles, 65 tiles: 104 / 85 / 94 / 102 for 1 to 4; 32 clusters of 34 fp32 tiles 12.3 /
+    // 12.1 / 24 for 4 / 8 / 16).
     while (S < kMaxSplits && S < tiles && (clusters * S < n_sm || (clusters * S < 2 * n_sm && tiles / (2 * S) >= 16))) S *= 2;
   } else {
     static ClusterCount at_once;
@@ -907,9 +914,9 @@ cudaError_t launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStre
   // Rows of a CTA: as many as there are (K and V are read once for them), in two
   // blocks once there are 32 (one block's softmax overlaps the other's MMAs); but
   // fewer while the clusters, split eight ways, would leave SMs without a CTA
-  // (16 nodes x 8 heads over 4097 rows, fp32: 16 / 32 / 64 rows 16.5 / 18.6 / 20.6 us).
-  // 128 rows at most: 256 fill tensor memory and leave one CTA on an SM (16 x 64
-  // nodes over 1024..8192 rows: 119 against 109 us).
+  // (16 nodes x 8 heads over 4097 rows, fp32: 16 / 32 rows 12.1 / 14.2 us).
+  // 128 rows at most (16 x 64 nodes over 1024..8192 rows: 32 / 64 / 128 rows 155 / 147 /
+  // 85 us): 256 would fill tensor memory and leave one CTA on an SM.
   const int M = p.n * p.gq, most = f32 ? 32 : 128;
   int N = 16;
   while (N < M && N < most) N *= 2;

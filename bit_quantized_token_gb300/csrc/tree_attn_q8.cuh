@@ -11,6 +11,10 @@
 // - The sums of p are the threads' own (16 rows a block), added at the end.
 // A non-finite scale of a tree row is left out of the products and added at the
 // end for the nodes that see the row.
+// Bound: a tile takes ~2 us in a CTA that has the SM to itself, a third of the
+// issue slots for the widening, the rest latency of the chain from scores to P V.
+// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 36.6 us, 16 % of the
+// copy rate (bf16 rows are twice the bytes and wait for memory instead).
 #pragma once
 #pragma once
 #include "tree_attn.cuh"
