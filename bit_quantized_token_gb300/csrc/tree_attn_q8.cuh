@@ -4,17 +4,16 @@
 //   for the K tiles (exact), eight for the V tiles.
 // - S^T of each group of 32 dims has columns of its own; the softmax thread, which
 //   is one key, adds them with its key's scales: s = sum_g ks_g S_g.
-// - A value is its code times its scale, 8 + 11 bits, rounded to bf16 (2^-9 rms of
-//   it, a fifth of what the codes' own rounding left; fp32 queries: three bf16 parts,
-//   exact, each a tile of its own). Two parts took 36.5 us where one takes 32.2 (below):
-//   shared memory's bandwidth is the bound. A form with the scales in the
-//   probabilities, P for every group, took twice the time of two parts.
+// - A value is its code times its scale, 8 + 11 bits, in two bf16 parts (16 bits;
+//   fp32 queries: three, exact), each a tile of its own. A form with the scales in
+//   the probabilities, P for every group, took twice the time: the softmax wrote
+//   four times as much, and three quarters of the product were not used.
 // - The sums of p are the threads' own (16 rows a block), added at the end.
 // A non-finite scale of a tree row is left out of the products and added at the
 // end for the nodes that see the row.
-// Bound: shared memory. A tile of 128 dims moves ~230 KB through it (codes in and
-// out, bf16 in, the MMAs' fetches, P), 1,800 cycles at 128 bytes a cycle.
-// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 32.2 us, 18 % of the
+// Bound: a tile takes ~2 us in a CTA that has the SM to itself, a third of the
+// issue slots for the widening, the rest latency of the chain from scores to P V.
+// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 36.6 us, 16 % of the
 // copy rate (bf16 rows are twice the bytes and wait for memory instead).
 #pragma once
 #pragma once
@@ -79,7 +78,7 @@ __device__ __forceinline__ void i8x4_scaled(uint32_t w, float f, uint2 (&out)[NP
 template <int HD, bool F32, int G>
 struct TreeQ8 {
   static constexpr int NB = 16, N = NB * G, BK = 128, H = HD / 64, NG = HD / 32;
-  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2, NV = F32 ? 3 : 1;  // parts of the queries, of P, of V
+  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
   static constexpr int NS = NQ * NB, NO = NP * NB;   // columns of a group's S and O of a block
   static constexpr int NSA = G * NS, NOA = G * NO;   // of all blocks: one product serves them
   static constexpr int NT = 32 * (4 * G + 12 + 2);
@@ -88,8 +87,8 @@ struct TreeQ8 {
   static constexpr int kQ = NQ * N * HD * 2;
   static constexpr int kOffRow = 1024;
   static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4);
-  static constexpr int PB = (1 + NV) * kConv + 2 * kP + kQ + kSmall + 1024 + 4 * kRaw <= 232448 ? 2 : 1;  // buffers of P
-  static constexpr int kFixed = (1 + NV) * kConv + PB * kP + kQ + kSmall + 1024;
+  static constexpr int PB = (1 + NP) * kConv + 2 * kP + kQ + kSmall + 1024 + 4 * kRaw <= 232448 ? 2 : 1;  // buffers of P
+  static constexpr int kFixed = (1 + NP) * kConv + PB * kP + kQ + kSmall + 1024;
   static constexpr int fit = (232448 - kFixed) / (2 * kRaw);
   static constexpr int R = fit < 4 ? fit : 4;                             // raw tiles of each of K and V
   static constexpr int kSmem = kFixed + 2 * R * kRaw;
@@ -102,15 +101,15 @@ template <int HD, bool F32, int G>
 __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel(const __grid_constant__ TreeAttnTcParams tp) {
   using C = TreeQ8<HD, F32, G>;
   constexpr int N = C::N, NT = C::NT, NB = C::NB, NQ = C::NQ, NP = C::NP, NG = C::NG, BK = C::BK, H = C::H, R = C::R;
-  constexpr int NS = C::NS, NO = C::NO, NSA = C::NSA, NOA = C::NOA, PB = C::PB, NV = C::NV;
+  constexpr int NS = C::NS, NO = C::NO, NSA = C::NSA, NOA = C::NOA, PB = C::PB;
   constexpr int kConvWarp = 4 * G, kTmaWarp = 4 * G + 12, kMmaWarp = 4 * G + 13;
   constexpr float kNone = -3e38f;
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  uint8_t* sconv = sm;                        // K, V's parts: [1 + NV][H][128 keys][128 B]
-  uint8_t* sraw = sconv + (1 + NV) * C::kConv;  // [2][R] tiles of codes
+  uint8_t* sconv = sm;                        // K, V's parts: [1 + NP][H][128 keys][128 B]
+  uint8_t* sraw = sconv + (1 + NP) * C::kConv;  // [2][R] tiles of codes
   uint8_t* sp = sraw + 2 * R * C::kRaw;       // [PB] P: columns [block][part][row]
   uint8_t* sq = sp + PB * C::kP;                   // [H][G][NQ][NB][128 B]
   uint8_t* small = sq + C::kQ;
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);             // [N]
   float* sfac = reinterpret_cast<float*>(sml + N);                   // [N]
   uint8_t* sjoin = sconv + N * HD * 4;                               // the other ranks' parts at the end
-  static_assert(N * HD * 4 + kJoin<HD, N> <= (1 + NV) * C::kConv, "room for them");
+  static_assert(N * HD * 4 + kJoin<HD, N> <= (1 + NP) * C::kConv, "room for them");
 
   if (tid == 32 * kTmaWarp) {
     *s_abort = 0;
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         const int n_steps = steps(t);
         const uint64_t dp = tc_desc(up + y * C::kP, BK * 128, 1024, 2);
 #pragma unroll 1
-        for (int k = 0; k < NV; ++k) {
+        for (int k = 0; k < NP; ++k) {
           // at 64 dims, rows 64.. are whatever lies behind the part: their products are not read
           const uint64_t da = tc_desc(uv + k * C::kConv, BK * 128, 1024, 2);
           if (elect_lane()) {
@@ -358,11 +357,11 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         for (int c = 0; c < NC; ++c) {
           const int at = 2 * ((half * NC + c) & 3);
           const float f = 2 * c < NC ? f0 : f1;
-          uint2 x[4][NV];
-          i8x4_scaled<NV>(w[c].x, f, x[0]), i8x4_scaled<NV>(w[c].y, f, x[1]);
-          i8x4_scaled<NV>(w[c].z, f, x[2]), i8x4_scaled<NV>(w[c].w, f, x[3]);
+          uint2 x[4][NP];
+          i8x4_scaled<NP>(w[c].x, f, x[0]), i8x4_scaled<NP>(w[c].y, f, x[1]);
+          i8x4_scaled<NP>(w[c].z, f, x[2]), i8x4_scaled<NP>(w[c].w, f, x[3]);
 #pragma unroll
-          for (int k = 0; k < NV; ++k) {
+          for (int k = 0; k < NP; ++k) {
             *reinterpret_cast<uint4*>(conv + k * C::kConv + 16 * (at ^ (r & 7))) = make_uint4(x[0][k].x, x[0][k].y, x[1][k].x, x[1][k].y);
             *reinterpret_cast<uint4*>(conv + k * C::kConv + 16 * ((at + 1) ^ (r & 7))) = make_uint4(x[2][k].x, x[2][k].y, x[3][k].x, x[3][k].y);
           }

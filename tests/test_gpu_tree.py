@@ -12,7 +12,7 @@ output element, with A = sum_j p_j |v_j| (the largest any error in p can weigh):
   output: one rounding, 2^-8 |o| (bf16) or 2^-24 |o| (fp32).
 The relative errors of o and l add: tol = round |o| + A (2 ds + 2^-21 + part + 2 (N + 64) 2^-23).
 int8 rows: the products of a group's scale add 2 2^-24 to each score term (inside the 8 above), and a value, code
-  times scale, is rounded to bf16 for bf16 queries, 2^-8 of it, so 2^-8 A in all (three parts for fp32 hold it exactly).
+  times scale, is rounded to two bf16 parts for bf16 queries, (2^-8)^2 of it (three for fp32 hold it exactly).
 """
 import math
 
@@ -118,7 +118,7 @@ class Problem:
                     if bf and self.kv == "bf16" and self.n * self.gq > 64:
                         part = 2 * 2.0 ** -8
                     if bf and self.kv == "q8":
-                        part += 2.0 ** -8
+                        part += 2.0 ** -16
                     tol = rnd * o.abs() + A * (2 * ds + 2.0 ** -21 + part + 2 * (K.shape[0] + 64) * 2.0 ** -23)
                     err = (got - o).abs()
                     assert (err <= tol).all(), (b, i, h, float((err / tol).max()))
