@@ -5,15 +5,16 @@
 // - S^T of each group of 32 dims has columns of its own; the softmax thread, which
 //   is one key, adds them with its key's scales: s = sum_g ks_g S_g.
 // - A value is its code times its scale, 8 + 11 bits, in two bf16 parts (16 bits;
-//   fp32 queries: three, exact), each a tile of its own. A form with the scales in
-//   the probabilities, P for every group, took twice the time: the softmax wrote
-//   four times as much, and three quarters of the product were not used.
+//   fp32 queries: three, exact), each a tile of its own. One part took 32.3 us where
+//   two take 36.5 (below), with 1.42 times the error of an exactly rounded output. A form
+//   with the scales in the probabilities, P for every group, took twice the time: the
+//   softmax wrote four times as much, and three quarters of the product were not used.
 // - The sums of p are the threads' own (16 rows a block), added at the end.
 // A non-finite scale of a tree row is left out of the products and added at the
 // end for the nodes that see the row.
-// Bound: a tile takes ~2 us in a CTA that has the SM to itself, a third of the
-// issue slots for the widening, the rest latency of the chain from scores to P V.
-// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 36.6 us, 16 % of the
+// Bound: shared memory. A tile of 128 dims moves ~310 KB through it (codes in and
+// out, bf16 in, the MMAs' fetches, P), 2,400 cycles at 128 bytes a cycle of its 3,600.
+// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 36.5 us, 16 % of the
 // copy rate (bf16 rows are twice the bytes and wait for memory instead).
 #pragma once
 #pragma once
