@@ -76,6 +76,15 @@ __device__ __forceinline__ void i8x4_scaled(uint32_t w, float f, uint2 (&out)[NP
   for (int k = 0; k < NP; ++k) out[k] = make_uint2(a[k], b[k]);
 }
 
+// A from tensor memory: lane = row, 16 bf16 of K a step in 8 columns
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
 template <int HD, bool F32, int G>
 struct TreeQ8 {
   static constexpr int NB = 16, N = NB * G, BK = 128, H = HD / 64, NG = HD / 32;
@@ -88,14 +97,15 @@ struct TreeQ8 {
   static constexpr int kQ = NQ * N * HD * 2;
   static constexpr int kOffRow = 1024;
   static constexpr int kSmall = kOffRow + N * (8 + 4 + 16 + 8 + 4);
-  static constexpr int PB = (1 + NP) * kConv + 2 * kP + kQ + kSmall + 1024 + 4 * kRaw <= 232448 ? 2 : 1;  // buffers of P
-  static constexpr int kFixed = (1 + NP) * kConv + PB * kP + kQ + kSmall + 1024;
+  static constexpr int PB = NP * kConv + 2 * kP + kQ + kSmall + 1024 + 4 * kRaw <= 232448 ? 2 : 1;  // buffers of P
+  static constexpr int kFixed = NP * kConv + PB * kP + kQ + kSmall + 1024;
   static constexpr int fit = (232448 - kFixed) / (2 * kRaw);
   static constexpr int R = fit < 4 ? fit : 4;                             // raw tiles of each of K and V
   static constexpr int kSmem = kFixed + 2 * R * kRaw;
-  static constexpr int kUsed = 2 * NG * NSA + NOA;                        // two buffers of S: the scores are a tile ahead
+  static constexpr int kAtK = 2 * NG * NSA + NOA;                         // two buffers of S: the scores are a tile ahead
+  static constexpr int kUsed = kAtK + HD / 2;                             // and the widened K tile
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(R >= 2 && kUsed <= 512 && N * HD * 4 <= 2 * kConv && G * 4096 <= kP, "fits");
+  static_assert(R >= 2 && kUsed <= 512 && G * 4096 <= kP, "fits");
 };
 
 template <int HD, bool F32, int G>
@@ -109,8 +119,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
-  uint8_t* sconv = sm;                        // K, V's parts: [1 + NP][H][128 keys][128 B]
-  uint8_t* sraw = sconv + (1 + NP) * C::kConv;  // [2][R] tiles of codes
+  uint8_t* sconv = sm;                        // V's parts: [NP][H][128 keys][128 B]
+  uint8_t* sraw = sconv + NP * C::kConv;      // [2][R] tiles of codes
   uint8_t* sp = sraw + 2 * R * C::kRaw;       // [PB] P: columns [block][part][row]
   uint8_t* sq = sp + PB * C::kP;                   // [H][G][NQ][NB][128 B]
   uint8_t* small = sq + C::kQ;
@@ -127,7 +137,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   float2* sml = reinterpret_cast<float2*>(sm_w + 4 * N);             // [N]
   float* sfac = reinterpret_cast<float*>(sml + N);                   // [N]
   uint8_t* sjoin = sconv + N * HD * 4;                               // the other ranks' parts at the end
-  static_assert(N * HD * 4 + kJoin<HD, N> <= (1 + NP) * C::kConv, "room for them");
+  static_assert(N * HD * 4 + kJoin<HD, N> <= NP * C::kConv, "room for them");
 
   if (tid == 32 * kTmaWarp) {
     *s_abort = 0;
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
     constexpr uint32_t idesc_s = base_i | ((uint32_t)(NSA >> 3) << 17);
     constexpr uint32_t idesc_o = base_i | ((uint32_t)(NOA >> 3) << 17) | (1u << 15) | (1u << 16);
-    const uint32_t uq = smem_u32(sq), up = smem_u32(sp), uk = smem_u32(sconv), uv = uk + C::kConv;
+    const uint32_t uq = smem_u32(sq), up = smem_u32(sp), uv = smem_u32(sconv);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
 #pragma unroll 1
@@ -274,12 +284,11 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         tc_fence_after();
 #pragma unroll 1
         for (int u = 0; u < H; ++u) {
-          const uint64_t da = tc_desc(uk + u * BK * 128, 16, 1024, 2);
           const uint64_t dq = tc_desc(uq + u * NSA * 128, 16, 1024, 2);
           if (elect_lane()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tc_mma(tm + (x * NG + 2 * u + ks / 2) * NSA, da + 2 * ks, dq + 2 * ks, idesc_s, ks & 1);
+              tc_mma_ts(tm + (x * NG + 2 * u + ks / 2) * NSA, tm + C::kAtK + 32 * u + 8 * ks, dq + 2 * ks, idesc_s, ks & 1);
           }
           __syncwarp();
         }
@@ -302,7 +311,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     const int r = (warp & 3) * 32 + lane;
     const int sel = HD == 128 ? r & 7 : (r >> 1) & 3;
     if (!of_v) {
-      uint8_t* conv = sconv + r * 128;
+      const uint32_t tk = tmem + ((uint32_t)(warp & 3) << 21) + C::kAtK;
 #pragma unroll 1
       for (int t = 0; t < n_own; ++t) {
         const int slot = t % R;
@@ -312,21 +321,28 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + 16 * (c ^ sel));
         if (t > 0) tc_wait(conv_empty, (t - 1) & 1, s_abort, p.status);
+        __syncwarp();
+        tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < HD / 16; ++c) {
-          const uint2 a = i8x4_to_bf16(w[c].x), d = i8x4_to_bf16(w[c].y), e = i8x4_to_bf16(w[c].z), f = i8x4_to_bf16(w[c].w);
-          uint8_t* dst = conv + (c / 4) * BK * 128;
-          *reinterpret_cast<uint4*>(dst + 16 * ((2 * (c & 3)) ^ (r & 7))) = make_uint4(a.x, a.y, d.x, d.y);
-          *reinterpret_cast<uint4*>(dst + 16 * ((2 * (c & 3) + 1) ^ (r & 7))) = make_uint4(e.x, e.y, f.x, f.y);
+        for (int c = 0; c < HD / 16; c += 2) {
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint2 v = i8x4_to_bf16((&w[c + i / 4].x)[i & 3]);
+            x[2 * i] = __uint_as_float(v.x), x[2 * i + 1] = __uint_as_float(v.y);
+          }
+          tc_st16(tk + 8 * c, x);
         }
+        tc_wait_st();
         fence_async_smem();
+        tc_fence_before();
         mbar_arrive(raw_empty + slot);
         mbar_arrive(conv_full);
       }
     } else {
       constexpr int NC = HD / 32;  // chunks of 16 codes a thread
       const int half = warp >= kConvWarp + 8;
-      uint8_t* conv = sconv + C::kConv + (HD == 128 ? half * BK * 128 : 0) + r * 128;
+      uint8_t* conv = sconv + (HD == 128 ? half * BK * 128 : 0) + r * 128;
       // the scales of the thread's codes (of one or two groups) in tile t: two halves a word
       auto scales = [&](int t) -> uint32_t {
         const bool tree = t >= n_pre;
