@@ -1,20 +1,23 @@
 // Tree attention over int8 rows with a scale per 32 values, on the tensor cores
 // (the products, roles and references of tree_attn.cuh; what differs:)
 // - Converter warps widen the codes, which TMA brings as they are, to bf16: four
-//   for the K tiles (exact), eight for the V tiles.
+//   for the K tiles (exact; into tensor memory, lane = key, as the product's A: a
+//   third of the tile's shared memory traffic less), eight for the V tiles.
 // - S^T of each group of 32 dims has columns of its own; the softmax thread, which
 //   is one key, adds them with its key's scales: s = sum_g ks_g S_g.
 // - A value is its code times its scale, 8 + 11 bits, in two bf16 parts (16 bits;
-//   fp32 queries: three, exact), each a tile of its own. One part took 32.3 us where
-//   two take 36.5 (below), with 1.42 times the error of an exactly rounded output. A form
+//   fp32 queries: three, exact), each a tile of its own. One part took 12 % less
+//   time, with 1.42 times the error of an exactly rounded output. A form
 //   with the scales in the probabilities, P for every group, took twice the time: the
 //   softmax wrote four times as much, and three quarters of the product were not used.
 // - The sums of p are the threads' own (16 rows a block), added at the end.
 // A non-finite scale of a tree row is left out of the products and added at the
 // end for the nodes that see the row.
-// Bound: shared memory. A tile of 128 dims moves ~310 KB through it (codes in and
-// out, bf16 in, the MMAs' fetches, P), 2,400 cycles at 128 bytes a cycle of its 3,600.
-// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 36.5 us, 16 % of the
+// Bound: a tile takes ~3,500 cycles; widening V and P V take turns on its one buffer
+// (1,500 and 1,000), and the ~250 KB that pass through shared memory (codes in and
+// out, V's parts, the MMAs' fetches, P) are 1,900 of them. Giving the buffer back in
+// two halves took 10 to 15 % more: all of it competes for the same bandwidth.
+// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 35.8 us, 16 % of the
 // copy rate (bf16 rows are twice the bytes and wait for memory instead).
 #pragma once
 #pragma once
