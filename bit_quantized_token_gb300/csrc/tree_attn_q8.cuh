@@ -2,7 +2,7 @@
 // (the products, roles and references of tree_attn.cuh; what differs:)
 // - Converter warps widen the codes, which TMA brings as they are, to bf16: four
 //   for the K tiles (exact; into tensor memory, lane = key, as the product's A: a
-//   third of the tile's shared memory traffic less), eight for the V tiles.
+//   fifth of the tile's shared memory traffic less), eight for the V tiles.
 // - S^T of each group of 32 dims has columns of its own; the softmax thread, which
 //   is one key, adds them with its key's scales: s = sum_g ks_g S_g.
 // - A value is its code times its scale, 8 + 11 bits, in two bf16 parts (16 bits;
@@ -19,7 +19,6 @@
 // two halves took 10 to 15 % more: all of it competes for the same bandwidth.
 // 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 35.8 us, 16 % of the
 // copy rate (bf16 rows are twice the bytes and wait for memory instead).
-#pragma once
 #pragma once
 #include "tree_attn.cuh"
 
