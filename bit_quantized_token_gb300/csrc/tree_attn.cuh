@@ -32,7 +32,7 @@
 // 36.6 us, 70 % of the copy rate: what two CTAs' rings hold on their way to an SM.
 // 16 x 64 nodes, 32/4 heads x 64 over 1024..8192 rows 84 us: a tile's chain from
 // scores to probabilities to P V (3,200 cycles, two CTAs an SM) and the uneven last
-// CTAs. 16 fp32 nodes over 4097 rows 12.2 us and one over 256 rows 5.9: start, a few
+// CTAs. 16 fp32 nodes over 4097 rows 12.7 us and one over 256 rows 5.9: start, a few
 // tiles, join.
 #pragma once
 #include <cuda.h>
@@ -53,6 +53,12 @@ struct TreeAttnTcParams {
 };
 
 constexpr int kMaxSplits = 16;  // CTAs of a cluster
+// For fp32 queries, tiles that O adds up in tensor memory. An MMA cuts its sum off
+// where an add would round, so long sums come out low: 1e-6 of the output after 8
+// tiles and 8e-6 after 125 (int8, three parts of V: 3e-6 and 1e-5), against 2e-7 for
+// sums that round. Every two tiles (int8: each) the sums go to registers, which
+// round: 4e-7, at 0.5 us of 12.3 (16 nodes over 4097 rows).
+constexpr int kTogether = 2;
 
 template <int HD, bool F32, int NB, int G>
 struct TreeTc {
@@ -536,7 +542,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
               for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 2 KB further
                 if (ks < n_steps)
                   tc_mma(tm + DB * C::NSA + u * C::NOA, da + ks * (uint64_t)128 - ((uint64_t)(ks * 128) << 16),
-                         dp + (ks * step_p >> 4), idesc_o, t > 0 || ks > 0);
+                         dp + (ks * step_p >> 4), idesc_o, (F32 ? t % kTogether : t) > 0 || ks > 0);
             }
             __syncwarp();
             tc_commit(empty + slot);
@@ -576,6 +582,26 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 #pragma unroll
         for (int j = 0; j < W; ++j) v[0][j] += v[1][j] + v[2][j];
     };
+    float acc[F32 ? H : 1][16];  // fp32: O of the tiles that have left tensor memory
+    static_assert(!F32 || NB == 16, "a thread's sums");
+    auto part_of = [&](float (&x)[16], uint32_t at) {  // this thread's O, its parts added, the small ones first
+      float v[NP][16];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) tc_ld(v[k], at + k * NB);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) tc_wait_ld(v[k]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[j] = v[NP - 1][j];
+#pragma unroll
+        for (int k = NP - 2; k >= 0; --k) x[j] += v[k][j];
+      }
+    };
+    if constexpr (F32)
+#pragma unroll
+      for (int u = 0; u < H; ++u)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[u][j] = 0.f;
     for (int t = t0; t < t1; ++t) {
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
       const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
@@ -710,6 +736,25 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
             tc_st16(at, s);
           }
           tc_wait_st();
+          if constexpr (F32)
+#pragma unroll
+            for (int u = 0; u < H; ++u)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[u][j] *= sfac[g * NB + j];
+        }
+      }
+      if constexpr (F32) {
+        if (t > t0 && (t - t0) % kTogether == 0) {  // the next P V starts anew
+          tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < H; ++u) {
+            float x[16];
+            part_of(x, tO + u * C::NOA);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[u][j] += x[j];
+          }
         }
       }
       if (!whole) {
@@ -764,25 +809,22 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     if (p.S > 1) cluster_arrive();
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
     const bool have = t0 < t1;
-#pragma unroll 1
+#pragma unroll(F32 ? H : 1)
     for (int c0 = 0; c0 < NB * H; c0 += 16) {
       const int u = c0 / NB, r0 = c0 % NB;
-      float s[NP][16];
+      float x[16];
       if (have) {
+        part_of(x, tO + u * C::NOA + r0);
+        if constexpr (F32)
 #pragma unroll
-        for (int k = 0; k < NP; ++k) tc_ld(s[k], tO + u * C::NOA + k * NB + r0);
-#pragma unroll
-        for (int k = 0; k < NP; ++k) tc_wait_ld(s[k]);
+          for (int j = 0; j < 16; ++j) x[j] += acc[u][j];
       }
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        float x = 0.f;
-        if (have)
-#pragma unroll
-          for (int k = NP - 1; k >= 0; --k) x += s[k][j];
-        if (key < 64) so[(r0 + j) * HD + 64 * u + key] = x;
-        sum = lane == j ? x : sum;
+        if (!have) x[j] = 0.f;
+        if (key < 64) so[(r0 + j) * HD + 64 * u + key] = x[j];
+        sum = lane == j ? x[j] : sum;
       }
       // the lanes from 64 on all hold the sums: lane j of the third warp keeps row j's
       if (u == 0 && (warp & 3) == 2 && lane < 16) sml[g * NB + r0 + lane] = make_float2(-m[r0 + lane], sum);

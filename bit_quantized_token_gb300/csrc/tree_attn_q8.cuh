@@ -265,14 +265,14 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         const int n_steps = steps(t);
         const uint64_t dp = tc_desc(up + y * C::kP, BK * 128, 1024, 2);
 #pragma unroll 1
-        for (int k = 0; k < NP; ++k) {
+        for (int k = NP - 1; k >= 0; --k) {  // the small part first: fewer steps cut off at the sum's own size
           // at 64 dims, rows 64.. are whatever lies behind the part: their products are not read
           const uint64_t da = tc_desc(uv + k * C::kConv, BK * 128, 1024, 2);
           if (elect_lane()) {
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
               if (ks < n_steps)
-                tc_mma(tm + 2 * NG * NSA, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o, t > 0 || k > 0 || ks > 0);
+                tc_mma(tm + 2 * NG * NSA, da + ks * (uint64_t)128, dp + ks * (uint64_t)128, idesc_o, (!F32 && t > 0) || k < NP - 1 || ks > 0);
           }
           __syncwarp();
         }
@@ -431,9 +431,25 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       return __half2float(__ushort_as_half((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu)));
     };
     scales(t0);
-    float l[NB];
+    float l[NB], acc[F32 ? NB : 1];  // fp32: O of the tiles that have left tensor memory
 #pragma unroll
-    for (int j = 0; j < NB; ++j) l[j] = 0.f;
+    for (int j = 0; j < NB; ++j) {
+      l[j] = 0.f;
+      if constexpr (F32) acc[j] = 0.f;
+    }
+    auto part_of = [&](float (&x)[NB]) {  // this thread's O, its parts added, the small ones first
+      float o[NP][NB];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) tc_ld(o[k], tO + k * NB);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) tc_wait_ld(o[k]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        x[j] = o[NP - 1][j];
+#pragma unroll
+        for (int k = NP - 2; k >= 0; --k) x[j] += o[k][j];
+      }
+    };
 #pragma unroll 1
     for (int t = t0; t < t1; ++t) {
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len, valid = valid_at(t);
@@ -552,6 +568,9 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
               tc_st16(tO + c0, o);
             }
             tc_wait_st();
+            if constexpr (F32)
+#pragma unroll
+              for (int j = 0; j < NB; ++j) acc[j] *= sfac[g * NB + j];
           }
           continue;
         }
@@ -572,6 +591,17 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         }
         break;
       }
+      if constexpr (F32) {
+        if (i_own > 0) {  // every tile: its P V, three times the steps of a bf16 tile's, starts anew
+          tc_wait(o_done + (i_own - 1) % PB, ((i_own - 1) / PB) & 1, s_abort, p.status);
+          __syncwarp();
+          tc_fence_after();
+          float x[NB];
+          part_of(x);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) acc[j] += x[j];
+        }
+      }
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(p_full + y);
@@ -583,21 +613,15 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     if (p.S > 1) cluster_arrive();
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
     if (key < HD) {  // lanes are dims
-      float o[NP][NB];
+      float x[NB];
       if (n_own > 0) {
+        part_of(x);
+        if constexpr (F32)
 #pragma unroll
-        for (int k = 0; k < NP; ++k) tc_ld(o[k], tO + k * NB);
-#pragma unroll
-        for (int k = 0; k < NP; ++k) tc_wait_ld(o[k]);
+          for (int j = 0; j < NB; ++j) x[j] += acc[j];
       }
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        float x = 0.f;
-        if (n_own > 0)
-#pragma unroll
-          for (int k = NP - 1; k >= 0; --k) x += o[k][j];
-        so[j * HD + key] = x;
-      }
+      for (int j = 0; j < NB; ++j) so[j * HD + key] = n_own > 0 ? x[j] : 0.f;
       const unsigned long long bad = *s_bad;
       if (bad && t1 == n_tiles) {  // tree values with non-finite scales, where they are seen
         const int64_t at = (int64_t)b * p.tree.seq + (int64_t)hkv * p.tree.head + key;

@@ -421,8 +421,10 @@ typedef struct {
 
 /* out = softmax(scale q K^T over the visible rows) V; query head h reads kv
  * head h / (n_heads / cache heads). Products on the tensor cores, sums in
- * fp32; fp32 queries and their probabilities carry 24 bits, for bf16 queries
- * the probabilities at least 8 and int8 rows' values 16 (rounding below that of the output). A node that sees no row gets
+ * fp32 (for fp32 queries the tensor cores, which cut off, add up 256 rows at
+ * most); fp32 queries and their probabilities carry 24 bits, for bf16 queries
+ * the probabilities at least 8 and int8 rows' values 16 (rounding below that of
+ * the output). A node that sees no row gets
  * zeros. A row that a node does not see has no influence on it, whatever it
  * holds. With n_nodes = 1 and tree = NULL this is one decode token's
  * attention over a cache that already holds its row. */

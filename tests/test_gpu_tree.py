@@ -208,6 +208,28 @@ def test_attention_repeats_bit_for_bit(n, kv, hd):
         assert torch.equal(p.call(), first)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+def test_attention_fp32_sums_do_not_drift(kv):
+    """fp32 queries over rows of one CTA each: the outputs are not low on the whole. An MMA step cuts off up to
+    2^-23 of its sum, half of that on average; of the steps between two roundings at most 16 add to sums of full
+    size, so the mean is off by less than 16 2^-24 (sums of 250 steps would be off by several times that)."""
+    L = 4000
+    p = Problem(B=20, n=2, Hkv=8, gq=2, hd=64, cap=L + 1, lens=(L,) * 20, q="f32", kv=kv)
+    p.call()
+    k, v, tk, tv = (values(a, b) for a, b in ((p.k, p.ks), (p.v, p.vs), (p.tk, p.tks), (p.tv, p.tvs)))
+    off = size = 0.0
+    for b in (0, 19):
+        for i in range(2):
+            seen = [j for j in range(2) if int(p.mask[b, i]) >> j & 1]
+            for h in range(0, 16, 3):
+                K = torch.cat([k[b, h // 2, :L], tk[b, h // 2][seen]]).double()
+                V = torch.cat([v[b, h // 2, :L], tv[b, h // 2][seen]]).double()
+                o = torch.softmax(K @ p.q[b, i, h].double() * 64 ** -0.5, 0) @ V
+                off += float(((p.out[b, i, h].double() - o) * o).sum())
+                size += float((o * o).sum())
+    assert abs(off / size) < 16 * 2.0 ** -24, off / size
+
+
 def test_attention_scores_far_apart_and_scale():
     for scale in (0.0, -0.3, 4.0):
         p = Problem(B=1, n=4, cap=200, lens=(200,), q="f32")
