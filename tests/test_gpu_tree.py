@@ -10,6 +10,7 @@ output element, with A = sum_j p_j |v_j| (the largest any error in p can weigh):
   sums over N keys: N 2^-23 for each of o and l (rescaling included), joined over
     splits: 64 more.
   output: one rounding, 2^-8 |o| (bf16) or 2^-24 |o| (fp32).
+  underflow: a reference is at most the row's maximum, and a p below 2^-126 of its reference is 0: N 2^-126 max |v|.
 The relative errors of o and l add: tol = round |o| + A (2 ds + 2^-21 + part + 2 (N + 64) 2^-23).
 int8 rows: the products of a group's scale add 2 2^-24 to each score term (inside the 8 above), and a value, code
   times scale, is rounded to two bf16 parts for bf16 queries, (2^-8)^2 of it (three for fp32 hold it exactly).
@@ -120,6 +121,7 @@ class Problem:
                     if bf and self.kv == "q8":
                         part += 2.0 ** -16
                     tol = rnd * o.abs() + A * (2 * ds + 2.0 ** -21 + part + 2 * (K.shape[0] + 64) * 2.0 ** -23)
+                    tol = tol + K.shape[0] * 2.0 ** -126 * V.abs().max()
                     err = (got - o).abs()
                     assert (err <= tol).all(), (b, i, h, float((err / tol).max()))
                     worst = max(worst, float((err / tol).max()))
@@ -206,6 +208,20 @@ def test_attention_repeats_bit_for_bit(n, kv, hd):
     for _ in range(20):
         p.out.fill_(float("nan"))
         assert torch.equal(p.call(), first)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q", ["f32", "bf16"])
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+@pytest.mark.parametrize("n", [5, 24, 64])
+def test_attention_renews_its_references_in_any_tile(n, kv, q, hd):
+    """Every third node's scores spread over hundreds, so that tiles along a CTA's way renew the references of the
+    block's other rows too, whose sums so far are scaled."""
+    p = Problem(B=40, n=n, Hkv=4, gq=2, hd=hd, cap=1301, lens=(1300, 700, 1151, 260), q=q, kv=kv)
+    p.q[:, ::3] *= 60
+    p.call()
+    p.B = 4
+    p.check()
 
 
 @pytest.mark.parametrize("kv", ["bf16", "q8"])
