@@ -1148,8 +1148,9 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
   p.mask = a->mask;
   p.mask_seq = a->n_nodes;
   p.counts = a->counts;
-  p.c = (float)((double)a->scale * 1.4426950408889634);
-  if (std::fabs(p.c) < 1e-30f) p.c = 1e-30f;  // a scale of 0: every score below 2^-60, and c times -inf still -inf
+  // a scale of 0: every score's difference times c below 2^-60, and c times -inf still -inf
+  p.c = (float)std::fmin(std::fmax(std::fabs((double)a->scale) * 1.4426950408889634, 1e-30), 3e38);
+  p.neg = a->scale < 0.f;
   const cudaError_t es = status_word(c.dev, &p.status);
   if (es != cudaSuccess) return cuda_bad(es, "status word");
   p.B = a->n_seq;

@@ -122,7 +122,8 @@ struct TreeAttnParams {
   const uint64_t* mask;      // [B][n] tree rows that a node sees
   const int* counts;         // [B] nodes of a sequence, or null: n
   int64_t mask_seq;
-  float c;                   // scale * log2(e)
+  float c;                   // |scale| log2(e), above 0
+  bool neg = false;          // the scale is negative: the queries change their signs
   int B, n, Hkv, gq;
   FastDiv by_gq;
   int S;                     // CTAs of a cluster: splits of the keys

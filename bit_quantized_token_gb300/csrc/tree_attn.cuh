@@ -4,8 +4,11 @@
 // tree rows whose bits its mask sets. The gq query heads of a kv head and the
 // n nodes form M = n gq query rows against the same keys (row r: node r / gq,
 // head r % gq), so one pass over K and V serves all of them:
-//   o_r = sum_j 2^(c s_rj - m_r) v_j / sum_j 2^(c s_rj - m_r),  s_rj = q_r . k_j,
-// with c = scale log2(e), the references m_r and the sums in fp32.
+//   o_r = sum_j 2^(c (s_rj - m_r)) v_j / sum_j 2^(c (s_rj - m_r)),  s_rj = q_r . k_j,
+// with c = |scale| log2(e) (a negative scale turns the queries' signs), the
+// references m_r and the sums in fp32. A reference is a score: c s - m, one
+// operation less, has no reference within 2^60 of a row's largest once that passes
+// 2^30, where fp32 steps by 128.
 //
 // The products run transposed, so that the few query rows are the narrow side:
 //   S^T [128 keys x N rows] = K_tile Q^T     (A = the K tile as TMA lays it down, K-major)
@@ -30,7 +33,7 @@
 // costs no second CTA, and the scores are then a tile ahead.
 // Measured (GB300): 32 sequences x 8 nodes, 16/8 heads x 128 over 512..2048 rows
 // 36.6 us, 70 % of the copy rate: what two CTAs' rings hold on their way to an SM.
-// 16 x 64 nodes, 32/4 heads x 64 over 1024..8192 rows 84 us: a tile's chain from
+// 16 x 64 nodes, 32/4 heads x 64 over 1024..8192 rows 85 us: a tile's chain from
 // scores to probabilities to P V (3,200 cycles, two CTAs an SM) and the uneven last
 // CTAs. 16 fp32 nodes over 4097 rows 12.7 us and one over 256 rows 5.9: start, a few
 // tiles, join.
@@ -53,6 +56,7 @@ struct TreeAttnTcParams {
 };
 
 constexpr int kMaxSplits = 16;  // CTAs of a cluster
+constexpr float kNone = -3.402823466e38f;  // a row's reference before any visible score
 // For fp32 queries, tiles that O adds up in tensor memory. An MMA cuts its sum off
 // where an add would round, so long sums come out low: 1e-6 of the output after 8
 // tiles and 8e-6 after 125 (int8, three parts of V: 3e-6 and 1e-5), against 2e-7 for
@@ -281,7 +285,6 @@ constexpr int kJoin = N * HD * 4 + N * 12;
 template <int HD, bool F32, int N, int NT>
 __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float* so, const float2* sml, uint8_t* in,
                                             int rank, int b, int hkv, int m0, int rows) {
-  constexpr float kNone = -3e38f;
   constexpr int R4 = HD / 4;
   const int tid = threadIdx.x, S = p.S, share = (rows + S - 1) / S;
   const float4* part = reinterpret_cast<const float4*>(so);  // [S][share][R4]
@@ -313,7 +316,7 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
     for (int k = 1; k < S; ++k) M = fmaxf(M, ml[k * share + r].x);
     for (int k = 0; k < S; ++k) {
       const float2 x = ml[k * share + r];
-      const float w = x.x <= kNone ? 0.f : ex2(x.x - M);
+      const float w = x.x <= kNone ? 0.f : ex2((x.x - M) * p.c);
       L = fmaf(x.y, w, L);
       sw[k * share + r] = w;
     }
@@ -345,7 +348,6 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     const __grid_constant__ TreeAttnTcParams tp) {
   using C = TreeTc<HD, F32, NB, G>;
   constexpr int N = C::N, NT = C::NT, NST = C::NST, NQ = C::NQ, NP = C::NP, NG = HD / 32, BK = C::BK, H = C::H, DB = C::DB;
-  constexpr float kNone = -3e38f;  // the reference before any visible score
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -436,6 +438,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           const float4 lo = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off);
           const float4 hi = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off + 4);
           x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = p.neg ? -x[e] : x[e];
         }
         uint32_t part[4][3];
 #pragma unroll
@@ -444,9 +448,11 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         for (int k = 0; k < 3; ++k)
           *reinterpret_cast<uint4*>(dst + k * NB * 128) = make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
       } else {
-        *reinterpret_cast<uint4*>(dst) = node < cnt
-                                             ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off)
-                                             : make_uint4(0u, 0u, 0u, 0u);
+        uint4 w = node < cnt ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off)
+                             : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t turn = p.neg ? 0x80008000u : 0u;
+        w.x ^= turn, w.y ^= turn, w.z ^= turn, w.w ^= turn;
+        *reinterpret_cast<uint4*>(dst) = w;
       }
     }
     for (int i = tid; i < C::kOnes / 16; i += 128 * G)
@@ -563,7 +569,6 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     uint32_t tS = tmem + ((uint32_t)(warp & 3) << 21) + g * C::NS;
     const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + DB * C::NSA + g * C::NO;  // of 64 dims u: + u NOA
     float* m = sm_m + g * NB;  // the references, negated
-    const float masked = p.c < 0.f ? INFINITY : -INFINITY;  // times c: -inf (c is not 0)
     if (p.tree.k)
       for (int r = key; r < NB; r += 128) {
         const int node = p.by_gq.div(m0 + g * NB + r);
@@ -638,7 +643,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         float y = INFINITY;
         if (key < NB) {  // a thread per row (NB <= 128)
           const int j = tree ? __ffsll(srow[g * NB + key]) - 1 : 0;
-          if (j >= 0) y = first[j * NB + key] * p.c;
+          if (j >= 0) y = first[j * NB + key];
           m[key] = fabsf(y) < 1e38f ? -y : -kNone;
         }
         // every block's first scores have been read: P may be written
@@ -654,10 +659,10 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           if (tree) {
 #pragma unroll
             for (int j = 0; j < W; ++j)
-              if (!sees(c0 + j)) s[j] = masked;
+              if (!sees(c0 + j)) s[j] = -INFINITY;
           } else if (!whole && !valid) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) s[j] = masked;
+            for (int j = 0; j < W; ++j) s[j] = -INFINITY;
           }
           uint32_t part[W / 8][4][NP];
 #pragma unroll
@@ -666,8 +671,10 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
             for (int j = 0; j < 8; j += 4) {
               const float4 ref = *reinterpret_cast<const float4*>(m + c0 + 8 * h + j);
               float y[4] = {ref.x, ref.y, ref.z, ref.w};
-              fma2(y[0], y[1], s[8 * h + j], s[8 * h + j + 1], p.c, p.c);
-              fma2(y[2], y[3], s[8 * h + j + 2], s[8 * h + j + 3], p.c, p.c);
+              add2(y[0], y[1], y[0], y[1], s[8 * h + j], s[8 * h + j + 1]);
+              add2(y[2], y[3], y[2], y[3], s[8 * h + j + 2], s[8 * h + j + 3]);
+              mul2(y[0], y[1], y[0], y[1], p.c);
+              mul2(y[2], y[3], y[2], y[3], p.c);
               split_pack<NP>(ex2(y[0]), ex2(y[1]), part[h][j / 2]);
               split_pack<NP>(ex2(y[2]), ex2(y[3]), part[h][j / 2 + 1]);
               top = max_bf16x2(top, max_bf16x2(part[h][j / 2][0], part[h][j / 2 + 1][0]));
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 #pragma unroll
           for (int j = 0; j < W; ++j) {
             const bool in = tree ? sees(c0 + j) : valid;
-            float y = in ? v[0][j] * p.c : -INFINITY;
+            float y = in ? v[0][j] : -INFINITY;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
             if (lane == 0) sm_w[(warp & 3) * N + g * NB + c0 + j] = y;
@@ -719,7 +726,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           const float* w = sm_w + g * NB + key;
           const float old = -m[key], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
           m[key] = -now;
-          sfac[g * NB + key] = old == now ? 1.f : exp2f(old - now);
+          sfac[g * NB + key] = old == now ? 1.f : exp2f((old - now) * p.c);
         }
         group_sync(g);
         if (t > t0) {

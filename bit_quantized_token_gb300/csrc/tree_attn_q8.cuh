@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   constexpr int N = C::N, NT = C::NT, NB = C::NB, NQ = C::NQ, NP = C::NP, NG = C::NG, BK = C::BK, H = C::H, R = C::R;
   constexpr int NS = C::NS, NO = C::NO, NSA = C::NSA, NOA = C::NOA, PB = C::PB;
   constexpr int kConvWarp = 4 * G, kTmaWarp = 4 * G + 12, kMmaWarp = 4 * G + 13;
-  constexpr float kNone = -3e38f;
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,6 +197,8 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
           const float4 lo = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off);
           const float4 hi = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off + 4);
           x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = p.neg ? -x[e] : x[e];
         }
         uint32_t part[4][3];
 #pragma unroll
@@ -206,9 +207,11 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         for (int k = 0; k < 3; ++k)
           *reinterpret_cast<uint4*>(dst + k * NB * 128) = make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
       } else {
-        *reinterpret_cast<uint4*>(dst) = node < cnt
-                                             ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off)
-                                             : make_uint4(0u, 0u, 0u, 0u);
+        uint4 w = node < cnt ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off)
+                             : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t turn = p.neg ? 0x80008000u : 0u;
+        w.x ^= turn, w.y ^= turn, w.z ^= turn, w.w ^= turn;
+        *reinterpret_cast<uint4*>(dst) = w;
       }
     }
     for (int i = th; i < N; i += nth) sm_m[i] = -kNone;
@@ -396,7 +399,6 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     uint32_t tS = 0;  // S of block g, group 0; of group q: + q NSA
     const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + 2 * NG * NSA + g * NO;
     float* m = sm_m + g * NB;
-    const float masked = p.c < 0.f ? INFINITY : -INFINITY;
     if (p.tree.k && key < NB) {
       const int node = p.by_gq.div(m0 + g * NB + key);
       srow[g * NB + key] = node < cnt ? smask[node] & seen : 0;
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         float y = INFINITY;
         if (key < NB) {
           const int j = tree ? __ffsll(srow[g * NB + key]) - 1 : 0;
-          if (j >= 0) y = first[j * NB + key] * p.c;
+          if (j >= 0) y = first[j * NB + key];
           m[key] = fabsf(y) < 1e38f ? -y : -kNone;
         }
         // every block's first scores have been read: P may be written
@@ -517,18 +519,20 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
           const uint32_t bits = row_bits();
 #pragma unroll
           for (int j = 0; j < NB; ++j)
-            if (!((bits >> j) & 1)) s[j] = masked;
+            if (!((bits >> j) & 1)) s[j] = -INFINITY;
         } else if (!whole && !valid) {
 #pragma unroll
-          for (int j = 0; j < NB; ++j) s[j] = masked;
+          for (int j = 0; j < NB; ++j) s[j] = -INFINITY;
         }
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < NB; j += 4) {
           const float4 ref = *reinterpret_cast<const float4*>(m + j);
           float y[4] = {ref.x, ref.y, ref.z, ref.w};
-          fma2(y[0], y[1], s[j], s[j + 1], p.c, p.c);
-          fma2(y[2], y[3], s[j + 2], s[j + 3], p.c, p.c);
+          add2(y[0], y[1], y[0], y[1], s[j], s[j + 1]);
+          add2(y[2], y[3], y[2], y[3], s[j + 2], s[j + 3]);
+          mul2(y[0], y[1], y[0], y[1], p.c);
+          mul2(y[2], y[3], y[2], y[3], p.c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[j + i] = ex2(y[i]);
           top = fmaxf(top, fmaxf(fmaxf(s[j], s[j + 1]), fmaxf(s[j + 2], s[j + 3])));
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             const bool in = (bits >> j) & 1;
-            float y = in ? z[j] * p.c : -INFINITY;
+            float y = in ? z[j] : -INFINITY;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
             if (lane == 0) sm_w[(warp & 3) * N + g * NB + j] = y;
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
             const float* w = sm_w + g * NB + key;
             const float old = -m[key], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
             m[key] = -now;
-            sfac[g * NB + key] = old == now ? 1.f : exp2f(old - now);
+            sfac[g * NB + key] = old == now ? 1.f : exp2f((old - now) * p.c);
           }
           group_sync(g);
 #pragma unroll

@@ -1,0 +1,78 @@
+"""Edges of the tree-decoding operators' domains (GPU): scores of any size, rows whose support is drafted."""
+import pytest
+import torch
+
+import bit_quantized_token_gb300 as bq
+from test_gpu_tree import Problem, gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    bq.build()
+    torch.cuda.set_device(0)
+
+
+def seen_rows(p, b, i):
+    """K and V rows that node i of sequence b sees, [head, row, dim]."""
+    L, js = int(p.lens[b]), [j for j in range(p.n) if int(p.mask[b, i]) >> j & 1]
+    return [torch.cat([a[b, :, :L], t[b, :, js]], 1) for a, t in ((p.k, p.tk), (p.v, p.tv))]
+
+
+@pytest.mark.parametrize("exponent,scale", [(20, None), (31, -0.3), (34, None), (60, 4.0), (100, None)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q", ["f32", "bf16"])
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+@pytest.mark.parametrize("n", [5, 24, 64])
+def test_attention_scores_of_any_size(n, kv, q, hd, exponent, scale):
+    """A query is 2^exponent in one dim, the keys there are whole numbers from -7 to 7: scores are exact, two of them
+    apart by 2^exponent at least, so a row's output is the mean of the V rows of its largest score. Exact sums of V
+    (bf16 products with 1, or code times scale 1 / 64) over at most N rows, cut off by up to 2^-23 a step; 1 / l and its
+    product 2^-23; one rounding of the output."""
+    p = Problem(B=3, n=n, Hkv=2, gq=2, hd=hd, cap=701, lens=(700, 129, 5), q=q, kv=kv, seed=exponent)
+    g = gen(n)
+    dims = torch.randint(0, hd, p.q.shape[:3], device="cuda", generator=g)
+    sign = torch.randint(0, 2, p.q.shape[:3], device="cuda", generator=g) * 2 - 1
+    p.q.zero_().scatter_(3, dims[..., None], (sign * 2.0 ** exponent)[..., None].to(p.q.dtype))
+    for t in (p.k, p.tk):
+        t.copy_(torch.randint(-7, 8, t.shape, device="cuda", generator=g))
+    if kv == "q8":
+        for t in (p.ks, p.tks):
+            t.fill_(1.0)
+        for t in (p.vs, p.tvs):
+            t.fill_(1 / 64)
+    p.scale = scale
+    p.call()
+    for b in range(3):
+        for i in range(0, n, max(1, n // 12)):
+            K, V = seen_rows(p, b, i)
+            for h in range(4):
+                s = K[h // 2].double() @ p.q[b, i, h].double() * (1.0 if scale is None else scale)
+                v = V[h // 2][s == s.max()].double() * (1.0 if kv == "bf16" else 1 / 64)
+                o, A = v.mean(0), v.abs().mean(0)
+                tol = o.abs() * (2.0 ** -8 if q == "bf16" else 2.0 ** -24) + A * (v.shape[0] + 4) * 2.0 ** -23
+                err = (p.out[b, i, h].double() - o).abs()
+                assert (err <= tol).all(), (b, i, h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q", ["f32", "bf16"])
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+@pytest.mark.parametrize("n", [3, 64])
+def test_attention_large_random_scores(n, kv, q, hd):
+    """Scores around 2^40, rounded as fp32 sums are: an output is a mean of visible V rows, whichever the weights."""
+    p = Problem(B=2, n=n, Hkv=2, gq=2, hd=hd, cap=401, lens=(400, 77), q=q, kv=kv, seed=3)
+    p.q *= 2.0 ** 40
+    p.call()
+    for b in range(2):
+        for i in range(n):
+            V = seen_rows(p, b, i)[1].double()
+            if kv == "q8":
+                js = [j for j in range(n) if int(p.mask[b, i]) >> j & 1]
+                sc = torch.cat([p.vs[b, :, :int(p.lens[b])], p.tvs[b][:, js]], 1).double()
+                V = V * sc.repeat_interleave(32, -1)
+            lo, hi = V.amin(1).repeat_interleave(2, 0), V.amax(1).repeat_interleave(2, 0)
+            room = 2.0 ** -6 * V.abs().amax()
+            o = p.out[b, i].double()
+            assert ((o >= lo - room) & (o <= hi + room)).all(), (b, i)
