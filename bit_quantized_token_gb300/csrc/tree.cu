@@ -636,6 +636,8 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
     if constexpr (SOFT) {
       qr = qb + (int64_t)cur * p.q_node;
     } else {
+      gone_bits = 0;
+      gone_far = false;
 #pragma unroll 1
       for (u64 w = s.child[cur]; w; w &= w - 1) {
         const int off = s.tok[__ffsll(w) - 1] - w0, e = off >> 5;
@@ -663,6 +665,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   bool known = true;     // s.mass[k], s.inv[k] are set
   Two left = {1.f, 0.f}; // !SOFT: 1 less the probability of the rejected children
   Two tot;
+  int no_mass = V - 1;   // the next token where nothing is left to draw from
   const u64 first_take = s.take;
   for (u64 w = s.child[0];;) {
 #pragma unroll 1
@@ -692,7 +695,38 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
       }
     }
     tot = total();
-    if (!SOFT) break;
+    if constexpr (!SOFT) {
+      if (tot.h > 0.f || k == 0) break;
+      // The children's tokens are the row's whole support (and fp32 probabilities that sum to less than 1 can all be
+      // rejected). The rejection of the last one that has mass does not count: a later sibling with its token is
+      // tested against the same mass, and it is what the next token is drawn from.
+      int z = -1;
+      left = {1.f, 0.f};  // less the tokens ahead of z
+#pragma unroll 1
+      for (u64 c = s.child[cur]; c; c &= c - 1) {
+        const int i = __ffsll(c) - 1;
+        if (s.px[i] > 0.f) {
+          if (z >= 0) left = left + Two{-s.px[z], 0.f};
+          z = i;
+        }
+      }
+      if (z < 0) break;  // a row without mass
+      no_mass = s.tok[z];
+      int again = -1;
+#pragma unroll 1
+      for (u64 c = s.child[cur] & ~((2ull << z) - 1); c && again < 0; c &= c - 1) {
+        const int i = __ffsll(c) - 1;
+        if (s.tok[i] == no_mass && left * Two{s.u[i], 0.f} < Two{s.px[z], 0.f}) again = i;
+      }
+      if (again < 0) break;
+      if (tid == 0) s.path[n_path] = again;
+      cur = again;
+      ++n_path;
+      k = 0;
+      w = s.child[cur];
+      no_mass = V - 1;
+      continue;
+    }
     if (tot.h > 0.f || k == 0) {
       if (w == 0) break;  // no child is left: tot is what the next token is drawn from
       if (tid == 0) {
@@ -717,7 +751,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyParams 
   if (rank == 0 && tid < p.n) path_out[tid] = tid < n_path ? s.path[tid] : -1;
   if (rank == 0 && tid == 0) {
     p.n_path[b] = n_path;
-    if (owner < 0) p.next[b] = V - 1;  // a row without mass
+    if (owner < 0) p.next[b] = no_mass;
   }
   if (owner != rank) return;  // no rank reads or writes another's memory from here on
   mine = lane < NW ? s.warp_sum[lane] : Two{0.f, 0.f};

@@ -469,12 +469,13 @@ typedef struct {
  * u_i q(x) < r(x) / m and becomes the current node; otherwise r becomes
  * max(r/m - q, 0) and m its sum (a rejection that leaves nothing does not
  * count). Without draft_probs q(x) = 1 and a rejected token loses its
- * probability. When no child is left, next is the first token where the running
- * sum of r exceeds u_0 times r's sum (vocab - 1 if r has no mass). Decisions
- * are made with sums of at least 45 bits. Negative and NaN probabilities count
- * as 0; a token outside 0..vocab-1 is never kept. counts[b] = 0: path all -1,
- * n_path 0, next -1. Greedy mode: a child is kept when its token equals
- * targets[current]; next = targets[last]. */
+ * probability: r(x) becomes 0, and m, from 1 on, less by it (rows are taken to
+ * sum to 1 up to their rounding). When no child is left, next is the first token
+ * where the running sum of r exceeds u_0 times r's sum (vocab - 1 if probs[node]
+ * has no mass). Decisions are made with sums of at least 45 bits. Negative and
+ * NaN probabilities count as 0; a token outside 0..vocab-1 is never kept.
+ * counts[b] = 0: path all -1, n_path 0, next -1. Greedy mode: a child is kept
+ * when its token equals targets[current]; next = targets[last]. */
 int llm_verify_tree(const llm_verify_tree_args* args, void* cuda_stream);
 
 /* cache row lens[b] + k = tree row path[b][k] for k < n_path[b], in every layer
