@@ -2174,12 +2174,6 @@ int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int3
     vp.targets = d->argmax;
   }
   CK(launch_verify_tree(vp, m->n_sm, m->stream), "verification launch");
-  TreeState::Out* out = reinterpret_cast<TreeState::Out*>(m->h_stage + kStageTree);
-  CK(cudaMemcpyAsync(out, &d->out, sizeof(*out), cudaMemcpyDeviceToHost, m->stream), "outcome read");
-  CK(cudaMemcpyAsync(m->h_stage + kStageStatus, m->d_status, 4, cudaMemcpyDeviceToHost, m->stream), "status read");
-  CK(cudaStreamSynchronize(m->stream), "tree sync");
-  // an error leaves the sequence as it was: nothing has gone into the cache
-  if ((rc = status_of(m, m->h_stage[kStageStatus])) != LLM_OK) return rc;
   CommitParams cp{};
   cp.cache = layer_rows(m, seq, 0, false);
   cp.tree = layer_rows(m, 0, 0, true);
@@ -2200,9 +2194,16 @@ int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int3
   cp.row_bytes = c.head_dim * (m->kv8 ? 1 : 2);
   cp.srow_bytes = m->kv8 ? c.head_dim / 16 : 0;
   cp.pdl = pdl;
+  cp.status = m->d_status;  // an error leaves the sequence as it was: nothing goes into the cache
+  cp.next = &d->out.next;
+  cp.tok = m->d_tok + seq;
+  cp.argmax = m->d_argmax + seq;
   CK(launch_commit_tree(cp, m->stream), "commit launch");
-  CK(cudaMemcpyAsync(m->d_tok + seq, &d->out.next, 4, cudaMemcpyDeviceToDevice, m->stream), "next token");
-  CK(cudaMemcpyAsync(m->d_argmax + seq, &d->out.next, 4, cudaMemcpyDeviceToDevice, m->stream), "next token");
+  TreeState::Out* out = reinterpret_cast<TreeState::Out*>(m->h_stage + kStageTree);
+  CK(cudaMemcpyAsync(out, &d->out, sizeof(*out), cudaMemcpyDeviceToHost, m->stream), "outcome read");
+  CK(cudaMemcpyAsync(m->h_stage + kStageStatus, m->d_status, 4, cudaMemcpyDeviceToHost, m->stream), "status read");
+  CK(cudaStreamSynchronize(m->stream), "tree sync");
+  if ((rc = status_of(m, m->h_stage[kStageStatus])) != LLM_OK) return rc;
   m->len[seq] += out->n_path;
   CK(cudaMemcpy(path_out, out->path, (size_t)n * 4, cudaMemcpyDefault), "path copy");
   CK(cudaMemcpy(n_path_out, &out->n_path, 4, cudaMemcpyDefault), "path copy");

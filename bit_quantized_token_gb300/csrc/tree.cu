@@ -857,6 +857,7 @@ __global__ void __launch_bounds__(256) commit_kernel(const CommitParams p) {
   const int b = blockIdx.y, tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
+  if (p.status && *p.status) return;
   const int len = max(p.lens[b], 0);
   const int n = min(min(max(p.n_path[b], 0), p.n), max(p.cache.rows - len, 0));
   if (p.new_lens != p.lens && blockIdx.x == 0 && tid == 0) p.new_lens[b] = len + n;
@@ -903,7 +904,8 @@ __global__ void __launch_bounds__(256) advance_kernel(const CommitParams p) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  if (b >= p.B) return;
+  if (b >= p.B || (p.status && *p.status)) return;
+  if (p.next) *p.tok = *p.argmax = *p.next;
   const int len = max(p.lens[b], 0);
   p.new_lens[b] = len + min(min(max(p.n_path[b], 0), p.n), max(p.cache.rows - len, 0));
 }

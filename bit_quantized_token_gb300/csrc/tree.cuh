@@ -169,6 +169,10 @@ struct CommitParams {
   int64_t c_layer, c_slayer, t_layer, t_slayer;
   const int *lens, *path, *n_path;
   int* new_lens;             // may be lens itself
+  // a model's own sequence (one, new_lens is lens): where *status is set nothing is committed; the
+  // next token goes where the model's steps look for it
+  const int *status = nullptr, *next = nullptr;
+  int *tok = nullptr, *argmax = nullptr;
   int64_t path_seq;
   FastDiv by_heads;
   bool pdl = true;

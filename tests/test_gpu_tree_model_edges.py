@@ -1,0 +1,101 @@
+"""llm_decode_tree as a caller meets it: what it leaves behind on an error, what has run when it returns (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_token_gb300 as bq
+import synth
+from test_gpu_tree_model import config, rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    bq.build()
+
+
+@pytest.mark.parametrize("temperature", [0.0, 0.9])
+def test_an_error_leaves_rows_length_and_next_token(temperature):
+    """A node whose embedding is NaN fails the call; the sequences then go on as in a model that never saw it."""
+    cfg = config("tiny")
+    w = synth.make_weights(cfg)
+    bad = 77
+    w["embed"]["data"] = w["embed"]["data"].copy()
+    w["embed"]["data"].reshape(cfg["vocab"], -1)[bad] = np.nan
+    prompts = [[5, 9, 2], [1, 3]]
+    ends = []
+    for fail in (False, True):
+        with bq.Model(cfg, w, max_seq=48, max_batch=2) as m:
+            for s, p in enumerate(prompts):
+                m.prefill(s, p)
+            m.decode_step_batch([4, 6])  # leaves each sequence's next token on the device
+            before = [m.kv_len(s) for s in range(2)]
+            if fail:
+                m.set_sampling(temperature, top_k=4)
+                with pytest.raises(bq.LlmError, match="NaN"):
+                    m.decode_tree(1, [8, 3, bad, 2], [-1, 0, 1, 0], uniforms=[0.5] * 4)
+                m.set_sampling(0.0)
+                assert [m.kv_len(s) for s in range(2)] == before
+            got = []
+            for _ in range(3):
+                am = np.zeros(2, np.int32)
+                m.decode_step_batch(None, argmax=am)
+                got.append(am.tolist())
+            ends.append((got, [np.stack(rows(m, 1, l, 0, m.kv_len(1), "bf16")) for l in range(cfg["n_layers"])]))
+    assert ends[0][0] == ends[1][0]
+    for a, b in zip(ends[0][1], ends[1][1]):
+        assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("flags", [0, bq.LLM_KV_Q8])
+def test_batched_steps_continue_from_the_next_token(flags):
+    """After a tree the device-side token is the one that follows the kept nodes."""
+    cfg = config("tiny")
+    w = synth.make_weights(cfg)
+    with bq.Model(cfg, w, max_seq=48, max_batch=2, flags=flags) as m:
+        m.prefill(0, [5, 9, 2])
+        m.prefill(1, [1, 3])
+        try:
+            m.decode_step_batch([4, 6])
+        except bq.LlmError as e:
+            pytest.skip(str(e))
+        path, nxt = m.decode_tree(1, [8, 3, 2], [-1, 0, 0])
+        a, b = np.zeros(2, np.int32), np.zeros(2, np.int32)
+        m.decode_step_batch(None, argmax=a)
+    with bq.Model(cfg, w, max_seq=48, max_batch=2, flags=flags) as m:
+        m.prefill(0, [5, 9, 2])
+        m.prefill(1, [1, 3])
+        m.decode_step_batch([4, 6])
+        _, again = m.decode_tree(1, [8, 3, 2], [-1, 0, 0])
+        assert again == nxt
+        am = np.zeros(2, np.int32)
+        m.decode_step(1, nxt, argmax=am)
+        b[1] = am[0]
+    assert a[1] == b[1]
+
+
+def test_all_work_has_run_when_the_call_returns():
+    """The call is synchronous: nothing is left on the model's stream, the commit and the next token among it. Large
+    kernels on another stream delay every launch, so that what the call would leave behind is still there."""
+    cfg = config("tiny")
+    stream = torch.cuda.Stream()
+    tokens, parents = np.array([8, 3, 2], np.int32), np.array([-1, 0, 0], np.int32)
+    out = [np.zeros(k, np.int32) for k in (3, 1, 1)]
+    at = [x.ctypes.data for x in out]
+    with bq.Model(cfg, synth.make_weights(cfg), max_seq=400, stream=stream.cuda_stream) as m:
+        m.prefill(0, [5, 9, 2])
+        call, busy = bq.lib().llm_decode_tree, 0
+        x = torch.zeros(1 << 28, device="cuda")
+        other = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            for _ in range(400):
+                x.add_(1.0)
+        for _ in range(4):
+            rc = call(m.h, 0, tokens.ctypes.data, parents.ctypes.data, 3, None, None, *at, None)
+            busy += not stream.query()
+            assert rc == 0
+        assert not other.query(), "the other stream had nothing left to do"
+        other.synchronize()
+    assert busy == 0
