@@ -291,13 +291,21 @@ class Model:
                self.h)
 
     def decode_tree(self, seq: int, tokens, parents, draft_probs=None, uniforms=None, logits=None):
-        """One step over a drafted tree (node 0: the last chosen token): the kept nodes and the token after them."""
+        """One step over a drafted tree (node 0: the last chosen token): the kept nodes and the token after them.
+
+        draft_probs may still be in the making on torch's current stream (or the default one).
+        """
         toks, par = np.ascontiguousarray(tokens, np.int32), np.ascontiguousarray(parents, np.int32)
         if toks.ndim != 1 or par.shape != toks.shape:
             raise LlmError(-1, "tokens and parents must be one-dimensional and of one length")
         u = None if uniforms is None else np.ascontiguousarray(uniforms, np.float32)
         if u is not None and u.shape != toks.shape:
             raise LlmError(-1, "uniforms must have one value per node")
+        if getattr(draft_probs, "is_cuda", False):
+            import torch
+            current = torch.cuda.current_stream(draft_probs.device)
+            if current.cuda_stream:  # (the library waits for the default stream itself)
+                current.synchronize()
         path, n, nxt = np.empty(toks.size, np.int32), np.empty(1, np.int32), np.empty(1, np.int32)
         _check(lib().llm_decode_tree(self.h, seq, toks.ctypes.data, par.ctypes.data, toks.size, _ptr(draft_probs),
                                      _ptr(u), path.ctypes.data, n.ctypes.data, nxt.ctypes.data, _ptr(logits)), self.h)

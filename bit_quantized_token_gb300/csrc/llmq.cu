@@ -298,6 +298,7 @@ struct llm_model {
   uint16_t *d_tree_ks = nullptr, *d_tree_vs = nullptr;
   float *d_tree_q = nullptr, *d_tree_o = nullptr;
   TreeState* d_tree = nullptr;
+  cudaEvent_t inputs = nullptr;               // the caller's work that a call's device inputs come from
   int* h_stage = nullptr;                     // pinned staging (slots: kStage*)
   float* h_logits = nullptr;                  // pinned logits of a batch-1 call with host outputs
   size_t h_logits_n = 0;
@@ -1257,6 +1258,7 @@ void llm_model_destroy(llm_model* m) {
   for (void* p : m->allocs) cudaFree(p);
   if (m->h_stage) cudaFreeHost(m->h_stage);
   if (m->h_logits) cudaFreeHost(m->h_logits);
+  if (m->inputs) cudaEventDestroy(m->inputs);
   if (m->own_stream && m->stream) cudaStreamDestroy(m->stream);
   delete m;
 }
@@ -1427,6 +1429,8 @@ int llm_model_create(const llm_config* cfg, const llm_tensor* tensors, int32_t n
     if (e != cudaSuccess) return fail(cuda_fail(nullptr, e, "stream create"));
     m->own_stream = true;
   }
+  if (cudaError_t e = cudaEventCreateWithFlags(&m->inputs, cudaEventDisableTiming); e != cudaSuccess)
+    return fail(cuda_fail(nullptr, e, "event create"));
   auto A = [&](auto** p, size_t bytes, const char* what) -> int {
     cudaError_t e = dalloc(m, p, bytes);
     if (e == cudaErrorMemoryAllocation) {
@@ -2166,6 +2170,10 @@ int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int3
     pp.status = m->d_status;
     pp.pdl = pdl;
     CK(launch_token_probs(pp, m->n_sm, m->stream), "token probabilities launch");
+    if (draft_probs) {  // the model's stream does not wait for the caller's by itself
+      CK(cudaEventRecord(m->inputs, cudaStreamLegacy), "draft_probs event");
+      CK(cudaStreamWaitEvent(m->stream, m->inputs, 0), "draft_probs wait");
+    }
     vp.p = m->d_blogits;
     vp.q = draft_probs;
     vp.p_node = vp.q_node = c.vocab;

@@ -494,7 +494,9 @@ int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n
  * seeing the cache, its ancestors and itself), then the drafts are verified
  * (llm_verify_tree): greedily, or with sampling on (llm_set_sampling) against
  * the sampler's distribution with `uniforms` [n] in [0, 1) (host or device) and
- * `draft_probs` [n][vocab] (device, or NULL: fixed choices). The kept nodes'
+ * `draft_probs` [n][vocab] (device, or NULL: fixed choices; read behind the work
+ * that the legacy default stream has at the call: work on a stream that does not
+ * synchronize with it has to have ended, or to be on the model's). The kept nodes'
  * K/V rows are appended and the sequence grows by their number. path_out [n]
  * receives the kept nodes (then -1), n_path_out their number, next_out the
  * token after them (the next tree's root), logits_out (may be NULL) the [n][vocab] logits of

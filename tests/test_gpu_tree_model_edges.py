@@ -99,3 +99,39 @@ def test_all_work_has_run_when_the_call_returns():
         assert not other.query(), "the other stream had nothing left to do"
         other.synchronize()
     assert busy == 0
+
+
+@pytest.mark.parametrize("side", [False, True], ids=["default-stream", "side-stream"])
+def test_draft_probabilities_in_the_making(side):
+    """draft_probs written by work that the caller's stream has yet to run, at the call."""
+    cfg = config("tiny")
+    V = cfg["vocab"]
+    with bq.Model(cfg, synth.make_weights(cfg), max_seq=48) as m:
+        m.set_sampling(2.0, top_k=50, top_p=1.0)
+
+        def step(x, q, stream=None):
+            m.kv_reset(0)
+            m.prefill(0, [5, 9, 2])
+            if stream is not None:  # q is on its way
+                torch.cuda._sleep(200_000_000)  # about 0.1 s
+                q.copy_(sure)
+                assert not stream.query()
+            logits = np.empty((2, V), np.float32)
+            path, nxt = m.decode_tree(0, [3, x], [-1, 0], draft_probs=q, uniforms=[0.5, 0.97], logits=logits)
+            return path.tolist(), nxt, logits[0]
+
+        x = int(step(1, torch.zeros(2, V, device="cuda"))[2].argmax())
+        sure = torch.zeros(2, V, device="cuda")
+        sure[0, x] = 1.0
+        zeros = torch.zeros(2, V, device="cuda")
+        torch.cuda.synchronize()
+        assert step(x, zeros)[0] == [0, 1]  # a draft that had no probability is kept: what reading early gives
+        want = step(x, sure)
+        assert want[0] == [0]
+        stream = torch.cuda.Stream() if side else torch.cuda.default_stream()
+        for _ in range(3):
+            q = torch.zeros(2, V, device="cuda")
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                got = step(x, q, stream)
+            assert got[:2] == want[:2]
