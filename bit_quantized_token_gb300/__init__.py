@@ -301,6 +301,8 @@ class Model:
         u = None if uniforms is None else np.ascontiguousarray(uniforms, np.float32)
         if u is not None and u.shape != toks.shape:
             raise LlmError(-1, "uniforms must have one value per node")
+        self._check_rows("draft_probs", draft_probs, toks.size)
+        self._check_rows("logits", logits, toks.size)
         if getattr(draft_probs, "is_cuda", False):
             import torch
             current = torch.cuda.current_stream(draft_probs.device)
@@ -310,6 +312,16 @@ class Model:
         _check(lib().llm_decode_tree(self.h, seq, toks.ctypes.data, par.ctypes.data, toks.size, _ptr(draft_probs),
                                      _ptr(u), path.ctypes.data, n.ctypes.data, nxt.ctypes.data, _ptr(logits)), self.h)
         return path[:int(n[0])], int(nxt[0])
+
+    def _check_rows(self, name: str, a, n: int) -> None:
+        """A float32 array or tensor of n rows of the vocabulary at least (an address is the caller's word)."""
+        if a is None or isinstance(a, int):
+            return
+        V, shape = self.cfg["vocab"], tuple(a.shape)
+        contiguous = a.flags["C_CONTIGUOUS"] if isinstance(a, np.ndarray) else a.is_contiguous()
+        if (not str(a.dtype).endswith("float32") or not contiguous or int(np.prod(shape)) < n * V
+                or (len(shape) > 1 and shape[-1] != V)):
+            raise LlmError(-1, f"{name}: contiguous float32 of shape {(n, V)} is needed, not {a.dtype} {shape}")
 
     # ---- cache -------------------------------------------------------------
     def kv_reset(self, seq: int = -1) -> None:

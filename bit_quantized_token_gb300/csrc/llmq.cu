@@ -353,13 +353,13 @@ cudaError_t dalloc(llm_model* m, T** p, size_t bytes) {
   return cudaSuccess;
 }
 
-bool is_device_ptr(const void* p) {
+bool is_device_ptr(const void* p, int of = -1) {  // of: this device's (or managed)
   cudaPointerAttributes a{};
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
+  return (a.type == cudaMemoryTypeDevice && (of < 0 || a.device == of)) || a.type == cudaMemoryTypeManaged;
 }
 
 // An NVTX range over one public call (a no-op unless a profiler listens).
@@ -2115,8 +2115,8 @@ int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int3
   if (m->sampling && !uniforms) return set_err(m, LLM_ERR_INVALID_ARG, "sampled verification needs uniforms");
   if (draft_probs && !m->sampling)
     return set_err(m, LLM_ERR_INVALID_ARG, "draft_probs are for sampled verification (temperature > 0)");
-  if (draft_probs && !is_device_ptr(draft_probs))
-    return set_err(m, LLM_ERR_INVALID_ARG, "draft_probs must be device memory");
+  if (draft_probs && !is_device_ptr(draft_probs, m->device))
+    return set_err(m, LLM_ERR_INVALID_ARG, "draft_probs must be device memory of the model's device");
   TreeState::In in{};  // (pageable copies are staged before the call returns to this frame's end: it synchronizes)
   CK(cudaMemcpy(in.tok, tokens, (size_t)n * 4, cudaMemcpyDefault), "token read");
   CK(cudaMemcpy(in.parent, parents, (size_t)n * 4, cudaMemcpyDefault), "parent read");

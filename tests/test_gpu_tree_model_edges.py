@@ -135,3 +135,24 @@ def test_draft_probabilities_in_the_making(side):
             with torch.cuda.stream(stream):
                 got = step(x, q, stream)
             assert got[:2] == want[:2]
+
+
+def test_rows_of_another_size_or_type_are_refused():
+    cfg = config("tiny")
+    V = cfg["vocab"]
+    with bq.Model(cfg, synth.make_weights(cfg), max_seq=48) as m:
+        m.prefill(0, [5, 9, 2])
+        m.set_sampling(0.7, top_k=5)
+        tree, u = ([8, 3, 2], [-1, 0, 0]), [0.5] * 3
+        zeros = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
+        for q in (zeros(2, V), zeros(3, V - 1), zeros(3, V, dtype=torch.float64), zeros(3, V, dtype=torch.bfloat16),
+                  zeros(3, 2 * V)[:, :V], zeros(2 * V)):
+            with pytest.raises(bq.LlmError, match="draft_probs: contiguous float32"):
+                m.decode_tree(0, *tree, draft_probs=q, uniforms=u)
+        for out in (np.zeros((2, V), np.float32), np.zeros((3, V)), np.zeros((V, 3), np.float32).T,
+                    zeros(2, V)):
+            with pytest.raises(bq.LlmError, match="logits: contiguous float32"):
+                m.decode_tree(0, *tree, uniforms=u, logits=out)
+        assert m.kv_len(0) == 3
+        m.decode_tree(0, *tree, uniforms=u, draft_probs=zeros(32, V),  # room for more nodes
+                      logits=np.zeros((32, V), np.float32))
