@@ -2113,6 +2113,8 @@ int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int3
   if (n < 1 || n > kBM) return set_err(m, LLM_ERR_UNSUPPORTED, "a tree has 1 to 32 nodes");
   if (m->len[seq] + n > c.max_seq) return set_err(m, LLM_ERR_CTX_FULL, "the tree would exceed max_seq");
   if (m->sampling && !uniforms) return set_err(m, LLM_ERR_INVALID_ARG, "sampled verification needs uniforms");
+  if (m->sampling && c.vocab > 16 * kProbTopSlice)
+    return set_err(m, LLM_ERR_UNSUPPORTED, "sampled verification of a vocabulary over 524288");
   if (draft_probs && !m->sampling)
     return set_err(m, LLM_ERR_INVALID_ARG, "draft_probs are for sampled verification (temperature > 0)");
   if (draft_probs && !is_device_ptr(draft_probs, m->device))

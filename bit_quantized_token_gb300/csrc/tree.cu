@@ -90,8 +90,6 @@ __device__ __forceinline__ Two two_scan(Two v, int lane) {  // inclusive, over t
 // candidates are all that crosses the cluster. A NaN counts as -inf, +inf as
 // the largest finite value; a row without a finite logit is all zeros.
 constexpr int kProbThreads = 512;
-constexpr int kProbSlice = 51200;  // floats of a row that one CTA keeps
-constexpr int kProbTopSlice = 32768;
 
 __device__ __forceinline__ float clean_logit(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f); }
 

@@ -137,6 +137,9 @@ cudaError_t launch_tree_attn(const TreeAttnParams& p, int hd, bool f32, bool q8,
 cudaError_t launch_tree_attn_64(const TreeAttnParams& p, bool f32, bool q8, int n_sm, cudaStream_t st);
 cudaError_t launch_tree_attn_128(const TreeAttnParams& p, bool f32, bool q8, int n_sm, cudaStream_t st);
 
+constexpr int kProbSlice = 51200;     // floats of a row that one CTA of 16 keeps
+constexpr int kProbTopSlice = 32768;  // with top_k
+
 struct TokenProbsParams {
   const float* logits;
   float* probs;

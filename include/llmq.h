@@ -502,8 +502,8 @@ int llm_commit_tree(const llm_kv_view* cache, const llm_kv_view* tree, int32_t n
  * token after them (the next tree's root), logits_out (may be NULL) the [n][vocab] logits of
  * every node: host or device. Synchronous. With greedy choices the tokens are
  * those of llm_decode_greedy within floating-point tolerance. An error leaves
- * the sequence as it was. Errors: INVALID_ARG, UNSUPPORTED (n), CTX_FULL (len + n > max_seq),
- * NAN, CUDA, TIMEOUT.
+ * the sequence as it was. Errors: INVALID_ARG, UNSUPPORTED (n; with sampling on,
+ * a vocab over 524288), CTX_FULL (len + n > max_seq), NAN, CUDA, TIMEOUT.
  * Source: no page drafts tokens; the pipeline is llm_prefill_batched's. */
 int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int32_t* parents, int32_t n,
                     const float* draft_probs, const float* uniforms, int32_t* path_out, int32_t* n_path_out,

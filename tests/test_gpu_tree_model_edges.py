@@ -156,3 +156,17 @@ def test_rows_of_another_size_or_type_are_refused():
         assert m.kv_len(0) == 3
         m.decode_tree(0, *tree, uniforms=u, draft_probs=zeros(32, V),  # room for more nodes
                       logits=np.zeros((32, V), np.float32))
+
+
+def test_sampling_over_too_large_a_vocabulary_is_refused():
+    cfg = dict(config("tiny"), vocab=524_320, dim=128, ffn_dim=128, n_layers=1, n_heads=2, n_kv_heads=2)
+    with bq.Model(cfg, synth.make_weights(cfg), max_seq=32) as m:
+        m.prefill(0, [5, 9, 2])
+        m.set_sampling(0.7, top_k=5)
+        with pytest.raises(bq.LlmError, match="UNSUPPORTED.*524288") as e:
+            m.decode_tree(0, [8, 3], [-1, 0], uniforms=[0.5, 0.5])
+        assert e.value.code == -2
+        m.set_sampling(0.0)
+        assert m.kv_len(0) == 3
+        path, _ = m.decode_tree(0, [8], [-1])  # the model is as before
+        assert path.tolist() == [0] and m.kv_len(0) == 4
