@@ -2166,7 +2166,8 @@ int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int3
     pp.l_row = pp.p_row = c.vocab;
     pp.R = n;
     pp.V = c.vocab;
-    pp.c = (float)(1.4426950408889634 / (double)m->samp.temperature);
+    // (finite, or the largest logit's 0 times it were NaN: a temperature below 5e-39 counts as that)
+    pp.c = (float)std::min(1.4426950408889634 / (double)m->samp.temperature, 3e38);
     pp.top_k = m->samp.top_k;
     pp.top_p = m->samp.top_p;
     pp.status = m->d_status;

@@ -170,3 +170,22 @@ def test_sampling_over_too_large_a_vocabulary_is_refused():
         assert m.kv_len(0) == 3
         path, _ = m.decode_tree(0, [8], [-1])  # the model is as before
         assert path.tolist() == [0] and m.kv_len(0) == 4
+
+
+@pytest.mark.parametrize("temperature", [1e-3, 1e-30, 5e-39, 1e-40, 1.5e-45])
+def test_sampling_at_the_smallest_temperatures_is_greedy(temperature):
+    """set_sampling takes any temperature above 0: down to the smallest fp32 number the largest logit has it all."""
+    cfg = config("tiny")
+    with bq.Model(cfg, synth.make_weights(cfg), max_seq=48) as m:
+        m.prefill(0, [5, 9, 2])
+        logits = np.empty((3, cfg["vocab"]), np.float32)
+        _, first = m.decode_tree(0, [8], [-1], logits=logits[:1])
+        m.kv_reset(0)
+        m.prefill(0, [5, 9, 2])
+        m.set_sampling(temperature, top_k=20, top_p=1.0)
+        tokens = [8, (first + 1) % cfg["vocab"], first]
+        path, nxt = m.decode_tree(0, tokens, [-1, 0, 0], uniforms=[0.99, 0.0, 0.99], logits=logits)
+        gap = np.sort(logits, -1)
+        # the others' mass: at most 19 e^-10 < 1e-3 of the largest's, which passes 0.99 and, first or not, is drawn
+        assert (gap[:, -1] - gap[:, -2] > 10 * temperature).all()
+        assert path.tolist() == [0, 2] and nxt == int(logits[2].argmax())
