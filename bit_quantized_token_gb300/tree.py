@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import ctypes as C
 import struct
-import sys
 
 import bit_quantized_token_gb300 as _base
 from bit_quantized_token_gb300 import LLM_BF16, LLM_F32, LLM_Q8G32, LlmError
@@ -54,7 +53,7 @@ def _load():
     global _lib, _i32, _i64, _f32, _f16, _bf16, _i8
     if _lib is None:
         lib = _base.lib()
-        torch = sys.modules["torch"]  # the tensors are torch's
+        import torch  # the tensors are torch's
         _i32, _i64, _f32, _f16, _bf16, _i8 = (torch.int32, torch.int64, torch.float32, torch.float16, torch.bfloat16,
                                               torch.int8)
         _lib = lib
@@ -67,7 +66,7 @@ def _fail(msg: str, code: int = _INVALID):
 
 def _check(rc: int) -> None:
     if rc != 0:
-        raise LlmError(rc, _lib.llm_last_error(None).decode())
+        raise LlmError(rc, _base.lib().llm_last_error(None).decode())
 
 
 def _name(t) -> str:
@@ -165,8 +164,7 @@ def tree_attention(q, cache: KVView, tree: KVView | None, lens, mask, out, count
 
 def tree_status(stream: int | None = None) -> None:
     """Wait for the stream and raise if a tree operator's device-side wait passed its limit; see llm_tree_status."""
-    L = _lib or _load()
-    _check(L.llm_tree_status(stream))
+    _check(_base.lib().llm_tree_status(stream))
 
 
 def token_probs(logits, out, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0,
