@@ -255,14 +255,21 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
   for (int k = 0; k < C; ++k) M = fmaxf(M, s_ms[k].x);
   for (int k = 0; k < C; ++k)
     if (s_ms[k].x != -INFINITY) S += s_ms[k].y * exp2f((s_ms[k].x - M) * p.c);
-  const float f = S > 0.f && own.x != -INFINITY ? exp2f((own.x - M) * p.c) / S : 0.f;
-  if (has_edge) dst[edge - sl.off] = sx[edge] * f;
+  // 2^((own.x - M) c) / S in two factors: own terms reach 2^60, the largest rank's sum 2^77, so the whole may lie
+  // below fp32's range where its products do not
+  const int e2 = S > 0.f ? (int)(__float_as_uint(S) >> 23) - 127 : 0;
+  const float h = S > 0.f && own.x != -INFINITY ? exp2f((own.x - M) * p.c * 0.5f) : 0.f;
+  const float f1 = h * __uint_as_float((uint32_t)(127 - e2 / 2) << 23);
+  const float f2 = h * __uint_as_float((uint32_t)(127 - (e2 - e2 / 2)) << 23) /
+                   (S > 0.f ? __uint_as_float((__float_as_uint(S) & 0x007FFFFFu) | 0x3F800000u) : 1.f);
+  if (has_edge) dst[edge - sl.off] = sx[edge] * f1 * f2;
   if ((int)((reinterpret_cast<uintptr_t>(dst) >> 2) & 3) == sl.off) {
     for (int q = 0; q < kPieces; ++q) {
 #pragma unroll 2
       for (int i = piece(q) + tid; i < piece(q + 1); i += kSoftThreads) {
         float4 x = reinterpret_cast<const float4*>(sx)[i];
-        x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+        x.x *= f1, x.y *= f1, x.z *= f1, x.w *= f1;
+        x.x *= f2, x.y *= f2, x.z *= f2, x.w *= f2;
         reinterpret_cast<float4*>(sx)[i] = x;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
     if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // written before the CTA ends
   } else {
     __syncthreads();
-    for (int i = 4 * sl.v0 - sl.off + tid; i < 4 * sl.v1 - sl.off; i += kSoftThreads) dst[i] = sx[sl.off + i] * f;
+    for (int i = 4 * sl.v0 - sl.off + tid; i < 4 * sl.v1 - sl.off; i += kSoftThreads) dst[i] = sx[sl.off + i] * f1 * f2;
   }
 }
 

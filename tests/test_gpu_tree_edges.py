@@ -1,4 +1,6 @@
 """Edges of the tree-decoding operators' domains (GPU): scores of any size, rows whose support is drafted."""
+import math
+
 import pytest
 import torch
 
@@ -76,3 +78,33 @@ def test_attention_large_random_scores(n, kv, q, hd):
             room = 2.0 ** -6 * V.abs().amax()
             o = p.out[b, i].double()
             assert ((o >= lo - room) & (o <= hi + room)).all(), (b, i)
+
+
+@pytest.mark.parametrize("V", [32768, 151936, 1000])
+@pytest.mark.parametrize("T", [1.0, 0.02, 30.0])
+def test_token_probs_keep_terms_far_below_the_largest(T, V):
+    """Eighths of a row (what a CTA takes) at levels of their own, in powers of two of the probability: the second half
+    of one lies up to 2^59 above its first, all of it up to 2^200 below the largest. Terms above 2^-126 keep fp32's
+    precision (tolerance as for all rows: the argument's roundings, exp2f, the sum, the normalising)."""
+    half = V // 16
+    levels = torch.full((6, 16), -300.0, dtype=torch.float64)
+    levels[:, 0:2] = 0.0                       # the largest eighth
+    levels[0, 2:4] = torch.tensor([-140.0, -81.0])
+    levels[1, 2:4] = torch.tensor([-170.0, -111.0])
+    levels[2, 2:4] = torch.tensor([-100.0, -41.0])
+    levels[3, 0:2] = torch.tensor([-59.0, 0.0])  # the largest, as a sum of terms around 2^59
+    levels[3, 2:4] = torch.tensor([-160.0, -101.0])
+    levels[4, 0:2] = torch.tensor([-59.0, 0.0])
+    levels[4, 2:4] = torch.tensor([-110.0, -52.0])
+    levels[4, 4:6] = torch.tensor([-30.0, -80.0])
+    levels[5, 2:] = -20.0
+    x = levels.repeat_interleave(half, 1)
+    x = torch.cat([x, torch.full((6, V - x.shape[1]), -300.0, dtype=torch.float64)], 1)
+    x = ((x + 0.2 * torch.rand(6, V, dtype=torch.float64, generator=torch.Generator().manual_seed(V))) * math.log(2) * T).float()
+    out = torch.empty(6, V, device="cuda")
+    bq.token_probs(x.cuda(), out, T, 0, 1.0)
+    for r in range(6):
+        got, ref = out[r].double().cpu(), torch.softmax(x[r].double() / T, 0)
+        tol = ref * ((3 * 300 * math.log(2) * 2.0 ** -24 + 2.0 ** -22) * 2 + 210 * 2.0 ** -24) + 2.0 ** -140
+        err = (got - ref).abs()
+        assert (err <= tol).all(), (r, float((err / tol).max()))
