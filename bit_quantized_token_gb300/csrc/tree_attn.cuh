@@ -126,6 +126,12 @@ static __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity,
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   return mbar_try_wait(bar, parity) || tc_wait_long(bar, parity, abort_flag, status);
 }
+// By all lanes of a warp, which go on converged: the tensor memory accesses behind
+// such a wait are the warp's together, and a wait can end for some lanes first.
+__device__ __forceinline__ void tc_wait_together(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  tc_wait(bar, parity, abort_flag, status);
+  __syncwarp();
+}
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int row, int head, int seq,
                                         uint64_t* bar) {
   asm volatile(
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
       const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
       const int x = DB == 2 ? (t - t0) & 1 : 0;
-      tc_wait(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
+      tc_wait_together(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
       tc_fence_after();
       if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NSA + g * C::NS;
       // tree: whether row r of the block sees this thread's tree row
@@ -730,7 +736,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         }
         group_sync(g);
         if (t > t0) {
-          tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V is in O
+          tc_wait_together(o_done, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V is in O
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < C::NO * H; c0 += 16) {
@@ -752,8 +758,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       }
       if constexpr (F32) {
         if (t > t0 && (t - t0) % kTogether == 0) {  // the next P V starts anew
-          tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
-          __syncwarp();
+          tc_wait_together(o_done, (t - t0 - 1) & 1, s_abort, p.status);
           tc_fence_after();
 #pragma unroll
           for (int u = 0; u < H; ++u) {
@@ -808,8 +813,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     }
     // ---- O^T and the sums to shared memory, [row][dim]
     // (one phase at a time: with two buffers the last but one P V may still run)
-    if (DB == 2 && n_own > 1) tc_wait(o_done, (n_own - 2) & 1, s_abort, p.status);
-    if (n_own > 0) tc_wait(o_done, (n_own - 1) & 1, s_abort, p.status);
+    if (DB == 2 && n_own > 1) tc_wait_together(o_done, (n_own - 2) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait_together(o_done, (n_own - 1) & 1, s_abort, p.status);
     tc_fence_after();
     // every block's last MMAs have read the ring and P before any block writes over them
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");

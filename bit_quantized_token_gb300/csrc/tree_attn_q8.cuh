@@ -325,8 +325,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         uint4 w[HD / 16];
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + 16 * (c ^ sel));
-        if (t > 0) tc_wait(conv_empty, (t - 1) & 1, s_abort, p.status);
-        __syncwarp();
+        if (t > 0) tc_wait_together(conv_empty, (t - 1) & 1, s_abort, p.status);
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < HD / 16; c += 2) {
@@ -460,7 +459,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       for (int i = 0; i < NW; ++i) own[i] = sc[i];
       scales(t + 1);  // the next tile's are on their way meanwhile
       const int i_own = t - t0, x = i_own & 1, y = i_own % PB;
-      tc_wait(s_full + x, (i_own >> 1) & 1, s_abort, p.status);
+      tc_wait_together(s_full + x, (i_own >> 1) & 1, s_abort, p.status);
       tc_fence_after();
       tS = tmem + ((uint32_t)(warp & 3) << 21) + x * NG * NSA + g * NS;
       auto scores = [&](float (&s)[NB]) {
@@ -560,7 +559,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll
           for (int j = 0; j < NB; ++j) l[j] *= sfac[g * NB + j];
           if (t > t0) {
-            tc_wait(o_done + (i_own - 1) % PB, ((i_own - 1) / PB) & 1, s_abort, p.status);
+            tc_wait_together(o_done + (i_own - 1) % PB, ((i_own - 1) / PB) & 1, s_abort, p.status);
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < NO; c0 += 16) {
@@ -597,8 +596,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       }
       if constexpr (F32) {
         if (i_own > 0) {  // every tile: its P V, three times the steps of a bf16 tile's, starts anew
-          tc_wait(o_done + (i_own - 1) % PB, ((i_own - 1) / PB) & 1, s_abort, p.status);
-          __syncwarp();
+          tc_wait_together(o_done + (i_own - 1) % PB, ((i_own - 1) / PB) & 1, s_abort, p.status);
           tc_fence_after();
           float x[NB];
           part_of(x);
@@ -611,7 +609,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       mbar_arrive(p_full + y);
     }
     // ---- O^T and the sums to shared memory, [row][dim]
-    if (n_own > 0) tc_wait(o_done + (n_own - 1) % PB, ((n_own - 1) / PB) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait_together(o_done + (n_own - 1) % PB, ((n_own - 1) / PB) & 1, s_abort, p.status);
     tc_fence_after();
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");  // every block's MMAs have read the tiles
     if (p.S > 1) cluster_arrive();
