@@ -108,3 +108,51 @@ def test_token_probs_keep_terms_far_below_the_largest(T, V):
         tol = ref * ((3 * 300 * math.log(2) * 2.0 ** -24 + 2.0 ** -22) * 2 + 210 * 2.0 ** -24) + 2.0 ** -140
         err = (got - ref).abs()
         assert (err <= tol).all(), (r, float((err / tol).max()))
+
+
+def bf16_parts(x, n):
+    """x in n bf16 parts: their sum."""
+    total = torch.zeros_like(x)
+    for _ in range(n):
+        total = total + (x - total).bfloat16().float()
+    return total
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+@pytest.mark.parametrize("what", ["queries", "probabilities"])
+def test_fp32_queries_and_probabilities_carry_24_bits(what, kv):
+    """Two keys, 64 in a dim of their own; values 1 in a dim of their own, so that the outputs are the probabilities
+    p = r / (1 + r) and 1 / (1 + r), r = 2^y, y = c (s1 - s0). Scores are exact (64 times a query's value), as is their
+    difference (both lie in one binade). y: the roundings of c and of the product, so r is off by |y| ln 2 2^-23, exp2
+    2^-22 and three parts 2^-23; then the sum, its reciprocal and two products 4 2^-24. Queries far enough apart show
+    their own third part (8 units of y to a unit of q), those close together that of the probabilities: with two parts
+    of either, which the same formulas give on the host, a good part of the outputs is off by more."""
+    B, n, H, hd = 4, 16, 8, 64
+    a = 1 + torch.rand(2, B, n, H, generator=torch.Generator().manual_seed(3))
+    if what == "probabilities":
+        a[1] = a[0] + (a[1] - a[0]) / 16  # r from 0.5 to 2
+    q = torch.zeros(B, n, H, hd)
+    q[..., 0], q[..., 1] = a[0], a[1]
+    rows = torch.zeros(2, B, 1, 2, hd)
+    rows[0, :, :, 0, 0] = rows[0, :, :, 1, 1] = 64
+    rows[1, :, :, 0, 5] = rows[1, :, :, 1, 40] = 1
+    scales = None if kv == "bf16" else torch.ones(B, 1, 2, hd // 32, dtype=torch.float16, device="cuda")
+    k, v = (x.cuda().to(torch.bfloat16 if kv == "bf16" else torch.int8) for x in rows)
+    out = torch.empty(B, n, H, hd, device="cuda")
+    lens = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    bq.tree_attention(q.cuda(), bq.KVView(k, v, scales, scales), None, lens, None, out, scale=1 / 8)
+    bq.tree_status()
+
+    def probabilities(a, parts):
+        y = 8 * (a[1].double() - a[0].double()) / math.log(2)
+        w = torch.exp2(torch.stack([torch.zeros_like(y), y]))
+        if parts:
+            w = bf16_parts(w.float(), parts).double()
+        return w / w.sum(0), y
+
+    ref, y = probabilities(a, 0)
+    tol = ref[0] * ref[1] * (y.abs() * math.log(2) * 2.0 ** -23 + 2.0 ** -22 + 2.0 ** -23) + 4 * 2.0 ** -24 * ref
+    got = torch.stack([out[..., 5], out[..., 40]]).double().cpu()
+    assert ((got - ref).abs() <= tol).all(), float(((got - ref).abs() / tol).max())
+    less = probabilities(bf16_parts(a, 2), 0)[0] if what == "queries" else probabilities(a, 2)[0]
+    assert ((less - ref).abs() > tol).double().mean() > 0.25
