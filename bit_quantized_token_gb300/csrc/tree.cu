@@ -158,11 +158,15 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 // of the copy rate); 512 threads 71.5, four pieces 66.2, one 70.6; 16 CTAs a row 75.6.
 constexpr int kSoftThreads = 256;
 constexpr int kPieces = 2;
+static __device__ __noinline__ void wait_or_late(uint64_t* bar, uint32_t parity, int* status, int* late) {
+  if (!mbar_wait(bar, parity, status)) *late = 1;
+}
 __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenProbsParams p) {
   extern __shared__ __align__(16) float sx[];
   __shared__ __align__(8) uint64_t bars[kPieces];
   __shared__ float2 s_warp[kSoftThreads / 32];
   __shared__ float2 s_ms[16];
+  __shared__ int s_late;  // a wait has run out
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
   auto started = cl.barrier_arrive();  // shared memory of another CTA: only once that CTA runs
@@ -173,6 +177,7 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
   const int nv = max(sl.v1 - sl.v0, 0);
   auto piece = [&](int q) { return sl.v0 + (int)((int64_t)nv * q / kPieces); };
   if (tid == 0) {
+    s_late = 0;
     for (int q = 0; q < kPieces; ++q) mbar_init(bars + q, 1);
     mbar_fence_init();
   }
@@ -208,13 +213,17 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
     return w;
   };
   float ref = 0.f;
-  for (int turn = 0; turn < 2; ++turn) {
+  int turn = 0;
+  auto landed = [&](int q) {
+    if (!mbar_try_wait(bars + q, turn)) wait_or_late(bars + q, turn, p.status, &s_late);
+  };
+  for (; turn < 2; ++turn) {
     __syncthreads();  // the barriers are ready; a second turn: the slice has been read
     if (tid == 0) request();
     const float x_edge = has_edge ? clean_logit(src[edge - sl.off]) : -INFINITY;
     if (turn == 0) {
       float mx = x_edge;
-      mbar_wait(bars, 0, p.status);
+      landed(0);
       for (int i = piece(0) + tid; i < piece(1); i += kSoftThreads) {
         const float4 x = reinterpret_cast<const float4*>(sx)[i];
         mx = fmaxf(mx, fmaxf(fmaxf(clean_logit(x.x), clean_logit(x.y)), fmaxf(clean_logit(x.z), clean_logit(x.w))));
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
       sum += e;
     }
     for (int q = 0; q < kPieces; ++q) {
-      mbar_wait(bars + q, turn, p.status);
+      landed(q);
 #pragma unroll 2
       for (int i = piece(q) + tid; i < piece(q + 1); i += kSoftThreads) {
         float4 x = reinterpret_cast<const float4*>(sx)[i];
@@ -244,10 +253,12 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
     const float2 w = reduce(mx, sum);
     own = make_float2(w.x == -INFINITY ? -INFINITY : ref, w.y);
     // (below it only where the first piece had none: small terms would be lost)
-    if (turn == 1 || w.x == -INFINITY || (w.x >= ref && (w.x - ref) * p.c <= 60.f)) break;
+    if (turn == 1 || s_late || w.x == -INFINITY || (w.x >= ref && (w.x - ref) * p.c <= 60.f)) break;
     ref = w.x;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the slice is overwritten by bulk copies
   }
+  if (s_late && tid == 0)  // no copy in flight outlives the CTA
+    for (int q = 0; q < kPieces; ++q) landed(q);
   cl.barrier_wait(std::move(started));
   if (tid < C) cl.map_shared_rank(s_ms, tid)[rank] = own;  // to every rank
   cl.sync();  // after it no rank touches another's memory

@@ -103,22 +103,42 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, vol
   return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, status));
 }
 // A bounded wait: past the limit the CTA's abort flag and the device's status
-// word are set and every wait of the CTA returns at once, so that all loops
-// run to their end (on data that does not matter) and no barrier is missed.
+// word are set, and from kGraceNs later on every wait of the CTA that is not over
+// fails at once, so that the loops end and no barrier is missed. (In the time of grace
+// what is in flight lands.) A block of softmax warps one of whose waits for scores has
+// failed agrees on it by its barriers and leaves its loop; the MMA warp issues nothing
+// behind a failed wait, and a wait that ends with the flag set has failed too: threads
+// that go on may let phases complete out of turn. A poll is over within kPollNs of
+// its look at the flag, long before that. In a CTA with the flag set the MMA warp and
+// the TMA lane wait at the end for all that they have issued; without it the other
+// warps' waits were for the same.
 // (A call: the kernel's code is fetched anew by every CTA, and short ones wait for it.)
+constexpr unsigned long long kGraceNs = 200000;
+constexpr uint32_t kPollNs = 20000;
+constexpr int kAbortAt = 10;  // ints from the flag on: the time when it was set
 static __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  volatile unsigned long long* aborted = reinterpret_cast<volatile unsigned long long*>(abort_flag + kAbortAt);
   unsigned long long start = 0;
   for (uint32_t i = 0;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 63) {
-      if (*abort_flag) return false;
+    const int set = *abort_flag;
+    uint32_t over;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(over)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
+        : "memory");
+    if (over) return set == 0;
+    if (set) {
+      if (globaltimer() > *aborted + kGraceNs) return false;
+    } else if ((i & 63) == 63) {
       const unsigned long long t = globaltimer();
       if (start == 0) {
         start = t;
       } else if (t - start > kWaitLimitNs) {
+        *aborted = t;
+        __threadfence_block();
         *abort_flag = 1;
         atomicOr(status, ST_TIMEOUT);
-        return false;
       }
     }
   }
@@ -367,6 +387,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   uint64_t *full = bars, *empty = bars + 12, *s_full = bars + 24, *p_full = bars + 26, *o_done = bars + 28, *drain = bars + 30;
   volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);
   int* s_any = reinterpret_cast<int*>(small + 260);
+  volatile int* s_stop = reinterpret_cast<volatile int*>(small + 288);  // [G] a wait of the block's has failed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 264);
   uint64_t* smask = reinterpret_cast<uint64_t*>(small + 512);          // [64]
   uint64_t* srow = reinterpret_cast<uint64_t*>(small + C::kOffRow);    // [N] what each row sees of the tree
@@ -384,6 +405,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   if (tid == 4 * G * 32) {
     *s_abort = 0;
     *s_any = 0;
+    s_stop[0] = s_stop[1] = 0;
     for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
     mbar_fence_init();
   }
@@ -485,19 +507,13 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     return max(1, (n + 15) / 16);
   };
 
+  int sent = min(NST, n_units);  // by the TMA lane
   if (warp == 4 * G) {
     if (lane == 0) {
-      int i = min(NST, n_units);
-      for (; i < n_units; ++i) {
+      for (int& i = sent; i < n_units; ++i) {
         if (!tc_wait(empty + i % NST, (i / NST - 1) & 1, s_abort, p.status)) break;
         request(i);
       }
-      if (*s_abort)  // leave no copy in flight
-        for (int j = max(0, i - NST); j < i; ++j) {
-          const unsigned long long s0 = globaltimer();
-          while (!mbar_try_wait(full + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
-          }
-        }
     }
   } else if (warp == 4 * G + 1) {
     // ---- MMA: commits release units and publish scores
@@ -563,12 +579,6 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         }
       }
     }
-    if (!ok) {  // no MMA may outlive its operands
-      tc_commit(drain);
-      const unsigned long long s0 = globaltimer();
-      while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
-      }
-    }
   } else {
     // ---- softmax: thread = key
     const int g = warp >> 2, key = (warp & 3) * 32 + lane;
@@ -617,7 +627,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       const bool tree = t >= n_pre, whole = !tree && (t + 1) * BK <= len;
       const bool valid = tree ? key < kTreeMaxNodes && ((seen >> (key & 63)) & 1) : t * BK + key < len;
       const int x = DB == 2 ? (t - t0) & 1 : 0;
-      tc_wait_together(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
+      const bool failed = !tc_wait_warp(s_full + x, (DB == 2 ? (t - t0) >> 1 : t - t0) & 1, s_abort, p.status);
       tc_fence_after();
       if constexpr (DB == 2) tS = tmem + ((uint32_t)(warp & 3) << 21) + x * C::NSA + g * C::NS;
       // tree: whether row r of the block sees this thread's tree row
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       if (t == t0) {  // the references: the score of the first key that a row sees (renewed below if not finite)
         float* first = reinterpret_cast<float*>(sp + x * C::kP) + g * 64 * NB;  // [64][NB], where P comes to lie
         static_assert(64 * N * 4 <= C::kP, "room for the first scores");
-        if (warp < 4 * g + (tree ? 2 : 1))
+        if (!failed && warp < 4 * g + (tree ? 2 : 1))
 #pragma unroll 1
           for (int c0 = 0; c0 < NB; c0 += W) {
             float v[NQ][W];
@@ -658,6 +668,12 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       uint8_t* prow = sp + x * C::kP + key * C::kRowP;
       const int sel = C::kRowP == 128 ? key & 7 : (C::kRowP == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
       for (;;) {
+        if (failed) {  // the block's other warps learn of it where they would renew their references
+          group_any(g, true);
+          s_stop[g] = 1;
+          group_sync(g);
+          goto stopped;
+        }
         // probabilities with the references as they are; the largest excess over them
         uint32_t top = 0;  // of P's first parts, two at a time
         auto take = [&](float (&v)[NQ][W], int c0) {
@@ -728,6 +744,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
           }
         }
         group_sync(g);
+        if (s_stop[g]) goto stopped;
         if (key < NB) {
           const float* w = sm_w + g * NB + key;
           const float old = -m[key], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
@@ -811,6 +828,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       tc_fence_before();
       mbar_arrive(p_full + x);
     }
+  stopped:
     // ---- O^T and the sums to shared memory, [row][dim]
     // (one phase at a time: with two buffers the last but one P V may still run)
     if (DB == 2 && n_own > 1) tc_wait_together(o_done, (n_own - 2) & 1, s_abort, p.status);
@@ -820,7 +838,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
     if (p.S > 1) cluster_arrive();
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
-    const bool have = t0 < t1;
+    const bool have = t0 < t1 && !__any_sync(0xffffffffu, *s_abort);
 #pragma unroll(F32 ? H : 1)
     for (int c0 = 0; c0 < NB * H; c0 += 16) {
       const int u = c0 / NB, r0 = c0 % NB;
@@ -857,6 +875,21 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   __syncwarp();
   if (warp >= 4 * G && p.S > 1) cluster_arrive();
   join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
+  if (warp >= 4 * G && *s_abort) {  // no copy and no product in flight outlives the CTA
+    const unsigned long long s0 = globaltimer();
+    if (warp == 4 * G && lane == 0)
+#pragma unroll 1
+      for (int j = max(0, sent - NST); j < sent; ++j)
+        while (!mbar_try_wait(full + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
+        }
+    __syncwarp();
+    if (warp == 4 * G + 1) {
+      tc_commit(drain);
+      while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  }
   // Freed last: no two CTAs that hold and that wait for tensor memory share an
   // SM (kernels whose columns exceed half take all of its shared memory), so a
   // CTA that holds it while its cluster gathers cannot keep a peer waiting.

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
            *p_full = bars + 22, *o_done = bars + 24, *drain = bars + 26;  // [2][4], then pairs
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(small + 272);  // tree rows with a non-finite scale of V
   volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);
+  volatile int* s_stop = reinterpret_cast<volatile int*>(small + 288);  // [G] a wait of the block's has failed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 264);
   uint64_t* smask = reinterpret_cast<uint64_t*>(small + 512);        // [64]
   uint64_t* srow = reinterpret_cast<uint64_t*>(small + C::kOffRow);  // [N]
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   if (tid == 32 * kTmaWarp) {
     *s_abort = 0;
     *s_bad = 0;
+    s_stop[0] = s_stop[1] = 0;
     for (int i = 0; i < 8; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, i < 4 ? 128 : 256);
     mbar_fence_init();
   }
@@ -233,23 +235,15 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     return max(1, (n + 15) / 16);
   };
 
+  int sent = 2 * min(R, n_own);  // by the TMA lane
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      int i = 2 * min(R, n_own);
 #pragma unroll 1
-      for (; i < 2 * n_own; ++i) {
+      for (int& i = sent; i < 2 * n_own; ++i) {
         const int t = i >> 1, kv = i & 1;
         if (!tc_wait(raw_empty + 4 * kv + t % R, (t / R - 1) & 1, s_abort, p.status)) break;
         request(t, kv);
       }
-      if (*s_abort)  // leave no copy in flight
-#pragma unroll 1
-        for (int j = max(0, i - 2 * R); j < i; ++j) {
-          const unsigned long long s0 = globaltimer();
-          while (!mbar_try_wait(raw_full + 4 * (j & 1) + (j >> 1) % R, ((j >> 1) / R) & 1) &&
-                 globaltimer() - s0 < kWaitLimitNs) {
-          }
-        }
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
@@ -299,12 +293,6 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
         }
         tc_commit(conv_empty);
         tc_commit(s_full + x);
-      }
-    }
-    if (!ok) {  // no MMA may outlive its operands
-      tc_commit(drain);
-      const unsigned long long s0 = globaltimer();
-      while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
       }
     }
   } else if (warp >= kConvWarp) {
@@ -459,7 +447,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       for (int i = 0; i < NW; ++i) own[i] = sc[i];
       scales(t + 1);  // the next tile's are on their way meanwhile
       const int i_own = t - t0, x = i_own & 1, y = i_own % PB;
-      tc_wait_together(s_full + x, (i_own >> 1) & 1, s_abort, p.status);
+      const bool failed = !tc_wait_warp(s_full + x, (i_own >> 1) & 1, s_abort, p.status);
       tc_fence_after();
       tS = tmem + ((uint32_t)(warp & 3) << 21) + x * NG * NSA + g * NS;
       auto scores = [&](float (&s)[NB]) {
@@ -492,7 +480,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       };
       if (t == t0) {  // the references: the score of the first key that a row sees
         float* first = reinterpret_cast<float*>(sp) + g * 64 * NB;  // [64][NB], where P comes to lie
-        if (warp < 4 * g + (tree ? 2 : 1)) {
+        if (!failed && warp < 4 * g + (tree ? 2 : 1)) {
           float s[NB];
           scores(s);
           if (tree || lane == 0)
@@ -512,6 +500,12 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       }
       uint8_t* prow = sp + y * C::kP + key * 128;
       for (;;) {
+        if (failed) {  // (see tree_attn_tc_kernel)
+          group_any(g, true);
+          s_stop[g] = 1;
+          group_sync(g);
+          goto stopped;
+        }
         float s[NB];
         scores(s);
         if (tree) {
@@ -549,6 +543,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
             if (lane == 0) sm_w[(warp & 3) * N + g * NB + j] = y;
           }
           group_sync(g);
+          if (s_stop[g]) goto stopped;
           if (key < NB) {
             const float* w = sm_w + g * NB + key;
             const float old = -m[key], now = fmaxf(fmaxf(fmaxf(w[0], w[N]), fmaxf(w[2 * N], w[3 * N])), old);
@@ -608,22 +603,24 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
       tc_fence_before();
       mbar_arrive(p_full + y);
     }
+  stopped:
     // ---- O^T and the sums to shared memory, [row][dim]
     if (n_own > 0) tc_wait_together(o_done + (n_own - 1) % PB, ((n_own - 1) / PB) & 1, s_abort, p.status);
     tc_fence_after();
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");  // every block's MMAs have read the tiles
     if (p.S > 1) cluster_arrive();
     float* so = reinterpret_cast<float*>(sm) + g * NB * HD;
+    const bool have = n_own > 0 && !__any_sync(0xffffffffu, *s_abort);
     if (key < HD) {  // lanes are dims
       float x[NB];
-      if (n_own > 0) {
+      if (have) {
         part_of(x);
         if constexpr (F32)
 #pragma unroll
           for (int j = 0; j < NB; ++j) x[j] += acc[j];
       }
 #pragma unroll
-      for (int j = 0; j < NB; ++j) so[j * HD + key] = n_own > 0 ? x[j] : 0.f;
+      for (int j = 0; j < NB; ++j) so[j * HD + key] = have ? x[j] : 0.f;
       const unsigned long long bad = *s_bad;
       if (bad && t1 == n_tiles) {  // tree values with non-finite scales, where they are seen
         const int64_t at = (int64_t)b * p.tree.seq + (int64_t)hkv * p.tree.head + key;
@@ -654,6 +651,22 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   __syncwarp();
   if (warp >= kConvWarp && p.S > 1) cluster_arrive();
   join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
+  if (warp >= kTmaWarp && *s_abort) {  // (see tree_attn_tc_kernel)
+    const unsigned long long s0 = globaltimer();
+    if (warp == kTmaWarp && lane == 0)
+#pragma unroll 1
+      for (int j = max(0, sent - 2 * R); j < sent; ++j)
+        while (!mbar_try_wait(raw_full + 4 * (j & 1) + (j >> 1) % R, ((j >> 1) / R) & 1) &&
+               globaltimer() - s0 < kWaitLimitNs) {
+        }
+    __syncwarp();
+    if (warp == kMmaWarp) {
+      tc_commit(drain);
+      while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  }
   if (warp == kMmaWarp) {  // (freed last: see tree_attn_tc_kernel)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kCols));
