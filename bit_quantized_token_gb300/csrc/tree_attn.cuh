@@ -33,9 +33,9 @@
 // costs no second CTA, and the scores are then a tile ahead.
 // Measured (GB300): 32 sequences x 8 nodes, 16/8 heads x 128 over 512..2048 rows
 // 36.6 us, 70 % of the copy rate: what two CTAs' rings hold on their way to an SM.
-// 16 x 64 nodes, 32/4 heads x 64 over 1024..8192 rows 85 us: a tile's chain from
+// 16 x 64 nodes, 32/4 heads x 64 over 1024..8192 rows 85.5 us: a tile's chain from
 // scores to probabilities to P V (3,200 cycles, two CTAs an SM) and the uneven last
-// CTAs. 16 fp32 nodes over 4097 rows 12.7 us and one over 256 rows 5.9: start, a few
+// CTAs. 16 fp32 nodes over 4097 rows 13.0 us and one over 256 rows 5.9: start, a few
 // tiles, join.
 #pragma once
 #include <cuda.h>

@@ -17,7 +17,7 @@
 // (1,500 and 1,000), and the ~250 KB that pass through shared memory (codes in and
 // out, V's parts, the MMAs' fetches, P) are 1,900 of them. Giving the buffer back in
 // two halves took 10 to 15 % more: all of it competes for the same bandwidth.
-// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 35.8 us, 16 % of the
+// 8 sequences x 13 nodes, 16/8 heads x 128 over 301..4099 rows 36.0 us, 16 % of the
 // copy rate (bf16 rows are twice the bytes and wait for memory instead).
 #pragma once
 #include "tree_attn.cuh"

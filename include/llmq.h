@@ -423,11 +423,14 @@ typedef struct {
  * head h / (n_heads / cache heads). Products on the tensor cores, sums in
  * fp32 (for fp32 queries the tensor cores, which cut off, add up 256 rows at
  * most); fp32 queries and their probabilities carry 24 bits, for bf16 queries
- * the probabilities at least 8 and int8 rows' values 16 (rounding below that of
- * the output). A node that sees no row gets
- * zeros. A row that a node does not see has no influence on it, whatever it
- * holds. With n_nodes = 1 and tree = NULL this is one decode token's
- * attention over a cache that already holds its row. */
+ * the probabilities and int8 rows' values 16. Over bf16 rows, where a CTA takes
+ * 128 query rows (more than 64 of a kv head's nodes x heads, in a batch that
+ * fills the GPU), bf16 queries' probabilities carry 8: the error is then 1.41
+ * times that of an exact output rounded to bf16, and so depends on the batch.
+ * Scores may have any finite size. A node that sees no row gets zeros. A row that
+ * a node does not see has no influence on it, whatever it holds. With n_nodes = 1
+ * and tree = NULL this is one decode token's attention over a cache that already
+ * holds its row. */
 int llm_tree_attention(const llm_tree_attention_args* args, void* cuda_stream);
 
 /* Wait for `cuda_stream` and report whether a device-side wait of a
@@ -441,8 +444,10 @@ int llm_tree_status(void* cuda_stream);
  * top_p, renormalised; every other token 0. fp32 rows at the given strides
  * (elements); probs may be logits itself. A NaN logit counts as -inf, +inf as the
  * largest finite value, a row without a finite logit gives zeros.
- * UNSUPPORTED: top_p < 1 without a top_k, vocab over 524288 (819200 without
- * top_k). */
+ * With a top_k, a row takes time quadratic in the number of its largest logits
+ * where they crowd at fewer than top_k of the 128 places (j mod 512) / 4 of a
+ * slice of it (9 ms for half of 151936 tokens). UNSUPPORTED: top_p < 1 without
+ * a top_k, vocab over 524288 (819200 without top_k). */
 int llm_token_probs(const float* logits, int64_t logits_stride, float* probs, int64_t probs_stride, int32_t n_rows,
                     int32_t vocab, float temperature, int32_t top_k, float top_p, void* cuda_stream);
 

@@ -1,4 +1,5 @@
-"""Edges of the tree-decoding operators' domains (GPU): scores of any size, rows whose support is drafted."""
+"""Edges of tree attention's and the token probabilities' domains (GPU): scores of any size, terms far below the largest,
+the bits that fp32 queries carry."""
 import math
 
 import pytest
