@@ -44,7 +44,7 @@ EXPORTS = ["llm_model_create", "llm_model_destroy", "llm_prefill", "llm_prefill_
            "llm_decode_greedy", "llm_set_sampling",
            "llm_decode_step_batch", "llm_kv_reset", "llm_kv_write", "llm_kv_read", "llm_kv_read_q8", "llm_kv_len",
            "llm_debug_hidden", "llm_debug_unpack", "llm_model_stats", "llm_profile_step", "llm_time_kernel", "llm_sync",
-           "llm_last_error", "llm_op_matvec", "llm_op_matvec_w4a8", "llm_matvec_noalloc", "llm_phase_times", "llm_debug_fail_alloc",
+           "llm_last_error", "llm_op_matvec", "llm_op_matvec_w4a8", "llm_matvec_noalloc", "llm_phase_times", "llm_debug_fail_alloc", "llm_debug_expire_waits",
            "llm_debug_hidden_batch", "llm_tree_attention", "llm_tree_status", "llm_token_probs", "llm_verify_tree", "llm_commit_tree", "llm_decode_tree"]
 
 
@@ -168,6 +168,7 @@ def lib() -> C.CDLL:
             "llm_matvec_noalloc": (i32, [P, C.c_char_p, P, P, P]),
             "llm_phase_times": (i32, [P, i32, i32, i32, P, C.c_int64]),
             "llm_debug_fail_alloc": (i32, [i32]),
+            "llm_debug_expire_waits": (i32, [i32]),
             "llm_debug_hidden_batch": (i32, [P, P]),
             "llm_tree_attention": (i32, [P, P]),
             "llm_tree_status": (i32, [P]),
@@ -435,6 +436,11 @@ def matvec_w4a8(t: dict, x) -> np.ndarray:
 def debug_fail_alloc(nth: int) -> None:
     """Test hook: the nth device allocation of the models created next fails (0 disarms)."""
     _check(lib().llm_debug_fail_alloc(int(nth)))
+
+
+def debug_expire_waits(on: bool) -> None:
+    """Test hook: see llm_debug_expire_waits in include/llmq.h."""
+    _check(lib().llm_debug_expire_waits(int(on)))
 
 
 def matvec_noalloc(model: Model, name: str, x, y, stream: int | None = None) -> None:

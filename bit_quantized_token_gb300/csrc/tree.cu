@@ -15,6 +15,8 @@
 namespace llmq {
 namespace cg = cooperative_groups;
 
+std::atomic<bool> g_expire_waits{false};
+
 cudaError_t launch_tree_attn(const TreeAttnParams& p, int hd, bool f32, bool q8, int n_sm, cudaStream_t st) {
   return hd == 64 ? launch_tree_attn_64(p, f32, q8, n_sm, st) : launch_tree_attn_128(p, f32, q8, n_sm, st);
 }
@@ -158,8 +160,8 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 // of the copy rate); 512 threads 71.5, four pieces 66.2, one 70.6; 16 CTAs a row 75.6.
 constexpr int kSoftThreads = 256;
 constexpr int kPieces = 2;
-static __device__ __noinline__ void wait_or_late(uint64_t* bar, uint32_t parity, int* status, int* late) {
-  if (!mbar_wait(bar, parity, status)) *late = 1;
+static __device__ __noinline__ void wait_or_late(uint64_t* bar, uint32_t parity, int* status, uint32_t ns, int* late) {
+  if (!mbar_wait(bar, parity, status, ns)) *late = 1;
 }
 __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenProbsParams p) {
   extern __shared__ __align__(16) float sx[];
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
   auto piece = [&](int q) { return sl.v0 + (int)((int64_t)nv * q / kPieces); };
   if (tid == 0) {
     s_late = 0;
-    for (int q = 0; q < kPieces; ++q) mbar_init(bars + q, 1);
+    for (int q = 0; q < kPieces; ++q) mbar_init(bars + q, 1 + p.wait.missing);
     mbar_fence_init();
   }
   pdl_wait();
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kSoftThreads) softmax_rows_kernel(const TokenP
   float ref = 0.f;
   int turn = 0;
   auto landed = [&](int q) {
-    if (!mbar_try_wait(bars + q, turn)) wait_or_late(bars + q, turn, p.status, &s_late);
+    if (!mbar_try_wait(bars + q, turn)) wait_or_late(bars + q, turn, p.status, p.wait.ns, &s_late);
   };
   for (; turn < 2; ++turn) {
     __syncthreads();  // the barriers are ready; a second turn: the slice has been read
@@ -1215,6 +1217,11 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
   return finish(launch_tree_attn(p, (int)hd, a->dtype == LLM_F32, v.dtype == LLM_Q8G32, c.n_sm,
                                  static_cast<cudaStream_t>(cuda_stream)),
                 "tree attention launch");
+}
+
+int llm_debug_expire_waits(int32_t on) {
+  g_expire_waits.store(on != 0, std::memory_order_relaxed);
+  return LLM_OK;
 }
 
 int llm_tree_status(void* cuda_stream) {

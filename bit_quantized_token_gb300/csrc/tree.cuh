@@ -12,6 +12,15 @@
 
 namespace llmq {
 
+// How long a device-side wait of these kernels may take. The test hook makes a
+// barrier of each CTA expect a warp's arrivals more than it gets, with a short limit.
+struct WaitLimit {
+  uint32_t ns = 2000000000;
+  int missing = 0;
+};
+extern std::atomic<bool> g_expire_waits;  // llm_debug_expire_waits
+inline WaitLimit wait_limit() { return g_expire_waits.load(std::memory_order_relaxed) ? WaitLimit{1000000, 32} : WaitLimit{}; }
+
 constexpr int kTreeMaxNodes = 64;  // a node's visible set is one 64-bit word
 
 // A kernel's dynamic shared memory limit (and the leave for clusters of 16), set once per device (one of these,
@@ -130,6 +139,7 @@ struct TreeAttnParams {
   bool pdl = true;           // launch as a programmatic dependent
   bool sorted;               // blocks take the sequences longest first
   int* status;               // the device's status word (bounded waits)
+  WaitLimit wait = wait_limit();
 };
 
 // f32: q and out are fp32 (else bf16); q8: int8 rows. n_sm: SMs of the device.
@@ -151,6 +161,7 @@ struct TokenProbsParams {
   bool pdl = true;
   int cap = 0;               // set by the launch: floats of a slice
   int* status;               // the device's status word (bounded waits)
+  WaitLimit wait = wait_limit();
 };
 cudaError_t launch_token_probs(const TokenProbsParams& p, int n_sm, cudaStream_t st);
 

@@ -106,16 +106,17 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, vol
 // word are set, and from kGraceNs later on every wait of the CTA that is not over
 // fails at once, so that the loops end and no barrier is missed. (In the time of grace
 // what is in flight lands.) A block of softmax warps one of whose waits for scores has
-// failed agrees on it by its barriers and leaves its loop; the MMA warp issues nothing
-// behind a failed wait, and a wait that ends with the flag set has failed too: threads
-// that go on may let phases complete out of turn. A poll is over within kPollNs of
-// its look at the flag, long before that. In a CTA with the flag set the MMA warp and
-// the TMA lane wait at the end for all that they have issued; without it the other
-// warps' waits were for the same.
+// failed agrees on it by its barriers and leaves its loop (an arrival out of turn can
+// find fewer pending than a warp brings, which faults); the MMA warp issues nothing
+// behind a failed wait, and a wait that ends with the flag set has failed too: the
+// converters of int8 rows go on and may let phases complete out of turn. A poll is
+// over within kPollNs of its look at the flag, long before that. In a CTA with the
+// flag set the MMA warp and the TMA lane wait at the end for all that they have
+// issued; without it the other warps' waits were for the same.
 // (A call: the kernel's code is fetched anew by every CTA, and short ones wait for it.)
 constexpr unsigned long long kGraceNs = 200000;
 constexpr uint32_t kPollNs = 20000;
-constexpr int kAbortAt = 10;  // ints from the flag on: the time when it was set
+constexpr int kLimitAt = 3, kAbortAt = 10;  // ints from the flag on: the limit in ns, the time when the flag was set
 static __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   volatile unsigned long long* aborted = reinterpret_cast<volatile unsigned long long*>(abort_flag + kAbortAt);
   unsigned long long start = 0;
@@ -134,7 +135,7 @@ static __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity,
       const unsigned long long t = globaltimer();
       if (start == 0) {
         start = t;
-      } else if (t - start > kWaitLimitNs) {
+      } else if (t - start > (uint32_t)abort_flag[kLimitAt]) {
         *aborted = t;
         __threadfence_block();
         *abort_flag = 1;
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 
   // TMA: the units in the order in which the MMAs release them
   if (tid == 4 * G * 32) {
-    *s_abort = 0;
+    s_abort[0] = 0, s_abort[kLimitAt] = p.wait.ns;
     *s_any = 0;
     s_stop[0] = s_stop[1] = 0;
     for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       for (int i = 0; i < NST && i < n_units; ++i) request(i);
   } else if (warp == 4 * G + 1) {
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 * G);
+      for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 * G + p.wait.missing);
       mbar_init(o_done, 1);
       mbar_init(drain, 1);
       mbar_fence_init();

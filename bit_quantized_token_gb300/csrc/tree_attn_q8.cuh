@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   static_assert(N * HD * 4 + kJoin<HD, N> <= NP * C::kConv, "room for them");
 
   if (tid == 32 * kTmaWarp) {
-    *s_abort = 0;
+    s_abort[0] = 0, s_abort[kLimitAt] = p.wait.ns;
     *s_bad = 0;
     s_stop[0] = s_stop[1] = 0;
     for (int i = 0; i < 8; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, i < 4 ? 128 : 256);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(conv_full + i, i ? 256 : 128), mbar_init(conv_empty + i, 1);
-        mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 * G), mbar_init(o_done + i, 1);
+        mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 * G + p.wait.missing), mbar_init(o_done + i, 1);
       }
       mbar_init(drain, 1);
       mbar_fence_init();

@@ -259,6 +259,13 @@ int llm_debug_unpack(llm_model* m, const char* name, uint8_t* codes, uint16_t* s
  * Source: zynfer PR #100, stage M6 (allocation behaviour tested with a failing allocator). */
 int llm_debug_fail_alloc(int32_t nth);
 
+/* Test hook: on != 0 makes a wait of each CTA of the llm_tree_attention and plain
+ * llm_token_probs calls launched from then on (llm_decode_tree's among them) run
+ * out, after 1 ms; their outputs are not valid, and llm_tree_status, or the model's
+ * call, reports TIMEOUT. Process-wide; returns LLM_OK.
+ * Source: as llm_debug_fail_alloc. */
+int llm_debug_expire_waits(int32_t on);
+
 /* Sizes and counts of the model (host struct).
  * Source: zynfer PR #100, stages M2-M4 (bytes per token for the roofline estimate). */
 int llm_model_stats(const llm_model* m, llm_stats* out);
