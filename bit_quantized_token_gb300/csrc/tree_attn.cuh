@@ -67,7 +67,11 @@ constexpr int kTogether = 2;
 template <int HD, bool F32, int NB, int G>
 struct TreeTc {
   static constexpr int N = NB * G, BK = 128, H = HD / 64;
-  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : (N > 64 ? 1 : 2);  // parts of the queries, of P
+  // Parts of the queries, of P. One part of P (8 bits) where a CTA takes 128 rows: the outputs' error is 0.0024 of
+  // their size, with two parts 0.0017, what rounding them to bf16 gives. Two parts would leave one CTA on an SM at 64
+  // dims (16 x 64 nodes over 1024..8192 rows 86 -> 87 us, 32 x 16 over 512..4096 34 -> 45) and do not fit tensor
+  // memory at 128 (64 rows a CTA instead: 105 -> 113 and 112 -> 251 us for 2 and 4 query heads a kv head).
+  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : (N > 64 ? 1 : 2);
   static constexpr int NS = NQ * NB, NO = NP * NB;                        // columns of a block's S, of its O (64 dims)
   static constexpr int NSA = G * NS, NOA = G * NO;                        // of all blocks
   static constexpr int NT = 32 * (4 * G + 2);
