@@ -1,0 +1,390 @@
+// New tokens' K and V rows into a cache, with the norms and the rotation of
+// their q and k heads, and cached rows back out as values (see serve.cuh).
+#include "common.cuh"
+#include "op_call.cuh"
+#include "serve.cuh"
+
+namespace llmq {
+namespace {
+
+// ---- append --------------------------------------------------------------------
+// A head of q or k: x / sqrt(mean(x^2) + eps) w (with a norm), then the pairs
+// (i, i + hd/2) or (2i, 2i + 1) turned by position times freq_i. A group of hd/8
+// lanes holds a row, a lane four dims of the first half and the same four of the
+// second: both kinds of pairs lie in one lane, 32 neighbouring dims in eight, and
+// the norm is a sum over the group. Everything is fp32 and rounded once, into
+// the outputs' type.
+//
+// Angles: the turn of a position is kept modulo 1 in 64-bit fixed point, so that
+// position times turn wraps where an angle would and no position is too far (the
+// table's 2^-50 of a turn grows with the position: 2^-30 at 2^20). The quadrant is
+// taken off in integers; sincospi sees at most a quarter of a half turn.
+//
+// Int8 rows: per 32 values a scale fp16(amax / 127) and codes round(x / scale),
+// halves away from zero, clamped to +-127, decided in fp32: the cache's own
+// format and roundings. A scale past fp16's range saturates (values beyond 8.3e6
+// become the largest that the row can hold), a NaN makes its 32 values NaN.
+//
+// Bound by HBM for many tokens (8192 tokens of 16/8 heads x 128 in bf16, norms and
+// rotation), by the launch for few.
+constexpr int kAppendThreads = 128;
+
+template <int N>
+__device__ __forceinline__ void load_vals(float (&x)[N], const void* base, int64_t at, bool f32);
+template <>
+__device__ __forceinline__ void load_vals<4>(float (&x)[4], const void* base, int64_t at, bool f32) {
+  if (f32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+    x[0] = __uint_as_float(a.x << 16), x[1] = __uint_as_float(a.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(a.y << 16), x[3] = __uint_as_float(a.y & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void store4(void* base, int64_t at, const float* x, bool f32) {
+  if (f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(x[0], x[1], x[2], x[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
+}
+
+// cos and sin of `angle` 2^-64 turns
+__device__ __forceinline__ float2 turn_of(uint64_t angle) {
+  const uint32_t hi = (uint32_t)(angle >> 32);
+  const uint32_t quad = (hi + 0x20000000u) >> 30;                         // the nearest quarter turn
+  const float r = (float)(int)(hi - (quad << 30)) * 4.656612873e-10f;     // 2^-31: half turns, within +-1/4
+  float s, c;
+  sincospif(r, &s, &c);
+  const float a = quad & 1 ? s : c, b = quad & 1 ? c : s;
+  return make_float2((quad + 1) & 2 ? -a : a, quad & 2 ? -b : b);
+}
+
+template <int HD, bool Q8>
+__global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int LPR = HD / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, c = lane % LPR;
+  const int heads = p.Hq + 2 * p.Hkv, per = RPW * p.passes, slices = (heads + per - 1) / per;
+  const int64_t w = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int t = (int)(w / slices), h0 = (int)(w - (int64_t)t * slices) * per + lane / LPR;
+  if (t >= p.T) return;
+  const int seq = p.seqs[t], row = p.rows[t];
+  const bool kept = seq >= 0 && seq < p.n_seq && row >= 0 && row < p.cache.rows;
+  float2 cs[4];
+  if (p.rotate) {
+    const int64_t pos = p.positions ? p.positions[t] : row;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = p.neox ? 4 * c + e : (e < 2 ? 2 * c + e : HD / 4 + 2 * c + e - 2);
+      cs[e] = turn_of((uint64_t)pos * p.freq[i]);
+    }
+  }
+#pragma unroll 2
+  for (int j = 0; j < p.passes; ++j) {
+    const int h = h0 + j * RPW;  // q heads, then k heads, then v heads
+    const bool in = h < heads;
+    const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2, hh = kind == 0 ? h : (h - p.Hq) - (kind - 1) * p.Hkv;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (in) {
+      const void* src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+      const int64_t at = t * (kind == 0 ? p.q_tok : kind == 1 ? p.k_tok : p.v_tok) +
+                         hh * (kind == 0 ? p.q_head : kind == 1 ? p.k_head : p.v_head) + 4 * c;
+      float lo[4], hi[4];
+      load_vals<4>(lo, src, at, p.f32);
+      load_vals<4>(hi, src, at + HD / 2, p.f32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
+    }
+    const float* wn = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
+    if (p.q_norm || p.k_norm) {  // (by the whole warp: its rows may be of different kinds)
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (wn && in) {
+        const float inv = 1.0f / sqrtf(ss / (float)HD + p.eps);
+        const float4 a = __ldg(reinterpret_cast<const float4*>(wn) + c);
+        const float4 b = __ldg(reinterpret_cast<const float4*>(wn + HD / 2) + c);
+        x[0] *= inv * a.x, x[1] *= inv * a.y, x[2] *= inv * a.z, x[3] *= inv * a.w;
+        x[4] *= inv * b.x, x[5] *= inv * b.y, x[6] *= inv * b.z, x[7] *= inv * b.w;
+      }
+    }
+    if (p.rotate && kind < 2) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int ia = p.neox ? e : 2 * e, ib = p.neox ? e + 4 : 2 * e + 1;
+        const float a = x[ia], b = x[ib];
+        x[ia] = a * cs[e].x - b * cs[e].y;
+        x[ib] = a * cs[e].y + b * cs[e].x;
+      }
+    }
+    if (in && kind == 0) {
+      const int64_t at = t * p.o_tok + hh * p.o_head + 4 * c;
+      store4(p.q_out, at, x, p.out_f32);
+      store4(p.q_out, at + HD / 2, x + 4, p.out_f32);
+    }
+    uint8_t* base = const_cast<uint8_t*>(kind == 2 ? p.cache.v : p.cache.k);
+    const int64_t at = (int64_t)seq * p.cache.seq + (int64_t)hh * p.cache.head + (int64_t)row * p.cache.row;
+    if constexpr (!Q8) {
+      if (in && kind > 0 && kept) {
+        store4(base, at + 4 * c, x, false);
+        store4(base, at + HD / 2 + 4 * c, x + 4, false);
+      }
+    } else if (__any_sync(0xffffffffu, in && kind > 0)) {
+      uint32_t word[2];
+      uint16_t sc[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {  // of either half: eight lanes hold 32 neighbouring dims
+        uint32_t top = 0;            // of the sizes as integers: a NaN's is above all others
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[4 * g + e]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float amax = __uint_as_float(top);
+        const __half dh = __float2half_rn(top > 0x7F800000u ? amax : fminf(amax / 127.0f, 65504.f));
+        const float dq = __half2float(dh);
+        uint32_t codes = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float cf = dq == 0.f ? 0.f : fminf(fmaxf(roundf(x[4 * g + e] / dq), -127.f), 127.f);
+          codes |= ((uint32_t)(int)cf & 0xFFu) << (8 * e);
+        }
+        word[g] = codes;
+        sc[g] = __half_as_ushort(dh);
+      }
+      if (in && kind > 0 && kept) {
+        *reinterpret_cast<uint32_t*>(base + at + 4 * c) = word[0];
+        *reinterpret_cast<uint32_t*>(base + at + HD / 2 + 4 * c) = word[1];
+        if ((c & 7) == 0) {
+          uint16_t* s = const_cast<uint16_t*>(kind == 2 ? p.cache.vs : p.cache.ks) + (int64_t)seq * p.cache.sseq +
+                        (int64_t)hh * p.cache.shead + (int64_t)row * p.cache.srow;
+          s[c / 8] = sc[0];
+          s[HD / 64 + c / 8] = sc[1];
+        }
+      }
+    }
+  }
+}
+
+// ---- read ----------------------------------------------------------------------
+// A lane takes 16 bytes of a row: 8 bf16 values or 16 codes and their scale;
+// four rows of a thread in flight. Rows run over (token, head, K or V) of a layer,
+// so that neighbouring ones write neighbouring outputs. A token whose sequence or
+// row is out of range reads zeros.
+constexpr int kReadThreads = 256, kReadRows = 4;
+
+template <int HD, bool Q8>
+__global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const ReadParams p) {
+  constexpr int VPL = Q8 ? 16 : 8, LPR = HD / VPL, RPB = kReadThreads / LPR;  // values of a lane; rows of a block's pass
+  pdl_wait();
+  pdl_trigger();
+  const int c = threadIdx.x % LPR, l = blockIdx.y;
+  const int64_t n = (int64_t)2 * p.T * p.H, first = (int64_t)blockIdx.x * RPB * kReadRows + threadIdx.x / LPR;
+  uint4 x[kReadRows];
+  float f[kReadRows];
+#pragma unroll
+  for (int u = 0; u < kReadRows; ++u) {
+    const int64_t i = first + u * RPB;
+    x[u] = make_uint4(0u, 0u, 0u, 0u);
+    f[u] = 0.f;
+    if (i >= n) continue;
+    const int kv = i >= (int64_t)p.T * p.H, r = (int)(i - (kv ? (int64_t)p.T * p.H : 0)), t = p.by_heads.div(r), h = r - t * p.H;
+    const int seq = p.seqs[t], row = p.rows[t];
+    if (seq < 0 || seq >= p.n_seq || row < 0 || row >= p.cache.rows) continue;
+    const int64_t at = (int64_t)seq * p.cache.seq + l * p.layer + h * p.cache.head + (int64_t)row * p.cache.row + VPL * c;
+    x[u] = __ldcs(reinterpret_cast<const uint4*>((kv ? p.cache.v : p.cache.k) + (Q8 ? 1 : 2) * at));
+    if constexpr (Q8)
+      f[u] = __half2float(__ushort_as_half((kv ? p.cache.vs : p.cache.ks)[(int64_t)seq * p.cache.sseq + l * p.slayer +
+                                                                          h * p.cache.shead + (int64_t)row * p.cache.srow + c / 2]));
+  }
+#pragma unroll
+  for (int u = 0; u < kReadRows; ++u) {
+    const int64_t i = first + u * RPB;
+    if (i >= n) continue;
+    const int kv = i >= (int64_t)p.T * p.H, r = (int)(i - (kv ? (int64_t)p.T * p.H : 0)), t = p.by_heads.div(r), h = r - t * p.H;
+    const int64_t at = l * p.o_layer + (int64_t)t * p.o_tok + h * p.o_head + VPL * c;
+    void* out = kv ? p.v : p.k;
+    if constexpr (!Q8) {
+      if (!p.f32) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = x[u];
+      } else {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[2 * e] = __uint_as_float((&x[u].x)[e] << 16);
+          y[2 * e + 1] = __uint_as_float((&x[u].x)[e] & 0xFFFF0000u);
+        }
+        store4(out, at, y, true);
+        store4(out, at + 4, y + 4, true);
+      }
+    } else {
+      float y[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)  // (0 times an infinite scale is NaN, as it would be in a product)
+        y[e] = (float)(int8_t)((&x[u].x)[e / 4] >> (8 * (e & 3))) * f[u];
+      if (p.f32) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) store4(out, at + e, y + e, true);
+      } else {
+        uint32_t z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = bf16_pair(y[2 * e], y[2 * e + 1]);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+        dst[0] = make_uint4(z[0], z[1], z[2], z[3]);
+        dst[1] = make_uint4(z[4], z[5], z[6], z[7]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append_kv(AppendParams& p, int hd, bool q8, int n_sm, cudaStream_t st) {
+  const int rpw = 256 / hd, heads = p.Hq + 2 * p.Hkv, groups = (heads + rpw - 1) / rpw;
+  // One pass a warp while the warps fit the SMs at once (16 a SM); a warp that takes
+  // more rows of its token computes the token's angles once for them.
+  const int64_t per = (int64_t)p.T * groups / (16 * (int64_t)n_sm);
+  p.passes = (int)(per < 1 ? 1 : per < groups ? per : groups);
+  const int64_t warps = (int64_t)p.T * ((heads + rpw * p.passes - 1) / (rpw * p.passes));
+  const dim3 grid((unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
+  const auto kern = hd == 64 ? (q8 ? append_kv_kernel<64, true> : append_kv_kernel<64, false>)
+                             : (q8 ? append_kv_kernel<128, true> : append_kv_kernel<128, false>);
+  return launch_cluster(kern, grid, kAppendThreads, 1, 0, st, p, p.pdl);
+}
+
+cudaError_t launch_read_kv(const ReadParams& p, int hd, bool q8, cudaStream_t st) {
+  const int64_t rows = (int64_t)2 * p.T * p.H, per = (int64_t)kReadRows * kReadThreads * (q8 ? 16 : 8) / hd;
+  const auto kern = hd == 64 ? (q8 ? read_kv_kernel<64, true> : read_kv_kernel<64, false>)
+                             : (q8 ? read_kv_kernel<128, true> : read_kv_kernel<128, false>);
+  return launch_cluster(kern, dim3((unsigned)((rows + per - 1) / per), p.L), kReadThreads, 1, 0, st, p, p.pdl);
+}
+
+}  // namespace llmq
+
+// ---- C entries -------------------------------------------------------------------
+using namespace llmq;
+
+namespace {
+
+// The turns of base^(-2i/hd) radians a position, in 2^-64 turns. Powers of one
+// root by its binary powers: six calls of pow, each power within 2^-50.
+void turns_of(double theta, int hd, uint64_t* freq) {
+  double root[6];
+  for (int k = 0; k < 6; ++k) root[k] = std::pow(theta, -2.0 * (1 << k) / hd);
+  for (int i = 0; i < hd / 2; ++i) {
+    double f = 0.15915494309189533577;  // 1 / (2 pi)
+    for (int k = 0; k < 6; ++k)
+      if (i >> k & 1) f *= root[k];
+    f -= std::floor(f);  // (a base below 1 turns faster)
+    const double x = std::nearbyint(f * 18446744073709551616.0);
+    freq[i] = x >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(x);
+  }
+}
+
+bool strides_ok(Call& c, const int64_t* s, int n, int64_t m, const char* name) {
+  for (int i = 0; i < n; ++i)
+    if (!c.need(s[i] >= 0 && s[i] % m == 0 && s[i] < (1ll << 38), LLM_ERR_INVALID_ARG,
+                "a stride of %s is negative, over 2^38 or no multiple of 16 bytes", name))
+      return false;
+  return true;
+}
+
+bool view_apart(const llm_kv_view& v) {
+  const int64_t size[4] = {v.n_seq, v.n_layers, v.n_heads, v.rows};
+  const int64_t stride[4] = {v.seq_stride, v.layer_stride, v.head_stride, v.row_stride};
+  const int64_t sstride[4] = {v.scale_seq_stride, v.scale_layer_stride, v.scale_head_stride, v.scale_row_stride};
+  return apart(v.head_dim, 4, size, stride) && (v.dtype != LLM_Q8G32 || apart(v.head_dim / 32, 4, size, sstride));
+}
+
+}  // namespace
+
+extern "C" {
+
+int llm_append_kv(const llm_append_kv_args* a, void* cuda_stream) {
+  Call c;
+  if (!c.need(a != nullptr, LLM_ERR_INVALID_ARG, "the arguments are null")) return c.rc;
+  if (!c.need((a->dtype == LLM_BF16 || a->dtype == LLM_F32) && (a->out_dtype == LLM_BF16 || a->out_dtype == LLM_F32),
+              LLM_ERR_UNSUPPORTED, "q, k, v and q_out are bf16 or f32") ||
+      !c.need(a->n_tokens >= 1 && a->n_tokens <= (1 << 24), LLM_ERR_INVALID_ARG, "n_tokens is not in 1..2^24") ||
+      !check_view(c, a->cache, "cache"))
+    return c.rc;
+  const llm_kv_view& v = *a->cache;
+  if (!c.need(v.n_layers == 1, LLM_ERR_INVALID_ARG, "the cache view has several layers") ||
+      !c.need(a->n_heads >= 0 && a->n_heads <= 4096 && v.n_heads <= 4096, LLM_ERR_UNSUPPORTED, "too many heads") ||
+      !c.need((a->n_heads > 0) == (a->q != nullptr), LLM_ERR_INVALID_ARG, "n_heads and q do not match") ||
+      !c.need(a->rope_theta == 0.0 || (a->rope_theta > 0.0 && std::isfinite(a->rope_theta)), LLM_ERR_INVALID_ARG,
+              "rope_theta is not positive and finite (0: no rotation)") ||
+      !c.need(a->rope_neox == 0 || a->rope_neox == 1, LLM_ERR_INVALID_ARG, "rope_neox must be 0 or 1") ||
+      !c.need(!(a->q_norm || a->k_norm) || (a->norm_eps > 0.f && std::isfinite(a->norm_eps)), LLM_ERR_INVALID_ARG,
+              "norm_eps is not positive"))
+    return c.rc;
+  const int64_t m = a->dtype == LLM_F32 ? 4 : 8, mo = a->out_dtype == LLM_F32 ? 4 : 8;
+  const int64_t size[2] = {a->n_tokens, a->n_heads};
+  if (!strides_ok(c, a->k_strides, 2, m, "k") || !strides_ok(c, a->v_strides, 2, m, "v") ||
+      (a->q && (!strides_ok(c, a->q_strides, 2, m, "q") || !strides_ok(c, a->out_strides, 2, mo, "q_out") ||
+                !c.need(apart(v.head_dim, 2, size, a->out_strides), LLM_ERR_INVALID_ARG, "rows of q_out overlap") ||
+                !c.need(a->q_out != a->q || (a->dtype == a->out_dtype && a->q_strides[0] == a->out_strides[0] &&
+                                             a->q_strides[1] == a->out_strides[1]),
+                        LLM_ERR_INVALID_ARG, "q_out is q with another type or strides"))) ||
+      !c.need(view_apart(v), LLM_ERR_INVALID_ARG, "rows of the cache overlap") || !view_memory(c, a->cache, "cache") ||
+      !c.device("k", a->k, 16) || !c.device("v", a->v, 16) || !c.device("seqs", a->seqs, 4) ||
+      !c.device("rows", a->rows, 4) || (a->positions && !c.device("positions", a->positions, 4)) ||
+      (a->q && (!c.device("q", a->q, 16) || !c.device("q_out", a->q_out, 16))) ||
+      (a->q_norm && !c.device("q_norm", a->q_norm, 16)) || (a->k_norm && !c.device("k_norm", a->k_norm, 16)))
+    return c.rc;
+  AppendParams p{};
+  p.q = a->q, p.k = a->k, p.v = a->v, p.q_out = a->q_out;
+  p.q_tok = a->q_strides[0], p.q_head = a->q_strides[1];
+  p.k_tok = a->k_strides[0], p.k_head = a->k_strides[1];
+  p.v_tok = a->v_strides[0], p.v_head = a->v_strides[1];
+  p.o_tok = a->out_strides[0], p.o_head = a->out_strides[1];
+  p.cache = rows_of(v);
+  p.seqs = a->seqs, p.rows = a->rows, p.positions = a->positions;
+  p.q_norm = a->q ? a->q_norm : nullptr, p.k_norm = a->k_norm;
+  p.eps = a->norm_eps;
+  p.T = a->n_tokens, p.Hq = a->q ? a->n_heads : 0, p.Hkv = v.n_heads, p.n_seq = v.n_seq;
+  p.rotate = a->rope_theta > 0.0;
+  p.neox = a->rope_neox;
+  p.f32 = a->dtype == LLM_F32, p.out_f32 = a->out_dtype == LLM_F32;
+  if (p.rotate) turns_of(a->rope_theta, v.head_dim, p.freq);
+  return finish(launch_append_kv(p, v.head_dim, v.dtype == LLM_Q8G32, c.n_sm, static_cast<cudaStream_t>(cuda_stream)),
+                "append launch");
+}
+
+int llm_read_kv(const llm_kv_view* cache, int32_t n_tokens, const int32_t* seqs, const int32_t* rows, int32_t out_dtype,
+                void* k, void* v, const int64_t* out_strides, void* cuda_stream) {
+  Call c;
+  if (!c.need(out_dtype == LLM_BF16 || out_dtype == LLM_F32, LLM_ERR_UNSUPPORTED, "k and v are read as bf16 or f32") ||
+      !c.need(n_tokens >= 1, LLM_ERR_INVALID_ARG, "n_tokens is not positive") || !check_view(c, cache, "cache") ||
+      !c.need(cache->n_layers <= 65535, LLM_ERR_UNSUPPORTED, "too many layers") ||
+      !c.need((int64_t)n_tokens * cache->n_heads * cache->n_heads < (1ll << 32) && (int64_t)n_tokens * cache->n_heads < (1ll << 31),
+              LLM_ERR_UNSUPPORTED, "too many tokens and heads") ||
+      !c.need(out_strides != nullptr, LLM_ERR_INVALID_ARG, "out_strides is null") ||
+      !strides_ok(c, out_strides, 3, out_dtype == LLM_F32 ? 4 : 8, "k and v"))
+    return c.rc;
+  const int64_t size[3] = {cache->n_layers, n_tokens, cache->n_heads};
+  if (!c.need(apart(cache->head_dim, 3, size, out_strides), LLM_ERR_INVALID_ARG, "rows of the outputs overlap") ||
+      !view_memory(c, cache, "cache") || !c.device("seqs", seqs, 4) || !c.device("rows", rows, 4) ||
+      !c.device("k", k, 16) || !c.device("v", v, 16))
+    return c.rc;
+  ReadParams p{};
+  p.cache = rows_of(*cache);
+  p.layer = cache->layer_stride, p.slayer = cache->scale_layer_stride;
+  p.seqs = seqs, p.rows = rows;
+  p.k = k, p.v = v;
+  p.o_layer = out_strides[0], p.o_tok = out_strides[1], p.o_head = out_strides[2];
+  p.T = n_tokens, p.L = cache->n_layers, p.H = cache->n_heads, p.n_seq = cache->n_seq;
+  p.by_heads = FastDiv(p.H);
+  p.f32 = out_dtype == LLM_F32;
+  return finish(launch_read_kv(p, cache->head_dim, cache->dtype == LLM_Q8G32, static_cast<cudaStream_t>(cuda_stream)),
+                "read launch");
+}
+
+}  // extern "C"

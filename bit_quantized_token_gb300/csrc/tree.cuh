@@ -194,6 +194,9 @@ struct CommitParams {
 };
 cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st);
 
+// The device's status word of the bounded waits (llm_tree_status).
+cudaError_t status_word(int dev, int** p);
+
 // Records the calling thread's error text of a call without a model (llm_last_error(NULL)); returns code.
 int op_error(int code, const char* msg) noexcept;
 

@@ -521,6 +521,51 @@ int llm_decode_tree(llm_model* m, int32_t seq, const int32_t* tokens, const int3
                     const float* draft_probs, const float* uniforms, int32_t* path_out, int32_t* n_path_out,
                     int32_t* next_out, float* logits_out);
 
+/* ---- serving ---------------------------------------------------------------
+ * Operators of a decoding step of a served batch on the caller's own tensors:
+ * llm_append_kv norms and rotates new tokens' heads and writes their rows,
+ * llm_prefix_attention attends behind prefixes that sequences share,
+ * llm_sample_tokens draws the next tokens, llm_read_kv reads rows back. The
+ * conventions are those of the tree-decoding operators above (streams, errors,
+ * captures, values read on the device); they follow one another and those on one
+ * stream: llm_append_kv writes rows of the views that the attentions read.
+ * Source: as the tree-decoding operators; the formats are llm_kv_write's, the
+ * options llm_set_sampling's. */
+
+typedef struct {
+  int32_t dtype;                /* of q, k and v: LLM_BF16 or LLM_F32 */
+  int32_t out_dtype;            /* of q_out: LLM_BF16 or LLM_F32 */
+  int32_t n_tokens, n_heads;    /* n_heads: of q (0 with q NULL); k and v have the cache's heads */
+  const void *q, *k, *v;        /* [token][head][head_dim]; q may be NULL */
+  void* q_out;                  /* [token][head][head_dim]; may be q itself (same type and strides) */
+  int64_t q_strides[2], k_strides[2], v_strides[2], out_strides[2];  /* elements (token, head), multiples of 16 bytes */
+  const llm_kv_view* cache;     /* one layer */
+  const int32_t* seqs;          /* [n_tokens] sequence and */
+  const int32_t* rows;          /* [n_tokens] row that a token's k and v go to; out of range: they go nowhere */
+  const int32_t* positions;     /* [n_tokens] of the rotation, any int32; NULL: rows */
+  const float *q_norm, *k_norm; /* [head_dim] RMSNorm weights of a head (16-byte aligned), or NULL: no norm */
+  float norm_eps;
+  double rope_theta;            /* base; 0: no rotation */
+  int32_t rope_neox;            /* as in llm_config */
+} llm_append_kv_args;
+
+/* Per token and head: q and k normed (x / sqrt(mean(x^2) + eps) * weight) and
+ * rotated by position * rope_theta^(-2i/head_dim), q to q_out, k and v (as they
+ * are) to the cache's row in its format: bf16, or int8 codes and scales with the
+ * roundings of LLM_KV_Q8. Computed in fp32, angles in 64-bit fixed point (2^-30 of a
+ * turn at position 2^20), rounded once into the outputs. Int8 rows: values past
+ * 65504 * 127 saturate, a NaN makes its 32 values NaN. With q, norms and rope_theta
+ * left out it writes rows as they are, quantised for an int8 cache. The (seq, row)
+ * pairs of a call differ; of two equal ones the row holds parts of either. */
+int llm_append_kv(const llm_append_kv_args* args, void* cuda_stream);
+
+/* k[l][t], v[l][t] = the values of row rows[t] of sequence seqs[t] in every layer
+ * and head, as LLM_BF16 or LLM_F32 (int8 rows: code times scale, rounded once);
+ * zeros where seqs[t] or rows[t] is out of range. Both outputs lie at out_strides
+ * (elements: layer, token, head; multiples of 16 bytes). */
+int llm_read_kv(const llm_kv_view* cache, int32_t n_tokens, const int32_t* seqs, const int32_t* rows, int32_t out_dtype,
+                void* k, void* v, const int64_t* out_strides, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
