@@ -902,7 +902,7 @@ cudaError_t enqueue_tree_attention(llm_model* m, const BatchedIO& io, int l) {
   ap.mask_seq = io.M;
   ap.c = (float)(1.4426950408889634 / std::sqrt((double)hd));
   ap.B = 1;
-  ap.n = io.M;
+  ap.n = ap.nodes = io.M;
   ap.Hkv = H;
   ap.gq = m->gq;
   ap.by_gq = FastDiv(m->gq);

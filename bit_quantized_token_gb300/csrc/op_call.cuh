@@ -160,4 +160,7 @@ inline KvRows rows_of(const llm_kv_view& v) {
 
 inline int finish(cudaError_t e, const char* what) { return e == cudaSuccess ? LLM_OK : cuda_bad(e, what); }
 
+// The checks of llm_tree_attention's arguments, and the kernel's from them.
+bool attention_params(Call& c, const llm_tree_attention_args* a, TreeAttnParams& p);
+
 }  // namespace llmq

@@ -39,4 +39,9 @@ struct ReadParams {
 };
 cudaError_t launch_read_kv(const ReadParams& p, int hd, bool q8, cudaStream_t st);
 
+// Attention in two parts: every group's queries over the rows that its sequences
+// share (first), then every sequence's over its own, joined (second; see TreeAttnParams::Part).
+cudaError_t launch_prefix_attn(const TreeAttnParams& first, const TreeAttnParams& second, int hd, bool f32, bool q8,
+                               int n_sm, cudaStream_t st);
+
 }  // namespace llmq

@@ -1002,20 +1002,14 @@ cudaError_t status_word(int dev, int** p) {
   return cudaSuccess;
 }
 
-}  // namespace llmq
-
-extern "C" {
-
-int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
-  Call c;
-  if (!c.need(a != nullptr, LLM_ERR_INVALID_ARG, "the arguments are null")) return c.rc;
-  if (!c.need(a->dtype == LLM_BF16 || a->dtype == LLM_F32, LLM_ERR_UNSUPPORTED, "queries are bf16 or f32")) return c.rc;
+bool attention_params(Call& c, const llm_tree_attention_args* a, TreeAttnParams& p) {
+  if (!c.need(a->dtype == LLM_BF16 || a->dtype == LLM_F32, LLM_ERR_UNSUPPORTED, "queries are bf16 or f32")) return false;
   if (!c.need(a->n_nodes >= 1 && a->n_nodes <= kTreeMaxNodes, LLM_ERR_UNSUPPORTED, "%sn_nodes %lld (1..64)", "",
               a->n_nodes) ||
       !c.need(a->n_seq >= 1, LLM_ERR_INVALID_ARG, "n_seq is not positive") ||
       !c.need(std::isfinite(a->scale), LLM_ERR_INVALID_ARG, "the scale is not finite") ||
       !check_view(c, a->cache, "cache"))
-    return c.rc;
+    return false;
   const llm_kv_view &v = *a->cache, *t = a->tree;
   if (!c.need(a->n_heads > 0 && a->n_heads % v.n_heads == 0, LLM_ERR_INVALID_ARG,
               "n_heads is no multiple of the cache's heads") ||
@@ -1024,25 +1018,24 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
       !c.need((int64_t)v.n_heads * ((int64_t)a->n_nodes * (a->n_heads / v.n_heads) / 16 + 1) <= 65535,
               LLM_ERR_UNSUPPORTED, "too many heads") ||
       !c.need((int64_t)a->n_nodes * (a->n_heads / v.n_heads) < 65536, LLM_ERR_UNSUPPORTED, "too many heads"))
-    return c.rc;
+    return false;
   if (t && (!check_view(c, t, "tree") ||
             !c.need(t->dtype == v.dtype && t->head_dim == v.head_dim && t->n_heads == v.n_heads && t->n_layers == 1 &&
                         t->n_seq >= a->n_seq && t->rows >= a->n_nodes,
                     LLM_ERR_INVALID_ARG, "the tree's rows do not match the cache or the nodes")))
-    return c.rc;
+    return false;
   const int64_t hd = v.head_dim, m = a->dtype == LLM_F32 ? 4 : 8;
   const int64_t size[3] = {a->n_seq, a->n_nodes, a->n_heads};
   for (int i = 0; i < 3; ++i)
     if (!c.need(a->q_strides[i] >= 0 && a->out_strides[i] >= 0 && a->q_strides[i] % m == 0 &&
                     a->out_strides[i] % m == 0,
                 LLM_ERR_INVALID_ARG, "a stride of q or out is negative or no multiple of 16 bytes"))
-      return c.rc;
+      return false;
   if (!c.need(apart(hd, 3, size, a->out_strides), LLM_ERR_INVALID_ARG, "rows of out overlap") ||
       !view_memory(c, a->cache, "cache") || (t && (!view_memory(c, t, "tree") || !c.device("mask", a->mask, 8))) ||
       !c.device("q", a->q, 16) || !c.device("out", a->out, 16) || !c.device("lens", a->lens, 4) ||
       (a->counts && !c.device("counts", a->counts, 4)))
-    return c.rc;
-  TreeAttnParams p{};
+    return false;
   p.q = a->q;
   p.out = a->out;
   p.q_seq = a->q_strides[0], p.q_node = a->q_strides[1], p.q_head = a->q_strides[2];
@@ -1057,13 +1050,24 @@ int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
   p.c = (float)std::fmin(std::fmax(std::fabs((double)a->scale) * 1.4426950408889634, 1e-30), 3e38);
   p.neg = a->scale < 0.f;
   const cudaError_t es = status_word(c.dev, &p.status);
-  if (es != cudaSuccess) return cuda_bad(es, "status word");
+  if (es != cudaSuccess) c.rc = cuda_bad(es, "status word");
   p.B = a->n_seq;
-  p.n = a->n_nodes;
+  p.n = p.nodes = a->n_nodes;
   p.Hkv = v.n_heads;
   p.gq = a->n_heads / v.n_heads;
   p.by_gq = FastDiv(p.gq);
-  return finish(launch_tree_attn(p, (int)hd, a->dtype == LLM_F32, v.dtype == LLM_Q8G32, c.n_sm,
+  return c.rc == LLM_OK;
+}
+
+}  // namespace llmq
+
+extern "C" {
+
+int llm_tree_attention(const llm_tree_attention_args* a, void* cuda_stream) {
+  Call c;
+  TreeAttnParams p{};
+  if (!c.need(a != nullptr, LLM_ERR_INVALID_ARG, "the arguments are null") || !attention_params(c, a, p)) return c.rc;
+  return finish(launch_tree_attn(p, a->cache->head_dim, a->dtype == LLM_F32, a->cache->dtype == LLM_Q8G32, c.n_sm,
                                  static_cast<cudaStream_t>(cuda_stream)),
                 "tree attention launch");
 }

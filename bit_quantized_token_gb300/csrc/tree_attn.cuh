@@ -301,6 +301,26 @@ __device__ __forceinline__ int nth_longest(const int* lens, int B, int z, int la
   return ha ? __ffs(ha) - 1 : 31 + __ffs(hc);
 }
 
+// A block's sequence of queries (the first of several) and its nodes.
+struct TreeBlock {
+  int seq, cnt;
+  __device__ TreeBlock(const TreeAttnParams& p, int b) {
+    if (p.part == TreeAttnParams::kFirst) {
+      seq = min(max(p.starts[b], 0), p.all);
+      cnt = (min(max(p.starts[b + 1], seq), p.all) - seq) * p.n;
+    } else {
+      seq = b;
+      const int c = p.counts ? p.counts[b] : p.n;
+      cnt = min(max(c, 0), p.n);
+    }
+  }
+  // offset of a node's queries
+  __device__ __forceinline__ int64_t q_at(const TreeAttnParams& p, int node) const {
+    const int s = p.part == TreeAttnParams::kFirst ? p.by_n.div(node) : 0;
+    return (int64_t)(seq + s) * p.q_seq + (int64_t)(node - s * p.n) * p.q_node;
+  }
+};
+
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
@@ -311,8 +331,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // adds the parts from its own shared memory. (Loads from the other ranks took a
 // round trip for the weights and one for the parts, and a barrier more.) With S >
 // 1 every thread has arrived once (cluster_arrive) when its CTA's part of `in` was free.
+// In an attention of two parts the owner writes them out, or joins its row with the
+// first part's, which it waits for here: the kernels overlap until then.
 template <int HD, int N>
-constexpr int kJoin = N * HD * 4 + N * 12;
+constexpr int kJoin = N * HD * 4 + N * 16;
 template <int HD, bool F32, int N, int NT>
 __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float* so, const float2* sml, uint8_t* in,
                                             int rank, int b, int hkv, int m0, int rows) {
@@ -321,6 +343,15 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
   const float4* part = reinterpret_cast<const float4*>(so);  // [S][share][R4]
   const float2* ml = sml;                                    // [S][share]
   float* sw = reinterpret_cast<float*>(in + N * HD * 4 + N * 8);
+  float* sw_first = sw + N;                                  // the first part's weight
+  // row m0 + r of the block (its nodes follow one another): index of its (sequence, node, head) in part_ml
+  auto part_at = [&](int row) {
+    const int node = p.by_gq.div(row);
+    return ((int64_t)b * p.n + node) * (p.Hkv * p.gq) + hkv * p.gq + row - node * p.gq;
+  };
+  const bool second = p.part == TreeAttnParams::kSecond;
+  if (second) pdl_wait();
+  const bool first_has = second && b >= p.starts[0] && b < p.starts[p.G];
   __syncthreads();
   if (S > 1) {
     cg::cluster_group cl = cg::this_cluster();
@@ -351,7 +382,16 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
       L = fmaf(x.y, w, L);
       sw[k * share + r] = w;
     }
-    const float f = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
+    float f = L == 0.f ? 0.f : 1.f / L;  // nothing seen: 0
+    if (p.part == TreeAttnParams::kFirst) p.part_ml[part_at(m0 + rank * share + r)] = make_float2(M, L);
+    if (second) {
+      const float2 o = first_has ? __ldcg(p.part_ml + part_at(m0 + rank * share + r)) : make_float2(kNone, 0.f);
+      const float top = fmaxf(M, o.x), own_w = M <= kNone ? 0.f : ex2((M - top) * p.c);
+      const float first_w = o.x <= kNone ? 0.f : ex2((o.x - top) * p.c) * o.y, sum = fmaf(own_w, L, first_w);
+      f = sum == 0.f ? 0.f : 1.f / sum;
+      sw_first[r] = first_w * f;
+      f *= own_w;
+    }
     for (int k = 0; k < S; ++k) sw[k * share + r] *= f;
   }
   __syncthreads();
@@ -363,6 +403,15 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
     for (int k = 0; k < S; ++k) {
       const float4 x = part[k * share * R4 + i];
       const float f = sw[k * share + r];
+      a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+    }
+    if (p.part == TreeAttnParams::kFirst) {
+      reinterpret_cast<float4*>(p.part_o)[part_at(row) * R4 + i % R4] = a;
+      continue;
+    }
+    if (first_has && sw_first[r] != 0.f) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o) + part_at(row) * R4 + i % R4);
+      const float f = sw_first[r];
       a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
     }
     const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % R4);
@@ -414,13 +463,17 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
     mbar_fence_init();
   }
-  pdl_wait();  // nothing before this touches global memory
+  if (p.part != TreeAttnParams::kSecond) pdl_wait();  // nothing before this touches global memory
   pdl_trigger();
   const int hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
   const int b = p.sorted ? nth_longest(p.lens, p.B, blockIdx.z, lane) : blockIdx.z;
-  const int len_b = p.lens[b], cnt_b = p.counts ? p.counts[b] : p.n;
-  const int cnt = min(max(cnt_b, 0), p.n);
-  if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
+  const int len_b = p.lens[b];
+  const TreeBlock block(p, b);
+  const int cnt = block.cnt;
+  if (m0 >= cnt * p.gq) {  // no rows: the same in every CTA of the cluster
+    if (p.part == TreeAttnParams::kSecond) pdl_wait();  // (the kernel ends after the first part's)
+    return;
+  }
   const int len = min(max(len_b, 0), p.cache.rows);
   const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
   const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S);
@@ -463,7 +516,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
 #pragma unroll 4
     for (int i = tid; i < N * (HD / 8); i += 128 * G) {
       const int r = i / (HD / 8), ch = i % (HD / 8), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
-      const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
+      const int64_t off = block.q_at(p, node) + (int64_t)h * p.q_head + 8 * ch;
       uint8_t* dst = sq + (((ch / 8) * G + r / NB) * NQ * NB + r % NB) * 128 + 16 * ((ch & 7) ^ (r & 7));
       if constexpr (F32) {
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -879,7 +932,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   }
   __syncwarp();
   if (warp >= 4 * G && p.S > 1) cluster_arrive();
-  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
+  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, block.seq, hkv, m0, min(N, cnt * p.gq - m0));
   if (warp >= 4 * G && *s_abort) {  // no copy and no product in flight outlives the CTA
     const unsigned long long s0 = globaltimer();
     if (warp == 4 * G && lane == 0)
@@ -977,7 +1030,7 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   cudaError_t e = limit.raise(kern, C::kSmem, true);
   if (e != cudaSuccess) return e;
   TreeAttnParams& p = tp.p;
-  const int m_tiles = (p.n * p.gq + C::N - 1) / C::N;
+  const int m_tiles = (p.nodes * p.gq + C::N - 1) / C::N;
   const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
   int S = 1;
@@ -1009,7 +1062,7 @@ cudaError_t launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStre
   // (16 nodes x 8 heads over 4097 rows, fp32: 16 / 32 rows 12.1 / 14.2 us).
   // 128 rows at most (16 x 64 nodes over 1024..8192 rows: 32 / 64 / 128 rows 155 / 147 /
   // 85 us): 256 would fill tensor memory and leave one CTA on an SM.
-  const int M = p.n * p.gq, most = f32 ? 32 : 128;
+  const int M = p.nodes * p.gq, most = f32 ? 32 : 128;
   int N = 16;
   while (N < M && N < most) N *= 2;
   while (N > 16 && (int64_t)p.B * p.Hkv * ((M + N - 1) / N) * 8 < n_sm) N /= 2;

@@ -148,13 +148,17 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
     for (int i = 0; i < 8; ++i) mbar_init(raw_full + i, 1), mbar_init(raw_empty + i, i < 4 ? 128 : 256);
     mbar_fence_init();
   }
-  pdl_wait();
+  if (p.part != TreeAttnParams::kSecond) pdl_wait();
   pdl_trigger();
   const int hkv = blockIdx.y % p.Hkv, m0 = (blockIdx.y / p.Hkv) * N, rank = blockIdx.x;
   const int b = p.sorted ? nth_longest(p.lens, p.B, blockIdx.z, lane) : blockIdx.z;
-  const int len_b = p.lens[b], cnt_b = p.counts ? p.counts[b] : p.n;
-  const int cnt = min(max(cnt_b, 0), p.n);
-  if (m0 >= cnt * p.gq) return;  // no rows: the same in every CTA of the cluster
+  const int len_b = p.lens[b];
+  const TreeBlock block(p, b);
+  const int cnt = block.cnt;
+  if (m0 >= cnt * p.gq) {  // no rows: the same in every CTA of the cluster
+    if (p.part == TreeAttnParams::kSecond) pdl_wait();  // (the kernel ends after the first part's)
+    return;
+  }
   const int len = min(max(len_b, 0), p.cache.rows);
   const int n_pre = (len + BK - 1) / BK, n_tiles = n_pre + (p.tree.k ? 1 : 0);
   const int t0 = (int)((int64_t)n_tiles * rank / p.S), t1 = (int)((int64_t)n_tiles * (rank + 1) / p.S), n_own = t1 - t0;
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
 #pragma unroll 1
     for (int i = th; i < N * (HD / 8); i += nth) {
       const int r = i / (HD / 8), ch = i % (HD / 8), node = p.by_gq.div(m0 + r), h = hkv * p.gq + m0 + r - node * p.gq;
-      const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * ch;
+      const int64_t off = block.q_at(p, node) + (int64_t)h * p.q_head + 8 * ch;
       uint8_t* dst = sq + (((ch / 8) * G + r / NB) * NQ * NB + r % NB) * 128 + 16 * ((ch & 7) ^ (r & 7));
       if constexpr (F32) {
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(TreeQ8<HD, F32, G>::NT, 1) tree_attn_q8_kernel
   }
   __syncwarp();
   if (warp >= kConvWarp && p.S > 1) cluster_arrive();
-  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, b, hkv, m0, min(N, cnt * p.gq - m0));
+  join_splits<HD, F32, N, NT>(p, reinterpret_cast<float*>(sm), sml, sjoin, rank, block.seq, hkv, m0, min(N, cnt * p.gq - m0));
   if (warp >= kTmaWarp && *s_abort) {  // (see tree_attn_tc_kernel)
     const unsigned long long s0 = globaltimer();
     if (warp == kTmaWarp && lane == 0)
@@ -681,7 +685,7 @@ cudaError_t launch_tree_q8_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   cudaError_t e = limit.raise(kern, C::kSmem, true);
   if (e != cudaSuccess) return e;
   TreeAttnParams& p = tp.p;
-  const int m_tiles = (p.n * p.gq + C::N - 1) / C::N;
+  const int m_tiles = (p.nodes * p.gq + C::N - 1) / C::N;
   const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
   static ClusterCount at_once;
@@ -695,7 +699,7 @@ cudaError_t launch_tree_q8(const TreeAttnParams& p, bool f32, int n_sm, cudaStre
   TreeAttnTcParams tp;
   tp.p = p;
   if (!encode_all<HD, true>(tp)) return cudaErrorNotSupported;
-  const int M = p.n * p.gq;
+  const int M = p.nodes * p.gq;
   // 16 rows a block; two blocks share the widened tiles where tensor memory holds both
   if (f32)
     return HD == 128 || M <= 16 ? launch_tree_q8_t<HD, true, 1>(tp, n_sm, st)

@@ -10,6 +10,7 @@ from . import tree as _t
 from .tree import KVView, _check, _fail, _flat, _name
 
 _APPEND = struct.Struct("@4i4P8q6Pfdi0P").pack
+_PREFIX = struct.Struct("@4i2P6q5Pf0PPi0PPPPq").pack
 _STRIDES = struct.Struct("@3q").pack
 _DTYPES: dict = {}  # torch's dtype objects -> llm_dtype, once a tensor has come in
 _UNSUPPORTED = -2
@@ -90,5 +91,46 @@ def read_kv(cache: KVView, seqs, rows, k, v, stream: int | None = None) -> None:
     T = shape[1]
     rc = L.llm_read_kv(cache._at, T, _flat(seqs, "seqs", _t._i32, (T,)), _flat(rows, "rows", _t._i32, (T,)), kind,
                        k.data_ptr(), v.data_ptr(), _STRIDES(*stride[:3]), stream)
+    if rc:
+        _check(rc)
+
+
+def prefix_workspace(q) -> int:
+    """Bytes of prefix_attention's workspace for queries of q's shape [seq, node, head, head_dim]; see
+    llm_prefix_workspace."""
+    n = _t._base.lib().llm_prefix_workspace(*q.shape)
+    if n < 0:
+        _check(n)
+    return n
+
+
+def prefix_attention(q, prefix: KVView, starts, prefix_lens, cache: KVView, tree: KVView | None, lens, mask, out,
+                     workspace, counts=None, scale: float | None = None, stream: int | None = None) -> None:
+    """tree_attention where sequences starts[g] .. starts[g + 1] - 1 also see the first prefix_lens[g] rows of the
+    prefix view's sequence g, which are read once for all of them. workspace: a contiguous CUDA tensor of
+    prefix_workspace(q) bytes, one for each of the calls that may overlap; see llm_prefix_attention."""
+    L = _load()
+    shape, dt = q.shape, q.dtype
+    kind = _kind(q, "queries")
+    B, n, H, hd = shape
+    if out.shape != shape or out.dtype is not dt:
+        _fail("out must have q's shape and type")
+    if cache.shape[4] != hd:
+        _fail(f"q has head_dim {hd}, the cache {cache.shape[4]}")
+    q0, q1, q2, q3 = q.stride()
+    o0, o1, o2, o3 = out.stride()
+    if q3 != 1 or o3 != 1:
+        _fail("a head's values must be contiguous in q and out")
+    G = prefix_lens.shape[0]
+    if not workspace.is_contiguous():
+        _fail("the workspace is not contiguous")
+    rc = L.llm_prefix_attention(
+        _PREFIX(kind, B, n, H, q.data_ptr(), out.data_ptr(), q0, q1, q2, o0, o1, o2, cache._at,
+                0 if tree is None else tree._at, _flat(lens, "lens", _t._i32, (B,)),
+                0 if tree is None else _flat(mask, "mask", _t._i64, (B, n)),
+                0 if counts is None else _flat(counts, "counts", _t._i32, (B,)), hd ** -0.5 if scale is None else scale,
+                prefix._at, G, _flat(starts, "starts", _t._i32, (G + 1,)),
+                _flat(prefix_lens, "prefix_lens", _t._i32, (G,)), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size()), stream)
     if rc:
         _check(rc)

@@ -566,6 +566,30 @@ int llm_append_kv(const llm_append_kv_args* args, void* cuda_stream);
 int llm_read_kv(const llm_kv_view* cache, int32_t n_tokens, const int32_t* seqs, const int32_t* rows, int32_t out_dtype,
                 void* k, void* v, const int64_t* out_strides, void* cuda_stream);
 
+typedef struct {
+  llm_tree_attention_args attention;  /* the queries, every sequence's own rows, its new tokens (tree, mask), the output */
+  const llm_kv_view* prefix;    /* one layer, alike the cache: rows of its sequence g are those that group g shares */
+  int32_t n_groups;             /* up to the prefix view's sequences */
+  const int32_t* starts;        /* [n_groups + 1] ascending: sequences starts[g] .. starts[g + 1] - 1 are group g */
+  const int32_t* prefix_lens;   /* [n_groups] rows of each prefix (clamped to 0..rows) */
+  void* workspace;              /* device memory, 16-byte aligned; calls that may overlap have one each */
+  int64_t workspace_bytes;      /* at least llm_prefix_workspace's */
+} llm_prefix_attention_args;
+
+/* llm_tree_attention where every node sees, before its sequence's own rows, the
+ * first prefix_lens[g] rows of its group's prefix; those are read and multiplied
+ * once for all sequences of the group. Sequences outside of starts[0] ..
+ * starts[n_groups] - 1 see no prefix. What llm_tree_attention says of types,
+ * precision, counts, masks and empty rows holds here too (bf16 queries over bf16
+ * prefix rows: the probabilities carry 8 bits where more than 64 query rows of a kv
+ * head share them). One decode token: n_nodes = 1, its row already in the cache and
+ * tree NULL, or its row as the tree's. llm_tree_status reports waits that ran out. */
+int llm_prefix_attention(const llm_prefix_attention_args* args, void* cuda_stream);
+
+/* Bytes of llm_prefix_attention's workspace, or a negative llm_status. Nothing in it
+ * has to be set, or is kept for another call. */
+int64_t llm_prefix_workspace(int32_t n_seq, int32_t n_nodes, int32_t n_heads, int32_t head_dim);
+
 #ifdef __cplusplus
 }
 #endif

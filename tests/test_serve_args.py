@@ -3,9 +3,18 @@ import pytest
 import torch
 
 import bit_quantized_token_gb300 as bq
-from test_tree_args import Fake, view
+from test_tree_args import Fake as _Fake
+from test_tree_args import view
 
 F32, BF16, I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+class Fake(_Fake):
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -77,3 +86,42 @@ def test_refused(i):
     with pytest.raises(bq.LlmError) as e:
         call()
     assert text in str(e.value), str(e.value)
+
+
+def attend(B=4, n=2, H=4, hd=64, G=2, dtype=BF16, cache=None, tree=None, prefix=None, size=None, **kw):
+    q = Fake((B, n, H, hd), dtype)
+    a = dict(q=q, prefix=prefix or view(G, hd=hd), starts=Fake((G + 1,), I32), prefix_lens=Fake((G,), I32),
+             cache=cache or view(B, hd=hd), tree=tree or view(B, rows=n, hd=hd), lens=Fake((B,), I32),
+             mask=Fake((B, n), torch.int64), out=Fake((B, n, H, hd), dtype), workspace=Fake((1 << 20,), torch.uint8))
+    a.update(kw)
+    bq.prefix_attention(**a)
+
+
+REFUSED_PREFIX = [
+    ("n_nodes", lambda: attend(n=65, tree=view(4, rows=65))),
+    ("queries of type float16", lambda: attend(dtype=torch.float16)),
+    ("out must have", lambda: attend(out=Fake((4, 2, 4, 64), F32))),
+    ("multiple of the cache's heads", lambda: attend(H=3)),
+    ("head_dim 64, the cache 128", lambda: attend(cache=view(4, hd=128))),
+    ("fewer sequences", lambda: attend(cache=view(3))),
+    ("scale is not finite", lambda: attend(scale=float("inf"))),
+    ("contiguous int32", lambda: attend(starts=Fake((2,), I32))),
+    ("contiguous int32", lambda: attend(prefix_lens=Fake((2,), torch.int64))),
+    ("contiguous int64", lambda: attend(mask=Fake((4, 2), I32))),
+    ("not aligned", lambda: attend(cache=view(4, at=(1 << 20) + 8))),
+]
+
+
+@pytest.mark.parametrize("i", range(len(REFUSED_PREFIX)))
+def test_prefix_refused(i):
+    text, call = REFUSED_PREFIX[i]
+    with pytest.raises(bq.LlmError) as e:
+        call()
+    assert text in str(e.value), str(e.value)
+
+
+def test_prefix_workspace_sizes():
+    assert bq.prefix_workspace(Fake((4, 2, 6, 64))) == 4 * 2 * 6 * (64 * 4 + 8)
+    for shape in ((0, 2, 6, 64), (4, 65, 6, 64), (4, 2, 6, 96), (4, 2, 0, 128), (1 << 17, 2, 6, 64)):
+        with pytest.raises(bq.LlmError):
+            bq.prefix_workspace(Fake(shape))
