@@ -46,12 +46,12 @@ EXPORTS = ["llm_model_create", "llm_model_destroy", "llm_prefill", "llm_prefill_
            "llm_debug_hidden", "llm_debug_unpack", "llm_model_stats", "llm_profile_step", "llm_time_kernel", "llm_sync",
            "llm_last_error", "llm_op_matvec", "llm_op_matvec_w4a8", "llm_matvec_noalloc", "llm_phase_times", "llm_debug_fail_alloc", "llm_debug_expire_waits",
            "llm_debug_hidden_batch", "llm_tree_attention", "llm_tree_status", "llm_token_probs", "llm_verify_tree", "llm_commit_tree", "llm_decode_tree",
-           "llm_append_kv", "llm_read_kv", "llm_prefix_attention", "llm_prefix_workspace"]
+           "llm_append_kv", "llm_read_kv", "llm_prefix_attention", "llm_prefix_workspace", "llm_sample_tokens"]
 
 
 # translation units of the library, compiled in parallel and linked into one shared object
 UNITS = ["llmq.cu", "step_kernels.cu", "step_kernels_kv8.cu", "stepll_kernels.cu", "tree.cu", "tree_attn_64.cu",
-         "tree_attn_128.cu", "kv_rows.cu", "prefix.cu"]
+         "tree_attn_128.cu", "kv_rows.cu", "prefix.cu", "sample_rows.cu"]
 BUILD_DIR = os.path.join(_HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -181,6 +181,7 @@ def lib() -> C.CDLL:
             "llm_read_kv": (i32, [P, i32, P, P, i32, P, P, P, P]),
             "llm_prefix_attention": (i32, [P, P]),
             "llm_prefix_workspace": (C.c_int64, [i32, i32, i32, i32]),
+            "llm_sample_tokens": (i32, [P, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -457,5 +458,5 @@ def matvec_noalloc(model: Model, name: str, x, y, stream: int | None = None) -> 
     _check(lib().llm_matvec_noalloc(model.h, name.encode(), _ptr(x), _ptr(y), stream), model.h)
 
 
-from .serve import append_kv, prefix_attention, prefix_workspace, read_kv  # noqa: E402
+from .serve import append_kv, prefix_attention, prefix_workspace, read_kv, sample_tokens  # noqa: E402
 from .tree import KVView, commit_tree, token_probs, tree_attention, tree_masks, tree_status, verify_tree  # noqa: E402

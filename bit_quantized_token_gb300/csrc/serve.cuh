@@ -44,4 +44,19 @@ cudaError_t launch_read_kv(const ReadParams& p, int hd, bool q8, cudaStream_t st
 cudaError_t launch_prefix_attn(const TreeAttnParams& first, const TreeAttnParams& second, int hd, bool f32, bool q8,
                                int n_sm, cudaStream_t st);
 
+constexpr int kSampleList = 2048;  // tokens around the borders that one CTA sorts
+
+struct SampleRowsParams {
+  const float* logits;
+  int64_t stride;            // of the rows, in elements
+  const float *u, *temperature, *top_p, *min_p;  // [R]; all but u may be null
+  const int* top_k;          // [R] or null
+  int* tokens;               // [R]
+  float* probs;              // [R] or null
+  int R, V;
+  int slice;                 // set by the launch: logits of a CTA
+  bool pdl = true;
+};
+cudaError_t launch_sample_rows(SampleRowsParams& p, int n_sm, cudaStream_t st);
+
 }  // namespace llmq

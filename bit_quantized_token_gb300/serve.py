@@ -11,6 +11,7 @@ from .tree import KVView, _check, _fail, _flat, _name
 
 _APPEND = struct.Struct("@4i4P8q6Pfdi0P").pack
 _PREFIX = struct.Struct("@4i2P6q5Pf0PPi0PPPPq").pack
+_SAMPLE = struct.Struct("@Pq2i7P").pack
 _STRIDES = struct.Struct("@3q").pack
 _DTYPES: dict = {}  # torch's dtype objects -> llm_dtype, once a tensor has come in
 _UNSUPPORTED = -2
@@ -132,5 +133,27 @@ def prefix_attention(q, prefix: KVView, starts, prefix_lens, cache: KVView, tree
                 prefix._at, G, _flat(starts, "starts", _t._i32, (G + 1,)),
                 _flat(prefix_lens, "prefix_lens", _t._i32, (G,)), workspace.data_ptr(),
                 workspace.numel() * workspace.element_size()), stream)
+    if rc:
+        _check(rc)
+
+
+def sample_tokens(logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,
+                  stream: int | None = None) -> None:
+    """tokens [row] int32 = a token of each row of logits [row, vocab], drawn with uniforms [row] under the row's own
+    temperature, top_p, min_p (float32 [row]) and top_k (int32 [row]; None: off); probs [row] float32: what it was
+    drawn with; see llm_sample_tokens."""
+    L = _load()
+    R, V = logits.shape
+    s0, s1 = logits.stride()
+    if logits.dtype is not _t._f32 or (V > 1 and s1 != 1):
+        _fail("logits: float32 with contiguous rows is needed")
+    shape, f32, i32 = (R,), _t._f32, _t._i32
+    rc = L.llm_sample_tokens(
+        _SAMPLE(logits.data_ptr(), s0, R, V, _flat(uniforms, "uniforms", f32, shape),
+                0 if temperature is None else _flat(temperature, "temperature", f32, shape),
+                0 if top_k is None else _flat(top_k, "top_k", i32, shape),
+                0 if top_p is None else _flat(top_p, "top_p", f32, shape),
+                0 if min_p is None else _flat(min_p, "min_p", f32, shape), _flat(tokens, "tokens", i32, shape),
+                0 if probs is None else _flat(probs, "probs", f32, shape)), stream)
     if rc:
         _check(rc)

@@ -590,6 +590,32 @@ int llm_prefix_attention(const llm_prefix_attention_args* args, void* cuda_strea
  * has to be set, or is kept for another call. */
 int64_t llm_prefix_workspace(int32_t n_seq, int32_t n_nodes, int32_t n_heads, int32_t head_dim);
 
+typedef struct {
+  const float* logits;          /* [n_rows][vocab] at logits_stride (elements) */
+  int64_t logits_stride;
+  int32_t n_rows, vocab;
+  const float* uniforms;        /* [n_rows] in [0, 1) (others are clamped) */
+  const float* temperature;     /* [n_rows]; 0 (or below, NaN): the largest logit; NULL: 1 */
+  const int32_t* top_k;         /* [n_rows]; 0 (or below) or NULL: off; up to vocab */
+  const float* top_p;           /* [n_rows]; 1 (or above, NaN) or NULL: off */
+  const float* min_p;           /* [n_rows]; 0 (or below, NaN) or NULL: off */
+  int32_t* tokens;              /* [n_rows] out */
+  float* probs;                 /* [n_rows] out: what the token was drawn with, or NULL */
+} llm_sample_args;
+
+/* The next token of every row, under options of its own, read on the device. In
+ * the order of llm_set_sampling (the largest logit first, ties by id) the options
+ * keep, of p = softmax(logit / temperature): the first top_k tokens; of those the
+ * shortest prefix whose mass reaches top_p of theirs; of those the ones with p >=
+ * min_p times the largest p. The token is the first whose cumulative probability
+ * exceeds uniforms[r] times the kept ones' total, as llm_set_sampling chooses it from
+ * the same draw; probs[r] is its share of that total. Borders are decided with sums
+ * of 36 bits or more (of the whole row's mass). A NaN logit counts as -inf, +inf as the
+ * largest finite value; a row without a finite logit gives -1. The same inputs give the
+ * same token in any batch. A row with thousands of logits around a border (all alike,
+ * or crowds of equal ones) takes up to 0.2 ms. UNSUPPORTED: vocab over 524288. */
+int llm_sample_tokens(const llm_sample_args* args, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

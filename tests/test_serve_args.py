@@ -125,3 +125,36 @@ def test_prefix_workspace_sizes():
     for shape in ((0, 2, 6, 64), (4, 65, 6, 64), (4, 2, 6, 96), (4, 2, 0, 128), (1 << 17, 2, 6, 64)):
         with pytest.raises(bq.LlmError):
             bq.prefix_workspace(Fake(shape))
+
+
+def sample(R=3, V=100, **kw):
+    f = lambda *s: Fake(s, F32)  # noqa: E731
+    a = dict(logits=f(R, V), uniforms=f(R), tokens=Fake((R,), I32), temperature=f(R), top_k=Fake((R,), I32), top_p=f(R),
+             min_p=f(R), probs=f(R))
+    a.update(kw)
+    bq.sample_tokens(**a)
+
+
+REFUSED_SAMPLE = [
+    ("logits: float32", lambda: sample(logits=Fake((3, 100), BF16))),
+    ("logits: float32", lambda: sample(logits=Fake((3, 100), F32, stride=(200, 2)))),
+    ("uniforms is needed", lambda: sample(uniforms=None)),
+    ("tokens: a contiguous int32", lambda: sample(tokens=Fake((3,), torch.int64))),
+    ("temperature: a contiguous float32", lambda: sample(temperature=Fake((2,), F32))),
+    ("top_k: a contiguous int32", lambda: sample(top_k=Fake((3,), F32))),
+    ("top_p: a contiguous float32", lambda: sample(top_p=Fake((3, 1), F32))),
+    ("min_p: a contiguous float32", lambda: sample(min_p=Fake((3,), BF16))),
+    ("probs: a contiguous float32", lambda: sample(probs=Fake((3,), I32))),
+    ("n_rows or vocab", lambda: sample(R=0)),
+    ("n_rows or vocab", lambda: sample(V=0)),
+    ("too large", lambda: sample(V=524289)),
+    ("not aligned", lambda: sample(logits=Fake((3, 100), F32, at=(1 << 20) + 2))),
+]
+
+
+@pytest.mark.parametrize("i", range(len(REFUSED_SAMPLE)))
+def test_sample_refused(i):
+    text, call = REFUSED_SAMPLE[i]
+    with pytest.raises(bq.LlmError) as e:
+        call()
+    assert text in str(e.value), str(e.value)
