@@ -6,23 +6,26 @@
 // top_k; of those the shortest whose mass reaches top_p of theirs; the w_j of at least
 // min_p. The token is the first one whose cumulative mass passes u times the kept
 // one's. So nothing is sorted but what lies around the borders:
-//   1. a cluster holds a row in registers, read once; its largest logit;
-//   2. a histogram over Y (32 buckets an octave, 64 octaves; finer for high
-//      temperatures): the count and the mass of every bucket;
-//   3. from their running sums, the few buckets in which the borders can lie (the
-//      border of one option moves the next one's by a bucket's mass at most);
-//   4. their tokens, some hundreds, to the first CTA, which sorts them and finds all
-//      borders exactly.
-// Rows that put more than kSampleList tokens into those buckets (all logits alike,
-// crowds of equal ones) take the long way: each border by three digits of the
+//   1. a histogram over -l log2(e) / T, 32 buckets an octave (finer for high
+//      temperatures): the count and the mass of every bucket, in one pass, whose
+//      window hangs on the largest of the first logits;
+//   2. from the running sums below the row's largest logit, the few buckets in which
+//      the borders can lie (the border of one option moves the next one's by a
+//      bucket's mass at most);
+//   3. a second pass brings their tokens, some hundreds, to the first CTA, which
+//      sorts them and finds all borders exactly.
+// A window that turns out too low, or too narrow, is set again from the row's exact
+// range. Rows that put more than kSampleList tokens into those buckets (all logits
+// alike, crowds of equal ones) take the long way: each border by three digits of the
 // logits' keys, over all tokens.
 //
-// Masses decide integers, so they are integers: a term is 2^-37 steps below its
-// bucket's largest, computed from the logit's exact distance in pairs of floats and
-// then in fixed point; sums have 2^-44 steps, in 64 bits, whatever their order. A
-// border is off by less than 2^-36 of the row's mass: of 150,000 borders, one draw in
-// some 10^5 .. 10^6 falls on another side than with exact sums. fp32 sums would lose one draw in
-// 2,000, fp64 has 1/64 of fp32's lanes here.
+// Masses decide integers, so they are integers: a term is a number of 2^-34 steps
+// below its bucket's largest, from the exact product of logit and temperature in a
+// pair of floats and then in fixed point; sums have 2^-44 steps, in 64 bits, whatever
+// their order. A border is off by less than 2^-34 of the row's mass: of 150,000 borders, one draw
+// in some 10^5 .. 10^6 falls on another side than with exact sums. fp32 sums would lose one draw
+// in 2,000, and fp64 has 1/64 of fp32's lanes here. Terms below 2^-4 of the largest
+// need no more than fp32 for their place in the bucket.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -35,8 +38,13 @@ namespace cg = cooperative_groups;
 namespace {
 
 using u64 = unsigned long long;
-constexpr int kSampNT = 512, kSampB = 2048;  // threads; buckets of the histogram (in fours of a thread)
+constexpr int kSampNT = 512;
+constexpr int kSampB = 2048;           // buckets below the row's largest logit: 64 octaves (fewer, finer ones)
+constexpr int kSampTable = 2 * kSampB; // a CTA's buckets, by their number modulo the table
 constexpr int kSampPer = kSampB / kSampNT;
+constexpr int kSampMaxSlice = 180000;
+constexpr int kSampU = 8;               // loads of a thread in flight
+constexpr int kListPer = kSampleList / kSampNT;
 
 __constant__ const u64 kRoot32[32] = {  // 2^(63 - j/32)
     0x8000000000000000ull, 0x7D41D96DB915019Dull, 0x7A92BE8A92436616ull, 0x77F25CCDEE6D7AE6ull,
@@ -48,33 +56,39 @@ __constant__ const u64 kRoot32[32] = {  // 2^(63 - j/32)
     0x4C1BF828C6DC54B8ull, 0x4A7A77D47F7B84B1ull, 0x48E1E9B9D588E19Bull, 0x47521CC5A2E6A9E0ull,
     0x45CAE0F1F545EB73ull, 0x444C0740496D4294ull, 0x42D561B3E6243D8Aull, 0x4166C34C5615D0ECull};
 
+
 struct SampShared {
-  u64 mass[kSampB];         // running sums over the buckets, inclusive
-  uint32_t count[kSampB];
   union {
-    uint32_t h[3][kSampB];  // this CTA's histogram: sums of D, counts (low half) and carries of D (high half)
+    struct {                     // this CTA's histogram
+      uint32_t lo[kSampTable];   // how far its terms lie below a bucket's largest, in 2^-34 steps, added up
+      uint32_t hi[kSampTable];   // their number (18 bits), carries of lo (14 bits: a term's is below 2^28.5)
+    };
+    uint32_t h[3][kSampB];       // the long way's: sums of the terms' low and high words, counts
     struct {
-      u64 local[kSampleList];   // entries of this CTA; later, on the first, the list's running masses
-      uint32_t start[kSampB];   // first entry of a bucket
+      u64 local[kSampleList];    // entries of this CTA; later, on the first, the list's running masses
+      uint32_t start[kSampB];    // first entry of a bucket
+      uint16_t bucket[kSampleList];
     };
   };
-  u64 list[kSampleList];    // of the first CTA: every CTA's entries, (key, complement of the id)
-  uint8_t flag[kSampB];     // 1: the bucket is gathered; 2: it or a neighbour
-  u64 best[16];             // every CTA's largest (key, complement of the id)
-  float least[16];
+  u64 mass[kSampB];              // running sums over the buckets, inclusive
+  uint32_t count[kSampB];
+  u64 list[kSampleList];         // of the first CTA: every CTA's entries, (key, complement of the id)
+  uint8_t flag[kSampB];          // the bucket is gathered
+  u64 best[16];                  // greedy: every CTA's largest (key, complement of the id)
+  float4 range[16];              // of every CTA: largest logit, least in its window, largest outside, first bucket
   u64 warp64[kSampNT / 32];
   uint32_t warp32[kSampNT / 32];
-  float fwarp[kSampNT / 32];
-  int found[2];
+  float3 warpf[kSampNT / 32];
+  int found;
   uint32_t total, n_local, n_list, base;
   // the options
-  float ch, cl, u;
-  double y_min;             // -log2(min_p), or infinite
-  u64 p_fix;                // top_p in 2^-64 steps; 0: off
-  int top_k, greedy;
-  // the first CTA's answers
+  float ch, cl, u;               // log2(e) / T
+  double y_min;                  // -log2(min_p)
+  u64 p_fix;                     // top_p in 2^-64 steps; 0: off
+  int top_k, greedy, by_m;       // by_m: min_p leaves something out
+  // answers
   u64 res_mass[3];
-  uint32_t res_rank[3];
+  uint32_t res_rank[2];
   u64 key;
 };
 
@@ -82,24 +96,31 @@ struct Term {
   int b;       // bucket
   uint32_t q;  // place in it, 2^-32 steps
 };
-
-// Y in S = 32 << fine buckets an octave. False: no weight (2^-64 and below).
-__device__ __forceinline__ bool term_of(float l, float m, float ch, float cl, float S, Term& t) {
+// The long way's: Y = (m - l) log2(e) / T in 32 buckets an octave. False: no weight (2^-64 and below).
+__device__ __forceinline__ bool term_of(float l, float m, float ch, float cl, Term& t) {
   const float d = __fsub_rn(m, l), bb = __fsub_rn(d, m);
   const float dl = __fsub_rn(__fsub_rn(m, __fsub_rn(d, bb)), __fadd_rn(l, bb));  // m - l = d + dl, exactly
-  const float p = __fmul_rn(d, ch), y = __fmul_rn(p, S);
+  const float p = __fmul_rn(d, ch), y = __fmul_rn(p, 32.f);
   if (!(y < (float)kSampB + 1.f)) return false;
   float e = __fmaf_rn(d, ch, -p);
   e = __fmaf_rn(d, cl, e);
   e = __fmaf_rn(dl, ch, e);
   const float fl = floorf(y);
-  const long long q = (long long)__float2uint_rn((y - fl) * 4294967296.f) + __float2int_rn(e * S * 4294967296.f);
+  const long long q = (long long)__float2uint_rn((y - fl) * 4294967296.f) + __float2int_rn(e * 137438953472.f);
   t.b = (int)fl + (int)(q >> 32);  // (the remainder may take it past a border)
   t.q = (uint32_t)q;
   return t.b >= 0 && t.b < kSampB;
 }
+// -l log2(e) / T in S buckets an octave (ch, cl times S), |y| below 2^22: the bucket's number and place.
+__device__ __forceinline__ Term place_of(float l, float chS, float clS) {
+  const float p = __fmul_rn(-l, chS), fl = floorf(p);
+  float e = __fmaf_rn(-l, chS, -p);
+  e = __fmaf_rn(-l, clS, e);
+  const long long q = (long long)__float2uint_rn((p - fl) * 4294967296.f) + __float2int_rn(e * 4294967296.f);
+  return {(int)fl + (int)(q >> 32), (uint32_t)q};
+}
 // 2^37 (1 - 2^-z) for the place q of a bucket: z - z^2/2 + z^3/6 - .. in fixed point
-__device__ __forceinline__ uint32_t below(uint32_t q, int fine) {
+__device__ __forceinline__ uint32_t below37(uint32_t q, int fine) {
   const uint32_t z = __umulhi(q, 2977044472u) >> fine;  // 2^37 ln(2) / S: below 2^31.5
   uint32_t a = ~__umulhi(z, 26843546u);                 // 1 - z/5
   a = ~__umulhi(z >> 7, a);                             // 1 - z/4 ..
@@ -107,20 +128,20 @@ __device__ __forceinline__ uint32_t below(uint32_t q, int fine) {
   a = ~__umulhi(z >> 6, a);
   return __umulhi(z, a);
 }
-// a 2^-37 steps of the largest term of bucket b, in 2^-44 steps of the row's largest
+__device__ __forceinline__ uint32_t below(uint32_t q, int fine) { return (below37(q, fine) + 4) >> 3; }
+// a 2^-34 steps of the largest term of bucket b, in 2^-44 steps of the largest of bucket 0
 __device__ __forceinline__ u64 weight_of(u64 a, int b, int fine) {
+  a <<= 10;
   if (fine) {
     const int lo = b & ((1 << fine) - 1);
-    if (lo) {
-      const uint32_t f = below((uint32_t)lo << (32 - fine), 0);
-      a = __umul64hi(a << 7, ((1ull << 37) - f) << 27) >> 7;
-    }
+    if (lo) a = __umul64hi(a, ((1ull << 37) - below37((uint32_t)lo << (32 - fine), 0)) << 27);
     b >>= fine;
   }
-  const u64 r = __umul64hi(a << 7, kRoot32[b & 31]);
+  const u64 r = __umul64hi(a, kRoot32[b & 31]);
   const int s = (b >> 5) - 1;
   return s < 0 ? r << 1 : s == 0 ? r : (r + (1ull << (s - 1))) >> s;
 }
+__device__ __forceinline__ u64 weight_of(const Term& t, int fine) { return weight_of((1ull << 34) - below(t.q, fine), t.b, fine); }
 __device__ __forceinline__ float key_float(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
@@ -150,24 +171,86 @@ __device__ __forceinline__ void scan2(u64& a, uint32_t& c, SampShared& s) {
 
 // ceil(mass f 2^-64)
 __device__ __forceinline__ u64 ceil_part(u64 mass, u64 f) { return __umul64hi(mass, f) + (mass * f != 0); }
+// The first of kSampB rising values at which f holds (kSampB: none), by a warp.
+template <typename F>
+__device__ __forceinline__ int first_at(F f) {
+  const int lane = threadIdx.x & 31;
+  constexpr int Q = kSampB / 32;
+  const unsigned c = __ballot_sync(0xffffffffu, f(Q * lane + Q - 1));
+  if (!c) return kSampB;
+  const int at = Q * (__ffs(c) - 1);
+  static_assert(Q == 64, "two a lane");
+  const bool odd = f(at + 2 * lane + 1), even = f(at + 2 * lane);
+  const int l = __ffs(__ballot_sync(0xffffffffu, odd)) - 1;
+  return at + 2 * l + !__shfl_sync(0xffffffffu, even, l);
+}
 
-template <int KPT>
-__global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel(const SampleRowsParams p) {
+// Entries e 512 + tid in v[e], sorted from the largest on (bitonic; n2, a power of two, from 32 on, or 512 E with
+// E > 1: those that are not 0). buf: room for 512 E.
+template <int E>
+__device__ __forceinline__ void sort_list(u64 (&v)[kListPer], u64* buf, int n2) {
+  const int tid = threadIdx.x;
+#pragma unroll 1
+  for (int k = 2; k <= n2; k *= 2)
+#pragma unroll 1
+    for (int j = k / 2; j > 0; j /= 2) {
+      if (E > 1 && j >= kSampNT) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int f = e + 1; f < E; ++f)
+            if ((e ^ f) == j / kSampNT && (v[e] < v[f]) == (((e * kSampNT) & k) == 0)) {
+              const u64 x = v[e];
+              v[e] = v[f], v[f] = x;
+            }
+        continue;
+      }
+      u64 o[E];
+      if (j >= 32) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) buf[e * kSampNT + tid] = v[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = buf[e * kSampNT + (tid ^ j)];
+        __syncthreads();
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = (u64)__shfl_xor_sync(0xffffffffu, v[e], j);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool larger = (((e * kSampNT + tid) & k) == 0) == ((tid & j) == 0);  // keeps the larger one
+        v[e] = (o[e] > v[e]) == larger ? o[e] : v[e];
+      }
+    }
+}
+
+__global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRowsParams p) {
   extern __shared__ __align__(16) uint8_t sm_raw[];
   SampShared& s = *reinterpret_cast<SampShared*>(sm_raw);
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto started = cl.barrier_arrive();  // shared memory of another CTA: only once that CTA runs
-  for (int i = tid; i < 2 * kSampB; i += kSampNT) (&s.h[0][0])[i] = 0;
-  if (tid == 0) s.n_local = s.n_list = s.total = 0;
+  auto clear = [&]() {
+    uint4* h = reinterpret_cast<uint4*>(s.lo);
+    for (int i = tid; i < 2 * kSampTable / 4; i += kSampNT) h[i] = make_uint4(0u, 0u, 0u, 0u);
+  };
+  clear();
   pdl_wait();
   pdl_trigger();
-  // ---- the row, its largest logit
-  const int first = rank * p.slice, n = min(p.V - first, p.slice);
+  const int first = rank * p.slice, n = max(min(p.V - first, p.slice), 0);
   const float* src = p.logits + (int64_t)row * p.stride + first;
-  float x[KPT];
+  float cur[kSampU];
+  auto load = [&](float (&x)[kSampU], int i0) {
+    if (i0 + kSampU * kSampNT <= n) {
 #pragma unroll
-  for (int e = 0; e < KPT; ++e) x[e] = e * kSampNT + tid < n ? __ldcs(src + e * kSampNT + tid) : -INFINITY;
+      for (int e = 0; e < kSampU; ++e) x[e] = __ldg(src + i0 + e * kSampNT + tid);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kSampU; ++e) x[e] = i0 + e * kSampNT + tid < n ? __ldg(src + i0 + e * kSampNT + tid) : -INFINITY;
+    }
+  };
+  load(cur, 0);
   if (tid == kSampNT - 1) {
     const float T = p.temperature ? p.temperature[row] : 1.f, P = p.top_p ? p.top_p[row] : 1.f;
     const float mp = p.min_p ? p.min_p[row] : 0.f, u = p.u[row];
@@ -178,302 +261,387 @@ __global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel
     s.u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
     s.top_k = p.top_k ? max(p.top_k[row], 0) : 0;
     s.p_fix = P < 1.f ? max(__float2ull_rn(fmaxf(P, 0.f) * 18446744073709551616.f), 1ull) : 0;
-    s.y_min = mp > 0.f ? -log2((double)fminf(mp, 1.f)) : 1e30;
+    s.y_min = mp > 0.f ? -log2((double)fminf(mp, 1.f)) : 64.0;
+    s.by_m = s.y_min < 63.0;
   }
-  float mx = -INFINITY;
-  int at = 0;
+  // over the CTA: largest, least, largest
+  auto reduce3 = [&](float3 v) {
 #pragma unroll
-  for (int e = 0; e < KPT; ++e) {
-    x[e] = x[e] != x[e] ? -INFINITY : fminf(x[e], 3.402823466e38f);
-    if (x[e] > mx) mx = x[e], at = e;
-  }
-  u64 best = mx == -INFINITY ? 0 : ((u64)sample_key(mx) << 32) | (uint32_t)~(first + at * kSampNT + tid);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = max(best, (u64)__shfl_xor_sync(0xffffffffu, best, o));
-  if (lane == 0) s.warp64[warp] = best;
-  __syncthreads();
-  best = s.warp64[lane & 15];
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) best = max(best, (u64)__shfl_xor_sync(0xffffffffu, best, o));
-  const float ch = s.ch, cl_ = s.cl;
-  const bool hot = ch < 0.72f && !s.greedy;  // T above 2: the row may need finer buckets
-  float least = INFINITY;
-  if (hot) {
-    const float from = best ? key_float((uint32_t)(best >> 32)) - 64.f / ch : -INFINITY;
-#pragma unroll
-    for (int e = 0; e < KPT; ++e)
-      if (x[e] >= from && x[e] != -INFINITY) least = fminf(least, x[e]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-    if (lane == 0) s.fwarp[warp] = least;
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+      v.y = fminf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+      v.z = fmaxf(v.z, __shfl_xor_sync(0xffffffffu, v.z, o));
+    }
+    __syncthreads();  // (the last reduction has been read; the options are there)
+    if (lane == 0) s.warpf[warp] = v;
     __syncthreads();
-    least = s.fwarp[lane & 15];
+    v = s.warpf[lane & 15];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-  }
-  cl.barrier_wait(std::move(started));
-  if (tid < C) {
-    cl.map_shared_rank(s.best, tid)[rank] = best;
-    cl.map_shared_rank(s.least, tid)[rank] = least;
-  }
-  cl.sync();
-  for (int k = 0; k < C; ++k) best = max(best, s.best[k]), least = fminf(least, s.least[k]);
-  if (best == 0 || s.greedy) {
+    for (int o = 8; o > 0; o >>= 1) {
+      v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+      v.y = fminf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+      v.z = fmaxf(v.z, __shfl_xor_sync(0xffffffffu, v.z, o));
+    }
+    return v;
+  };
+  float top = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < kSampU; ++e) top = fmaxf(top, cur[e]);
+  top = reduce3(make_float3(top, INFINITY, -INFINITY)).x;
+  const float ch = s.ch, cl_ = s.cl;
+  if (s.greedy) {
+    float mx = -INFINITY;
+    int at = 0;
+    for (int i = tid; i < n; i += kSampNT) {
+      const float l = src[i];
+      if (l > mx) mx = l, at = i;
+    }
+    u64 best = mx == -INFINITY ? 0 : ((u64)sample_key(fminf(mx, 3.402823466e38f)) << 32) | (uint32_t)~(first + at);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, (u64)__shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) s.warp64[warp] = best;
+    __syncthreads();
+    for (int w = 0; w < kSampNT / 32; ++w) best = max(best, s.warp64[w]);
+    cl.barrier_wait(std::move(started));
+    if (tid == 0) cl.map_shared_rank(s.best, 0)[rank] = best;
+    cl.sync();
     if (rank == 0 && tid == 0) {
+      for (int k = 0; k < C; ++k) best = max(best, s.best[k]);
       p.tokens[row] = best ? (int)~(uint32_t)best : -1;
       if (p.probs) p.probs[row] = best ? 1.f : 0.f;
     }
     return;
   }
-  const float m = key_float((uint32_t)(best >> 32));
-  int fine = 0;
-  if (hot) {
-    const float span = fminf(64.f, __fmul_rn(__fsub_rn(m, least), ch));
-    while (fine < 15 && span * (float)(64 << fine) < (float)(kSampB - 2)) ++fine;
-  }
-  const float S = (float)(32 << fine);
   // ---- the histogram
-#pragma unroll
-  for (int e = 0; e < KPT; ++e) {
-    Term t;
-    if (term_of(x[e], m, ch, cl_, S, t)) {
-      const uint32_t D = below(t.q, fine), old = atomicAdd(&s.h[0][t.b], D);
-      atomicAdd(&s.h[1][t.b], old + D < old ? 65537u : 1u);
-    }
-  }
-  cl.sync();
-  {
-    const int share = kSampB / C;
-    for (int i = tid; i < share; i += kSampNT) {
-      const int b = rank * share + i;
-      u64 D = 0;
-      uint32_t c = 0;
-#pragma unroll 4
-      for (int k = 0; k < C; ++k) {
-        const uint32_t(*h)[kSampB] = cl.map_shared_rank(&s.h[0], k);
-        const uint32_t lo = h[0][b], hi = h[1][b];
-        D += ((u64)(hi >> 16) << 32) + lo;
-        c += hi & 0xFFFFu;
-      }
-      const u64 w = c ? weight_of(((u64)c << 37) - D, b, fine) : 0;
-      for (int k = 0; k < C; ++k) {
-        cl.map_shared_rank(s.mass, k)[b] = w;
-        cl.map_shared_rank(s.count, k)[b] = c;
-      }
-    }
-  }
-  cl.sync();
-  // ---- running sums over the buckets; where the borders can be
-  {
-    u64 a[kSampPer], sum = 0;
-    uint32_t c[kSampPer], cnt = 0;
-#pragma unroll
-    for (int i = 0; i < kSampPer; ++i) {
-      a[i] = sum += s.mass[kSampPer * tid + i];
-      c[i] = cnt += s.count[kSampPer * tid + i];
-    }
-    u64 up = sum;
-    uint32_t nup = cnt;
-    scan2(up, nup, s);
-#pragma unroll
-    for (int i = 0; i < kSampPer; ++i) {
-      s.mass[kSampPer * tid + i] = up - sum + a[i];
-      s.count[kSampPer * tid + i] = nup - cnt + c[i];
-    }
-  }
-  __syncthreads();
-  const u64 all = s.mass[kSampB - 1];
-  const uint32_t n_all = s.count[kSampB - 1];
+  // High temperatures: buckets as fine as lets the window take 40 above and below the
+  // first logits' largest (the second time, the row's own range).
+  int fine = 0;
+  while (fine < 15 && 40.f * ch * (float)(64 << fine) < (float)kSampB) ++fine;
+  float m = top;  // the row's largest, at last
+  float S, chS, clS, lo_y, hi_y;
+  Term tm;        // its place
+  bool window, crowd = false;
+  const bool by_p = s.p_fix != 0, by_m = s.by_m;
+  bool by_k;
+  const u64 u_fix = __float2ull_rn(s.u * 18446744073709551616.f);
+  uint32_t n_all;
+  u64 all;
   auto mass_to = [&](int b) { return b < 0 ? 0ull : s.mass[min(b, kSampB - 1)]; };
   auto count_to = [&](int b) { return b < 0 ? 0u : s.count[min(b, kSampB - 1)]; };
-  // the first buckets at which two rising conditions hold (kSampB: none)
-  auto find = [&](auto f, auto g, int& bf, int& bg) {
-    if (tid == 0) s.found[0] = s.found[1] = kSampB;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kSampPer; ++i) {
-      const int b = kSampPer * tid + i;
-      if (f(b) && (b == 0 || !f(b - 1))) s.found[0] = b;
-      if (g(b) && (b == 0 || !g(b - 1))) s.found[1] = b;
-    }
-    __syncthreads();
-    bf = s.found[0], bg = s.found[1];
-    __syncthreads();
-  };
-  const bool by_k = s.top_k > 0 && (uint32_t)s.top_k < n_all, by_p = s.p_fix != 0;
-  const double y_min = s.y_min * (double)S;
-  const bool by_m = y_min < (double)kSampB;
-  const int bm = by_m ? (int)y_min : kSampB;
-  const uint32_t qm = by_m ? (uint32_t)fmin((y_min - (double)bm) * 4294967296.0, 4294967295.0) : 0;
-  int bk = -1, pl = -1, ph = -2, bl, bh;
-  u64 k_lo = all, k_hi = all;
-  if (by_k) {
-    const uint32_t k = s.top_k;
-    int unused;
-    find([&](int b) { return s.count[b] >= k; }, [&](int) { return false; }, bk, unused);
-    k_lo = mass_to(bk - 1), k_hi = mass_to(bk);
-  }
-  u64 lo = k_lo, hi = k_hi;  // of the kept mass
-  if (by_p) {
-    const u64 tl = __umul64hi(k_lo, s.p_fix), th = __umul64hi(k_hi, s.p_fix) + 2;
-    find([&](int b) { return s.mass[b] >= tl; }, [&](int b) { return s.mass[b] >= th; }, pl, ph);
-    ph = min(ph, by_k ? bk : kSampB - 1);
-    pl = min(pl, ph);
-    lo = min(lo, mass_to(pl - 1)), hi = min(hi, mass_to(ph));
-  }
-  if (by_m) lo = min(lo, mass_to(bm - 1)), hi = min(hi, mass_to(bm));
-  const u64 u_fix = __float2ull_rn(s.u * 18446744073709551616.f);
-  {
-    const u64 tl = __umul64hi(lo, u_fix), th = __umul64hi(hi, u_fix) + 2;
-    find([&](int b) { return s.mass[b] > tl; }, [&](int b) { return s.mass[b] > th; }, bl, bh);
-    bl = min(bl, kSampB - 1), bh = min(bh, kSampB - 1);
-  }
-  {
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < kSampPer; ++i) {
-      const int b = kSampPer * tid + i;
-      auto in = [&](int d) {  // bucket b within d of one that is gathered
-        return abs(b - bk) <= d || (pl >= 0 && b >= pl - d && b <= ph + d) || (by_m && abs(b - bm) <= d) || (b >= bl - d && b <= bh + d);
-      };
-      s.flag[b] = (in(0) ? 1 : 0) | (in(1) ? 2 : 0);
-      if (in(0)) mine += count_to(b) - count_to(b - 1);
-    }
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0 && mine) atomicAdd(&s.total, mine);
-  }
-  __syncthreads();
-  if (s.total <= (uint32_t)kSampleList) {
-    // ---- their tokens to the first CTA
-    float mo = m;
-    asm volatile("" : "+f"(mo));  // (the terms anew: kept from the histogram they would not fit the registers)
-#pragma unroll
-    for (int e = 0; e < KPT; ++e) {
-      const float y = (mo - x[e]) * ch * S;
-      if (y < (float)kSampB + 1.f && (s.flag[min((int)y, kSampB - 1)] & 2)) {
-        Term t;
-        if (term_of(x[e], mo, ch, cl_, S, t) && (s.flag[t.b] & 1))
-          s.local[atomicAdd(&s.n_local, 1u)] = ((u64)sample_key(x[e]) << 32) | (uint32_t)~(first + e * kSampNT + tid);
-      }
-    }
-    __syncthreads();
-    if (tid == 0 && s.n_local) s.base = atomicAdd(cl.map_shared_rank(&s.n_list, 0), s.n_local);
-    __syncthreads();
-    u64* list0 = cl.map_shared_rank(s.list, 0);
-    for (uint32_t i = tid; i < s.n_local; i += kSampNT) list0[s.base + i] = s.local[i];
-    cl.sync();
-    if (rank != 0) return;
-    const int N = s.n_list;
-    int n2 = 2;
-    while (n2 < N) n2 *= 2;
-    for (int i = N + tid; i < n2; i += kSampNT) s.list[i] = 0;
-    __syncthreads();
+  int bk = -4, bm, bl, bh, pl, ph = -4;
+  uint32_t qm;
 #pragma unroll 1
-    for (int k = 2; k <= n2; k *= 2)  // bitonic, descending
+  for (int turn = 0;; ++turn) {
+    S = (float)(32 << fine), chS = ch * S, clS = cl_ * S;
+    // buckets [from, from + kSampTable): half of them above the reference
+    // buckets [from, from + kSampTable): half of them above the reference
+    window = fabsf(m * chS) < 2090000.f;  // (else, and for no reference: nothing is in it)
+    const float ref = floorf(-m * chS), from = ref - (turn ? 2.f : (float)kSampB);
+    lo_y = window ? from + 1.f : INFINITY, hi_y = window ? from + (float)(kSampTable - 1) : -INFINITY;
+    const float small = ref + 4.f * S;  // 2^-4 of the reference and less
+    const float kap = 0.693147181f / S, k1 = kap * 17179869184.f, k2 = -0.5f * kap * k1, k3 = kap * kap / 6.f * k1, k4 = kap * kap * kap / -24.f * k1;
+    float3 r = make_float3(-INFINITY, INFINITY, -INFINITY);  // the largest, the least in the window, the largest outside
+    auto put = [&](int b, uint32_t D) {
+      b &= kSampTable - 1;
+      const uint32_t old = atomicAdd(&s.lo[b], D);
+      atomicAdd(&s.hi[b], old + D < old ? 262145u : 1u);
+    };
 #pragma unroll 1
-      for (int j = k / 2; j > 0; j /= 2) {
-        for (int i = tid; i < n2 / 2; i += kSampNT) {
-          const int a = 2 * i - (i & (j - 1)), b = a + j;
-          const u64 va = s.list[a], vb = s.list[b];
-          if ((va < vb) == ((a & k) == 0)) s.list[a] = vb, s.list[b] = va;
+    for (int i0 = 0; i0 < n; i0 += kSampU * kSampNT) {
+      float next[kSampU];
+      load(next, i0 + kSampU * kSampNT);
+#pragma unroll
+      for (int e = 0; e < kSampU; e += 2) {
+        const float l[2] = {cur[e], cur[e + 1]};
+        float y[2], z[2], nr[2], fl[2], D[2];
+        mul2(y[0], y[1], l[0], l[1], -chS);
+        z[0] = -y[0], z[1] = -y[1];
+        fma2(z[0], z[1], l[0], l[1], -chS, -chS);
+        fma2(z[0], z[1], l[0], l[1], -clS, -clS);       // what the product lost
+        add2(nr[0], nr[1], y[0], y[1], -0.5f, -0.5f);
+        add2(nr[0], nr[1], nr[0], nr[1], 12582912.f, 12582912.f);  // the floor, or one less where y is whole
+        sub2(fl[0], fl[1], nr[0], nr[1], 12582912.f, 12582912.f);
+        sub2(y[0], y[1], y[0], y[1], fl[0], fl[1]);
+        add2(z[0], z[1], z[0], z[1], y[0], y[1]);       // the place in the bucket
+        D[0] = k3, D[1] = k3;
+        fma2(D[0], D[1], z[0], z[1], k4, k4);
+        float q[2] = {k2, k2};
+        fma2(q[0], q[1], D[0], D[1], z[0], z[1]);
+        D[0] = k1, D[1] = k1;
+        fma2(D[0], D[1], q[0], q[1], z[0], z[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          r.x = fmaxf(r.x, l[i]);
+          if (!(fl[i] >= lo_y && fl[i] < hi_y)) {
+            r.z = fmaxf(r.z, l[i]);
+          } else {
+            if (fine) r.y = fminf(r.y, l[i]);
+            // (near the bucket's ends the remainder decides which)
+            if (fl[i] < small || z[i] < 1e-6f || z[i] > 0.999999f) {
+              const Term p = place_of(l[i], chS, clS);
+              put(p.b, below(p.q, fine));
+            } else {
+              put(__float_as_int(nr[i]) - 0x4B400000, __float2uint_rn(D[i] * z[i]));
+            }
+          }
         }
+      }
+#pragma unroll
+      for (int e = 0; e < kSampU; ++e) cur[e] = next[e];
+    }
+    r = reduce3(r);
+    if (turn == 0) cl.barrier_wait(std::move(started));
+    if (tid < C) cl.map_shared_rank(s.range, tid)[rank] = make_float4(r.x, r.y, r.z, window ? from : -1e9f);
+    cl.sync();
+    float least = INFINITY, out = -INFINITY;
+    m = -INFINITY;
+    for (int k = 0; k < C; ++k) {
+      const float4 o = s.range[k];
+      m = fmaxf(m, o.x), least = fminf(least, o.y), out = fmaxf(out, o.z);
+    }
+    if (m == -INFINITY) {
+      if (rank == 0 && tid == 0) {
+        p.tokens[row] = -1;
+        if (p.probs) p.probs[row] = 0.f;
+      }
+      return;
+    }
+    if (m == INFINITY) m = 3.402823466e38f;
+    // logits of weight (2^-63 and more) that the buckets below the largest miss
+    const bool missed = (m - out) * ch < 63.f || (fine > 0 && (m - least) * chS >= (float)(kSampB - 2));
+    crowd = !(fabsf(m * ch) < 32768.f) || (missed && turn == 1);
+    if (crowd) break;
+    if (!missed) {
+      // ---- the CTAs' buckets from the largest logit's on, added up
+      tm = place_of(m, chS, clS);
+      if (tid == 0)  // the place up to which min_p keeps, behind the largest logit's
+        s.key = tm.q + (by_m ? (u64)(s.y_min * (double)S * 4294967296.0) : 0ull);
+      if (tid == 0) s.total = s.n_local = s.n_list = 0;
+      const int share = kSampB / C;
+      for (int i = tid; i < share; i += kSampNT) {
+        const int j = rank * share + i, b = tm.b + j;
+        u64 D = 0;
+        uint32_t c = 0;
+#pragma unroll 8
+        for (int k = 0; k < C; ++k) {
+          const int at = b - (int)s.range[k].w;
+          if (at >= 0 && at < kSampTable) {
+            const SampShared& o = *cl.map_shared_rank(&s, k);
+            const uint32_t lo = o.lo[b & (kSampTable - 1)], hi = o.hi[b & (kSampTable - 1)];
+            D += ((u64)(hi >> 18) << 32) + lo;
+            c += hi & 0x3FFFFu;
+          }
+        }
+        const u64 w = c ? weight_of(((u64)c << 34) - D, j, fine) : 0;
+        for (int k = 0; k < C; ++k) {
+          cl.map_shared_rank(s.mass, k)[j] = w;
+          cl.map_shared_rank(s.count, k)[j] = c;
+        }
+      }
+      cl.sync();
+      // ---- running sums over the buckets; where the borders can be
+      {
+        u64 a[kSampPer], sum = 0;
+        uint32_t c[kSampPer], cnt = 0;
+#pragma unroll
+        for (int i = 0; i < kSampPer; ++i) {
+          a[i] = sum += s.mass[kSampPer * tid + i];
+          c[i] = cnt += s.count[kSampPer * tid + i];
+        }
+        u64 up = sum;
+        uint32_t nup = cnt;
+        scan2(up, nup, s);
+#pragma unroll
+        for (int i = 0; i < kSampPer; ++i) {
+          s.mass[kSampPer * tid + i] = up - sum + a[i];
+          s.count[kSampPer * tid + i] = nup - cnt + c[i];
+        }
+      }
+      __syncthreads();
+      all = s.mass[kSampB - 1];
+      n_all = s.count[kSampB - 1];
+      by_k = s.top_k > 0 && (uint32_t)s.top_k < n_all;
+      const u64 m_at = s.key;
+      bm = by_m ? (int)min(m_at >> 32, (u64)kSampB) : kSampB, qm = (uint32_t)m_at;
+      pl = -1;
+      u64 k_lo = all, k_hi = all;
+      if (by_k) {
+        const uint32_t k = s.top_k;
+        bk = first_at([&](int b) { return s.count[b] >= k; });
+        k_lo = mass_to(bk - 1), k_hi = mass_to(bk);
+      }
+      u64 lo = k_lo, hi = k_hi;  // of the kept mass
+      if (by_p) {
+        const u64 tl = __umul64hi(k_lo, s.p_fix), th = __umul64hi(k_hi, s.p_fix) + 2;
+        pl = first_at([&](int b) { return s.mass[b] >= tl; });
+        ph = min(first_at([&](int b) { return s.mass[b] >= th; }), by_k ? bk : kSampB - 1);
+        pl = min(pl, ph);
+        lo = min(lo, mass_to(pl - 1)), hi = min(hi, mass_to(ph));
+      }
+      if (by_m) lo = min(lo, mass_to(bm - 1)), hi = min(hi, mass_to(bm));
+      {
+        const u64 tl = __umul64hi(lo, u_fix), th = __umul64hi(hi, u_fix) + 2;
+        bl = min(first_at([&](int b) { return s.mass[b] > tl; }), kSampB - 1);
+        bh = min(first_at([&](int b) { return s.mass[b] > th; }), kSampB - 1);
+      }
+      {
+        uint32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < kSampPer; ++i) {
+          const int b = kSampPer * tid + i;
+          const bool in = b == bk || (by_p && b >= pl && b <= ph) || (by_m && b == bm) || (b >= bl && b <= bh);
+          s.flag[b] = in;
+          if (in) mine += count_to(b) - count_to(b - 1);
+        }
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if (lane == 0 && mine) atomicAdd(&s.total, mine);
         __syncthreads();
-      }
-    // masses and running sums of the list: a thread has the entries kListPer tid ..
-    constexpr int kListPer = kSampleList / kSampNT;
-    u64 w[kListPer], sum = 0;
-    Term t[kListPer];
-    uint32_t none = 0;
-#pragma unroll
-    for (int i = 0; i < kListPer; ++i) {
-      const int j = kListPer * tid + i;
-      w[i] = 0;
-      t[i].b = -1, t[i].q = 0;
-      if (j < N && term_of(key_float((uint32_t)(s.list[j] >> 32)), m, ch, cl_, S, t[i]))
-        w[i] = weight_of((1ull << 37) - below(t[i].q, fine), t[i].b, fine);
-      sum += w[i];
-    }
-    u64 up = sum;
-    scan2(up, none, s);
-    up -= sum;
-#pragma unroll
-    for (int i = 0; i < kListPer; ++i) {
-      s.local[kListPer * tid + i] = up += w[i];
-      const int j = kListPer * tid + i;
-      if (j < N) {
-        Term before;
-        before.b = -1;
-        if (j > 0) term_of(key_float((uint32_t)(s.list[j - 1] >> 32)), m, ch, cl_, S, before);
-        if (before.b != t[i].b) s.start[t[i].b] = j;
+        crowd = s.total > (uint32_t)kSampleList;
+        break;
       }
     }
-    if (tid < 3) s.res_rank[tid] = 0xFFFFFFFFu, s.res_mass[tid] = all;
-    if (tid == 0) s.key = 0;
+    // once more, from the exact range: the least logit of any weight
+    float3 low = make_float3(0.f, INFINITY, 0.f);
+    for (int i = tid; i < n; i += kSampNT) {
+      const float l = src[i];
+      if ((m - l) * ch < 63.f) low.y = fminf(low.y, l);
+    }
+    low = reduce3(low);
+    cl.sync();  // every CTA has read the ranges
+    if (tid < C) cl.map_shared_rank(s.range, tid)[rank] = make_float4(0.f, low.y, 0.f, 0.f);
+    cl.sync();
+    for (int k = 0; k < C; ++k) low.y = fminf(low.y, s.range[k].y);
+    const float wide = (m - low.y) * ch;
+    fine = 0;
+    while (fine < 15 && wide * (float)(64 << fine) < (float)(kSampB - 4) && fabsf(m * ch) * (float)(64 << fine) < 1048576.f)
+      ++fine;
+    clear();
+    cl.sync();
+    load(cur, 0);
+  }
+  if (!crowd) {
+    // ---- the second pass: their tokens to the first CTA
+    // (from the end on: what was read last is in L2 still, where the rows together are larger)
+    // the gathered buckets, a little wider (y is within 2^-8 of the exact place): the draw's, top_p's, and the others'
+    const float b0 = (float)tm.b, g0 = fmaxf(b0 + (float)bl - 0.01f, lo_y), g1 = fminf(b0 + (float)bh + 1.01f, hi_y);
+    const float g2 = fmaxf(b0 + (float)pl - 0.01f, lo_y), g3 = by_p ? fminf(b0 + (float)ph + 1.01f, hi_y) : -INFINITY;
+    const int other = by_k && by_m ? min(bk, bm) : by_k ? bk : bm, others = by_k && by_m ? max(bk, bm) : other;
+    const float g4 = fmaxf(b0 + (float)other - 0.01f, lo_y), g5 = by_k || by_m ? fminf(b0 + (float)others + 1.01f, hi_y) : -INFINITY;
+    constexpr int step = kSampU * kSampNT;
+    const int last = n > 0 ? (n - 1) / step * step : -1;
+    if (last >= 0) load(cur, last);
+#pragma unroll 1
+    for (int i0 = last; i0 >= 0; i0 -= step) {
+      float next[kSampU];
+      if (i0 > 0) load(next, i0 - step);
+#pragma unroll
+      for (int e = 0; e < kSampU; ++e) {
+        const float y = __fmul_rn(-cur[e], chS);
+        if ((y >= g0 && y < g1) || (y >= g2 && y < g3) || (y >= g4 && y < g5)) {
+          const int j = place_of(cur[e], chS, clS).b - tm.b;
+          if (j >= 0 && j < kSampB && s.flag[j])
+            s.local[atomicAdd(&s.n_local, 1u)] =
+                ((u64)sample_key(cur[e]) << 32) | (uint32_t)~(first + i0 + e * kSampNT + tid);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kSampU; ++e) cur[e] = next[e];
+    }
     __syncthreads();
-    u64 G[kListPer];       // mass up to and with the entry
-    uint32_t place[kListPer];  // its place in the row's order, from 1
-#pragma unroll
-    for (int i = 0; i < kListPer; ++i) {
-      const int j = kListPer * tid + i;
-      G[i] = 0, place[i] = 0;
-      if (j < N) {
-        const int f = s.start[t[i].b];
-        G[i] = mass_to(t[i].b - 1) + s.local[j] - (f ? s.local[f - 1] : 0ull);
-        place[i] = count_to(t[i].b - 1) + (uint32_t)(j - f) + 1;
-        if (by_k && place[i] == (uint32_t)s.top_k) s.res_rank[0] = place[i], s.res_mass[0] = G[i];
-      }
+    if (C > 1) {
+      if (tid == 0 && s.n_local) s.base = atomicAdd(cl.map_shared_rank(&s.n_list, 0), s.n_local);
+      __syncthreads();
+      u64* list0 = cl.map_shared_rank(s.list, 0);
+      for (uint32_t i = tid; i < s.n_local; i += kSampNT) list0[s.base + i] = s.local[i];
+      cl.sync();
+      if (rank != 0) return;
     }
+    const u64* in = C > 1 ? s.list : s.local;
+    const int N = C > 1 ? s.n_list : s.n_local;
+    int E = 1, n2 = 32;
+    while (E * kSampNT < N) E *= 2;
+    while (n2 < N) n2 *= 2;
+    u64 v[kListPer];
+#pragma unroll
+    for (int e = 0; e < kListPer; ++e) v[e] = e * kSampNT + tid < N ? in[e * kSampNT + tid] : 0;
+    __syncthreads();
+    if (E == 1) sort_list<1>(v, s.list, n2);
+    else if (E == 2) sort_list<2>(v, s.list, n2);
+    else sort_list<4>(v, s.list, n2);
+    // masses, running sums and first entries of the buckets
+    Term t[kListPer];
+    u64 G[kListPer], carry = 0;  // up to and with an entry: first of the list, then of the row
+#pragma unroll
+    for (int e = 0; e < kListPer; ++e) {
+      t[e].b = -1, t[e].q = 0, G[e] = 0;
+      if (e >= E) continue;
+      if (v[e]) {
+        t[e] = place_of(key_float((uint32_t)(v[e] >> 32)), chS, clS);
+        t[e].b -= tm.b;
+        G[e] = weight_of(t[e], fine);
+        s.bucket[e * kSampNT + tid] = (uint16_t)t[e].b;
+      }
+      uint32_t none = 0;
+      scan2(G[e], none, s);
+      if (tid == kSampNT - 1) s.res_mass[0] = G[e];
+      G[e] += carry;
+      s.local[e * kSampNT + tid] = G[e];
+      __syncthreads();
+      carry += s.res_mass[0];
+      if (v[e]) {
+        const int j = e * kSampNT + tid;
+        if (j == 0 || s.bucket[j - 1] != t[e].b) s.start[t[e].b] = j;
+      }
+      __syncthreads();
+    }
+    // the masses that top_k, top_p and min_p keep
+    if (tid == 0) {
+      s.res_mass[0] = s.res_mass[1] = all;
+      s.res_mass[2] = by_m ? mass_to(bm - 1) : all;  // or more, of min_p's own bucket
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kListPer; ++e)
+      if (e < E && v[e]) {
+        const int f = s.start[t[e].b], j = e * kSampNT + tid;
+        G[e] = mass_to(t[e].b - 1) + G[e] - (f ? s.local[f - 1] : 0ull);
+        if (by_k && count_to(t[e].b - 1) + (uint32_t)(j - f) + 1 == (uint32_t)s.top_k) s.res_mass[0] = G[e];
+        if (by_m && t[e].b == bm && t[e].q <= qm) atomicMax(&s.res_mass[2], G[e]);
+      }
     __syncthreads();
     if (by_p) {
       const u64 target = ceil_part(s.res_mass[0], s.p_fix);
 #pragma unroll
-      for (int i = 0; i < kListPer; ++i)
-        if (place[i] && G[i] >= target && t[i].b >= pl) atomicMin(&s.res_rank[1], place[i]);
-    }
-    if (by_m) {  // the last one that min_p keeps, in its bucket or before it
-      if (tid == 0) s.res_rank[2] = count_to(bm - 1), s.res_mass[2] = mass_to(bm - 1);
+      for (int e = 0; e < kListPer; ++e)
+        if (e < E && v[e] && G[e] >= target && t[e].b >= pl) atomicMin(&s.res_mass[1], G[e]);
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kListPer; ++i)
-        if (place[i] && t[i].b == bm && t[i].q <= qm) atomicMax(&s.res_rank[2], place[i]);
     }
+    const u64 mass = min(min(s.res_mass[0], s.res_mass[1]), s.res_mass[2]), target = __umul64hi(mass, u_fix);
+    if (tid == 0) s.found = kSampleList;
     __syncthreads();
-    if (by_p || by_m) {
 #pragma unroll
-      for (int i = 0; i < kListPer; ++i) {
-        if (by_p && place[i] && place[i] == s.res_rank[1]) s.res_mass[1] = G[i];
-        if (by_m && place[i] && t[i].b == bm && place[i] == s.res_rank[2]) s.res_mass[2] = G[i];
+    for (int e = 0; e < kListPer; ++e)
+      if (e < E && v[e] && G[e] > target && t[e].b >= bl) atomicMin(&s.found, e * kSampNT + tid);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kListPer; ++e)
+      if (v[e] && e * kSampNT + tid == (s.found < kSampleList ? s.found : 0)) {
+        p.tokens[row] = (int)~(uint32_t)v[e];
+        if (p.probs)
+          p.probs[row] = (float)((1ull << 34) - below(t[e].q, fine)) * exp2f(-(float)t[e].b / S) * 1024.f / (float)mass;
       }
-    }
-    __syncthreads();
-    uint32_t kept = n_all;
-    u64 mass = all;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (s.res_rank[i] < kept) kept = s.res_rank[i], mass = s.res_mass[i];
-    const u64 target = __umul64hi(mass, u_fix);
-#pragma unroll
-    for (int i = 0; i < kListPer; ++i)  // keys fall along the list: the first one over the target is the largest
-      if (place[i] && place[i] <= kept && G[i] > target && t[i].b >= bl) atomicMax(&s.key, s.list[kListPer * tid + i]);
-    __syncthreads();
-    if (tid == 0) {
-      const u64 k = s.key ? s.key : best;
-      Term t0;
-      term_of(key_float((uint32_t)(k >> 32)), m, ch, cl_, S, t0);
-      p.tokens[row] = (int)~(uint32_t)k;
-      if (p.probs)
-        p.probs[row] = (float)((1ull << 37) - below(t0.q, fine)) * exp2f(-(float)t0.b / S) * 128.f / (float)mass;
-    }
     return;
   }
   // ---- the long way: the borders of top_k (or all tokens), top_p and the draw in
-  // turn, each by three digits of the keys from the top, over all tokens (read
-  // again: registers held through here would cost the short way)
+  // turn, each by three digits of the keys from the top, over all tokens
   auto logit = [&](int i) {
     const float l = i < n ? src[i] : -INFINITY;
     return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
   };
+  if (tid == 0) s.key = by_m ? (u64)(s.y_min * 137438953472.0) : 0ull;  // of 32 buckets an octave, from the largest logit
   cl.sync();
+  by_k = s.top_k > 0;
+  if (by_m) bm = (int)min(s.key >> 32, (u64)kSampB), qm = (uint32_t)s.key;
   uint32_t kept = 0;
   u64 mass = 0;
   uint32_t key = 0, above = 0, equal = 0;  // a border's key, tokens above it and of it
@@ -487,8 +655,8 @@ __global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel
 #pragma unroll 1
       for (int i = tid; i < n; i += kSampNT) {
         Term t;
-        if (term_of(logit(i), m, ch, cl_, S, t) && (t.b < bm || (t.b == bm && t.q <= qm)))
-          a += weight_of((1ull << 37) - below(t.q, fine), t.b, fine), ++c;
+        if (term_of(logit(i), m, ch, cl_, t) && (t.b < bm || (t.b == bm && t.q <= qm)))
+          a += weight_of(t, 0), ++c;
       }
       scan2(a, c, s);
       if (tid == kSampNT - 1) s.list[0] = a, s.list[1] = c;
@@ -502,7 +670,7 @@ __global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel
       cl.sync();
     }
     // found is where the count (turn 0) or the mass (1) reaches the target, or the mass passes it (2)
-    const u64 target = turn == 0 ? (by_k ? (u64)s.top_k : (u64)n_all) : turn == 1 ? ceil_part(mass, s.p_fix) : __umul64hi(mass, u_fix);
+    const u64 target = turn == 0 ? (by_k ? (u64)s.top_k : ~0ull) : turn == 1 ? ceil_part(mass, s.p_fix) : __umul64hi(mass, u_fix);
     auto over = [&](u64 m_, uint32_t n_) { return turn == 0 ? n_ >= target : turn == 1 ? m_ >= target : m_ > target; };
     key = above = 0, mass_above = 0;
 #pragma unroll 1
@@ -510,15 +678,15 @@ __global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel
       const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bins = level == 2 ? 1024 : 2048;
       const uint32_t prefix_mask = level == 0 ? 0u : level == 1 ? 0xFFE00000u : 0xFFFFFC00u;
       for (int i = tid; i < 3 * kSampB; i += kSampNT) (&s.h[0][0])[i] = 0;
-      if (tid == 0) s.found[0] = -1;
+      if (tid == 0) s.found = -1;
       __syncthreads();
 #pragma unroll 1
       for (int i = tid; i < n; i += kSampNT) {
         Term t;
         const float l = logit(i);
         const uint32_t k = sample_key(l);
-        if ((k & prefix_mask) == key && term_of(l, m, ch, cl_, S, t)) {
-          const u64 w = weight_of((1ull << 37) - below(t.q, fine), t.b, fine);
+        if ((k & prefix_mask) == key && term_of(l, m, ch, cl_, t)) {
+          const u64 w = weight_of(t, 0);
           const uint32_t bin = (k >> shift) & (bins - 1), lo32 = (uint32_t)w, old = atomicAdd(&s.h[0][bin], lo32);
           atomicAdd(&s.h[1][bin], (uint32_t)(w >> 32) + (old + lo32 < old));
           atomicAdd(&s.h[2][bin], 1u);
@@ -543,14 +711,16 @@ __global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel
       u64 up = sum;
       uint32_t nup = cnt;
       scan2(up, nup, s);
+      if (tid == kSampNT - 1) s.total = nup;
+      __syncthreads();
       up -= sum, nup -= cnt;
-      // the first non-empty bin over the target; past everything (by rounding), the last non-empty one
+      // the first non-empty bin over the target; if there is none, the last non-empty one
 #pragma unroll
       for (int i = 0; i < kSampPer; ++i) {
         const bool was = over(mass_above + up, above + nup), is = over(mass_above + up + a[i], above + nup + c[i]);
-        const bool last = above + nup + c[i] == (level == 0 ? n_all : above + equal) && !is;
+        const bool last = nup + c[i] == s.total && !is;
         if (c[i] && !was && (is || last)) {
-          s.found[0] = bins - 1 - (kSampPer * tid + i);
+          s.found = bins - 1 - (kSampPer * tid + i);
           s.res_mass[0] = mass_above + up;
           s.res_rank[0] = above + nup;
           s.res_rank[1] = c[i];
@@ -558,15 +728,15 @@ __global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel
         up += a[i], nup += c[i];
       }
       __syncthreads();
-      key |= (uint32_t)max(s.found[0], 0) << shift;
+      key |= (uint32_t)max(s.found, 0) << shift;
       mass_above = s.res_mass[0], above = s.res_rank[0], equal = s.res_rank[1];
       cl.sync();  // every CTA has read the histograms (the last turn's stay) and the result
     }
     Term t;
     each = 0;
-    if (term_of(key_float(key), m, ch, cl_, S, t)) each = weight_of((1ull << 37) - below(t.q, fine), t.b, fine);
+    if (term_of(key_float(key), m, ch, cl_, t)) each = weight_of(t, 0);
     if (turn == 0) {
-      kept = (uint32_t)target;
+      kept = (uint32_t)min(target, (u64)(above + equal));
       mass = mass_above + (u64)(kept - above) * each;
     } else if (turn == 1) {
       const u64 more = target > mass_above ? target - mass_above : 0;
@@ -605,26 +775,18 @@ __global__ void __launch_bounds__(kSampNT, KPT <= 20 ? 2 : 1) sample_rows_kernel
   }
 }
 
-template <int KPT>
-cudaError_t launch_sample_t(SampleRowsParams& p, int C, cudaStream_t st) {
-  const auto kern = sample_rows_kernel<KPT>;
-  static SmemLimit limit;
-  const cudaError_t e = limit.raise(kern, (int)sizeof(SampShared), true);
-  return e == cudaSuccess ? launch_cluster(kern, dim3(p.R * C), kSampNT, C, sizeof(SampShared), st, p, p.pdl) : e;
-}
-
 }  // namespace
 
 cudaError_t launch_sample_rows(SampleRowsParams& p, int n_sm, cudaStream_t st) {
-  // CTAs of a row: so many that a thread holds 20 logits at most (two CTAs on an SM; V up to
-  // 163840 with 16), and for few rows as many as have 1024 logits each.
+  // CTAs of a row: as many as run at once, two on an SM (a CTA's fixed work, ten
+  // microseconds, is spent once for as many logits as can be), of 1024 logits or more; at
+  // most 180000 (the histogram's counts).
   int C = 1;
-  while (C < 16 && (p.V + C - 1) / C > 20 * kSampNT) C *= 2;
-  while (C < 16 && (int64_t)p.R * C < n_sm && p.V / (2 * C) >= 1024) C *= 2;
+  while (C < 16 && ((p.V + C - 1) / C > kSampMaxSlice || ((int64_t)2 * p.R * C <= 2 * n_sm && p.V / (2 * C) >= 1024))) C *= 2;
   p.slice = (p.V + C - 1) / C;
-  const int per = (p.slice + kSampNT - 1) / kSampNT;
-  return per <= 8 ? launch_sample_t<8>(p, C, st) : per <= 20 ? launch_sample_t<20>(p, C, st)
-         : per <= 64 ? launch_sample_t<64>(p, C, st) : cudaErrorInvalidValue;
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(sample_rows_kernel, (int)sizeof(SampShared), true);
+  return e == cudaSuccess ? launch_cluster(sample_rows_kernel, dim3(p.R * C), kSampNT, C, sizeof(SampShared), st, p, p.pdl) : e;
 }
 
 }  // namespace llmq
@@ -636,7 +798,7 @@ extern "C" int llm_sample_tokens(const llm_sample_args* a, void* cuda_stream) {
   Call c;
   if (!c.need(a != nullptr, LLM_ERR_INVALID_ARG, "the arguments are null") ||
       !c.need(a->n_rows >= 1 && a->vocab >= 1, LLM_ERR_INVALID_ARG, "n_rows or vocab is not positive") ||
-      !c.need(a->vocab <= 16 * 64 * kSampNT, LLM_ERR_UNSUPPORTED, "%svocab %lld is too large", "", a->vocab) ||
+      !c.need(a->vocab <= 1 << 19, LLM_ERR_UNSUPPORTED, "%svocab %lld is too large", "", a->vocab) ||
       !c.need((int64_t)a->n_rows * 16 <= 0x7FFFFFFF, LLM_ERR_UNSUPPORTED, "too many rows") ||
       !c.need(a->logits_stride >= 0, LLM_ERR_INVALID_ARG, "a stride is negative") || !c.device("logits", a->logits, 4) ||
       !c.device("uniforms", a->uniforms, 4) || !c.device("tokens", a->tokens, 4) ||

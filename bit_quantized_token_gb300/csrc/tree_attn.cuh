@@ -240,18 +240,6 @@ __device__ __forceinline__ void split_pack(float a, float b, uint32_t (&part)[NP
     if (k + 1 < NP) sub2(a, b, a, b, __uint_as_float(part[k] << 16), __uint_as_float(part[k] & 0xFFFF0000u));
   }
 }
-__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b) {
-  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
-      "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b));
-}
-__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
 // Bit j of lane i's word becomes bit i of lane j's: halves of ever smaller blocks change places.
 __device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
 #pragma unroll
