@@ -1,13 +1,22 @@
 // Attention of sequences that share prefixes: two launches, of which the second
 // overlaps the first (see serve.cuh, tree_attn.cuh).
 #include "op_call.cuh"
+#include "prefix_attn.cuh"
 #include "serve.cuh"
 
 namespace llmq {
 
+constexpr int kWideFrom = 128;
+
 cudaError_t launch_prefix_attn(const TreeAttnParams& first, const TreeAttnParams& second, int hd, bool f32, bool q8,
                                int n_sm, cudaStream_t st) {
-  const cudaError_t e = launch_tree_attn(first, hd, f32, q8, n_sm, st);
+  // Rows of a kv head that a group can have: from 128 on the wide kernel.
+  const int64_t rows = (int64_t)first.nodes * first.gq;
+  const bool wide = !f32 && !q8 && rows >= kWideFrom && first.B <= kWideGroups &&
+                    (rows / kWideRows + first.B) * first.Hkv * (first.cache.rows / 128 + 1) < (1ll << 31) &&
+                    rows * first.Hkv < (1ll << 30);
+  const cudaError_t e = !wide ? launch_tree_attn(first, hd, f32, q8, n_sm, st)
+                        : hd == 64 ? launch_wide<64>(first, n_sm, st) : launch_wide<128>(first, n_sm, st);
   return e == cudaSuccess ? launch_tree_attn(second, hd, f32, q8, n_sm, st) : e;
 }
 
@@ -18,10 +27,9 @@ using namespace llmq;
 
 namespace {
 
-// [rows][head_dim] results, then [rows] (reference, sum), of rows = sequences x nodes x heads
-int64_t part_bytes(int64_t n_seq, int64_t n_nodes, int64_t n_heads, int64_t head_dim) {
-  return n_seq * n_nodes * n_heads * (head_dim * 4 + 8);
-}
+// [parts][rows][head_dim] results, [parts][rows] (reference, sum), [rows] numbers of parts, of rows = sequences x
+// nodes x heads
+int64_t part_bytes(int64_t rows, int64_t head_dim) { return rows * (wide_parts(rows) * (head_dim * 4 + 8) + 4); }
 
 }  // namespace
 
@@ -33,7 +41,7 @@ int64_t llm_prefix_workspace(int32_t n_seq, int32_t n_nodes, int32_t n_heads, in
                   (head_dim == 64 || head_dim == 128),
               LLM_ERR_INVALID_ARG, "a size is out of range"))
     return c.rc;
-  return part_bytes(n_seq, n_nodes, n_heads, head_dim);
+  return part_bytes((int64_t)n_seq * n_nodes * n_heads, head_dim);
 }
 
 int llm_prefix_attention(const llm_prefix_attention_args* a, void* cuda_stream) {
@@ -48,12 +56,12 @@ int llm_prefix_attention(const llm_prefix_attention_args* a, void* cuda_stream) 
               "n_groups is not positive or over the prefix view's sequences") ||
       !c.need(f.dtype == v.dtype && f.head_dim == v.head_dim && f.n_heads == v.n_heads && f.n_layers == 1,
               LLM_ERR_INVALID_ARG, "the prefix's rows do not match the cache") ||
-      !c.need(v.n_heads * (nodes * gq / 16 + 1) <= 65535 && (nodes + 128) * gq * gq < (1ll << 32) &&
+      !c.need(v.n_heads * (nodes * gq / 16 + 1) <= 65535 && (nodes + 256) * gq * gq < (1ll << 32) &&
                   nodes * t.n_nodes < (1ll << 32),
               LLM_ERR_UNSUPPORTED, "too many sequences and heads") ||
       !view_memory(c, a->prefix, "prefix") || !c.device("starts", a->starts, 4) ||
-      !c.device("prefix_lens", a->prefix_lens, 4) || !c.device("workspace", a->workspace, 16) ||
-      !c.need(a->workspace_bytes >= part_bytes(t.n_seq, t.n_nodes, t.n_heads, v.head_dim), LLM_ERR_INVALID_ARG,
+      !c.device("prefix_lens", a->prefix_lens, 4) || !c.device("workspace", a->workspace, 32) ||
+      !c.need(a->workspace_bytes >= part_bytes(nodes * t.n_heads, v.head_dim), LLM_ERR_INVALID_ARG,
               "the workspace is smaller than llm_prefix_workspace says"))
     return c.rc;
   const bool f32 = t.dtype == LLM_F32, q8 = v.dtype == LLM_Q8G32;
@@ -63,8 +71,11 @@ int llm_prefix_attention(const llm_prefix_attention_args* a, void* cuda_stream) 
   p.G = a->n_groups;
   p.all = t.n_seq;
   p.by_n = FastDiv(t.n_nodes);
+  p.part_rows = nodes * t.n_heads;
+  p.max_parts = wide_parts(p.part_rows);
   p.part_o = static_cast<float*>(a->workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + nodes * t.n_heads * v.head_dim);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + p.max_parts * p.part_rows * v.head_dim);
+  p.part_n = reinterpret_cast<int*>(p.part_ml + p.max_parts * p.part_rows);
   TreeAttnParams first = p;
   p.part = TreeAttnParams::kSecond;
   first.part = TreeAttnParams::kFirst;

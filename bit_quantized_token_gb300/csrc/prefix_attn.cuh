@@ -1,0 +1,485 @@
+// Attention of many query rows over bf16 K/V rows that they all see: the first part
+// of prefix_attention where a group has more rows than the tree attention's
+// kernels take at once (see TreeAttnParams::Part).
+//
+// Rows (a group's sequences x nodes x query heads of a kv head) are the long side here,
+// so the products run untransposed, a tile of 128 rows against 128 keys:
+//   S [128 rows x 128 keys] = Q K_tile^T        (both K-major, from shared memory)
+//   O [128 rows x dims]    += P V_tile          (P from tensor memory, V as TMA lays it down)
+// A CTA takes two tiles of rows over the same keys: while one tile's four warps turn
+// scores into probabilities, the tensor cores work for the other. A thread is a row:
+// its scores, reference and sum are its own. The reference is the first tile's maximum
+// and is renewed only when a tile's probabilities pass 2^60 (bf16 and fp32 keep their
+// precision over that range), so O is hardly ever touched between products.
+// P lies in columns of its own at 64 dims; at 128 dims, where O takes half of tensor
+// memory, over the scores it came from, and the next scores wait for P V.
+// P is rounded to bf16 (8 bits): the outputs' error is 1.41 times what rounding them
+// to bf16 gives. Two parts of it would make half as many matrix operations more.
+//
+// Work: the (group, kv head, 256 rows, key tile) units in one row are cut into equal
+// ranges, one for each CTA, so that every SM has the same number whatever the sizes of the
+// groups; the pieces of a row tile (max_parts at most) are joined by the second part.
+#pragma once
+#include "tree_attn_q8.cuh"
+
+namespace llmq {
+
+constexpr int kWideRows = 256;       // query rows of a CTA
+constexpr int kWideGroups = 1024;    // most groups
+// Pieces that a row tile may be cut into, of all n heads rows: few rows need them to fill the SMs.
+inline int wide_parts(int64_t rows) { return rows <= 10240 ? 8 : rows <= 40960 ? 4 : 1; }
+
+template <int HD>
+struct Wide {
+  static constexpr int H = HD / 64, BK = 128, NT = 320;
+  static constexpr int kTile = 128 * HD * 2, kUnit = 128 * 128;  // bytes of 128 rows of Q, K or V; of 64 dims of them
+  static constexpr int NST = HD == 64 ? 8 : 4;                   // K and V tiles in flight
+  static constexpr int kSmall = 512 + 4 * (kWideGroups + 1);
+  static constexpr int kSmem = 2 * kTile + NST * kTile + kSmall + 1024;
+  // more than half of an SM's: no CTA that holds tensor memory shares the SM (this one takes all of it)
+  static_assert(kSmem > 140000 && kSmem <= 232448, "shared memory");
+  static constexpr bool own_p = HD == 64;
+  __host__ __device__ static constexpr int at_p(int t) { return own_p ? 256 + 64 * t : 128 * t; }
+  __host__ __device__ static constexpr int at_o(int t) { return own_p ? 384 + 64 * t : 256 + 128 * t; }
+};
+
+struct WideParams {
+  CUtensorMap k, v;
+  TreeAttnParams p;
+  int head, seq;        // 0 where a stride is 0, else 1
+  bool whole;           // max_parts too few for cuts: ranges of row tiles
+};
+
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+      "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
+      "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32f(uint32_t addr, const float (&v)[32]) {
+  uint32_t u[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]);
+  tc_st32(addr, u);
+}
+__device__ __forceinline__ void st_global8(float* at, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
+               "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// What a CTA has to do, one stretch of keys of a row tile after the other.
+struct WideSegment {
+  int g, hkv, row0, rows, k0, k1, len;  // group; rows row0 .. of the group; key tiles k0 .. k1 - 1 of the prefix's len rows
+  int first, piece, pieces;             // the group's first sequence; which piece of the row tile, of how many
+};
+struct WidePlan {
+  const TreeAttnParams& p;
+  const uint32_t* cum;  // [G + 1] units before a group
+  bool whole;
+  int64_t U, N, pos, end;
+  __device__ WidePlan(const TreeAttnParams& p_, const uint32_t* cum_, bool whole_, int kt_max) : p(p_), cum(cum_), whole(whole_) {
+    U = cum[p.B];
+    N = min((int64_t)gridDim.x, U);
+    if (!whole && U > 0) N = max(min(N, U * (p.max_parts - 2) / kt_max), (int64_t)1);  // no row tile in more pieces
+    pos = (int)blockIdx.x < N ? U * blockIdx.x / N : 0;
+    end = (int)blockIdx.x < N ? U * (blockIdx.x + 1) / N : 0;
+  }
+  __device__ static int tiles(const TreeAttnParams& p, int g, int& first, int& rows, int& len) {
+    first = min(max(p.starts[g], 0), p.all);
+    rows = (min(max(p.starts[g + 1], first), p.all) - first) * p.n * p.gq;
+    len = min(max(p.lens[g], 0), p.cache.rows);
+    return (len + 127) / 128;
+  }
+  __device__ int cta_of(int64_t u) const { return (int)(((u + 1) * N - 1) / U); }
+  __device__ bool next(WideSegment& s) {
+    if (pos >= end) return false;
+    int lo = 0, hi = p.B - 1;  // the last group that starts at or before pos and is not empty
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (cum[mid] <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    s.g = lo;
+    int rows;
+    const int kt = tiles(p, lo, s.first, rows, s.len), rt = (rows + kWideRows - 1) / kWideRows, per = whole ? 1 : kt;
+    const int off = (int)(pos - cum[lo]), q = off / per;
+    s.hkv = q / rt;
+    s.row0 = (q - s.hkv * rt) * kWideRows;
+    s.rows = min(rows - s.row0, kWideRows);
+    const int64_t start = (int64_t)cum[lo] + (int64_t)q * per;
+    s.k0 = whole ? 0 : off - q * kt;
+    s.k1 = whole ? kt : (int)min((int64_t)kt, s.k0 + end - pos);
+    s.piece = whole ? 0 : (int)blockIdx.x - cta_of(start);
+    s.pieces = whole ? 1 : cta_of(start + kt - 1) - cta_of(start) + 1;
+    pos += whole ? 1 : s.k1 - s.k0;
+    return true;
+  }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid_constant__ WideParams wp) {
+  using C = Wide<HD>;
+  constexpr int H = C::H, NST = C::NST, BK = C::BK;
+  extern __shared__ uint8_t sm_raw[];
+  const TreeAttnParams& p = wp.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+  uint8_t* sq = sm;                       // [2][H][128 rows][128 B]
+  uint8_t* sring = sq + 2 * C::kTile;     // [NST][H][128 keys][128 B]
+  uint8_t* small = sring + NST * C::kTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(small);
+  uint64_t *full = bars, *empty = bars + 8, *q_full = bars + 16, *s_full = bars + 18, *p_full = bars + 20, *o_done = bars + 22,
+           *drain = bars + 24;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);  // (11 ints: see tc_wait_long)
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 320);
+  int* s_kt = reinterpret_cast<int*>(small + 324);   // most key tiles of a group
+  int* s_none = reinterpret_cast<int*>(small + 328);  // a group without prefix rows
+  uint32_t* cum = reinterpret_cast<uint32_t*>(small + 512);
+  if (tid == 0) {
+    s_abort[0] = 0, s_abort[kLimitAt] = p.wait.ns;
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+    for (int i = 0; i < 2; ++i)
+      mbar_init(q_full + i, 128), mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 + p.wait.missing), mbar_init(o_done + i, 1);
+    mbar_init(drain, 1);
+    mbar_fence_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else if (warp == 9) {  // units before each group
+    uint32_t before = 0;
+    int most = 1;
+    bool none = false;
+    for (int g0 = 0; g0 < p.B; g0 += 32) {
+      int first, rows = 0, len, kt = 0;
+      if (g0 + lane < p.B) kt = WidePlan::tiles(p, g0 + lane, first, rows, len);
+      const int rt = (rows + kWideRows - 1) / kWideRows;
+      uint32_t u = kt > 0 ? (uint32_t)rt * (wp.whole ? 1 : kt) * p.Hkv : 0u, x = u;
+      if (u) most = max(most, kt);
+      none |= rows > 0 && kt == 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (g0 + lane < p.B) cum[g0 + lane] = before + x - u;
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    none = __any_sync(0xffffffffu, none);
+    if (lane == 0) cum[p.B] = before, *s_kt = most, *s_none = none;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  if (*s_none)
+    for (int g = 0; g < p.B; ++g) {
+      int first, rows, len;
+      if (WidePlan::tiles(p, g, first, rows, len) == 0)
+        for (int i = blockIdx.x * C::NT + tid; i < rows * p.Hkv; i += gridDim.x * C::NT)
+          p.part_n[(int64_t)first * p.n * p.Hkv * p.gq + i] = 0;
+    }
+  WidePlan plan(p, cum, wp.whole, *s_kt);
+  WideSegment seg;
+  uint32_t base = 0;  // K and V tiles of the segments before
+  // The ring's order in a segment of n tiles: K0 K1 V0 K2 V1 ..
+  auto k_at = [&](int t) { return base + (t == 0 ? 0 : 2 * t - 1); };
+  auto v_at = [&](int t, int n) { return base + (t == n - 1 ? 2 * t + 1 : 2 * t + 2); };
+  uint32_t sent = 0;
+  if (warp == 9) {
+    if (lane == 0) {
+      bool ok = true;
+      while (ok && plan.next(seg)) {
+        const int n = seg.k1 - seg.k0;
+#pragma unroll 1
+        for (int j = 0; j < 2 * n && ok; ++j) {
+          const bool val = j > 0 && (!(j & 1) || j == 2 * n - 1);
+          const int t = seg.k0 + (j == 2 * n - 1 ? n - 1 : val ? j / 2 - 1 : (j + 1) / 2);
+          const uint32_t i = base + j, slot = i % NST;
+          if (i >= (uint32_t)NST) ok = tc_wait(empty + slot, (i / NST - 1) & 1, s_abort, p.status);
+          if (!ok) break;
+          mbar_expect_tx(full + slot, C::kTile);
+#pragma unroll
+          for (int u = 0; u < H; ++u)
+            tma_box(sring + slot * C::kTile + u * C::kUnit, val ? &wp.v : &wp.k, 64 * u, t * BK, seg.hkv * wp.head, seg.g * wp.seq,
+                    full + slot);
+          sent = i + 1;
+        }
+        base += 2 * n;
+      }
+    }
+  } else if (warp == 8) {
+    // ---- MMA
+    constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 x bf16, 128 rows
+    constexpr uint32_t idesc_s = base_i | ((uint32_t)(BK >> 3) << 17);
+    constexpr uint32_t idesc_o = base_i | ((uint32_t)(HD >> 3) << 17) | (1u << 16);  // V is MN-major
+    const uint32_t uq = smem_u32(sq), ur = smem_u32(sring);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    bool ok = true;
+    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // segments, tiles of either tile of rows so far
+    while (ok && plan.next(seg)) {
+      const int n = seg.k1 - seg.k0, nt = seg.rows > 128 ? 2 : 1;
+      auto scores = [&](int t, uint32_t slot) {
+        const uint64_t da = tc_desc(uq + t * C::kTile, 16, 1024, 2), db = tc_desc(ur + slot * C::kTile, 16, 1024, 2);
+        if (elect_lane()) {
+#pragma unroll
+          for (int u = 0; u < H; ++u)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
+              tc_mma(tm + 128 * t, da + (u * C::kUnit >> 4) + 2 * ks, db + (u * C::kUnit >> 4) + 2 * ks, idesc_s, u > 0 || ks > 0);
+        }
+        __syncwarp();
+        tc_commit(s_full + t);
+      };
+      {
+        const uint32_t i = k_at(0), slot = i % NST;
+        ok = tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
+        for (int t = 0; t < nt && ok; ++t) {
+          ok = tc_wait_warp(q_full + t, nq[t] & 1, s_abort, p.status);
+          if (!ok) break;
+          ++nq[t];
+          tc_fence_after();
+          scores(t, slot);
+        }
+        if (ok) tc_commit(empty + slot);
+      }
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const bool more = i + 1 < n;
+        const uint32_t ik = k_at(i + 1), iv = v_at(i, n), sk = ik % NST, sv = iv % NST;
+        if (more) ok = tc_wait_warp(full + sk, (ik / NST) & 1, s_abort, p.status);
+        for (int t = 0; t < nt && ok; ++t) {
+          ok = tc_wait_warp(p_full + t, np[t] & 1, s_abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (C::own_p && more) scores(t, sk);
+          if (t == 0) ok = tc_wait_warp(full + sv, (iv / NST) & 1, s_abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t db = tc_desc(ur + sv * C::kTile, C::kUnit, 1024, 2);
+          if (elect_lane()) {
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 8 columns of P, 2 KB of V further
+              tc_mma_ts(tm + C::at_o(t), tm + C::at_p(t) + 8 * ks, db + ks * (uint64_t)128, idesc_o, i > 0 || ks > 0);
+          }
+          __syncwarp();
+          tc_commit(o_done + t);
+          if (!C::own_p && more) {  // the scores come to lie where P is
+            ok = tc_wait_warp(o_done + t, np[t] & 1, s_abort, p.status);
+            if (!ok) break;
+            scores(t, sk);
+          }
+          ++np[t];
+        }
+        if (ok && more) tc_commit(empty + sk);
+        if (ok) tc_commit(empty + sv);
+      }
+      base += 2 * n;
+    }
+  } else {
+    // ---- softmax: thread = row of tile t
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t tS = tmem + lanes + 128 * t, tP = tmem + lanes + C::at_p(t), tO = tmem + lanes + C::at_o(t);
+    uint32_t ns = 0;  // tiles so far
+    bool ok = true;
+    while (ok && plan.next(seg)) {
+      const int n = seg.k1 - seg.k0;
+      if (t * 128 >= seg.rows) {
+        base += 2 * n;
+        continue;
+      }
+      const int row = seg.row0 + t * 128 + r, node = p.by_gq.div(row), h = seg.hkv * p.gq + row - node * p.gq;
+      const bool there = t * 128 + r < seg.rows;
+      {  // Q: 128-byte rows of 64 dims, chunks permuted as by TMA's 128-byte swizzle
+        const int s = p.by_n.div(node);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (int64_t)(seg.first + s) * p.q_seq +
+                                                          (int64_t)(node - s * p.n) * p.q_node + (int64_t)h * p.q_head);
+        const uint32_t turn = p.neg ? 0x80008000u : 0u;
+        uint8_t* dst = sq + t * C::kTile + r * 128;
+#pragma unroll
+        for (int ch = 0; ch < HD / 8; ++ch) {
+          uint4 w = there ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
+          w.x ^= turn, w.y ^= turn, w.z ^= turn, w.w ^= turn;
+          *reinterpret_cast<uint4*>(dst + (ch / 8) * C::kUnit + 16 * ((ch & 7) ^ (r & 7))) = w;
+        }
+        fence_async_smem();
+        mbar_arrive(q_full + t);
+      }
+      float ref = -kNone, l = 0.f;  // the reference, negated; the sum of the probabilities
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int left = seg.len - (seg.k0 + i) * BK;  // keys from this tile on
+        ok = tc_wait_warp(s_full + t, ns & 1, s_abort, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        float a[32], b[32];
+        auto mask = [&](float (&v)[32], int c0) {
+          if (left < BK)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c0 + j >= left) v[j] = -INFINITY;
+        };
+        auto highest = [&]() {
+          float m = -INFINITY;
+#pragma unroll
+          for (int c0 = 0; c0 < BK; c0 += 32) {
+            tc_ld(a, tS + c0);
+            tc_wait_ld(a);
+            mask(a, c0);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m = fmaxf(m, a[j]);
+          }
+          return m;
+        };
+        if (i == 0) {
+          const float m = highest();
+          ref = fabsf(m) < 1e38f ? -m : -kNone;
+        }
+        uint32_t pk[BK / 2];
+        float sum;
+        for (;;) {
+          float s0 = 0.f, s1 = 0.f;
+          auto take = [&](float (&v)[32], int c0) {
+            mask(v, c0);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              add2(v[j], v[j + 1], v[j], v[j + 1], ref, ref);
+              mul2(v[j], v[j + 1], v[j], v[j + 1], p.c);
+              v[j] = ex2(v[j]), v[j + 1] = ex2(v[j + 1]);
+              add2(s0, s1, s0, s1, v[j], v[j + 1]);
+              pk[(c0 + j) / 2] = pack_bf16x2(v[j], v[j + 1]);
+            }
+          };
+          tc_ld(a, tS);
+          tc_wait_ld(a);
+          tc_ld(b, tS + 32);
+          take(a, 0);
+          tc_wait_ld(b);
+          tc_ld(a, tS + 64);
+          take(b, 32);
+          tc_wait_ld(a);
+          tc_ld(b, tS + 96);
+          take(a, 64);
+          tc_wait_ld(b);
+          take(b, 96);
+          sum = s0 + s1;
+          const bool over = sum > 1152921504606846976.f;  // 2^60
+          if (!__any_sync(0xffffffffu, over)) break;
+          // renew the references of the warp's rows; rescale O and the sums
+          const float m = highest(), old = -ref, now = fmaxf(m, old), f = !over || old == now ? 1.f : exp2f((old - now) * p.c);
+          if (over && now > old) ref = -now;
+          l *= f;
+          if (i > 0) {
+            ok = tc_wait_warp(o_done + t, (ns - 1) & 1, s_abort, p.status);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+              tc_ld(a, tO + c0);
+              tc_wait_ld(a);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) a[j] *= f;
+              tc_st32f(tO + c0, a);
+            }
+            tc_wait_st();
+          }
+          if (!ok) break;
+        }
+        if (!ok) break;
+        l += sum;
+        if (left < BK) {  // V rows that are not there become zeros: 0 times whatever lies there need not be 0
+          const uint32_t iv = v_at(i, n), slot = iv % NST;
+          ok = tc_wait_warp(full + slot, (iv / NST) & 1, s_abort, p.status);
+          if (!ok) break;
+#pragma unroll 1
+          for (int c = r; c < (BK - left) * (HD / 8); c += 128) {
+            const int row_v = left + c / (HD / 8), ch = c % (HD / 8);
+            *reinterpret_cast<uint4*>(sring + slot * C::kTile + (ch / 8) * C::kUnit + row_v * 128 + 16 * (ch & 7)) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+        }
+        if (C::own_p && i > 0) {  // the last P V has read P
+          ok = tc_wait_warp(o_done + t, (ns - 1) & 1, s_abort, p.status);
+          if (!ok) break;
+        }
+        tc_st32(tP, pk);
+        tc_st32(tP + 32, pk + 32);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full + t);
+        ++ns;
+      }
+      if (!ok) break;
+      ok = tc_wait_warp(o_done + t, (ns - 1) & 1, s_abort, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const int64_t at = ((int64_t)seg.first * p.n + node) * (p.Hkv * p.gq) + h;
+      const float f = l == 0.f ? 0.f : 1.f / l;
+      float* out = p.part_o + (seg.piece * p.part_rows + at) * HD;
+#pragma unroll
+      for (int c0 = 0; c0 < HD; c0 += 32) {
+        float a[32];
+        tc_ld(a, tO + c0);
+        tc_wait_ld(a);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) a[j] *= f;
+        if (there)
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) st_global8(out + c0 + j, a + j);
+      }
+      if (there) {
+        p.part_ml[seg.piece * p.part_rows + at] = make_float2(-ref, l);
+        if (seg.piece == 0) p.part_n[at] = seg.pieces;
+      }
+      tc_fence_before();
+      base += 2 * n;
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (*s_abort) {  // no copy and no product in flight outlives the CTA
+    const unsigned long long s0 = globaltimer();
+    if (warp == 9 && lane == 0)
+#pragma unroll 1
+      for (uint32_t j = sent > (uint32_t)NST ? sent - NST : 0; j < sent; ++j)
+        while (!mbar_try_wait(full + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
+        }
+    __syncwarp();
+    if (warp == 8) {
+      tc_commit(drain);
+      while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+    __syncthreads();
+  }
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+template <int HD>
+cudaError_t launch_wide(const TreeAttnParams& p, int n_sm, cudaStream_t st) {
+  WideParams wp;
+  wp.p = p;
+  wp.head = p.cache.head != 0, wp.seq = p.cache.seq != 0;
+  wp.whole = p.max_parts < 3;
+  if (!encode_rows<HD, false>(&wp.k, p.cache.k, p.cache, p.B, p.Hkv) || !encode_rows<HD, false>(&wp.v, p.cache.v, p.cache, p.B, p.Hkv))
+    return cudaErrorNotSupported;
+  const auto kern = wide_attn_kernel<HD>;
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(kern, Wide<HD>::kSmem);
+  return e == cudaSuccess ? launch_cluster(kern, dim3(n_sm), Wide<HD>::NT, 1, Wide<HD>::kSmem, st, wp, p.pdl) : e;
+}
+
+}  // namespace llmq

@@ -778,11 +778,17 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRow
 }  // namespace
 
 cudaError_t launch_sample_rows(SampleRowsParams& p, int n_sm, cudaStream_t st) {
-  // CTAs of a row: as many as run at once, two on an SM (a CTA's fixed work, ten
-  // microseconds, is spent once for as many logits as can be), of 1024 logits or more; at
-  // most 180000 (the histogram's counts).
+  // CTAs of a row: a CTA's fixed work (about 12 us) pays for as many logits as can be,
+  // so as many as have an SM each, with 1000 logits or more, or two on an SM for long slices;
+  // at most 180000 (the histogram's counts). Measured, us for 1, 2, 4, 8, 16: 1 x 32000 26 / 21 /
+  // 17 / 15 / 15, 32 x 32000 30 / 23 / 18 / 25 / 43, 64 x 151936 89 / 53 / 46 / 57 / 99, 256 x 151936
+  // 135 / 139 / 156 / 205 / 357.
+  const auto more = [&](int C) {
+    const int64_t ctas = (int64_t)2 * p.R * C;
+    return (p.V + C - 1) / C > kSampMaxSlice || (ctas <= n_sm && p.V / (2 * C) >= 1000) || (ctas <= 2 * n_sm && p.V / C >= 65536);
+  };
   int C = 1;
-  while (C < 16 && ((p.V + C - 1) / C > kSampMaxSlice || ((int64_t)2 * p.R * C <= 2 * n_sm && p.V / (2 * C) >= 1024))) C *= 2;
+  while (C < 16 && more(C)) C *= 2;
   p.slice = (p.V + C - 1) / C;
   static SmemLimit limit;
   const cudaError_t e = limit.raise(sample_rows_kernel, (int)sizeof(SampShared), true);

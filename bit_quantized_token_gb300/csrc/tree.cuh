@@ -140,14 +140,17 @@ struct TreeAttnParams {
   bool sorted;               // blocks take the sequences longest first
   // Attention in two parts over different rows. kFirst: "sequence" b of the cache is one that the sequences
   // starts[b] .. starts[b + 1] - 1 (of all) share, whose nodes follow one another as its rows; the results go to
-  // part_o, part_ml instead of out. kSecond: the results are joined with those of the first part, launched just
-  // before it, where the sequence is in starts[0] .. starts[B] - 1.
+  // part_o, part_ml instead of out, in part_n pieces. kSecond: the results are joined with those of the first part,
+  // launched just before it, where the sequence is in starts[0] .. starts[B] - 1.
   enum Part : int { kWhole, kFirst, kSecond } part = kWhole;
   const int* starts = nullptr;
   int G = 0, all = 0;        // groups, sequences
   int nodes;                 // most nodes of a block's sequence(s): n, or all n
-  float* part_o = nullptr;   // [all][n][heads][head_dim] normalised
-  float2* part_ml = nullptr; // [all][n][heads] (reference, sum)
+  int* part_n = nullptr;     // [all][n][heads] pieces of a row: 1 .. max_parts
+  int max_parts = 1;
+  int64_t part_rows = 0;     // all n heads
+  float* part_o = nullptr;   // [max_parts][all][n][heads][head_dim] normalised
+  float2* part_ml = nullptr; // [max_parts][all][n][heads] (reference, sum)
   FastDiv by_n;
   int* status;               // the device's status word (bounded waits)
   WaitLimit wait = wait_limit();

@@ -572,7 +572,7 @@ typedef struct {
   int32_t n_groups;             /* up to the prefix view's sequences */
   const int32_t* starts;        /* [n_groups + 1] ascending: sequences starts[g] .. starts[g + 1] - 1 are group g */
   const int32_t* prefix_lens;   /* [n_groups] rows of each prefix (clamped to 0..rows) */
-  void* workspace;              /* device memory, 16-byte aligned; calls that may overlap have one each */
+  void* workspace;              /* device memory, 32-byte aligned; calls that may overlap have one each */
   int64_t workspace_bytes;      /* at least llm_prefix_workspace's */
 } llm_prefix_attention_args;
 
@@ -581,8 +581,8 @@ typedef struct {
  * once for all sequences of the group. Sequences outside of starts[0] ..
  * starts[n_groups] - 1 see no prefix. What llm_tree_attention says of types,
  * precision, counts, masks and empty rows holds here too (bf16 queries over bf16
- * prefix rows: the probabilities carry 8 bits where more than 64 query rows of a kv
- * head share them). One decode token: n_nodes = 1, its row already in the cache and
+ * prefix rows: the probabilities carry 8 bits where the batch has more than 64 query
+ * rows, n_seq x n_nodes x heads, of a kv head). One decode token: n_nodes = 1, its row already in the cache and
  * tree NULL, or its row as the tree's. llm_tree_status reports waits that ran out. */
 int llm_prefix_attention(const llm_prefix_attention_args* args, void* cuda_stream);
 

@@ -3,8 +3,11 @@
 Tolerances are those of the tree attention's tests (its docstring derives them), over all the keys that a node sees:
 per output element, with A = sum_j p_j |v_j|,
   tol = round |o| + A (2 ds + 2^-21 + part + 2 (N + 64) 2^-23) + N 2^-126 max |v|,  ds = (hd + 8) 2^-23 max_j sum_d |q k| scale,
-part = 2^-23 for fp32 queries (three bf16 parts), 2^-16 for bf16 ones and 2 2^-8 where more than 64 query rows of a kv
-head share bf16 rows (one part), 2^-16 more for int8 values. Joining the two parts: their two weights are within 2^-21
+part = 2^-23 for fp32 queries (three bf16 parts), 2^-16 for bf16 ones and 2 2^-8 where the batch has more than 64 query
+rows of a kv head over bf16 rows (one part), 2^-16 more for int8 values. One part: every p of the prefix is rounded to
+bf16 once, half a step of 2^-8 p at most, so sum p v is off by 2^-8 A; where the sum of p is taken of the rounded ones it
+is off by 2^-8 of itself, 2^-8 A again. The kernel is chosen on the host, which knows the batch's rows and not how they
+fall into groups, so it is the batch's number that counts: a small group beside large ones has one part too. Joining the two parts: their two weights are within 2^-21
 (exp2, products, a quotient), so 2^-20 A more.
 """
 import math
@@ -88,7 +91,6 @@ class Problem:
             g = next((g for g in range(self.G) if self.starts[g] <= b < self.starts[g + 1]), None)
             P = 0 if g is None else min(max(self.plens[g], 0), self.rows["prefix"][0].shape[2])
             L = min(max(self.lens[b], 0), self.rows["cache"][0].shape[2])
-            size = 0 if g is None else (self.starts[g + 1] - self.starts[g]) * n * gq
             for i in range(cnt):
                 js = [j for j in range(cnt) if self.tree and self.words[b][i] >> j & 1]
                 K, V = (torch.cat([wide["prefix"][m][g or 0, :, :P], wide["cache"][m][b, :, :L], wide["tree"][m][b][:, js]], 1)
@@ -102,7 +104,7 @@ class Problem:
                 o, A = w @ V, w @ V.abs()
                 ds = (hd + 8) * 2.0 ** -23 * (x.abs() @ K.abs().transpose(1, 2)).amax(-1, keepdim=True) * abs(scale)
                 rnd, part = (2.0 ** -8, 2.0 ** -16) if bf else (2.0 ** -24, 2.0 ** -23)
-                if bf and self.kv == "bf16" and max(size, n * gq) > 64:
+                if bf and self.kv == "bf16" and self.B * n * gq > 64:
                     part = 2 * 2.0 ** -8
                 if bf and self.kv == "q8":
                     part += 2.0 ** -16

@@ -121,7 +121,7 @@ def test_prefix_refused(i):
 
 
 def test_prefix_workspace_sizes():
-    assert bq.prefix_workspace(Fake((4, 2, 6, 64))) == 4 * 2 * 6 * (64 * 4 + 8)
+    assert bq.prefix_workspace(Fake((4, 2, 6, 64))) == 4 * 2 * 6 * (8 * (64 * 4 + 8) + 4)
     for shape in ((0, 2, 6, 64), (4, 65, 6, 64), (4, 2, 6, 96), (4, 2, 0, 128), (1 << 17, 2, 6, 64)):
         with pytest.raises(bq.LlmError):
             bq.prefix_workspace(Fake(shape))
