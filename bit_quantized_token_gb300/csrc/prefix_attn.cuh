@@ -6,13 +6,15 @@
 // so the products run untransposed, a tile of 128 rows against 128 keys:
 //   S [128 rows x 128 keys] = Q K_tile^T        (both K-major, from shared memory)
 //   O [128 rows x dims]    += P V_tile          (P from tensor memory, V as TMA lays it down)
-// A CTA takes two tiles of rows over the same keys: while one tile's four warps turn
-// scores into probabilities, the tensor cores work for the other. A thread is a row:
-// its scores, reference and sum are its own. The reference is the first tile's maximum
-// and is renewed only when a tile's probabilities pass 2^60 (bf16 and fp32 keep their
-// precision over that range), so O is hardly ever touched between products.
-// P lies in columns of its own at 64 dims; at 128 dims, where O takes half of tensor
-// memory, over the scores it came from, and the next scores wait for P V.
+// A CTA takes two tiles of rows over the same keys, 64 keys (a block) at a time; a tile
+// has three blocks of scores in tensor memory at 64 dims, two at 128 (O takes the rest), so that
+// scores are made while the block before them becomes probabilities, which come to lie
+// over them. A thread is a row: its scores, reference and sum are its own. The
+// reference is the first block's maximum and is renewed only when a block's
+// probabilities pass 2^60 (bf16 and fp32 keep their precision over that range), so O is
+// hardly ever touched between products. Four softmax warps and one that issues
+// products for each tile: a wait takes 75 cycles even when it is over, and one warp
+// for both had 1,400 cycles to a block's turn.
 // P is rounded to bf16 (8 bits): the outputs' error is 1.41 times what rounding them
 // to bf16 gives. Two parts of it would make half as many matrix operations more.
 //
@@ -31,16 +33,17 @@ inline int wide_parts(int64_t rows) { return rows <= 10240 ? 8 : rows <= 40960 ?
 
 template <int HD>
 struct Wide {
-  static constexpr int H = HD / 64, BK = 128, NT = 320;
+  static constexpr int H = HD / 64, BK = 128, KB = 64;            // keys of a tile in shared memory, of a block
+  static constexpr int NBUF = HD == 64 ? 3 : 2;                   // blocks of scores of a row tile
+  static constexpr int kMmaWarp = 8, kTmaWarp = 10, NT = 352;
   static constexpr int kTile = 128 * HD * 2, kUnit = 128 * 128;  // bytes of 128 rows of Q, K or V; of 64 dims of them
   static constexpr int NST = HD == 64 ? 8 : 4;                   // K and V tiles in flight
-  static constexpr int kSmall = 512 + 4 * (kWideGroups + 1);
+  static constexpr int kOffCum = 512, kSmall = kOffCum + 4 * (kWideGroups + 1);
   static constexpr int kSmem = 2 * kTile + NST * kTile + kSmall + 1024;
   // more than half of an SM's: no CTA that holds tensor memory shares the SM (this one takes all of it)
   static_assert(kSmem > 140000 && kSmem <= 232448, "shared memory");
-  static constexpr bool own_p = HD == 64;
-  __host__ __device__ static constexpr int at_p(int t) { return own_p ? 256 + 64 * t : 128 * t; }
-  __host__ __device__ static constexpr int at_o(int t) { return own_p ? 384 + 64 * t : 256 + 128 * t; }
+  static constexpr int kAtO = 2 * NBUF * KB;                      // columns: S of tile t, buffer x at (t NBUF + x) KB; then O
+  static_assert(kAtO + 2 * HD <= 512, "tensor memory");
 };
 
 struct WideParams {
@@ -59,12 +62,6 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* v) {
       "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
       "r"(v[31])
       : "memory");
-}
-__device__ __forceinline__ void tc_st32f(uint32_t addr, const float (&v)[32]) {
-  uint32_t u[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]);
-  tc_st32(addr, u);
 }
 __device__ __forceinline__ void st_global8(float* at, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
@@ -124,7 +121,7 @@ struct WidePlan {
 template <int HD>
 __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid_constant__ WideParams wp) {
   using C = Wide<HD>;
-  constexpr int H = C::H, NST = C::NST, BK = C::BK;
+  constexpr int H = C::H, NST = C::NST, BK = C::BK, KB = C::KB, NBUF = C::NBUF;
   extern __shared__ uint8_t sm_raw[];
   const TreeAttnParams& p = wp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -133,27 +130,28 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
   uint8_t* sring = sq + 2 * C::kTile;     // [NST][H][128 keys][128 B]
   uint8_t* small = sring + NST * C::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
-  uint64_t *full = bars, *empty = bars + 8, *q_full = bars + 16, *s_full = bars + 18, *p_full = bars + 20, *o_done = bars + 22,
-           *drain = bars + 24;
-  volatile int* s_abort = reinterpret_cast<volatile int*>(small + 256);  // (11 ints: see tc_wait_long)
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 320);
-  int* s_kt = reinterpret_cast<int*>(small + 324);   // most key tiles of a group
-  int* s_none = reinterpret_cast<int*>(small + 328);  // a group without prefix rows
-  uint32_t* cum = reinterpret_cast<uint32_t*>(small + 512);
+  uint64_t *full = bars, *empty = bars + 8, *q_full = bars + 16, *s_full = bars + 18, *p_full = bars + 24, *o_done = bars + 30,
+           *drain = bars + 36;  // [NST], [NST], [2], then [2][3]
+  volatile int* s_abort = reinterpret_cast<volatile int*>(small + 304);  // (12 ints: see tc_wait_long)
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 352);
+  int* s_kt = reinterpret_cast<int*>(small + 356);   // most key tiles of a group
+  int* s_none = reinterpret_cast<int*>(small + 360);  // a group without prefix rows
+  uint32_t* cum = reinterpret_cast<uint32_t*>(small + C::kOffCum);
   if (tid == 0) {
     s_abort[0] = 0, s_abort[kLimitAt] = p.wait.ns;
-    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
-    for (int i = 0; i < 2; ++i)
-      mbar_init(q_full + i, 128), mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 + p.wait.missing), mbar_init(o_done + i, 1);
-    mbar_init(drain, 1);
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 2);
+    for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 128);
+    for (int i = 0; i < 6; ++i)
+      mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 + p.wait.missing), mbar_init(o_done + i, 1);
+    mbar_init(drain, 2);
     mbar_fence_init();
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == 8) {
+  if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  } else if (warp == 9) {  // units before each group
+  } else if (warp == C::kTmaWarp) {  // units before each group
     uint32_t before = 0;
     int most = 1;
     bool none = false;
@@ -188,13 +186,14 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
           p.part_n[(int64_t)first * p.n * p.Hkv * p.gq + i] = 0;
     }
   WidePlan plan(p, cum, wp.whole, *s_kt);
-  WideSegment seg;
+  WideSegment seg{};
   uint32_t base = 0;  // K and V tiles of the segments before
   // The ring's order in a segment of n tiles: K0 K1 V0 K2 V1 ..
   auto k_at = [&](int t) { return base + (t == 0 ? 0 : 2 * t - 1); };
   auto v_at = [&](int t, int n) { return base + (t == n - 1 ? 2 * t + 1 : 2 * t + 2); };
+  auto blocks = [&]() { return min(2 * (seg.k1 - seg.k0), (seg.len - seg.k0 * BK + KB - 1) / KB); };
   uint32_t sent = 0;
-  if (warp == 9) {
+  if (warp == C::kTmaWarp) {
     if (lane == 0) {
       bool ok = true;
       while (ok && plan.next(seg)) {
@@ -216,83 +215,84 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         base += 2 * n;
       }
     }
-  } else if (warp == 8) {
-    // ---- MMA
+  } else if (warp >= C::kMmaWarp) {
+    // ---- MMA, of row tile t
     constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 x bf16, 128 rows
-    constexpr uint32_t idesc_s = base_i | ((uint32_t)(BK >> 3) << 17);
+    constexpr uint32_t idesc_s = base_i | ((uint32_t)(KB >> 3) << 17);
     constexpr uint32_t idesc_o = base_i | ((uint32_t)(HD >> 3) << 17) | (1u << 16);  // V is MN-major
-    const uint32_t uq = smem_u32(sq), ur = smem_u32(sring);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const int t = warp - C::kMmaWarp;
+    const uint32_t ur = smem_u32(sring), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t tS = tm + t * NBUF * KB, tO = tm + C::kAtO + t * HD;
+    const uint64_t da = tc_desc(smem_u32(sq) + t * C::kTile, 16, 1024, 2);
     bool ok = true;
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // segments, tiles of either tile of rows so far
+    uint32_t n_seg = 0, done = 0;  // segments, blocks so far
+    const auto landed = [&](uint32_t i) { return tc_wait_warp(full + i % NST, (i / NST) & 1, s_abort, p.status); };
     while (ok && plan.next(seg)) {
-      const int n = seg.k1 - seg.k0, nt = seg.rows > 128 ? 2 : 1;
-      auto scores = [&](int t, uint32_t slot) {
-        const uint64_t da = tc_desc(uq + t * C::kTile, 16, 1024, 2), db = tc_desc(ur + slot * C::kTile, 16, 1024, 2);
+      const int n = seg.k1 - seg.k0, nb = blocks();
+      if (t * 128 >= seg.rows) {  // no rows: the tiles are given back as they come
+#pragma unroll 1
+        for (uint32_t i = base; i < base + 2 * n && ok; ++i) {
+          ok = landed(i);
+          if (ok && lane == 0) mbar_arrive(empty + i % NST);
+        }
+        base += 2 * n;
+        continue;
+      }
+      auto scores = [&](int j) {  // of block j, once its keys are there
+        const uint32_t i = k_at(j >> 1), slot = i % NST, x = (done + j) % NBUF;
+        if (!(j & 1)) ok = ok && landed(i);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t db = tc_desc(ur + slot * C::kTile + (j & 1) * KB * 128, 16, 1024, 2);
         if (elect_lane()) {
 #pragma unroll
           for (int u = 0; u < H; ++u)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
-              tc_mma(tm + 128 * t, da + (u * C::kUnit >> 4) + 2 * ks, db + (u * C::kUnit >> 4) + 2 * ks, idesc_s, u > 0 || ks > 0);
+              tc_mma(tS + x * KB, da + (u * C::kUnit >> 4) + 2 * ks, db + (u * C::kUnit >> 4) + 2 * ks, idesc_s, u > 0 || ks > 0);
         }
         __syncwarp();
-        tc_commit(s_full + t);
+        tc_commit(s_full + 3 * t + x);
+        if ((j & 1) || j == nb - 1) tc_commit(empty + slot);
       };
-      {
-        const uint32_t i = k_at(0), slot = i % NST;
-        ok = tc_wait_warp(full + slot, (i / NST) & 1, s_abort, p.status);
-        for (int t = 0; t < nt && ok; ++t) {
-          ok = tc_wait_warp(q_full + t, nq[t] & 1, s_abort, p.status);
-          if (!ok) break;
-          ++nq[t];
-          tc_fence_after();
-          scores(t, slot);
-        }
-        if (ok) tc_commit(empty + slot);
-      }
+      ok = tc_wait_warp(q_full + t, n_seg & 1, s_abort, p.status);
+      ++n_seg;
+      for (int j = 0; j < NBUF - 1 && j < nb; ++j) scores(j);
 #pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-        const bool more = i + 1 < n;
-        const uint32_t ik = k_at(i + 1), iv = v_at(i, n), sk = ik % NST, sv = iv % NST;
-        if (more) ok = tc_wait_warp(full + sk, (ik / NST) & 1, s_abort, p.status);
-        for (int t = 0; t < nt && ok; ++t) {
-          ok = tc_wait_warp(p_full + t, np[t] & 1, s_abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (C::own_p && more) scores(t, sk);
-          if (t == 0) ok = tc_wait_warp(full + sv, (iv / NST) & 1, s_abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t db = tc_desc(ur + sv * C::kTile, C::kUnit, 1024, 2);
-          if (elect_lane()) {
-#pragma unroll
-            for (int ks = 0; ks < BK / 16; ++ks)  // 16 keys: 8 columns of P, 2 KB of V further
-              tc_mma_ts(tm + C::at_o(t), tm + C::at_p(t) + 8 * ks, db + ks * (uint64_t)128, idesc_o, i > 0 || ks > 0);
-          }
-          __syncwarp();
-          tc_commit(o_done + t);
-          if (!C::own_p && more) {  // the scores come to lie where P is
-            ok = tc_wait_warp(o_done + t, np[t] & 1, s_abort, p.status);
-            if (!ok) break;
-            scores(t, sk);
-          }
-          ++np[t];
+      for (int j = 0; j < nb && ok; ++j) {
+        if (j + NBUF - 1 < nb) {  // into the buffer of the block before: its P V is done
+          const uint32_t before = done + j - 1;
+          if (j > 0) ok = tc_wait_warp(o_done + 3 * t + before % NBUF, (before / NBUF) & 1, s_abort, p.status);
+          scores(j + NBUF - 1);
         }
-        if (ok && more) tc_commit(empty + sk);
-        if (ok) tc_commit(empty + sv);
+        const uint32_t b = done + j, x = b % NBUF, iv = v_at(j >> 1, n), sv = iv % NST;
+        if (!(j & 1)) ok = ok && landed(iv);
+        ok = ok && tc_wait_warp(p_full + 3 * t + x, (b / NBUF) & 1, s_abort, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t db = tc_desc(ur + sv * C::kTile + (j & 1) * KB * 128, C::kUnit, 1024, 2);
+        if (elect_lane()) {
+#pragma unroll
+          for (int ks = 0; ks < KB / 16; ++ks)  // 16 keys: 8 columns of P, 2 KB of V further
+            tc_mma_ts(tO, tS + x * KB + 8 * ks, db + ks * (uint64_t)128, idesc_o, j > 0 || ks > 0);
+        }
+        __syncwarp();
+        tc_commit(o_done + 3 * t + x);
+        if ((j & 1) || j == nb - 1) tc_commit(empty + sv);
       }
+      done += nb;
       base += 2 * n;
     }
   } else {
     // ---- softmax: thread = row of tile t
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t tS = tmem + lanes + 128 * t, tP = tmem + lanes + C::at_p(t), tO = tmem + lanes + C::at_o(t);
-    uint32_t ns = 0;  // tiles so far
+    const uint32_t tS0 = tmem + lanes + t * NBUF * KB, tO = tmem + lanes + C::kAtO + t * HD;
+    uint32_t done = 0;  // blocks so far
     bool ok = true;
+    auto pv_done = [&](uint32_t b) { return tc_wait_warp(o_done + 3 * t + b % NBUF, (b / NBUF) & 1, s_abort, p.status); };
     while (ok && plan.next(seg)) {
-      const int n = seg.k1 - seg.k0;
+      const int n = seg.k1 - seg.k0, nb = blocks();
       if (t * 128 >= seg.rows) {
         base += 2 * n;
         continue;
@@ -316,110 +316,100 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
       }
       float ref = -kNone, l = 0.f;  // the reference, negated; the sum of the probabilities
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int left = seg.len - (seg.k0 + i) * BK;  // keys from this tile on
-        ok = tc_wait_warp(s_full + t, ns & 1, s_abort, p.status);
+      for (int j = 0; j < nb; ++j) {
+        const uint32_t blk = done + j, x = blk % NBUF, tS = tS0 + x * KB;
+        const int left = seg.len - seg.k0 * BK - j * KB;  // keys from this block on
+        ok = tc_wait_warp(s_full + 3 * t + x, (blk / NBUF) & 1, s_abort, p.status);
         if (!ok) break;
         tc_fence_after();
         float a[32], b[32];
-        auto mask = [&](float (&v)[32], int c0) {
-          if (left < BK)
+        auto load = [&]() {
+          tc_ld(a, tS);
+          tc_ld(b, tS + 32);
+          tc_wait_ld(a);
+          tc_wait_ld(b);
+          if (left < KB)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c0 + j >= left) v[j] = -INFINITY;
+            for (int i = 0; i < 32; ++i) {
+              if (i >= left) a[i] = -INFINITY;
+              if (32 + i >= left) b[i] = -INFINITY;
+            }
         };
         auto highest = [&]() {
           float m = -INFINITY;
 #pragma unroll
-          for (int c0 = 0; c0 < BK; c0 += 32) {
-            tc_ld(a, tS + c0);
-            tc_wait_ld(a);
-            mask(a, c0);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) m = fmaxf(m, a[j]);
-          }
+          for (int i = 0; i < 32; ++i) m = fmaxf(m, fmaxf(a[i], b[i]));
           return m;
         };
-        if (i == 0) {
+        load();
+        if (j == 0) {
           const float m = highest();
           ref = fabsf(m) < 1e38f ? -m : -kNone;
         }
-        uint32_t pk[BK / 2];
+        uint32_t pk[KB / 2];
         float sum;
         for (;;) {
-          float s0 = 0.f, s1 = 0.f;
-          auto take = [&](float (&v)[32], int c0) {
-            mask(v, c0);
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              add2(v[j], v[j + 1], v[j], v[j + 1], ref, ref);
-              mul2(v[j], v[j + 1], v[j], v[j + 1], p.c);
-              v[j] = ex2(v[j]), v[j + 1] = ex2(v[j + 1]);
-              add2(s0, s1, s0, s1, v[j], v[j + 1]);
-              pk[(c0 + j) / 2] = pack_bf16x2(v[j], v[j + 1]);
-            }
-          };
-          tc_ld(a, tS);
-          tc_wait_ld(a);
-          tc_ld(b, tS + 32);
-          take(a, 0);
-          tc_wait_ld(b);
-          tc_ld(a, tS + 64);
-          take(b, 32);
-          tc_wait_ld(a);
-          tc_ld(b, tS + 96);
-          take(a, 64);
-          tc_wait_ld(b);
-          take(b, 96);
-          sum = s0 + s1;
+          for (int i = 0; i < 32; i += 2) {
+            add2(a[i], a[i + 1], a[i], a[i + 1], ref, ref);
+            add2(b[i], b[i + 1], b[i], b[i + 1], ref, ref);
+            mul2(a[i], a[i + 1], a[i], a[i + 1], p.c);
+            mul2(b[i], b[i + 1], b[i], b[i + 1], p.c);
+            a[i] = ex2(a[i]), a[i + 1] = ex2(a[i + 1]);
+            b[i] = ex2(b[i]), b[i + 1] = ex2(b[i + 1]);
+            add2(s0, s1, s0, s1, a[i], a[i + 1]);
+            add2(s2, s3, s2, s3, b[i], b[i + 1]);
+            pk[i / 2] = pack_bf16x2(a[i], a[i + 1]);
+            pk[16 + i / 2] = pack_bf16x2(b[i], b[i + 1]);
+          }
+          sum = (s0 + s1) + (s2 + s3);
           const bool over = sum > 1152921504606846976.f;  // 2^60
           if (!__any_sync(0xffffffffu, over)) break;
           // renew the references of the warp's rows; rescale O and the sums
-          const float m = highest(), old = -ref, now = fmaxf(m, old), f = !over || old == now ? 1.f : exp2f((old - now) * p.c);
+          load();
+          const float old = -ref, now = fmaxf(highest(), old), f = !over || old == now ? 1.f : exp2f((old - now) * p.c);
           if (over && now > old) ref = -now;
           l *= f;
-          if (i > 0) {
-            ok = tc_wait_warp(o_done + t, (ns - 1) & 1, s_abort, p.status);
+          if (j > 0) {
+            ok = pv_done(blk - 1);
+            if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < HD; c0 += 32) {
-              tc_ld(a, tO + c0);
-              tc_wait_ld(a);
+            for (int c0 = 0; c0 < HD; c0 += 16) {
+              float o[16];
+              tc_ld(o, tO + c0);
+              tc_wait_ld(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) a[j] *= f;
-              tc_st32f(tO + c0, a);
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tc_st16(tO + c0, o);
             }
             tc_wait_st();
           }
-          if (!ok) break;
         }
         if (!ok) break;
         l += sum;
-        if (left < BK) {  // V rows that are not there become zeros: 0 times whatever lies there need not be 0
-          const uint32_t iv = v_at(i, n), slot = iv % NST;
+        if (left < KB) {  // V rows that are not there become zeros: 0 times whatever lies there need not be 0
+          const uint32_t iv = v_at(j >> 1, n), slot = iv % NST;
           ok = tc_wait_warp(full + slot, (iv / NST) & 1, s_abort, p.status);
           if (!ok) break;
 #pragma unroll 1
-          for (int c = r; c < (BK - left) * (HD / 8); c += 128) {
-            const int row_v = left + c / (HD / 8), ch = c % (HD / 8);
+          for (int c = r; c < (KB - left) * (HD / 8); c += 128) {
+            const int row_v = (j & 1) * KB + left + c / (HD / 8), ch = c % (HD / 8);
             *reinterpret_cast<uint4*>(sring + slot * C::kTile + (ch / 8) * C::kUnit + row_v * 128 + 16 * (ch & 7)) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
           fence_async_smem();
         }
-        if (C::own_p && i > 0) {  // the last P V has read P
-          ok = tc_wait_warp(o_done + t, (ns - 1) & 1, s_abort, p.status);
-          if (!ok) break;
-        }
-        tc_st32(tP, pk);
-        tc_st32(tP + 32, pk + 32);
+        tc_st32(tS, pk);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(p_full + t);
-        ++ns;
+        mbar_arrive(p_full + 3 * t + x);
       }
       if (!ok) break;
-      ok = tc_wait_warp(o_done + t, (ns - 1) & 1, s_abort, p.status);
+      done += nb;
+      // (one phase of a buffer at a time: the last but one of each is over when its scores have come)
+      for (int k = min(nb, NBUF); k > 0 && ok; --k) ok = pv_done(done - k);
       if (!ok) break;
       tc_fence_after();
       const int64_t at = ((int64_t)seg.first * p.n + node) * (p.Hkv * p.gq) + h;
@@ -431,10 +421,10 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         tc_ld(a, tO + c0);
         tc_wait_ld(a);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) a[j] *= f;
+        for (int i = 0; i < 32; ++i) a[i] *= f;
         if (there)
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) st_global8(out + c0 + j, a + j);
+          for (int i = 0; i < 32; i += 8) st_global8(out + c0 + i, a + i);
       }
       if (there) {
         p.part_ml[seg.piece * p.part_rows + at] = make_float2(-ref, l);
@@ -448,21 +438,21 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
   __syncthreads();
   if (*s_abort) {  // no copy and no product in flight outlives the CTA
     const unsigned long long s0 = globaltimer();
-    if (warp == 9 && lane == 0)
+    if (warp == C::kTmaWarp && lane == 0)
 #pragma unroll 1
       for (uint32_t j = sent > (uint32_t)NST ? sent - NST : 0; j < sent; ++j)
         while (!mbar_try_wait(full + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
         }
     __syncwarp();
-    if (warp == 8) {
-      tc_commit(drain);
+    if (warp >= C::kMmaWarp && warp < C::kTmaWarp) {
+      tc_commit(drain);  // of a warp's own products
       while (!mbar_try_wait(drain, 0) && globaltimer() - s0 < kWaitLimitNs) {
       }
     }
     __syncwarp();
     __syncthreads();
   }
-  if (warp == 8) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }

@@ -292,9 +292,15 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRow
   if (s.greedy) {
     float mx = -INFINITY;
     int at = 0;
-    for (int i = tid; i < n; i += kSampNT) {
-      const float l = src[i];
-      if (l > mx) mx = l, at = i;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kSampU * kSampNT) {
+      float next[kSampU];
+      load(next, i0 + kSampU * kSampNT);
+#pragma unroll
+      for (int e = 0; e < kSampU; ++e) {
+        if (cur[e] > mx) mx = cur[e], at = i0 + e * kSampNT + tid;
+        cur[e] = next[e];
+      }
     }
     u64 best = mx == -INFINITY ? 0 : ((u64)sample_key(fminf(mx, 3.402823466e38f)) << 32) | (uint32_t)~(first + at);
 #pragma unroll
@@ -502,9 +508,12 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRow
     }
     // once more, from the exact range: the least logit of any weight
     float3 low = make_float3(0.f, INFINITY, 0.f);
-    for (int i = tid; i < n; i += kSampNT) {
-      const float l = src[i];
-      if ((m - l) * ch < 63.f) low.y = fminf(low.y, l);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kSampU * kSampNT) {
+      load(cur, i0);
+#pragma unroll
+      for (int e = 0; e < kSampU; ++e)
+        if ((m - cur[e]) * ch < 63.f) low.y = fminf(low.y, cur[e]);
     }
     low = reduce3(low);
     cl.sync();  // every CTA has read the ranges

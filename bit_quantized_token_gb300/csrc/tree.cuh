@@ -146,7 +146,8 @@ struct TreeAttnParams {
   const int* starts = nullptr;
   int G = 0, all = 0;        // groups, sequences
   int nodes;                 // most nodes of a block's sequence(s): n, or all n
-  int* part_n = nullptr;     // [all][n][heads] pieces of a row: 1 .. max_parts
+  static constexpr int kMaxParts = 8;
+  int* part_n = nullptr;     // [all][n][heads] pieces of a row: 0 .. max_parts, which is kMaxParts at most
   int max_parts = 1;
   int64_t part_rows = 0;     // all n heads
   float* part_o = nullptr;   // [max_parts][all][n][heads][head_dim] normalised

@@ -322,7 +322,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // In an attention of two parts the owner writes them out, or joins its row with the
 // first part's, which it waits for here: the kernels overlap until then.
 template <int HD, int N>
-constexpr int kJoin = N * HD * 4 + N * 20;
+constexpr int kJoin = N * HD * 4 + N * (12 + 4 * TreeAttnParams::kMaxParts);
 template <int HD, bool F32, int N, int NT>
 __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float* so, const float2* sml, uint8_t* in,
                                             int rank, int b, int hkv, int m0, int rows) {
@@ -331,7 +331,7 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
   const float4* part = reinterpret_cast<const float4*>(so);  // [S][share][R4]
   const float2* ml = sml;                                    // [S][share]
   float* sw = reinterpret_cast<float*>(in + N * HD * 4 + N * 8);
-  float2* sfirst = reinterpret_cast<float2*>(sw + N);        // of the first part: the common reference, 1 / the sum
+  float* sw_first = sw + N;                                  // [pieces][share] of the first part
   // row m0 + r of the block (its nodes follow one another): index of its (sequence, node, head) in part_ml
   auto part_at = [&](int row) {
     const int node = p.by_gq.div(row);
@@ -378,17 +378,25 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
     }
     if (second) {
       const int64_t at = part_at(m0 + rank * share + r);
-      const int n = first_has ? min(__ldcg(p.part_n + at), p.max_parts) : 0;
+      const int n = first_has ? __ldcg(p.part_n + at) : 0;
+      float2 o[TreeAttnParams::kMaxParts];
       float top = M, sum = 0.f;
-      for (int k = 0; k < n; ++k) top = fmaxf(top, __ldcg(p.part_ml + k * p.part_rows + at).x);
+#pragma unroll
+      for (int k = 0; k < TreeAttnParams::kMaxParts; ++k) {
+        o[k] = k < n && k < p.max_parts ? __ldcg(p.part_ml + k * p.part_rows + at) : make_float2(kNone, 0.f);
+        top = fmaxf(top, o[k].x);
+      }
       const float own_w = M <= kNone ? 0.f : ex2((M - top) * p.c);
-      for (int k = 0; k < n; ++k) {
-        const float2 o = __ldcg(p.part_ml + k * p.part_rows + at);
-        if (o.x > kNone) sum = fmaf(ex2((o.x - top) * p.c), o.y, sum);
+#pragma unroll
+      for (int k = 0; k < TreeAttnParams::kMaxParts; ++k) {
+        o[k].y = o[k].x <= kNone ? 0.f : ex2((o[k].x - top) * p.c) * o[k].y;
+        sum += o[k].y;
       }
       sum = fmaf(own_w, L, sum);
       f = sum == 0.f ? 0.f : 1.f / sum;
-      sfirst[r] = make_float2(top, f);
+#pragma unroll
+      for (int k = 0; k < TreeAttnParams::kMaxParts; ++k)
+        if (k < p.max_parts) sw_first[k * share + r] = o[k].y * f;
       f *= own_w;
     }
     for (int k = 0; k < S; ++k) sw[k * share + r] *= f;
@@ -409,13 +417,12 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
       continue;
     }
     if (first_has) {
-      const int64_t at = part_at(row);
-      const int n = min(__ldcg(p.part_n + at), p.max_parts);
-      for (int k = 0; k < n; ++k) {
-        const float2 o = __ldcg(p.part_ml + k * p.part_rows + at);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (k * p.part_rows + at) * R4 + i % R4);
-        const float f = o.x <= kNone ? 0.f : ex2((o.x - sfirst[r].x) * p.c) * o.y * sfirst[r].y;
-        if (f != 0.f) a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+      const float4* o = reinterpret_cast<const float4*>(p.part_o) + part_at(row) * R4 + i % R4;
+#pragma unroll 4
+      for (int k = 0; k < p.max_parts; ++k) {
+        const float f = sw_first[k * share + r];
+        const float4 x = f != 0.f ? __ldcg(o + k * p.part_rows * R4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y), a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
       }
     }
     const int64_t off = (int64_t)b * p.o_seq + (int64_t)node * p.o_node + (int64_t)h * p.o_head + 4 * (i % R4);
