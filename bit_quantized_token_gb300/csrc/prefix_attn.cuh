@@ -12,9 +12,9 @@
 // over them. A thread is a row: its scores, reference and sum are its own. The
 // reference is the first block's maximum and is renewed only when a block's
 // probabilities pass 2^60 (bf16 and fp32 keep their precision over that range), so O is
-// hardly ever touched between products. Four softmax warps and one that issues
-// products for each tile: a wait takes 75 cycles even when it is over, and one warp
-// for both had 1,400 cycles to a block's turn.
+// hardly ever touched between products. Four softmax warps for each tile, one that
+// issues Q K and one that issues P V: beside the softmax a wait takes 150 cycles even when it
+// is over, and a warp that issued both was the slowest (1,250 cycles a block).
 // P is rounded to bf16 (8 bits): the outputs' error is 1.41 times what rounding them
 // to bf16 gives. Two parts of it would make half as many matrix operations more.
 //
@@ -35,7 +35,7 @@ template <int HD>
 struct Wide {
   static constexpr int H = HD / 64, BK = 128, KB = 64;            // keys of a tile in shared memory, of a block
   static constexpr int NBUF = HD == 64 ? 3 : 2;                   // blocks of scores of a row tile
-  static constexpr int kMmaWarp = 8, kTmaWarp = 10, NT = 352;
+  static constexpr int kMmaWarp = 8, kTmaWarp = 12, NT = 416;
   static constexpr int kTile = 128 * HD * 2, kUnit = 128 * 128;  // bytes of 128 rows of Q, K or V; of 64 dims of them
   static constexpr int NST = HD == 64 ? 8 : 4;                   // K and V tiles in flight
   static constexpr int kOffCum = 512, kSmall = kOffCum + 4 * (kWideGroups + 1);
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 128);
     for (int i = 0; i < 6; ++i)
       mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 + p.wait.missing), mbar_init(o_done + i, 1);
-    mbar_init(drain, 2);
+    mbar_init(drain, 4);
     mbar_fence_init();
   }
   pdl_wait();
@@ -216,11 +216,12 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
       }
     }
   } else if (warp >= C::kMmaWarp) {
-    // ---- MMA, of row tile t
+    // ---- products of row tile t: Q K, or P V
     constexpr uint32_t base_i = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 x bf16, 128 rows
     constexpr uint32_t idesc_s = base_i | ((uint32_t)(KB >> 3) << 17);
     constexpr uint32_t idesc_o = base_i | ((uint32_t)(HD >> 3) << 17) | (1u << 16);  // V is MN-major
-    const int t = warp - C::kMmaWarp;
+    const int t = warp & 1;
+    const bool values = warp >= C::kMmaWarp + 2;
     const uint32_t ur = smem_u32(sring), tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t tS = tm + t * NBUF * KB, tO = tm + C::kAtO + t * HD;
     const uint64_t da = tc_desc(smem_u32(sq) + t * C::kTile, 16, 1024, 2);
@@ -231,54 +232,55 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
       const int n = seg.k1 - seg.k0, nb = blocks();
       if (t * 128 >= seg.rows) {  // no rows: the tiles are given back as they come
 #pragma unroll 1
-        for (uint32_t i = base; i < base + 2 * n && ok; ++i) {
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t i = values ? v_at(j, n) : k_at(j);
           ok = landed(i);
           if (ok && lane == 0) mbar_arrive(empty + i % NST);
         }
         base += 2 * n;
         continue;
       }
-      auto scores = [&](int j) {  // of block j, once its keys are there
-        const uint32_t i = k_at(j >> 1), slot = i % NST, x = (done + j) % NBUF;
-        if (!(j & 1)) ok = ok && landed(i);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t db = tc_desc(ur + slot * C::kTile + (j & 1) * KB * 128, 16, 1024, 2);
-        if (elect_lane()) {
-#pragma unroll
-          for (int u = 0; u < H; ++u)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
-              tc_mma(tS + x * KB, da + (u * C::kUnit >> 4) + 2 * ks, db + (u * C::kUnit >> 4) + 2 * ks, idesc_s, u > 0 || ks > 0);
-        }
-        __syncwarp();
-        tc_commit(s_full + 3 * t + x);
-        if ((j & 1) || j == nb - 1) tc_commit(empty + slot);
-      };
-      ok = tc_wait_warp(q_full + t, n_seg & 1, s_abort, p.status);
-      ++n_seg;
-      for (int j = 0; j < NBUF - 1 && j < nb; ++j) scores(j);
+      if (!values) {
+        ok = tc_wait_warp(q_full + t, n_seg & 1, s_abort, p.status);
+        ++n_seg;
 #pragma unroll 1
-      for (int j = 0; j < nb && ok; ++j) {
-        if (j + NBUF - 1 < nb) {  // into the buffer of the block before: its P V is done
-          const uint32_t before = done + j - 1;
-          if (j > 0) ok = tc_wait_warp(o_done + 3 * t + before % NBUF, (before / NBUF) & 1, s_abort, p.status);
-          scores(j + NBUF - 1);
-        }
-        const uint32_t b = done + j, x = b % NBUF, iv = v_at(j >> 1, n), sv = iv % NST;
-        if (!(j & 1)) ok = ok && landed(iv);
-        ok = ok && tc_wait_warp(p_full + 3 * t + x, (b / NBUF) & 1, s_abort, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t db = tc_desc(ur + sv * C::kTile + (j & 1) * KB * 128, C::kUnit, 1024, 2);
-        if (elect_lane()) {
+        for (int j = 0; j < nb && ok; ++j) {
+          const uint32_t b = done + j, x = b % NBUF, i = k_at(j >> 1), slot = i % NST;
+          if (!(j & 1)) ok = landed(i);
+          // into the buffer of the block NBUF before: its P V is done (of the segment before, all are)
+          if (j >= NBUF) ok = ok && tc_wait_warp(o_done + 3 * t + x, (b / NBUF - 1) & 1, s_abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t db = tc_desc(ur + slot * C::kTile + (j & 1) * KB * 128, 16, 1024, 2);
+          if (elect_lane()) {
 #pragma unroll
-          for (int ks = 0; ks < KB / 16; ++ks)  // 16 keys: 8 columns of P, 2 KB of V further
-            tc_mma_ts(tO, tS + x * KB + 8 * ks, db + ks * (uint64_t)128, idesc_o, j > 0 || ks > 0);
+            for (int u = 0; u < H; ++u)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)  // 16 dims: 32 bytes further
+                tc_mma(tS + x * KB, da + (u * C::kUnit >> 4) + 2 * ks, db + (u * C::kUnit >> 4) + 2 * ks, idesc_s, u > 0 || ks > 0);
+          }
+          __syncwarp();
+          tc_commit(s_full + 3 * t + x);
+          if ((j & 1) || j == nb - 1) tc_commit(empty + slot);
         }
-        __syncwarp();
-        tc_commit(o_done + 3 * t + x);
-        if ((j & 1) || j == nb - 1) tc_commit(empty + sv);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < nb && ok; ++j) {
+          const uint32_t b = done + j, x = b % NBUF, i = v_at(j >> 1, n), slot = i % NST;
+          if (!(j & 1)) ok = landed(i);
+          ok = ok && tc_wait_warp(p_full + 3 * t + x, (b / NBUF) & 1, s_abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t db = tc_desc(ur + slot * C::kTile + (j & 1) * KB * 128, C::kUnit, 1024, 2);
+          if (elect_lane()) {
+#pragma unroll
+            for (int ks = 0; ks < KB / 16; ++ks)  // 16 keys: 8 columns of P, 2 KB of V further
+              tc_mma_ts(tO, tS + x * KB + 8 * ks, db + ks * (uint64_t)128, idesc_o, j > 0 || ks > 0);
+          }
+          __syncwarp();
+          tc_commit(o_done + 3 * t + x);
+          if ((j & 1) || j == nb - 1) tc_commit(empty + slot);
+        }
       }
       done += nb;
       base += 2 * n;
