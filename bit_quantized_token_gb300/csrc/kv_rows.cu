@@ -1,5 +1,7 @@
 // New tokens' K and V rows into a cache, with the norms and the rotation of
 // their q and k heads, and cached rows back out as values (see serve.cuh).
+#include <type_traits>
+
 #include "common.cuh"
 #include "op_call.cuh"
 #include "serve.cuh"
@@ -9,9 +11,9 @@ namespace {
 
 // ---- append --------------------------------------------------------------------
 // A head of q or k: x / sqrt(mean(x^2) + eps) w (with a norm), then the pairs
-// (i, i + hd/2) or (2i, 2i + 1) turned by position times freq_i. A group of hd/8
-// lanes holds a row, a lane four dims of the first half and the same four of the
-// second: both kinds of pairs lie in one lane, 32 neighbouring dims in eight, and
+// (i, i + hd/2) or (2i, 2i + 1) turned by position times freq_i. A group of hd/16
+// lanes holds a row, a lane eight dims of the first half and the same eight of the
+// second: both kinds of pairs lie in one lane, 32 neighbouring dims in four, and
 // the norm is a sum over the group. Everything is fp32 and rounded once, into
 // the outputs' type.
 //
@@ -29,19 +31,28 @@ namespace {
 // rotation), by the launch for few.
 constexpr int kAppendThreads = 128;
 
-template <int N>
-__device__ __forceinline__ void load_vals(float (&x)[N], const void* base, int64_t at, bool f32);
-template <>
-__device__ __forceinline__ void load_vals<4>(float (&x)[4], const void* base, int64_t at, bool f32) {
-  if (f32) {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
-    x[0] = __uint_as_float(a.x << 16), x[1] = __uint_as_float(a.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(a.y << 16), x[3] = __uint_as_float(a.y & 0xFFFF0000u);
+// eight values, of which the loads come before any use
+struct Eight {
+  uint4 w[2];
+  __device__ __forceinline__ void load(const void* base, int64_t at, bool f32) {
+    if (f32) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
+      w[0] = s[0], w[1] = s[1];
+    } else {
+      w[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+    }
   }
-}
+  __device__ __forceinline__ void get(float* x, bool f32) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (f32) {
+        x[e] = __uint_as_float((&w[0].x)[e]), x[4 + e] = __uint_as_float((&w[1].x)[e]);
+      } else {
+        x[2 * e] = __uint_as_float((&w[0].x)[e] << 16), x[2 * e + 1] = __uint_as_float((&w[0].x)[e] & 0xFFFF0000u);
+      }
+    }
+  }
+};
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -51,6 +62,16 @@ __device__ __forceinline__ void store4(void* base, int64_t at, const float* x, b
     *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(x[0], x[1], x[2], x[3]);
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
+}
+
+__device__ __forceinline__ void store8(void* base, int64_t at, const float* x, bool f32) {
+  if (f32) {
+    store4(base, at, x, true);
+    store4(base, at + 4, x + 4, true);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) =
+        make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+  }
 }
 
 // cos and sin of `angle` 2^-64 turns
@@ -64,9 +85,9 @@ __device__ __forceinline__ float2 turn_of(uint64_t angle) {
   return make_float2((quad + 1) & 2 ? -a : a, quad & 2 ? -b : b);
 }
 
-template <int HD, bool Q8>
+template <int HD, bool Q8, bool F32>
 __global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int LPR = HD / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+  constexpr int LPR = HD / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, c = lane % LPR;
@@ -74,99 +95,118 @@ __global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const __grid_
   const int64_t w = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int t = (int)(w / slices), h0 = (int)(w - (int64_t)t * slices) * per + lane / LPR;
   if (t >= p.T) return;
+  // a pass's row: q heads, then k heads, then v heads
+  Eight lo, hi;
+  auto row_of = [&](int j, int& kind, int& hh) {
+    const int h = h0 + j * RPW;
+    kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
+    hh = kind == 0 ? h : (h - p.Hq) - (kind - 1) * p.Hkv;
+    return h < heads && j < p.passes;
+  };
+  auto load = [&](int j) {
+    int kind, hh;
+    if (row_of(j, kind, hh)) {
+      const void* src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+      const int64_t at = t * (kind == 0 ? p.q_tok : kind == 1 ? p.k_tok : p.v_tok) +
+                         hh * (kind == 0 ? p.q_head : kind == 1 ? p.k_head : p.v_head) + 8 * c;
+      lo.load(src, at, F32);
+      hi.load(src, at + HD / 2, F32);
+    } else {
+      lo.w[0] = lo.w[1] = hi.w[0] = hi.w[1] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load(0);  // on its way while the angles are computed
   const int seq = p.seqs[t], row = p.rows[t];
   const bool kept = seq >= 0 && seq < p.n_seq && row >= 0 && row < p.cache.rows;
-  float2 cs[4];
+  float2 cs[8];
   if (p.rotate) {
     const int64_t pos = p.positions ? p.positions[t] : row;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = p.neox ? 4 * c + e : (e < 2 ? 2 * c + e : HD / 4 + 2 * c + e - 2);
+    for (int e = 0; e < 8; ++e) {
+      const int i = p.neox ? 8 * c + e : (e < 4 ? 4 * c + e : HD / 4 + 4 * c + e - 4);
       cs[e] = turn_of((uint64_t)pos * p.freq[i]);
     }
   }
-#pragma unroll 2
+#pragma unroll 1
   for (int j = 0; j < p.passes; ++j) {
-    const int h = h0 + j * RPW;  // q heads, then k heads, then v heads
-    const bool in = h < heads;
-    const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2, hh = kind == 0 ? h : (h - p.Hq) - (kind - 1) * p.Hkv;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      const void* src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-      const int64_t at = t * (kind == 0 ? p.q_tok : kind == 1 ? p.k_tok : p.v_tok) +
-                         hh * (kind == 0 ? p.q_head : kind == 1 ? p.k_head : p.v_head) + 4 * c;
-      float lo[4], hi[4];
-      load_vals<4>(lo, src, at, p.f32);
-      load_vals<4>(hi, src, at + HD / 2, p.f32);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
-    }
+    int kind, hh;
+    const bool in = row_of(j, kind, hh);
+    float x[16];
+    lo.get(x, F32);
+    hi.get(x + 8, F32);
+    load(j + 1);
     const float* wn = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
     if (p.q_norm || p.k_norm) {  // (by the whole warp: its rows may be of different kinds)
       float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (wn && in) {
-        const float inv = 1.0f / sqrtf(ss / (float)HD + p.eps);
-        const float4 a = __ldg(reinterpret_cast<const float4*>(wn) + c);
-        const float4 b = __ldg(reinterpret_cast<const float4*>(wn + HD / 2) + c);
-        x[0] *= inv * a.x, x[1] *= inv * a.y, x[2] *= inv * a.z, x[3] *= inv * a.w;
-        x[4] *= inv * b.x, x[5] *= inv * b.y, x[6] *= inv * b.z, x[7] *= inv * b.w;
+        const float inv = rsqrtf(fmaf(ss, 1.0f / HD, p.eps));
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(wn + (e & 8 ? HD / 2 : 0) + 8 * c + (e & 4)));
+          x[e] *= inv * a.x, x[e + 1] *= inv * a.y, x[e + 2] *= inv * a.z, x[e + 3] *= inv * a.w;
+        }
       }
     }
     if (p.rotate && kind < 2) {
+      auto turned = [&](float& a, float& b, float2 cs_) {
+        const float a0 = a;
+        a = a0 * cs_.x - b * cs_.y;
+        b = a0 * cs_.y + b * cs_.x;
+      };
+      if (p.neox) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int ia = p.neox ? e : 2 * e, ib = p.neox ? e + 4 : 2 * e + 1;
-        const float a = x[ia], b = x[ib];
-        x[ia] = a * cs[e].x - b * cs[e].y;
-        x[ib] = a * cs[e].y + b * cs[e].x;
+        for (int e = 0; e < 8; ++e) turned(x[e], x[e + 8], cs[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turned(x[2 * e], x[2 * e + 1], cs[e]);
       }
     }
     if (in && kind == 0) {
-      const int64_t at = t * p.o_tok + hh * p.o_head + 4 * c;
-      store4(p.q_out, at, x, p.out_f32);
-      store4(p.q_out, at + HD / 2, x + 4, p.out_f32);
+      const int64_t at = t * p.o_tok + hh * p.o_head + 8 * c;
+      store8(p.q_out, at, x, p.out_f32);
+      store8(p.q_out, at + HD / 2, x + 8, p.out_f32);
     }
     uint8_t* base = const_cast<uint8_t*>(kind == 2 ? p.cache.v : p.cache.k);
     const int64_t at = (int64_t)seq * p.cache.seq + (int64_t)hh * p.cache.head + (int64_t)row * p.cache.row;
     if constexpr (!Q8) {
       if (in && kind > 0 && kept) {
-        store4(base, at + 4 * c, x, false);
-        store4(base, at + HD / 2 + 4 * c, x + 4, false);
+        store8(base, at + 8 * c, x, false);
+        store8(base, at + HD / 2 + 8 * c, x + 8, false);
       }
     } else if (__any_sync(0xffffffffu, in && kind > 0)) {
-      uint32_t word[2];
+      uint2 word[2];
       uint16_t sc[2];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {  // of either half: eight lanes hold 32 neighbouring dims
+      for (int g = 0; g < 2; ++g) {  // of either half: four lanes hold 32 neighbouring dims
         uint32_t top = 0;            // of the sizes as integers: a NaN's is above all others
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[4 * g + e]) & 0x7FFFFFFFu);
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[8 * g + e]) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float amax = __uint_as_float(top);
         const __half dh = __float2half_rn(top > 0x7F800000u ? amax : fminf(amax / 127.0f, 65504.f));
         const float dq = __half2float(dh);
-        uint32_t codes = 0;
+        uint32_t codes[2] = {0, 0};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float cf = dq == 0.f ? 0.f : fminf(fmaxf(roundf(x[4 * g + e] / dq), -127.f), 127.f);
-          codes |= ((uint32_t)(int)cf & 0xFFu) << (8 * e);
+        for (int e = 0; e < 8; ++e) {
+          const float cf = dq == 0.f ? 0.f : fminf(fmaxf(roundf(x[8 * g + e] / dq), -127.f), 127.f);
+          codes[e / 4] |= ((uint32_t)(int)cf & 0xFFu) << (8 * (e & 3));
         }
-        word[g] = codes;
+        word[g] = make_uint2(codes[0], codes[1]);
         sc[g] = __half_as_ushort(dh);
       }
       if (in && kind > 0 && kept) {
-        *reinterpret_cast<uint32_t*>(base + at + 4 * c) = word[0];
-        *reinterpret_cast<uint32_t*>(base + at + HD / 2 + 4 * c) = word[1];
-        if ((c & 7) == 0) {
+        *reinterpret_cast<uint2*>(base + at + 8 * c) = word[0];
+        *reinterpret_cast<uint2*>(base + at + HD / 2 + 8 * c) = word[1];
+        if ((c & 3) == 0) {
           uint16_t* s = const_cast<uint16_t*>(kind == 2 ? p.cache.vs : p.cache.ks) + (int64_t)seq * p.cache.sseq +
                         (int64_t)hh * p.cache.shead + (int64_t)row * p.cache.srow;
-          s[c / 8] = sc[0];
-          s[HD / 64 + c / 8] = sc[1];
+          s[c / 4] = sc[0];
+          s[HD / 64 + c / 4] = sc[1];
         }
       }
     }
@@ -247,15 +287,19 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const ReadParams 
 }  // namespace
 
 cudaError_t launch_append_kv(AppendParams& p, int hd, bool q8, int n_sm, cudaStream_t st) {
-  const int rpw = 256 / hd, heads = p.Hq + 2 * p.Hkv, groups = (heads + rpw - 1) / rpw;
+  const int rpw = 512 / hd, heads = p.Hq + 2 * p.Hkv, groups = (heads + rpw - 1) / rpw;
   // One pass a warp while the warps fit the SMs at once (16 a SM); a warp that takes
   // more rows of its token computes the token's angles once for them.
   const int64_t per = (int64_t)p.T * groups / (16 * (int64_t)n_sm);
   p.passes = (int)(per < 1 ? 1 : per < groups ? per : groups);
   const int64_t warps = (int64_t)p.T * ((heads + rpw * p.passes - 1) / (rpw * p.passes));
   const dim3 grid((unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
-  const auto kern = hd == 64 ? (q8 ? append_kv_kernel<64, true> : append_kv_kernel<64, false>)
-                             : (q8 ? append_kv_kernel<128, true> : append_kv_kernel<128, false>);
+  const auto of_type = [&](auto f32) {
+    constexpr bool F32 = decltype(f32)::value;
+    return hd == 64 ? (q8 ? append_kv_kernel<64, true, F32> : append_kv_kernel<64, false, F32>)
+                    : (q8 ? append_kv_kernel<128, true, F32> : append_kv_kernel<128, false, F32>);
+  };
+  const auto kern = p.f32 ? of_type(std::true_type()) : of_type(std::false_type());
   return launch_cluster(kern, grid, kAppendThreads, 1, 0, st, p, p.pdl);
 }
 

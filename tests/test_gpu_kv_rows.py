@@ -1,7 +1,7 @@
 """append_kv and read_kv against the formulas in 64 bits (GPU).
 
 Tolerances from the roundings, with u = 2^-24: the norm's sum of hd squares is within hd u, its square root halves
-that; quotient, root and two products 4 u, so a normed value is within (hd / 2 + 8) u. cos and sin: a quarter half-turn
+that; the reciprocal root 4 u and two products 2 u, so a normed value is within (hd / 2 + 8) u. cos and sin: a quarter half-turn
 in fp32, sincospi within 2 steps, the turn's table 2^-50 a position: 2^-22 + 2 pi |pos| 2^-50. A rotated value is two
 products and a sum: tol = (|a| + |b|) ((hd / 2 + 8) u + 2^-22 + 2 pi |pos| 2^-50 + 3 u), and half a step of the output.
 Int8: a code is within half a scale of the value that it stands for (the scale's own rounding leaves 127.07 at most, so
