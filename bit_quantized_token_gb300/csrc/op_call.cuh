@@ -44,7 +44,9 @@ inline AddressRange address_range() {
 struct Call {
   int dev = -1, n_sm = 0, rc = LLM_OK;
   cudaError_t e = cudaSuccess;  // reported by the first buffer's check, after those of sizes
-  uintptr_t lo = 0, size = 0;   // the allocation of the last buffer looked up
+  static constexpr int kRanges = 4;
+  uintptr_t lo[kRanges] = {}, size[kRanges] = {};  // the allocations of the last buffers looked up
+  int n_ranges = 0;
   Call() {
     static std::atomic<int> sms[64];
     e = cudaGetDevice(&dev);
@@ -71,7 +73,8 @@ struct Call {
       return false;
     }
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    if (at - lo < size) return true;  // in the allocation of the buffer before: a pool's small tensors share one
+    for (int i = 0; i < kRanges; ++i)
+      if (at - lo[i] < size[i]) return true;  // in the allocation of a buffer before: a pool's tensors share some
     cudaPointerAttributes a{};
     if (cudaPointerGetAttributes(&a, p) != cudaSuccess) cudaGetLastError();
     const bool dm = a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged;
@@ -82,7 +85,10 @@ struct Call {
     CUdeviceptr base = 0;
     size_t n = 0;
     const auto range = address_range();
-    if (range && range(&base, &n, static_cast<CUdeviceptr>(at)) == CUDA_SUCCESS) lo = base, size = n;
+    if (range && range(&base, &n, static_cast<CUdeviceptr>(at)) == CUDA_SUCCESS) {
+      lo[n_ranges % kRanges] = base;
+      size[n_ranges++ % kRanges] = n;
+    }
     return true;
   }
   bool need(bool ok, int code, const char* fmt, const char* a = "", long long b = 0) {

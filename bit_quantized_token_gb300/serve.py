@@ -31,13 +31,24 @@ def _kind(t, name: str) -> int:
     return d
 
 
-def _heads(t, name: str, dtype, shape: tuple):
+def _heads(t, name: str, dtype, shape):
     """Address and strides of a [token, head, head_dim] tensor."""
     s0, s1, s2 = t.stride()
     if t.dtype is not dtype or t.shape != shape or s2 != 1:
-        _fail(f"{name}: {str(dtype).rpartition('.')[2]} of shape {shape} with contiguous heads is needed, not {_name(t)} "
-              f"{tuple(t.shape)}")
+        _fail(f"{name}: {str(dtype).rpartition('.')[2]} of shape {tuple(shape)} with contiguous heads is needed, not "
+              f"{_name(t)} {tuple(t.shape)}")
     return t.data_ptr(), s0, s1
+
+
+def _row(t, name: str, dtype, n: int) -> int:
+    """Address of a contiguous tensor of n values of this type."""
+    if t is not None and t.dtype is dtype and t.shape == (n,) and (n == 1 or t.stride(0) == 1):
+        return t.data_ptr()
+    return _flat(t, name, dtype, (n,))  # (says what is wrong)
+
+
+def _opt(t, name: str, dtype, n: int) -> int:
+    return 0 if t is None else _row(t, name, dtype, n)
 
 
 def append_kv(k, v, cache: KVView, seqs, rows, *, q=None, q_out=None, positions=None, rope_theta: float | None = None,
@@ -46,32 +57,35 @@ def append_kv(k, v, cache: KVView, seqs, rows, *, q=None, q_out=None, positions=
     by positions (None: rows); q [token, head, head_dim] likewise to q_out (may be q). rope_theta None: no rotation;
     see llm_append_kv."""
     L = _load()
-    dt = k.dtype
+    dt, shape = k.dtype, k.shape
     kind = out_kind = _kind(k, "k")
-    T, H, hd = k.shape
+    T, H, hd = shape
     if cache.shape[2] != H or cache.shape[4] != hd:
         _fail(f"k has {H} heads x {hd}, the cache {cache.shape[2]} x {cache.shape[4]}")
-    kp, k0, k1 = _heads(k, "k", dt, (T, H, hd))
-    vp, v0, v1 = _heads(v, "v", dt, (T, H, hd))
+    kp, k0, k1 = _heads(k, "k", dt, shape)
+    vp, v0, v1 = _heads(v, "v", dt, shape)
     Hq = qp = q0 = q1 = op = o0 = o1 = 0
     if q is not None:
-        Hq = q.shape[1]
-        qp, q0, q1 = _heads(q, "q", dt, (T, Hq, hd))
+        of_q = q.shape
+        Hq = of_q[1]
+        if of_q[0] != T or of_q[2] != hd:
+            of_q = (T, Hq, hd)
+        qp, q0, q1 = _heads(q, "q", dt, of_q)
         if q_out is None:
             _fail("q needs q_out")
         out_kind = _kind(q_out, "q_out")
-        op, o0, o1 = _heads(q_out, "q_out", q_out.dtype, (T, Hq, hd))
+        op, o0, o1 = _heads(q_out, "q_out", q_out.dtype, of_q)
     elif q_out is not None:
         _fail("q_out needs q")
-    if rope_theta is not None and not rope_theta > 0:
+    if rope_theta is None:
+        rope_theta = 0.0
+    elif not rope_theta > 0:
         _fail("rope_theta is not positive (None: no rotation)")
+    i32, f32 = _t._i32, _t._f32
     rc = L.llm_append_kv(
         _APPEND(kind, out_kind, T, Hq, qp, kp, vp, op, q0, q1, k0, k1, v0, v1, o0, o1, cache._at,
-                _flat(seqs, "seqs", _t._i32, (T,)), _flat(rows, "rows", _t._i32, (T,)),
-                0 if positions is None else _flat(positions, "positions", _t._i32, (T,)),
-                0 if q_norm is None else _flat(q_norm, "q_norm", _t._f32, (hd,)),
-                0 if k_norm is None else _flat(k_norm, "k_norm", _t._f32, (hd,)), eps,
-                0.0 if rope_theta is None else rope_theta, rope_neox), stream)
+                _row(seqs, "seqs", i32, T), _row(rows, "rows", i32, T), _opt(positions, "positions", i32, T),
+                _opt(q_norm, "q_norm", f32, hd), _opt(k_norm, "k_norm", f32, hd), eps, rope_theta, rope_neox), stream)
     if rc:
         _check(rc)
 
@@ -83,15 +97,15 @@ def read_kv(cache: KVView, seqs, rows, k, v, stream: int | None = None) -> None:
     kind = _kind(k, "k")
     _, layers, H, _, hd = cache.shape
     shape, stride = k.shape, k.stride()
-    if v.shape != shape or v.stride() != stride or v.dtype is not k.dtype:
+    if v.dtype is not k.dtype or v.shape != shape or v.stride() != stride:
         _fail("k and v differ in shape, strides or type")
     if len(shape) == 3 and layers == 1:
         shape, stride = (1, *shape), (0, *stride)
     if len(shape) != 4 or shape[0] != layers or shape[2] != H or shape[3] != hd or stride[3] != 1:
         _fail(f"k: shape ({layers}, tokens, {H}, {hd}) with contiguous heads is needed, not {tuple(k.shape)}")
-    T = shape[1]
-    rc = L.llm_read_kv(cache._at, T, _flat(seqs, "seqs", _t._i32, (T,)), _flat(rows, "rows", _t._i32, (T,)), kind,
-                       k.data_ptr(), v.data_ptr(), _STRIDES(*stride[:3]), stream)
+    T, i32 = shape[1], _t._i32
+    rc = L.llm_read_kv(cache._at, T, _row(seqs, "seqs", i32, T), _row(rows, "rows", i32, T), kind, k.data_ptr(),
+                       v.data_ptr(), _STRIDES(*stride[:3]), stream)
     if rc:
         _check(rc)
 
@@ -125,14 +139,13 @@ def prefix_attention(q, prefix: KVView, starts, prefix_lens, cache: KVView, tree
     G = prefix_lens.shape[0]
     if not workspace.is_contiguous():
         _fail("the workspace is not contiguous")
+    i32 = _t._i32
     rc = L.llm_prefix_attention(
         _PREFIX(kind, B, n, H, q.data_ptr(), out.data_ptr(), q0, q1, q2, o0, o1, o2, cache._at,
-                0 if tree is None else tree._at, _flat(lens, "lens", _t._i32, (B,)),
-                0 if tree is None else _flat(mask, "mask", _t._i64, (B, n)),
-                0 if counts is None else _flat(counts, "counts", _t._i32, (B,)), hd ** -0.5 if scale is None else scale,
-                prefix._at, G, _flat(starts, "starts", _t._i32, (G + 1,)),
-                _flat(prefix_lens, "prefix_lens", _t._i32, (G,)), workspace.data_ptr(),
-                workspace.numel() * workspace.element_size()), stream)
+                0 if tree is None else tree._at, _row(lens, "lens", i32, B),
+                0 if tree is None else _flat(mask, "mask", _t._i64, (B, n)), _opt(counts, "counts", i32, B),
+                hd ** -0.5 if scale is None else scale, prefix._at, G, _row(starts, "starts", i32, G + 1),
+                _row(prefix_lens, "prefix_lens", i32, G), workspace.data_ptr(), workspace.nbytes), stream)
     if rc:
         _check(rc)
 
@@ -147,13 +160,10 @@ def sample_tokens(logits, uniforms, tokens, temperature=None, top_k=None, top_p=
     s0, s1 = logits.stride()
     if logits.dtype is not _t._f32 or (V > 1 and s1 != 1):
         _fail("logits: float32 with contiguous rows is needed")
-    shape, f32, i32 = (R,), _t._f32, _t._i32
+    f32, i32 = _t._f32, _t._i32
     rc = L.llm_sample_tokens(
-        _SAMPLE(logits.data_ptr(), s0, R, V, _flat(uniforms, "uniforms", f32, shape),
-                0 if temperature is None else _flat(temperature, "temperature", f32, shape),
-                0 if top_k is None else _flat(top_k, "top_k", i32, shape),
-                0 if top_p is None else _flat(top_p, "top_p", f32, shape),
-                0 if min_p is None else _flat(min_p, "min_p", f32, shape), _flat(tokens, "tokens", i32, shape),
-                0 if probs is None else _flat(probs, "probs", f32, shape)), stream)
+        _SAMPLE(logits.data_ptr(), s0, R, V, _row(uniforms, "uniforms", f32, R), _opt(temperature, "temperature", f32, R),
+                _opt(top_k, "top_k", i32, R), _opt(top_p, "top_p", f32, R), _opt(min_p, "min_p", f32, R),
+                _row(tokens, "tokens", i32, R), _opt(probs, "probs", f32, R)), stream)
     if rc:
         _check(rc)

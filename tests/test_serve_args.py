@@ -10,11 +10,12 @@ F32, BF16, I32 = torch.float32, torch.bfloat16, torch.int32
 
 
 class Fake(_Fake):
-    def numel(self):
-        return self.shape.numel()
+    @property
+    def nbytes(self):
+        return self.shape.numel() * self.dtype.itemsize
 
-    def element_size(self):
-        return self.dtype.itemsize
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
 
 
 @pytest.fixture(scope="module", autouse=True)
