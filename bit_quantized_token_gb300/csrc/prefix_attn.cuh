@@ -38,7 +38,7 @@ struct Wide {
   static constexpr int kMmaWarp = 8, kTmaWarp = 12, NT = 416;
   static constexpr int kTile = 128 * HD * 2, kUnit = 128 * 128;  // bytes of 128 rows of Q, K or V; of 64 dims of them
   static constexpr int NST = HD == 64 ? 8 : 4;                   // K and V tiles in flight
-  static constexpr int kOffCum = 512, kSmall = kOffCum + 4 * (kWideGroups + 1);
+  static constexpr int kOffCum = 512, kOffGroup = kOffCum + 4 * (kWideGroups + 4), kSmall = kOffGroup + 12 * kWideGroups;
   static constexpr int kSmem = 2 * kTile + NST * kTile + kSmall + 1024;
   // more than half of an SM's: no CTA that holds tensor memory shares the SM (this one takes all of it)
   static_assert(kSmem > 140000 && kSmem <= 232448, "shared memory");
@@ -74,25 +74,39 @@ struct WideSegment {
   int g, hkv, row0, rows, k0, k1, len;  // group; rows row0 .. of the group; key tiles k0 .. k1 - 1 of the prefix's len rows
   int first, piece, pieces;             // the group's first sequence; which piece of the row tile, of how many
 };
+struct WideGroup {
+  int first, rows, len;  // its first sequence, query rows of a kv head, prefix rows
+  __device__ int key_tiles() const { return (len + 127) / 128; }
+  __device__ int row_tiles() const { return (rows + kWideRows - 1) / kWideRows; }
+};
+__device__ __forceinline__ WideGroup wide_group(const TreeAttnParams& p, int g) {
+  WideGroup x;
+  x.first = min(max(p.starts[g], 0), p.all);
+  x.rows = (min(max(p.starts[g + 1], x.first), p.all) - x.first) * p.n * p.gq;
+  x.len = min(max(p.lens[g], 0), p.cache.rows);
+  return x;
+}
 struct WidePlan {
   const TreeAttnParams& p;
-  const uint32_t* cum;  // [G + 1] units before a group
+  const uint32_t* cum;      // [G + 1] units before a group
+  const WideGroup* groups;  // [G]
   bool whole;
-  int64_t U, N, pos, end;
-  __device__ WidePlan(const TreeAttnParams& p_, const uint32_t* cum_, bool whole_, int kt_max) : p(p_), cum(cum_), whole(whole_) {
+  uint32_t U, N, pos, end;
+  // a b / c, of 32 bits; a 64-bit quotient takes some hundred cycles
+  __device__ static uint32_t muldiv(uint32_t a, uint32_t b, uint32_t c) {
+    return __umulhi(a, b) ? (uint32_t)((uint64_t)a * b / c) : a * b / c;
+  }
+  __device__ WidePlan(const TreeAttnParams& p_, const uint32_t* cum_, const WideGroup* groups_, bool whole_, int kt_max)
+      : p(p_), cum(cum_), groups(groups_), whole(whole_) {
     U = cum[p.B];
-    N = min((int64_t)gridDim.x, U);
-    if (!whole && U > 0) N = max(min(N, U * (p.max_parts - 2) / kt_max), (int64_t)1);  // no row tile in more pieces
-    pos = (int)blockIdx.x < N ? U * blockIdx.x / N : 0;
-    end = (int)blockIdx.x < N ? U * (blockIdx.x + 1) / N : 0;
+    N = min(gridDim.x, U);
+    if (!whole && U > 0) N = max((uint32_t)min((uint64_t)N, (uint64_t)U * (p.max_parts - 2) / kt_max), 1u);  // no row tile in more pieces
+    pos = blockIdx.x < N ? muldiv(U, blockIdx.x, N) : 0;
+    end = blockIdx.x < N ? muldiv(U, blockIdx.x + 1, N) : 0;
   }
-  __device__ static int tiles(const TreeAttnParams& p, int g, int& first, int& rows, int& len) {
-    first = min(max(p.starts[g], 0), p.all);
-    rows = (min(max(p.starts[g + 1], first), p.all) - first) * p.n * p.gq;
-    len = min(max(p.lens[g], 0), p.cache.rows);
-    return (len + 127) / 128;
+  __device__ int cta_of(uint32_t u) const {  // ((u + 1) N - 1) / U
+    return __umulhi(u + 1, N) ? (int)(((uint64_t)(u + 1) * N - 1) / U) : (int)(((u + 1) * N - 1) / U);
   }
-  __device__ int cta_of(int64_t u) const { return (int)(((u + 1) * N - 1) / U); }
   __device__ bool next(WideSegment& s) {
     if (pos >= end) return false;
     int lo = 0, hi = p.B - 1;  // the last group that starts at or before pos and is not empty
@@ -101,16 +115,15 @@ struct WidePlan {
       if (cum[mid] <= pos) lo = mid;
       else hi = mid - 1;
     }
-    s.g = lo;
-    int rows;
-    const int kt = tiles(p, lo, s.first, rows, s.len), rt = (rows + kWideRows - 1) / kWideRows, per = whole ? 1 : kt;
-    const int off = (int)(pos - cum[lo]), q = off / per;
+    const WideGroup x = groups[lo];
+    const uint32_t kt = x.key_tiles(), rt = x.row_tiles(), per = whole ? 1 : kt, off = pos - cum[lo], q = off / per;
+    s.g = lo, s.first = x.first, s.len = x.len;
     s.hkv = q / rt;
     s.row0 = (q - s.hkv * rt) * kWideRows;
-    s.rows = min(rows - s.row0, kWideRows);
-    const int64_t start = (int64_t)cum[lo] + (int64_t)q * per;
+    s.rows = min(x.rows - s.row0, kWideRows);
+    const uint32_t start = cum[lo] + q * per;
     s.k0 = whole ? 0 : off - q * kt;
-    s.k1 = whole ? kt : (int)min((int64_t)kt, s.k0 + end - pos);
+    s.k1 = whole ? kt : min(kt, s.k0 + end - pos);
     s.piece = whole ? 0 : (int)blockIdx.x - cta_of(start);
     s.pieces = whole ? 1 : cta_of(start + kt - 1) - cta_of(start) + 1;
     pos += whole ? 1 : s.k1 - s.k0;
@@ -137,6 +150,7 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
   int* s_kt = reinterpret_cast<int*>(small + 356);   // most key tiles of a group
   int* s_none = reinterpret_cast<int*>(small + 360);  // a group without prefix rows
   uint32_t* cum = reinterpret_cast<uint32_t*>(small + C::kOffCum);
+  WideGroup* groups = reinterpret_cast<WideGroup*>(small + C::kOffGroup);
   if (tid == 0) {
     s_abort[0] = 0, s_abort[kLimitAt] = p.wait.ns;
     for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 2);
@@ -156,12 +170,12 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     int most = 1;
     bool none = false;
     for (int g0 = 0; g0 < p.B; g0 += 32) {
-      int first, rows = 0, len, kt = 0;
-      if (g0 + lane < p.B) kt = WidePlan::tiles(p, g0 + lane, first, rows, len);
-      const int rt = (rows + kWideRows - 1) / kWideRows;
-      uint32_t u = kt > 0 ? (uint32_t)rt * (wp.whole ? 1 : kt) * p.Hkv : 0u, x = u;
+      WideGroup own{0, 0, 0};
+      if (g0 + lane < p.B) groups[g0 + lane] = own = wide_group(p, g0 + lane);
+      const int kt = own.key_tiles();
+      uint32_t u = kt > 0 ? (uint32_t)own.row_tiles() * (wp.whole ? 1 : kt) * p.Hkv : 0u, x = u;
       if (u) most = max(most, kt);
-      none |= rows > 0 && kt == 0;
+      none |= own.rows > 0 && kt == 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -180,12 +194,12 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
   const uint32_t tmem = *s_tmem;
   if (*s_none)
     for (int g = 0; g < p.B; ++g) {
-      int first, rows, len;
-      if (WidePlan::tiles(p, g, first, rows, len) == 0)
-        for (int i = blockIdx.x * C::NT + tid; i < rows * p.Hkv; i += gridDim.x * C::NT)
-          p.part_n[(int64_t)first * p.n * p.Hkv * p.gq + i] = 0;
+      const WideGroup x = groups[g];
+      if (x.len == 0)
+        for (int i = blockIdx.x * C::NT + tid; i < x.rows * p.Hkv; i += gridDim.x * C::NT)
+          p.part_n[(int64_t)x.first * p.n * p.Hkv * p.gq + i] = 0;
     }
-  WidePlan plan(p, cum, wp.whole, *s_kt);
+  WidePlan plan(p, cum, groups, wp.whole, *s_kt);
   WideSegment seg{};
   uint32_t base = 0;  // K and V tiles of the segments before
   // The ring's order in a segment of n tiles: K0 K1 V0 K2 V1 ..

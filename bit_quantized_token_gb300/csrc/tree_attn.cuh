@@ -1033,6 +1033,12 @@ int lone_splits(int64_t clusters, int tiles, AtOnce at_once) {
   return best;
 }
 
+// Clusters of a launch (but for their splits) that have rows. Of groups that share the sequences, most blocks of
+// the grid have none: it is as wide as if any one of them had all.
+inline int64_t busy_clusters(const TreeAttnParams& p, int m_tiles) {
+  return (int64_t)p.Hkv * (p.part == TreeAttnParams::kFirst ? m_tiles + p.B - 1 : (int64_t)p.B * m_tiles);
+}
+
 template <int HD, bool F32, int NB, int G>
 cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   using C = TreeTc<HD, F32, NB, G>;
@@ -1042,7 +1048,7 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   TreeAttnParams& p = tp.p;
   const int m_tiles = (p.nodes * p.gq + C::N - 1) / C::N;
-  const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
+  const int64_t clusters = busy_clusters(p, m_tiles);
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
   int S = 1;
   if constexpr (C::two) {
@@ -1076,7 +1082,7 @@ cudaError_t launch_tree_tc(const TreeAttnParams& p, bool f32, int n_sm, cudaStre
   const int M = p.nodes * p.gq, most = f32 ? 32 : 128;
   int N = 16;
   while (N < M && N < most) N *= 2;
-  while (N > 16 && (int64_t)p.B * p.Hkv * ((M + N - 1) / N) * 8 < n_sm) N /= 2;
+  while (N > 16 && busy_clusters(p, (M + N - 1) / N) * 8 < n_sm) N /= 2;
   if (f32)
     return N == 16 ? launch_tree_tc_t<HD, true, 16, 1>(tp, n_sm, st) : launch_tree_tc_t<HD, true, 16, 2>(tp, n_sm, st);
   return N == 16   ? launch_tree_tc_t<HD, false, 16, 1>(tp, n_sm, st)

@@ -686,7 +686,7 @@ cudaError_t launch_tree_q8_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   TreeAttnParams& p = tp.p;
   const int m_tiles = (p.nodes * p.gq + C::N - 1) / C::N;
-  const int64_t clusters = (int64_t)p.B * p.Hkv * m_tiles;
+  const int64_t clusters = busy_clusters(p, m_tiles);
   const int tiles = (p.cache.rows + C::BK - 1) / C::BK + 1;
   static ClusterCount at_once;
   p.S = lone_splits(clusters, tiles, [&](int S) { return at_once.get(kern, S, C::NT, C::kSmem); });
