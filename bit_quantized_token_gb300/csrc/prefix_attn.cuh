@@ -37,9 +37,9 @@ struct Wide {
   static constexpr int NBUF = HD == 64 ? 3 : 2;                   // blocks of scores of a row tile
   static constexpr int kMmaWarp = 8, kTmaWarp = 12, NT = 416;
   static constexpr int kTile = 128 * HD * 2, kUnit = 128 * 128;  // bytes of 128 rows of Q, K or V; of 64 dims of them
-  static constexpr int NST = HD == 64 ? 8 : 4;                   // K and V tiles in flight
+  static constexpr int NST = HD == 64 ? 4 : 2;                   // K tiles in flight, and V tiles
   static constexpr int kOffCum = 512, kOffGroup = kOffCum + 4 * (kWideGroups + 4), kSmall = kOffGroup + 12 * kWideGroups;
-  static constexpr int kSmem = 2 * kTile + NST * kTile + kSmall + 1024;
+  static constexpr int kSmem = 2 * kTile + 2 * NST * kTile + kSmall + 1024;
   // more than half of an SM's: no CTA that holds tensor memory shares the SM (this one takes all of it)
   static_assert(kSmem > 140000 && kSmem <= 232448, "shared memory");
   static constexpr int kAtO = 2 * NBUF * KB;                      // columns: S of tile t, buffer x at (t NBUF + x) KB; then O
@@ -140,11 +140,11 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
   uint8_t* sq = sm;                       // [2][H][128 rows][128 B]
-  uint8_t* sring = sq + 2 * C::kTile;     // [NST][H][128 keys][128 B]
-  uint8_t* small = sring + NST * C::kTile;
+  uint8_t* sring = sq + 2 * C::kTile;     // [K, V][NST][H][128 keys][128 B]
+  uint8_t* small = sring + 2 * NST * C::kTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(small);
   uint64_t *full = bars, *empty = bars + 8, *q_full = bars + 16, *s_full = bars + 18, *p_full = bars + 24, *o_done = bars + 30,
-           *drain = bars + 36;  // [NST], [NST], [2], then [2][3]
+           *drain = bars + 36;  // [K, V][4], [K, V][4], [2], then [2][3]
   volatile int* s_abort = reinterpret_cast<volatile int*>(small + 304);  // (12 ints: see tc_wait_long)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(small + 352);
   int* s_kt = reinterpret_cast<int*>(small + 356);   // most key tiles of a group
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
   WideGroup* groups = reinterpret_cast<WideGroup*>(small + C::kOffGroup);
   if (tid == 0) {
     s_abort[0] = 0, s_abort[kLimitAt] = p.wait.ns;
-    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 2);
+    for (int i = 0; i < 8; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 2);
     for (int i = 0; i < 2; ++i) mbar_init(q_full + i, 128);
     for (int i = 0; i < 6; ++i)
       mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 + p.wait.missing), mbar_init(o_done + i, 1);
@@ -201,32 +201,33 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     }
   WidePlan plan(p, cum, groups, wp.whole, *s_kt);
   WideSegment seg{};
-  uint32_t base = 0;  // K and V tiles of the segments before
-  // The ring's order in a segment of n tiles: K0 K1 V0 K2 V1 ..
-  auto k_at = [&](int t) { return base + (t == 0 ? 0 : 2 * t - 1); };
-  auto v_at = [&](int t, int n) { return base + (t == n - 1 ? 2 * t + 1 : 2 * t + 2); };
+  // Key tiles are counted over all segments. K and V have rings of their own: a warp
+  // that waits for some tiles of a ring waits for all of them, in order, since a wait for a
+  // phase whose predecessor is not over is over at once.
+  uint32_t base = 0;  // key tiles of the segments before
+  auto landed = [&](int kv, uint32_t i) { return tc_wait_warp(full + 4 * kv + i % NST, (i / NST) & 1, s_abort, p.status); };
   auto blocks = [&]() { return min(2 * (seg.k1 - seg.k0), (seg.len - seg.k0 * BK + KB - 1) / KB); };
-  uint32_t sent = 0;
+  uint32_t sent[2] = {0, 0};  // by the TMA lane
   if (warp == C::kTmaWarp) {
     if (lane == 0) {
       bool ok = true;
       while (ok && plan.next(seg)) {
         const int n = seg.k1 - seg.k0;
 #pragma unroll 1
-        for (int j = 0; j < 2 * n && ok; ++j) {
-          const bool val = j > 0 && (!(j & 1) || j == 2 * n - 1);
-          const int t = seg.k0 + (j == 2 * n - 1 ? n - 1 : val ? j / 2 - 1 : (j + 1) / 2);
-          const uint32_t i = base + j, slot = i % NST;
-          if (i >= (uint32_t)NST) ok = tc_wait(empty + slot, (i / NST - 1) & 1, s_abort, p.status);
+        for (int j = 0; j < 2 * n && ok; ++j) {  // K0 K1 V0 K2 V1 .. V
+          const int kv = j > 0 && (!(j & 1) || j == 2 * n - 1), k = j == 2 * n - 1 ? n - 1 : kv ? j / 2 - 1 : (j + 1) / 2;
+          const uint32_t i = base + k, slot = i % NST;
+          uint64_t* bar = full + 4 * kv + slot;
+          if (i >= (uint32_t)NST) ok = tc_wait(empty + 4 * kv + slot, (i / NST - 1) & 1, s_abort, p.status);
           if (!ok) break;
-          mbar_expect_tx(full + slot, C::kTile);
+          mbar_expect_tx(bar, C::kTile);
 #pragma unroll
           for (int u = 0; u < H; ++u)
-            tma_box(sring + slot * C::kTile + u * C::kUnit, val ? &wp.v : &wp.k, 64 * u, t * BK, seg.hkv * wp.head, seg.g * wp.seq,
-                    full + slot);
-          sent = i + 1;
+            tma_box(sring + (kv * NST + slot) * C::kTile + u * C::kUnit, kv ? &wp.v : &wp.k, 64 * u, (seg.k0 + k) * BK,
+                    seg.hkv * wp.head, seg.g * wp.seq, bar);
+          sent[kv] = i + 1;
         }
-        base += 2 * n;
+        base += n;
       }
     }
   } else if (warp >= C::kMmaWarp) {
@@ -236,22 +237,20 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     constexpr uint32_t idesc_o = base_i | ((uint32_t)(HD >> 3) << 17) | (1u << 16);  // V is MN-major
     const int t = warp & 1;
     const bool values = warp >= C::kMmaWarp + 2;
-    const uint32_t ur = smem_u32(sring), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t ur = smem_u32(sring) + (values ? NST * C::kTile : 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t tS = tm + t * NBUF * KB, tO = tm + C::kAtO + t * HD;
     const uint64_t da = tc_desc(smem_u32(sq) + t * C::kTile, 16, 1024, 2);
     bool ok = true;
     uint32_t n_seg = 0, done = 0;  // segments, blocks so far
-    const auto landed = [&](uint32_t i) { return tc_wait_warp(full + i % NST, (i / NST) & 1, s_abort, p.status); };
     while (ok && plan.next(seg)) {
       const int n = seg.k1 - seg.k0, nb = blocks();
       if (t * 128 >= seg.rows) {  // no rows: the tiles are given back as they come
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j) {
-          const uint32_t i = values ? v_at(j, n) : k_at(j);
-          ok = landed(i);
-          if (ok && lane == 0) mbar_arrive(empty + i % NST);
+          ok = landed(values, base + j);
+          if (ok && lane == 0) mbar_arrive(empty + 4 * values + (base + j) % NST);
         }
-        base += 2 * n;
+        base += n;
         continue;
       }
       if (!values) {
@@ -259,8 +258,8 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         ++n_seg;
 #pragma unroll 1
         for (int j = 0; j < nb && ok; ++j) {
-          const uint32_t b = done + j, x = b % NBUF, i = k_at(j >> 1), slot = i % NST;
-          if (!(j & 1)) ok = landed(i);
+          const uint32_t b = done + j, x = b % NBUF, i = base + (j >> 1), slot = i % NST;
+          if (!(j & 1)) ok = landed(0, i);
           // into the buffer of the block NBUF before: its P V is done (of the segment before, all are)
           if (j >= NBUF) ok = ok && tc_wait_warp(o_done + 3 * t + x, (b / NBUF - 1) & 1, s_abort, p.status);
           if (!ok) break;
@@ -280,8 +279,8 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
       } else {
 #pragma unroll 1
         for (int j = 0; j < nb && ok; ++j) {
-          const uint32_t b = done + j, x = b % NBUF, i = v_at(j >> 1, n), slot = i % NST;
-          if (!(j & 1)) ok = landed(i);
+          const uint32_t b = done + j, x = b % NBUF, i = base + (j >> 1), slot = i % NST;
+          if (!(j & 1)) ok = landed(1, i);
           ok = ok && tc_wait_warp(p_full + 3 * t + x, (b / NBUF) & 1, s_abort, p.status);
           if (!ok) break;
           tc_fence_after();
@@ -293,11 +292,11 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
           }
           __syncwarp();
           tc_commit(o_done + 3 * t + x);
-          if ((j & 1) || j == nb - 1) tc_commit(empty + slot);
+          if ((j & 1) || j == nb - 1) tc_commit(empty + 4 + slot);
         }
       }
       done += nb;
-      base += 2 * n;
+      base += n;
     }
   } else {
     // ---- softmax: thread = row of tile t
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     while (ok && plan.next(seg)) {
       const int n = seg.k1 - seg.k0, nb = blocks();
       if (t * 128 >= seg.rows) {
-        base += 2 * n;
+        base += n;
         continue;
       }
       const int row = seg.row0 + t * 128 + r, node = p.by_gq.div(row), h = seg.hkv * p.gq + row - node * p.gq;
@@ -406,13 +405,14 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         if (!ok) break;
         l += sum;
         if (left < KB) {  // V rows that are not there become zeros: 0 times whatever lies there need not be 0
-          const uint32_t iv = v_at(j >> 1, n), slot = iv % NST;
-          ok = tc_wait_warp(full + slot, (iv / NST) & 1, s_abort, p.status);
+          // (V of NST tiles before is there: these scores were made behind a P V of it, or of a later tile)
+          const uint32_t iv = base + (j >> 1), slot = iv % NST;
+          ok = landed(1, iv);
           if (!ok) break;
 #pragma unroll 1
           for (int c = r; c < (KB - left) * (HD / 8); c += 128) {
             const int row_v = (j & 1) * KB + left + c / (HD / 8), ch = c % (HD / 8);
-            *reinterpret_cast<uint4*>(sring + slot * C::kTile + (ch / 8) * C::kUnit + row_v * 128 + 16 * (ch & 7)) =
+            *reinterpret_cast<uint4*>(sring + (NST + slot) * C::kTile + (ch / 8) * C::kUnit + row_v * 128 + 16 * (ch & 7)) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
           fence_async_smem();
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         if (seg.piece == 0) p.part_n[at] = seg.pieces;
       }
       tc_fence_before();
-      base += 2 * n;
+      base += n;
     }
   }
   __syncwarp();
@@ -456,9 +456,11 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     const unsigned long long s0 = globaltimer();
     if (warp == C::kTmaWarp && lane == 0)
 #pragma unroll 1
-      for (uint32_t j = sent > (uint32_t)NST ? sent - NST : 0; j < sent; ++j)
-        while (!mbar_try_wait(full + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
-        }
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll 1
+        for (uint32_t j = sent[kv] > (uint32_t)NST ? sent[kv] - NST : 0; j < sent[kv]; ++j)
+          while (!mbar_try_wait(full + 4 * kv + j % NST, (j / NST) & 1) && globaltimer() - s0 < kWaitLimitNs) {
+          }
     __syncwarp();
     if (warp >= C::kMmaWarp && warp < C::kTmaWarp) {
       tc_commit(drain);  // of a warp's own products

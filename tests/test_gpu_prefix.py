@@ -225,6 +225,23 @@ def test_captured_and_repeated():
     p.check()
 
 
+@pytest.mark.parametrize("starts,gq,hd", [((0, 64), 2, 128), ((0, 64), 2, 64), ((0, 30, 90, 154, 300), 1, 128), ((0, 257), 4, 64)])
+def test_many_calls_in_a_row(starts, gq, hd):
+    """The same bits from every one of 300 calls behind one another, row tiles without rows among them, and no wait that
+    runs out."""
+    p = Problem(starts=starts, gq=gq, hd=hd, Hkv=8, P=2100, plens=(2100, 130, 1999), own=20, lens=(7, 20), tree=False)
+    p.call()
+    p.check()
+    first = p.out.clone()
+    outs = [torch.empty_like(p.out) for _ in range(3)]
+    for i in range(300):
+        p.out = outs[i % 3]
+        p.call()
+        if i % 3 == 2:
+            assert all(torch.equal(o, first) for o in outs), i
+    bq.tree_status()
+
+
 def test_a_step_of_a_served_batch():
     """Append, then attend with the appended row as the last own row, on one stream without waits between them."""
     g = torch.Generator("cuda")
