@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
   } else if (warp == 4 * G + 1) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 128 * G + p.wait.missing);
-      mbar_init(o_done, 1);
+      mbar_init(o_done, 1), mbar_init(o_done + 1, 1);
       mbar_init(drain, 1);
       mbar_fence_init();
     }
@@ -575,6 +575,11 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     const int n = t0 + t >= n_pre ? 64 - __clzll((long long)seen) : min(BK, len - (t0 + t) * BK);
     return max(1, (n + 15) / 16);
   };
+
+  // P V of own tile t. With two buffers a barrier for each: a wait for the last but one, once it has handed
+  // over the last one's P, would otherwise come too late when both are over, and see the phase behind them.
+  auto pv_bar = [&](int t) { return o_done + (DB == 2 ? t & 1 : 0); };
+  auto pv_parity = [&](int t) { return (uint32_t)(DB == 2 ? t >> 1 : t) & 1; };
 
   int sent = min(NST, n_units);  // by the TMA lane
   if (warp == 4 * G) {
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
             __syncwarp();
             tc_commit(empty + slot);
           }
-          if (ok) tc_commit(o_done);
+          if (ok) tc_commit(o_done + x);
         }
       }
     }
@@ -771,7 +776,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
               top = max_bf16x2(top, max_bf16x2(part[h][j / 2][0], part[h][j / 2 + 1][0]));
             }
           // one buffer of P: the last P V has read it (with two, that of this buffer came before these scores)
-          if (DB == 1 && c0 == 0 && t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+          if (DB == 1 && c0 == 0 && t > t0) tc_wait(pv_bar(t - t0 - 1), pv_parity(t - t0 - 1), s_abort, p.status);
 #pragma unroll
           for (int h = 0; h < W / 8; ++h)
 #pragma unroll
@@ -822,7 +827,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         }
         group_sync(g);
         if (t > t0) {
-          tc_wait_together(o_done, (t - t0 - 1) & 1, s_abort, p.status);  // the last P V is in O
+          tc_wait_together(pv_bar(t - t0 - 1), pv_parity(t - t0 - 1), s_abort, p.status);  // the last P V is in O
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < C::NO * H; c0 += 16) {
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       }
       if constexpr (F32) {
         if (t > t0 && (t - t0) % kTogether == 0) {  // the next P V starts anew
-          tc_wait_together(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+          tc_wait_together(pv_bar(t - t0 - 1), pv_parity(t - t0 - 1), s_abort, p.status);
           tc_fence_after();
 #pragma unroll
           for (int u = 0; u < H; ++u) {
@@ -859,7 +864,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
         // V rows that are not there become zeros, non-finite tree values too (noted for the
         // rows that see them), in the steps that are multiplied. After the last P V, so that
         // the slot's last unit has been read and its barrier is in this unit's phase.
-        if (t > t0) tc_wait(o_done, (t - t0 - 1) & 1, s_abort, p.status);
+        if (t > t0) tc_wait(pv_bar(t - t0 - 1), pv_parity(t - t0 - 1), s_abort, p.status);
         for (int u = 0; u < H; ++u) {
           const int i = v_unit(t - t0) + u;
           tc_wait(full + i % NST, (i / NST) & 1, s_abort, p.status);
@@ -899,9 +904,7 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     }
   stopped:
     // ---- O^T and the sums to shared memory, [row][dim]
-    // (one phase at a time: with two buffers the last but one P V may still run)
-    if (DB == 2 && n_own > 1) tc_wait_together(o_done, (n_own - 2) & 1, s_abort, p.status);
-    if (n_own > 0) tc_wait_together(o_done, (n_own - 1) & 1, s_abort, p.status);
+    if (n_own > 0) tc_wait_together(pv_bar(n_own - 1), pv_parity(n_own - 1), s_abort, p.status);
     tc_fence_after();
     // every block's last MMAs have read the ring and P before any block writes over them
     asm volatile("bar.sync %0, %1;" ::"r"(3), "n"(128 * G) : "memory");
