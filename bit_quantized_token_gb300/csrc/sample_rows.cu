@@ -14,10 +14,10 @@
 //      bucket's mass at most);
 //   3. a second pass brings their tokens, some hundreds, to the first CTA, which
 //      sorts them and finds all borders exactly.
-// A window that turns out too low, or too narrow, is set again from the row's exact
-// range. Rows that put more than kSampleList tokens into those buckets (all logits
-// alike, crowds of equal ones) take the long way: each border by three digits of the
-// logits' keys, over all tokens.
+// A window that turns out too low, or too narrow, or buckets that hold more than
+// kSampleList tokens around the borders (flat rows), are set again from the row's exact
+// range, once. Rows that still have more there (crowds of equal logits) take the long
+// way: each border by three digits of the logits' keys, over all tokens.
 //
 // Masses decide integers, so they are integers: a term is a number of 2^-34 steps
 // below its bucket's largest, from the exact product of logit and temperature in a
@@ -44,7 +44,7 @@ constexpr int kSampTable = 2 * kSampB; // a CTA's buckets, by their number modul
 constexpr int kSampPer = kSampB / kSampNT;
 constexpr int kSampMaxSlice = 180000;
 constexpr int kSampU = 8;               // loads of a thread in flight
-constexpr int kListPer = kSampleList / kSampNT;
+constexpr int kSortRegs = 4;            // entries of a thread that are sorted in registers
 
 __constant__ const u64 kRoot32[32] = {  // 2^(63 - j/32)
     0x8000000000000000ull, 0x7D41D96DB915019Dull, 0x7A92BE8A92436616ull, 0x77F25CCDEE6D7AE6ull,
@@ -188,7 +188,7 @@ __device__ __forceinline__ int first_at(F f) {
 // Entries e 512 + tid in v[e], sorted from the largest on (bitonic; n2, a power of two, from 32 on, or 512 E with
 // E > 1: those that are not 0). buf: room for 512 E.
 template <int E>
-__device__ __forceinline__ void sort_list(u64 (&v)[kListPer], u64* buf, int n2) {
+__device__ __forceinline__ void sort_list(u64 (&v)[kSortRegs], u64* buf, int n2) {
   const int tid = threadIdx.x;
 #pragma unroll 1
   for (int k = 2; k <= n2; k *= 2)
@@ -225,7 +225,222 @@ __device__ __forceinline__ void sort_list(u64 (&v)[kListPer], u64* buf, int n2) 
     }
 }
 
-__global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRowsParams p) {
+// The same for more, N of them, in shared memory (a function of its own: with eight entries a thread
+// the ordinary way's registers spilled, 2 us of every call).
+__device__ __noinline__ void sort_long(u64* list, const u64* in, int N) {
+  const int tid = threadIdx.x;
+#pragma unroll 1
+  for (int i = tid; i < kSampleList; i += kSampNT) list[i] = i < N ? in[i] : 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 2; k <= kSampleList; k *= 2)
+#pragma unroll 1
+    for (int j = k / 2; j > 0; j /= 2) {
+#pragma unroll 1
+      for (int i = tid; i < kSampleList / 2; i += kSampNT) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;  // pairs of places that differ in the bit j
+        const u64 x = list[lo], y = list[hi];
+        if ((x < y) == ((lo & k) == 0)) list[lo] = y, list[hi] = x;
+      }
+      __syncthreads();
+    }
+}
+
+// The long way: the borders of top_k (or all tokens), top_p and the draw in turn, each by
+// three digits of the keys from the top, over all tokens. m: the row's largest logit.
+// (A function of its own, so that the ordinary way has its registers to itself.)
+__device__ __noinline__ void sample_crowd(const SampleRowsParams& p, SampShared& s, float m) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = cl.num_blocks(), rank = cl.block_rank(), row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
+  const int first = rank * p.slice, n = max(min(p.V - first, p.slice), 0);
+  const float* src = p.logits + (int64_t)row * p.stride + first;
+  const float ch = s.ch, cl_ = s.cl;
+  const bool by_k = s.top_k > 0, by_p = s.p_fix != 0, by_m = s.by_m;
+  const u64 u_fix = __float2ull_rn(s.u * 18446744073709551616.f);
+  auto logit = [&](int i) {
+    const float l = i < n ? src[i] : -INFINITY;
+    return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
+  };
+  if (tid == 0) s.key = by_m ? (u64)(s.y_min * 137438953472.0) : 0ull;  // of 32 buckets an octave, from the largest logit
+  cl.sync();
+  const int bm = by_m ? (int)min(s.key >> 32, (u64)kSampB) : kSampB;
+  const uint32_t qm = (uint32_t)s.key;
+  uint32_t kept = 0;
+  u64 mass = 0;
+  uint32_t key = 0, above = 0, equal = 0;  // a border's key, tokens above it and of it
+  u64 mass_above = 0, each = 0;            // mass above it, and of one token of it
+#pragma unroll 1
+  for (int turn = 0; turn < 3; ++turn) {
+    if (turn == 1 && !by_p) continue;
+    if (turn == 0 ? !by_k : turn == 2 && by_m) {  // tokens and mass of all, or that min_p keeps
+      u64 a = 0;
+      uint32_t c = 0;
+#pragma unroll 1
+      for (int i0 = tid; i0 < n; i0 += 4 * kSampNT) {
+        float l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[e] = logit(i0 + e * kSampNT);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          Term t;
+          if (term_of(l[e], m, ch, cl_, t) && (turn == 0 || t.b < bm || (t.b == bm && t.q <= qm)))
+            a += weight_of(t, 0), ++c;
+        }
+      }
+      scan2(a, c, s);
+      if (tid == kSampNT - 1) s.list[0] = a, s.list[1] = c;
+      cl.sync();
+      a = 0, c = 0;
+      for (int k = 0; k < C; ++k) {
+        const u64* o = cl.map_shared_rank(s.list, k);
+        a += o[0], c += (uint32_t)o[1];
+      }
+      if (turn == 0 || c < kept) kept = c, mass = a;
+      cl.sync();
+      if (turn == 0) continue;
+    }
+    // found is where the count (turn 0) or the mass (1) reaches the target, or the mass passes it (2)
+    const u64 target = turn == 0 ? (u64)s.top_k : turn == 1 ? ceil_part(mass, s.p_fix) : __umul64hi(mass, u_fix);
+    auto over = [&](u64 m_, uint32_t n_) { return turn == 0 ? n_ >= target : turn == 1 ? m_ >= target : m_ > target; };
+    // A digit's bins are few and full (the highest one is the exponent), so a warp's terms of one bin are added
+    // first, for up to four bins
+    auto put = [&](bool in, uint32_t bin, u64 w) {
+      unsigned left = __ballot_sync(0xffffffffu, in);
+      auto add = [&](u64 w, uint32_t n_) {
+        const uint32_t lo32 = (uint32_t)w, old = atomicAdd(&s.h[0][bin], lo32);
+        atomicAdd(&s.h[1][bin], (uint32_t)(w >> 32) + (old + lo32 < old));
+        atomicAdd(&s.h[2][bin], n_);
+      };
+#pragma unroll 1
+      for (int r = 0; r < 4 && left; ++r) {
+        const int leader = __ffs(left) - 1;
+        const uint32_t one = __shfl_sync(0xffffffffu, bin, leader);
+        const unsigned same = __ballot_sync(0xffffffffu, in && bin == one);
+        const bool mine = in && bin == one;
+        const uint32_t lo = __reduce_add_sync(0xffffffffu, mine ? (uint32_t)w & 0x3FFFFFu : 0u);
+        const uint32_t hi = __reduce_add_sync(0xffffffffu, mine ? (uint32_t)(w >> 22) : 0u);  // (below 2^27)
+        if (lane == leader) add(((u64)hi << 22) + lo, __popc(same));
+        left &= ~same;
+      }
+      if (left >> lane & 1) add(w, 1u);
+    };
+    key = above = 0, mass_above = 0;
+#pragma unroll 1
+    for (int level = 0; level < 3; ++level) {
+      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bins = level == 2 ? 1024 : 2048;
+      const uint32_t prefix_mask = level == 0 ? 0u : level == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+      for (int i = tid; i < 3 * kSampB; i += kSampNT) (&s.h[0][0])[i] = 0;
+      if (tid == 0) s.found = -1;
+      __syncthreads();
+#pragma unroll 1
+      for (int i0 = tid; i0 - lane < n; i0 += 4 * kSampNT) {
+        float l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[e] = logit(i0 + e * kSampNT);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          Term t;
+          const uint32_t k = sample_key(l[e]);
+          const bool in = (k & prefix_mask) == key && term_of(l[e], m, ch, cl_, t);
+          const u64 w = in ? weight_of(t, 0) : 0;
+          put(in, (k >> shift) & (bins - 1), w);
+        }
+      }
+      cl.sync();
+      // a CTA adds up its share of the bins, in descending order, for all
+      const int share = bins / C;
+      for (int i = tid; i < share; i += kSampNT) {
+        const int j = rank * share + i, bin = bins - 1 - j;
+        u64 w = 0;
+        uint32_t c = 0;
+#pragma unroll 8
+        for (int k = 0; k < C; ++k) {
+          const uint32_t(*h)[kSampB] = cl.map_shared_rank(&s.h[0], k);
+          w += ((u64)h[1][bin] << 32) + h[0][bin];
+          c += h[2][bin];
+        }
+        for (int k = 0; k < C; ++k) {
+          cl.map_shared_rank(s.mass, k)[j] = w;
+          cl.map_shared_rank(s.count, k)[j] = c;
+        }
+      }
+      cl.sync();
+      u64 a[kSampPer], sum = 0;
+      uint32_t c[kSampPer], cnt = 0;
+#pragma unroll
+      for (int i = 0; i < kSampPer; ++i) {
+        const int j = kSampPer * tid + i;
+        a[i] = j < bins ? s.mass[j] : 0, c[i] = j < bins ? s.count[j] : 0;
+        sum += a[i], cnt += c[i];
+      }
+      u64 up = sum;
+      uint32_t nup = cnt;
+      scan2(up, nup, s);
+      if (tid == kSampNT - 1) s.total = nup;
+      __syncthreads();
+      up -= sum, nup -= cnt;
+      // the first non-empty bin over the target; if there is none, the last non-empty one
+#pragma unroll
+      for (int i = 0; i < kSampPer; ++i) {
+        const bool was = over(mass_above + up, above + nup), is = over(mass_above + up + a[i], above + nup + c[i]);
+        const bool last = nup + c[i] == s.total && !is;
+        if (c[i] && !was && (is || last)) {
+          s.found = bins - 1 - (kSampPer * tid + i);
+          s.res_mass[0] = mass_above + up;
+          s.res_rank[0] = above + nup;
+          s.res_rank[1] = c[i];
+        }
+        up += a[i], nup += c[i];
+      }
+      __syncthreads();
+      key |= (uint32_t)max(s.found, 0) << shift;
+      mass_above = s.res_mass[0], above = s.res_rank[0], equal = s.res_rank[1];
+      __syncthreads();  // the result has been read; the sums are of the next level's only behind its first cluster barrier
+    }
+    Term t;
+    each = 0;
+    if (term_of(key_float(key), m, ch, cl_, t)) each = weight_of(t, 0);
+    if (turn == 0) {
+      kept = (uint32_t)min(target, (u64)(above + equal));
+      mass = mass_above + (u64)(kept - above) * each;
+    } else if (turn == 1) {
+      const u64 more = target > mass_above ? target - mass_above : 0;
+      const uint32_t j = each ? (uint32_t)min(max((more + each - 1) / each, 1ull), (u64)equal) : equal;
+      if (above + j < kept) kept = above + j, mass = mass_above + j * each;
+    }
+  }
+  const u64 target = __umul64hi(mass, u_fix);
+  uint32_t j = each && target > mass_above ? (uint32_t)min((target - mass_above) / each, (u64)(equal - 1)) : 0u;
+  if (above + j >= kept) j = kept > above ? kept - above - 1 : 0;
+  // the j-th token of that key, by id: the CTAs hold ascending ids, their passes too
+  int owner = 0;
+  for (; owner < C - 1; ++owner) {
+    const uint32_t c = cl.map_shared_rank(&s.h[0], owner)[2][key & 1023u];
+    if (j < c) break;
+    j -= c;
+  }
+  cl.sync();  // no CTA's shared memory is read from here on
+  if (rank != owner) return;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kSampNT) {
+    const float l = logit(i0 + tid);
+    const bool hit = l != -INFINITY && sample_key(l) == key;
+    u64 unused = 0;
+    uint32_t c = hit;
+    scan2(unused, c, s);
+    if (hit && c == j + 1) {
+      p.tokens[row] = first + i0 + tid;
+      if (p.probs) p.probs[row] = (float)each / (float)mass;
+    }
+    if (tid == kSampNT - 1) s.total = c;
+    __syncthreads();
+    if (j < s.total) return;
+    j -= s.total;
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_constant__ SampleRowsParams p) {
   extern __shared__ __align__(16) uint8_t sm_raw[];
   SampShared& s = *reinterpret_cast<SampShared*>(sm_raw);
   cg::cluster_group cl = cg::this_cluster();
@@ -339,7 +554,6 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRow
 #pragma unroll 1
   for (int turn = 0;; ++turn) {
     S = (float)(32 << fine), chS = ch * S, clS = cl_ * S;
-    // buckets [from, from + kSampTable): half of them above the reference
     // buckets [from, from + kSampTable): half of them above the reference
     window = fabsf(m * chS) < 2090000.f;  // (else, and for no reference: nothing is in it)
     const float ref = floorf(-m * chS), from = ref - (turn ? 2.f : (float)kSampB);
@@ -503,10 +717,10 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRow
         if (lane == 0 && mine) atomicAdd(&s.total, mine);
         __syncthreads();
         crowd = s.total > (uint32_t)kSampleList;
-        break;
+        if (!crowd || turn == 1) break;
       }
     }
-    // once more, from the exact range: the least logit of any weight
+    // once more, from the exact range (finer buckets too, if that is what it takes): the least logit of any weight
     float3 low = make_float3(0.f, INFINITY, 0.f);
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += kSampU * kSampNT) {
@@ -521,280 +735,158 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const SampleRow
     cl.sync();
     for (int k = 0; k < C; ++k) low.y = fminf(low.y, s.range[k].y);
     const float wide = (m - low.y) * ch;
+    const int was = fine;
     fine = 0;
     while (fine < 15 && wide * (float)(64 << fine) < (float)(kSampB - 4) && fabsf(m * ch) * (float)(64 << fine) < 1048576.f)
       ++fine;
+    if (crowd && fine <= was) break;
     clear();
     cl.sync();
     load(cur, 0);
   }
-  if (!crowd) {
-    // ---- the second pass: their tokens to the first CTA
-    // (from the end on: what was read last is in L2 still, where the rows together are larger)
-    // the gathered buckets, a little wider (y is within 2^-8 of the exact place): the draw's, top_p's, and the others'
-    const float b0 = (float)tm.b, g0 = fmaxf(b0 + (float)bl - 0.01f, lo_y), g1 = fminf(b0 + (float)bh + 1.01f, hi_y);
-    const float g2 = fmaxf(b0 + (float)pl - 0.01f, lo_y), g3 = by_p ? fminf(b0 + (float)ph + 1.01f, hi_y) : -INFINITY;
-    const int other = by_k && by_m ? min(bk, bm) : by_k ? bk : bm, others = by_k && by_m ? max(bk, bm) : other;
-    const float g4 = fmaxf(b0 + (float)other - 0.01f, lo_y), g5 = by_k || by_m ? fminf(b0 + (float)others + 1.01f, hi_y) : -INFINITY;
-    constexpr int step = kSampU * kSampNT;
-    const int last = n > 0 ? (n - 1) / step * step : -1;
-    if (last >= 0) load(cur, last);
+  if (crowd) {
+    sample_crowd(p, s, m);
+    return;
+  }
+  // ---- the second pass: their tokens to the first CTA
+  // (from the end on: what was read last is in L2 still, where the rows together are larger)
+  // the gathered buckets, a little wider (y is within 2^-8 of the exact place): the draw's, top_p's, and the others'
+  const float b0 = (float)tm.b, g0 = fmaxf(b0 + (float)bl - 0.01f, lo_y), g1 = fminf(b0 + (float)bh + 1.01f, hi_y);
+  const float g2 = fmaxf(b0 + (float)pl - 0.01f, lo_y), g3 = by_p ? fminf(b0 + (float)ph + 1.01f, hi_y) : -INFINITY;
+  const int other = by_k && by_m ? min(bk, bm) : by_k ? bk : bm, others = by_k && by_m ? max(bk, bm) : other;
+  const float g4 = fmaxf(b0 + (float)other - 0.01f, lo_y), g5 = by_k || by_m ? fminf(b0 + (float)others + 1.01f, hi_y) : -INFINITY;
+  constexpr int step = kSampU * kSampNT;
+  const int last = n > 0 ? (n - 1) / step * step : -1;
+  if (last >= 0) load(cur, last);
 #pragma unroll 1
-    for (int i0 = last; i0 >= 0; i0 -= step) {
-      float next[kSampU];
-      if (i0 > 0) load(next, i0 - step);
+  for (int i0 = last; i0 >= 0; i0 -= step) {
+    float next[kSampU];
+    if (i0 > 0) load(next, i0 - step);
 #pragma unroll
-      for (int e = 0; e < kSampU; ++e) {
-        const float y = __fmul_rn(-cur[e], chS);
-        if ((y >= g0 && y < g1) || (y >= g2 && y < g3) || (y >= g4 && y < g5)) {
-          const int j = place_of(cur[e], chS, clS).b - tm.b;
-          if (j >= 0 && j < kSampB && s.flag[j])
-            s.local[atomicAdd(&s.n_local, 1u)] =
-                ((u64)sample_key(cur[e]) << 32) | (uint32_t)~(first + i0 + e * kSampNT + tid);
-        }
+    for (int e = 0; e < kSampU; ++e) {
+      const float y = __fmul_rn(-cur[e], chS);
+      if ((y >= g0 && y < g1) || (y >= g2 && y < g3) || (y >= g4 && y < g5)) {
+        const int j = place_of(cur[e], chS, clS).b - tm.b;
+        if (j >= 0 && j < kSampB && s.flag[j])
+          s.local[atomicAdd(&s.n_local, 1u)] =
+              ((u64)sample_key(cur[e]) << 32) | (uint32_t)~(first + i0 + e * kSampNT + tid);
       }
-#pragma unroll
-      for (int e = 0; e < kSampU; ++e) cur[e] = next[e];
     }
+#pragma unroll
+    for (int e = 0; e < kSampU; ++e) cur[e] = next[e];
+  }
+  __syncthreads();
+  if (C > 1) {
+    if (tid == 0 && s.n_local) s.base = atomicAdd(cl.map_shared_rank(&s.n_list, 0), s.n_local);
     __syncthreads();
-    if (C > 1) {
-      if (tid == 0 && s.n_local) s.base = atomicAdd(cl.map_shared_rank(&s.n_list, 0), s.n_local);
-      __syncthreads();
-      u64* list0 = cl.map_shared_rank(s.list, 0);
-      for (uint32_t i = tid; i < s.n_local; i += kSampNT) list0[s.base + i] = s.local[i];
-      cl.sync();
-      if (rank != 0) return;
-    }
-    const u64* in = C > 1 ? s.list : s.local;
-    const int N = C > 1 ? s.n_list : s.n_local;
-    int E = 1, n2 = 32;
-    while (E * kSampNT < N) E *= 2;
-    while (n2 < N) n2 *= 2;
-    u64 v[kListPer];
+    u64* list0 = cl.map_shared_rank(s.list, 0);
+    for (uint32_t i = tid; i < s.n_local; i += kSampNT) list0[s.base + i] = s.local[i];
+    cl.sync();
+    if (rank != 0) return;
+  }
+  const u64* in = C > 1 ? s.list : s.local;
+  const int N = C > 1 ? s.n_list : s.n_local;
+  int E = 1, n2 = 32;
+  while (E * kSampNT < N) E *= 2;
+  while (n2 < N) n2 *= 2;
+  if (E > kSortRegs) {
+    sort_long(s.list, in, N);
+  } else {
+    u64 v[kSortRegs];
 #pragma unroll
-    for (int e = 0; e < kListPer; ++e) v[e] = e * kSampNT + tid < N ? in[e * kSampNT + tid] : 0;
+    for (int e = 0; e < kSortRegs; ++e) v[e] = e * kSampNT + tid < N ? in[e * kSampNT + tid] : 0;
     __syncthreads();
     if (E == 1) sort_list<1>(v, s.list, n2);
     else if (E == 2) sort_list<2>(v, s.list, n2);
     else sort_list<4>(v, s.list, n2);
-    // masses, running sums and first entries of the buckets
-    Term t[kListPer];
-    u64 G[kListPer], carry = 0;  // up to and with an entry: first of the list, then of the row
 #pragma unroll
-    for (int e = 0; e < kListPer; ++e) {
-      t[e].b = -1, t[e].q = 0, G[e] = 0;
-      if (e >= E) continue;
-      if (v[e]) {
-        t[e] = place_of(key_float((uint32_t)(v[e] >> 32)), chS, clS);
-        t[e].b -= tm.b;
-        G[e] = weight_of(t[e], fine);
-        s.bucket[e * kSampNT + tid] = (uint16_t)t[e].b;
-      }
-      uint32_t none = 0;
-      scan2(G[e], none, s);
-      if (tid == kSampNT - 1) s.res_mass[0] = G[e];
-      G[e] += carry;
-      s.local[e * kSampNT + tid] = G[e];
-      __syncthreads();
-      carry += s.res_mass[0];
-      if (v[e]) {
-        const int j = e * kSampNT + tid;
-        if (j == 0 || s.bucket[j - 1] != t[e].b) s.start[t[e].b] = j;
-      }
-      __syncthreads();
-    }
-    // the masses that top_k, top_p and min_p keep
-    if (tid == 0) {
-      s.res_mass[0] = s.res_mass[1] = all;
-      s.res_mass[2] = by_m ? mass_to(bm - 1) : all;  // or more, of min_p's own bucket
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kListPer; ++e)
-      if (e < E && v[e]) {
-        const int f = s.start[t[e].b], j = e * kSampNT + tid;
-        G[e] = mass_to(t[e].b - 1) + G[e] - (f ? s.local[f - 1] : 0ull);
-        if (by_k && count_to(t[e].b - 1) + (uint32_t)(j - f) + 1 == (uint32_t)s.top_k) s.res_mass[0] = G[e];
-        if (by_m && t[e].b == bm && t[e].q <= qm) atomicMax(&s.res_mass[2], G[e]);
-      }
-    __syncthreads();
-    if (by_p) {
-      const u64 target = ceil_part(s.res_mass[0], s.p_fix);
-#pragma unroll
-      for (int e = 0; e < kListPer; ++e)
-        if (e < E && v[e] && G[e] >= target && t[e].b >= pl) atomicMin(&s.res_mass[1], G[e]);
-      __syncthreads();
-    }
-    const u64 mass = min(min(s.res_mass[0], s.res_mass[1]), s.res_mass[2]), target = __umul64hi(mass, u_fix);
-    if (tid == 0) s.found = kSampleList;
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kListPer; ++e)
-      if (e < E && v[e] && G[e] > target && t[e].b >= bl) atomicMin(&s.found, e * kSampNT + tid);
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kListPer; ++e)
-      if (v[e] && e * kSampNT + tid == (s.found < kSampleList ? s.found : 0)) {
-        p.tokens[row] = (int)~(uint32_t)v[e];
-        if (p.probs)
-          p.probs[row] = (float)((1ull << 34) - below(t[e].q, fine)) * exp2f(-(float)t[e].b / S) * 1024.f / (float)mass;
-      }
-    return;
+    for (int e = 0; e < kSortRegs; ++e)
+      if (e < E) s.list[e * kSampNT + tid] = v[e];  // read by this thread alone
   }
-  // ---- the long way: the borders of top_k (or all tokens), top_p and the draw in
-  // turn, each by three digits of the keys from the top, over all tokens
-  auto logit = [&](int i) {
-    const float l = i < n ? src[i] : -INFINITY;
-    return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
+  // masses, running sums and first entries of the buckets
+  auto entry = [&](u64 v) {
+    Term t = place_of(key_float((uint32_t)(v >> 32)), chS, clS);
+    t.b -= tm.b;
+    return t;
   };
-  if (tid == 0) s.key = by_m ? (u64)(s.y_min * 137438953472.0) : 0ull;  // of 32 buckets an octave, from the largest logit
-  cl.sync();
-  by_k = s.top_k > 0;
-  if (by_m) bm = (int)min(s.key >> 32, (u64)kSampB), qm = (uint32_t)s.key;
-  uint32_t kept = 0;
-  u64 mass = 0;
-  uint32_t key = 0, above = 0, equal = 0;  // a border's key, tokens above it and of it
-  u64 mass_above = 0, each = 0;            // mass above it, and of one token of it
+  u64 carry = 0;
 #pragma unroll 1
-  for (int turn = 0; turn < 3; ++turn) {
-    if (turn == 1 && !by_p) continue;
-    if (turn == 2 && by_m) {  // tokens and mass that min_p keeps
-      u64 a = 0;
-      uint32_t c = 0;
-#pragma unroll 1
-      for (int i = tid; i < n; i += kSampNT) {
-        Term t;
-        if (term_of(logit(i), m, ch, cl_, t) && (t.b < bm || (t.b == bm && t.q <= qm)))
-          a += weight_of(t, 0), ++c;
-      }
-      scan2(a, c, s);
-      if (tid == kSampNT - 1) s.list[0] = a, s.list[1] = c;
-      cl.sync();
-      a = 0, c = 0;
-      for (int k = 0; k < C; ++k) {
-        const u64* o = cl.map_shared_rank(s.list, k);
-        a += o[0], c += (uint32_t)o[1];
-      }
-      if (c < kept) kept = c, mass = a;
-      cl.sync();
+  for (int j = tid; j < E * kSampNT; j += kSampNT) {
+    const u64 v = s.list[j];
+    Term t = {-1, 0u};
+    u64 g = 0;  // up to and with an entry: first of the list, then of the row
+    if (v) {
+      t = entry(v);
+      g = weight_of(t, fine);
+      s.bucket[j] = (uint16_t)t.b;
     }
-    // found is where the count (turn 0) or the mass (1) reaches the target, or the mass passes it (2)
-    const u64 target = turn == 0 ? (by_k ? (u64)s.top_k : ~0ull) : turn == 1 ? ceil_part(mass, s.p_fix) : __umul64hi(mass, u_fix);
-    auto over = [&](u64 m_, uint32_t n_) { return turn == 0 ? n_ >= target : turn == 1 ? m_ >= target : m_ > target; };
-    key = above = 0, mass_above = 0;
-#pragma unroll 1
-    for (int level = 0; level < 3; ++level) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bins = level == 2 ? 1024 : 2048;
-      const uint32_t prefix_mask = level == 0 ? 0u : level == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-      for (int i = tid; i < 3 * kSampB; i += kSampNT) (&s.h[0][0])[i] = 0;
-      if (tid == 0) s.found = -1;
-      __syncthreads();
-#pragma unroll 1
-      for (int i = tid; i < n; i += kSampNT) {
-        Term t;
-        const float l = logit(i);
-        const uint32_t k = sample_key(l);
-        if ((k & prefix_mask) == key && term_of(l, m, ch, cl_, t)) {
-          const u64 w = weight_of(t, 0);
-          const uint32_t bin = (k >> shift) & (bins - 1), lo32 = (uint32_t)w, old = atomicAdd(&s.h[0][bin], lo32);
-          atomicAdd(&s.h[1][bin], (uint32_t)(w >> 32) + (old + lo32 < old));
-          atomicAdd(&s.h[2][bin], 1u);
-        }
-      }
-      cl.sync();
-      // every CTA adds all of them up; a thread has four bins of the descending order
-      u64 a[kSampPer], sum = 0;
-      uint32_t c[kSampPer], cnt = 0;
-#pragma unroll
-      for (int i = 0; i < kSampPer; ++i) {
-        const int bin = bins - 1 - (kSampPer * tid + i);
-        a[i] = 0, c[i] = 0;
-        if (bin >= 0)
-          for (int k = 0; k < C; ++k) {
-            const uint32_t(*h)[kSampB] = cl.map_shared_rank(&s.h[0], k);
-            a[i] += ((u64)h[1][bin] << 32) + h[0][bin];
-            c[i] += h[2][bin];
-          }
-        sum += a[i], cnt += c[i];
-      }
-      u64 up = sum;
-      uint32_t nup = cnt;
-      scan2(up, nup, s);
-      if (tid == kSampNT - 1) s.total = nup;
-      __syncthreads();
-      up -= sum, nup -= cnt;
-      // the first non-empty bin over the target; if there is none, the last non-empty one
-#pragma unroll
-      for (int i = 0; i < kSampPer; ++i) {
-        const bool was = over(mass_above + up, above + nup), is = over(mass_above + up + a[i], above + nup + c[i]);
-        const bool last = nup + c[i] == s.total && !is;
-        if (c[i] && !was && (is || last)) {
-          s.found = bins - 1 - (kSampPer * tid + i);
-          s.res_mass[0] = mass_above + up;
-          s.res_rank[0] = above + nup;
-          s.res_rank[1] = c[i];
-        }
-        up += a[i], nup += c[i];
-      }
-      __syncthreads();
-      key |= (uint32_t)max(s.found, 0) << shift;
-      mass_above = s.res_mass[0], above = s.res_rank[0], equal = s.res_rank[1];
-      cl.sync();  // every CTA has read the histograms (the last turn's stay) and the result
-    }
-    Term t;
-    each = 0;
-    if (term_of(key_float(key), m, ch, cl_, t)) each = weight_of(t, 0);
-    if (turn == 0) {
-      kept = (uint32_t)min(target, (u64)(above + equal));
-      mass = mass_above + (u64)(kept - above) * each;
-    } else if (turn == 1) {
-      const u64 more = target > mass_above ? target - mass_above : 0;
-      const uint32_t j = each ? (uint32_t)min(max((more + each - 1) / each, 1ull), (u64)equal) : equal;
-      if (above + j < kept) kept = above + j, mass = mass_above + j * each;
-    }
-  }
-  const u64 target = __umul64hi(mass, u_fix);
-  uint32_t j = each && target > mass_above ? (uint32_t)min((target - mass_above) / each, (u64)(equal - 1)) : 0u;
-  if (above + j >= kept) j = kept > above ? kept - above - 1 : 0;
-  // the j-th token of that key, by id: the CTAs hold ascending ids, their passes too
-  int owner = 0;
-  for (; owner < C - 1; ++owner) {
-    const uint32_t c = cl.map_shared_rank(&s.h[0], owner)[2][key & 1023u];
-    if (j < c) break;
-    j -= c;
-  }
-  cl.sync();  // no CTA's shared memory is read from here on
-  if (rank != owner) return;
-#pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += kSampNT) {
-    const float l = logit(i0 + tid);
-    const bool hit = l != -INFINITY && sample_key(l) == key;
-    u64 unused = 0;
-    uint32_t c = hit;
-    scan2(unused, c, s);
-    if (hit && c == j + 1) {
-      p.tokens[row] = first + i0 + tid;
-      if (p.probs) p.probs[row] = (float)each / (float)mass;
-    }
-    if (tid == kSampNT - 1) s.total = c;
+    uint32_t none = 0;
+    scan2(g, none, s);
+    if (tid == kSampNT - 1) s.res_mass[0] = g;
+    s.local[j] = g + carry;
     __syncthreads();
-    if (j < s.total) return;
-    j -= s.total;
+    carry += s.res_mass[0];
+    if (v && (j == 0 || s.bucket[j - 1] != t.b)) s.start[t.b] = j;
     __syncthreads();
+  }
+  // the masses that top_k, top_p and min_p keep
+  if (tid == 0) {
+    s.res_mass[0] = s.res_mass[1] = all;
+    s.res_mass[2] = by_m ? mass_to(bm - 1) : all;  // or more, of min_p's own bucket
+  }
+  __syncthreads();
+  auto row_mass = [&](int j, int b) {
+    const int f = s.start[b];
+    return mass_to(b - 1) + s.local[j] - (f ? s.local[f - 1] : 0ull);
+  };
+#pragma unroll 1
+  for (int j = tid; j < N; j += kSampNT) {
+    const Term t = entry(s.list[j]);
+    const u64 g = row_mass(j, t.b);
+    if (by_k && count_to(t.b - 1) + (uint32_t)(j - s.start[t.b]) + 1 == (uint32_t)s.top_k) s.res_mass[0] = g;
+    if (by_m && t.b == bm && t.q <= qm) atomicMax(&s.res_mass[2], g);
+  }
+  __syncthreads();
+  if (by_p) {
+    const u64 target = ceil_part(s.res_mass[0], s.p_fix);
+#pragma unroll 1
+    for (int j = tid; j < N; j += kSampNT) {
+      const int b = s.bucket[j];
+      if (b < pl) continue;
+      const u64 g = row_mass(j, b);
+      if (g >= target) atomicMin(&s.res_mass[1], g);
+    }
+    __syncthreads();
+  }
+  const u64 mass = min(min(s.res_mass[0], s.res_mass[1]), s.res_mass[2]), target = __umul64hi(mass, u_fix);
+  if (tid == 0) s.found = kSampleList;
+  __syncthreads();
+#pragma unroll 1
+  for (int j = tid; j < N; j += kSampNT) {
+    const int b = s.bucket[j];
+    if (b >= bl && row_mass(j, b) > target) atomicMin(&s.found, j);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    const u64 v = s.list[s.found < kSampleList ? s.found : 0];
+    const Term t = entry(v);
+    p.tokens[row] = (int)~(uint32_t)v;
+    if (p.probs)
+      p.probs[row] = (float)((1ull << 34) - below(t.q, fine)) * exp2f(-(float)t.b / S) * 1024.f / (float)mass;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_sample_rows(SampleRowsParams& p, int n_sm, cudaStream_t st) {
-  // CTAs of a row: a CTA's fixed work (about 12 us) pays for as many logits as can be,
-  // so as many as have an SM each, with 1000 logits or more, or two on an SM for long slices;
-  // at most 180000 (the histogram's counts). Measured, us for 1, 2, 4, 8, 16: 1 x 32000 26 / 21 /
-  // 17 / 15 / 15, 32 x 32000 30 / 23 / 18 / 25 / 43, 64 x 151936 89 / 53 / 46 / 57 / 99, 256 x 151936
-  // 135 / 139 / 156 / 205 / 357.
+  // CTAs of a row: a CTA's fixed work (about 12 us) pays for as many logits as can be, so as many as
+  // have an SM each, with 1000 logits or more, or two on an SM for slices of 32768 and more; at most
+  // 180000 (the histogram's counts). Measured, us for 1, 2, 4, 8, 16: 1 x 32000 26 / 21 / 17 / 15 / 15,
+  // 32 x 32000 30 / 23 / 18 / 25 / 43, 32 x 151936 86 / 54 / 37 / 35 / 57, 64 x 151936 89 / 53 / 46 / 57 / 99,
+  // 256 x 151936 135 / 139 / 156 / 205 / 357.
   const auto more = [&](int C) {
     const int64_t ctas = (int64_t)2 * p.R * C;
-    return (p.V + C - 1) / C > kSampMaxSlice || (ctas <= n_sm && p.V / (2 * C) >= 1000) || (ctas <= 2 * n_sm && p.V / C >= 65536);
+    return (p.V + C - 1) / C > kSampMaxSlice || (ctas <= n_sm && p.V / (2 * C) >= 1000) || (ctas <= 2 * n_sm && p.V / C >= 32768);
   };
   int C = 1;
   while (C < 16 && more(C)) C *= 2;

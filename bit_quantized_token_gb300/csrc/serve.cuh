@@ -44,7 +44,7 @@ cudaError_t launch_read_kv(const ReadParams& p, int hd, bool q8, cudaStream_t st
 cudaError_t launch_prefix_attn(const TreeAttnParams& first, const TreeAttnParams& second, int hd, bool f32, bool q8,
                                int n_sm, cudaStream_t st);
 
-constexpr int kSampleList = 2048;  // tokens around the borders that one CTA sorts
+constexpr int kSampleList = 4096;  // tokens around the borders that one CTA sorts
 
 struct SampleRowsParams {
   const float* logits;

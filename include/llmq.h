@@ -259,9 +259,9 @@ int llm_debug_unpack(llm_model* m, const char* name, uint8_t* codes, uint16_t* s
  * Source: zynfer PR #100, stage M6 (allocation behaviour tested with a failing allocator). */
 int llm_debug_fail_alloc(int32_t nth);
 
-/* Test hook: on != 0 makes a wait of each CTA of the llm_tree_attention and plain
- * llm_token_probs calls launched from then on (llm_decode_tree's among them) run
- * out, after 1 ms; their outputs are not valid, and llm_tree_status, or the model's
+/* Test hook: on != 0 makes a wait of each CTA of the llm_tree_attention,
+ * llm_prefix_attention and plain llm_token_probs calls launched from then on
+ * (llm_decode_tree's among them) run out, after 1 ms; their outputs are not valid, and llm_tree_status, or the model's
  * call, reports TIMEOUT. Process-wide; returns LLM_OK.
  * Source: as llm_debug_fail_alloc. */
 int llm_debug_expire_waits(int32_t on);
@@ -441,7 +441,7 @@ typedef struct {
 int llm_tree_attention(const llm_tree_attention_args* args, void* cuda_stream);
 
 /* Wait for `cuda_stream` and report whether a device-side wait of a
- * llm_tree_attention or llm_token_probs on the current device passed its limit
+ * llm_tree_attention, llm_prefix_attention or llm_token_probs on the current device passed its limit
  * (2 s) since the last call (TIMEOUT: the outputs of that call are not valid). */
 int llm_tree_status(void* cuda_stream);
 
@@ -611,9 +611,12 @@ typedef struct {
  * exceeds uniforms[r] times the kept ones' total, as llm_set_sampling chooses it from
  * the same draw; probs[r] is its share of that total. Borders are decided with sums
  * of 36 bits or more (of the whole row's mass). A NaN logit counts as -inf, +inf as the
- * largest finite value; a row without a finite logit gives -1. The same inputs give the
- * same token in any batch. A row with thousands of logits around a border (all alike,
- * or crowds of equal ones) takes up to 0.2 ms. UNSUPPORTED: vocab over 524288. */
+ * largest finite value; a row without a finite logit gives -1. The same call gives
+ * the same tokens every time; a row in another batch gives the same one, but for
+ * borders that lie within those sums' last bits. Rows with thousands of logits around a
+ * border (untrained ones, high temperatures) take up to three times as long, rows with
+ * crowds of equal logits around it about ten times (151936 equal ones 0.2 ms, 256 rows of
+ * them 3.7 ms). UNSUPPORTED: vocab over 524288. */
 int llm_sample_tokens(const llm_sample_args* args, void* cuda_stream);
 
 #ifdef __cplusplus

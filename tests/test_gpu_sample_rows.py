@@ -123,6 +123,16 @@ def test_crowds(V):
     check(mixed, **o)
 
 
+@pytest.mark.parametrize("V,sd", [(151936, 2.5), (151936, 0.75), (151936, 0.1), (300001, 2.0), (524288, 1.0), (65536, 0.3)])
+def test_flat_rows(V, sd):
+    """High temperatures and narrow logits: thousands of tokens in the buckets around a border, or finer buckets."""
+    R = 12
+    rng = np.random.default_rng(V)
+    for k, m in ((0, 0.0), (V // 3, 0.0), (V // 2, 0.001)):
+        check(logits(R, V, sd, k + 11), T=rng.choice([1.0, 1.4, 1.79], R), k=k, p=rng.choice([0.9, 0.5, 0.97], R), m=m,
+              u=rng.random(R).astype(np.float32))
+
+
 def test_odd_values():
     R, V = 9, 7001
     x = logits(R, V, 2.0, 2)
