@@ -1,0 +1,273 @@
+// The second part of the attention behind shared prefixes for few rows: a token's
+// (or a small tree's) queries over its sequence's own rows and the tree's.
+//
+// At most eight query rows of a kv head meet keys that no other block reads, so
+// the work is latency: a warp takes 16 keys at a time, its fragments straight
+// from global memory in 16-byte loads, and no barrier stands between a load and
+// the products.
+//   S^T[keys][rows] = K Q^T     mma m16n8k16: A = K, a lane has 16-byte pieces of
+//                               keys g and g + 8 (g = lane / 4), B = Q, of row g;
+//                               which dims make up a step is free, so a piece's
+//                               words are the steps' halves
+//   P^T -> B                    8 x 8 transposed in registers
+//   O^T[dims][rows] = V^T P^T   A = V^T from pieces of keys 2t, 2t + 1, 2t + 8,
+//                               2t + 9 (t = lane % 4): pairs of keys by byte permutes
+// P in NP bf16 parts (16 bits for bf16 queries, 24 for fp32 ones, whose Q has
+// three parts as well). A row's reference is renewed when a probability passes
+// 2^60, so most steps have no reduction over lanes. The warps' results are joined
+// in shared memory, then as those of the tree attention are.
+//
+// (tcgen05 instructions hold 128 rows, a tile's loads, barriers and tensor memory:
+// about 7 us a CTA whatever its rows are, and two CTAs on an SM.)
+#pragma once
+#include "tree_attn.cuh"
+
+namespace llmq {
+
+template <int HD, bool F32>
+struct Own {
+  static constexpr int NT = 128, NW = NT / 32, N = 8;
+  static constexpr int NQ = F32 ? 3 : 1, NP = F32 ? 3 : 2;
+  static constexpr int kBlocks = HD == 64 && !F32 ? 5 : HD == 128 && F32 ? 2 : 3;  // on an SM
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float max_of_keys(float x) {  // over the lanes of a row
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+template <int HD, bool F32>
+__global__ void __launch_bounds__(Own<HD, F32>::NT, Own<HD, F32>::kBlocks) own_attn_kernel(const __grid_constant__ TreeAttnParams p) {
+  using C = Own<HD, F32>;
+  constexpr int NW = C::NW, N = C::N, NQ = C::NQ, NP = C::NP, NT = C::NT;
+  constexpr int NC = HD / 32;  // 16-byte pieces of a row that a lane has
+  __shared__ __align__(16) float s_o[NW][N][HD];
+  __shared__ float2 s_ml[NW][N];
+  __shared__ __align__(16) float so[N * HD];
+  __shared__ float2 sml[N];
+  __shared__ __align__(16) uint8_t s_in[kJoin<HD, N>];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  pdl_trigger();
+  const int hkv = blockIdx.y, b = blockIdx.z, rank = blockIdx.x;
+  const TreeBlock block(p, b);
+  const int cnt = block.cnt, rows = cnt * p.gq;
+  if (rows == 0) {  // (in every CTA of the cluster)
+    pdl_wait();     // the kernel ends after the first part's
+    return;
+  }
+  if (p.S > 1) cluster_arrive();
+  const int len = min(max(p.lens[b], 0), p.cache.rows), n_pre = (len + 15) / 16, n_all = n_pre + (p.tree.k ? 1 : 0);
+  const int c0 = (int)((int64_t)n_all * rank / p.S), c1 = (int)((int64_t)n_all * (rank + 1) / p.S);
+
+  uint32_t q[NQ][NC][4];  // row g
+  {
+    const int node = p.by_gq.div(g), h = hkv * p.gq + g - node * p.gq;
+    const int64_t off = (int64_t)b * p.q_seq + (int64_t)node * p.q_node + (int64_t)h * p.q_head + 8 * t;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if constexpr (F32) {
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (g < rows) {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + off + 32 * i);
+          const float4 lo = src[0], hi = src[1];
+          x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = p.neg ? -x[e] : x[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t part[NQ];
+          split_pack<NQ>(x[2 * e], x[2 * e + 1], part);
+#pragma unroll
+          for (int k = 0; k < NQ; ++k) q[k][i][e] = part[k];
+        }
+      } else {
+        const uint4 w = g < rows ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + off + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t turn = p.neg ? 0x80008000u : 0u;
+        q[0][i][0] = w.x ^ turn, q[0][i][1] = w.y ^ turn, q[0][i][2] = w.z ^ turn, q[0][i][3] = w.w ^ turn;
+      }
+    }
+  }
+  // what the lane's rows 2t and 2t + 1 see of the tree
+  uint64_t sees[2] = {0, 0};
+  if (p.tree.k)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (2 * t + e < rows) sees[e] = p.mask[(int64_t)b * p.mask_seq + p.by_gq.div(2 * t + e)] & ((1ull << cnt) - 1);
+
+  float o[HD / 16][4];  // [16 dims]: (dim, row 2t), (dim, row 2t + 1), (next dim, ..)
+#pragma unroll
+  for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  float m[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int c = c0 + warp; c < c1; c += NW) {
+    const bool tree = c >= n_pre;
+    const KvRows& from = tree ? p.tree : p.cache;
+    const int k0 = tree ? 0 : 16 * c, n = tree ? cnt : len - k0;  // keys of the step
+    const int64_t base = (int64_t)b * from.seq + (int64_t)hkv * from.head + (int64_t)k0 * from.row;
+    const uint16_t* kp = reinterpret_cast<const uint16_t*>(from.k) + base + 8 * t;
+    const uint16_t* vp = reinterpret_cast<const uint16_t*>(from.v) + base + 8 * g;
+    uint32_t kw[2][NC][4], vw[4][HD / 64][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int key = g + 8 * e;
+        const uint4 w = key < n ? __ldcg(reinterpret_cast<const uint4*>(kp + key * from.row + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+        kw[e][i][0] = w.x, kw[e][i][1] = w.y, kw[e][i][2] = w.z, kw[e][i][3] = w.w;
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i) {
+        const int key = 2 * t + (e & 1) + 8 * (e >> 1);
+        const uint4 w = key < n ? __ldcg(reinterpret_cast<const uint4*>(vp + key * from.row + 64 * i)) : make_uint4(0u, 0u, 0u, 0u);
+        vw[e][i][0] = w.x, vw[e][i][1] = w.y, vw[e][i][2] = w.z, vw[e][i][3] = w.w;
+      }
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};  // (key g, rows 2t, 2t + 1), (key g + 8, ..)
+#pragma unroll
+    for (int k = NQ - 1; k >= 0; --k)  // the smallest part first
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        mma_16816(s, kw[0][i][0], kw[1][i][0], kw[0][i][1], kw[1][i][1], q[k][i][0], q[k][i][1]);
+        mma_16816(s2, kw[0][i][2], kw[1][i][2], kw[0][i][3], kw[1][i][3], q[k][i][2], q[k][i][3]);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = g + 8 * (e >> 1);
+      s[e] += s2[e];
+      if (key >= n || (tree && !(sees[e & 1] >> key & 1))) s[e] = -INFINITY;
+    }
+    float x[4];
+    bool over = c == c0 + warp;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = ex2((s[e] - m[e & 1]) * p.c);
+      over |= x[e] > 1152921504606846976.f;  // 2^60
+    }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float top = max_of_keys(fmaxf(s[r], s[r + 2]));
+        // (NaN or infinite scores alone: any reference does, the sum says what the row is)
+        const unsigned odd = __ballot_sync(0xffffffffu, s[r] != s[r] || s[r + 2] != s[r + 2]) & (0x11111111u << t);
+        float now = fmaxf(m[r], top < INFINITY ? top : kNone);
+        if (now <= kNone && (odd || top == INFINITY)) now = 0.f;
+        const float f = exp2f((m[r] - now) * p.c);
+        m[r] = now;
+        l[r] *= f;
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) o[i][r] *= f, o[i][r + 2] *= f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = ex2((s[e] - m[e & 1]) * p.c);
+    }
+    l[0] += x[0] + x[2], l[1] += x[1] + x[3];
+    uint32_t lo[NP], hi[NP];
+    split_pack<NP>(x[0], x[1], lo);
+    split_pack<NP>(x[2], x[3], hi);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) lo[k] = transposed(lo[k]), hi[k] = transposed(hi[k]);  // row g, keys 2t, 2t + 1 (+ 8)
+    bool odd = false;  // of the tree, infinities and NaNs have to stay away from the rows that do not see them
+    if (tree) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            odd |= (vw[e][i][w] & 0x7F80u) == 0x7F80u || (vw[e][i][w] & 0x7F800000u) == 0x7F800000u;
+      odd = __any_sync(0xffffffffu, odd);
+    }
+    if (!odd) {
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a0 = __byte_perm(vw[0][i][w], vw[1][i][w], 0x5410), a1 = __byte_perm(vw[0][i][w], vw[1][i][w], 0x7632);
+          const uint32_t a2 = __byte_perm(vw[2][i][w], vw[3][i][w], 0x5410), a3 = __byte_perm(vw[2][i][w], vw[3][i][w], 0x7632);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) mma_16816(o[4 * i + w], a0, a1, a2, a3, lo[k], hi[k]);
+        }
+    } else {  // one tree row at a time, added where it is seen
+#pragma unroll 1
+      for (int j = 0; j < cnt; ++j) {
+        const bool mine = t == j / 2;  // the lane has its values
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t v = mine ? (j & 1 ? vw[1][i][w] : vw[0][i][w]) : 0u;
+            const uint32_t a0 = j & 1 ? v << 16 : v & 0xFFFFu, a1 = j & 1 ? v & 0xFFFF0000u : v >> 16;
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NP; ++k) mma_16816(y, a0, a1, 0u, 0u, lo[k], 0u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (sees[e & 1] >> j & 1) o[4 * i + w][e] += y[e];
+          }
+      }
+    }
+  }
+  // ---- the warps' results joined
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+  if (lane < 4) s_ml[warp][2 * t] = make_float2(m[0], l[0]), s_ml[warp][2 * t + 1] = make_float2(m[1], l[1]);
+#pragma unroll
+  for (int i = 0; i < HD / 16; ++i) {
+    const int d = 64 * (i / 4) + 8 * g + 2 * (i & 3);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) *reinterpret_cast<float2*>(&s_o[warp][2 * t + r][d]) = make_float2(o[i][r], o[i][r + 2]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = tid; i < N * HD / 4; i += NT) {
+    const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
+    float M = kNone, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][r].x);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float2 ml = s_ml[w][r];
+      const float f = ml.x <= kNone ? 0.f : ex2((ml.x - M) * p.c);
+      const float4 y = *reinterpret_cast<const float4*>(&s_o[w][r][d]);
+      L = fmaf(ml.y, f, L);
+      a.x = fmaf(y.x, f, a.x), a.y = fmaf(y.y, f, a.y), a.z = fmaf(y.z, f, a.z), a.w = fmaf(y.w, f, a.w);
+    }
+    *reinterpret_cast<float4*>(so + r * HD + d) = a;
+    if (d == 0) sml[r] = make_float2(M, L);
+  }
+  join_splits<HD, F32, N, NT>(p, so, sml, s_in, rank, b, hkv, 0, rows);
+}
+
+// Whether a call's second part has few enough rows.
+inline bool own_fits(const TreeAttnParams& p, bool q8) { return !q8 && p.part == TreeAttnParams::kSecond && p.n * p.gq <= 8; }
+
+template <int HD, bool F32>
+cudaError_t launch_own(TreeAttnParams p, int n_sm, cudaStream_t st) {
+  using C = Own<HD, F32>;
+  // Splits of the keys: until the CTAs fill the SMs' places, while a CTA has 256 rows.
+  const int64_t clusters = (int64_t)p.Hkv * p.B;
+  int S = 1;
+  while (S < 8 && clusters * S * 2 <= (int64_t)n_sm * C::kBlocks && p.cache.rows / (2 * S) >= 256) S *= 2;
+  p.S = S;
+  return launch_cluster(own_attn_kernel<HD, F32>, dim3(S, p.Hkv, p.B), C::NT, S, 0, st, p, p.pdl);
+}
+
+}  // namespace llmq

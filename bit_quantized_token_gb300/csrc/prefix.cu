@@ -1,6 +1,7 @@
 // Attention of sequences that share prefixes: two launches, of which the second
 // overlaps the first (see serve.cuh, tree_attn.cuh).
 #include "op_call.cuh"
+#include "own_attn.cuh"
 #include "prefix_attn.cuh"
 #include "serve.cuh"
 
@@ -17,7 +18,10 @@ cudaError_t launch_prefix_attn(const TreeAttnParams& first, const TreeAttnParams
                     rows * first.Hkv < (1ll << 30);
   const cudaError_t e = !wide ? launch_tree_attn(first, hd, f32, q8, n_sm, st)
                         : hd == 64 ? launch_wide<64>(first, n_sm, st) : launch_wide<128>(first, n_sm, st);
-  return e == cudaSuccess ? launch_tree_attn(second, hd, f32, q8, n_sm, st) : e;
+  if (e != cudaSuccess) return e;
+  if (!own_fits(second, q8)) return launch_tree_attn(second, hd, f32, q8, n_sm, st);
+  return hd == 64 ? (f32 ? launch_own<64, true>(second, n_sm, st) : launch_own<64, false>(second, n_sm, st))
+                  : (f32 ? launch_own<128, true>(second, n_sm, st) : launch_own<128, false>(second, n_sm, st));
 }
 
 }  // namespace llmq
