@@ -19,9 +19,12 @@ cudaError_t launch_prefix_attn(const TreeAttnParams& first, const TreeAttnParams
   const cudaError_t e = !wide ? launch_tree_attn(first, hd, f32, q8, n_sm, st)
                         : hd == 64 ? launch_wide<64>(first, n_sm, st) : launch_wide<128>(first, n_sm, st);
   if (e != cudaSuccess) return e;
-  if (!own_fits(second, q8)) return launch_tree_attn(second, hd, f32, q8, n_sm, st);
-  return hd == 64 ? (f32 ? launch_own<64, true>(second, n_sm, st) : launch_own<64, false>(second, n_sm, st))
-                  : (f32 ? launch_own<128, true>(second, n_sm, st) : launch_own<128, false>(second, n_sm, st));
+  if (!own_fits(second, hd, q8)) return launch_tree_attn(second, hd, f32, q8, n_sm, st);
+  const auto launch = hd == 64 ? (f32 ? (q8 ? launch_own<64, true, true> : launch_own<64, true, false>)
+                                      : (q8 ? launch_own<64, false, true> : launch_own<64, false, false>))
+                               : (f32 ? (q8 ? launch_own<128, true, true> : launch_own<128, true, false>)
+                                      : (q8 ? launch_own<128, false, true> : launch_own<128, false, false>));
+  return launch(second, n_sm, st);
 }
 
 }  // namespace llmq
