@@ -62,6 +62,45 @@ __device__ __forceinline__ float max_of_keys(float x) {  // over the lanes of a 
   return x;
 }
 
+// The z-th of at most 256 sequences, by eighths of the longest cache, the longest first: blocks start in grid order
+// (rising lengths, 256 x 4 x 64 and 128 x 8 x 128 of 16 .. 300 rows: 64 and 48 us in the order given, 59 and 39 longest
+// first). Every warp finds it by itself.
+__device__ __forceinline__ int nearly_longest(const int* lens, int B, int z, int lane) {
+  constexpr int K = 8;
+  int l[K], top = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    l[k] = lane + 32 * k < B ? max(lens[lane + 32 * k], 0) : -1;
+    top = max(top, l[k]);
+  }
+  const float f = 8.f / ((float)__reduce_max_sync(0xffffffffu, top) + 1.f);
+  uint64_t n[2] = {0, 0};  // sequences of each eighth, in 16 bits
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int v = 7 - min((int)((float)l[k] * f), 7);
+    if (l[k] >= 0) n[v >> 2] += 1ull << (16 * (v & 3));
+    l[k] = l[k] >= 0 ? v : -1;
+  }
+  uint64_t to[2] = {n[0], n[1]};  // up to and with this lane's
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t x = __shfl_up_sync(0xffffffffu, to[i], o);
+      if (lane >= o) to[i] += x;
+    }
+  auto of = [](const uint64_t (&x)[2], int v) { return (int)((v & 4 ? x[1] : x[0]) >> (16 * (v & 3))) & 0xFFFF; };
+  const uint64_t all[2] = {__shfl_sync(0xffffffffu, to[0], 31), __shfl_sync(0xffffffffu, to[1], 31)};
+  int v = 0;
+  for (; v < 7 && z >= of(all, v); ++v) z -= of(all, v);
+  int left = z - (of(to, v) - of(n, v)), found = -1;  // of this lane's in that eighth
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (l[k] == v && left-- == 0) found = lane + 32 * k;
+  const unsigned who = __ballot_sync(0xffffffffu, found >= 0);
+  return __shfl_sync(0xffffffffu, found, __ffs(who) - 1);
+}
+
 template <int HD, bool F32, bool Q8>
 __global__ void __launch_bounds__(Own<HD, F32, Q8>::NT, Own<HD, F32, Q8>::kBlocks) own_attn_kernel(const __grid_constant__ TreeAttnParams p) {
   using C = Own<HD, F32, Q8>;
@@ -75,7 +114,7 @@ __global__ void __launch_bounds__(Own<HD, F32, Q8>::NT, Own<HD, F32, Q8>::kBlock
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_trigger();
   const int hkv = blockIdx.y, rank = blockIdx.x;
-  const int b = p.sorted ? nth_longest(p.lens, p.B, blockIdx.z, lane) : blockIdx.z;
+  const int b = !p.sorted ? blockIdx.z : p.B <= 64 ? nth_longest(p.lens, p.B, blockIdx.z, lane) : nearly_longest(p.lens, p.B, blockIdx.z, lane);
   const TreeBlock block(p, b);
   const int len = min(max(p.lens[b], 0), p.cache.rows), n_pre = (len + 15) / 16, n_all = n_pre + (p.tree.k ? 1 : 0);
   const int cnt = block.cnt, rows = cnt * p.gq, most = p.n * p.gq;
@@ -363,7 +402,7 @@ cudaError_t launch_own(TreeAttnParams p, int n_sm, cudaStream_t st) {
   int S = 1;
   while (S < 8 && clusters * S < (int64_t)n_sm * C::kBlocks && p.cache.rows / (2 * S) >= 256) S *= 2;
   p.S = S;
-  p.sorted = p.B > 1 && p.B <= 64 && p.cache.rows > 128;
+  p.sorted = p.B > 1 && p.B <= 256 && p.cache.rows > 128;
   return launch_cluster(own_attn_kernel<HD, F32, Q8>, dim3(S, p.Hkv, p.B), C::NT, S, 0, st, p, p.pdl);
 }
 
