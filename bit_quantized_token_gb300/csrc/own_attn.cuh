@@ -314,41 +314,46 @@ __global__ void __launch_bounds__(Own<HD, F32, Q8>::NT, Own<HD, F32, Q8>::kBlock
       }
     } else {
       parts(x);
-      bool odd = false;  // of the tree, infinities and NaNs have to stay away from the rows that do not see them
+      // Of the tree, infinities and NaNs have to stay away from the rows that do not see them: zeros in the
+      // product, added to the others behind it.
+      uint32_t odd = 0;
+      auto bad = [](uint32_t v) {  // halves whose exponents are all ones
+        return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+      };
       if (tree) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int i = 0; i < HD / 64; ++i)
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              odd |= (vw[e][i][w] & 0x7F80u) == 0x7F80u || (vw[e][i][w] & 0x7F800000u) == 0x7F800000u;
+            for (int w = 0; w < 4; ++w) odd |= bad(vw[e][i][w]);
         odd = __any_sync(0xffffffffu, odd);
       }
-      if (!odd) {
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) product(4 * i + w, vw[0][i][w], vw[1][i][w], vw[2][i][w], vw[3][i][w]);
-      } else {  // one tree row at a time, added where it is seen
+      if (odd) {
 #pragma unroll 1
-        for (int j = 0; j < cnt; ++j) {
-          const bool mine = t == j / 2;  // the lane has its values
+        for (int j = 0; j < cnt; ++j)
 #pragma unroll
           for (int i = 0; i < HD / 64; ++i)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const uint32_t v = mine ? (j & 1 ? vw[1][i][w] : vw[0][i][w]) : 0u;
-              const uint32_t a0 = j & 1 ? v << 16 : v & 0xFFFFu, a1 = j & 1 ? v & 0xFFFF0000u : v >> 16;
-              float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int k = 0; k < NP; ++k) mma_16816(y, a0, a1, 0u, 0u, lo[k], 0u);
+              const uint32_t mine = j & 1 ? vw[1][i][w] : vw[0][i][w];  // the lane t = j / 2 has it
+              const uint32_t v = __shfl_sync(0xffffffffu, mine, (lane & 28) | (j >> 1)), is = bad(v);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (sees[e & 1] >> j & 1) o[4 * i + w][e] += y[e];
+                if ((e & 2 ? is >> 16 : is & 0xFFFFu) && (sees[e & 1] >> j & 1))
+                  o[4 * i + w][e] += __uint_as_float(e & 2 ? v & 0xFFFF0000u : v << 16);
             }
-        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < HD / 64; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vw[e][i][w] &= ~bad(vw[e][i][w]);
       }
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) product(4 * i + w, vw[0][i][w], vw[1][i][w], vw[2][i][w], vw[3][i][w]);
     }
   }
   // ---- the warps' results joined

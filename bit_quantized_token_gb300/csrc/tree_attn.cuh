@@ -361,12 +361,14 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
     part = in4, ml = in_ml;
   }
   const int own = min(share, rows - rank * share);  // (none: 0 or less)
+  // no visible score (NaN scores alone leave no reference either, but a NaN sum, which has to count)
+  auto none = [](float2 ml) { return ml.x <= kNone && ml.y == ml.y; };
   for (int r = tid; r < own; r += NT) {
     float M = ml[r].x, L = 0.f;
     for (int k = 1; k < S; ++k) M = fmaxf(M, ml[k * share + r].x);
     for (int k = 0; k < S; ++k) {
       const float2 x = ml[k * share + r];
-      const float w = x.x <= kNone ? 0.f : ex2((x.x - M) * p.c);
+      const float w = none(x) ? 0.f : ex2((x.x - M) * p.c);
       L = fmaf(x.y, w, L);
       sw[k * share + r] = w;
     }
@@ -386,10 +388,10 @@ __device__ __forceinline__ void join_splits(const TreeAttnParams& p, const float
         o[k] = k < n && k < p.max_parts ? __ldcg(p.part_ml + k * p.part_rows + at) : make_float2(kNone, 0.f);
         top = fmaxf(top, o[k].x);
       }
-      const float own_w = M <= kNone ? 0.f : ex2((M - top) * p.c);
+      const float own_w = none(make_float2(M, L)) ? 0.f : ex2((M - top) * p.c);
 #pragma unroll
       for (int k = 0; k < TreeAttnParams::kMaxParts; ++k) {
-        o[k].y = o[k].x <= kNone ? 0.f : ex2((o[k].x - top) * p.c) * o[k].y;
+        o[k].y = none(o[k]) ? 0.f : ex2((o[k].x - top) * p.c) * o[k].y;
         sum += o[k].y;
       }
       sum = fmaf(own_w, L, sum);

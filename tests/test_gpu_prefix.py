@@ -164,6 +164,54 @@ def test_rows_that_nobody_sees(starts, gq, kv):
     assert torch.equal(p.out, clean)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q", ["bf16", "f32"])
+@pytest.mark.parametrize("starts,gq,n", [((0, 3), 2, 4), ((0, 3), 4, 4), ((0, 90), 2, 3)])
+def test_infinities_and_nan_of_the_tree(starts, gq, n, q, hd):
+    """Where they are seen they are the result, elsewhere they have no influence."""
+    p = Problem(starts=starts, gq=gq, n=n, hd=hd, q=q, P=150, plens=(140,))
+    p.words = [[1 << i for i in range(n)] for _ in range(p.B)]
+    p.t["mask"] = torch.tensor(p.words, device="cuda")
+    clean = p.call().clone()
+    v = p.rows["tree"][1]
+    v[1, :, 1, 5::7] = math.inf
+    v[1, :, 1, 6::7] = -math.inf
+    v[1, :, 2, 9] = math.nan
+    p.rows["tree"][0][2, :, 0] = math.nan  # every score of node 0's own row
+    out = p.call()
+    bq.tree_status()
+    want = clean.clone()
+    want[1, 1, :, 5::7] = math.inf
+    want[1, 1, :, 6::7] = -math.inf
+    want[1, 2, :, 9] = math.nan
+    want[2, 0] = math.nan
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out[~want.isnan()], want[~want.isnan()])
+
+
+@pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 3), 16), ((0, 90), 4)])
+@pytest.mark.parametrize("kv", ["bf16", "q8"])
+def test_a_nan_query_is_its_rows_result(starts, gq, kv):
+    for lens, tree in (((17,), True), ((0,), False)):
+        p = Problem(starts=starts, gq=gq, kv=kv, lens=lens, tree=tree)
+        clean = p.call().clone()
+        p.q[1, 0, 0] = math.nan
+        out = p.call()
+        bq.tree_status()
+        assert out[1, 0, 0].isnan().all()
+        out[1, 0, 0] = clean[1, 0, 0]
+        assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("B,gq,hd,kv", [(100, 4, 64, "bf16"), (256, 1, 128, "bf16"), (70, 2, 128, "q8"), (300, 2, 64, "bf16")])
+def test_many_sequences_of_rising_lengths(B, gq, hd, kv):
+    lens = [b * 300 // B for b in range(B)]
+    p = Problem(starts=(0, B - 3), B=B, gq=gq, hd=hd, kv=kv, P=130, plens=(129,), own=300, lens=lens, Hkv=1)
+    p.call()
+    p.check()
+    assert torch.equal(p.out, p.call())
+
+
 @pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 90), 4)])
 def test_scores_of_any_size(starts, gq):
     """Scores far apart, in the prefix or in the own rows: one key takes it all."""
