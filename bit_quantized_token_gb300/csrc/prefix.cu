@@ -7,13 +7,15 @@
 
 namespace llmq {
 
-constexpr int kWideFrom = 128;
-
 cudaError_t launch_prefix_attn(const TreeAttnParams& first, const TreeAttnParams& second, int hd, bool f32, bool q8,
                                int n_sm, cudaStream_t st) {
-  // Rows of a kv head that a group can have: from 128 on the wide kernel.
+  // By the rows of a kv head that a group can have. The tree attention's kernel splits the keys further, the wide one
+  // reads them once for 256 rows. Measured, wide / narrow, us a call: 64 dims, 4 kv heads, 128 rows behind 2048 /
+  // 8192 prefix rows 12.6 / 12.9, 20.7 / 18.0; 256 rows 15.3 / 14.2, 26.0 / 20.5; 512 rows 15.5 / 17.7, 26.2 / 27.8;
+  // 128 dims, 8 kv heads, 128 rows 18.5 / 19.1, 27.7 / 29.1; 256 rows 28.9 / 29.2, 42.4 / 48.3.
+  const int wide_from = hd == 64 ? 257 : 128;
   const int64_t rows = (int64_t)first.nodes * first.gq;
-  const bool wide = !f32 && !q8 && rows >= kWideFrom && first.B <= kWideGroups &&
+  const bool wide = !f32 && !q8 && rows >= wide_from && first.B <= kWideGroups &&
                     (rows / kWideRows + first.B) * first.Hkv * (first.cache.rows / 128 + 1) < (1ll << 31) &&
                     rows * first.Hkv < (1ll << 30);
   const cudaError_t e = !wide ? launch_tree_attn(first, hd, f32, q8, n_sm, st)

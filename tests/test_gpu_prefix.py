@@ -126,6 +126,7 @@ CASES = [
     dict(starts=(0, 40), n=1, P=700, plens=(650,), gq=4, Hkv=2, lens=(0, 1, 39)),  # 160 rows a kv head
     dict(starts=(0, 33, 50), n=2, P=515, plens=(515, 384), gq=7, Hkv=1, hd=128),
     dict(starts=(0, 100, 130, 131), n=1, P=1100, plens=(1100, 1024, 999), gq=8, Hkv=2),
+    dict(starts=(0, 65, 130), n=1, P=700, plens=(650, 0), gq=4, Hkv=2, lens=(0, 1, 39)),  # 520 rows of 64 dims
     dict(starts=(0, 129), n=1, P=1290, plens=(1283,), gq=2, Hkv=2, hd=128, tree=False),
     dict(starts=(0, 20), n=7, P=256, plens=(256,), gq=2, kv="q8", hd=64),
     dict(starts=(0, 3), P=300, scale=-0.3, q="f32"),
@@ -141,7 +142,7 @@ def test_against_the_formula(i):
     p.check()
 
 
-@pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 90), 4)])
+@pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 90), 4), ((0, 130), 4)])
 @pytest.mark.parametrize("kv", ["bf16", "q8"])
 def test_rows_that_nobody_sees(starts, gq, kv):
     """Infinities and NaN behind the prefix's, the cache's and the tree's ends have no influence."""
@@ -166,7 +167,7 @@ def test_rows_that_nobody_sees(starts, gq, kv):
 
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("q", ["bf16", "f32"])
-@pytest.mark.parametrize("starts,gq,n", [((0, 3), 2, 4), ((0, 3), 4, 4), ((0, 90), 2, 3)])
+@pytest.mark.parametrize("starts,gq,n", [((0, 3), 2, 4), ((0, 3), 4, 4), ((0, 90), 2, 3), ((0, 130), 2, 3)])
 def test_infinities_and_nan_of_the_tree(starts, gq, n, q, hd):
     """Where they are seen they are the result, elsewhere they have no influence."""
     p = Problem(starts=starts, gq=gq, n=n, hd=hd, q=q, P=150, plens=(140,))
@@ -189,7 +190,7 @@ def test_infinities_and_nan_of_the_tree(starts, gq, n, q, hd):
     assert torch.equal(out[~want.isnan()], want[~want.isnan()])
 
 
-@pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 3), 16), ((0, 90), 4)])
+@pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 3), 16), ((0, 90), 4), ((0, 130), 4)])
 @pytest.mark.parametrize("kv", ["bf16", "q8"])
 def test_a_nan_query_is_its_rows_result(starts, gq, kv):
     for lens, tree in (((17,), True), ((0,), False)):
@@ -212,7 +213,7 @@ def test_many_sequences_of_rising_lengths(B, gq, hd, kv):
     assert torch.equal(p.out, p.call())
 
 
-@pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 90), 4)])
+@pytest.mark.parametrize("starts,gq", [((0, 3), 2), ((0, 90), 4), ((0, 130), 4)])
 def test_scores_of_any_size(starts, gq):
     """Scores far apart, in the prefix or in the own rows: one key takes it all."""
     for where in ("prefix", "cache"):
