@@ -27,8 +27,9 @@ namespace {
 // format and roundings. A scale past fp16's range saturates (values beyond 8.3e6
 // become the largest that the row can hold), a NaN makes its 32 values NaN.
 //
-// Bound by HBM for many tokens (8192 tokens of 16/8 heads x 128 in bf16, norms and
-// rotation), by the launch for few.
+// Bound by HBM and its own instructions for many tokens (8192 of 16/8 heads x 128 in bf16, norms and rotation:
+// 30 us, 4.4 TB/s; a lane that held four neighbouring dims instead took 74), by the launch for few (one token of 32/4
+// heads x 64 2.6 us, 32 of 16/8 heads x 128 into int8 rows 4.3).
 constexpr int kAppendThreads = 128;
 
 // eight values, of which the loads come before any use
@@ -214,71 +215,83 @@ __global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const __grid_
 }
 
 // ---- read ----------------------------------------------------------------------
-// A lane takes 16 bytes of a row: 8 bf16 values or 16 codes and their scale;
-// four rows of a thread in flight. Rows run over (token, head, K or V) of a layer,
-// so that neighbouring ones write neighbouring outputs. A token whose sequence or
-// row is out of range reads zeros.
-constexpr int kReadThreads = 256, kReadRows = 4;
+// A lane takes eight values of a K row and of the V row beside it (one index for both: the
+// index arithmetic of every row by itself took half of the issue slots) and writes 16 bytes,
+// or 32, of each output; two such pairs of a thread in flight. Rows run over (token, head) of
+// a layer, so that neighbouring ones write neighbouring outputs. A token whose sequence
+// or row is out of range reads zeros.
+//
+// Bound by HBM: 4099 tokens x 28 layers x 8 heads x 128 of int8 rows to bf16 124 us (5.8 TB/s, 85 % of
+// a copy's; 121 / 124 / 139 with one, two and four pairs in flight, but fp32 231 / 217 / 230), of bf16 rows
+// 136 us (6.9 TB/s); by the launch for few: 37 tokens x 8 layers x 4 heads x 64 2.6 us.
+constexpr int kReadThreads = 256, kReadRows = 2;
+
+// the values of eight bf16 or, times f, of eight codes (0 times an infinite scale is NaN, as in a product)
+template <bool Q8>
+__device__ __forceinline__ void values_of(float* y, uint4 x, float f) {
+  if constexpr (Q8) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {  // bytes behind 2^23, less 2^23 + 128
+      const uint32_t codes = (e < 4 ? x.x : x.y) ^ 0x80808080u;
+      y[e] = __uint_as_float(__byte_perm(codes, 0x4B000000u, 0x7440 + (e & 3)));
+      y[e + 1] = __uint_as_float(__byte_perm(codes, 0x4B000000u, 0x7441 + (e & 3)));
+      add2(y[e], y[e + 1], y[e], y[e + 1], -8388736.f, -8388736.f);
+      mul2(y[e], y[e + 1], y[e], y[e + 1], f);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[2 * e] = __uint_as_float((&x.x)[e] << 16);
+      y[2 * e + 1] = __uint_as_float((&x.x)[e] & 0xFFFF0000u);
+    }
+  }
+}
 
 template <int HD, bool Q8>
 __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const ReadParams p) {
-  constexpr int VPL = Q8 ? 16 : 8, LPR = HD / VPL, RPB = kReadThreads / LPR;  // values of a lane; rows of a block's pass
+  constexpr int LPR = HD / 8, RPB = kReadThreads / LPR;  // lanes of a row; rows of a block's pass
   pdl_wait();
   pdl_trigger();
-  const int c = threadIdx.x % LPR, l = blockIdx.y;
-  const int64_t n = (int64_t)2 * p.T * p.H, first = (int64_t)blockIdx.x * RPB * kReadRows + threadIdx.x / LPR;
-  uint4 x[kReadRows];
-  float f[kReadRows];
+  const int c = threadIdx.x % LPR, l = blockIdx.y, n = p.T * p.H;
+  const int64_t first = (int64_t)blockIdx.x * RPB * kReadRows + threadIdx.x / LPR;
+  uint4 x[kReadRows][2];
+  float f[kReadRows][2];
+  int64_t to[kReadRows];
 #pragma unroll
   for (int u = 0; u < kReadRows; ++u) {
     const int64_t i = first + u * RPB;
-    x[u] = make_uint4(0u, 0u, 0u, 0u);
-    f[u] = 0.f;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) x[u][kv] = make_uint4(0u, 0u, 0u, 0u), f[u][kv] = 0.f;
+    to[u] = -1;
     if (i >= n) continue;
-    const int kv = i >= (int64_t)p.T * p.H, r = (int)(i - (kv ? (int64_t)p.T * p.H : 0)), t = p.by_heads.div(r), h = r - t * p.H;
+    const int t = p.by_heads.div((int)i), h = (int)i - t * p.H;
+    to[u] = l * p.o_layer + (int64_t)t * p.o_tok + h * p.o_head + 8 * c;
     const int seq = p.seqs[t], row = p.rows[t];
     if (seq < 0 || seq >= p.n_seq || row < 0 || row >= p.cache.rows) continue;
-    const int64_t at = (int64_t)seq * p.cache.seq + l * p.layer + h * p.cache.head + (int64_t)row * p.cache.row + VPL * c;
-    x[u] = __ldcs(reinterpret_cast<const uint4*>((kv ? p.cache.v : p.cache.k) + (Q8 ? 1 : 2) * at));
-    if constexpr (Q8)
-      f[u] = __half2float(__ushort_as_half((kv ? p.cache.vs : p.cache.ks)[(int64_t)seq * p.cache.sseq + l * p.slayer +
-                                                                          h * p.cache.shead + (int64_t)row * p.cache.srow + c / 2]));
+    const int64_t at = (int64_t)seq * p.cache.seq + l * p.layer + h * p.cache.head + (int64_t)row * p.cache.row + 8 * c;
+    if constexpr (!Q8) {
+      x[u][0] = __ldcs(reinterpret_cast<const uint4*>(p.cache.k + 2 * at));
+      x[u][1] = __ldcs(reinterpret_cast<const uint4*>(p.cache.v + 2 * at));
+    } else {
+      const uint2 k = __ldcs(reinterpret_cast<const uint2*>(p.cache.k + at)), v = __ldcs(reinterpret_cast<const uint2*>(p.cache.v + at));
+      x[u][0].x = k.x, x[u][0].y = k.y, x[u][1].x = v.x, x[u][1].y = v.y;
+      const int64_t s = (int64_t)seq * p.cache.sseq + l * p.slayer + h * p.cache.shead + (int64_t)row * p.cache.srow + c / 4;
+      f[u][0] = __half2float(__ushort_as_half(p.cache.ks[s]));
+      f[u][1] = __half2float(__ushort_as_half(p.cache.vs[s]));
+    }
   }
 #pragma unroll
   for (int u = 0; u < kReadRows; ++u) {
-    const int64_t i = first + u * RPB;
-    if (i >= n) continue;
-    const int kv = i >= (int64_t)p.T * p.H, r = (int)(i - (kv ? (int64_t)p.T * p.H : 0)), t = p.by_heads.div(r), h = r - t * p.H;
-    const int64_t at = l * p.o_layer + (int64_t)t * p.o_tok + h * p.o_head + VPL * c;
-    void* out = kv ? p.v : p.k;
-    if constexpr (!Q8) {
-      if (!p.f32) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = x[u];
+    if (to[u] < 0) continue;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      void* out = kv ? p.v : p.k;
+      if (!Q8 && !p.f32) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to[u]) = x[u][kv];
       } else {
         float y[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = __uint_as_float((&x[u].x)[e] << 16);
-          y[2 * e + 1] = __uint_as_float((&x[u].x)[e] & 0xFFFF0000u);
-        }
-        store4(out, at, y, true);
-        store4(out, at + 4, y + 4, true);
-      }
-    } else {
-      float y[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e)  // (0 times an infinite scale is NaN, as it would be in a product)
-        y[e] = (float)(int8_t)((&x[u].x)[e / 4] >> (8 * (e & 3))) * f[u];
-      if (p.f32) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) store4(out, at + e, y + e, true);
-      } else {
-        uint32_t z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = bf16_pair(y[2 * e], y[2 * e + 1]);
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-        dst[0] = make_uint4(z[0], z[1], z[2], z[3]);
-        dst[1] = make_uint4(z[4], z[5], z[6], z[7]);
+        values_of<Q8>(y, x[u][kv], f[u][kv]);
+        store8(out, to[u], y, p.f32);
       }
     }
   }
@@ -288,9 +301,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const ReadParams 
 
 cudaError_t launch_append_kv(AppendParams& p, int hd, bool q8, int n_sm, cudaStream_t st) {
   const int rpw = 512 / hd, heads = p.Hq + 2 * p.Hkv, groups = (heads + rpw - 1) / rpw;
-  // One pass a warp while the warps fit the SMs at once (16 a SM); a warp that takes
-  // more rows of its token computes the token's angles once for them.
-  const int64_t per = (int64_t)p.T * groups / (16 * (int64_t)n_sm);
+  // One pass a warp while there are fewer than six warps an SM; a warp that takes more rows of its token computes the
+  // token's angles once for them (8192 tokens of 16/8 heads x 128: 61 / 40 / 32 / 30 us with 1, 2, 4, 8 passes, 512: 6.1
+  // / 5.7 / 4.7 / 6.0, 64: 2.8 / 3.3 / 4.1 / 5.9).
+  const int64_t per = (int64_t)p.T * groups / (6 * (int64_t)n_sm);
   p.passes = (int)(per < 1 ? 1 : per < groups ? per : groups);
   const int64_t warps = (int64_t)p.T * ((heads + rpw * p.passes - 1) / (rpw * p.passes));
   const dim3 grid((unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
@@ -304,7 +318,7 @@ cudaError_t launch_append_kv(AppendParams& p, int hd, bool q8, int n_sm, cudaStr
 }
 
 cudaError_t launch_read_kv(const ReadParams& p, int hd, bool q8, cudaStream_t st) {
-  const int64_t rows = (int64_t)2 * p.T * p.H, per = (int64_t)kReadRows * kReadThreads * (q8 ? 16 : 8) / hd;
+  const int64_t rows = (int64_t)p.T * p.H, per = (int64_t)kReadRows * kReadThreads * 8 / hd;
   const auto kern = hd == 64 ? (q8 ? read_kv_kernel<64, true> : read_kv_kernel<64, false>)
                              : (q8 ? read_kv_kernel<128, true> : read_kv_kernel<128, false>);
   return launch_cluster(kern, dim3((unsigned)((rows + per - 1) / per), p.L), kReadThreads, 1, 0, st, p, p.pdl);
