@@ -20,7 +20,8 @@
 // in shared memory, then as those of the tree attention are.
 //
 // (tcgen05 instructions hold 128 rows, a tile's loads, barriers and tensor memory:
-// about 7 us a CTA whatever its rows are, and two CTAs on an SM.)
+// about 7 us a CTA whatever its rows are, and two CTAs on an SM: 256 sequences of 32/4 heads x 64 with 1 to 300
+// rows of their own take them 27 us, this kernel 13; DRAM at 28 %, issue slots 38 %, the rest is the loads' latency.)
 #pragma once
 #include "tree_attn.cuh"
 

@@ -21,6 +21,10 @@
 // Work: the (group, kv head, 256 rows, key tile) units in one row are cut into equal
 // ranges, one for each CTA, so that every SM has the same number whatever the sizes of the
 // groups; the pieces of a row tile (max_parts at most) are joined by the second part.
+//
+// Measured: 256 sequences of 32/4 heads x 64 behind 16384 rows 49 us of the call's 62 (34.4 GFLOP, 700 TFLOP/s). Bound by
+// the softmax warps: about 1,000 cycles for a block of 128 rows x 64 keys (exponentials alone 512 for the two tiles) and 400 between blocks,
+// tensor pipe 32 % and issue slots 43 % busy; 16 softmax warps instead of 8 gained nothing.
 #pragma once
 #include "tree_attn_q8.cuh"
 
@@ -28,7 +32,9 @@ namespace llmq {
 
 constexpr int kWideRows = 256;       // query rows of a CTA
 constexpr int kWideGroups = 1024;    // most groups
-// Pieces that a row tile may be cut into, of all n heads rows: few rows need them to fill the SMs.
+// Pieces that a row tile may be cut into, of all n heads rows: few rows need them to fill the SMs, many have
+// tiles enough, and their pieces would be memory (8, 4, 1 piece, us a call, 32/4 heads x 64: 2048 rows behind 8192 26 / 54 /
+// 95, 8192 behind 16384 62 / 105 / 191, 14336 behind 4096 45 / 47 / 65, 32768 87 / 85 / 84, 57344 132 / 129 / 142).
 inline int wide_parts(int64_t rows) { return rows <= 10240 ? 8 : rows <= 40960 ? 4 : 1; }
 
 template <int HD>

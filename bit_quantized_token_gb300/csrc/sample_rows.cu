@@ -26,6 +26,11 @@
 // in some 10^5 .. 10^6 falls on another side than with exact sums. fp32 sums would lose one draw
 // in 2,000, and fp64 has 1/64 of fp32's lanes here. Terms below 2^-4 of the largest
 // need no more than fp32 for their place in the bucket.
+//
+// Measured: 1 x 32000 14.8 us (of which the CTAs' exchanges and the sort of some hundred entries about 12), 32 x 151936
+// 32, 256 x 151936 130 at temperature 0.8 and top-p 0.95: two passes of some 70 instructions a warp's 32 logits,
+// 64 % of the issue slots, HBM at 25 %. The second pass reads memory again (156 MB of rows and 129 MB of L2). A form
+// that kept the logits in shared memory, and so took up to 16 CTAs a row, needed 391 us for the last.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
