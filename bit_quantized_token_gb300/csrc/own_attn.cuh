@@ -297,8 +297,16 @@ __global__ void __launch_bounds__(Own<HD, F32, Q8>::NT, Own<HD, F32, Q8>::kBlock
     auto product = [&](int i, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
       const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
       const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+      if constexpr (F32) {  // the products cut off where an add rounds: over many steps sums would come out low
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < NP; ++k) mma_16816(o[i], a0, a1, a2, a3, lo[k], hi[k]);
+        for (int k = NP - 1; k >= 0; --k) mma_16816(y, a0, a1, a2, a3, lo[k], hi[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] += y[e];
+      } else {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) mma_16816(o[i], a0, a1, a2, a3, lo[k], hi[k]);
+      }
     };
     if constexpr (Q8) {
 #pragma unroll

@@ -204,6 +204,22 @@ def test_a_nan_query_is_its_rows_result(starts, gq, kv):
         assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("kv,hd,own", [("bf16", 64, 16000), ("bf16", 128, 380), ("q8", 128, 9000)])
+def test_long_fp32_sums_do_not_come_out_low(kv, hd, own):
+    """Positive values, so that what is cut off adds up: a step's three products lose less than 2^-23 of its sum each,
+    always downwards; all other additions round, either way. The mean error is below 4 2^-23."""
+    p = Problem(starts=(0, 1), B=1, gq=4, hd=hd, q="f32", kv=kv, P=16, plens=(1,), own=own, lens=(own,), tree=False)
+    p.q *= 0.05
+    for name in ("prefix", "cache"):
+        p.rows[name][1].abs_()
+    p.call()
+    bq.tree_status()
+    K, V = (torch.cat([values(p.rows["prefix"][i], p.rows["prefix"][2 + i])[0][:, :1],
+                       values(p.rows["cache"][i], p.rows["cache"][2 + i])[0]], 1) for i in (0, 1))
+    want = (torch.softmax(p.q[0, 0].double().view(2, 4, hd) @ K.transpose(1, 2) * hd ** -0.5, -1) @ V).view(8, hd)
+    assert abs(float(((p.out[0, 0].double() - want) / want).mean())) < 2.0 ** -21
+
+
 @pytest.mark.parametrize("B,gq,hd,kv", [(100, 4, 64, "bf16"), (256, 1, 128, "bf16"), (70, 2, 128, "q8"), (300, 2, 64, "bf16")])
 def test_many_sequences_of_rising_lengths(B, gq, hd, kv):
     lens = [b * 300 // B for b in range(B)]
