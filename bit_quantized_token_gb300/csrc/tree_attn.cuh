@@ -42,6 +42,8 @@
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "attn_mma.cuh"
 #include "tree.cuh"
 
@@ -1062,7 +1064,11 @@ cudaError_t launch_tree_tc_t(TreeAttnTcParams& tp, int n_sm, cudaStream_t st) {
     // (32 sequences x 8 kv heads, 17 tiles: 37 / 39 / 45 us for 1 / 2 / 3; 16 x 4 x 4 row
     // tiles, 65 tiles: 104 / 85 / 94 / 102 for 1 to 4; 32 clusters of 34 fp32 tiles 12.3 /
     // 12.1 / 24 for 4 / 8 / 16).
-    while (S < kMaxSplits && S < tiles && (clusters * S < n_sm || (clusters * S < 2 * n_sm && tiles / (2 * S) >= 16))) S *= 2;
+    // The first of two parts: two tiles or more a CTA and eight splits at most, since the second part's CTAs want
+    // places too (16 sequences of 2 rows, 8 kv heads x 128 behind 4096 rows: 16.0 / 21.8 us for 8 / 16; 32 of them
+    // behind 512 12.5 / 12.4 / 15.2 for 2, 4, 8; 8 of 8 rows, 4 x 64 behind 2048 11.3 / 17.2 for 8 / 16).
+    const int most = p.part == TreeAttnParams::kFirst ? std::min(8, (tiles + 1) / 2) : std::min(kMaxSplits, tiles);
+    while ((p.part == TreeAttnParams::kFirst ? 2 * S <= most : S < most) && (clusters * S < n_sm || (clusters * S < 2 * n_sm && tiles / (2 * S) >= 16))) S *= 2;
   } else {
     static ClusterCount at_once;
     S = lone_splits(clusters, tiles, [&](int s) { return at_once.get(kern, s, C::NT, C::kSmem); });
