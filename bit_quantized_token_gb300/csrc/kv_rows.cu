@@ -28,8 +28,9 @@ namespace {
 // become the largest that the row can hold), a NaN makes its 32 values NaN.
 //
 // Bound by HBM and its own instructions for many tokens (8192 of 16/8 heads x 128 in bf16, norms and rotation:
-// 30 us, 4.4 TB/s; a lane that held four neighbouring dims instead took 74), by the launch for few (one token of 32/4
-// heads x 64 2.6 us, 32 of 16/8 heads x 128 into int8 rows 4.3).
+// 28 us, 4.9 TB/s, into int8 rows 41; a lane that held four neighbouring dims instead took 74; packed products of two
+// values no less), by the launch for few (one token of 32/4 heads x 64 2.8 us, 32 of 16/8 heads x 128 into int8 rows 4.2).
+// Seven CTAs on an SM, in 72 registers: 30.9 / 27.8 / 27.7 / 33.0 us with the compiler's 80, 72, 64 and 48.
 constexpr int kAppendThreads = 128;
 
 // eight values, of which the loads come before any use
@@ -87,7 +88,7 @@ __device__ __forceinline__ float2 turn_of(uint64_t angle) {
 }
 
 template <int HD, bool Q8, bool F32>
-__global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 7) append_kv_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = HD / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   pdl_wait();
   pdl_trigger();
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const ReadParams 
 cudaError_t launch_append_kv(AppendParams& p, int hd, bool q8, int n_sm, cudaStream_t st) {
   const int rpw = 512 / hd, heads = p.Hq + 2 * p.Hkv, groups = (heads + rpw - 1) / rpw;
   // One pass a warp while there are fewer than six warps an SM; a warp that takes more rows of its token computes the
-  // token's angles once for them (8192 tokens of 16/8 heads x 128: 61 / 40 / 32 / 30 us with 1, 2, 4, 8 passes, 512: 6.1
+  // token's angles once for them (with 80 registers, 8192 tokens of 16/8 heads x 128: 61 / 40 / 32 / 30 us with 1, 2, 4, 8 passes, 512: 6.1
   // / 5.7 / 4.7 / 6.0, 64: 2.8 / 3.3 / 4.1 / 5.9).
   const int64_t per = (int64_t)p.T * groups / (6 * (int64_t)n_sm);
   p.passes = (int)(per < 1 ? 1 : per < groups ? per : groups);
