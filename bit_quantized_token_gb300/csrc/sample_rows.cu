@@ -755,11 +755,12 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
   }
   // ---- the second pass: their tokens to the first CTA
   // (from the end on: what was read last is in L2 still, where the rows together are larger)
-  // the gathered buckets, a little wider (y is within 2^-8 of the exact place): the draw's, top_p's, and the others'
-  const float b0 = (float)tm.b, g0 = fmaxf(b0 + (float)bl - 0.01f, lo_y), g1 = fminf(b0 + (float)bh + 1.01f, hi_y);
-  const float g2 = fmaxf(b0 + (float)pl - 0.01f, lo_y), g3 = by_p ? fminf(b0 + (float)ph + 1.01f, hi_y) : -INFINITY;
+  // the gathered buckets, a little wider (y is within 2^-24 of its size, and as much again for the ratio's lower part, of the
+  // exact place, and these numbers are rounded too): the draw's, top_p's, and the others'
+  const float b0 = (float)tm.b, aside = 0.01f + fabsf(b0) * 2.4e-7f, g0 = fmaxf(b0 + (float)bl - aside, lo_y), g1 = fminf(b0 + (float)bh + 1.f + aside, hi_y);
+  const float g2 = fmaxf(b0 + (float)pl - aside, lo_y), g3 = by_p ? fminf(b0 + (float)ph + 1.f + aside, hi_y) : -INFINITY;
   const int other = by_k && by_m ? min(bk, bm) : by_k ? bk : bm, others = by_k && by_m ? max(bk, bm) : other;
-  const float g4 = fmaxf(b0 + (float)other - 0.01f, lo_y), g5 = by_k || by_m ? fminf(b0 + (float)others + 1.01f, hi_y) : -INFINITY;
+  const float g4 = fmaxf(b0 + (float)other - aside, lo_y), g5 = by_k || by_m ? fminf(b0 + (float)others + 1.f + aside, hi_y) : -INFINITY;
   constexpr int step = kSampU * kSampNT;
   const int last = n > 0 ? (n - 1) / step * step : -1;
   if (last >= 0) load(cur, last);

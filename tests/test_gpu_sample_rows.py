@@ -133,6 +133,17 @@ def test_flat_rows(V, sd):
               u=rng.random(R).astype(np.float32))
 
 
+@pytest.mark.parametrize("at", [100.0, -3e3, 2e4])
+def test_logits_far_from_zero(at):
+    """Bucket numbers are large where the logits are, or where the buckets are fine: their borders must not be missed."""
+    R, V = 24, 26105
+    for sd in (0.01, 0.3, 2.5):
+        rng = np.random.default_rng(int(abs(at)))
+        for x in (logits(R, V, sd, 3), logits(R, V, sd, 4).to(torch.bfloat16).float()):
+            check(x + at, T=rng.choice([0.7, 1.0, 1.79, 4.0], R), k=rng.choice([0, 0, 900, V // 2], R),
+                  p=rng.choice([1.0, 0.95, 0.5], R), m=rng.choice([0.0, 0.0, 0.01], R), u=rng.random(R).astype(np.float32))
+
+
 def test_odd_values():
     R, V = 9, 7001
     x = logits(R, V, 2.0, 2)
