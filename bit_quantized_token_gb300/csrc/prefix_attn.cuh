@@ -209,7 +209,9 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
   WideSegment seg{};
   // Key tiles are counted over all segments. K and V have rings of their own: a warp
   // that waits for some tiles of a ring waits for all of them, in order, since a wait for a
-  // phase whose predecessor is not over is over at once.
+  // phase whose predecessor is not over is over at once. (So the warps that issue wait for
+  // tiles, those of row tiles without rows too, and the softmax warps, which pass over
+  // such segments, never do.)
   uint32_t base = 0;  // key tiles of the segments before
   auto landed = [&](int kv, uint32_t i) { return tc_wait_warp(full + 4 * kv + i % NST, (i / NST) & 1, s_abort, p.status); };
   auto blocks = [&]() { return min(2 * (seg.k1 - seg.k0), (seg.len - seg.k0 * BK + KB - 1) / KB); };
@@ -287,7 +289,20 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         for (int j = 0; j < nb && ok; ++j) {
           const uint32_t b = done + j, x = b % NBUF, i = base + (j >> 1), slot = i % NST;
           if (!(j & 1)) ok = landed(1, i);
-          ok = ok && tc_wait_warp(p_full + 3 * t + x, (b / NBUF) & 1, s_abort, p.status);
+          if (!ok) break;
+          const int left = seg.len - seg.k0 * BK - j * KB;  // keys from this block on
+          if (left < KB) {  // V rows that are not there become zeros: 0 times whatever lies there need not be 0
+            // (both row tiles' warps write them, the same; the tile goes back only when both have multiplied it)
+#pragma unroll 1
+            for (int c = lane; c < (KB - left) * (HD / 8); c += 32) {
+              const int row = (j & 1) * KB + left + c / (HD / 8), ch = c % (HD / 8);
+              *reinterpret_cast<uint4*>(sring + (NST + slot) * C::kTile + (ch / 8) * C::kUnit + row * 128 + 16 * (ch & 7)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+            __syncwarp();
+          }
+          ok = tc_wait_warp(p_full + 3 * t + x, (b / NBUF) & 1, s_abort, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t db = tc_desc(ur + slot * C::kTile + (j & 1) * KB * 128, C::kUnit, 1024, 2);
@@ -313,11 +328,8 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     bool ok = true;
     auto pv_done = [&](uint32_t b) { return tc_wait_warp(o_done + 3 * t + b % NBUF, (b / NBUF) & 1, s_abort, p.status); };
     while (ok && plan.next(seg)) {
-      const int n = seg.k1 - seg.k0, nb = blocks();
-      if (t * 128 >= seg.rows) {
-        base += n;
-        continue;
-      }
+      const int nb = blocks();
+      if (t * 128 >= seg.rows) continue;
       const int row = seg.row0 + t * 128 + r, node = p.by_gq.div(row), h = seg.hkv * p.gq + row - node * p.gq;
       const bool there = t * 128 + r < seg.rows;
       {  // Q: 128-byte rows of 64 dims, chunks permuted as by TMA's 128-byte swizzle
@@ -410,19 +422,6 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         }
         if (!ok) break;
         l += sum;
-        if (left < KB) {  // V rows that are not there become zeros: 0 times whatever lies there need not be 0
-          // (V of NST tiles before is there: these scores were made behind a P V of it, or of a later tile)
-          const uint32_t iv = base + (j >> 1), slot = iv % NST;
-          ok = landed(1, iv);
-          if (!ok) break;
-#pragma unroll 1
-          for (int c = r; c < (KB - left) * (HD / 8); c += 128) {
-            const int row_v = (j & 1) * KB + left + c / (HD / 8), ch = c % (HD / 8);
-            *reinterpret_cast<uint4*>(sring + (NST + slot) * C::kTile + (ch / 8) * C::kUnit + row_v * 128 + 16 * (ch & 7)) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_async_smem();
-        }
         tc_st32(tS, pk);
         tc_wait_st();
         tc_fence_before();
@@ -453,7 +452,6 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         if (seg.piece == 0) p.part_n[at] = seg.pieces;
       }
       tc_fence_before();
-      base += n;
     }
   }
   __syncwarp();

@@ -1,0 +1,42 @@
+"""prefix_attention over batches of many groups of unlike sizes (GPU); tolerances as in test_gpu_prefix."""
+import math
+
+import pytest
+import torch
+
+import bit_quantized_token_gb300 as bq
+from test_gpu_prefix import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    bq.build()
+    torch.cuda.set_device(0)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("short", [100, 37, 127])
+def test_small_groups_before_large_ones(hd, short):
+    """Groups of at most 128 query rows of a kv head behind long prefixes, each before one of more rows behind a prefix
+    that ends inside a key tile: the second half of a CTA's rows has nothing to do for many key tiles, then meets a tile
+    of which the rows behind the prefix's end are infinite or NaN. The same bits as with finite ones there, every time."""
+    starts = [0]
+    for _ in range(6):
+        starts += [starts[-1] + 20, starts[-1] + 70]
+    p = Problem(starts=tuple(starts), gq=4, hd=hd, Hkv=8, P=2048, plens=(2048, short), own=8, lens=(3, 8, 0), tree=False)
+    p.call()
+    p.check()
+    clean = p.out.clone()
+    for g in range(1, p.G, 2):
+        for m in (0, 1):
+            p.rows["prefix"][m][g, :, short:] = math.nan
+            p.rows["prefix"][m][g, :, short + 1::2] = math.inf
+    outs = [torch.empty_like(clean) for _ in range(4)]
+    for i in range(100):
+        p.out = outs[i % 4]
+        p.call()
+        if i % 4 == 3:
+            assert all(torch.equal(o, clean) for o in outs), i
+    bq.tree_status()
