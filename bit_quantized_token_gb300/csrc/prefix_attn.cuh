@@ -85,13 +85,6 @@ struct WideGroup {
   __device__ int key_tiles() const { return (len + 127) / 128; }
   __device__ int row_tiles() const { return (rows + kWideRows - 1) / kWideRows; }
 };
-__device__ __forceinline__ WideGroup wide_group(const TreeAttnParams& p, int g) {
-  WideGroup x;
-  x.first = min(max(p.starts[g], 0), p.all);
-  x.rows = (min(max(p.starts[g + 1], x.first), p.all) - x.first) * p.n * p.gq;
-  x.len = min(max(p.lens[g], 0), p.cache.rows);
-  return x;
-}
 struct WidePlan {
   const TreeAttnParams& p;
   const uint32_t* cum;      // [G + 1] units before a group
@@ -173,11 +166,24 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   } else if (warp == C::kTmaWarp) {  // units before each group
     uint32_t before = 0;
-    int most = 1;
+    int most = 1, begun = 0;
     bool none = false;
     for (int g0 = 0; g0 < p.B; g0 += 32) {
+      // No group begins before one ahead of it, whatever `starts` says: the groups are apart, so that their units
+      // stay within 32 bits and their rows within the queries'
+      const int g = g0 + lane;
+      int from = g < p.B ? min(max(p.starts[g], 0), p.all) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) from = max(from, __shfl_up_sync(0xffffffffu, from, o));
+      from = max(from, begun);
+      begun = __shfl_sync(0xffffffffu, from, 31);
       WideGroup own{0, 0, 0};
-      if (g0 + lane < p.B) groups[g0 + lane] = own = wide_group(p, g0 + lane);
+      if (g < p.B) {
+        own.first = from;
+        own.rows = (max(min(p.starts[g + 1], p.all), from) - from) * p.n * p.gq;
+        own.len = min(max(p.lens[g], 0), p.cache.rows);
+        groups[g] = own;
+      }
       const int kt = own.key_tiles();
       uint32_t u = kt > 0 ? (uint32_t)own.row_tiles() * (wp.whole ? 1 : kt) * p.Hkv : 0u, x = u;
       if (u) most = max(most, kt);
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(Wide<HD>::NT, 1) wide_attn_kernel(const __grid
         const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (g0 + lane < p.B) cum[g0 + lane] = before + x - u;
+      if (g < p.B) cum[g] = before + x - u;
       before += __shfl_sync(0xffffffffu, x, 31);
     }
     most = __reduce_max_sync(0xffffffffu, most);

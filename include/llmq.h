@@ -570,7 +570,8 @@ typedef struct {
   llm_tree_attention_args attention;  /* the queries, every sequence's own rows, its new tokens (tree, mask), the output */
   const llm_kv_view* prefix;    /* one layer, alike the cache: rows of its sequence g are those that group g shares */
   int32_t n_groups;             /* up to the prefix view's sequences */
-  const int32_t* starts;        /* [n_groups + 1] ascending: sequences starts[g] .. starts[g + 1] - 1 are group g */
+  const int32_t* starts;        /* [n_groups + 1] ascending: sequences starts[g] .. starts[g + 1] - 1 are group g
+                                 * (of others, the rows are whatever they come to; nothing else is written) */
   const int32_t* prefix_lens;   /* [n_groups] rows of each prefix (clamped to 0..rows) */
   void* workspace;              /* device memory, 32-byte aligned; calls that may overlap have one each */
   int64_t workspace_bytes;      /* at least llm_prefix_workspace's */

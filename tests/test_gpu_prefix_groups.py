@@ -40,3 +40,13 @@ def test_small_groups_before_large_ones(hd, short):
         if i % 4 == 3:
             assert all(torch.equal(o, clean) for o in outs), i
     bq.tree_status()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_groups_out_of_order_stay_apart(hd):
+    """Many rows: a group that would begin inside the ones ahead of it begins where they end, so that no two groups have
+    the same rows and all units together stay within the checked number."""
+    kw = dict(B=170, gq=4, hd=hd, P=300, plens=(300, 200, 77, 150), lens=(5, 0, 40))
+    p, want = Problem(starts=(0, 60, 20, 130, 170), **kw), Problem(starts=(0, 60, 60, 130, 170), **kw)
+    assert torch.equal(p.call(), want.call())
+    want.check()
