@@ -841,9 +841,12 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
     s.res_mass[2] = by_m ? mass_to(bm - 1) : all;  // or more, of min_p's own bucket
   }
   __syncthreads();
+  // up to and with entry j, of bucket b. An entry's weight is rounded and a bucket's mass is not the sum of them to the
+  // last bit: its last entry ends where it does, so that a border found between two buckets is found here too
   auto row_mass = [&](int j, int b) {
     const int f = s.start[b];
-    return mass_to(b - 1) + s.local[j] - (f ? s.local[f - 1] : 0ull);
+    const u64 end = mass_to(b);
+    return j + 1 == N || s.bucket[j + 1] != b ? end : min(mass_to(b - 1) + s.local[j] - (f ? s.local[f - 1] : 0ull), end);
   };
 #pragma unroll 1
   for (int j = tid; j < N; j += kSampNT) {
@@ -865,7 +868,7 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
     __syncthreads();
   }
   const u64 mass = min(min(s.res_mass[0], s.res_mass[1]), s.res_mass[2]), target = __umul64hi(mass, u_fix);
-  if (tid == 0) s.found = kSampleList;
+  if (tid == 0) s.found = max(N, 1) - 1;
   __syncthreads();
 #pragma unroll 1
   for (int j = tid; j < N; j += kSampNT) {
@@ -874,7 +877,7 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
   }
   __syncthreads();
   if (tid == 0) {
-    const u64 v = s.list[s.found < kSampleList ? s.found : 0];
+    const u64 v = s.list[s.found];
     const Term t = entry(v);
     p.tokens[row] = (int)~(uint32_t)v;
     if (p.probs)
