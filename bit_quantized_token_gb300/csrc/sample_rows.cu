@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
     }
     if (m == INFINITY) m = 3.402823466e38f;
     // logits of weight (2^-63 and more) that the buckets below the largest miss
-    const bool missed = (m - out) * ch < 63.f || (fine > 0 && (m - least) * chS >= (float)(kSampB - 2));
+    // (an infinite one is outside, and the difference times 0 at an infinite temperature says nothing)
+    const bool missed = out > m || (m - out) * ch < 63.f || (fine > 0 && (m - least) * chS >= (float)(kSampB - 2));
     crowd = !(fabsf(m * ch) < 32768.f) || (missed && turn == 1);
     if (crowd) break;
     if (!missed) {

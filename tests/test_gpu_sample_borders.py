@@ -1,4 +1,5 @@
 """sample_tokens where a border falls between two buckets of its histogram, or on odd values (GPU)."""
+import math
 from decimal import Decimal, getcontext
 
 import numpy as np
@@ -60,3 +61,16 @@ def test_borders_between_buckets():
         assert set(draw(xs, u, top_p=0.5)[0].tolist()) <= kept
         assert set(draw(xs, u, top_p=0.5, min_p=0.5)[0].tolist()) <= kept
         assert set(draw(xs, u, top_p=0.5, top_k=x.shape[1] - 1)[0].tolist()) <= kept
+
+
+@pytest.mark.parametrize("V,at", [(3000, 2999), (3000, 5), (9001, 5), (40000, 20001)])
+def test_an_infinite_logit_at_an_infinite_temperature(V, at):
+    """All tokens but those of -inf are alike; an infinite logit counts as the largest finite one."""
+    x = torch.zeros(8, V, device="cuda")
+    x[:, at] = math.inf
+    x[:, 7] = -math.inf
+    for u in (0.0, 0.5, 0.99):
+        token, prob = choose(x[0].cpu().numpy(), math.inf, 0, 1.0, 0.0, np.float32(u))
+        tokens, probs = draw(x, u, temperature=math.inf)
+        assert set(tokens.tolist()) == {token}
+        assert (abs(probs - prob) <= prob * 2.0 ** -20).all()
