@@ -49,6 +49,7 @@ constexpr int kSampTable = 2 * kSampB; // a CTA's buckets, by their number modul
 constexpr int kSampPer = kSampB / kSampNT;
 constexpr int kSampMaxSlice = 180000;
 constexpr int kSampU = 8;               // loads of a thread in flight
+constexpr float kLargest = 3.402823466e38f;  // what an infinite logit counts as
 constexpr int kSortRegs = 4;            // entries of a thread that are sorted in registers
 
 __constant__ const u64 kRoot32[32] = {  // 2^(63 - j/32)
@@ -264,7 +265,7 @@ __device__ __noinline__ void sample_crowd(const SampleRowsParams& p, SampShared&
   const u64 u_fix = __float2ull_rn(s.u * 18446744073709551616.f);
   auto logit = [&](int i) {
     const float l = i < n ? src[i] : -INFINITY;
-    return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
+    return l != l ? -INFINITY : fminf(l, kLargest);
   };
   if (tid == 0) s.key = by_m ? (u64)(s.y_min * 137438953472.0) : 0ull;  // of 32 buckets an octave, from the largest logit
   cl.sync();
@@ -518,11 +519,11 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
       load(next, i0 + kSampU * kSampNT);
 #pragma unroll
       for (int e = 0; e < kSampU; ++e) {
-        if (cur[e] > mx) mx = cur[e], at = i0 + e * kSampNT + tid;
+        if (cur[e] > mx && mx < kLargest) mx = fminf(cur[e], kLargest), at = i0 + e * kSampNT + tid;
         cur[e] = next[e];
       }
     }
-    u64 best = mx == -INFINITY ? 0 : ((u64)sample_key(fminf(mx, 3.402823466e38f)) << 32) | (uint32_t)~(first + at);
+    u64 best = mx == -INFINITY ? 0 : ((u64)sample_key(mx) << 32) | (uint32_t)~(first + at);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = max(best, (u64)__shfl_xor_sync(0xffffffffu, best, o));
     if (lane == 0) s.warp64[warp] = best;
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
       }
       return;
     }
-    if (m == INFINITY) m = 3.402823466e38f;
+    if (m == INFINITY) m = kLargest;
     // logits of weight (2^-63 and more) that the buckets below the largest miss
     // (an infinite one is outside, and the difference times 0 at an infinite temperature says nothing)
     const bool missed = out > m || (m - out) * ch < 63.f || (fine > 0 && (m - least) * chS >= (float)(kSampB - 2));

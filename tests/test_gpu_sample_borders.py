@@ -74,3 +74,13 @@ def test_an_infinite_logit_at_an_infinite_temperature(V, at):
         tokens, probs = draw(x, u, temperature=math.inf)
         assert set(tokens.tolist()) == {token}
         assert (abs(probs - prob) <= prob * 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("gap", [1, 512, 4096])
+def test_the_largest_finite_and_an_infinite_logit_are_a_tie(gap):
+    """The lower id is the greedy choice, whether or not one thread has the two."""
+    x = torch.zeros(2, 9000, device="cuda")
+    x[0, 100], x[0, 100 + gap] = torch.finfo(torch.float32).max, math.inf
+    x[1, 100], x[1, 100 + gap] = math.inf, torch.finfo(torch.float32).max
+    tokens, probs = draw(x, 0.5, temperature=0.0)
+    assert tokens.tolist() == [100, 100] and probs.tolist() == [1.0, 1.0]
