@@ -22,10 +22,13 @@
 // Masses decide integers, so they are integers: a term is a number of 2^-34 steps
 // below its bucket's largest, from the exact product of logit and temperature in a
 // pair of floats and then in fixed point; sums have 2^-44 steps, in 64 bits, whatever
-// their order. A border is off by less than 2^-34 of the row's mass: of 150,000 borders, one draw
-// in some 10^5 .. 10^6 falls on another side than with exact sums. fp32 sums would lose one draw
-// in 2,000, and fp64 has 1/64 of fp32's lanes here. Terms below 2^-4 of the largest
-// need no more than fp32 for their place in the bucket.
+// their order. Terms below 2^-4 of the largest have their place in the bucket in fp32,
+// whose roundings (of the place, of the polynomial, of their product: 11, 16 and 16 of
+// those steps, with the rest 45) leave them 28 bits. They are of either sign: over
+// rows of normal logits a border is off by 2^-35 of the row's mass, of bf16 ones by
+// 2^-34, of thousands of equal ones in the tail by 2^-30. Of 150,000 borders, one draw
+// in some 10^5 .. 10^6 falls on another side than with exact sums; fp32 sums would lose one draw
+// in 2,000, and fp64 has 1/64 of fp32's lanes here.
 //
 // Measured: 1 x 32000 14.8 us (of which the CTAs' exchanges and the sort of some hundred entries about 12), 32 x 151936
 // 32, 256 x 151936 130 at temperature 0.8 and top-p 0.95: two passes of some 70 instructions a warp's 32 logits,

@@ -610,8 +610,10 @@ typedef struct {
  * shortest prefix whose mass reaches top_p of theirs; of those the ones with p >=
  * min_p times the largest p. The token is the first whose cumulative probability
  * exceeds uniforms[r] times the kept ones' total, as llm_set_sampling chooses it from
- * the same draw; probs[r] is its share of that total. Borders are decided with sums
- * of 36 bits or more (of the whole row's mass). A NaN logit counts as -inf, +inf as the
+ * the same draw; probs[r] is its share of that total. Borders are decided with
+ * 64-bit sums of weights of 34 bits, 28 below 1/16 of the largest: with errors of either
+ * sign a border is off by 2^-34 of the row's mass, by 2^-28 at most (thousands of equal
+ * logits below 1/16). A NaN logit counts as -inf, +inf as the
  * largest finite value; a row without a finite logit gives -1. The same call gives
  * the same tokens every time; a row in another batch gives the same one, but for
  * borders that lie within those sums' last bits. Rows with thousands of logits around a

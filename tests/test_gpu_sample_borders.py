@@ -84,3 +84,22 @@ def test_the_largest_finite_and_an_infinite_logit_are_a_tie(gap):
     x[1, 100], x[1, 100 + gap] = math.inf, torch.finfo(torch.float32).max
     tokens, probs = draw(x, 0.5, temperature=0.0)
     assert tokens.tolist() == [100, 100] and probs.tolist() == [1.0, 1.0]
+
+
+@pytest.mark.parametrize("below", [2.8, 3.1, 4.0, 5.5])
+def test_equal_logits_in_the_tail(below):
+    """One token and 4000 equal ones below 1/16 of it, draws at their borders. The equal ones have the same error: the
+    place is rounded by 2^-25 of a bucket of 2^28.5 steps, the polynomial and their product by 16 steps each, the rest
+    comes to 2, so 45 steps of 2^-34 of the bucket's largest weight, 2^-28.5. The draw is off by 2^-28 of the mass at
+    most."""
+    n, R = 4000, 4000
+    x = torch.full((1, 1 + n), -below, device="cuda")
+    x[0, 0] = 0.0
+    w = math.exp(float(x[0, 1]))
+    total = 1 + n * w
+    u = ((1 + w * np.arange(R)) / total).astype(np.float32)
+    tokens = torch.empty(R, dtype=torch.int32, device="cuda")
+    bq.sample_tokens(x.expand(R, -1), torch.from_numpy(u).cuda(), tokens)
+    lo, hi = (np.floor((u.astype(np.float64) * total - 1 + s * 2.0 ** -28 * total) / w) + 1 for s in (-1, 1))
+    got = tokens.cpu().numpy()
+    assert ((got >= np.maximum(lo, 0)) & (got <= np.minimum(hi, n))).all()
