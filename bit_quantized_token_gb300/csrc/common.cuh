@@ -53,6 +53,14 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // Code before pdl_wait() may only read data no kernel of the step writes
 // (weights). Every kernel triggers its dependents right after its own wait,
 // so a dependent's pre-wait code never overlaps kernels older than this one.
+// The exception: the second part of an attention in two parts (prefix.cu)
+// triggers first, and reads its inputs and takes its tensor memory without a
+// wait; it waits before it reads the first part's results and, without rows,
+// before it ends. That is sound because the first part, launched just before it,
+// waits before it triggers: what is older than both is over, and the second part
+// never ends before the first. So a dependent's pre-wait code can overlap both
+// parts (it must not touch their workspace or tensor memory), and no kernel that
+// triggers before its wait may stand in the first part's place.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

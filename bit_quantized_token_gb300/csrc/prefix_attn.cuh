@@ -46,8 +46,7 @@ struct Wide {
   static constexpr int NST = HD == 64 ? 4 : 2;                   // K tiles in flight, and V tiles
   static constexpr int kOffCum = 512, kOffGroup = kOffCum + 4 * (kWideGroups + 4), kSmall = kOffGroup + 12 * kWideGroups;
   static constexpr int kSmem = 2 * kTile + 2 * NST * kTile + kSmall + 1024;
-  // more than half of an SM's: no CTA that holds tensor memory shares the SM (this one takes all of it)
-  static_assert(kSmem > 140000 && kSmem <= 232448, "shared memory");
+  static_assert(kSmem <= 232448 && tmem_fits(kSmem, 512), "shared memory");
   static constexpr int kAtO = 2 * NBUF * KB;                      // columns: S of tile t, buffer x at (t NBUF + x) KB; then O
   static_assert(kAtO + 2 * HD <= 512, "tensor memory");
 };

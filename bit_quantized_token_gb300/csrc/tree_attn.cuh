@@ -66,6 +66,15 @@ constexpr float kNone = -3.402823466e38f;  // a row's reference before any visib
 // round: 4e-7, at 0.5 us of 12.3 (16 nodes over 4097 rows).
 constexpr int kTogether = 2;
 
+// Whether CTAs that take tensor memory, each with this shared memory and these columns, find their columns wherever
+// an SM's 228 KB (a CTA's own and 1 KB) hold them together: at most two share an SM, and one of more than half of the
+// columns shares it with none. So an allocation never waits for a CTA that waits for its kernel (a cluster that
+// gathers, a second part that waits for the first).
+constexpr bool tmem_fits(int smem, int cols) {
+  constexpr int kSm = 228 * 1024, kOwn = 1024, kThird = kSm / 3;
+  return smem + kOwn > kThird && (cols <= 256 || smem + kOwn + kThird >= kSm);
+}
+
 template <int HD, bool F32, int NB, int G>
 struct TreeTc {
   static constexpr int N = NB * G, BK = 128, H = HD / 64;
@@ -101,6 +110,7 @@ struct TreeTc {
   static constexpr int kUsed = DB * NSA + H * NOA;                       // S, and O of every 64 dims
   static_assert(kUsed <= 512, "tensor memory");
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(tmem_fits(kSmem, kCols), "tensor memory of CTAs on an SM");
 };
 
 // A warp's bounded wait with one answer for all lanes.
@@ -518,7 +528,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
       mbar_fence_init();
     }
     __syncwarp();
-    // (after pdl_wait: held earlier, it could be what the kernel before this one is waiting for)
+    // (after pdl_wait: held earlier, it could be what the kernel before this one is waiting for. A second part takes
+    // it while the first still may: both find room on an SM, see tmem_fits)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
                  "r"((uint32_t)C::kCols)
                  : "memory");
@@ -967,8 +978,8 @@ __global__ void __launch_bounds__(TreeTc<HD, F32, NB, G>::NT, TreeTc<HD, F32, NB
     __syncwarp();
   }
   // Freed last: no two CTAs that hold and that wait for tensor memory share an
-  // SM (kernels whose columns exceed half take all of its shared memory), so a
-  // CTA that holds it while its cluster gathers cannot keep a peer waiting.
+  // SM (see tmem_fits), so a CTA that holds it while its cluster gathers cannot
+  // keep a peer waiting.
   if (warp == 4 * G + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kCols));

@@ -108,6 +108,7 @@ struct TreeQ8 {
   static constexpr int kUsed = kAtK + HD / 2;                             // and the widened K tile
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(R >= 2 && kUsed <= 512 && G * 4096 <= kP, "fits");
+  static_assert(tmem_fits(kSmem, kCols), "tensor memory of CTAs on an SM");
 };
 
 template <int HD, bool F32, int G>
