@@ -18,9 +18,10 @@ _UNSUPPORTED = -2
 
 
 def _load():
+    global _DTYPES
     lib = _t._lib or _t._load()
     if not _DTYPES:
-        _DTYPES[_t._f32], _DTYPES[_t._bf16] = _t.LLM_F32, _t.LLM_BF16
+        _DTYPES = {_t._f32: _t.LLM_F32, _t._bf16: _t.LLM_BF16}  # all at once: another thread may come in between
     return lib
 
 
