@@ -341,7 +341,7 @@ void turns_of(double theta, int hd, uint64_t* freq) {
     double f = 0.15915494309189533577;  // 1 / (2 pi)
     for (int k = 0; k < 6; ++k)
       if (i >> k & 1) f *= root[k];
-    f -= std::floor(f);  // (a base below 1 turns faster)
+    f -= std::floor(f);  // (a base below 1/(2 pi) turns more than once)
     const double x = std::nearbyint(f * 18446744073709551616.0);
     freq[i] = x >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(x);
   }
@@ -380,6 +380,8 @@ int llm_append_kv(const llm_append_kv_args* a, void* cuda_stream) {
       !c.need((a->n_heads > 0) == (a->q != nullptr), LLM_ERR_INVALID_ARG, "n_heads and q do not match") ||
       !c.need(a->rope_theta == 0.0 || (a->rope_theta > 0.0 && std::isfinite(a->rope_theta)), LLM_ERR_INVALID_ARG,
               "rope_theta is not positive and finite (0: no rotation)") ||
+      // (a base near 0 turns so fast that 64 bits of theta^(-2i/hd) leave nothing of its fraction)
+      !c.need(a->rope_theta == 0.0 || a->rope_theta >= 1.0 / 1024, LLM_ERR_UNSUPPORTED, "rope_theta is below 2^-10") ||
       !c.need(a->rope_neox == 0 || a->rope_neox == 1, LLM_ERR_INVALID_ARG, "rope_neox must be 0 or 1") ||
       !c.need(!(a->q_norm || a->k_norm) || (a->norm_eps > 0.f && std::isfinite(a->norm_eps)), LLM_ERR_INVALID_ARG,
               "norm_eps is not positive"))

@@ -545,7 +545,7 @@ typedef struct {
   const int32_t* positions;     /* [n_tokens] of the rotation, any int32; NULL: rows */
   const float *q_norm, *k_norm; /* [head_dim] RMSNorm weights of a head (16-byte aligned), or NULL: no norm */
   float norm_eps;
-  double rope_theta;            /* base; 0: no rotation */
+  double rope_theta;            /* base, at least 2^-10; 0: no rotation */
   int32_t rope_neox;            /* as in llm_config */
 } llm_append_kv_args;
 
@@ -553,7 +553,7 @@ typedef struct {
  * rotated by position * rope_theta^(-2i/head_dim), q to q_out, k and v (as they
  * are) to the cache's row in its format: bf16, or int8 codes and scales with the
  * roundings of LLM_KV_Q8. Computed in fp32, angles in 64-bit fixed point (2^-30 of a
- * turn at position 2^20), rounded once into the outputs. Int8 rows: values past
+ * turn at position 2^20, of bases from 1/4 on), rounded once into the outputs. Int8 rows: values past
  * 65504 * 127 saturate, a NaN makes its 32 values NaN. With q, norms and rope_theta
  * left out it writes rows as they are, quantised for an int8 cache. The (seq, row)
  * pairs of a call differ; of two equal ones the row holds parts of either. */
