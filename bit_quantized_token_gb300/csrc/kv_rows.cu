@@ -432,6 +432,7 @@ int llm_read_kv(const llm_kv_view* cache, int32_t n_tokens, const int32_t* seqs,
     return c.rc;
   const int64_t size[3] = {cache->n_layers, n_tokens, cache->n_heads};
   if (!c.need(apart(cache->head_dim, 3, size, out_strides), LLM_ERR_INVALID_ARG, "rows of the outputs overlap") ||
+      !c.need(k != v || !k, LLM_ERR_INVALID_ARG, "k and v are the same memory") ||
       !view_memory(c, cache, "cache") || !c.device("seqs", seqs, 4) || !c.device("rows", rows, 4) ||
       !c.device("k", k, 16) || !c.device("v", v, 16))
     return c.rc;
