@@ -50,3 +50,29 @@ def test_groups_out_of_order_stay_apart(hd):
     p, want = Problem(starts=(0, 60, 20, 130, 170), **kw), Problem(starts=(0, 60, 60, 130, 170), **kw)
     assert torch.equal(p.call(), want.call())
     want.check()
+
+
+MANY = [
+    # more groups than a warp has lanes, some without sequences or rows
+    dict(starts=tuple(sorted(3 * (i // 4 * 4) + 5 * (i % 4 == 3) for i in range(41))), gq=8, P=200, plens=(200, 0, 131, 64, 1)),
+    dict(starts=tuple(range(0, 144, 2)), gq=2, hd=128, P=140, plens=(140, 129, 128, 0)),
+    # more groups than the kernel for many rows keeps
+    dict(starts=tuple(range(1031)), gq=1, Hkv=1, P=24, plens=(24, 1, 0, 17), own=4, lens=(4, 0, 1)),
+    # more than 10240 and 40960 rows of all heads: row tiles in at most four pieces, and whole
+    dict(starts=(0, 30, 41, 48), n=14, gq=8, P=1300, plens=(1300, 700, 129), own=20),
+    dict(starts=(0, 48), n=14, gq=8, hd=128, P=1300, plens=(1290,), own=20),
+    dict(starts=(0, 33, 59, 60), n=44, gq=8, P=900, plens=(900, 650, 0), own=20, counts=(44, 3, 0)),
+    dict(starts=(0, 60), n=44, gq=8, hd=128, P=700, plens=(690,), own=20, counts=(44, 3)),
+    # nothing but the prefix
+    dict(starts=(0, 3), P=200, plens=(190,), own=0, lens=(0,), tree=False),
+    dict(starts=(0, 90), P=200, plens=(190,), own=0, lens=(5,), tree=False, gq=4),
+    dict(starts=(0, 3), n=6, P=200, plens=(190,), own=0, lens=(0,), tree=False, gq=4, kv="q8", q="f32"),
+]
+
+
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_against_the_formula(i):
+    p = Problem(**MANY[i], seed=i)
+    p.call()
+    p.check()
+    assert torch.equal(p.out, p.call())
