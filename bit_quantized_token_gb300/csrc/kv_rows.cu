@@ -28,8 +28,8 @@ namespace {
 // become the largest that the row can hold), a NaN makes its 32 values NaN.
 //
 // Bound by HBM and its own instructions for many tokens (8192 of 16/8 heads x 128 in bf16, norms and rotation:
-// 28 us, 4.9 TB/s, into int8 rows 41; a lane that held four neighbouring dims instead took 74; packed products of two
-// values no less), by the launch for few (one token of 32/4 heads x 64 2.8 us, 32 of 16/8 heads x 128 into int8 rows 4.2).
+// 29 us, 4.6 TB/s, into int8 rows 42; a lane that held four neighbouring dims instead took 74; packed products of two
+// values no less), by the launch for few (one token of 32/4 heads x 64 2.2 us, 32 of 16/8 heads x 128 into int8 rows 4.0).
 // Seven CTAs on an SM, in 72 registers: 30.9 / 27.8 / 27.7 / 33.0 us with the compiler's 80, 72, 64 and 48.
 constexpr int kAppendThreads = 128;
 
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kAppendThreads, 7) append_kv_kernel(const __gr
 //
 // Bound by HBM: 4099 tokens x 28 layers x 8 heads x 128 of int8 rows to bf16 124 us (5.8 TB/s, 85 % of
 // a copy's; 121 / 124 / 139 with one, two and four pairs in flight, but fp32 231 / 217 / 230), of bf16 rows
-// 136 us (6.9 TB/s); by the launch for few: 37 tokens x 8 layers x 4 heads x 64 2.6 us.
+// 136 us (6.9 TB/s); by the launch for few: 37 tokens x 22 layers x 4 heads x 64, bf16 to fp32, 2.4 us.
 constexpr int kReadThreads = 256, kReadRows = 2;
 
 // the values of eight bf16 or, times f, of eight codes (0 times an infinite scale is NaN, as in a product)

@@ -22,9 +22,9 @@
 // ranges, one for each CTA, so that every SM has the same number whatever the sizes of the
 // groups; the pieces of a row tile (max_parts at most) are joined by the second part.
 //
-// Measured: 256 sequences of 32/4 heads x 64 behind 16384 rows 49 us of the call's 62 (34.4 GFLOP, 700 TFLOP/s). Bound by
+// Measured: 256 sequences of 32/4 heads x 64 behind 16384 rows 49 us of the call's 64 (34.4 GFLOP, 700 TFLOP/s). Bound by
 // the softmax warps: about 1,000 cycles for a block of 128 rows x 64 keys (exponentials alone 512 for the two tiles) and 400 between blocks,
-// tensor pipe 32 % and issue slots 43 % busy; 16 softmax warps instead of 8 gained nothing.
+// tensor pipe 33 % and issue slots 44 % busy; 16 softmax warps instead of 8 gained nothing.
 #pragma once
 #include "tree_attn_q8.cuh"
 

@@ -17,7 +17,8 @@
 // A window that turns out too low, or too narrow, or buckets that hold more than
 // kSampleList tokens around the borders (flat rows), are set again from the row's exact
 // range, once. Rows that still have more there (crowds of equal logits) take the long
-// way: each border by three digits of the logits' keys, over all tokens.
+// way: each border by three digits of the logits' keys, over all tokens (256 x 151936
+// 2.9 ms). So do rows whose largest logit is 32768 octaves or more from 0 (1.5 ms).
 //
 // Masses decide integers, so they are integers: a term is a number of 2^-34 steps
 // below its bucket's largest, from the exact product of logit and temperature in a
@@ -30,9 +31,10 @@
 // in some 10^5 .. 10^6 falls on another side than with exact sums; fp32 sums would lose one draw
 // in 2,000, and fp64 has 1/64 of fp32's lanes here.
 //
-// Measured: 1 x 32000 14.8 us (of which the CTAs' exchanges and the sort of some hundred entries about 12), 32 x 151936
-// 32, 256 x 151936 130 at temperature 0.8 and top-p 0.95: two passes of some 70 instructions a warp's 32 logits,
-// 64 % of the issue slots, HBM at 25 %. The second pass reads memory again (156 MB of rows and 129 MB of L2). A form
+// Measured at temperature 0.8 and top-p 0.95: 1 x 32000 15.8 us (of which the CTAs' exchanges and the sort of some
+// hundred entries about 12), 32 x 151936 37.5, 256 x 151936 130 (rows of mixed options 38, temperatures 0.7 and 1 with
+// min-p 144): two passes of some 70 instructions a warp's 32 logits, 64 % of the issue slots, HBM at 25 %. The second
+// pass reads memory again (156 MB of rows and 129 MB of L2). A form
 // that kept the logits in shared memory, and so took up to 16 CTAs a row, needed 391 us for the last.
 #include <cooperative_groups.h>
 
@@ -639,6 +641,7 @@ __global__ void __launch_bounds__(kSampNT, 2) sample_rows_kernel(const __grid_co
     // logits of weight (2^-63 and more) that the buckets below the largest miss
     // (an infinite one is outside, and the difference times 0 at an infinite temperature says nothing)
     const bool missed = out > m || (m - out) * ch < 63.f || (fine > 0 && (m - least) * chS >= (float)(kSampB - 2));
+    // (the long way too where bucket numbers come near 2^21, what the floor in fp32 and the window hold)
     crowd = !(fabsf(m * ch) < 32768.f) || (missed && turn == 1);
     if (crowd) break;
     if (!missed) {

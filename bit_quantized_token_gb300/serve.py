@@ -124,7 +124,8 @@ def prefix_attention(q, prefix: KVView, starts, prefix_lens, cache: KVView, tree
                      workspace, counts=None, scale: float | None = None, stream: int | None = None) -> None:
     """tree_attention where sequences starts[g] .. starts[g + 1] - 1 also see the first prefix_lens[g] rows of the
     prefix view's sequence g, which are read once for all of them. workspace: a contiguous CUDA tensor of
-    prefix_workspace(q) bytes, one for each of the calls that may overlap; see llm_prefix_attention."""
+    prefix_workspace(q) bytes, one for each of the calls that may overlap. Views narrowed to the batch's longest
+    lengths (k[:, :, :rows]) are faster than ones of a cache's whole room; see llm_prefix_attention."""
     L = _load()
     shape, dt = q.shape, q.dtype
     kind = _kind(q, "queries")

@@ -584,7 +584,12 @@ typedef struct {
  * precision, counts, masks and empty rows holds here too (bf16 queries over bf16
  * prefix rows: the probabilities carry 8 bits where the batch has more than 64 query
  * rows, n_seq x n_nodes x heads, of a kv head). One decode token: n_nodes = 1, its row already in the cache and
- * tree NULL, or its row as the tree's. llm_tree_status reports waits that ran out. */
+ * tree NULL, or its row as the tree's. llm_tree_status reports waits that ran out.
+ * The host chooses kernels and splits and does not know the lengths: it goes by the rows
+ * of the views. Views narrowed to the batch's longest length are faster than ones of a
+ * cache's whole room (32 sequences of 20 rows, 16/8 heads x 128, behind 2048: 16 us in
+ * bf16 views of 20 rows, 28 of 4096; int8 prefixes of 2048 rows 19 us, in a view of 32768
+ * 37). */
 int llm_prefix_attention(const llm_prefix_attention_args* args, void* cuda_stream);
 
 /* Bytes of llm_prefix_attention's workspace, or a negative llm_status. Nothing in it
@@ -617,9 +622,11 @@ typedef struct {
  * largest finite value; a row without a finite logit gives -1. The same call gives
  * the same tokens every time; a row in another batch gives the same one, but for
  * borders that lie within those sums' last bits. Rows with thousands of logits around a
- * border (untrained ones, high temperatures) take up to three times as long, rows with
- * crowds of equal logits around it about ten times (151936 equal ones 0.2 ms, 256 rows of
- * them 3.7 ms). UNSUPPORTED: vocab over 524288. */
+ * border (untrained ones, high temperatures) take up to three times as long. Rows with
+ * crowds of equal logits around it take 8 to 25 times (151936 equal ones 0.17 ms, 256 rows
+ * of them 2.9 ms), rows whose largest logit is 22713 temperatures or more from 0 (20 at a
+ * temperature of 0.00088) 4 to 12 times (0.09 and 1.5 ms; a temperature of 0 takes the
+ * usual time). UNSUPPORTED: vocab over 524288. */
 int llm_sample_tokens(const llm_sample_args* args, void* cuda_stream);
 
 #ifdef __cplusplus
