@@ -561,8 +561,8 @@ int llm_append_kv(const llm_append_kv_args* args, void* cuda_stream);
 
 /* k[l][t], v[l][t] = the values of row rows[t] of sequence seqs[t] in every layer
  * and head, as LLM_BF16 or LLM_F32 (int8 rows: code times scale, rounded once);
- * zeros where seqs[t] or rows[t] is out of range. Both outputs lie at out_strides
- * (elements: layer, token, head; multiples of 16 bytes). */
+ * zeros where seqs[t] or rows[t] is out of range. Both outputs, each in memory of its
+ * own, lie at out_strides (elements: layer, token, head; multiples of 16 bytes). */
 int llm_read_kv(const llm_kv_view* cache, int32_t n_tokens, const int32_t* seqs, const int32_t* rows, int32_t out_dtype,
                 void* k, void* v, const int64_t* out_strides, void* cuda_stream);
 
